@@ -289,6 +289,147 @@ MGQA_API mgqa_status masked_gqa_attn_decode_append_rope(
     const int64_t *v_new_stride, int32_t *kv_len_out, const mgqa_qk_rope *rope, void *workspace,
     size_t workspace_bytes, cudaStream_t stream);
 
+/* ---- sliding windows, drafted tokens, and a cache in pages -------------------
+ * Later steps of a serving loop around the same attention; no passage of the
+ * engine pages has a counterpart. */
+
+/* masked_gqa_attn_prefill with a sliding window: query row i stands at position
+ * i + (Lk - Lq) and sees key j when, besides every mask form given in args,
+ *   j > position - window, or j < sinks       (sinks: first keys that stay visible)
+ * and, unless args->causal is set (then j <= position, as ever),
+ *   j < position + window, or j < sinks       (the window reaches both ways).
+ * window >= 1 counts the query's own position; sinks >= 0. Only the key tiles
+ * that the window and the sinks reach are read. Same types, head dims, strides
+ * and errors as masked_gqa_attn_prefill; with kv_len or segment ids the forms
+ * are combined with AND, so a padded row keeps positions 0 .. Lk - 1. */
+MGQA_API mgqa_status masked_gqa_attn_prefill_window(const mgqa_args *args, int32_t window,
+                                                    int32_t sinks, cudaStream_t stream);
+
+/* A cache in pages: slot j of request b lies in page table[b*table_stride +
+ * j/page_size] at slot j % page_size. With pages, args->k and args->v are the
+ * pools [num_pages][Hkv][page_size][D] (k_stride, v_stride = page, head, slot)
+ * and args->Lk is max_pages * page_size. Any page_size >= 1. Entries of slots
+ * that no query sees (behind kv_len, or between the sinks and the window) are
+ * not looked at. An entry outside [0, num_pages) that is needed is a device
+ * error; its slots count as masked. */
+typedef struct {
+  const int32_t *table;   /* device [B][max_pages] */
+  int64_t table_stride;   /* in elements, >= max_pages when B > 1 */
+  int32_t num_pages, page_size, max_pages;
+} mgqa_pages;
+
+/* Drafted tokens (Lq of them per request, 1 .. 256) that follow the cache. */
+typedef struct {
+  const void *k_new, *v_new;         /* device [B][Hkv][Lq][D], the drafts' keys and values,
+                                        dtype of the call, 16-byte aligned */
+  int64_t k_stride[3], v_stride[3];  /* batch, head, draft, in elements; multiples of 16 bytes */
+  const uint32_t *bits;              /* optional device words: bit s % 32 of word
+                                        bits[b*bits_stride_b + t*bits_stride_t + s/32] is 1 when draft t
+                                        sees draft s (its ancestors and itself); NULL: a chain, s <= t */
+  int64_t bits_stride_b, bits_stride_t;  /* in words; 0 broadcasts, else >= ceil(Lq/32) */
+  const int32_t *len;                /* optional device [B]: live drafts (0 .. Lq); the rows behind
+                                        them see nothing and are seen by none: out = 0, lse = -inf */
+} mgqa_tree;
+
+/* Bytes of the workspace of the two calls below; the same for every shape.
+ * The workspace (device, 16-byte aligned) needs no initial contents and
+ * carries nothing from call to call. Calls that may run at the same time (two
+ * streams, two graphs) need a workspace each. */
+MGQA_API size_t masked_gqa_attn_cache_workspace_size(void);
+
+/* One query per request (Lq == 1), the last cached token's, with a sliding
+ * window over a cache in slots (pages NULL: args->k, v [B][Hkv][Lk][D]) or in
+ * pages: with n = kv_len[b] it sees slots j < n with n - 1 - j < window or
+ * j < sinks. kv_len is required; bits, segment ids and causal are not accepted.
+ * kv_len outside [0, Lk] is a device error (clamped). Lk <= 2^24. The work is
+ * spread over the GPU by the requests' own lengths. */
+MGQA_API mgqa_status masked_gqa_attn_decode_window(const mgqa_args *args, const mgqa_pages *pages,
+                                                   int32_t window, int32_t sinks, void *workspace,
+                                                   size_t workspace_bytes, cudaStream_t stream);
+
+/* Attention of drafted tokens over a cache, for the check of a speculative
+ * step: draft t of request b sees every cached slot j < kv_len[b] and the
+ * drafts that its bits name. Its position is kv_len[b] plus the number of other
+ * drafts that it sees (its depth); with window > 0 keys at a distance of window
+ * or more, sinks apart, are hidden from it, cached or drafted (window 0: none).
+ * q, out [B][Hq][Lq][D]. The drafts' keys and values come from `tree` and are
+ * not written to the cache: masked_gqa_cache_append stores the accepted ones.
+ * Cache forms, kv_len, workspace and errors as for
+ * masked_gqa_attn_decode_window. Values of rows that are seen by any draft of a
+ * request have to be finite. */
+MGQA_API mgqa_status masked_gqa_attn_decode_tree(const mgqa_args *args, const mgqa_pages *pages,
+                                                 const mgqa_tree *tree, int32_t window,
+                                                 int32_t sinks, void *workspace,
+                                                 size_t workspace_bytes, cudaStream_t stream);
+
+/* The key/value cache of `layers` layers that share one page table, for the
+ * calls below. Without pages (page_table NULL) it is the static cache: page b is
+ * request b's slots (num_pages == rows, page_size slots each). */
+typedef struct {
+  mgqa_dtype dtype;
+  int32_t layers, num_pages, Hkv, page_size, D;
+  void *k, *v;                       /* device [layers][num_pages][Hkv][page_size][D], 16-byte aligned */
+  int64_t k_stride[4], v_stride[4];  /* layer, page, head, slot, in elements; multiples of 16 bytes */
+  int32_t rows, max_pages;           /* requests; table entries of each */
+  int32_t *page_table;               /* device [rows][max_pages]; -1: no page */
+  int64_t table_stride;
+  int32_t *kv_len;                   /* device [rows] */
+  int32_t *ref;                      /* device [num_pages]: how many table entries hold the page
+                                        (fork and compact; 0: free) */
+  int32_t *dev_error;                /* optional, as in mgqa_args */
+} mgqa_cache;
+
+/* Appends T new rows, or the chosen ones of them, to every request and layer:
+ * for i < count[b] (count NULL: T) slot kv_len[b] + i gets row index[b*T + i]
+ * (index NULL: i) of k_new and v_new ([layers][rows][Hkv][T][D], strides layer,
+ * batch, head, row). kv_len_out[b] = kv_len[b] + count[b]; it must not alias
+ * kv_len. A request whose count is outside [0, T], or whose rows would pass its
+ * last slot, appends nothing and keeps its length; an index outside [0, T) or a
+ * missing page leaves that slot as it was; each sets *dev_error. No other slot
+ * is written. Requests must not share the pages that they append to (fork sees
+ * to that). */
+MGQA_API mgqa_status masked_gqa_cache_append(const mgqa_cache *cache, const void *k_new,
+                                             const void *v_new, const int64_t *k_new_stride,
+                                             const int64_t *v_new_stride, int32_t T,
+                                             const int32_t *index, const int32_t *count,
+                                             int32_t *kv_len_out, cudaStream_t stream);
+
+/* Bytes of the workspace of fork (n pairs) and compact (n = 0) for this cache;
+ * 0 when the arguments are invalid. It needs no initial contents. */
+MGQA_API size_t masked_gqa_cache_workspace_size(const mgqa_cache *cache, int32_t n);
+
+/* Forks, frees and reserves: for i < n (n <= 1024; src, dst device [n]) request
+ * dst[i] becomes a continuation of request src[i]:
+ *   src >= 0, src != dst: dst gives back its pages and takes over src's length.
+ *            The pages that src fills are shared (ref + 1); the last, partly
+ *            filled one is copied to a page of dst's own.
+ *   src == dst: dst keeps its pages; one that it will write to (at or behind
+ *            slot kv_len) and does not hold alone is replaced by a page of its
+ *            own, with the filled slots copied.
+ *   src == -1: dst gives back its pages and is empty (length 0).
+ * Then, unless src is -1, dst gets pages for `extra` more tokens. New pages are
+ * the free ones (ref 0 once every page is given back and every share taken, and
+ * read by no copy of this call) of lowest index, handed out in the order of the
+ * pairs. All pairs read the tables and lengths as they were before the call. A
+ * pair that the free pages, together with the pairs before it, do not suffice
+ * for is not carried out: dst is left empty (src != dst) or unchanged; a pair
+ * with src or dst out of range, or with the dst of an earlier pair, is skipped;
+ * each sets *dev_error. Table entries outside [0, num_pages) count as -1.
+ * num_pages <= 2^20. */
+MGQA_API mgqa_status masked_gqa_cache_fork(const mgqa_cache *cache, int32_t n, const int32_t *src,
+                                           const int32_t *dst, int32_t extra, void *workspace,
+                                           size_t workspace_bytes, cudaStream_t stream);
+
+/* Packs the pool: with U pages in use (ref > 0), the i-th used page of index
+ * >= U moves, in ascending order, to the i-th free page of index < U; every
+ * layer's keys and values are copied, page_table_out and ref_out get the
+ * renamed tables (they may be page_table and ref themselves) and *used_out,
+ * when given, U. Pages moved away from keep their contents and become free. */
+MGQA_API mgqa_status masked_gqa_cache_compact(const mgqa_cache *cache, int32_t *page_table_out,
+                                              int64_t table_out_stride, int32_t *ref_out,
+                                              int32_t *used_out, void *workspace,
+                                              size_t workspace_bytes, cudaStream_t stream);
+
 /* Static description of a status code. */
 MGQA_API const char *mgqa_status_string(mgqa_status status);
 

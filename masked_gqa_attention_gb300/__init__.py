@@ -10,7 +10,13 @@ Entry points (same names as the C ABI):
     under a packed-bit mask, per-row key lengths and/or segment ids;
   * :func:`masked_gqa_attn_decode` -- one query per row over a static KV
     cache, merged on chip (the ``workspace`` arguments are accepted and
-    ignored).
+    ignored);
+  * :func:`masked_gqa_attn_prefill_window`, :func:`masked_gqa_attn_decode_window`
+    -- attention with a sliding window and sinks, over whole sequences and for
+    one token over a cache in slots or pages;
+  * :func:`masked_gqa_attn_decode_tree` -- drafted tokens over such a cache;
+  * :func:`masked_gqa_cache_append`, :func:`masked_gqa_cache_fork`,
+    :func:`masked_gqa_cache_compact` -- the cache's own steps.
 """
 from __future__ import annotations
 
@@ -35,6 +41,11 @@ __all__ = [
     "debug_lib", "MGQA_ERR_DEVICE_CHECK", "MgqaQkRope", "make_qk_rope",
     "masked_gqa_attn_prefill_rope", "masked_gqa_attn_decode_append_rope", "masked_gqa_rope",
     "masked_gqa_rope_pair",
+    "MgqaPages", "MgqaTree", "MgqaCache",
+    "masked_gqa_attn_prefill_window", "masked_gqa_attn_decode_window",
+    "masked_gqa_attn_decode_tree", "masked_gqa_attn_cache_workspace_size", "new_cache_attn_workspace",
+    "masked_gqa_cache_append", "masked_gqa_cache_fork", "masked_gqa_cache_compact",
+    "masked_gqa_cache_workspace_size",
 ]
 
 (MGQA_OK, MGQA_ERR_INVALID_ARG, MGQA_ERR_UNSUPPORTED, MGQA_ERR_CUDA, MGQA_ERR_TIMEOUT,
@@ -56,6 +67,14 @@ EXPORTED_SYMBOLS = (
     "masked_gqa_attn_prefill_rope",
     "masked_gqa_attn_decode_append_rope",
     "masked_gqa_rope_pair",
+    "masked_gqa_attn_prefill_window",
+    "masked_gqa_attn_cache_workspace_size",
+    "masked_gqa_attn_decode_window",
+    "masked_gqa_attn_decode_tree",
+    "masked_gqa_cache_append",
+    "masked_gqa_cache_workspace_size",
+    "masked_gqa_cache_fork",
+    "masked_gqa_cache_compact",
 )
 # exported by the debug library only (include/masked_gqa_attn_debug.h)
 DEBUG_SYMBOLS = (
@@ -122,6 +141,39 @@ class MgqaQkRope(ctypes.Structure):
     ]
 
 
+class MgqaPages(ctypes.Structure):
+    """Mirror of ``mgqa_pages`` in include/masked_gqa_attn.h."""
+    _fields_ = [
+        ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+        ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+    ]
+
+
+class MgqaTree(ctypes.Structure):
+    """Mirror of ``mgqa_tree`` in include/masked_gqa_attn.h."""
+    _fields_ = [
+        ("k_new", ctypes.c_void_p), ("v_new", ctypes.c_void_p),
+        ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+        ("bits", ctypes.c_void_p),
+        ("bits_stride_b", ctypes.c_int64), ("bits_stride_t", ctypes.c_int64),
+        ("len", ctypes.c_void_p),
+    ]
+
+
+class MgqaCache(ctypes.Structure):
+    """Mirror of ``mgqa_cache`` in include/masked_gqa_attn.h."""
+    _fields_ = [
+        ("dtype", ctypes.c_int),
+        ("layers", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("D", ctypes.c_int32),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_stride", ctypes.c_int64 * 4), ("v_stride", ctypes.c_int64 * 4),
+        ("rows", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+        ("kv_len", ctypes.c_void_p), ("ref", ctypes.c_void_p), ("dev_error", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 _lib_debug = None
 
@@ -163,6 +215,19 @@ def _bind(L: ctypes.CDLL) -> ctypes.CDLL:
     L.masked_gqa_attn_decode_append_rope.argtypes = [ctypes.POINTER(MgqaArgs), P, P, I64P, I64P, P,
                                                      ctypes.POINTER(MgqaQkRope), P, ctypes.c_size_t, P]
     L.masked_gqa_attn_decode_append_rope.restype = ctypes.c_int
+    # (structs of the cache calls go as plain addresses: cheaper per call than typed pointers)
+    SZ, I64 = ctypes.c_size_t, ctypes.c_int64
+    for name, args, res in (
+            ("masked_gqa_attn_prefill_window", [P, I32, I32, P], ctypes.c_int),
+            ("masked_gqa_attn_cache_workspace_size", [], SZ),
+            ("masked_gqa_attn_decode_window", [P, P, I32, I32, P, SZ, P], ctypes.c_int),
+            ("masked_gqa_attn_decode_tree", [P, P, P, I32, I32, P, SZ, P], ctypes.c_int),
+            ("masked_gqa_cache_append", [P, P, P, P, P, I32, P, P, P, P], ctypes.c_int),
+            ("masked_gqa_cache_workspace_size", [P, I32], SZ),
+            ("masked_gqa_cache_fork", [P, I32, P, P, I32, P, SZ, P], ctypes.c_int),
+            ("masked_gqa_cache_compact", [P, P, I64, P, P, P, SZ, P], ctypes.c_int)):
+        f = getattr(L, name)
+        f.argtypes, f.restype = args, res
     return L
 
 
@@ -561,3 +626,298 @@ def masked_gqa_attn_decode_append_rope(q, k_cache, v_cache, k_new, v_new, kv_len
         _ptr(_dev(kv_len_out, "kv_len_out", torch.int32)), ctypes.byref(r), wp, wn,
         _stream_handle(stream)))
     return out
+
+
+# ---- sliding windows, drafted tokens, and a cache in slots or pages ---------------
+
+_ARRAY3, _ARRAY4 = ctypes.c_int64 * 3, ctypes.c_int64 * 4
+_CODES = {torch.bfloat16: MGQA_BF16, torch.float16: MGQA_FP16, torch.float32: MGQA_FP32}
+
+
+def _addr(x):
+    return ctypes.addressof(x)
+
+
+def _together(first, **others):
+    """Every tensor on the device of `first`, a CUDA device."""
+    if not first.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    dev = first.device
+    for name, t in others.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+def _ints(t, name, shape, contiguous=True):
+    """Pointer of an int32 tensor of the given shape (None: absent)."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or (contiguous and not t.is_contiguous()):
+        raise ValueError(f"{name} must be {'contiguous ' if contiguous else ''}int32 {list(shape)}")
+    return t.data_ptr()
+
+
+def _go(tensor, stream, fn, *args):
+    """fn(*args, stream) with the tensors' device current; its own current
+    stream unless one is given."""
+    dev = tensor.device.index
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            status = fn(*args, _stream_handle(stream))
+    else:
+        status = fn(*args, _stream_handle(stream))
+    if status != MGQA_OK:
+        _check(status)
+
+
+def masked_gqa_attn_prefill_window(q, k, v, out=None, *, window, sinks=0, causal=True, scale=None,
+                                   mask_bits=None, kv_len=None, seg_q=None, seg_k=None, lse=None,
+                                   dev_error=None, stream=None):
+    """masked_gqa_attn_prefill with a sliding window: query i, at position
+    i + Lk - Lq, sees keys less than `window` behind it (its own position
+    counts; without causal also ahead of it) and the first `sinks` keys, AND
+    whatever the other mask forms allow. Returns out."""
+    _together(q, k=k, v=v, out=out, mask_bits=mask_bits, kv_len=kv_len, seg_q=seg_q, seg_k=seg_k,
+              lse=lse, dev_error=dev_error)
+    if out is None:
+        out = torch.empty_like(q)
+    a = make_args(q, k, v, out, scale=scale, mask_bits=mask_bits, kv_len=kv_len, seg_q=seg_q,
+                  seg_k=seg_k, lse=lse, dev_error=dev_error, causal=causal)
+    _go(q, stream, lib().masked_gqa_attn_prefill_window, _addr(a), int(window), int(sinks))
+    return out
+
+
+_cache_ws_bytes = 0
+
+
+def masked_gqa_attn_cache_workspace_size() -> int:
+    """Bytes of the workspace of the two calls below; the same for every shape."""
+    global _cache_ws_bytes
+    if not _cache_ws_bytes:
+        _cache_ws_bytes = int(lib().masked_gqa_attn_cache_workspace_size())
+    return _cache_ws_bytes
+
+
+def new_cache_attn_workspace(device="cuda") -> torch.Tensor:
+    """A workspace (uint8) for masked_gqa_attn_decode_window / _tree. Nothing in
+    it outlives a call; calls that may overlap need one each."""
+    return torch.empty(masked_gqa_attn_cache_workspace_size(), dtype=torch.uint8, device=device)
+
+
+def _cached_args(q, k_cache, v_cache, kv_len, out, page_table, scale, lse, dev_error):
+    """(MgqaArgs, MgqaPages or None) of a call over a cache in slots
+    [B, Hkv, Lk, D] or, with a page table, in pages [pages, Hkv, page_size, D]."""
+    if q.dim() != 4 or k_cache.dim() != 4 or v_cache.shape != k_cache.shape or out.shape != q.shape:
+        raise ValueError("q, out must be [B, Hq, L, D] and the caches [B or pages, Hkv, slots, D]")
+    dt = _CODES.get(q.dtype)
+    if dt is None or not (k_cache.dtype == v_cache.dtype == out.dtype == q.dtype):
+        raise ValueError("q, out and the caches must share one dtype of bfloat16, float16, float32")
+    B, Hq, L, D = q.shape
+    P0, Hkv, S, Dk = k_cache.shape
+    qs, ks, vs, os_ = q.stride(), k_cache.stride(), v_cache.stride(), out.stride()
+    if Dk != D or qs[3] != 1 or ks[3] != 1 or vs[3] != 1 or os_[3] != 1:
+        raise ValueError("the head dims must agree and have unit stride")
+    pages, cap = None, S
+    if page_table is not None:
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B \
+                or page_table.stride(1) != 1:
+            raise ValueError("page_table must be int32 [B, max_pages] with unit-stride rows")
+        mp = page_table.shape[1]
+        pages = MgqaPages(page_table.data_ptr(), page_table.stride(0), P0, S, mp)
+        cap = mp * S
+    elif P0 != B:
+        raise ValueError("a cache without a page table must be [B, Hkv, slots, D]")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq, L)
+                            or not lse.is_contiguous()):
+        raise ValueError("lse must be contiguous fp32 [B, Hq, L]")
+    if kv_len is None:
+        raise ValueError("kv_len is required")
+    a = MgqaArgs(dt, B, Hq, Hkv, L, cap, D, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                 out.data_ptr(), _ARRAY3(*qs[:3]), _ARRAY3(*ks[:3]), _ARRAY3(*vs[:3]),
+                 _ARRAY3(*os_[:3]), None, 0, 0, _ints(kv_len, "kv_len", (B,)), None, None,
+                 1.0 / math.sqrt(D) if scale is None else scale,
+                 None if lse is None else lse.data_ptr(), _ints(dev_error, "dev_error", (1,)), 0)
+    return a, pages
+
+
+def _cache_ws(workspace, q):
+    if workspace is None:
+        workspace = new_cache_attn_workspace(q.device)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def masked_gqa_attn_decode_window(q, k_cache, v_cache, kv_len, out=None, *, window, sinks=0,
+                                  page_table=None, workspace=None, scale=None, lse=None,
+                                  dev_error=None, stream=None):
+    """One query per request (q [B, Hq, 1, D], the last cached token's) with a
+    sliding window over a cache: slots j < kv_len[b] less than `window` behind
+    the last one, and the first `sinks`. The cache is [B, Hkv, slots, D], or
+    [pages, Hkv, page_size, D] with page_table int32 [B, max_pages].
+    workspace: new_cache_attn_workspace() (None: allocated here). Returns out."""
+    if out is None:
+        out = torch.empty_like(q)
+    _together(q, k_cache=k_cache, v_cache=v_cache, kv_len=kv_len, out=out, page_table=page_table,
+              workspace=workspace, lse=lse, dev_error=dev_error)
+    a, pages = _cached_args(q, k_cache, v_cache, kv_len, out, page_table, scale, lse, dev_error)
+    keep, wp, wn = _cache_ws(workspace, q)
+    _go(q, stream, lib().masked_gqa_attn_decode_window, _addr(a),
+        None if pages is None else _addr(pages), int(window), int(sinks), wp, wn)
+    return out
+
+
+def masked_gqa_attn_decode_tree(q, k_cache, v_cache, k_new, v_new, kv_len, out=None, *,
+                                tree_bits=None, tree_len=None, window=0, sinks=0, page_table=None,
+                                workspace=None, scale=None, lse=None, dev_error=None, stream=None):
+    """Attention of drafted tokens (q [B, Hq, T, D], T <= 256) over the cached
+    keys (as for masked_gqa_attn_decode_window; window 0: all of them) and the
+    drafts' own k_new / v_new [B, Hkv, T, D]: draft t sees draft s when bit
+    s % 32 of word s // 32 of tree_bits[b, t] is set (int32 / uint32
+    [B or 1, T or 1, >= ceil(T/32)]; None: s <= t). tree_len int32 [B]: live
+    drafts; the rows behind them give 0 and -inf. The drafts are not written to
+    the cache (masked_gqa_cache_append). Returns out."""
+    if out is None:
+        out = torch.empty_like(q)
+    _together(q, k_cache=k_cache, v_cache=v_cache, k_new=k_new, v_new=v_new, kv_len=kv_len, out=out,
+              tree_bits=tree_bits, tree_len=tree_len, page_table=page_table, workspace=workspace,
+              lse=lse, dev_error=dev_error)
+    a, pages = _cached_args(q, k_cache, v_cache, kv_len, out, page_table, scale, lse, dev_error)
+    B, T = q.shape[0], q.shape[2]
+    shape = (B, k_cache.shape[1], T, q.shape[3])
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if t.dtype != q.dtype or tuple(t.shape) != shape or t.stride(3) != 1:
+            raise ValueError(f"{name} must be {q.dtype} {list(shape)} with a unit-stride head dim")
+    bits, sb, st = None, 0, 0
+    if tree_bits is not None:
+        if tree_bits.dtype not in (torch.int32, torch.uint32) or tree_bits.dim() != 3 \
+                or tree_bits.stride(2) != 1:
+            raise ValueError("tree_bits must be 3-D int32/uint32 words, contiguous along drafts")
+        b0, t0, w0 = tree_bits.shape
+        if b0 not in (1, B) or t0 not in (1, T) or w0 < (T + 31) // 32:
+            raise ValueError(f"tree_bits must be [B or 1, T or 1, >= {(T + 31) // 32}] words")
+        bits = tree_bits.data_ptr()
+        sb = tree_bits.stride(0) if b0 > 1 else 0
+        st = tree_bits.stride(1) if t0 > 1 else 0
+    tree = MgqaTree(k_new.data_ptr(), v_new.data_ptr(), _ARRAY3(*k_new.stride()[:3]),
+                    _ARRAY3(*v_new.stride()[:3]), bits, sb, st, _ints(tree_len, "tree_len", (B,)))
+    keep, wp, wn = _cache_ws(workspace, q)
+    _go(q, stream, lib().masked_gqa_attn_decode_tree, _addr(a),
+        None if pages is None else _addr(pages), _addr(tree), int(window), int(sinks), wp, wn)
+    return out
+
+
+def _cache(k_cache, v_cache, page_table, kv_len, ref, dev_error) -> MgqaCache:
+    """An MgqaCache of tensors [layers, pages, Hkv, page_size, D] (or without
+    the layer dimension)."""
+    ks, vs, sh = k_cache.stride(), v_cache.stride(), k_cache.shape
+    if k_cache.dim() not in (4, 5) or v_cache.shape != sh or ks[-1] != 1 or vs[-1] != 1:
+        raise ValueError("the caches must be [layers, pages, Hkv, page_size, D] (or 4-D, one layer) "
+                         "with a unit-stride head dim")
+    dt = _CODES.get(k_cache.dtype)
+    if dt is None or v_cache.dtype != k_cache.dtype:
+        raise ValueError("the caches must share one dtype of bfloat16, float16, float32")
+    if k_cache.dim() == 4:
+        sh, ks, vs = (1, *sh), (0, *ks), (0, *vs)
+    L, pages, Hkv, page, D = sh
+    rows, mp, tp, ts = pages, 0, None, 0
+    if page_table is not None:
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1:
+            raise ValueError("page_table must be int32 [rows, max_pages] with unit-stride rows")
+        rows, mp = page_table.shape
+        tp, ts = page_table.data_ptr(), page_table.stride(0)
+    return MgqaCache(dt, L, pages, Hkv, page, D, k_cache.data_ptr(), v_cache.data_ptr(),
+                     _ARRAY4(*ks[:4]), _ARRAY4(*vs[:4]), rows, mp, tp, ts,
+                     _ints(kv_len, "kv_len", (rows,)), _ints(ref, "ref", (pages,)),
+                     _ints(dev_error, "dev_error", (1,)))
+
+
+def masked_gqa_cache_append(k_cache, v_cache, k_new, v_new, kv_len, kv_len_out, *, index=None,
+                            count=None, page_table=None, dev_error=None, stream=None):
+    """Append rows of k_new / v_new [layers, B, Hkv, T, D] (4-D with a 4-D
+    cache) to every request: slot kv_len[b] + i of the cache gets row
+    index[b, i] (int32 [B, T]; None: i) for i < count[b] (int32 [B]; None: T).
+    kv_len_out (int32 [B], not kv_len) receives kv_len + count. The cache is
+    [layers, B, Hkv, slots, D], or in pages with page_table int32
+    [B, max_pages]. Returns kv_len_out."""
+    _together(k_cache, v_cache=v_cache, k_new=k_new, v_new=v_new, kv_len=kv_len,
+              kv_len_out=kv_len_out, index=index, count=count, page_table=page_table,
+              dev_error=dev_error)
+    c = _cache(k_cache, v_cache, page_table, kv_len, None, dev_error)
+    if k_new.dim() != k_cache.dim() or v_new.dim() != k_cache.dim():
+        raise ValueError("k_new and v_new need the cache's number of dimensions")
+    T = k_new.shape[-2]
+    want = (c.layers, c.rows, c.Hkv, T, c.D)[5 - k_cache.dim():]
+    strides = []
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if t.dtype != k_cache.dtype or tuple(t.shape) != want or t.stride(-1) != 1:
+            raise ValueError(f"{name} must be {k_cache.dtype} {list(want)} with a unit-stride head dim")
+        st = t.stride()
+        strides.append(_ARRAY4(*st[:4]) if len(st) == 5 else _ARRAY4(0, *st[:3]))
+    if kv_len is None or kv_len_out is None:
+        raise ValueError("kv_len and kv_len_out are required")
+    _go(k_cache, stream, lib().masked_gqa_cache_append, _addr(c), k_new.data_ptr(), v_new.data_ptr(),
+        _addr(strides[0]), _addr(strides[1]), T, _ints(index, "index", (c.rows, T)),
+        _ints(count, "count", (c.rows,)), _ints(kv_len_out, "kv_len_out", (c.rows,)))
+    return kv_len_out
+
+
+def masked_gqa_cache_workspace_size(k_cache, v_cache, page_table, ref, n=0) -> int:
+    """Bytes of the workspace of masked_gqa_cache_fork with n pairs, or (n = 0)
+    of masked_gqa_cache_compact."""
+    c = _cache(k_cache, v_cache, page_table, None, ref, None)
+    size = int(lib().masked_gqa_cache_workspace_size(_addr(c), int(n)))
+    if size == 0:
+        _check(MGQA_ERR_INVALID_ARG)
+    return size
+
+
+def _pages_ws(workspace, c, n, device):
+    if workspace is None:
+        size = int(lib().masked_gqa_cache_workspace_size(_addr(c), n))
+        if size == 0:
+            _check(MGQA_ERR_INVALID_ARG)
+        workspace = torch.empty(size, dtype=torch.uint8, device=device)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def masked_gqa_cache_fork(k_cache, v_cache, page_table, kv_len, ref, src, dst, *, extra=0,
+                          workspace=None, dev_error=None, stream=None):
+    """Requests dst[i] become continuations of src[i] (int32 [n] each): full
+    pages are shared, the last one is copied when partly filled; src == dst
+    keeps a request and makes the pages it writes to its own; src -1 frees it.
+    Then each gets pages for `extra` more tokens. page_table int32
+    [rows, max_pages], kv_len int32 [rows] and ref int32 [pages] (table entries
+    that hold a page) are updated in place; new pages are the free ones of
+    lowest index. The caches are [layers, pages, Hkv, page_size, D] or 4-D."""
+    _together(k_cache, v_cache=v_cache, page_table=page_table, kv_len=kv_len, ref=ref, src=src,
+              dst=dst, workspace=workspace, dev_error=dev_error)
+    if page_table is None or kv_len is None or ref is None:
+        raise ValueError("page_table, kv_len and ref are required")
+    n = src.shape[0] if src.dim() == 1 else -1
+    sp, dp = _ints(src, "src", (n,)), _ints(dst, "dst", (n,))
+    if n == 0:
+        return
+    c = _cache(k_cache, v_cache, page_table, kv_len, ref, dev_error)
+    keep, wp, wn = _pages_ws(workspace, c, n, k_cache.device)
+    _go(k_cache, stream, lib().masked_gqa_cache_fork, _addr(c), n, sp, dp, int(extra), wp, wn)
+
+
+def masked_gqa_cache_compact(k_cache, v_cache, page_table, ref, page_table_out=None, ref_out=None, *,
+                             used_out=None, workspace=None, dev_error=None, stream=None):
+    """Pack the pages in use (ref > 0) to the low end of the pool: keys and
+    values move, page_table_out and ref_out (default: page_table and ref, in
+    place) get the renamed tables and used_out (int32 [1], optional) the number
+    of pages in use. Returns (page_table_out, ref_out)."""
+    _together(k_cache, v_cache=v_cache, page_table=page_table, ref=ref, page_table_out=page_table_out,
+              ref_out=ref_out, used_out=used_out, workspace=workspace, dev_error=dev_error)
+    if page_table is None or ref is None:
+        raise ValueError("page_table and ref are required")
+    page_table_out = page_table if page_table_out is None else page_table_out
+    ref_out = ref if ref_out is None else ref_out
+    c = _cache(k_cache, v_cache, page_table, None, ref, dev_error)
+    tp = _ints(page_table_out, "page_table_out", tuple(page_table.shape), contiguous=False)
+    if page_table_out.stride(1) != 1:
+        raise ValueError("page_table_out must have unit-stride rows")
+    keep, wp, wn = _pages_ws(workspace, c, 0, k_cache.device)
+    _go(k_cache, stream, lib().masked_gqa_cache_compact, _addr(c), tp, page_table_out.stride(0),
+        _ints(ref_out, "ref_out", tuple(ref.shape)), _ints(used_out, "used_out", (1,)), wp, wn)
+    return page_table_out, ref_out

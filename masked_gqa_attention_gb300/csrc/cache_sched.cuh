@@ -1,0 +1,185 @@
+// Work split of the cache attention kernels (one new token, or a tree of
+// drafted tokens, per request over a cache in slots or pages).
+//
+// A request's keys are cut into tiles of kTile keys: the tiles of absolute
+// cache slots that some query of the request may see (the sinks' tiles, then
+// the window's), then the tiles of its drafted tokens. A unit is one (request,
+// KV head, block of query rows) with the request's tiles; the units' tiles form
+// one long row, in the order of the units, which the CTAs cut into equal runs.
+// Rows of very different lengths so cost every CTA the same, whatever the
+// batch. A unit inside one run is finished by its CTA; a unit that crosses a
+// run's end leaves one partial result per run in the workspace, and the merge
+// kernel joins them in ascending order. The cut depends on the lengths, the
+// call's shapes and the device alone, so results repeat bit for bit.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace mgqa {
+
+constexpr int kTile = 64;        // keys of a tile
+constexpr int kMaxDrafts = kMaxDraftsHost;
+constexpr int kNoWindow = 1 << 30;
+
+struct CacheAttnParams {
+  const void *q, *k, *v, *kn, *vn;
+  void *out;
+  int64_t qs[3], ks[3], vs[3], kns[3], vns[3], os[3];  // (batch | page, head, position | slot)
+  const int32_t *table;  // [B][max_pages], null: the static cache (one page per request)
+  int64_t table_stride;
+  int32_t page_size, page_shift;  // page_shift: log2 of a power-of-two page_size, else -1
+  int32_t num_pages, cap;         // cap: slots of a request
+  const int32_t *kv_len, *tree_len;
+  const uint32_t *bits;  // null: each draft sees those before it
+  int64_t bits_b, bits_t;
+  int32_t window, sinks;  // window: kNoWindow when there is none
+  int32_t tree;           // 1: drafts follow the cache; 0: the one query is the last cached token
+  int32_t B, Hq, Hkv, T, n_rep, R, RB;  // R = T * n_rep rows per KV head, in RB blocks
+  int32_t min_run;                      // fewest tiles of a CTA's run
+  float scale_log2;
+  float *lse;
+  int32_t *err;
+  float *part_o;    // [2 * grid][block rows][D] unnormalised partial outputs
+  float2 *part_ml;  // [2 * grid][block rows] their (max, sum)
+};
+
+// What one request's queries may see.
+struct RowPlan {
+  int n;        // cached tokens
+  int live;     // drafted tokens
+  int lo;       // first slot of the window (of the query that reaches furthest back)
+  int s_end;    // sinks in front of it: [0, s_end)
+  int ns, mt0;  // sink tiles; the window's tiles start at tile mt0
+  int np, nt;   // tiles of cached keys; all tiles (at least one, which may be empty)
+};
+
+MGQA_DEV RowPlan plan_row(const CacheAttnParams &p, int b, bool report) {
+  RowPlan r;
+  int n = __ldg(p.kv_len + b);
+  int live = p.tree ? p.T : 0;
+  bool bad = n < 0 || n > p.cap;
+  if (p.tree_len) {
+    live = __ldg(p.tree_len + b);
+    bad = bad || live < 0 || live > p.T;
+    live = min(max(live, 0), p.T);
+  }
+  if (bad && report) report_error(p.err, MGQA_ERR_INVALID_ARG);
+  n = min(max(n, 0), p.cap);
+  r.n = n;
+  r.live = live;
+  const int p0 = p.tree ? n : n - 1;  // the first query's position
+  r.lo = min(max(p0 - p.window + 1, 0), n);
+  r.s_end = min(p.sinks, r.lo);
+  r.ns = (r.s_end + kTile - 1) / kTile;
+  r.mt0 = max(r.lo / kTile, r.ns);
+  r.np = r.ns + max(0, (n + kTile - 1) / kTile - r.mt0);
+  if (p.tree && live == 0) r.np = 0;  // no query is left to see anything
+  r.nt = max(1, r.np + (live + kTile - 1) / kTile);
+  return r;
+}
+
+// The cut of one call: tiles in all, and tiles of a run.
+struct Cut {
+  int64_t total;
+  int64_t run;
+};
+
+// Scans the requests (every thread of the block takes part; scratch: one int64
+// per warp plus four). Finds the cut and, for the flat tile index `want` (a
+// function of the cut), its request and the flat index of that request's first
+// tile. `unit`: instead finds where request `want_b` starts.
+struct Located {
+  Cut cut;
+  int b;          // request holding the wanted tile, or the wanted request
+  int64_t start;  // flat index of its first tile
+};
+
+template <int THREADS>
+MGQA_DEV Located locate(const CacheAttnParams &p, int64_t *scratch, int grid, int cta, int want_b,
+                        bool report) {
+  constexpr int NW = THREADS / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.B + THREADS - 1) / THREADS;
+  const int64_t units = (int64_t)p.Hkv * p.RB;
+  int64_t mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    if (b < p.B) mine += plan_row(p, b, report).nt;
+  }
+  int64_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += up;
+  }
+  if (lane == 31) scratch[warp] = inc;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    if (w < warp) before += scratch[w];
+    total += scratch[w];
+  }
+  before += inc - mine;  // tiles (of one head and row block) of the requests ahead of mine
+  Located r;
+  r.cut.total = total * units;
+  r.cut.run = max((int64_t)p.min_run, (r.cut.total + grid - 1) / grid);
+  const int64_t want = (int64_t)cta * r.cut.run;
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    if (b >= p.B) break;
+    const int nt = plan_row(p, b, false).nt;
+    const bool hit = want_b >= 0 ? b == want_b
+                                 : (want >= before * units && want < (before + nt) * units);
+    if (hit) {
+      scratch[NW] = b;
+      scratch[NW + 1] = before * units;
+    }
+    before += nt;
+  }
+  __syncthreads();
+  r.b = (int)scratch[NW];
+  r.start = scratch[NW + 1];
+  return r;
+}
+
+// Page of slot j of a request (-1: no such page; the slot then counts as
+// masked and the call reports it).
+MGQA_DEV int page_of(const CacheAttnParams &p, int b, int j) {
+  if (!p.table) return b;
+  const int i = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
+  const int pg = __ldg(p.table + (int64_t)b * p.table_stride + i);
+  return (unsigned)pg < (unsigned)p.num_pages ? pg : -1;
+}
+MGQA_DEV int slot_in_page(const CacheAttnParams &p, int j) {
+  if (!p.table) return j;
+  return p.page_shift >= 0 ? j & (p.page_size - 1) : j % p.page_size;
+}
+
+// The drafts' ancestor masks and depths, staged for the masks of a unit:
+// see[t] has the bits of the drafts that draft t sees (live ones only), and
+// depth[t] the number of other drafts among them.
+struct Drafts {
+  uint32_t see[kMaxDrafts][kMaxDrafts / 32];
+  int32_t depth[kMaxDrafts];
+};
+
+MGQA_DEV void stage_drafts(const CacheAttnParams &p, Drafts &d, int b, int live, int tid, int threads) {
+  const int W = (p.T + 31) / 32;
+  for (int t = tid; t < p.T; t += threads) {
+    int depth = 0;
+    for (int w = 0; w < W; ++w) {
+      uint32_t x = p.bits ? __ldg(p.bits + (int64_t)b * p.bits_b + (int64_t)t * p.bits_t + w)
+                          : low_mask(t + 1 - 32 * w);
+      x &= low_mask(live - 32 * w);
+      if (t >= live) x = 0u;
+      d.see[t][w] = x;
+      if (t / 32 == w) x &= ~(1u << (t % 32));
+      depth += __popc(x);
+    }
+    d.depth[t] = depth;
+  }
+}
+
+}  // namespace mgqa

@@ -187,7 +187,19 @@ struct MaskView {
   const int32_t *seg_k;   // [B][Lk]
   int causal;             // key j only for query i with j <= i + coff
   int coff;               // Lk - Lq
+  int window;             // 0: none; else query i at i + coff sees keys less than this far back
+                          // (and ahead, unless causal) and the first `sinks` keys
+  int sinks;
 };
+
+MGQA_DEV uint32_t low_mask(int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : ((1u << n) - 1u)); }
+
+// The window's part of mask_word: keys jbase..jbase+31 that the query at
+// position pos sees by its window or as sinks (the causal limit is apart).
+MGQA_DEV uint32_t window_word(const MaskView &m, int pos, int jbase) {
+  const uint32_t ahead = m.causal ? 0xffffffffu : low_mask(pos + m.window - jbase);
+  return (ahead & ~low_mask(pos - m.window + 1 - jbase)) | low_mask(m.sinks - jbase);
+}
 
 // Bits t = 0..31 of the result: may query i of row b attend to key jbase + t?
 // jbase is a multiple of 32. kvl is the (clamped) kv_len of row b, segq the
@@ -199,6 +211,7 @@ MGQA_DEV uint32_t mask_word(const MaskView &m, int b, int i, int jbase, int Lk, 
   int lim = min(Lk, kvl) - jbase;
   if (m.causal) lim = min(lim, i + m.coff + 1 - jbase);
   uint32_t w = lim >= 32 ? 0xffffffffu : (lim <= 0 ? 0u : ((1u << lim) - 1u));
+  if (m.window) w &= window_word(m, i + m.coff, jbase);
   if (m.bits && w) w &= __ldg(m.bits + (int64_t)b * m.sb + (int64_t)i * m.sq + (jbase >> 5));
   if (m.seg_q && w) {
     if (segq < 0) return 0u;

@@ -16,6 +16,10 @@ mgqa_status fail(mgqa_status code, const char *fmt, ...);
 // Empties the calling thread's error detail (entry points call it first).
 void clear_error_detail();
 
+// Streaming multiprocessors of the current device (0 if unknown), looked up
+// once per device.
+int device_sm_count();
+
 // Raises `kern`'s dynamic shared-memory limit to `bytes` on the current
 // device the first time it launches there. The attribute belongs to a device,
 // so `done` (one per kernel instantiation, owned by its launcher) keeps a bit
@@ -119,6 +123,35 @@ mgqa_status launch_decode_append(const mgqa_args &a, const void *k_new, const vo
                                  int32_t *kv_len_out, cudaStream_t s,
                                  const FusedRope &rope = FusedRope());
 
+// One token (tree null) or a tree of drafted tokens per request over a cache
+// in slots or pages. window <= 0: none.
+constexpr int kCacheAttnMaxCtas = 320;  // partial results in the workspace: two per CTA
+size_t cache_attn_workspace_bytes();
+mgqa_status launch_cache_attn(const mgqa_args &a, const mgqa_pages *pages, const mgqa_tree *tree,
+                              int32_t window, int32_t sinks, void *ws, cudaStream_t s);
+constexpr int kMaxDraftsHost = 256;  // drafted tokens of a request
+
+// The cache's own steps (cache_pages.cu).
+constexpr int kMaxPages = 1 << 20;  // bounds the planning kernels' bitmaps
+constexpr int kMaxForks = 1024;     // pairs of a fork call: one thread each
+size_t cache_pages_workspace_bytes(const mgqa_cache &c, int n);
+mgqa_status launch_cache_append(const mgqa_cache &c, const void *k_new, const void *v_new,
+                                const int64_t *ks, const int64_t *vs, int32_t T,
+                                const int32_t *index, const int32_t *count, int32_t *kv_len_out,
+                                cudaStream_t s);
+mgqa_status launch_cache_fork(const mgqa_cache &c, int n, const int32_t *src, const int32_t *dst,
+                              int32_t extra, void *ws, cudaStream_t s);
+mgqa_status launch_cache_compact(const mgqa_cache &c, int32_t *table_out, int64_t table_out_stride,
+                                 int32_t *ref_out, int32_t *used_out, void *ws, cudaStream_t s);
+
+// A sliding window over the keys (0: none) and the first keys that stay
+// visible. At most kWidestWindow, past any distance, so sums with positions
+// stay in 32 bits.
+constexpr int kWidestWindow = 1 << 26;
+struct WindowRule {
+  int window = 0, sinks = 0;
+};
+
 // Packed-guidance row copies (pack or unpack one pair of sequences).
 mgqa_status pack_pair(bool unpack, mgqa_dtype dt, int B, int H, int D, const void *a,
                       const int64_t *as, int La, const void *b, const int64_t *bs, int Lb,
@@ -132,10 +165,12 @@ bool make_tma_map_4d(CUtensorMap *m, mgqa_dtype dt, const void *base, int B, int
                      const int64_t *st, int box_x, int box_y, bool swizzle128);
 
 // Prefill on the CUDA cores (fp32 I/O).
-mgqa_status launch_prefill_simt(const mgqa_args &a, cudaStream_t s);
+mgqa_status launch_prefill_simt(const mgqa_args &a, cudaStream_t s,
+                                const WindowRule &win = WindowRule());
 
 // Prefill on the tensor cores (bf16 / fp16 I/O): TMA + tcgen05 + TMEM.
 mgqa_status launch_prefill_tc(const mgqa_args &a, cudaStream_t s,
-                              const FusedRope &rope = FusedRope());
+                              const FusedRope &rope = FusedRope(),
+                              const WindowRule &win = WindowRule());
 
 }  // namespace mgqa

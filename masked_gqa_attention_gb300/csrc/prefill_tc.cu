@@ -186,6 +186,7 @@ MGQA_DEV void tile_mask_words(const TcParams &p, int b, int i, bool row_ok, int 
     int lim = min(p.Lk, kvl) - jw;
     if (p.mask.causal) lim = min(lim, i + p.mask.coff + 1 - jw);
     mw[w] = lim >= 32 ? 0xffffffffu : (lim <= 0 ? 0u : ((1u << lim) - 1u));
+    if (p.mask.window) mw[w] &= window_word(p.mask, i + p.mask.coff, jw);
   }
   if (p.mask.bits) {
     const uint32_t *mrow = p.mask.bits + (int64_t)b * p.mask.sb + (int64_t)i * p.mask.sq;
@@ -429,6 +430,17 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   const int g = h0 / p.n_rep;
   const int row0 = qt * BM;
   const int rows = min(BM, p.Lq - row0);
+  // Key tiles that a window leaves to this query tile: the sinks' tiles
+  // [0, w_sink) and [w_lo, w_hi); without a window [0, nkt). The tile loaded
+  // ahead of the classification is the first of them.
+  int w_sink = 0, w_lo = 0, w_hi = p.nkt;
+  if (p.mask.window) {
+    const int first = row0 + p.mask.coff, last = first + rows - 1;  // positions
+    w_sink = min(p.nkt, (p.mask.sinks + BN - 1) / BN);
+    w_lo = max(w_sink, max(0, first - p.mask.window + 1) / BN);
+    w_hi = min(p.nkt, (max(0, p.mask.causal ? last + 1 : last + p.mask.window) + BN - 1) / BN);
+  }
+  const int spec_kt = w_sink > 0 ? 0 : min(w_lo, p.nkt - 1);
 
   // ---- set-up that touches no global memory (may overlap the previous kernel)
   if (tid == 0) pre_stamp(0);
@@ -483,7 +495,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         const int w = u - nq, kv = w / (nk0 / 2), rr = (w / LPR) % min(BN, p.Lk), ln = w % LPR;
         const T *base = static_cast<const T *>(kv ? p.v : p.k);
         const int64_t *st = kv ? p.vs : p.ks;
-        prefetch_l2(base + ((int64_t)b * st[0] + (int64_t)g * st[1] + (int64_t)rr * st[2]) +
+        const int j = min(spec_kt * BN + rr, p.Lk - 1);
+        prefetch_l2(base + ((int64_t)b * st[0] + (int64_t)g * st[1] + (int64_t)j * st[2]) +
                     ln * (128 / (int)sizeof(T)));
       }
     }
@@ -535,10 +548,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     if (MGQA_DCHECK(g < p.Hkv, p.err)) {
       mbar_arrive_expect_tx(bar_kfull, KB * BOX);
       for (int c = 0; c < KB; ++c)
-        tc::tma_load_4d(smem + Lay::k_off + c * BOX, &tm_k, c * 64, 0, g, b, bar_kfull);
+        tc::tma_load_4d(smem + Lay::k_off + c * BOX, &tm_k, c * 64, spec_kt * BN, g, b, bar_kfull);
       mbar_arrive_expect_tx(bar_vfull, KB * BOX);
       for (int c = 0; c < KB; ++c)
-        tc::tma_load_4d(smem + Lay::v_off + c * BOX, &tm_v, c * 64, 0, g, b, bar_vfull);
+        tc::tma_load_4d(smem + Lay::v_off + c * BOX, &tm_v, c * 64, spec_kt * BN, g, b, bar_vfull);
     }
   }
   const int kvl = load_kv_len(p.mask.kv_len, b, p.Lk, p.err, qt == 0 && hp == 0 && tid == 0);
@@ -632,7 +645,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   if (tid == 0) pre_stamp(11);
 
   // ---- classify key tiles: non-empty (ne_bits), and of those full (no masking)
-  for (int kt = warp; kt < p.nkt; kt += nwarps) {
+  const int n_cand = w_sink + max(0, w_hi - w_lo);
+  for (int cand = warp; cand < n_cand; cand += nwarps) {
+    const int kt = cand < w_sink ? cand : w_lo + cand - w_sink;
     const int k0 = kt * BN;
     bool ne = k0 < p.Lk;
     bool full = k0 + BN <= p.Lk;
@@ -643,6 +658,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     if (p.mask.causal) {  // key j for query i when j <= i + coff
       ne = ne && k0 <= row0 + rows - 1 + p.mask.coff;
       full = full && k0 + BN - 1 <= row0 + p.mask.coff;
+    }
+    if (p.mask.window) {  // (the candidates hold a key that some row's window or sinks reach)
+      const int first = row0 + p.mask.coff, last = first + rows - 1;
+      full = full && (k0 + BN <= p.mask.sinks ||
+                      (k0 > last - p.mask.window && (p.mask.causal || k0 + BN <= first + p.mask.window)));
     }
     if (p.mask.bits && ne) {
       ne = (any_bits[kt >> 5] >> (kt & 31)) & 1u;  // ne was true here
@@ -686,9 +706,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     nk = __reduce_add_sync(0xffffffffu, cnt);
   }
   if (tid == 0) pre_stamp(2);
-  // speculation missed when the first non-empty tile is not tile 0: stage 0
-  // then holds a stale tile 0
-  const uint32_t spec_miss = (nk == 0 || (ne_bits[0] & 1u) == 0u) ? 1u : 0u;
+  // speculation missed when the first non-empty tile is not the one loaded
+  // ahead (no candidate lies before it): stage 0 then holds a stale tile
+  const uint32_t spec_miss =
+      (nk == 0 || ((ne_bits[spec_kt >> 5] >> (spec_kt & 31)) & 1u) == 0u) ? 1u : 0u;
   const uint32_t tmem = *tmem_slot;
   const uint32_t sm_base = smem_u32(smem);
   bool ok = true;
@@ -1064,19 +1085,6 @@ bool make_tma_map_4d(CUtensorMap *m, mgqa_dtype dt, const void *base, int B, int
 
 namespace {
 
-// Streaming multiprocessors of the current device (0 if unknown), looked up
-// once per device.
-int sm_count() {
-  static std::atomic<int> cached[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  int n = cached[dev].load(std::memory_order_relaxed);
-  if (n > 0) return n;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 0;
-  cached[dev].store(n, std::memory_order_relaxed);
-  return n;
-}
-
 template <typename T, int D, int NT, int STAGES, bool ROPE>
 mgqa_status launch_t(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                      const CUtensorMap &mo, const TcParams &p, cudaStream_t s) {
@@ -1107,7 +1115,8 @@ mgqa_status dispatch_d(int D, bool pair, const CUtensorMap &mq, const CUtensorMa
 
 }  // namespace
 
-mgqa_status launch_prefill_tc(const mgqa_args &a, cudaStream_t s, const FusedRope &rope) {
+mgqa_status launch_prefill_tc(const mgqa_args &a, cudaStream_t s, const FusedRope &rope,
+                              const WindowRule &win) {
   if (a.dtype != MGQA_BF16 && a.dtype != MGQA_FP16)
     return fail(MGQA_ERR_UNSUPPORTED, "tensor-core prefill takes bf16 or fp16");
   const int nkt = (a.Lk + BN - 1) / BN;
@@ -1121,7 +1130,7 @@ mgqa_status launch_prefill_tc(const mgqa_args &a, cudaStream_t s, const FusedRop
     return fail(MGQA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
   TcParams p{};
   p.mask = MaskView{a.mask_bits, a.mask_stride_b, a.mask_stride_q, a.kv_len, a.seg_q, a.seg_k,
-                    a.causal != 0, a.Lk - a.Lq};
+                    a.causal != 0, a.Lk - a.Lq, win.window, win.sinks};
   p.B = a.B; p.Hq = a.Hq; p.Hkv = a.Hkv; p.Lq = a.Lq; p.Lk = a.Lk;
   p.n_rep = a.Hq / a.Hkv; p.nkt = nkt;
   p.scale_log2 = a.scale * kLog2e;
@@ -1129,7 +1138,7 @@ mgqa_status launch_prefill_tc(const mgqa_args &a, cudaStream_t s, const FusedRop
   p.os[0] = a.o_stride[0]; p.os[1] = a.o_stride[1]; p.os[2] = a.o_stride[2];
   p.q = a.q; p.k = a.k; p.v = a.v;
   {
-    const int sms = sm_count();
+    const int sms = device_sm_count();
     const int64_t ctas = (int64_t)((a.Lq + BM - 1) / BM) * (a.Hq / ((a.Hq / a.Hkv) % 2 == 0 ? 2 : 1)) * a.B;
     p.warm = sms > 0 && ctas <= sms;
   }
