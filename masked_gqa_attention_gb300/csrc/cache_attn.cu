@@ -50,14 +50,6 @@ struct TileLoader {
   static_assert(THREADS % CH == 0 && kTile % RPP == 0, "whole rows per pass");
   int pg[NP];
 
-  // slot (or draft) of row r of tile i of the request; kind: 0 cached, 1 drafted
-  static MGQA_DEV int first_key(const RowPlan &rp, int i, int &kind) {
-    kind = i >= rp.np;
-    return kind ? (i - rp.np) * kTile : (i < rp.ns ? i : rp.mt0 + i - rp.ns) * kTile;
-  }
-  static MGQA_DEV bool wanted(const RowPlan &rp, int kind, int j) {
-    return kind ? j < rp.live : j < rp.n && (j >= rp.lo || j < rp.s_end);
-  }
   MGQA_DEV void look_up(const CacheAttnParams &p, const RowPlan &rp, int b, int i, int tid) {
     int kind;
     const int k0 = first_key(rp, i, kind);
@@ -100,50 +92,6 @@ struct TileLoader {
   }
 };
 
-// Where the finished or partial rows of a piece go. `whole`: the piece is the
-// whole unit.
-struct PieceOut {
-  bool whole;
-  int64_t slot;  // partial slot
-  int b, g, row0, rows;
-};
-
-// Four outputs (row r, features d..d+3) of a piece: o unnormalised, (m, l) of
-// the row in log2 units.
-template <typename T, int D, int BR>
-MGQA_DEV void put_out(const CacheAttnParams &p, const PieceOut &po, int r, int d, float4 o, float m, float l) {
-  if (!po.whole) {
-    *reinterpret_cast<float4 *>(p.part_o + (po.slot * BR + r) * D + d) = o;
-    if (d == 0) p.part_ml[po.slot * BR + r] = make_float2(m, l);
-    return;
-  }
-  const int row = po.row0 + r, t = row / p.n_rep, h = po.g * p.n_rep + row % p.n_rep;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  T *dst = static_cast<T *>(p.out) + (int64_t)po.b * p.os[0] + (int64_t)h * p.os[1] + (int64_t)t * p.os[2] + d;
-  if constexpr (sizeof(T) == 2) {
-    *reinterpret_cast<uint2 *>(dst) =
-        make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
-  } else {
-    *reinterpret_cast<float4 *>(dst) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-  }
-  if (d == 0 && p.lse)
-    p.lse[((int64_t)po.b * p.Hq + h) * p.T + t] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-}
-
-// Which keys of a partial tile a row may see.
-struct RowSight {
-  bool ok;       // the row exists and its draft is live
-  int t, lo;     // its draft; first slot of its window
-};
-
-MGQA_DEV bool sees_cached(const CacheAttnParams &p, const RowSight &rs, int j) {
-  return rs.ok && (j >= rs.lo || j < p.sinks);
-}
-MGQA_DEV bool sees_draft(const CacheAttnParams &p, const Drafts &d, const RowSight &rs, int n, int s) {
-  if (!rs.ok || !((d.see[rs.t][s >> 5] >> (s & 31)) & 1u)) return false;
-  return n + d.depth[s] >= rs.lo || n + d.depth[s] < p.sinks;
-}
-
 // ---- 16-bit: mma.sync -----------------------------------------------------------
 
 template <int D, int WM>
@@ -157,7 +105,7 @@ struct MmaCfg {
   static constexpr int ring = STAGES * 2 * TILEB;
   static_assert(WK * ROWS * OP * 4 <= ring, "the joined output fits in the ring");
   struct Misc {
-    Drafts drafts;
+    Drafts<kMaxDrafts> drafts;
     int64_t scratch[8];
     float wm[WK][ROWS], wl[WK][ROWS];
     uint8_t ok[STAGES][kTile];
@@ -184,28 +132,16 @@ cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
   grid_dependency_wait();
   allow_dependents();  // the merge kernel; lengths and tables are final from here on
   const Located loc = locate<kThreads>(p, sm.scratch, gridDim.x, blockIdx.x, -1, blockIdx.x == 0);
-  int64_t f = (int64_t)blockIdx.x * loc.cut.run;
-  const int64_t f1 = min(f + loc.cut.run, loc.cut.total);
-  const int units = p.Hkv * p.RB;
-  int b = loc.b;
-  int64_t base = loc.start;
-  RowPlan rp;
-  if (f < f1) rp = plan_row(p, b, false);
+  Walker walk;
+  walk.start(p, loc, blockIdx.x);
+  Piece pc;
   int staged = -1;  // request whose drafts are staged
 
-  while (f < f1) {
-    const int64_t rel = f - base;
-    if (rel >= (int64_t)units * rp.nt) {
-      base += (int64_t)units * rp.nt;
-      rp = plan_row(p, ++b, false);
-      continue;
-    }
-    const int unit = (int)(rel / rp.nt), t0 = (int)(rel - (int64_t)unit * rp.nt);
-    const int t1 = (int)min((int64_t)rp.nt, t0 + (f1 - f));
-    f += t1 - t0;
-    const int g = unit / p.RB, row0 = (unit % p.RB) * ROWS;
-    PieceOut po{t0 == 0 && t1 == rp.nt, (int64_t)blockIdx.x * 2 + (t0 > 0 ? 0 : 1), b, g, row0,
-                min(ROWS, p.R - row0)};
+  while (walk.next(p, pc)) {
+    const RowPlan &rp = pc.rp;
+    const int b = pc.b, g = pc.g, t0 = pc.t0, t1 = pc.t1;
+    const PieceOut po = out_of(p, pc, blockIdx.x, ROWS);
+    const int row0 = po.row0;
 
     // ---- the first tiles' copies, then q and the drafts' masks
     TileLoader<T, D, kThreads> ld;
@@ -288,7 +224,7 @@ cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
         }
       // scale and mask
       int kind;
-      const int k0 = TileLoader<T, D, kThreads>::first_key(rp, t0 + i, kind);
+      const int k0 = first_key(rp, t0 + i, kind);
       const bool full = !kind && !sm.bad && k0 + kTile <= rp.n &&
                         (k0 >= lo_all || k0 + kTile <= min(p.sinks, rp.s_end));
       if (full) {
@@ -393,7 +329,7 @@ cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
     for (int u = tid; u < po.rows * (D / 4); u += kThreads) {
       const int r = u / (D / 4), d = (u % (D / 4)) * 4;
       float mr = -INFINITY, lr = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < WK; ++w) mr = fmaxf(mr, sm.wm[w][r]);
 #pragma unroll
@@ -401,12 +337,12 @@ cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
         if (sm.wm[w][r] == -INFINITY) continue;
         lr = fmaf(sm.wl[w][r], fast_exp2(sm.wm[w][r] - mr), lr);
         const float4 x = *reinterpret_cast<const float4 *>(jo + (w * ROWS + r) * Cfg::OP + d);
-        acc.x += x.x;
-        acc.y += x.y;
-        acc.z += x.z;
-        acc.w += x.w;
+        acc[0] += x.x;
+        acc[1] += x.y;
+        acc[2] += x.z;
+        acc[3] += x.w;
       }
-      put_out<T, D, ROWS>(p, po, r, d, acc, mr, lr);
+      put_out<T, D, ROWS, 4>(p, po, r, d, acc, mr, lr);
     }
   }
 }
@@ -422,7 +358,7 @@ struct SimtCfg {
   static constexpr int TILEF = kTile * RP;
   static constexpr int floats = STAGES * 2 * TILEF + ROWS * RP + ROWS * PP;
   struct Misc {
-    Drafts drafts;
+    Drafts<kMaxDrafts> drafts;
     int64_t scratch[16];
     uint8_t ok[STAGES][kTile];
     int bad, maxdepth;
@@ -446,28 +382,16 @@ cache_attn_fp32_kernel(const __grid_constant__ CacheAttnParams p) {
   grid_dependency_wait();
   allow_dependents();
   const Located loc = locate<kSimtThreads>(p, sm.scratch, gridDim.x, blockIdx.x, -1, blockIdx.x == 0);
-  int64_t f = (int64_t)blockIdx.x * loc.cut.run;
-  const int64_t f1 = min(f + loc.cut.run, loc.cut.total);
-  const int units = p.Hkv * p.RB;
-  int b = loc.b;
-  int64_t base = loc.start;
-  RowPlan rp;
-  if (f < f1) rp = plan_row(p, b, false);
+  Walker walk;
+  walk.start(p, loc, blockIdx.x);
+  Piece pc;
   int staged = -1;
 
-  while (f < f1) {
-    const int64_t rel = f - base;
-    if (rel >= (int64_t)units * rp.nt) {
-      base += (int64_t)units * rp.nt;
-      rp = plan_row(p, ++b, false);
-      continue;
-    }
-    const int unit = (int)(rel / rp.nt), t0 = (int)(rel - (int64_t)unit * rp.nt);
-    const int t1 = (int)min((int64_t)rp.nt, t0 + (f1 - f));
-    f += t1 - t0;
-    const int g = unit / p.RB, row0 = (unit % p.RB) * ROWS;
-    PieceOut po{t0 == 0 && t1 == rp.nt, (int64_t)blockIdx.x * 2 + (t0 > 0 ? 0 : 1), b, g, row0,
-                min(ROWS, p.R - row0)};
+  while (walk.next(p, pc)) {
+    const RowPlan &rp = pc.rp;
+    const int b = pc.b, g = pc.g, t0 = pc.t0, t1 = pc.t1;
+    const PieceOut po = out_of(p, pc, blockIdx.x, ROWS);
+    const int row0 = po.row0;
     TileLoader<float, D, kSimtThreads> ld;
     const int nt = t1 - t0;
     if (tid == 0) {
@@ -552,7 +476,7 @@ cache_attn_fp32_kernel(const __grid_constant__ CacheAttnParams p) {
         }
       }
       int kind;
-      const int k0 = TileLoader<float, D, kSimtThreads>::first_key(rp, t0 + i, kind);
+      const int k0 = first_key(rp, t0 + i, kind);
       const bool full = !kind && !sm.bad && k0 + kTile <= rp.n &&
                         (k0 >= lo_all || k0 + kTile <= min(p.sinks, rp.s_end));
 #pragma unroll
@@ -615,11 +539,10 @@ cache_attn_fp32_kernel(const __grid_constant__ CacheAttnParams p) {
       const bool none = !sight[a].ok;
       if (r < po.rows)
 #pragma unroll
-        for (int c = 0; c < ND; ++c)
-          put_out<float, D, ROWS>(p, po, r, tx * 4 + 64 * c,
-                                  none ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                       : make_float4(o[a][c][0], o[a][c][1], o[a][c][2], o[a][c][3]),
-                                  none ? -INFINITY : m[a], none ? 0.f : ls);
+        for (int c = 0; c < ND; ++c) {
+          if (none) o[a][c][0] = o[a][c][1] = o[a][c][2] = o[a][c][3] = 0.f;
+          put_out<float, D, ROWS, 4>(p, po, r, tx * 4 + 64 * c, o[a][c], none ? -INFINITY : m[a], none ? 0.f : ls);
+        }
     }
   }
 }
@@ -651,7 +574,7 @@ cache_merge_kernel(const __grid_constant__ CacheAttnParams p, int grid) {
   for (int u = threadIdx.x; u < (r1 - r0) * (D / 4); u += kMergeThreads) {
     const int r = r0 + u / (D / 4), d = (u % (D / 4)) * 4;
     float m = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
     for (int64_t x = first; x <= last; ++x)
       m = fmaxf(m, p.part_ml[(2 * x + (x == first)) * BR + r].x);
@@ -663,25 +586,17 @@ cache_merge_kernel(const __grid_constant__ CacheAttnParams p, int grid) {
       const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
       l = fmaf(ml.y, w, l);
       if (w != 0.f) {
-        acc.x = fmaf(v.x, w, acc.x);
-        acc.y = fmaf(v.y, w, acc.y);
-        acc.z = fmaf(v.z, w, acc.z);
-        acc.w = fmaf(v.w, w, acc.w);
+        acc[0] = fmaf(v.x, w, acc[0]);
+        acc[1] = fmaf(v.y, w, acc[1]);
+        acc[2] = fmaf(v.z, w, acc[2]);
+        acc[3] = fmaf(v.w, w, acc[3]);
       }
     }
-    put_out<T, D, BR>(p, po, r, d, acc, m, l);
+    put_out<T, D, BR, 4>(p, po, r, d, acc, m, l);
   }
 }
 
 // ---- host side ---------------------------------------------------------------------
-
-// CTAs of the attention kernel: a fixed number per SM, fewer when even the
-// longest possible rows have fewer tiles.
-int64_t most_tiles(const CacheAttnParams &p) {
-  const int64_t span = (int64_t)p.window + p.T + p.sinks + 4 * kTile;
-  const int64_t keys = std::min<int64_t>(p.cap, span);
-  return ((keys + kTile - 1) / kTile + 2 + (p.T + kTile - 1) / kTile) * (int64_t)p.B * p.Hkv * p.RB;
-}
 
 template <typename T, int D, int BR>
 mgqa_status launch_merge(const CacheAttnParams &p, int grid, cudaStream_t s) {
@@ -690,45 +605,51 @@ mgqa_status launch_merge(const CacheAttnParams &p, int grid, cudaStream_t s) {
   if (e != cudaSuccess) return fail(MGQA_ERR_CUDA, "cache attention merge launch: %s", cudaGetErrorString(e));
   return MGQA_OK;
 }
+template <typename T, int D>
+mgqa_status launch_merge(const CacheAttnParams &p, int block_rows, int grid, cudaStream_t s) {
+  switch (block_rows) {
+    case 16: return launch_merge<T, D, 16>(p, grid, s);
+    case 32: return launch_merge<T, D, 32>(p, grid, s);
+    case 64: return launch_merge<T, D, 64>(p, grid, s);
+    default: return fail(MGQA_ERR_UNSUPPORTED, "merge: blocks of %d rows", block_rows);
+  }
+}
 
 template <typename T, int D, int BR, typename Kern>
-mgqa_status launch_with(Kern kern, int smem, std::atomic<uint64_t> &attr, int threads, int per_sm, int min_run,
-                        CacheAttnParams p, void *ws, cudaStream_t s) {
+mgqa_status launch_with(Kern kern, int smem, std::atomic<uint64_t> &attr, int threads, int per_sm, CacheAttnParams p,
+                        const CacheAttnLaunch &how, cudaStream_t s) {
   mgqa_status st = ensure_smem_attr(kern, smem, attr, "cache attention kernel");
   if (st != MGQA_OK) return st;
-  const int sms = device_sm_count();
-  if (sms < 1) return fail(MGQA_ERR_CUDA, "cannot read the SM count of the current device");
   p.RB = (p.R + BR - 1) / BR;
-  p.min_run = min_run;
-  const int grid = (int)std::max<int64_t>(
-      1, std::min<int64_t>(std::min(sms * per_sm, kCacheAttnMaxCtas), most_tiles(p)));
-  p.part_o = static_cast<float *>(ws);
-  p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)2 * grid * BR * D);
+  p.min_run = 2;
+  const int64_t tiles = (int64_t)p.B * p.Hkv * p.RB * most_tiles(p);
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(how.sms * per_sm, kCacheAttnMaxCtas), tiles));
+  set_partials(p, how.workspace, grid, BR, D);
   const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(threads), smem, s, p);
   if (e != cudaSuccess) return fail(MGQA_ERR_CUDA, "cache attention launch: %s", cudaGetErrorString(e));
   return launch_merge<T, D, BR>(p, grid, s);
 }
 
 template <typename T, int D, int WM>
-mgqa_status launch_mma(const CacheAttnParams &p, void *ws, cudaStream_t s) {
+mgqa_status launch_mma(const CacheAttnParams &p, const CacheAttnLaunch &how, cudaStream_t s) {
   static std::atomic<uint64_t> attr{0};
   using Cfg = MmaCfg<D, WM>;
-  return launch_with<T, D, Cfg::ROWS>(cache_attn_kernel<T, D, WM>, Cfg::smem, attr, kThreads, 2, 2, p, ws, s);
+  return launch_with<T, D, Cfg::ROWS>(cache_attn_kernel<T, D, WM>, Cfg::smem, attr, kThreads, 2, p, how, s);
 }
 
 template <typename T, int D>
-mgqa_status launch_16bit(const CacheAttnParams &p, void *ws, cudaStream_t s) {
+mgqa_status launch_16bit(const CacheAttnParams &p, const CacheAttnLaunch &how, cudaStream_t s) {
   // the smallest row block that holds the unit's rows
-  if (p.R <= 16) return launch_mma<T, D, 1>(p, ws, s);
-  if (p.R <= 32) return launch_mma<T, D, 2>(p, ws, s);
-  return launch_mma<T, D, 4>(p, ws, s);
+  if (p.R <= 16) return launch_mma<T, D, 1>(p, how, s);
+  if (p.R <= 32) return launch_mma<T, D, 2>(p, how, s);
+  return launch_mma<T, D, 4>(p, how, s);
 }
 
 template <int D, int RPT>
-mgqa_status launch_simt(const CacheAttnParams &p, void *ws, cudaStream_t s) {
+mgqa_status launch_simt(const CacheAttnParams &p, const CacheAttnLaunch &how, cudaStream_t s) {
   static std::atomic<uint64_t> attr{0};
   using Cfg = SimtCfg<D, RPT>;
-  return launch_with<float, D, Cfg::ROWS>(cache_attn_fp32_kernel<D, RPT>, Cfg::smem, attr, kSimtThreads, 1, 2, p, ws, s);
+  return launch_with<float, D, Cfg::ROWS>(cache_attn_fp32_kernel<D, RPT>, Cfg::smem, attr, kSimtThreads, 1, p, how, s);
 }
 
 }  // namespace
@@ -736,6 +657,14 @@ mgqa_status launch_simt(const CacheAttnParams &p, void *ws, cudaStream_t s) {
 size_t cache_attn_workspace_bytes() {
   // two partial results per CTA: up to 64 rows of (D + 2) floats, two CTAs an SM
   return (size_t)kCacheAttnMaxCtas * 2 * 64 * (128 + 2) * sizeof(float);
+}
+
+mgqa_status launch_cache_merge(const CacheAttnParams &p, mgqa_dtype dt, int D, int block_rows, int grid,
+                               cudaStream_t s) {
+  if (dt == MGQA_BF16)
+    return D == 64 ? launch_merge<__nv_bfloat16, 64>(p, block_rows, grid, s)
+                   : launch_merge<__nv_bfloat16, 128>(p, block_rows, grid, s);
+  return D == 64 ? launch_merge<__half, 64>(p, block_rows, grid, s) : launch_merge<__half, 128>(p, block_rows, grid, s);
 }
 
 mgqa_status launch_cache_attn(const mgqa_args &a, const mgqa_pages *pages, const mgqa_tree *tree, int32_t window,
@@ -776,14 +705,17 @@ mgqa_status launch_cache_attn(const mgqa_args &a, const mgqa_pages *pages, const
   p.R = p.T * p.n_rep;
   p.scale_log2 = a.scale * kLog2e;
   p.lse = a.lse; p.err = a.dev_error;
+  const CacheAttnLaunch how{ws, device_sm_count()};
+  if (how.sms < 1) return fail(MGQA_ERR_CUDA, "cannot read the SM count of the current device");
+  if (cache_attn_tma_takes(p, a.dtype)) return launch_cache_attn_tma(p, a.dtype, a.D, how, s);
   if (a.dtype == MGQA_BF16)
-    return a.D == 64 ? launch_16bit<__nv_bfloat16, 64>(p, ws, s)
-                     : launch_16bit<__nv_bfloat16, 128>(p, ws, s);
+    return a.D == 64 ? launch_16bit<__nv_bfloat16, 64>(p, how, s)
+                     : launch_16bit<__nv_bfloat16, 128>(p, how, s);
   if (a.dtype == MGQA_FP16)
-    return a.D == 64 ? launch_16bit<__half, 64>(p, ws, s) : launch_16bit<__half, 128>(p, ws, s);
+    return a.D == 64 ? launch_16bit<__half, 64>(p, how, s) : launch_16bit<__half, 128>(p, how, s);
   if (a.D == 64)
-    return p.R <= 16 ? launch_simt<64, 1>(p, ws, s) : launch_simt<64, 4>(p, ws, s);
-  return p.R <= 16 ? launch_simt<128, 1>(p, ws, s) : launch_simt<128, 4>(p, ws, s);
+    return p.R <= 16 ? launch_simt<64, 1>(p, how, s) : launch_simt<64, 4>(p, how, s);
+  return p.R <= 16 ? launch_simt<128, 1>(p, how, s) : launch_simt<128, 4>(p, how, s);
 }
 
 }  // namespace mgqa

@@ -44,6 +44,32 @@ struct CacheAttnParams {
   float2 *part_ml;  // [2 * grid][block rows] their (max, sum)
 };
 
+// What every launcher of the cache attention needs besides the parameters.
+struct CacheAttnLaunch {
+  void *workspace;
+  int sms;
+};
+
+// Tiles of one unit (a request's keys), at most.
+inline int64_t most_tiles(const CacheAttnParams &p) {
+  const int64_t span = (int64_t)p.window + p.T + p.sinks + 4 * kTile;
+  const int64_t keys = p.cap < span ? p.cap : span;
+  return (keys + kTile - 1) / kTile + 2 + (p.T + kTile - 1) / kTile;
+}
+
+// The workspace as the partial results of `grid` CTAs (two each).
+inline void set_partials(CacheAttnParams &p, void *ws, int grid, int block_rows, int D) {
+  p.part_o = static_cast<float *>(ws);
+  p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)2 * grid * block_rows * D);
+}
+
+mgqa_status launch_cache_merge(const CacheAttnParams &p, mgqa_dtype dt, int D, int block_rows, int grid,
+                               cudaStream_t s);
+// TMA-fed kernels (16-bit; slots, or pages of a multiple of 8 slots; few rows).
+bool cache_attn_tma_takes(const CacheAttnParams &p, mgqa_dtype dt);
+mgqa_status launch_cache_attn_tma(const CacheAttnParams &p, mgqa_dtype dt, int D, const CacheAttnLaunch &how,
+                                  cudaStream_t s);
+
 // What one request's queries may see.
 struct RowPlan {
   int n;        // cached tokens
@@ -73,7 +99,7 @@ MGQA_DEV RowPlan plan_row(const CacheAttnParams &p, int b, bool report) {
   r.s_end = min(p.sinks, r.lo);
   r.ns = (r.s_end + kTile - 1) / kTile;
   r.mt0 = max(r.lo / kTile, r.ns);
-  r.np = r.ns + max(0, (n + kTile - 1) / kTile - r.mt0);
+  r.np = r.ns + (r.lo < n ? max(0, (n + kTile - 1) / kTile - r.mt0) : 0);
   if (p.tree && live == 0) r.np = 0;  // no query is left to see anything
   r.nt = max(1, r.np + (live + kTile - 1) / kTile);
   return r;
@@ -160,12 +186,14 @@ MGQA_DEV int slot_in_page(const CacheAttnParams &p, int j) {
 // The drafts' ancestor masks and depths, staged for the masks of a unit:
 // see[t] has the bits of the drafts that draft t sees (live ones only), and
 // depth[t] the number of other drafts among them.
+template <int MAXT>
 struct Drafts {
-  uint32_t see[kMaxDrafts][kMaxDrafts / 32];
-  int32_t depth[kMaxDrafts];
+  uint32_t see[MAXT][MAXT / 32];
+  int32_t depth[MAXT];
 };
 
-MGQA_DEV void stage_drafts(const CacheAttnParams &p, Drafts &d, int b, int live, int tid, int threads) {
+template <int MAXT>
+MGQA_DEV void stage_drafts(const CacheAttnParams &p, Drafts<MAXT> &d, int b, int live, int tid, int threads) {
   const int W = (p.T + 31) / 32;
   for (int t = tid; t < p.T; t += threads) {
     int depth = 0;
@@ -180,6 +208,109 @@ MGQA_DEV void stage_drafts(const CacheAttnParams &p, Drafts &d, int b, int live,
     }
     d.depth[t] = depth;
   }
+}
+
+// Which keys of a partial tile a row may see.
+struct RowSight {
+  bool ok;    // the row exists and its draft is live
+  int t, lo;  // its draft; first slot of its window
+};
+
+MGQA_DEV bool sees_cached(const CacheAttnParams &p, const RowSight &rs, int j) {
+  return rs.ok && (j >= rs.lo || j < p.sinks);
+}
+template <int MAXT>
+MGQA_DEV bool sees_draft(const CacheAttnParams &p, const Drafts<MAXT> &d, const RowSight &rs, int n, int s) {
+  if (!rs.ok || !((d.see[rs.t][s >> 5] >> (s & 31)) & 1u)) return false;
+  return n + d.depth[s] >= rs.lo || n + d.depth[s] < p.sinks;
+}
+
+// Slot (or draft) of the first key of tile i of a request; kind: 0 cached, 1 drafted.
+MGQA_DEV int first_key(const RowPlan &rp, int i, int &kind) {
+  kind = i >= rp.np;
+  return kind ? (i - rp.np) * kTile : (i < rp.ns ? i : rp.mt0 + i - rp.ns) * kTile;
+}
+// Does key j of that kind count for any query?
+MGQA_DEV bool wanted(const RowPlan &rp, int kind, int j) {
+  return kind ? j < rp.live : j < rp.n && (j >= rp.lo || j < rp.s_end);
+}
+
+// The pieces of a CTA's run, in order: runs of tiles [t0, t1) of one unit.
+struct Piece {
+  RowPlan rp;
+  int b, g, rb, t0, t1;
+};
+struct Walker {
+  int64_t f, f1, base;
+  int b, units, RB;
+  RowPlan rp;
+
+  MGQA_DEV void start(const CacheAttnParams &p, const Located &loc, int cta) {
+    f = (int64_t)cta * loc.cut.run;
+    f1 = min(f + loc.cut.run, loc.cut.total);
+    base = loc.start;
+    b = loc.b;
+    RB = p.RB;
+    units = p.Hkv * p.RB;
+    if (f < f1) rp = plan_row(p, b, false);
+  }
+  MGQA_DEV bool next(const CacheAttnParams &p, Piece &pc) {
+    if (f >= f1) return false;
+    while (f - base >= (int64_t)units * rp.nt) {
+      base += (int64_t)units * rp.nt;
+      rp = plan_row(p, ++b, false);
+    }
+    const int64_t rel = f - base;
+    const int unit = (int)(rel / rp.nt);
+    pc.rp = rp;
+    pc.b = b;
+    pc.g = unit / RB;
+    pc.rb = unit % RB;
+    pc.t0 = (int)(rel - (int64_t)unit * rp.nt);
+    pc.t1 = (int)min((int64_t)rp.nt, pc.t0 + (f1 - f));
+    f += pc.t1 - pc.t0;
+    return true;
+  }
+};
+
+// Where the finished or partial rows of a piece go. `whole`: the piece is the
+// whole unit.
+struct PieceOut {
+  bool whole;
+  int64_t slot;  // partial slot
+  int b, g, row0, rows;
+};
+MGQA_DEV PieceOut out_of(const CacheAttnParams &p, const Piece &pc, int cta, int block_rows) {
+  return PieceOut{pc.t0 == 0 && pc.t1 == pc.rp.nt, (int64_t)cta * 2 + (pc.t0 > 0 ? 0 : 1), pc.b, pc.g,
+                  pc.rb * block_rows, min(block_rows, p.R - pc.rb * block_rows)};
+}
+
+// N consecutive outputs (row r, features d..) of a piece: o unnormalised,
+// (m, l) of the row in log2 units. BR: rows of a block.
+template <typename T, int D, int BR, int N>
+MGQA_DEV void put_out(const CacheAttnParams &p, const PieceOut &po, int r, int d, const float (&o)[N], float m,
+                      float l) {
+  static_assert(N == 2 || N == 4, "pairs or quads");
+  if (!po.whole) {
+    float *dst = p.part_o + (po.slot * BR + r) * D + d;
+    if constexpr (N == 4) *reinterpret_cast<float4 *>(dst) = make_float4(o[0], o[1], o[2], o[3]);
+    else *reinterpret_cast<float2 *>(dst) = make_float2(o[0], o[1]);
+    if (d == 0) p.part_ml[po.slot * BR + r] = make_float2(m, l);
+    return;
+  }
+  const int row = po.row0 + r, t = row / p.n_rep, h = po.g * p.n_rep + row % p.n_rep;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  T *dst = static_cast<T *>(p.out) + (int64_t)po.b * p.os[0] + (int64_t)h * p.os[1] + (int64_t)t * p.os[2] + d;
+  if constexpr (sizeof(T) == 4) {
+    if constexpr (N == 4) *reinterpret_cast<float4 *>(dst) = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+    else *reinterpret_cast<float2 *>(dst) = make_float2(o[0] * inv, o[1] * inv);
+  } else {
+    if constexpr (N == 4)
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv));
+    else *reinterpret_cast<uint32_t *>(dst) = pack2<T>(o[0] * inv, o[1] * inv);
+  }
+  if (d == 0 && p.lse)
+    p.lse[((int64_t)po.b * p.Hq + h) * p.T + t] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 }  // namespace mgqa
