@@ -37,6 +37,19 @@ def test_struct_layout_matches_header(tmp_path, cname, py):
     assert int(got["size"]) == ctypes.sizeof(py)
 
 
+@pytest.mark.parametrize("packer,py", [(M._ARGS, M.MgqaArgs), (M._PAGES, M.MgqaPages), (M._TREE, M.MgqaTree),
+                                       (M._CACHE, M.MgqaCache)])
+def test_packed_structs_have_the_mirrors_layout(packer, py):
+    # every value lands in its own field: pack 1, 2, 3, ... and read them through the mirror
+    n = len(packer.unpack(bytes(packer.size)))
+    got = py.from_buffer_copy(packer.pack(*range(1, n + 1)))
+    flat = []
+    for f, _ in py._fields_:
+        x = getattr(got, f)
+        flat += list(x) if hasattr(x, "__len__") else [x]
+    assert packer.size == ctypes.sizeof(py) and [int(x) for x in flat] == list(range(1, n + 1))
+
+
 def args(Lq=1, cap=1024, B=2):
     a = M.MgqaArgs()
     a.dtype = M.MGQA_BF16
