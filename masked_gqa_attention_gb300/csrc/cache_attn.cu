@@ -52,7 +52,7 @@ struct TileLoader {
 
   MGQA_DEV void look_up(const CacheAttnParams &p, const RowPlan &rp, int b, int i, int tid) {
     int kind;
-    const int k0 = first_key(rp, i, kind);
+    const int k0 = first_key(rp, i, 6, kind);
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
       const int j = k0 + tid / CH + u * RPP;
@@ -66,7 +66,7 @@ struct TileLoader {
   MGQA_DEV void issue(const CacheAttnParams &p, const RowPlan &rp, int g, int i, int tid,
                       uint32_t kdst, uint32_t vdst, uint8_t *ok, int *bad, RowAddr row_addr) const {
     int kind;
-    const int k0 = first_key(rp, i, kind);
+    const int k0 = first_key(rp, i, 6, kind);
     const char *kb = static_cast<const char *>(kind ? p.kn : p.k);
     const char *vb = static_cast<const char *>(kind ? p.vn : p.v);
     const int64_t *ks = kind ? p.kns : p.ks, *vs = kind ? p.vns : p.vs;
@@ -224,7 +224,7 @@ cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
         }
       // scale and mask
       int kind;
-      const int k0 = first_key(rp, t0 + i, kind);
+      const int k0 = first_key(rp, t0 + i, 6, kind);
       const bool full = !kind && !sm.bad && k0 + kTile <= rp.n &&
                         (k0 >= lo_all || k0 + kTile <= min(p.sinks, rp.s_end));
       if (full) {
@@ -476,7 +476,7 @@ cache_attn_fp32_kernel(const __grid_constant__ CacheAttnParams p) {
         }
       }
       int kind;
-      const int k0 = first_key(rp, t0 + i, kind);
+      const int k0 = first_key(rp, t0 + i, 6, kind);
       const bool full = !kind && !sm.bad && k0 + kTile <= rp.n &&
                         (k0 >= lo_all || k0 + kTile <= min(p.sinks, rp.s_end));
 #pragma unroll
@@ -611,6 +611,8 @@ mgqa_status launch_merge(const CacheAttnParams &p, int block_rows, int grid, cud
     case 16: return launch_merge<T, D, 16>(p, grid, s);
     case 32: return launch_merge<T, D, 32>(p, grid, s);
     case 64: return launch_merge<T, D, 64>(p, grid, s);
+    case 128: return launch_merge<T, D, 128>(p, grid, s);
+    case 256: return launch_merge<T, D, 256>(p, grid, s);
     default: return fail(MGQA_ERR_UNSUPPORTED, "merge: blocks of %d rows", block_rows);
   }
 }
@@ -621,6 +623,7 @@ mgqa_status launch_with(Kern kern, int smem, std::atomic<uint64_t> &attr, int th
   mgqa_status st = ensure_smem_attr(kern, smem, attr, "cache attention kernel");
   if (st != MGQA_OK) return st;
   p.RB = (p.R + BR - 1) / BR;
+  p.tile_shift = 6;
   p.min_run = 2;
   const int64_t tiles = (int64_t)p.B * p.Hkv * p.RB * most_tiles(p);
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(how.sms * per_sm, kCacheAttnMaxCtas), tiles));
@@ -655,8 +658,9 @@ mgqa_status launch_simt(const CacheAttnParams &p, const CacheAttnLaunch &how, cu
 }  // namespace
 
 size_t cache_attn_workspace_bytes() {
-  // two partial results per CTA: up to 64 rows of (D + 2) floats, two CTAs an SM
-  return (size_t)kCacheAttnMaxCtas * 2 * 64 * (128 + 2) * sizeof(float);
+  // two partial results per CTA, rows of D + 2 floats: up to 64 rows with two
+  // CTAs an SM, up to 256 with one
+  return (size_t)kCacheAttnMaxCtas / 2 * 2 * 256 * (128 + 2) * sizeof(float);
 }
 
 mgqa_status launch_cache_merge(const CacheAttnParams &p, mgqa_dtype dt, int D, int block_rows, int grid,
@@ -708,6 +712,7 @@ mgqa_status launch_cache_attn(const mgqa_args &a, const mgqa_pages *pages, const
   const CacheAttnLaunch how{ws, device_sm_count()};
   if (how.sms < 1) return fail(MGQA_ERR_CUDA, "cannot read the SM count of the current device");
   if (cache_attn_tma_takes(p, a.dtype)) return launch_cache_attn_tma(p, a.dtype, a.D, how, s);
+  if (cache_attn_tc_takes(p, a.dtype)) return launch_cache_attn_tc(p, a.dtype, a.D, how, s);
   if (a.dtype == MGQA_BF16)
     return a.D == 64 ? launch_16bit<__nv_bfloat16, 64>(p, how, s)
                      : launch_16bit<__nv_bfloat16, 128>(p, how, s);

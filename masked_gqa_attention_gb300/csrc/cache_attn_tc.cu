@@ -1,0 +1,556 @@
+// The 16-bit cache attention for more than 64 query rows per KV head (trees of
+// drafted tokens over grouped heads): the formulas of cache_attn.cu on the
+// 5th-generation tensor cores, over slots or pages of a multiple of 8 slots.
+//
+// With R rows per KV head a key costs 4 R D operations for its 4 D bytes: at
+// R = 256 the products take about as long as the reads, and mma.sync reaches a
+// fraction of the tensor rate, so here the scores and outputs live in tensor
+// memory. A CTA holds one block of up to 128 NT query rows (row = draft *
+// group + head, so a tile of keys serves every head of the group) and walks
+// its run of the flat tile list (cache_sched.cuh), one CTA an SM:
+//   warp 0      : follows the page table, K and V boxes of 128-key tiles by TMA
+//   warp 1      : tensor memory, the MMA loop (one elected lane issues)
+//   warps 4..   : one softmax warpgroup per 128 rows (thread = row)
+// Per tile n and row block t: S_t = Q_t K_n^T; softmax (running maximum, lazy
+// rescale of O_t past 2^8) hands P_t over in tensor memory; O_t += P_t V_n and
+// at once S_t(n+1), as in the prefill kernel. Between two pieces the softmax
+// warpgroups read O_t out, load the next Q_t and release both by mbarriers; K
+// and V of the next piece are already on their way. Values of keys that do not
+// count (the end of a request, a missing page) are cleared in shared memory by
+// the MMA warp before the product, on the tiles that have any.
+// Every wait is bounded and reports MGQA_ERR_TIMEOUT.
+#include <algorithm>
+#include <cmath>
+
+#include "cache_sched.cuh"
+#include "tc_ptx.cuh"
+
+namespace mgqa {
+namespace {
+
+constexpr int BM = 128, BN = 128, kShift = 7;
+constexpr int BOX = BN * 128;  // bytes of 128 rows x 64 columns, 128-byte swizzled
+constexpr int kOkRing = 8;     // tiles whose key masks are kept: the producer is at most 4 ahead of a softmax
+
+struct TcCacheParams {
+  CacheAttnParams a;
+  int32_t box_rows;
+};
+
+template <int D, int NT>
+struct Lay {
+  static constexpr int STAGES = D == 128 ? 2 : 4;
+  static constexpr int KB = D / 64;
+  static constexpr int q_off = 0;
+  static constexpr int k_off = q_off + NT * KB * BOX;
+  static constexpr int v_off = k_off + STAGES * KB * BOX;
+  static constexpr int misc_off = v_off + STAGES * KB * BOX;
+  static constexpr int threads = 128 * (1 + NT);
+  static constexpr int ROWS = BM * NT;
+  static constexpr uint32_t tmem_used = NT * (BN + D);
+  static constexpr uint32_t tmem_cols = tmem_used <= 256 ? 256 : 512;
+  struct Misc {
+    Drafts<kMaxDrafts> drafts;
+    int64_t scratch[threads / 32 + 4];
+    uint4 ok[kOkRing];  // which keys of a tile count
+    uint64_t kfull[STAGES], vfull[STAGES], kempty[STAGES], vempty[STAGES];
+    uint64_t sfull[NT], pfull[NT], odone[NT], ofree[NT], qfull[NT], drain;
+    uint32_t tmem;
+    int maxdepth;
+  };
+  static constexpr int smem = misc_off + (int)sizeof(Misc) + 1024;
+  static_assert(smem <= 227 * 1024, "shared memory");
+};
+
+MGQA_DEV uint32_t all_of(const uint4 &w) { return w.x & w.y & w.z & w.w; }
+MGQA_DEV uint32_t word_of(const uint4 &w, int i) { return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w; }
+
+// One 128-key tile of one softmax row (thread = row) in tensor memory: see the
+// prefill kernel's softmax_tile; the scale is non-negative here (the sign went
+// into q).
+template <typename T, int D, bool PARTIAL>
+MGQA_DEV void softmax_row(uint32_t t_s, uint32_t t_o, const uint32_t (&mw)[4], float sl2, float &m_used, float &l) {
+  uint32_t sr[BN];
+  float mr;
+  if constexpr (!PARTIAL) {
+    float red[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      tc::tmem_ld32_red<true>(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]), red[c]);
+    tc::tmem_wait_ld();
+    mr = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tc::tmem_ld32(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+    tc::tmem_wait_ld();
+    float mx[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mx[k] = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < BN; ++j)
+      mx[j & 7] = fmaxf(mx[j & 7], (mw[j >> 5] >> (j & 31)) & 1u ? __uint_as_float(sr[j]) : -INFINITY);
+#pragma unroll
+    for (int k = 4; k > 0; k >>= 1)
+#pragma unroll
+      for (int u = 0; u < k; ++u) mx[u] = fmaxf(mx[u], mx[u + k]);
+    mr = mx[0];
+  }
+  const float m_tile = mr == -INFINITY ? -INFINITY : mr * sl2;  // (a scale of 0 keeps "none")
+  const float m_new = fmaxf(m_used, m_tile);
+  bool rescale = false;
+  float factor = 1.f;
+  if (m_used == -INFINITY) {
+    m_used = m_new;
+  } else if (m_new - m_used > 8.f) {
+    rescale = true;
+    factor = tc::ex2(m_used - m_new);
+    m_used = m_new;
+    l *= factor;
+  }
+  if (__any_sync(0xffffffffu, rescale)) {
+    // O holds every P.V issued so far: S of this tile was issued behind them
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t o[32];
+      tc::tmem_ld32(t_o + c * 32, o);
+      tc::tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * factor);
+      tc::tmem_st32(t_o + c * 32, o);
+    }
+    tc::tmem_wait_st();
+  }
+  const float mb = m_used == -INFINITY ? 0.f : m_used;
+  const uint64_t sl2x2 = tc::pk2(sl2, sl2), nmb2 = tc::pk2(-mb, -mb);
+  uint64_t acc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = tc::pk2(0.f, 0.f);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int col = c * 32 + 2 * j;
+      const uint64_t y = tc::fma2(tc::pk2(__uint_as_float(sr[col]), __uint_as_float(sr[col + 1])), sl2x2, nmb2);
+      float y0, y1;
+      tc::upk2(y, y0, y1);
+      float p0 = tc::ex2(y0), p1 = tc::ex2(y1);
+      if (PARTIAL) {
+        if (!((mw[c] >> (2 * j)) & 1u)) p0 = 0.f;
+        if (!((mw[c] >> (2 * j + 1)) & 1u)) p1 = 0.f;
+      }
+      acc[j & 3] = tc::add2(acc[j & 3], tc::pk2(p0, p1));
+      pk[j] = pack2<T>(p0, p1);
+    }
+    tc::tmem_st16(t_s + c * 16, pk);
+  }
+  acc[0] = tc::add2(acc[0], acc[1]);
+  acc[2] = tc::add2(acc[2], acc[3]);
+  acc[0] = tc::add2(acc[0], acc[2]);
+  float s0, s1;
+  tc::upk2(acc[0], s0, s1);
+  l += s0 + s1;
+  tc::tmem_wait_st();
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(128 * (1 + NT), 1)
+cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_vn,
+                     const __grid_constant__ TcCacheParams tp) {
+  using L = Lay<D, NT>;
+  constexpr int KB = L::KB, STAGES = L::STAGES, ROWS = L::ROWS;
+  const CacheAttnParams &p = tp.a;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  auto &sm = *reinterpret_cast<typename L::Misc *>(smem + L::misc_off);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(sm.kfull + s, 1);
+      mbar_init(sm.vfull + s, 1);
+      mbar_init(sm.kempty + s, 1);
+      mbar_init(sm.vempty + s, 1);
+    }
+    for (int t = 0; t < NT; ++t) {
+      mbar_init(sm.sfull + t, 1);
+      mbar_init(sm.pfull + t, 128);
+      mbar_init(sm.odone + t, 1);
+      mbar_init(sm.ofree + t, 128);
+      mbar_init(sm.qfull + t, 128);
+    }
+    mbar_init(&sm.drain, 1);
+    fence_mbarrier_init();
+    tc::prefetch_tensormap(&tm_k);
+    tc::prefetch_tensormap(&tm_v);
+    tc::prefetch_tensormap(&tm_kn);
+    tc::prefetch_tensormap(&tm_vn);
+  }
+  if (warp == 1) tc::tmem_alloc(&sm.tmem, L::tmem_cols);
+  grid_dependency_wait();
+  allow_dependents();  // lengths and tables are final from here on
+  Walker walk;
+  walk.start(p, locate<L::threads>(p, sm.scratch, gridDim.x, blockIdx.x, -1, blockIdx.x == 0), blockIdx.x);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = sm.tmem;
+  bool ok = true;
+  Piece pc;
+  auto role_end = [&]() {
+    tc::fence_before_sync();
+    named_sync(1, L::threads);
+  };
+
+  if (warp == 0) {
+    if constexpr (NT == 2) tc::regs_dec<104>();
+    // ---------------- producer ----------------
+    const int br = tp.box_rows, nbox = BN / br;
+    int it = 0, v_issued = 0;  // tiles whose K (V) has been issued
+    while (ok && walk.next(p, pc)) {
+      const RowPlan &rp = pc.rp;
+      auto look_up = [&](int t) {
+        int kind;
+        const int j0 = first_key(rp, t, kShift, kind) + lane * br;
+        const bool some = !kind && lane < nbox && j0 < rp.n && ((rp.lo < rp.n && j0 + br > rp.lo) || j0 < rp.s_end);
+        return some ? page_of(p, pc.b, j0) : -2;  // -1: a page that is not there
+      };
+      int page = look_up(pc.t0);
+      for (int t = pc.t0; t < pc.t1; ++t) {
+        const int next = t + 1 < pc.t1 ? look_up(t + 1) : -2;
+        int kind;
+        const int k0 = first_key(rp, t, kShift, kind);
+        const int j0 = k0 + lane * br;
+        uint32_t mine[4] = {0u, 0u, 0u, 0u};
+        bool take = false;
+        if (kind) {
+          take = lane == 0 && rp.live > k0;
+          if (lane == 0)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) mine[w] = low_mask(rp.live - k0 - 32 * w);
+        } else if (page >= 0) {
+          take = true;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int j = k0 + 32 * w;
+            mine[w] = low_mask(rp.n - j) & (~low_mask(rp.lo - j) | low_mask(rp.s_end - j)) & low_mask(j0 + br - j) &
+                      ~low_mask(j0 - j);
+          }
+        } else if (page == -1) {
+          report_error(p.err, MGQA_ERR_INVALID_ARG);
+        }
+        uint4 words;
+        words.x = __reduce_or_sync(0xffffffffu, mine[0]);
+        words.y = __reduce_or_sync(0xffffffffu, mine[1]);
+        words.z = __reduce_or_sync(0xffffffffu, mine[2]);
+        words.w = __reduce_or_sync(0xffffffffu, mine[3]);
+        const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, take)) * (kind ? BN : br) * 128 * KB);
+        const int st = it % STAGES, use = it / STAGES;
+        const int slot = kind ? k0 : slot_in_page(p, j0), z = kind ? pc.b : page;
+        const int row_off = kind ? 0 : lane * br * 128;
+        if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(sm.kempty + st, (use - 1) & 1, p.err));
+        if (!ok) break;
+        if (lane == 0) {
+          sm.ok[it % kOkRing] = words;
+          mbar_arrive_expect_tx(sm.kfull + st, bytes);
+        }
+        __syncwarp();
+        if (take)
+#pragma unroll
+          for (int c = 0; c < KB; ++c)
+            tc::tma_load_4d(smem + L::k_off + (st * KB + c) * BOX + row_off, kind ? &tm_kn : &tm_k, c * 64, slot, pc.g,
+                            z, sm.kfull + st);
+        ++it;
+        if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(sm.vempty + st, (use - 1) & 1, p.err));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(sm.vfull + st, bytes);
+        __syncwarp();
+        if (take)
+#pragma unroll
+          for (int c = 0; c < KB; ++c)
+            tc::tma_load_4d(smem + L::v_off + (st * KB + c) * BOX + row_off, kind ? &tm_vn : &tm_v, c * 64, slot, pc.g,
+                            z, sm.vfull + st);
+        ++v_issued;
+        page = next;
+      }
+    }
+    // no copy may be in flight when the CTA exits (only this warp arms the full
+    // barriers: the last armed phase of each is the newest it can reach)
+    for (int i = max(0, it - STAGES); i < it; ++i) mbar_wait(sm.kfull + i % STAGES, (i / STAGES) & 1, p.err);
+    for (int i = max(0, v_issued - STAGES); i < v_issued; ++i) mbar_wait(sm.vfull + i % STAGES, (i / STAGES) & 1, p.err);
+    __syncwarp();
+    role_end();
+  } else if (warp == 1) {
+    if constexpr (NT == 2) tc::regs_dec<104>();
+    // ---------------- MMA issuer ----------------
+    const bool leader = tc::elect_one();
+    constexpr bool kBf16 = !__is_same(T, __half);
+    constexpr uint32_t id_s = tc::idesc_16bit(BM, BN, 0, 0, kBf16);
+    constexpr uint32_t id_pv = tc::idesc_16bit(BM, D, 0, 1, kBf16);
+    const uint32_t sb = smem_u32(smem);
+    const uint64_t qd0 = tc::sw128_desc(sb + L::q_off, 16, 1024);
+    const uint64_t kd0 = tc::sw128_desc(sb + L::k_off, 16, 1024);
+    const uint64_t vd0 = tc::sw128_desc(sb + L::v_off, BOX, 1024);
+    constexpr uint64_t kTileStep = (uint64_t)(KB * BOX) >> 4;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity, p.err));
+      return ok;
+    };
+    auto issue_s = [&](int t, int st, int k0, int k1) {
+      const uint64_t qd = qd0 + (uint64_t)t * kTileStep, kd = kd0 + (uint64_t)st * kTileStep;
+      if (leader) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          if (kk < k0 || kk >= k1) continue;
+          const uint64_t off = (uint64_t)((kk / 4) * BOX + (kk % 4) * 32) >> 4;
+          tc::mma_ss(tmem + t * BN, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
+        }
+        if (k1 == D / 16) {
+          tc::mma_commit(sm.sfull + t);
+          if (t == NT - 1) tc::mma_commit(sm.kempty + st);
+        }
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](int t, int st, int k0, int k1, bool first) {
+      const uint64_t vd = vd0 + (uint64_t)st * kTileStep;
+      if (leader) {
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk) {
+          if (kk < k0 || kk >= k1) continue;
+          tc::mma_ts(tmem + NT * BN + t * D, tmem + t * BN + kk * 8, vd + (uint64_t)(kk * 2048 >> 4), id_pv,
+                     (!first || kk > 0) ? 1u : 0u);
+        }
+      }
+      __syncwarp();
+    };
+    constexpr int kHalfPV = BN / 32, kLateS = D / 16 - 1;
+    int it = 0;  // tiles of the pieces before this one
+    for (int piece = 0; ok && walk.next(p, pc); ++piece) {
+      const int nk = pc.t1 - pc.t0;
+      if (!wait(sm.kfull + it % STAGES, (it / STAGES) & 1)) break;
+      for (int t = 0; t < NT && ok; ++t) {
+        if (!wait(sm.qfull + t, piece & 1)) break;
+        tc::fence_after_sync();
+        issue_s(t, it % STAGES, 0, D / 16);
+      }
+      if (!ok || !wait(sm.vfull + it % STAGES, (it / STAGES) & 1)) break;
+      bool p0_seen = false;
+      for (int n = 0; n < nk && ok; ++n) {
+        const int at = it + n, st = at % STAGES, st1 = (at + 1) % STAGES;
+        const uint32_t par1 = (uint32_t)((at + 1) / STAGES) & 1u;
+        const bool has_next = n + 1 < nk;
+        {  // values of keys that do not count: cleared (their rows may hold anything)
+          const uint4 okw = sm.ok[at % kOkRing];
+          if (all_of(okw) != 0xffffffffu) {
+            for (int r = 0; r < BN; ++r)
+              if (!((word_of(okw, r >> 5) >> (r & 31)) & 1u))
+                for (int c = lane; c < D / 8; c += 32)  // 16-byte pieces (the swizzle permutes them within the row)
+                  *reinterpret_cast<uint4 *>(smem + L::v_off + (st * KB + (c >> 3)) * BOX + r * 128 + (c & 7) * 16) =
+                      make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        bool p1_seen = false;
+        for (int t = 0; t < NT && ok; ++t) {
+          if (!(t == 0 ? p0_seen : p1_seen) && !wait(sm.pfull + t, at & 1)) break;
+          if (n == 0 && piece > 0 && !wait(sm.ofree + t, (piece - 1) & 1)) break;
+          tc::fence_after_sync();
+          issue_pv(t, st, 0, kHalfPV, n == 0);
+          if (has_next) {  // K of the next tile before its first S, V before the next P.V
+            if (t == 0 && !wait(sm.kfull + st1, par1)) break;
+            if (t == NT - 1 && !wait(sm.vfull + st1, par1)) break;
+            tc::fence_after_sync();
+          }
+          issue_pv(t, st, kHalfPV, BN / 16, n == 0);
+          if (leader) {
+            if (!has_next) tc::mma_commit(sm.odone + t);
+            if (t == NT - 1) tc::mma_commit(sm.vempty + st);
+          }
+          __syncwarp();
+          if (has_next) {
+            issue_s(t, st1, 0, kLateS);
+            if (NT > 1 && t == NT - 1) p0_seen = __all_sync(0xffffffffu, mbar_test_wait(sm.pfull, (at + 1) & 1));
+            else if (NT > 1) p1_seen = __all_sync(0xffffffffu, mbar_test_wait(sm.pfull + 1, at & 1));
+            issue_s(t, st1, kLateS, D / 16);
+          }
+        }
+      }
+      it += nk;
+    }
+    // the last release of every stage has landed before the CTA exits; after a
+    // wait that gave up, every MMA issued completes before tensor memory is freed
+    for (int i = max(0, it - STAGES); i < it && ok; ++i)
+      wait(sm.kempty + i % STAGES, (i / STAGES) & 1) && wait(sm.vempty + i % STAGES, (i / STAGES) & 1);
+    if (!ok) {
+      if (leader) tc::mma_commit(&sm.drain);
+      __syncwarp();
+      mbar_wait(&sm.drain, 0, p.err);
+    }
+    __syncwarp();
+    role_end();
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, L::tmem_cols);
+  } else if (warp < 4) {
+    if constexpr (NT == 2) tc::regs_dec<104>();
+    role_end();
+  } else {
+    if constexpr (NT == 2) tc::regs_inc<200>();
+    // ---------------- softmax warpgroup t ----------------
+    const int t = (warp - 4) >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;  // row of the tile
+    const int stid = tid - 128;         // thread among the softmax warps
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t t_s = tmem + lanes + t * BN, t_o = tmem + lanes + NT * BN + t * D;
+    const float sl2 = fabsf(p.scale_log2);
+    const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+    int it = 0, staged = -1;
+    for (int piece = 0; walk.next(p, pc); ++piece) {
+      const RowPlan &rp = pc.rp;
+      const PieceOut po = out_of(p, pc, blockIdx.x, ROWS);
+      // ---- this block's query rows, 16 bytes a step, into the swizzled layout
+      for (int u = stid & 127; u < BM * (D / 8); u += 128) {
+        const int qr = u / (D / 8), c = u % (D / 8), row = po.row0 + t * BM + qr;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (row < p.R) {
+          x = *reinterpret_cast<const uint4 *>(
+              static_cast<const T *>(p.q) + (int64_t)pc.b * p.qs[0] + (int64_t)(pc.g * p.n_rep + row % p.n_rep) * p.qs[1] +
+              (int64_t)(row / p.n_rep) * p.qs[2] + c * 8);
+          x.x ^= flip;
+          x.y ^= flip;
+          x.z ^= flip;
+          x.w ^= flip;
+        }
+        *reinterpret_cast<uint4 *>(smem + L::q_off + (t * KB + (c >> 3)) * BOX + qr * 128 + (((c & 7) ^ (qr & 7)) << 4)) = x;
+      }
+      fence_proxy_async_smem();  // the tensor cores read it through the async proxy
+      mbar_arrive(sm.qfull + t);
+      const bool need_drafts = p.tree && (p.window != kNoWindow || pc.t1 > rp.np);
+      if (need_drafts && staged != pc.b) {
+        named_sync(2, 128 * NT);  // the masks of an earlier request are no longer read
+        if (stid == 0) sm.maxdepth = 0;
+        stage_drafts(p, sm.drafts, pc.b, rp.live, stid, 128 * NT);
+        named_sync(2, 128 * NT);
+        int md = 0;
+        for (int x = stid; x < rp.live; x += 128 * NT) md = max(md, sm.drafts.depth[x]);
+        if (md) atomicMax(&sm.maxdepth, md);
+        named_sync(2, 128 * NT);
+        staged = pc.b;
+      }
+      const int row = po.row0 + t * BM + r;
+      RowSight rs;
+      rs.t = row / p.n_rep;
+      rs.ok = row < p.R && (!p.tree || rs.t < rp.live);
+      const int pt = p.tree ? rp.n + (need_drafts && rs.ok ? sm.drafts.depth[rs.t] : 0) : rp.n - 1;
+      rs.lo = pt - p.window + 1;
+      const int lo_all = rp.n + (p.tree ? (need_drafts ? sm.maxdepth : 0) : -1) - p.window + 1;
+      float m_used = -INFINITY, l = 0.f;
+      for (int i = pc.t0; i < pc.t1; ++i, ++it) {
+        if (ok) ok = mbar_wait(sm.sfull + t, it & 1, p.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {  // after a failed wait, tensor memory is left alone
+          int kind;
+          const int k0 = first_key(rp, i, kShift, kind);
+          const uint4 okw = sm.ok[it % kOkRing];
+          const bool full = !kind && all_of(okw) == 0xffffffffu && (k0 >= lo_all || k0 + BN <= min(p.sinks, rp.s_end));
+          tc::fence_after_sync();
+          uint32_t mw[4] = {0u, 0u, 0u, 0u};
+          if (full) {
+            softmax_row<T, D, false>(t_s, t_o, mw, sl2, m_used, l);
+          } else {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int j = k0 + 32 * w;
+              uint32_t x = rs.ok ? word_of(okw, w) : 0u;
+              if (!kind) {
+                x &= ~low_mask(rs.lo - j) | low_mask(p.sinks - j);
+              } else if (x) {
+                x &= sm.drafts.see[rs.t][j >> 5];
+                if (p.window != kNoWindow)
+                  for (uint32_t y = x; y; y &= y - 1) {
+                    const int s = __ffs(y) - 1, ps = rp.n + sm.drafts.depth[j + s];
+                    if (ps < rs.lo && ps >= p.sinks) x &= ~(1u << s);
+                  }
+              }
+              mw[w] = x;
+            }
+            softmax_row<T, D, true>(t_s, t_o, mw, sl2, m_used, l);
+          }
+          tc::fence_before_sync();
+        }
+        mbar_arrive(sm.pfull + t);
+      }
+      // ---- the piece's rows: O out of tensor memory, finished or as a partial result
+      if (ok) ok = mbar_wait(sm.odone + t, piece & 1, p.err);
+      ok = __all_sync(0xffffffffu, ok);
+      tc::fence_after_sync();
+      const bool none = !ok || !rs.ok || m_used == -INFINITY;
+      const float m = none ? -INFINITY : m_used, lr = none ? 0.f : l;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t x[32];
+        if (ok) {
+          tc::tmem_ld32(t_o + c * 32, x);
+          tc::tmem_wait_ld();
+        }
+        if (t * BM + r < po.rows)
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            float o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = none ? 0.f : __uint_as_float(x[j + e]);
+            put_out<T, D, ROWS, 4>(p, po, t * BM + r, c * 32 + j, o, m, lr);
+          }
+      }
+      tc::fence_before_sync();
+      mbar_arrive(sm.ofree + t);
+    }
+    role_end();
+  }
+}
+
+template <typename T, int D, int NT>
+mgqa_status launch_t(const CUtensorMap (&maps)[4], TcCacheParams tp, const CacheAttnLaunch &how, cudaStream_t s) {
+  using L = Lay<D, NT>;
+  auto kern = cache_attn_tc_kernel<T, D, NT>;
+  static std::atomic<uint64_t> attr{0};
+  const mgqa_status st = ensure_smem_attr(kern, L::smem, attr, "cache attention kernel");
+  if (st != MGQA_OK) return st;
+  CacheAttnParams &p = tp.a;
+  p.RB = (p.R + L::ROWS - 1) / L::ROWS;
+  p.tile_shift = kShift;
+  p.min_run = 2;
+  const int64_t tiles = (int64_t)p.B * p.Hkv * p.RB * most_tiles(p);
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(how.sms, kCacheAttnMaxCtas / 2), tiles));
+  set_partials(p, how.workspace, grid, L::ROWS, D);
+  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(L::threads), L::smem, s, maps[0], maps[1], maps[2], maps[3], tp);
+  if (e != cudaSuccess) return fail(MGQA_ERR_CUDA, "cache attention launch: %s", cudaGetErrorString(e));
+  return launch_cache_merge(p, __is_same(T, __half) ? MGQA_FP16 : MGQA_BF16, D, L::ROWS, grid, s);
+}
+
+template <typename T, int D>
+mgqa_status launch_d(const CUtensorMap (&maps)[4], const TcCacheParams &tp, const CacheAttnLaunch &how, cudaStream_t s) {
+  return tp.a.R <= BM ? launch_t<T, D, 1>(maps, tp, how, s) : launch_t<T, D, 2>(maps, tp, how, s);
+}
+
+}  // namespace
+
+bool cache_attn_tc_takes(const CacheAttnParams &p, mgqa_dtype dt) {
+  return dt != MGQA_FP32 && (!p.table || p.page_size % 8 == 0);
+}
+
+mgqa_status launch_cache_attn_tc(const CacheAttnParams &p, mgqa_dtype dt, int D, const CacheAttnLaunch &how,
+                                 cudaStream_t s) {
+  TcCacheParams tp{};
+  tp.a = p;
+  CUtensorMap maps[4];
+  if (!cache_attn_maps(p, dt, D, BN, maps, tp.box_rows))
+    return fail(MGQA_ERR_CUDA, "cuTensorMapEncodeTiled failed for the cache");
+  if (dt == MGQA_BF16)
+    return D == 64 ? launch_d<__nv_bfloat16, 64>(maps, tp, how, s) : launch_d<__nv_bfloat16, 128>(maps, tp, how, s);
+  return D == 64 ? launch_d<__half, 64>(maps, tp, how, s) : launch_d<__half, 128>(maps, tp, how, s);
+}
+
+}  // namespace mgqa

@@ -135,7 +135,7 @@ cache_attn_tma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
       // lane i: box i of the tile; the page of the next tile's box is looked up a tile ahead
       auto look_up = [&](int t) {
         int kind;
-        const int j0 = first_key(rp, t, kind) + lane * br;
+        const int j0 = first_key(rp, t, 6, kind) + lane * br;
         const bool some = !kind && lane < nbox && j0 < rp.n && ((rp.lo < rp.n && j0 + br > rp.lo) || j0 < rp.s_end);
         return some ? page_of(p, pc.b, j0) : -2;  // -1: a page that is not there
       };
@@ -143,7 +143,7 @@ cache_attn_tma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
       for (int t = pc.t0; t < pc.t1 && ok; ++t, ++it) {
         const int next = t + 1 < pc.t1 ? look_up(t + 1) : -2;
         int kind;
-        const int k0 = first_key(rp, t, kind);
+        const int k0 = first_key(rp, t, 6, kind);
         uint64_t bits = 0ull;
         if (kind) {
           bits = lane == 0 ? low64(rp.live - k0) : 0ull;
@@ -256,7 +256,7 @@ cache_attn_tma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
               mma_16816<T>(s[2 * np + 1], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b2, b3);
             }
           int kind;
-          const int k0 = first_key(rp, t, kind);
+          const int k0 = first_key(rp, t, 6, kind);
           const bool clean = (okw.x & okw.y) == 0xffffffffu;
           const bool full = !kind && clean && (k0 >= lo_all || k0 + kTile <= min(p.sinks, rp.s_end));
           if (full) {
@@ -484,6 +484,7 @@ mgqa_status launch_t(const CUtensorMap (&maps)[4], TmaParams tp, const CacheAttn
   if (st != MGQA_OK) return st;
   CacheAttnParams &p = tp.a;
   p.RB = (p.R + C::ROWS - 1) / C::ROWS;
+  p.tile_shift = 6;
   const int64_t units = (int64_t)p.B * p.Hkv * p.RB;
   const int64_t tiles = most_tiles(p);  // of one unit, at most
   // A cluster per unit while the call cannot be long: at most ~16 us of reads
@@ -518,6 +519,20 @@ mgqa_status launch_d(const CUtensorMap (&maps)[4], const TmaParams &tp, const Ca
 
 }  // namespace
 
+bool cache_attn_maps(const CacheAttnParams &p, mgqa_dtype dt, int D, int tile, CUtensorMap (&maps)[4], int &box_rows) {
+  box_rows = tile;
+  if (p.table)
+    for (; p.page_size % box_rows; box_rows /= 2) {}
+  const int pages = p.table ? p.num_pages : p.B, slots = p.table ? p.page_size : p.cap;
+  if (!make_tma_map_4d(&maps[0], dt, p.k, pages, p.Hkv, slots, D, p.ks, 64, box_rows, true) ||
+      !make_tma_map_4d(&maps[1], dt, p.v, pages, p.Hkv, slots, D, p.vs, 64, box_rows, true))
+    return false;
+  maps[2] = maps[0];
+  maps[3] = maps[1];
+  return !p.tree || (make_tma_map_4d(&maps[2], dt, p.kn, p.B, p.Hkv, p.T, D, p.kns, 64, tile, true) &&
+                     make_tma_map_4d(&maps[3], dt, p.vn, p.B, p.Hkv, p.T, D, p.vns, 64, tile, true));
+}
+
 bool cache_attn_tma_takes(const CacheAttnParams &p, mgqa_dtype dt) {
   return dt != MGQA_FP32 && p.R <= 64 && (!p.table || p.page_size % 8 == 0);
 }
@@ -526,19 +541,9 @@ mgqa_status launch_cache_attn_tma(const CacheAttnParams &p, mgqa_dtype dt, int D
                                   cudaStream_t s) {
   TmaParams tp{};
   tp.a = p;
-  tp.box_rows = kTile;
-  if (p.table)  // the largest power of two that divides the page
-    for (; p.page_size % tp.box_rows; tp.box_rows /= 2) {}
   CUtensorMap maps[4];
-  const int pages = p.table ? p.num_pages : p.B, slots = p.table ? p.page_size : p.cap;
-  bool ok = make_tma_map_4d(&maps[0], dt, p.k, pages, p.Hkv, slots, D, p.ks, 64, tp.box_rows, true) &&
-            make_tma_map_4d(&maps[1], dt, p.v, pages, p.Hkv, slots, D, p.vs, 64, tp.box_rows, true);
-  if (p.tree)
-    ok = ok && make_tma_map_4d(&maps[2], dt, p.kn, p.B, p.Hkv, p.T, D, p.kns, 64, kTile, true) &&
-         make_tma_map_4d(&maps[3], dt, p.vn, p.B, p.Hkv, p.T, D, p.vns, 64, kTile, true);
-  else
-    maps[2] = maps[0], maps[3] = maps[1];
-  if (!ok) return fail(MGQA_ERR_CUDA, "cuTensorMapEncodeTiled failed for the cache");
+  if (!cache_attn_maps(p, dt, D, kTile, maps, tp.box_rows))
+    return fail(MGQA_ERR_CUDA, "cuTensorMapEncodeTiled failed for the cache");
   if (dt == MGQA_BF16)
     return D == 64 ? launch_d<__nv_bfloat16, 64>(maps, tp, how, s) : launch_d<__nv_bfloat16, 128>(maps, tp, how, s);
   return D == 64 ? launch_d<__half, 64>(maps, tp, how, s) : launch_d<__half, 128>(maps, tp, how, s);

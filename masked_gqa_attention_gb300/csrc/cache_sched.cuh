@@ -1,7 +1,7 @@
 // Work split of the cache attention kernels (one new token, or a tree of
 // drafted tokens, per request over a cache in slots or pages).
 //
-// A request's keys are cut into tiles of kTile keys: the tiles of absolute
+// A request's keys are cut into tiles of 2^tile_shift keys: the tiles of absolute
 // cache slots that some query of the request may see (the sinks' tiles, then
 // the window's), then the tiles of its drafted tokens. A unit is one (request,
 // KV head, block of query rows) with the request's tiles; the units' tiles form
@@ -18,7 +18,7 @@
 
 namespace mgqa {
 
-constexpr int kTile = 64;        // keys of a tile
+constexpr int kTile = 64;        // keys of a tile of the mma.sync and CUDA-core kernels
 constexpr int kMaxDrafts = kMaxDraftsHost;
 constexpr int kNoWindow = 1 << 30;
 
@@ -36,6 +36,7 @@ struct CacheAttnParams {
   int32_t window, sinks;  // window: kNoWindow when there is none
   int32_t tree;           // 1: drafts follow the cache; 0: the one query is the last cached token
   int32_t B, Hq, Hkv, T, n_rep, R, RB;  // R = T * n_rep rows per KV head, in RB blocks
+  int32_t tile_shift;                   // log2 of a tile's keys
   int32_t min_run;                      // fewest tiles of a CTA's run
   float scale_log2;
   float *lse;
@@ -52,9 +53,10 @@ struct CacheAttnLaunch {
 
 // Tiles of one unit (a request's keys), at most.
 inline int64_t most_tiles(const CacheAttnParams &p) {
-  const int64_t span = (int64_t)p.window + p.T + p.sinks + 4 * kTile;
+  const int64_t tile = (int64_t)1 << p.tile_shift;
+  const int64_t span = (int64_t)p.window + p.T + p.sinks + 4 * tile;
   const int64_t keys = p.cap < span ? p.cap : span;
-  return (keys + kTile - 1) / kTile + 2 + (p.T + kTile - 1) / kTile;
+  return (keys + tile - 1) / tile + 2 + (p.T + tile - 1) / tile;
 }
 
 // The workspace as the partial results of `grid` CTAs (two each).
@@ -69,6 +71,13 @@ mgqa_status launch_cache_merge(const CacheAttnParams &p, mgqa_dtype dt, int D, i
 bool cache_attn_tma_takes(const CacheAttnParams &p, mgqa_dtype dt);
 mgqa_status launch_cache_attn_tma(const CacheAttnParams &p, mgqa_dtype dt, int D, const CacheAttnLaunch &how,
                                   cudaStream_t s);
+// Tensor-memory kernel (the same caches, more rows).
+bool cache_attn_tc_takes(const CacheAttnParams &p, mgqa_dtype dt);
+mgqa_status launch_cache_attn_tc(const CacheAttnParams &p, mgqa_dtype dt, int D, const CacheAttnLaunch &how,
+                                 cudaStream_t s);
+// Tensor maps of the cache (boxes of `box_rows` slots: the largest power of two
+// up to `tile` that divides the page) and of the drafts.
+bool cache_attn_maps(const CacheAttnParams &p, mgqa_dtype dt, int D, int tile, CUtensorMap (&maps)[4], int &box_rows);
 
 // What one request's queries may see.
 struct RowPlan {
@@ -97,11 +106,12 @@ MGQA_DEV RowPlan plan_row(const CacheAttnParams &p, int b, bool report) {
   const int p0 = p.tree ? n : n - 1;  // the first query's position
   r.lo = min(max(p0 - p.window + 1, 0), n);
   r.s_end = min(p.sinks, r.lo);
-  r.ns = (r.s_end + kTile - 1) / kTile;
-  r.mt0 = max(r.lo / kTile, r.ns);
-  r.np = r.ns + (r.lo < n ? max(0, (n + kTile - 1) / kTile - r.mt0) : 0);
+  const int ts = p.tile_shift, up = (1 << ts) - 1;
+  r.ns = (r.s_end + up) >> ts;
+  r.mt0 = max(r.lo >> ts, r.ns);
+  r.np = r.ns + (r.lo < n ? max(0, ((n + up) >> ts) - r.mt0) : 0);
   if (p.tree && live == 0) r.np = 0;  // no query is left to see anything
-  r.nt = max(1, r.np + (live + kTile - 1) / kTile);
+  r.nt = max(1, r.np + ((live + up) >> ts));
   return r;
 }
 
@@ -226,9 +236,9 @@ MGQA_DEV bool sees_draft(const CacheAttnParams &p, const Drafts<MAXT> &d, const 
 }
 
 // Slot (or draft) of the first key of tile i of a request; kind: 0 cached, 1 drafted.
-MGQA_DEV int first_key(const RowPlan &rp, int i, int &kind) {
+MGQA_DEV int first_key(const RowPlan &rp, int i, int tile_shift, int &kind) {
   kind = i >= rp.np;
-  return kind ? (i - rp.np) * kTile : (i < rp.ns ? i : rp.mt0 + i - rp.ns) * kTile;
+  return (kind ? i - rp.np : (i < rp.ns ? i : rp.mt0 + i - rp.ns)) << tile_shift;
 }
 // Does key j of that kind count for any query?
 MGQA_DEV bool wanted(const RowPlan &rp, int kind, int j) {
