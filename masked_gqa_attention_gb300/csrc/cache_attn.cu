@@ -342,7 +342,7 @@ cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
         acc[2] += x.z;
         acc[3] += x.w;
       }
-      put_out<T, D, ROWS, 4>(p, po, r, d, acc, mr, lr);
+      RowOut<T, D, ROWS>(p, po, r, mr, lr, d == 0).put(d, acc);
     }
   }
 }
@@ -537,12 +537,14 @@ cache_attn_fp32_kernel(const __grid_constant__ CacheAttnParams p) {
       for (int off = 1; off < 16; off <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, off);
       const int r = ty + 16 * a;
       const bool none = !sight[a].ok;
-      if (r < po.rows)
+      if (r < po.rows) {
+        const RowOut<float, D, ROWS> dst(p, po, r, none ? -INFINITY : m[a], none ? 0.f : ls, tx == 0);
 #pragma unroll
         for (int c = 0; c < ND; ++c) {
           if (none) o[a][c][0] = o[a][c][1] = o[a][c][2] = o[a][c][3] = 0.f;
-          put_out<float, D, ROWS, 4>(p, po, r, tx * 4 + 64 * c, o[a][c], none ? -INFINITY : m[a], none ? 0.f : ls);
+          dst.put(tx * 4 + 64 * c, o[a][c]);
         }
+      }
     }
   }
 }
@@ -550,58 +552,90 @@ cache_attn_fp32_kernel(const __grid_constant__ CacheAttnParams p) {
 // ---- joining the partial results -------------------------------------------------
 
 constexpr int kMergeThreads = 128;
-constexpr int kMergeRows = 16;  // rows of a block
 
-// Block (unit, group of rows): nothing to do for a unit that one CTA finished.
+// A thread has four features of a row; a block kMergeThreads / (D / 4) rows.
+// by_unit: block (unit, rows). Otherwise block (run, rows) serves the unit that
+// the run's start cuts, if it is the first cut of that unit: with more units
+// than runs most units are whole, and so need no block.
 template <typename T, int D, int BR>
 __global__ void __launch_bounds__(kMergeThreads)
-cache_merge_kernel(const __grid_constant__ CacheAttnParams p, int grid) {
+cache_merge_kernel(const __grid_constant__ CacheAttnParams p, int grid, int by_unit) {
   __shared__ int64_t scratch[8];
   const int units = p.Hkv * p.RB;
-  const int b = blockIdx.x / units, unit = blockIdx.x % units;
   // the lengths are final: this grid starts when every CTA of the attention
   // kernel is past its own wait
-  const Located loc = locate<kMergeThreads>(p, scratch, grid, 0, b, false);
-  const int nt = plan_row(p, b, false).nt;
-  const int64_t s = loc.start + (int64_t)unit * nt, e = s + nt;
-  const int64_t first = s / loc.cut.run, last = (e - 1) / loc.cut.run;
+  const int x0 = blockIdx.x;
+  const Located loc = locate<kMergeThreads>(p, scratch, grid, by_unit ? 0 : x0, by_unit ? x0 / units : -1, false);
+  const int64_t run = loc.cut.run, at = (int64_t)x0 * run;
+  bool mine = by_unit || at < loc.cut.total;
+  int b = 0, unit = 0;
+  int64_t first = 0, last = 0;
+  if (mine) {
+    b = by_unit ? x0 / units : loc.b;
+    const int len = plan_row(p, b, false).nt + p.lead;
+    unit = by_unit ? x0 % units : (int)((at - loc.start) / len);
+    const int64_t s = loc.start + (int64_t)unit * len;
+    first = (s + p.lead) / run;  // the run that holds the unit's first tile
+    last = (s + len - 1) / run;
+    mine = by_unit ? first != last : x0 == first + 1 && x0 <= last;
+  }
   grid_dependency_wait();
   allow_dependents();
-  if (first == last) return;
+  if (!mine) return;
   const int row0 = (unit % p.RB) * BR, rows = min(BR, p.R - row0);
-  PieceOut po{true, 0, b, unit / p.RB, row0, rows};
-  const int r0 = blockIdx.y * kMergeRows, r1 = min(rows, r0 + kMergeRows);
-  for (int u = threadIdx.x; u < (r1 - r0) * (D / 4); u += kMergeThreads) {
-    const int r = r0 + u / (D / 4), d = (u % (D / 4)) * 4;
-    float m = -INFINITY, l = 0.f;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int64_t x = first; x <= last; ++x)
-      m = fmaxf(m, p.part_ml[(2 * x + (x == first)) * BR + r].x);
-#pragma unroll 8
-    for (int64_t x = first; x <= last; ++x) {
-      const int64_t at = (2 * x + (x == first)) * BR + r;
-      const float2 ml = p.part_ml[at];
-      const float4 v = *reinterpret_cast<const float4 *>(p.part_o + at * D + d);
-      const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
-      l = fmaf(ml.y, w, l);
-      if (w != 0.f) {
-        acc[0] = fmaf(v.x, w, acc[0]);
-        acc[1] = fmaf(v.y, w, acc[1]);
-        acc[2] = fmaf(v.z, w, acc[2]);
-        acc[3] = fmaf(v.w, w, acc[3]);
+  const PieceOut po{true, 0, b, unit / p.RB, row0, rows};
+  const int r = blockIdx.y * (kMergeThreads / (D / 4)) + threadIdx.x / (D / 4), d = (threadIdx.x % (D / 4)) * 4;
+  if (r >= rows) return;
+  const float2 *ml = p.part_ml + r;
+  const float *po_ = p.part_o + (int64_t)r * D + d;
+  float m = -INFINITY, l = 0.f;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  constexpr int U = 8;  // partial results in flight
+  for (int64_t x = first; x <= last; x += U) {
+    float2 a[U];
+    float4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      a[u] = make_float2(-INFINITY, 0.f);
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (x + u <= last) {
+        const int64_t slot = (2 * (x + u) + (x + u == first)) * BR;
+        a[u] = ml[slot];
+        v[u] = *reinterpret_cast<const float4 *>(po_ + slot * D);
       }
     }
-    put_out<T, D, BR, 4>(p, po, r, d, acc, m, l);
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) mn = fmaxf(mn, a[u].x);
+    if (mn == -INFINITY) continue;
+    const float f = m == -INFINITY ? 0.f : exp2f(m - mn);
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] *= f;
+    m = mn;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (a[u].x == -INFINITY) continue;
+      const float w = exp2f(a[u].x - m);
+      l = fmaf(a[u].y, w, l);
+      acc[0] = fmaf(v[u].x, w, acc[0]);
+      acc[1] = fmaf(v[u].y, w, acc[1]);
+      acc[2] = fmaf(v[u].z, w, acc[2]);
+      acc[3] = fmaf(v[u].w, w, acc[3]);
+    }
   }
+  RowOut<T, D, BR>(p, po, r, m, l, d == 0).put(d, acc);
 }
 
 // ---- host side ---------------------------------------------------------------------
 
 template <typename T, int D, int BR>
 mgqa_status launch_merge(const CacheAttnParams &p, int grid, cudaStream_t s) {
-  const dim3 g((unsigned)((int64_t)p.B * p.Hkv * p.RB), (std::min(BR, p.R) + kMergeRows - 1) / kMergeRows);
-  const cudaError_t e = launch_pdl(cache_merge_kernel<T, D, BR>, g, dim3(kMergeThreads), 0, s, p, grid);
+  const int64_t units = (int64_t)p.B * p.Hkv * p.RB;
+  const int by_unit = units <= grid;
+  constexpr int rows = kMergeThreads / (D / 4);
+  const dim3 g((unsigned)(by_unit ? units : grid), (std::min(BR, p.R) + rows - 1) / rows);
+  const cudaError_t e = launch_pdl(cache_merge_kernel<T, D, BR>, g, dim3(kMergeThreads), 0, s, p, grid, by_unit);
   if (e != cudaSuccess) return fail(MGQA_ERR_CUDA, "cache attention merge launch: %s", cudaGetErrorString(e));
   return MGQA_OK;
 }
@@ -624,8 +658,9 @@ mgqa_status launch_with(Kern kern, int smem, std::atomic<uint64_t> &attr, int th
   if (st != MGQA_OK) return st;
   p.RB = (p.R + BR - 1) / BR;
   p.tile_shift = 6;
-  p.min_run = 2;
-  const int64_t tiles = (int64_t)p.B * p.Hkv * p.RB * most_tiles(p);
+  p.lead = 2;
+  p.min_run = 4;
+  const int64_t tiles = (int64_t)p.B * p.Hkv * p.RB * (most_tiles(p) + p.lead);
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(how.sms * per_sm, kCacheAttnMaxCtas), tiles));
   set_partials(p, how.workspace, grid, BR, D);
   const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(threads), smem, s, p);

@@ -344,11 +344,17 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         {  // values of keys that do not count: cleared (their rows may hold anything)
           const uint4 okw = sm.ok[at % kOkRing];
           if (all_of(okw) != 0xffffffffu) {
-            for (int r = 0; r < BN; ++r)
-              if (!((word_of(okw, r >> 5) >> (r & 31)) & 1u))
-                for (int c = lane; c < D / 8; c += 32)  // 16-byte pieces (the swizzle permutes them within the row)
-                  *reinterpret_cast<uint4 *>(smem + L::v_off + (st * KB + (c >> 3)) * BOX + r * 128 + (c & 7) * 16) =
-                      make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t w4[4] = {okw.x, okw.y, okw.z, okw.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              if (w4[w] != 0xffffffffu)  // 16-byte pieces (the swizzle permutes them within a row)
+#pragma unroll 8
+                for (int u = lane; u < 32 * (D / 8); u += 32) {
+                  const int r = u / (D / 8), c = u % (D / 8);
+                  if (!((w4[w] >> r) & 1u))
+                    *reinterpret_cast<uint4 *>(smem + L::v_off + (st * KB + (c >> 3)) * BOX + (32 * w + r) * 128 +
+                                               (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
             fence_proxy_async_smem();
             __syncwarp();
           }
@@ -410,20 +416,20 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     for (int piece = 0; walk.next(p, pc); ++piece) {
       const RowPlan &rp = pc.rp;
       const PieceOut po = out_of(p, pc, blockIdx.x, ROWS);
-      // ---- this block's query rows, 16 bytes a step, into the swizzled layout
-      for (int u = stid & 127; u < BM * (D / 8); u += 128) {
-        const int qr = u / (D / 8), c = u % (D / 8), row = po.row0 + t * BM + qr;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (row < p.R) {
-          x = *reinterpret_cast<const uint4 *>(
-              static_cast<const T *>(p.q) + (int64_t)pc.b * p.qs[0] + (int64_t)(pc.g * p.n_rep + row % p.n_rep) * p.qs[1] +
-              (int64_t)(row / p.n_rep) * p.qs[2] + c * 8);
-          x.x ^= flip;
-          x.y ^= flip;
-          x.z ^= flip;
-          x.w ^= flip;
-        }
-        *reinterpret_cast<uint4 *>(smem + L::q_off + (t * KB + (c >> 3)) * BOX + qr * 128 + (((c & 7) ^ (qr & 7)) << 4)) = x;
+      // ---- this thread's query row, into the swizzled layout (every load in flight at once)
+      const int row = po.row0 + t * BM + r;
+      {
+        const int qt = row / p.n_rep;
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            static_cast<const T *>(p.q) + (int64_t)pc.b * p.qs[0] + (int64_t)(pc.g * p.n_rep + row - qt * p.n_rep) * p.qs[1] +
+            (int64_t)qt * p.qs[2]);
+        uint4 x[D / 8];
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) x[c] = row < p.R ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          *reinterpret_cast<uint4 *>(smem + L::q_off + (t * KB + (c >> 3)) * BOX + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+              make_uint4(x[c].x ^ flip, x[c].y ^ flip, x[c].z ^ flip, x[c].w ^ flip);
       }
       fence_proxy_async_smem();  // the tensor cores read it through the async proxy
       mbar_arrive(sm.qfull + t);
@@ -439,7 +445,6 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         named_sync(2, 128 * NT);
         staged = pc.b;
       }
-      const int row = po.row0 + t * BM + r;
       RowSight rs;
       rs.t = row / p.n_rep;
       rs.ok = row < p.R && (!p.tree || rs.t < rp.live);
@@ -488,20 +493,22 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       tc::fence_after_sync();
       const bool none = !ok || !rs.ok || m_used == -INFINITY;
       const float m = none ? -INFINITY : m_used, lr = none ? 0.f : l;
-#pragma unroll 1
+      const bool has_row = t * BM + r < po.rows;
+      const RowOut<T, D, ROWS> dst(p, po, has_row ? t * BM + r : 0, m, lr, has_row);
+#pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t x[32];
         if (ok) {
           tc::tmem_ld32(t_o + c * 32, x);
           tc::tmem_wait_ld();
         }
-        if (t * BM + r < po.rows)
+        if (has_row)
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            float o[4];
+          for (int j = 0; j < 32; j += 8) {
+            float o[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = none ? 0.f : __uint_as_float(x[j + e]);
-            put_out<T, D, ROWS, 4>(p, po, t * BM + r, c * 32 + j, o, m, lr);
+            for (int e = 0; e < 8; ++e) o[e] = none ? 0.f : __uint_as_float(x[j + e]);
+            dst.put(c * 32 + j, o);
           }
       }
       tc::fence_before_sync();
@@ -521,8 +528,9 @@ mgqa_status launch_t(const CUtensorMap (&maps)[4], TcCacheParams tp, const Cache
   CacheAttnParams &p = tp.a;
   p.RB = (p.R + L::ROWS - 1) / L::ROWS;
   p.tile_shift = kShift;
-  p.min_run = 2;
-  const int64_t tiles = (int64_t)p.B * p.Hkv * p.RB * most_tiles(p);
+  p.lead = 3;
+  p.min_run = 4;
+  const int64_t tiles = (int64_t)p.B * p.Hkv * p.RB * (most_tiles(p) + p.lead);
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(how.sms, kCacheAttnMaxCtas / 2), tiles));
   set_partials(p, how.workspace, grid, L::ROWS, D);
   const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(L::threads), L::smem, s, maps[0], maps[1], maps[2], maps[3], tp);

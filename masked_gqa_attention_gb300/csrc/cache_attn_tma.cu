@@ -409,12 +409,13 @@ cache_attn_tma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int r = wm * 16 + gq + 8 * e;
-            if (r < po.rows)
+            if (r >= po.rows) continue;
+            const RowOut<T, D, ROWS> dst(p, po, r, m[e], l[e], tq == 0);
 #pragma unroll
-              for (int d = 0; d < D / 8; ++d) {
-                const float x[2] = {m[e] == -INFINITY ? 0.f : o[d][2 * e], m[e] == -INFINITY ? 0.f : o[d][2 * e + 1]};
-                put_out<T, D, ROWS, 2>(p, po, r, d * 8 + 2 * tq, x, m[e], l[e]);
-              }
+            for (int d = 0; d < D / 8; ++d) {
+              const float x[2] = {m[e] == -INFINITY ? 0.f : o[d][2 * e], m[e] == -INFINITY ? 0.f : o[d][2 * e + 1]};
+              dst.put(d * 8 + 2 * tq, x);
+            }
           }
         }
       } else {
@@ -467,7 +468,7 @@ cache_attn_tma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
           acc[2] = fmaf(v[x].z, w, acc[2]);
           acc[3] = fmaf(v[x].w, w, acc[3]);
         }
-        put_out<T, D, ROWS, 4>(p, po, r, d, acc, m, l);
+        RowOut<T, D, ROWS>(p, po, r, m, l, d == 0).put(d, acc);
       }
     }
     __syncwarp();
@@ -502,8 +503,10 @@ mgqa_status launch_t(const CUtensorMap (&maps)[4], TmaParams tp, const CacheAttn
     if (e != cudaSuccess) return fail(MGQA_ERR_CUDA, "cache attention launch: %s", cudaGetErrorString(e));
     return MGQA_OK;
   }
-  p.min_run = 2;
-  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(2 * how.sms, kCacheAttnMaxCtas), units * tiles));
+  p.lead = 4;
+  p.min_run = 4;
+  const int grid =
+      (int)std::max<int64_t>(1, std::min<int64_t>(std::min(2 * how.sms, kCacheAttnMaxCtas), units * (tiles + p.lead)));
   set_partials(p, how.workspace, grid, C::ROWS, D);
   const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kThreads), C::smem, s, maps[0], maps[1], maps[2], maps[3], tp);
   if (e != cudaSuccess) return fail(MGQA_ERR_CUDA, "cache attention launch: %s", cudaGetErrorString(e));

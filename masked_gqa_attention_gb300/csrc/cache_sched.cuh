@@ -4,12 +4,13 @@
 // A request's keys are cut into tiles of 2^tile_shift keys: the tiles of absolute
 // cache slots that some query of the request may see (the sinks' tiles, then
 // the window's), then the tiles of its drafted tokens. A unit is one (request,
-// KV head, block of query rows) with the request's tiles; the units' tiles form
-// one long row, in the order of the units, which the CTAs cut into equal runs.
-// Rows of very different lengths so cost every CTA the same, whatever the
-// batch. A unit inside one run is finished by its CTA; a unit that crosses a
-// run's end leaves one partial result per run in the workspace, and the merge
-// kernel joins them in ascending order. The cut depends on the lengths, the
+// KV head, block of query rows) with the request's tiles, ahead of which it
+// counts `lead` tiles for what a unit costs besides (its query rows, its
+// results, the pipeline's fill). The units form one long row of tiles, which
+// the CTAs cut into equal runs. Rows of very different lengths so cost every
+// CTA the same, whatever the batch. A unit inside one run is finished by its
+// CTA; a unit that crosses a run's end leaves one partial result per run in the
+// workspace, and the merge kernel joins them in ascending order. The cut depends on the lengths, the
 // call's shapes and the device alone, so results repeat bit for bit.
 #pragma once
 
@@ -37,6 +38,7 @@ struct CacheAttnParams {
   int32_t tree;           // 1: drafts follow the cache; 0: the one query is the last cached token
   int32_t B, Hq, Hkv, T, n_rep, R, RB;  // R = T * n_rep rows per KV head, in RB blocks
   int32_t tile_shift;                   // log2 of a tile's keys
+  int32_t lead;                         // tiles counted for a unit's own cost
   int32_t min_run;                      // fewest tiles of a CTA's run
   float scale_log2;
   float *lse;
@@ -141,7 +143,7 @@ MGQA_DEV Located locate(const CacheAttnParams &p, int64_t *scratch, int grid, in
   int64_t mine = 0;
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
-    if (b < p.B) mine += plan_row(p, b, report).nt;
+    if (b < p.B) mine += plan_row(p, b, report).nt + p.lead;
   }
   int64_t inc = mine;
 #pragma unroll
@@ -165,7 +167,7 @@ MGQA_DEV Located locate(const CacheAttnParams &p, int64_t *scratch, int grid, in
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
     if (b >= p.B) break;
-    const int nt = plan_row(p, b, false).nt;
+    const int nt = plan_row(p, b, false).nt + p.lead;
     const bool hit = want_b >= 0 ? b == want_b
                                  : (want >= before * units && want < (before + nt) * units);
     if (hit) {
@@ -252,7 +254,7 @@ struct Piece {
 };
 struct Walker {
   int64_t f, f1, base;
-  int b, units, RB;
+  int b, units, RB, lead;
   RowPlan rp;
 
   MGQA_DEV void start(const CacheAttnParams &p, const Located &loc, int cta) {
@@ -261,25 +263,32 @@ struct Walker {
     base = loc.start;
     b = loc.b;
     RB = p.RB;
+    lead = p.lead;
     units = p.Hkv * p.RB;
     if (f < f1) rp = plan_row(p, b, false);
   }
   MGQA_DEV bool next(const CacheAttnParams &p, Piece &pc) {
-    if (f >= f1) return false;
-    while (f - base >= (int64_t)units * rp.nt) {
-      base += (int64_t)units * rp.nt;
-      rp = plan_row(p, ++b, false);
+    while (f < f1) {
+      const int len = rp.nt + lead;
+      if (f - base >= (int64_t)units * len) {
+        base += (int64_t)units * len;
+        rp = plan_row(p, ++b, false);
+        continue;
+      }
+      const int64_t rel = f - base;
+      const int unit = (int)(rel / len), v0 = (int)(rel - (int64_t)unit * len);
+      const int v1 = (int)min((int64_t)len, v0 + (f1 - f));
+      f += v1 - v0;
+      if (v1 <= lead) continue;  // the run ends within the unit's lead: the next run has all of it
+      pc.rp = rp;
+      pc.b = b;
+      pc.g = unit / RB;
+      pc.rb = unit % RB;
+      pc.t0 = max(0, v0 - lead);
+      pc.t1 = v1 - lead;
+      return true;
     }
-    const int64_t rel = f - base;
-    const int unit = (int)(rel / rp.nt);
-    pc.rp = rp;
-    pc.b = b;
-    pc.g = unit / RB;
-    pc.rb = unit % RB;
-    pc.t0 = (int)(rel - (int64_t)unit * rp.nt);
-    pc.t1 = (int)min((int64_t)rp.nt, pc.t0 + (f1 - f));
-    f += pc.t1 - pc.t0;
-    return true;
+    return false;
   }
 };
 
@@ -295,32 +304,59 @@ MGQA_DEV PieceOut out_of(const CacheAttnParams &p, const Piece &pc, int cta, int
                   pc.rb * block_rows, min(block_rows, p.R - pc.rb * block_rows)};
 }
 
-// N consecutive outputs (row r, features d..) of a piece: o unnormalised,
-// (m, l) of the row in log2 units. BR: rows of a block.
-template <typename T, int D, int BR, int N>
-MGQA_DEV void put_out(const CacheAttnParams &p, const PieceOut &po, int r, int d, const float (&o)[N], float m,
-                      float l) {
-  static_assert(N == 2 || N == 4, "pairs or quads");
-  if (!po.whole) {
-    float *dst = p.part_o + (po.slot * BR + r) * D + d;
-    if constexpr (N == 4) *reinterpret_cast<float4 *>(dst) = make_float4(o[0], o[1], o[2], o[3]);
-    else *reinterpret_cast<float2 *>(dst) = make_float2(o[0], o[1]);
-    if (d == 0) p.part_ml[po.slot * BR + r] = make_float2(m, l);
-    return;
+// Where row r of a piece goes: its finished values, or its unnormalised ones.
+template <typename T, int D, int BR>
+struct RowOut {
+  T *out;       // finished
+  float *part;  // else
+  float inv;
+
+  // `m`, `l` of the row in log2 units; `tell`: this thread writes what the row
+  // has once (its log-sum, or its partial maximum and sum)
+  MGQA_DEV RowOut(const CacheAttnParams &p, const PieceOut &po, int r, float m, float l, bool tell) {
+    out = nullptr;
+    part = nullptr;
+    inv = l > 0.f ? 1.f / l : 0.f;
+    if (po.whole) {
+      const int row = po.row0 + r, t = row / p.n_rep, h = po.g * p.n_rep + row - t * p.n_rep;
+      out = static_cast<T *>(p.out) + (int64_t)po.b * p.os[0] + (int64_t)h * p.os[1] + (int64_t)t * p.os[2];
+      if (tell && p.lse)
+        p.lse[((int64_t)po.b * p.Hq + h) * p.T + t] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    } else {
+      part = p.part_o + (po.slot * BR + r) * D;
+      if (tell) p.part_ml[po.slot * BR + r] = make_float2(m, l);
+    }
   }
-  const int row = po.row0 + r, t = row / p.n_rep, h = po.g * p.n_rep + row % p.n_rep;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  T *dst = static_cast<T *>(p.out) + (int64_t)po.b * p.os[0] + (int64_t)h * p.os[1] + (int64_t)t * p.os[2] + d;
-  if constexpr (sizeof(T) == 4) {
-    if constexpr (N == 4) *reinterpret_cast<float4 *>(dst) = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
-    else *reinterpret_cast<float2 *>(dst) = make_float2(o[0] * inv, o[1] * inv);
-  } else {
-    if constexpr (N == 4)
-      *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv));
-    else *reinterpret_cast<uint32_t *>(dst) = pack2<T>(o[0] * inv, o[1] * inv);
+  // N consecutive features from d on, unnormalised
+  template <int N>
+  MGQA_DEV void put(int d, const float (&o)[N]) const {
+    static_assert(N == 2 || N == 4 || N == 8, "one store, or two");
+    if (part) {
+      if constexpr (N == 2) {
+        *reinterpret_cast<float2 *>(part + d) = make_float2(o[0], o[1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+          *reinterpret_cast<float4 *>(part + d + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+      }
+    } else if constexpr (sizeof(T) == 4) {
+      if constexpr (N == 2) {
+        *reinterpret_cast<float2 *>(out + d) = make_float2(o[0] * inv, o[1] * inv);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+          *reinterpret_cast<float4 *>(out + d + i) =
+              make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
+      }
+    } else {
+      uint32_t w[N / 2];
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) w[i] = pack2<T>(o[2 * i] * inv, o[2 * i + 1] * inv);
+      if constexpr (N == 2) *reinterpret_cast<uint32_t *>(out + d) = w[0];
+      else if constexpr (N == 4) *reinterpret_cast<uint2 *>(out + d) = make_uint2(w[0], w[1]);
+      else *reinterpret_cast<uint4 *>(out + d) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
-  if (d == 0 && p.lse)
-    p.lse[((int64_t)po.b * p.Hq + h) * p.T + t] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-}
+};
 
 }  // namespace mgqa
