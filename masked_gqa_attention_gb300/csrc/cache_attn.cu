@@ -106,7 +106,7 @@ struct MmaCfg {
   static_assert(WK * ROWS * OP * 4 <= ring, "the joined output fits in the ring");
   struct Misc {
     Drafts<kMaxDrafts> drafts;
-    int64_t scratch[8];
+    LocateScratch<kThreads> scratch;
     float wm[WK][ROWS], wl[WK][ROWS];
     uint8_t ok[STAGES][kTile];
     int bad, maxdepth;
@@ -140,7 +140,7 @@ cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
   while (walk.next(p, pc)) {
     const RowPlan &rp = pc.rp;
     const int b = pc.b, g = pc.g, t0 = pc.t0, t1 = pc.t1;
-    const PieceOut po = out_of(p, pc, blockIdx.x, ROWS);
+    const PieceOut po = out_of(p, pc, blockIdx.x);
     const int row0 = po.row0;
 
     // ---- the first tiles' copies, then q and the drafts' masks
@@ -359,7 +359,7 @@ struct SimtCfg {
   static constexpr int floats = STAGES * 2 * TILEF + ROWS * RP + ROWS * PP;
   struct Misc {
     Drafts<kMaxDrafts> drafts;
-    int64_t scratch[16];
+    LocateScratch<kSimtThreads> scratch;
     uint8_t ok[STAGES][kTile];
     int bad, maxdepth;
   };
@@ -390,7 +390,7 @@ cache_attn_fp32_kernel(const __grid_constant__ CacheAttnParams p) {
   while (walk.next(p, pc)) {
     const RowPlan &rp = pc.rp;
     const int b = pc.b, g = pc.g, t0 = pc.t0, t1 = pc.t1;
-    const PieceOut po = out_of(p, pc, blockIdx.x, ROWS);
+    const PieceOut po = out_of(p, pc, blockIdx.x);
     const int row0 = po.row0;
     TileLoader<float, D, kSimtThreads> ld;
     const int nt = t1 - t0;
@@ -553,41 +553,43 @@ cache_attn_fp32_kernel(const __grid_constant__ CacheAttnParams p) {
 
 constexpr int kMergeThreads = 128;
 
-// A thread has four features of a row; a block kMergeThreads / (D / 4) rows.
+// A thread has four features of a row; a block 16 rows by 32 features, so that
+// the partial results are read in runs of 16 rows x 16 bytes.
 // by_unit: block (unit, rows). Otherwise block (run, rows) serves the unit that
 // the run's start cuts, if it is the first cut of that unit: with more units
 // than runs most units are whole, and so need no block.
 template <typename T, int D, int BR>
 __global__ void __launch_bounds__(kMergeThreads)
 cache_merge_kernel(const __grid_constant__ CacheAttnParams p, int grid, int by_unit) {
-  __shared__ int64_t scratch[8];
+  __shared__ LocateScratch<kMergeThreads> scratch;
   const int units = p.Hkv * p.RB;
   // the lengths are final: this grid starts when every CTA of the attention
   // kernel is past its own wait
   const int x0 = blockIdx.x;
   const Located loc = locate<kMergeThreads>(p, scratch, grid, by_unit ? 0 : x0, by_unit ? x0 / units : -1, false);
-  const int64_t run = loc.cut.run, at = (int64_t)x0 * run;
+  const int run = (int)min(loc.cut.run, (int64_t)0x7fffffff);  // (a longer run has no second CTA)
+  const int64_t at = (int64_t)x0 * run;
   bool mine = by_unit || at < loc.cut.total;
   int b = 0, unit = 0;
   int64_t first = 0, last = 0;
   if (mine) {
     b = by_unit ? x0 / units : loc.b;
-    const int len = plan_row(p, b, false).nt + p.lead;
-    unit = by_unit ? x0 % units : (int)((at - loc.start) / len);
+    const int len = loc.rp.nt + p.lead;
+    unit = by_unit ? x0 % units : div_small(at - loc.start, len);
     const int64_t s = loc.start + (int64_t)unit * len;
-    first = (s + p.lead) / run;  // the run that holds the unit's first tile
-    last = (s + len - 1) / run;
+    first = div_up(s + p.lead + 1, run) - 1;  // the run that holds the unit's first tile
+    last = div_up(s + len, run) - 1;
     mine = by_unit ? first != last : x0 == first + 1 && x0 <= last;
   }
   grid_dependency_wait();
   allow_dependents();
   if (!mine) return;
-  const int row0 = (unit % p.RB) * BR, rows = min(BR, p.R - row0);
+  const int row0 = (unit % p.RB) * p.block_rows, rows = min(p.block_rows, p.R - row0);
   const PieceOut po{true, 0, b, unit / p.RB, row0, rows};
-  const int r = blockIdx.y * (kMergeThreads / (D / 4)) + threadIdx.x / (D / 4), d = (threadIdx.x % (D / 4)) * 4;
+  const int r = blockIdx.y * 16 + threadIdx.x % 16, d = (blockIdx.z * 8 + threadIdx.x / 16) * 4;
   if (r >= rows) return;
   const float2 *ml = p.part_ml + r;
-  const float *po_ = p.part_o + (int64_t)r * D + d;
+  const float *po_ = p.part_o + (d / 4) * (BR * 4) + r * 4;
   float m = -INFINITY, l = 0.f;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   constexpr int U = 8;  // partial results in flight
@@ -599,9 +601,9 @@ cache_merge_kernel(const __grid_constant__ CacheAttnParams p, int grid, int by_u
       a[u] = make_float2(-INFINITY, 0.f);
       v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (x + u <= last) {
-        const int64_t slot = (2 * (x + u) + (x + u == first)) * BR;
-        a[u] = ml[slot];
-        v[u] = *reinterpret_cast<const float4 *>(po_ + slot * D);
+        const int64_t slot = 2 * (x + u) + (x + u == first);
+        a[u] = ml[slot * BR];
+        v[u] = *reinterpret_cast<const float4 *>(po_ + slot * (BR * D));
       }
     }
     float mn = m;
@@ -633,8 +635,7 @@ template <typename T, int D, int BR>
 mgqa_status launch_merge(const CacheAttnParams &p, int grid, cudaStream_t s) {
   const int64_t units = (int64_t)p.B * p.Hkv * p.RB;
   const int by_unit = units <= grid;
-  constexpr int rows = kMergeThreads / (D / 4);
-  const dim3 g((unsigned)(by_unit ? units : grid), (std::min(BR, p.R) + rows - 1) / rows);
+  const dim3 g((unsigned)(by_unit ? units : grid), (std::min(p.block_rows, p.R) + 15) / 16, D / 32);
   const cudaError_t e = launch_pdl(cache_merge_kernel<T, D, BR>, g, dim3(kMergeThreads), 0, s, p, grid, by_unit);
   if (e != cudaSuccess) return fail(MGQA_ERR_CUDA, "cache attention merge launch: %s", cudaGetErrorString(e));
   return MGQA_OK;
@@ -656,6 +657,7 @@ mgqa_status launch_with(Kern kern, int smem, std::atomic<uint64_t> &attr, int th
                         const CacheAttnLaunch &how, cudaStream_t s) {
   mgqa_status st = ensure_smem_attr(kern, smem, attr, "cache attention kernel");
   if (st != MGQA_OK) return st;
+  p.block_rows = BR;
   p.RB = (p.R + BR - 1) / BR;
   p.tile_shift = 6;
   p.lead = 2;

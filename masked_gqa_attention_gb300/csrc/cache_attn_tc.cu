@@ -5,17 +5,20 @@
 // With R rows per KV head a key costs 4 R D operations for its 4 D bytes: at
 // R = 256 the products take about as long as the reads, and mma.sync reaches a
 // fraction of the tensor rate, so here the scores and outputs live in tensor
-// memory. A CTA holds one block of up to 128 NT query rows (row = draft *
-// group + head, so a tile of keys serves every head of the group) and walks
+// memory. A CTA holds NT blocks of up to 128 query rows (row = draft * group +
+// head, so a tile of keys serves every head of the group) and walks
 // its run of the flat tile list (cache_sched.cuh), one CTA an SM:
 //   warp 0      : follows the page table, K and V boxes of 128-key tiles by TMA
 //   warp 1      : tensor memory, the MMA loop (one elected lane issues)
+//   warps 2, 3  : the query rows of the next piece, as soon as the last S of
+//                 the current one is done, and its description for the others
 //   warps 4..   : one softmax warpgroup per 128 rows (thread = row)
 // Per tile n and row block t: S_t = Q_t K_n^T; softmax (running maximum, lazy
 // rescale of O_t past 2^8) hands P_t over in tensor memory; O_t += P_t V_n and
 // at once S_t(n+1), as in the prefill kernel. Between two pieces the softmax
-// warpgroups read O_t out, load the next Q_t and release both by mbarriers; K
-// and V of the next piece are already on their way. Values of keys that do not
+// warpgroups read O_t out while the next query rows, K and V are on their way.
+// (The softmax warps loading the rows themselves, between the pieces, cost ~4000
+// cycles a piece, and their walk over the pieces the registers of the score row.) Values of keys that do not
 // count (the end of a request, a missing page) are cleared in shared memory by
 // the MMA warp before the product, on the tiles that have any.
 // Every wait is bounded and reports MGQA_ERR_TIMEOUT.
@@ -30,11 +33,13 @@ namespace {
 
 constexpr int BM = 128, BN = 128, kShift = 7;
 constexpr int BOX = BN * 128;  // bytes of 128 rows x 64 columns, 128-byte swizzled
+constexpr int kPieceRing = 4;  // a piece's slot is taken again after the S of the third piece behind it
 constexpr int kOkRing = 8;     // tiles whose key masks are kept: the producer is at most 4 ahead of a softmax
 
 struct TcCacheParams {
   CacheAttnParams a;
   int32_t box_rows;
+  int32_t q_drafts;  // drafts of a block of up to 128 rows (each with all heads of the group)
 };
 
 template <int D, int NT>
@@ -51,7 +56,9 @@ struct Lay {
   static constexpr uint32_t tmem_cols = tmem_used <= 256 ? 256 : 512;
   struct Misc {
     Drafts<kMaxDrafts> drafts;
-    int64_t scratch[threads / 32 + 4];
+    LocateScratch<threads> scratch;
+    Piece pieces[kPieceRing];      // rp.nt < 0: no more
+    uint64_t pready[kPieceRing], qfree;
     uint4 ok[kOkRing];  // which keys of a tile count
     uint64_t kfull[STAGES], vfull[STAGES], kempty[STAGES], vempty[STAGES];
     uint64_t sfull[NT], pfull[NT], odone[NT], ofree[NT], qfull[NT], drain;
@@ -66,8 +73,7 @@ MGQA_DEV uint32_t all_of(const uint4 &w) { return w.x & w.y & w.z & w.w; }
 MGQA_DEV uint32_t word_of(const uint4 &w, int i) { return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w; }
 
 // One 128-key tile of one softmax row (thread = row) in tensor memory: see the
-// prefill kernel's softmax_tile; the scale is non-negative here (the sign went
-// into q).
+// prefill kernel's softmax_tile; the scale is not negative here.
 template <typename T, int D, bool PARTIAL>
 MGQA_DEV void softmax_row(uint32_t t_s, uint32_t t_o, const uint32_t (&mw)[4], float sl2, float &m_used, float &l) {
   uint32_t sr[BN];
@@ -155,7 +161,7 @@ MGQA_DEV void softmax_row(uint32_t t_s, uint32_t t_o, const uint32_t (&mw)[4], f
 
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(128 * (1 + NT), 1)
-cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_vn,
                      const __grid_constant__ TcCacheParams tp) {
   using L = Lay<D, NT>;
@@ -178,10 +184,13 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       mbar_init(sm.pfull + t, 128);
       mbar_init(sm.odone + t, 1);
       mbar_init(sm.ofree + t, 128);
-      mbar_init(sm.qfull + t, 128);
+      mbar_init(sm.qfull + t, 1);
     }
+    for (int i = 0; i < kPieceRing; ++i) mbar_init(sm.pready + i, 1);
+    mbar_init(&sm.qfree, 1);
     mbar_init(&sm.drain, 1);
     fence_mbarrier_init();
+    tc::prefetch_tensormap(&tm_q);
     tc::prefetch_tensormap(&tm_k);
     tc::prefetch_tensormap(&tm_v);
     tc::prefetch_tensormap(&tm_kn);
@@ -198,6 +207,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
   const uint32_t tmem = sm.tmem;
   bool ok = true;
   Piece pc;
+  int q_pieces = 0;
   auto role_end = [&]() {
     tc::fence_before_sync();
     named_sync(1, L::threads);
@@ -297,7 +307,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity, p.err));
       return ok;
     };
-    auto issue_s = [&](int t, int st, int k0, int k1) {
+    auto issue_s = [&](int t, int st, int k0, int k1, bool last) {
       const uint64_t qd = qd0 + (uint64_t)t * kTileStep, kd = kd0 + (uint64_t)st * kTileStep;
       if (leader) {
 #pragma unroll
@@ -309,6 +319,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         if (k1 == D / 16) {
           tc::mma_commit(sm.sfull + t);
           if (t == NT - 1) tc::mma_commit(sm.kempty + st);
+          if (t == NT - 1 && last) tc::mma_commit(&sm.qfree);  // the piece's query rows are read
         }
       }
       __syncwarp();
@@ -333,7 +344,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       for (int t = 0; t < NT && ok; ++t) {
         if (!wait(sm.qfull + t, piece & 1)) break;
         tc::fence_after_sync();
-        issue_s(t, it % STAGES, 0, D / 16);
+        issue_s(t, it % STAGES, 0, D / 16, nk == 1);
       }
       if (!ok || !wait(sm.vfull + it % STAGES, (it / STAGES) & 1)) break;
       bool p0_seen = false;
@@ -377,10 +388,10 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
           }
           __syncwarp();
           if (has_next) {
-            issue_s(t, st1, 0, kLateS);
+            issue_s(t, st1, 0, kLateS, false);
             if (NT > 1 && t == NT - 1) p0_seen = __all_sync(0xffffffffu, mbar_test_wait(sm.pfull, (at + 1) & 1));
             else if (NT > 1) p1_seen = __all_sync(0xffffffffu, mbar_test_wait(sm.pfull + 1, at & 1));
-            issue_s(t, st1, kLateS, D / 16);
+            issue_s(t, st1, kLateS, D / 16, n + 2 == nk);
           }
         }
       }
@@ -401,6 +412,37 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     tc::tmem_dealloc(tmem, L::tmem_cols);
   } else if (warp < 4) {
     if constexpr (NT == 2) tc::regs_dec<104>();
+    // ---------------- query rows and piece descriptions (warp 2) ----------------
+    bool more = warp == 2;
+    for (int piece = 0; more; ++piece) {
+      more = walk.next(p, pc);
+      // (the slot is free: its piece's query rows were overwritten long ago)
+      if (ok && piece > 0) ok = __all_sync(0xffffffffu, mbar_wait(&sm.qfree, (piece - 1) & 1, p.err));
+      if (!ok) more = false;
+      if (lane == 0) {
+        if (!more) pc.rp.nt = -1;
+        sm.pieces[piece % kPieceRing] = pc;
+        mbar_arrive(sm.pready + piece % kPieceRing);
+        if (more) {
+          // block t: its drafts, each with the group's heads as consecutive rows
+          const int drafts = tp.q_drafts, first = pc.rb * drafts * NT;
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            mbar_arrive_expect_tx(sm.qfull + t, (uint32_t)(KB * drafts * p.n_rep * 128));
+#pragma unroll
+            for (int c = 0; c < KB; ++c)
+              tc::tma_load_5d(smem + L::q_off + (t * KB + c) * BOX, &tm_q, c * 64, 0, first + t * drafts, pc.g, pc.b,
+                              sm.qfull + t);
+          }
+          q_pieces = piece + 1;
+        }
+      }
+      __syncwarp();
+    }
+    // no copy may be in flight when the CTA exits
+    if (q_pieces > 0)
+      for (int t = 0; t < NT; ++t) mbar_wait(sm.qfull + t, (q_pieces - 1) & 1, p.err);
+    __syncwarp();
     role_end();
   } else {
     if constexpr (NT == 2) tc::regs_inc<200>();
@@ -410,29 +452,18 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     const int stid = tid - 128;         // thread among the softmax warps
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t t_s = tmem + lanes + t * BN, t_o = tmem + lanes + NT * BN + t * D;
-    const float sl2 = fabsf(p.scale_log2);
-    const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+    const float sl2 = p.scale_log2;
     int it = 0, staged = -1;
-    for (int piece = 0; walk.next(p, pc); ++piece) {
+    for (int piece = 0;; ++piece) {
+      if (ok) ok = mbar_wait(sm.pready + piece % kPieceRing, (piece / kPieceRing) & 1, p.err);
+      ok = __all_sync(0xffffffffu, ok);
+      const Piece &pc = sm.pieces[piece % kPieceRing];
+      if (!ok || pc.rp.nt < 0) break;
       const RowPlan &rp = pc.rp;
-      const PieceOut po = out_of(p, pc, blockIdx.x, ROWS);
-      // ---- this thread's query row, into the swizzled layout (every load in flight at once)
-      const int row = po.row0 + t * BM + r;
-      {
-        const int qt = row / p.n_rep;
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            static_cast<const T *>(p.q) + (int64_t)pc.b * p.qs[0] + (int64_t)(pc.g * p.n_rep + row - qt * p.n_rep) * p.qs[1] +
-            (int64_t)qt * p.qs[2]);
-        uint4 x[D / 8];
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) x[c] = row < p.R ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          *reinterpret_cast<uint4 *>(smem + L::q_off + (t * KB + (c >> 3)) * BOX + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-              make_uint4(x[c].x ^ flip, x[c].y ^ flip, x[c].z ^ flip, x[c].w ^ flip);
-      }
-      fence_proxy_async_smem();  // the tensor cores read it through the async proxy
-      mbar_arrive(sm.qfull + t);
+      const PieceOut po = out_of(p, pc, blockIdx.x);
+      const int brow = t * tp.q_drafts * p.n_rep + r;  // row of the blocks
+      const int row = po.row0 + brow;
+      const bool has_row = r < tp.q_drafts * p.n_rep && brow < po.rows;
       const bool need_drafts = p.tree && (p.window != kNoWindow || pc.t1 > rp.np);
       if (need_drafts && staged != pc.b) {
         named_sync(2, 128 * NT);  // the masks of an earlier request are no longer read
@@ -447,12 +478,13 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       }
       RowSight rs;
       rs.t = row / p.n_rep;
-      rs.ok = row < p.R && (!p.tree || rs.t < rp.live);
+      rs.ok = has_row && (!p.tree || rs.t < rp.live);
       const int pt = p.tree ? rp.n + (need_drafts && rs.ok ? sm.drafts.depth[rs.t] : 0) : rp.n - 1;
       rs.lo = pt - p.window + 1;
       const int lo_all = rp.n + (p.tree ? (need_drafts ? sm.maxdepth : 0) : -1) - p.window + 1;
       float m_used = -INFINITY, l = 0.f;
-      for (int i = pc.t0; i < pc.t1; ++i, ++it) {
+      const int t1 = pc.t1;
+      for (int i = pc.t0; i < t1; ++i, ++it) {
         if (ok) ok = mbar_wait(sm.sfull + t, it & 1, p.err);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {  // after a failed wait, tensor memory is left alone
@@ -493,8 +525,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       tc::fence_after_sync();
       const bool none = !ok || !rs.ok || m_used == -INFINITY;
       const float m = none ? -INFINITY : m_used, lr = none ? 0.f : l;
-      const bool has_row = t * BM + r < po.rows;
-      const RowOut<T, D, ROWS> dst(p, po, has_row ? t * BM + r : 0, m, lr, has_row);
+      const RowOut<T, D, ROWS> dst(p, po, has_row ? brow : 0, m, lr, has_row);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t x[32];
@@ -519,34 +550,46 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
 }
 
 template <typename T, int D, int NT>
-mgqa_status launch_t(const CUtensorMap (&maps)[4], TcCacheParams tp, const CacheAttnLaunch &how, cudaStream_t s) {
+mgqa_status launch_t(const CUtensorMap (&maps)[4], TcCacheParams tp, mgqa_dtype dt, const CacheAttnLaunch &how,
+                     cudaStream_t s) {
   using L = Lay<D, NT>;
   auto kern = cache_attn_tc_kernel<T, D, NT>;
   static std::atomic<uint64_t> attr{0};
   const mgqa_status st = ensure_smem_attr(kern, L::smem, attr, "cache attention kernel");
   if (st != MGQA_OK) return st;
   CacheAttnParams &p = tp.a;
-  p.RB = (p.R + L::ROWS - 1) / L::ROWS;
+  tp.q_drafts = BM / p.n_rep;
+  p.block_rows = NT * tp.q_drafts * p.n_rep;
+  p.RB = (p.R + p.block_rows - 1) / p.block_rows;
   p.tile_shift = kShift;
+  // q [B][Hkv][T][group][D]: a box is a block's drafts with the heads of one group
+  CUtensorMap mq;
+  const int64_t dims[5] = {D, p.n_rep, p.T, p.Hkv, p.B};
+  const int64_t strides[4] = {p.qs[1], p.qs[2], p.qs[1] * p.n_rep, p.qs[0]};
+  const int box[5] = {64, p.n_rep, tp.q_drafts, 1, 1};
+  if (!make_tma_map(&mq, dt, p.q, 5, dims, strides, box, true))
+    return fail(MGQA_ERR_CUDA, "cuTensorMapEncodeTiled failed for q");
   p.lead = 3;
   p.min_run = 4;
   const int64_t tiles = (int64_t)p.B * p.Hkv * p.RB * (most_tiles(p) + p.lead);
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(how.sms, kCacheAttnMaxCtas / 2), tiles));
   set_partials(p, how.workspace, grid, L::ROWS, D);
-  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(L::threads), L::smem, s, maps[0], maps[1], maps[2], maps[3], tp);
+  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(L::threads), L::smem, s, mq, maps[0], maps[1], maps[2],
+                                   maps[3], tp);
   if (e != cudaSuccess) return fail(MGQA_ERR_CUDA, "cache attention launch: %s", cudaGetErrorString(e));
-  return launch_cache_merge(p, __is_same(T, __half) ? MGQA_FP16 : MGQA_BF16, D, L::ROWS, grid, s);
+  return launch_cache_merge(p, dt, D, L::ROWS, grid, s);
 }
 
 template <typename T, int D>
-mgqa_status launch_d(const CUtensorMap (&maps)[4], const TcCacheParams &tp, const CacheAttnLaunch &how, cudaStream_t s) {
-  return tp.a.R <= BM ? launch_t<T, D, 1>(maps, tp, how, s) : launch_t<T, D, 2>(maps, tp, how, s);
+mgqa_status launch_d(const CUtensorMap (&maps)[4], const TcCacheParams &tp, mgqa_dtype dt, const CacheAttnLaunch &how,
+                     cudaStream_t s) {
+  return tp.a.T <= BM / tp.a.n_rep ? launch_t<T, D, 1>(maps, tp, dt, how, s) : launch_t<T, D, 2>(maps, tp, dt, how, s);
 }
 
 }  // namespace
 
 bool cache_attn_tc_takes(const CacheAttnParams &p, mgqa_dtype dt) {
-  return dt != MGQA_FP32 && (!p.table || p.page_size % 8 == 0);
+  return dt != MGQA_FP32 && (!p.table || p.page_size % 8 == 0) && p.n_rep <= BM && p.scale_log2 >= 0.f;
 }
 
 mgqa_status launch_cache_attn_tc(const CacheAttnParams &p, mgqa_dtype dt, int D, const CacheAttnLaunch &how,
@@ -557,8 +600,8 @@ mgqa_status launch_cache_attn_tc(const CacheAttnParams &p, mgqa_dtype dt, int D,
   if (!cache_attn_maps(p, dt, D, BN, maps, tp.box_rows))
     return fail(MGQA_ERR_CUDA, "cuTensorMapEncodeTiled failed for the cache");
   if (dt == MGQA_BF16)
-    return D == 64 ? launch_d<__nv_bfloat16, 64>(maps, tp, how, s) : launch_d<__nv_bfloat16, 128>(maps, tp, how, s);
-  return D == 64 ? launch_d<__half, 64>(maps, tp, how, s) : launch_d<__half, 128>(maps, tp, how, s);
+    return D == 64 ? launch_d<__nv_bfloat16, 64>(maps, tp, dt, how, s) : launch_d<__nv_bfloat16, 128>(maps, tp, dt, how, s);
+  return D == 64 ? launch_d<__half, 64>(maps, tp, dt, how, s) : launch_d<__half, 128>(maps, tp, dt, how, s);
 }
 
 }  // namespace mgqa

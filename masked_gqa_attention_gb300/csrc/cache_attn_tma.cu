@@ -55,7 +55,7 @@ struct Cfg {
     float wm[WK][ROWS], wl[WK][ROWS];
     float2 ml[ROWS];  // the CTA's (m, l), read by its cluster
     Drafts<kMaxT> drafts;
-    int64_t scratch[8];
+    LocateScratch<kThreads> scratch;
     uint2 ok[STAGES];  // which keys of a stage's tile count
     uint64_t full[STAGES], empty[STAGES];
     int maxdepth;
@@ -196,7 +196,7 @@ cache_attn_tma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     if (S && only.t0 >= only.t1 && tid < ROWS) sm.ml[tid] = make_float2(-INFINITY, 0.f);  // no share of the unit
     while (next_piece(pc)) {
       const RowPlan &rp = pc.rp;
-      const PieceOut po = out_of(p, pc, blockIdx.x, ROWS);
+      const PieceOut po = out_of(p, pc, blockIdx.x);
       uint32_t qa[D / 16][4];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -484,6 +484,7 @@ mgqa_status launch_t(const CUtensorMap (&maps)[4], TmaParams tp, const CacheAttn
   mgqa_status st = ensure_cluster_attr(kern, C::smem, attr, "cache attention kernel");
   if (st != MGQA_OK) return st;
   CacheAttnParams &p = tp.a;
+  p.block_rows = C::ROWS;
   p.RB = (p.R + C::ROWS - 1) / C::ROWS;
   p.tile_shift = 6;
   const int64_t units = (int64_t)p.B * p.Hkv * p.RB;

@@ -37,13 +37,14 @@ struct CacheAttnParams {
   int32_t window, sinks;  // window: kNoWindow when there is none
   int32_t tree;           // 1: drafts follow the cache; 0: the one query is the last cached token
   int32_t B, Hq, Hkv, T, n_rep, R, RB;  // R = T * n_rep rows per KV head, in RB blocks
+  int32_t block_rows;                   // query rows of a block (a unit's)
   int32_t tile_shift;                   // log2 of a tile's keys
   int32_t lead;                         // tiles counted for a unit's own cost
   int32_t min_run;                      // fewest tiles of a CTA's run
   float scale_log2;
   float *lse;
   int32_t *err;
-  float *part_o;    // [2 * grid][block rows][D] unnormalised partial outputs
+  float *part_o;    // [2 * grid][D / 4][block rows][4] unnormalised partial outputs
   float2 *part_ml;  // [2 * grid][block rows] their (max, sum)
 };
 
@@ -123,27 +124,48 @@ struct Cut {
   int64_t run;
 };
 
-// Scans the requests (every thread of the block takes part; scratch: one int64
-// per warp plus four). Finds the cut and, for the flat tile index `want` (a
-// function of the cut), its request and the flat index of that request's first
-// tile. `unit`: instead finds where request `want_b` starts.
+// a / b for 0 <= a, 0 < b: in 32 bits wherever it fits.
+MGQA_DEV int64_t div_up(int64_t a, int b) {
+  a += b - 1;
+  return a <= 0x7fffffff ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+MGQA_DEV int div_small(int64_t a, int b) {  // the quotient fits in 32 bits
+  return a <= 0x7fffffff ? (int)((uint32_t)a / (uint32_t)b) : (int)(a / b);
+}
+
+// Scans the requests (every thread of the block takes part), finds the cut and
+// the request that holds the first tile of run `cta`, or, with want_b >= 0,
+// where request want_b starts.
 struct Located {
   Cut cut;
-  int b;          // request holding the wanted tile, or the wanted request
-  int64_t start;  // flat index of its first tile
+  int b;          // the request
+  int64_t start;  // flat index of its first (lead) tile
+  RowPlan rp;     // its plan
+};
+template <int THREADS>
+struct LocateScratch {
+  int64_t sum[THREADS / 32];
+  int64_t start;
+  int32_t b;
+  RowPlan rp;
 };
 
 template <int THREADS>
-MGQA_DEV Located locate(const CacheAttnParams &p, int64_t *scratch, int grid, int cta, int want_b,
+MGQA_DEV Located locate(const CacheAttnParams &p, LocateScratch<THREADS> &sc, int grid, int cta, int want_b,
                         bool report) {
   constexpr int NW = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + THREADS - 1) / THREADS;
   const int64_t units = (int64_t)p.Hkv * p.RB;
   int64_t mine = 0;
+  RowPlan one;  // the plan of this thread's only request, when it has one
+  one.nt = 0;
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
-    if (b < p.B) mine += plan_row(p, b, report).nt + p.lead;
+    if (b < p.B) {
+      one = plan_row(p, b, report);
+      mine += one.nt + p.lead;
+    }
   }
   int64_t inc = mine;
 #pragma unroll
@@ -151,34 +173,35 @@ MGQA_DEV Located locate(const CacheAttnParams &p, int64_t *scratch, int grid, in
     const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += up;
   }
-  if (lane == 31) scratch[warp] = inc;
+  if (lane == 31) sc.sum[warp] = inc;
   __syncthreads();
   int64_t before = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
-    if (w < warp) before += scratch[w];
-    total += scratch[w];
+    if (w < warp) before += sc.sum[w];
+    total += sc.sum[w];
   }
   before += inc - mine;  // tiles (of one head and row block) of the requests ahead of mine
   Located r;
   r.cut.total = total * units;
-  r.cut.run = max((int64_t)p.min_run, (r.cut.total + grid - 1) / grid);
+  r.cut.run = max((int64_t)p.min_run, div_up(r.cut.total, grid));
   const int64_t want = (int64_t)cta * r.cut.run;
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
     if (b >= p.B) break;
-    const int nt = plan_row(p, b, false).nt + p.lead;
-    const bool hit = want_b >= 0 ? b == want_b
-                                 : (want >= before * units && want < (before + nt) * units);
-    if (hit) {
-      scratch[NW] = b;
-      scratch[NW + 1] = before * units;
+    if (per > 1) one = plan_row(p, b, false);
+    const int len = one.nt + p.lead;
+    if (want_b >= 0 ? b == want_b : (want >= before * units && want < (before + len) * units)) {
+      sc.b = b;
+      sc.start = before * units;
+      sc.rp = one;
     }
-    before += nt;
+    before += len;
   }
   __syncthreads();
-  r.b = (int)scratch[NW];
-  r.start = scratch[NW + 1];
+  r.b = sc.b;
+  r.start = sc.start;
+  r.rp = sc.rp;
   return r;
 }
 
@@ -253,38 +276,39 @@ struct Piece {
   int b, g, rb, t0, t1;
 };
 struct Walker {
-  int64_t f, f1, base;
-  int b, units, RB, lead;
+  int64_t left;  // tiles of the run that are left
+  int b, unit, v0, units, RB, lead;
   RowPlan rp;
 
   MGQA_DEV void start(const CacheAttnParams &p, const Located &loc, int cta) {
-    f = (int64_t)cta * loc.cut.run;
-    f1 = min(f + loc.cut.run, loc.cut.total);
-    base = loc.start;
-    b = loc.b;
+    const int64_t f = (int64_t)cta * loc.cut.run;
+    left = min(loc.cut.run, loc.cut.total - f);
     RB = p.RB;
     lead = p.lead;
     units = p.Hkv * p.RB;
-    if (f < f1) rp = plan_row(p, b, false);
+    if (left <= 0) return;
+    b = loc.b;
+    rp = loc.rp;
+    unit = div_small(f - loc.start, rp.nt + lead);
+    v0 = (int)(f - loc.start - (int64_t)unit * (rp.nt + lead));
   }
   MGQA_DEV bool next(const CacheAttnParams &p, Piece &pc) {
-    while (f < f1) {
-      const int len = rp.nt + lead;
-      if (f - base >= (int64_t)units * len) {
-        base += (int64_t)units * len;
+    while (left > 0) {
+      if (unit == units) {
+        unit = 0;
         rp = plan_row(p, ++b, false);
-        continue;
       }
-      const int64_t rel = f - base;
-      const int unit = (int)(rel / len), v0 = (int)(rel - (int64_t)unit * len);
-      const int v1 = (int)min((int64_t)len, v0 + (f1 - f));
-      f += v1 - v0;
+      const int v1 = (int)min((int64_t)(rp.nt + lead), v0 + left);
+      const int from = v0;
+      pc.b = b;
+      pc.g = RB == 1 ? unit : unit / RB;
+      pc.rb = RB == 1 ? 0 : unit - pc.g * RB;
+      left -= v1 - from;
+      v0 = 0;
+      ++unit;
       if (v1 <= lead) continue;  // the run ends within the unit's lead: the next run has all of it
       pc.rp = rp;
-      pc.b = b;
-      pc.g = unit / RB;
-      pc.rb = unit % RB;
-      pc.t0 = max(0, v0 - lead);
+      pc.t0 = max(0, from - lead);
       pc.t1 = v1 - lead;
       return true;
     }
@@ -299,16 +323,17 @@ struct PieceOut {
   int64_t slot;  // partial slot
   int b, g, row0, rows;
 };
-MGQA_DEV PieceOut out_of(const CacheAttnParams &p, const Piece &pc, int cta, int block_rows) {
+MGQA_DEV PieceOut out_of(const CacheAttnParams &p, const Piece &pc, int cta) {
   return PieceOut{pc.t0 == 0 && pc.t1 == pc.rp.nt, (int64_t)cta * 2 + (pc.t0 > 0 ? 0 : 1), pc.b, pc.g,
-                  pc.rb * block_rows, min(block_rows, p.R - pc.rb * block_rows)};
+                  pc.rb * p.block_rows, min(p.block_rows, p.R - pc.rb * p.block_rows)};
 }
 
 // Where row r of a piece goes: its finished values, or its unnormalised ones.
+// BR: rows that a partial result has room for.
 template <typename T, int D, int BR>
 struct RowOut {
   T *out;       // finished
-  float *part;  // else
+  float *part;  // else: four features at part, the next four BR * 4 floats on
   float inv;
 
   // `m`, `l` of the row in log2 units; `tell`: this thread writes what the row
@@ -323,7 +348,7 @@ struct RowOut {
       if (tell && p.lse)
         p.lse[((int64_t)po.b * p.Hq + h) * p.T + t] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
     } else {
-      part = p.part_o + (po.slot * BR + r) * D;
+      part = p.part_o + po.slot * (BR * D) + r * 4;
       if (tell) p.part_ml[po.slot * BR + r] = make_float2(m, l);
     }
   }
@@ -332,12 +357,13 @@ struct RowOut {
   MGQA_DEV void put(int d, const float (&o)[N]) const {
     static_assert(N == 2 || N == 4 || N == 8, "one store, or two");
     if (part) {
+      // (rows side by side: the kernels' lanes hold consecutive rows)
       if constexpr (N == 2) {
-        *reinterpret_cast<float2 *>(part + d) = make_float2(o[0], o[1]);
+        *reinterpret_cast<float2 *>(part + (d / 4) * (BR * 4) + d % 4) = make_float2(o[0], o[1]);
       } else {
 #pragma unroll
         for (int i = 0; i < N; i += 4)
-          *reinterpret_cast<float4 *>(part + d + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          *reinterpret_cast<float4 *>(part + ((d + i) / 4) * (BR * 4)) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
       }
     } else if constexpr (sizeof(T) == 4) {
       if constexpr (N == 2) {

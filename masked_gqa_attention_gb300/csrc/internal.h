@@ -164,6 +164,11 @@ mgqa_status pack_pair(bool unpack, mgqa_dtype dt, int B, int H, int D, const voi
 bool make_tma_map_4d(CUtensorMap *m, mgqa_dtype dt, const void *base, int B, int H, int L, int D,
                      const int64_t *st, int box_x, int box_y, bool swizzle128);
 
+// The general form: `rank` dimensions, innermost first (its stride is 1; the
+// others' in elements).
+bool make_tma_map(CUtensorMap *m, mgqa_dtype dt, const void *base, int rank, const int64_t *dims,
+                  const int64_t *strides, const int *box, bool swizzle128);
+
 // Prefill on the CUDA cores (fp32 I/O).
 mgqa_status launch_prefill_simt(const mgqa_args &a, cudaStream_t s,
                                 const WindowRule &win = WindowRule());

@@ -1064,23 +1064,32 @@ static EncodeTiledFn encode_fn() {
   return f;
 }
 
-bool make_tma_map_4d(CUtensorMap *m, mgqa_dtype dt, const void *base, int B, int H, int L, int D,
-                     const int64_t *st, int box_x, int box_y, bool swizzle128) {
+bool make_tma_map(CUtensorMap *m, mgqa_dtype dt, const void *base, int rank, const int64_t *dims,
+                  const int64_t *strides, const int *box, bool swizzle128) {
   EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
+  if (!fn || rank < 2 || rank > 5) return false;
   const size_t es = dt == MGQA_FP32 ? 4 : 2;
   const CUtensorMapDataType t = dt == MGQA_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                 : dt == MGQA_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)L, (cuuint64_t)H, (cuuint64_t)B};
-  const cuuint64_t strides[3] = {(cuuint64_t)st[2] * es, (cuuint64_t)st[1] * es,
-                                 (cuuint64_t)st[0] * es};
-  const cuuint32_t box[4] = {(cuuint32_t)box_x, (cuuint32_t)box_y, 1, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(m, t, 4, const_cast<void *>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE,
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], estr[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = (cuuint64_t)dims[i];
+    b[i] = (cuuint32_t)box[i];
+    estr[i] = 1;
+    if (i) st[i - 1] = (cuuint64_t)strides[i - 1] * es;
+  }
+  return fn(m, t, (cuuint32_t)rank, const_cast<void *>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_tma_map_4d(CUtensorMap *m, mgqa_dtype dt, const void *base, int B, int H, int L, int D,
+                     const int64_t *st, int box_x, int box_y, bool swizzle128) {
+  const int64_t dims[4] = {D, L, H, B}, strides[3] = {st[2], st[1], st[0]};
+  const int box[4] = {box_x, box_y, 1, 1};
+  return make_tma_map(m, dt, base, 4, dims, strides, box, swizzle128);
 }
 
 namespace {

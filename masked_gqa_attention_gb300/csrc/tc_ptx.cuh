@@ -24,6 +24,16 @@ MGQA_DEV void tma_load_4d(void *dst, const CUtensorMap *map, int x, int y, int z
       : "memory");
 }
 
+MGQA_DEV void tma_load_5d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, int c4,
+                          uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+
 // 4-D tiled tensor store from this CTA's shared memory (bulk-group tracked);
 // coordinates are non-negative, x a multiple of 16 bytes of elements.
 MGQA_DEV void tma_store_4d(const CUtensorMap *map, const void *src, int x, int y, int z, int w) {
