@@ -748,7 +748,7 @@ mgqa_status launch_cache_attn(const mgqa_args &a, const mgqa_pages *pages, const
   p.lse = a.lse; p.err = a.dev_error;
   const CacheAttnLaunch how{ws, device_sm_count()};
   if (how.sms < 1) return fail(MGQA_ERR_CUDA, "cannot read the SM count of the current device");
-  if (cache_attn_tma_takes(p, a.dtype)) return launch_cache_attn_tma(p, a.dtype, a.D, how, s);
+  if (cache_attn_tma_takes(p, a.dtype, a.D)) return launch_cache_attn_tma(p, a.dtype, a.D, how, s);
   if (cache_attn_tc_takes(p, a.dtype)) return launch_cache_attn_tc(p, a.dtype, a.D, how, s);
   if (a.dtype == MGQA_BF16)
     return a.D == 64 ? launch_16bit<__nv_bfloat16, 64>(p, how, s)

@@ -14,8 +14,12 @@
 //                 the current one is done, and its description for the others
 //   warps 4..   : one softmax warpgroup per 128 rows (thread = row)
 // Per tile n and row block t: S_t = Q_t K_n^T; softmax (running maximum, lazy
-// rescale of O_t past 2^8) hands P_t over in tensor memory; O_t += P_t V_n and
-// at once S_t(n+1), as in the prefill kernel. Between two pieces the softmax
+// rescale of O_t past 2^8) hands P_t over in tensor memory; O_t += P_t V_n.
+// With two row blocks S_t(n+1) follows O_t += P_t V_n at once and the blocks
+// take turns on the tensor cores and the softmax warps, as the heads in the
+// prefill kernel. With one row block S has two buffers instead, and S(n+1) runs
+// under the softmax of tile n (S behind P V, the chain of softmax, P V and S took
+// 3000 cycles a tile, more than the reads'). Between two pieces the softmax
 // warpgroups read O_t out while the next query rows, K and V are on their way.
 // (The softmax warps loading the rows themselves, between the pieces, cost ~4000
 // cycles a piece, and their walk over the pieces the registers of the score row.) Values of keys that do not
@@ -52,7 +56,8 @@ struct Lay {
   static constexpr int misc_off = v_off + STAGES * KB * BOX;
   static constexpr int threads = 128 * (1 + NT);
   static constexpr int ROWS = BM * NT;
-  static constexpr uint32_t tmem_used = NT * (BN + D);
+  static constexpr int SB = NT == 1 ? 2 : 1;  // score buffers of a row block
+  static constexpr uint32_t tmem_used = NT * (SB * BN + D);
   static constexpr uint32_t tmem_cols = tmem_used <= 256 ? 256 : 512;
   struct Misc {
     Drafts<kMaxDrafts> drafts;
@@ -61,7 +66,7 @@ struct Lay {
     uint64_t pready[kPieceRing], qfree;
     uint4 ok[kOkRing];  // which keys of a tile count
     uint64_t kfull[STAGES], vfull[STAGES], kempty[STAGES], vempty[STAGES];
-    uint64_t sfull[NT], pfull[NT], odone[NT], ofree[NT], qfull[NT], drain;
+    uint64_t sfull[NT * SB], pfull[NT], odone[NT], ofree[NT], qfull[NT], drain;
     uint32_t tmem;
     int maxdepth;
   };
@@ -74,8 +79,11 @@ MGQA_DEV uint32_t word_of(const uint4 &w, int i) { return i == 0 ? w.x : i == 1 
 
 // One 128-key tile of one softmax row (thread = row) in tensor memory: see the
 // prefill kernel's softmax_tile; the scale is not negative here.
+// `pv_done`: phase `pv_parity` of that barrier tells that O holds every tile
+// before this one (null: S of this tile was issued behind them).
 template <typename T, int D, bool PARTIAL>
-MGQA_DEV void softmax_row(uint32_t t_s, uint32_t t_o, const uint32_t (&mw)[4], float sl2, float &m_used, float &l) {
+MGQA_DEV void softmax_row(uint32_t t_s, uint32_t t_o, const uint32_t (&mw)[4], float sl2, float &m_used, float &l,
+                          uint64_t *pv_done, uint32_t pv_parity, int32_t *err) {
   uint32_t sr[BN];
   float mr;
   if constexpr (!PARTIAL) {
@@ -114,7 +122,11 @@ MGQA_DEV void softmax_row(uint32_t t_s, uint32_t t_o, const uint32_t (&mw)[4], f
     l *= factor;
   }
   if (__any_sync(0xffffffffu, rescale)) {
-    // O holds every P.V issued so far: S of this tile was issued behind them
+    if (pv_done) {
+      mbar_wait(pv_done, pv_parity, err);
+      __syncwarp();
+      tc::fence_after_sync();
+    }
 #pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
       uint32_t o[32];
@@ -179,8 +191,8 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       mbar_init(sm.kempty + s, 1);
       mbar_init(sm.vempty + s, 1);
     }
+    for (int t = 0; t < NT * L::SB; ++t) mbar_init(sm.sfull + t, 1);
     for (int t = 0; t < NT; ++t) {
-      mbar_init(sm.sfull + t, 1);
       mbar_init(sm.pfull + t, 128);
       mbar_init(sm.odone + t, 1);
       mbar_init(sm.ofree + t, 128);
@@ -197,6 +209,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     tc::prefetch_tensormap(&tm_vn);
   }
   if (warp == 1) tc::tmem_alloc(&sm.tmem, L::tmem_cols);
+  if (warp == 2) touch_params(tp, lane);
   grid_dependency_wait();
   allow_dependents();  // lengths and tables are final from here on
   Walker walk;
@@ -307,30 +320,31 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity, p.err));
       return ok;
     };
-    auto issue_s = [&](int t, int st, int k0, int k1, bool last) {
+    // S of row block t, into score buffer sb
+    auto issue_s = [&](int t, int sb, int st, int k0, int k1, bool last) {
       const uint64_t qd = qd0 + (uint64_t)t * kTileStep, kd = kd0 + (uint64_t)st * kTileStep;
       if (leader) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           if (kk < k0 || kk >= k1) continue;
           const uint64_t off = (uint64_t)((kk / 4) * BOX + (kk % 4) * 32) >> 4;
-          tc::mma_ss(tmem + t * BN, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
+          tc::mma_ss(tmem + (t + sb) * BN, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
         }
         if (k1 == D / 16) {
-          tc::mma_commit(sm.sfull + t);
+          tc::mma_commit(sm.sfull + t + sb);
           if (t == NT - 1) tc::mma_commit(sm.kempty + st);
           if (t == NT - 1 && last) tc::mma_commit(&sm.qfree);  // the piece's query rows are read
         }
       }
       __syncwarp();
     };
-    auto issue_pv = [&](int t, int st, int k0, int k1, bool first) {
+    auto issue_pv = [&](int t, int sb, int st, int k0, int k1, bool first) {
       const uint64_t vd = vd0 + (uint64_t)st * kTileStep;
       if (leader) {
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk) {
           if (kk < k0 || kk >= k1) continue;
-          tc::mma_ts(tmem + NT * BN + t * D, tmem + t * BN + kk * 8, vd + (uint64_t)(kk * 2048 >> 4), id_pv,
+          tc::mma_ts(tmem + NT * L::SB * BN + t * D, tmem + (t + sb) * BN + kk * 8, vd + (uint64_t)(kk * 2048 >> 4), id_pv,
                      (!first || kk > 0) ? 1u : 0u);
         }
       }
@@ -344,7 +358,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       for (int t = 0; t < NT && ok; ++t) {
         if (!wait(sm.qfull + t, piece & 1)) break;
         tc::fence_after_sync();
-        issue_s(t, it % STAGES, 0, D / 16, nk == 1);
+        issue_s(t, it % L::SB, it % STAGES, 0, D / 16, nk == 1);
       }
       if (!ok || !wait(sm.vfull + it % STAGES, (it / STAGES) & 1)) break;
       bool p0_seen = false;
@@ -370,28 +384,47 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             __syncwarp();
           }
         }
-        bool p1_seen = false;
-        for (int t = 0; t < NT && ok; ++t) {
-          if (!(t == 0 ? p0_seen : p1_seen) && !wait(sm.pfull + t, at & 1)) break;
-          if (n == 0 && piece > 0 && !wait(sm.ofree + t, (piece - 1) & 1)) break;
-          tc::fence_after_sync();
-          issue_pv(t, st, 0, kHalfPV, n == 0);
-          if (has_next) {  // K of the next tile before its first S, V before the next P.V
-            if (t == 0 && !wait(sm.kfull + st1, par1)) break;
-            if (t == NT - 1 && !wait(sm.vfull + st1, par1)) break;
+        if constexpr (NT == 1) {
+          // the next S goes out ahead of this tile's softmax result
+          if (has_next) {
+            if (!wait(sm.kfull + st1, par1)) break;
             tc::fence_after_sync();
+            issue_s(0, (at + 1) & 1, st1, 0, D / 16, n + 2 == nk);
           }
-          issue_pv(t, st, kHalfPV, BN / 16, n == 0);
+          if (!wait(sm.pfull, at & 1)) break;
+          if (n == 0 && piece > 0 && !wait(sm.ofree, (piece - 1) & 1)) break;
+          tc::fence_after_sync();
+          issue_pv(0, at & 1, st, 0, BN / 16, n == 0);
           if (leader) {
-            if (!has_next) tc::mma_commit(sm.odone + t);
-            if (t == NT - 1) tc::mma_commit(sm.vempty + st);
+            tc::mma_commit(sm.vempty + st);
+            if (!has_next) tc::mma_commit(sm.odone);
           }
           __syncwarp();
-          if (has_next) {
-            issue_s(t, st1, 0, kLateS, false);
-            if (NT > 1 && t == NT - 1) p0_seen = __all_sync(0xffffffffu, mbar_test_wait(sm.pfull, (at + 1) & 1));
-            else if (NT > 1) p1_seen = __all_sync(0xffffffffu, mbar_test_wait(sm.pfull + 1, at & 1));
-            issue_s(t, st1, kLateS, D / 16, n + 2 == nk);
+          if (has_next && !wait(sm.vfull + st1, par1)) break;
+        } else {
+          bool p1_seen = false;
+          for (int t = 0; t < NT && ok; ++t) {
+            if (!(t == 0 ? p0_seen : p1_seen) && !wait(sm.pfull + t, at & 1)) break;
+            if (n == 0 && piece > 0 && !wait(sm.ofree + t, (piece - 1) & 1)) break;
+            tc::fence_after_sync();
+            issue_pv(t, 0, st, 0, kHalfPV, n == 0);
+            if (has_next) {  // K of the next tile before its first S, V before the next P.V
+              if (t == 0 && !wait(sm.kfull + st1, par1)) break;
+              if (t == NT - 1 && !wait(sm.vfull + st1, par1)) break;
+              tc::fence_after_sync();
+            }
+            issue_pv(t, 0, st, kHalfPV, BN / 16, n == 0);
+            if (leader) {
+              if (!has_next) tc::mma_commit(sm.odone + t);
+              if (t == NT - 1) tc::mma_commit(sm.vempty + st);
+            }
+            __syncwarp();
+            if (has_next) {
+              issue_s(t, 0, st1, 0, kLateS, false);
+              if (t == NT - 1) p0_seen = __all_sync(0xffffffffu, mbar_test_wait(sm.pfull, (at + 1) & 1));
+              else p1_seen = __all_sync(0xffffffffu, mbar_test_wait(sm.pfull + 1, at & 1));
+              issue_s(t, 0, st1, kLateS, D / 16, n + 2 == nk);
+            }
           }
         }
       }
@@ -451,7 +484,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     const int r = quarter * 32 + lane;  // row of the tile
     const int stid = tid - 128;         // thread among the softmax warps
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    const uint32_t t_s = tmem + lanes + t * BN, t_o = tmem + lanes + NT * BN + t * D;
+    const uint32_t t_s0 = tmem + lanes + t * BN, t_o = tmem + lanes + NT * L::SB * BN + t * D;
     const float sl2 = p.scale_log2;
     int it = 0, staged = -1;
     for (int piece = 0;; ++piece) {
@@ -485,7 +518,10 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       float m_used = -INFINITY, l = 0.f;
       const int t1 = pc.t1;
       for (int i = pc.t0; i < t1; ++i, ++it) {
-        if (ok) ok = mbar_wait(sm.sfull + t, it & 1, p.err);
+        // (a barrier per score buffer: S(n+1) may complete before S(n) is waited for)
+        const int sb = it % L::SB;
+        const uint32_t t_s = t_s0 + sb * BN;
+        if (ok) ok = mbar_wait(sm.sfull + t + sb, (it / L::SB) & 1, p.err);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {  // after a failed wait, tensor memory is left alone
           int kind;
@@ -493,9 +529,12 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           const uint4 okw = sm.ok[it % kOkRing];
           const bool full = !kind && all_of(okw) == 0xffffffffu && (k0 >= lo_all || k0 + BN <= min(p.sinks, rp.s_end));
           tc::fence_after_sync();
+          // (a rescale follows an earlier tile of the piece; its P V releases that tile's V stage)
+          uint64_t *pv_done = L::SB > 1 ? sm.vempty + (it - 1 + STAGES) % STAGES : nullptr;
+          const uint32_t pv_parity = (uint32_t)((it - 1) / STAGES) & 1u;
           uint32_t mw[4] = {0u, 0u, 0u, 0u};
           if (full) {
-            softmax_row<T, D, false>(t_s, t_o, mw, sl2, m_used, l);
+            softmax_row<T, D, false>(t_s, t_o, mw, sl2, m_used, l, pv_done, pv_parity, p.err);
           } else {
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
@@ -513,7 +552,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
               }
               mw[w] = x;
             }
-            softmax_row<T, D, true>(t_s, t_o, mw, sl2, m_used, l);
+            softmax_row<T, D, true>(t_s, t_o, mw, sl2, m_used, l, pv_done, pv_parity, p.err);
           }
           tc::fence_before_sync();
         }

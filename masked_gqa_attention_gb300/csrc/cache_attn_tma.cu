@@ -95,6 +95,7 @@ cache_attn_tma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
       tc::prefetch_tensormap(&tm_vn);
     }
   }
+  if (warp == 1) touch_params(tp, lane);
   grid_dependency_wait();
   allow_dependents();  // lengths and tables are final from here on
 
@@ -476,6 +477,13 @@ cache_attn_tma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
   }
 }
 
+// Whether the reads take at most ~10 us at 6.8 TB/s, whatever the lengths are.
+bool short_call(const CacheAttnParams &p, int D) {
+  CacheAttnParams q = p;
+  q.tile_shift = 6;
+  return (int64_t)p.B * p.Hkv * most_tiles(q) * (2 * kTile * D * 2) <= (int64_t)64 << 20;
+}
+
 template <typename T, int D, int WM>
 mgqa_status launch_t(const CUtensorMap (&maps)[4], TmaParams tp, const CacheAttnLaunch &how, cudaStream_t s) {
   using C = Cfg<D, WM>;
@@ -489,14 +497,13 @@ mgqa_status launch_t(const CUtensorMap (&maps)[4], TmaParams tp, const CacheAttn
   p.tile_shift = 6;
   const int64_t units = (int64_t)p.B * p.Hkv * p.RB;
   const int64_t tiles = most_tiles(p);  // of one unit, at most
-  // A cluster per unit while the call cannot be long: at most ~16 us of reads
-  // at 6.8 TB/s, whatever the lengths are. It saves the merge kernel's launch;
-  // equal runs balance long and ragged calls.
-  const int64_t bytes = units * tiles * 2 * C::TILEB;
+  // A cluster per unit while the call cannot be long (it saves the merge
+  // kernel's launch; equal runs balance long and ragged calls), and no more CTAs
+  // than SMs: a second one on an SM keeps whole clusters waiting.
   tp.cluster = 0;
-  if (bytes <= (int64_t)112 << 20) {
+  if (short_call(p, D)) {
     tp.cluster = 1;
-    while (tp.cluster < 16 && tp.cluster < tiles && units * tp.cluster * 2 <= 2 * how.sms) tp.cluster *= 2;
+    while (tp.cluster < 16 && tp.cluster < tiles && units * tp.cluster * 2 <= how.sms) tp.cluster *= 2;
   }
   if (tp.cluster) {
     const cudaError_t e = launch_pdl_cluster(kern, dim3((unsigned)(units * tp.cluster)), dim3(kThreads), C::smem, s,
@@ -537,8 +544,12 @@ bool cache_attn_maps(const CacheAttnParams &p, mgqa_dtype dt, int D, int tile, C
                      make_tma_map_4d(&maps[3], dt, p.vn, p.B, p.Hkv, p.T, D, p.vns, 64, tile, true));
 }
 
-bool cache_attn_tma_takes(const CacheAttnParams &p, mgqa_dtype dt) {
-  return dt != MGQA_FP32 && p.R <= 64 && (!p.table || p.page_size % 8 == 0);
+// Up to 64 rows; past 32 only short calls, where a cluster saves a launch: on
+// longer ones the tensor-memory kernel is ahead (64 rows, 4 requests of up to
+// 131072: 305 us here, 234 us there; one request of up to 4096: 13 and 19 us).
+bool cache_attn_tma_takes(const CacheAttnParams &p, mgqa_dtype dt, int D) {
+  if (dt == MGQA_FP32 || p.R > 64 || (p.table && p.page_size % 8)) return false;
+  return p.R <= 32 || short_call(p, D) || !cache_attn_tc_takes(p, dt);
 }
 
 mgqa_status launch_cache_attn_tma(const CacheAttnParams &p, mgqa_dtype dt, int D, const CacheAttnLaunch &how,

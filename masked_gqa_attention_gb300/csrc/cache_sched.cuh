@@ -71,7 +71,7 @@ inline void set_partials(CacheAttnParams &p, void *ws, int grid, int block_rows,
 mgqa_status launch_cache_merge(const CacheAttnParams &p, mgqa_dtype dt, int D, int block_rows, int grid,
                                cudaStream_t s);
 // TMA-fed kernels (16-bit; slots, or pages of a multiple of 8 slots; few rows).
-bool cache_attn_tma_takes(const CacheAttnParams &p, mgqa_dtype dt);
+bool cache_attn_tma_takes(const CacheAttnParams &p, mgqa_dtype dt, int D);
 mgqa_status launch_cache_attn_tma(const CacheAttnParams &p, mgqa_dtype dt, int D, const CacheAttnLaunch &how,
                                   cudaStream_t s);
 // Tensor-memory kernel (the same caches, more rows).
@@ -116,6 +116,15 @@ MGQA_DEV RowPlan plan_row(const CacheAttnParams &p, int b, bool report) {
   if (p.tree && live == 0) r.np = 0;  // no query is left to see anything
   r.nt = max(1, r.np + ((live + up) >> ts));
   return r;
+}
+
+// Brings the kernel's parameters into the constant cache, ahead of the grid-
+// dependency wait (each line's first use would cost a miss behind it).
+template <typename P>
+MGQA_DEV void touch_params(const P &p, int lane) {
+  uint32_t x = 0u;
+  for (int i = lane; i < (int)(sizeof(P) / 64); i += 32) x ^= reinterpret_cast<const uint32_t *>(&p)[i * 16];
+  asm volatile("" ::"r"(x));
 }
 
 // The cut of one call: tiles in all, and tiles of a run.
