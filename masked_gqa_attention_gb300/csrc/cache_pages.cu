@@ -2,17 +2,20 @@
 // of pages, and packing the pool. All of them move rows as they are; the
 // floor is one read and one write of every row moved.
 //
-// append: one pass, a block per (layer, request, run of rows); a thread has up
-//   to four 16-byte pieces of K and of V in flight, read in the order in which a
-//   projection leaves them ([T][Hkv][D]) and written as whole D-rows.
+// append: one pass, a block per (layer, request, run of rows); a thread has
+//   one 16-byte piece of K and of V in flight, read in the order in which a
+//   projection leaves them ([T][Hkv][D]) and written as whole D-rows. (32768 rows
+//   of 8 x 128 bf16: eight pieces a thread 64.6 us, four 51.7, two 45.5, one 42.2:
+//   smaller blocks overlap their look-ups with other blocks' copies.)
 // fork and compact: the page bookkeeping is integer work on a few arrays whose
 //   result every block needs, so it runs ahead of the copies in kernels of its
 //   own, joined by programmatic dependent launches:
-//     fork    -- gather (a block per pair: stages the source's table row, gives
-//                back and takes shares by integer atomics, whose order cannot
-//                matter), plan (one block: free pages as a bitmap in shared
-//                memory, requests and free pages matched by prefix sums), apply
-//                (table rows, lengths, and the copies);
+//     fork    -- gather (stages the sources' table rows, gives back and takes
+//                shares by integer atomics, whose order cannot matter; a block
+//                per pair, or, when the rows are few, the planning block itself:
+//                one launch less), plan (one block: free pages as a bitmap in
+//                shared memory, requests and free pages matched by prefix
+//                sums), apply (table rows, lengths, and the copies);
 //     compact -- plan (one block: the used pages as a bitmap, moves by prefix
 //                sums over its words) and apply (copies, table, counts).
 //   One block is enough for the plan: a pool of 2^16 pages is 256 KB of counts.
@@ -57,13 +60,13 @@ MGQA_DEV int valid_page(const Pool &p, int e) { return (unsigned)e < (unsigned)p
 // ---- append -------------------------------------------------------------------
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendU = 4;  // pieces of K (and of V) in flight per thread
 
 struct AppendParams {
   Pool c;
   const char *kn, *vn;
   int64_t kns[4], vns[4];  // layer, batch, head, row strides in bytes
   int32_t T;
+  int32_t block_rows;  // new rows of a block
   const int32_t *index, *count;
   int32_t *kv_len_out;
 };
@@ -76,26 +79,26 @@ append_kernel(const __grid_constant__ AppendParams p) {
   allow_dependents();
   const int64_t cap = c.table ? (int64_t)c.max_pages * c.page_size : c.page_size;
   const int n = __ldg(c.kv_len + b);
-  int cnt = p.count ? __ldg(p.count + b) : p.T;
+  const int cnt = p.count ? __ldg(p.count + b) : p.T;
   const bool bad = n < 0 || cnt < 0 || cnt > p.T || (int64_t)n + cnt > cap;
-  if (bad) cnt = 0;
-  if (blockIdx.x == 0 && layer == 0 && threadIdx.x == 0) {
-    if (bad) report_error(c.err, MGQA_ERR_INVALID_ARG);
-    p.kv_len_out[b] = n + cnt;
-  }
-  const int64_t total = (int64_t)cnt * c.Hkv * c.pieces;
-  const int64_t i0 = (int64_t)blockIdx.x * (kAppendThreads * kAppendU) + threadIdx.x;
-  uint4 kx[kAppendU], vx[kAppendU];
-  char *kd[kAppendU], *vd[kAppendU];
-#pragma unroll
-  for (int u = 0; u < kAppendU; ++u) {
-    const int64_t i = i0 + u * kAppendThreads;
-    kd[u] = nullptr;
-    if (i >= total) continue;
-    const int per = c.Hkv * c.pieces;
-    const int t = (int)(i / per), rem = (int)(i - (int64_t)t * per);
+  // the block's rows from t0 on, all heads of each. Without a count the new rows
+  // are read ahead of what tells where they go (the length, then the page).
+  const int per = c.Hkv * c.pieces;
+  const int t0 = (int)blockIdx.x * p.block_rows, rows = min(p.block_rows, p.T - t0);
+  for (int i = threadIdx.x; i < rows * per; i += kAppendThreads) {
+    const int tl = i / per, rem = i - tl * per, t = t0 + tl;
     const int h = rem / c.pieces, piece = rem - h * c.pieces;
+    if (p.count && (bad || t >= cnt)) break;
     const int from = p.index ? __ldg(p.index + (int64_t)b * p.T + t) : t;
+    const bool has = (unsigned)from < (unsigned)p.T;
+    uint4 kx, vx;
+    if (has) {
+      kx = __ldcs(reinterpret_cast<const uint4 *>(p.kn + layer * p.kns[0] + b * p.kns[1] + h * p.kns[2] +
+                                                  (int64_t)from * p.kns[3] + piece * 16));
+      vx = __ldcs(reinterpret_cast<const uint4 *>(p.vn + layer * p.vns[0] + b * p.vns[1] + h * p.vns[2] +
+                                                  (int64_t)from * p.vns[3] + piece * 16));
+    }
+    if (bad) break;
     const int j = n + t;
     int page = b, slot = j;
     if (c.table) {
@@ -103,59 +106,67 @@ append_kernel(const __grid_constant__ AppendParams p) {
       page = valid_page(c, __ldg(c.table + (int64_t)b * c.table_stride + pi));
       slot = j - pi * c.page_size;
     }
-    if ((unsigned)from >= (unsigned)p.T || page < 0) {
-      if (layer == 0 && rem == 0) report_error(c.err, MGQA_ERR_INVALID_ARG);
-      continue;
+    if (has && page >= 0) {
+      __stcs(reinterpret_cast<uint4 *>(c.k + layer * c.ks[0] + (int64_t)page * c.ks[1] + h * c.ks[2] +
+                                       (int64_t)slot * c.ks[3] + piece * 16), kx);
+      __stcs(reinterpret_cast<uint4 *>(c.v + layer * c.vs[0] + (int64_t)page * c.vs[1] + h * c.vs[2] +
+                                       (int64_t)slot * c.vs[3] + piece * 16), vx);
+    } else if (layer == 0 && rem == 0) {
+      report_error(c.err, MGQA_ERR_INVALID_ARG);
     }
-    kx[u] = __ldcs(reinterpret_cast<const uint4 *>(p.kn + layer * p.kns[0] + b * p.kns[1] + h * p.kns[2] +
-                                                   (int64_t)from * p.kns[3] + piece * 16));
-    vx[u] = __ldcs(reinterpret_cast<const uint4 *>(p.vn + layer * p.vns[0] + b * p.vns[1] + h * p.vns[2] +
-                                                   (int64_t)from * p.vns[3] + piece * 16));
-    kd[u] = c.k + layer * c.ks[0] + (int64_t)page * c.ks[1] + h * c.ks[2] + (int64_t)slot * c.ks[3] + piece * 16;
-    vd[u] = c.v + layer * c.vs[0] + (int64_t)page * c.vs[1] + h * c.vs[2] + (int64_t)slot * c.vs[3] + piece * 16;
   }
-#pragma unroll
-  for (int u = 0; u < kAppendU; ++u)
-    if (kd[u]) {
-      *reinterpret_cast<uint4 *>(kd[u]) = kx[u];
-      *reinterpret_cast<uint4 *>(vd[u]) = vx[u];
-    }
+  if (blockIdx.x == 0 && layer == 0 && threadIdx.x == 0) {
+    if (bad) report_error(c.err, MGQA_ERR_INVALID_ARG);
+    p.kv_len_out[b] = bad ? n : n + cnt;
+  }
 }
 
 // ---- copies of (parts of) pages --------------------------------------------------
 
-// Slots [0, slots) of page a of one layer's K or V to page b, by `threads`
-// threads of which this is `t`. Strides in bytes; a whole page without gaps is
-// one run.
-constexpr int kCopyU = 8;
+// Slots [0, slots) of page a of one layer's K or V to page b, by `warps` warps
+// of which this is `warp`: a warp, or several, per head's rows (per run of 16-
+// byte pieces, the whole page when it has no gaps).
+constexpr int kCopyU = 4;
 MGQA_DEV void copy_slots(char *base, const int64_t *st, int64_t layer, int a, int b, int heads, int slots,
-                         int page_size, int pieces, int t, int threads) {
+                         int page_size, int pieces, int warp, int warps) {
   const char *src = base + layer * st[0] + (int64_t)a * st[1];
   char *dst = base + layer * st[0] + (int64_t)b * st[1];
   const bool rows_run = st[3] == pieces * 16;
-  const bool run = rows_run && ((slots == page_size && st[2] == (int64_t)page_size * st[3]) || heads == 1);
-  const int per = slots * pieces;
-  const int64_t total = (int64_t)heads * per;
-  for (int64_t i0 = t; i0 < total; i0 += (int64_t)threads * kCopyU) {
-    uint4 x[kCopyU];
-    int64_t at[kCopyU];
+  int per = slots * pieces;  // pieces of a run
+  if (rows_run && slots == page_size && st[2] == (int64_t)page_size * st[3] && (int64_t)per * heads < 0x7fffffff) {
+    per *= heads;
+    heads = 1;
+  }
+  const int wph = max(1, warps / heads), step = 32 * wph;  // warps of a run
+  if (warp >= wph * heads) return;
+  for (int h = warp / wph; h < heads; h += warps / wph) {
+    const char *sh = src + h * st[2];
+    char *dh = dst + h * st[2];
+    const int first = (warp % wph) * 32 + (int)(threadIdx.x & 31);
+    if (rows_run) {
+      const uint4 *from = reinterpret_cast<const uint4 *>(sh);
+      uint4 *to = reinterpret_cast<uint4 *>(dh);
+      for (int i = first; i < per; i += step * kCopyU) {
+        uint4 x[kCopyU];
 #pragma unroll
-    for (int u = 0; u < kCopyU; ++u) {
-      const int64_t i = i0 + (int64_t)u * threads;
-      at[u] = -1;
-      if (i >= total) continue;
-      if (run) {
-        at[u] = i * 16;
-      } else {
-        const int h = (int)(i / per), rem = (int)(i - (int64_t)h * per);
-        at[u] = rows_run ? h * st[2] + (int64_t)rem * 16
-                         : h * st[2] + (rem / pieces) * st[3] + (int64_t)(rem % pieces) * 16;
+        for (int u = 0; u < kCopyU; ++u)
+          if (i + u * step < per) x[u] = __ldcs(from + i + u * step);
+#pragma unroll
+        for (int u = 0; u < kCopyU; ++u)
+          if (i + u * step < per) __stcs(to + i + u * step, x[u]);
       }
-      x[u] = __ldcs(reinterpret_cast<const uint4 *>(src + at[u]));
+    } else {
+      for (int i = first; i < per; i += step * 2) {  // rows apart: two pieces in flight
+        const int64_t at = (i / pieces) * st[3] + (i % pieces) * 16;
+        const int i2 = i + step;
+        const int64_t at2 = (i2 / pieces) * st[3] + (i2 % pieces) * 16;
+        uint4 y;
+        if (i2 < per) y = __ldcs(reinterpret_cast<const uint4 *>(sh + at2));
+        const uint4 x = __ldcs(reinterpret_cast<const uint4 *>(sh + at));
+        __stcs(reinterpret_cast<uint4 *>(dh + at), x);
+        if (i2 < per) __stcs(reinterpret_cast<uint4 *>(dh + at2), y);
+      }
     }
-#pragma unroll
-    for (int u = 0; u < kCopyU; ++u)
-      if (at[u] >= 0) __stcs(reinterpret_cast<uint4 *>(dst + at[u]), x[u]);
   }
 }
 
@@ -225,8 +236,9 @@ struct Pair {
   int32_t copy;       // page whose filled slots are copied (-1: none)
 };
 
-// Entries of the staged rows besides pages and -1: a fresh page, replacing
-// nothing, or page e which the row gives back.
+// Entries of a staged row that keeps its request (src == dst), besides pages
+// and -1: a fresh page, replacing nothing, or page e which the row gives back.
+// (A row that takes over another's gets fresh pages from its `full` on.)
 constexpr int32_t kFresh = -2;
 MGQA_DEV int32_t fresh_for(int e) { return e < 0 ? kFresh : -3 - e; }
 
@@ -237,37 +249,34 @@ struct ForkParams {
   int32_t *stage;  // [n][max_pages]
   Pair *pairs;     // [n]
   int32_t *fresh;  // [num_pages]
+  int32_t gather;  // the planning block gathers itself
 };
 
 constexpr int kForkThreads = 256;
 
-__global__ void __launch_bounds__(kForkThreads)
-fork_gather_kernel(const __grid_constant__ ForkParams p) {
+// Pair i: its numbers, its source's row staged, pages given back and shares
+// taken, by `threads` threads of which this is `t`; taken: an earlier pair has
+// this dst.
+MGQA_DEV void gather_pair(const ForkParams &p, int i, int s, int d, bool taken, int t, int threads) {
   const Pool &c = p.c;
-  const int i = blockIdx.x, tid = threadIdx.x;
-  grid_dependency_wait();
-  allow_dependents();
-  const int s = __ldg(p.src + i), d = __ldg(p.dst + i);
-  bool taken = false;
-  for (int k = tid; k < i; k += kForkThreads) taken = taken || __ldg(p.dst + k) == d;
-  const bool skip = __syncthreads_or(taken) || d < 0 || d >= c.rows || s < -1 || s >= c.rows;
+  const bool skip = taken || d < 0 || d >= c.rows || s < -1 || s >= c.rows;
   int len = 0;
   const int64_t cap = (int64_t)c.max_pages * c.page_size;
   if (!skip && s >= 0) {
     len = __ldg(c.kv_len + s);
     if (len < 0 || len > cap) {
-      if (tid == 0) report_error(c.err, MGQA_ERR_INVALID_ARG);
+      if (t == 0) report_error(c.err, MGQA_ERR_INVALID_ARG);
       len = len < 0 ? 0 : (int)cap;
     }
   }
   const int full = len / c.page_size;
-  if (tid == 0) {
+  if (t == 0) {
     if (skip) report_error(c.err, MGQA_ERR_INVALID_ARG);
     const int64_t need = s < 0 ? 0 : ((int64_t)len + p.extra + c.page_size - 1) / c.page_size;
     p.pairs[i] = Pair{s, skip ? -1 : d, len, full, need > c.max_pages ? -1 : (int32_t)need, 0, 0, -1};
   }
   if (skip) return;
-  for (int j = tid; j < c.max_pages; j += kForkThreads) {
+  for (int j = t; j < c.max_pages; j += threads) {
     const int e = s >= 0 ? valid_page(c, __ldg(c.table + (int64_t)s * c.table_stride + j)) : -1;
     p.stage[(int64_t)i * c.max_pages + j] = e;
     if (s != d) {
@@ -278,59 +287,114 @@ fork_gather_kernel(const __grid_constant__ ForkParams p) {
   }
 }
 
+__global__ void __launch_bounds__(kForkThreads)
+fork_gather_kernel(const __grid_constant__ ForkParams p) {
+  const int i = blockIdx.x, tid = threadIdx.x;
+  grid_dependency_wait();
+  allow_dependents();
+  const int s = __ldg(p.src + i), d = __ldg(p.dst + i);
+  bool taken = false;
+  for (int k = tid; k < i; k += kForkThreads) taken = taken || __ldg(p.dst + k) == d;
+  gather_pair(p, i, s, d, __syncthreads_or(taken), tid, kForkThreads);
+}
+
 // dynamic shared memory: the bitmap of free pages
 __global__ void __launch_bounds__(kPlanThreads)
 fork_plan_kernel(const __grid_constant__ ForkParams p) {
   extern __shared__ uint32_t bits[];
-  __shared__ int scratch[33], req_s[kMaxForks];
+  __shared__ int scratch[33], req_s[kMaxForks], dst_s[kMaxForks];
   const Pool &c = p.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int W = (c.num_pages + 31) / 32;
   grid_dependency_wait();
   allow_dependents();
+  if (p.gather) {
+    if (tid < p.n) dst_s[tid] = __ldg(p.dst + tid);
+    __syncthreads();
+    for (int i = warp; i < p.n; i += kPlanThreads / 32) {
+      const int d = dst_s[i];
+      bool taken = false;
+      for (int k = lane; k < i; k += 32) taken = taken || dst_s[k] == d;
+      gather_pair(p, i, __ldg(p.src + i), d, __any_sync(0xffffffffu, taken), lane, 32);
+    }
+    __threadfence();  // the counts were changed by atomics, the rows by other threads
+    __syncthreads();
+  }
   used_bitmap(c, bits);
   __syncthreads();
   for (int w = tid; w < W; w += kPlanThreads)
     bits[w] = ~bits[w] & low_mask(c.num_pages - 32 * w);
   __syncthreads();
-  // requests, a warp per pair; what is to become of each entry is noted in the
-  // staged row. Pages that a copy reads are not handed out.
-  for (int i = warp; i < p.n; i += kPlanThreads / 32) {
-    const Pair pr = p.pairs[i];
-    int req = 0;
-    if (pr.dst >= 0 && pr.src >= 0 && pr.need >= 0) {
-      int32_t *row = p.stage + (int64_t)i * c.max_pages;
-      for (int j0 = pr.full; j0 < pr.need; j0 += 32) {
-        const int j = j0 + lane;
-        bool fresh = false;
-        if (j < pr.need) {
-          const int e = __ldcg(row + j);
-          fresh = pr.src != pr.dst || e < 0 || __ldcg(c.ref + e) > 1;
-          if (fresh) {
-            if (j == pr.full && pr.len % c.page_size) {
-              p.pairs[i].copy = e;
-              if (e >= 0) atomicAnd(&bits[e >> 5], ~(1u << (e & 31)));
-              else report_error(c.err, MGQA_ERR_INVALID_ARG);  // the source lacks its last page
-            }
-            row[j] = pr.src == pr.dst ? fresh_for(e) : kFresh;
-          }
-        }
-        req += __popc(__ballot_sync(0xffffffffu, fresh));
+  // Requests. A row taken over asks for its pages from `full` on; a kept row for
+  // those it lacks or shares, noted in its staged row. The pages that copies read
+  // are not handed out.
+  Pair pr{-1, -1, 0, 0, 0, 0, 0, -1};
+  int req = 0;
+  if (tid < p.n) {
+    const int4 *q = reinterpret_cast<const int4 *>(p.pairs + tid);
+    const int4 a = __ldcg(q), b = __ldcg(q + 1);
+    pr = Pair{a.x, a.y, a.z, a.w, b.x, 0, 0, -1};
+  }
+  auto copy_from = [&](int i, int e) {  // the filled slots of page e go to a fresh one
+    if (e >= 0) atomicAnd(&bits[e >> 5], ~(1u << (e & 31)));
+    else report_error(c.err, MGQA_ERR_INVALID_ARG);  // the source lacks its last page
+    p.pairs[i].copy = e;
+  };
+  const bool asks = pr.dst >= 0 && pr.src >= 0 && pr.need >= 0;
+  constexpr int kFew = 8;  // entries that one thread looks at
+  if (asks && pr.src != pr.dst) {
+    req = pr.need - pr.full;
+    if (pr.len % c.page_size) copy_from(tid, __ldcg(p.stage + (int64_t)tid * c.max_pages + pr.full));
+  } else if (asks && pr.need - pr.full <= kFew) {
+    int32_t *row = p.stage + (int64_t)tid * c.max_pages + pr.full;
+    int e[kFew], r[kFew];
+#pragma unroll
+    for (int k = 0; k < kFew; ++k) e[k] = k < pr.need - pr.full ? __ldcg(row + k) : -1;
+#pragma unroll
+    for (int k = 0; k < kFew; ++k) r[k] = e[k] >= 0 ? __ldcg(c.ref + e[k]) : 2;
+#pragma unroll
+    for (int k = 0; k < kFew; ++k)
+      if (k < pr.need - pr.full && r[k] > 1) {
+        if (k == 0 && pr.len % c.page_size) copy_from(tid, e[0]);
+        row[k] = fresh_for(e[k]);
+        ++req;
       }
+  } else if (asks) {
+    req = -1;
+  }
+  if (tid < p.n) req_s[tid] = req;
+  __syncthreads();
+  for (int i = warp; i < p.n; i += kPlanThreads / 32) {  // kept rows with many entries: a warp each
+    if (req_s[i] >= 0) continue;
+    const int full = __ldcg(&p.pairs[i].full), need = __ldcg(&p.pairs[i].need), len = __ldcg(&p.pairs[i].len);
+    int32_t *row = p.stage + (int64_t)i * c.max_pages;
+    int n = 0;
+    for (int j0 = full; j0 < need; j0 += 32) {
+      const int j = j0 + lane;
+      bool fresh = false;
+      if (j < need) {
+        const int e = __ldcg(row + j);
+        fresh = e < 0 || __ldcg(c.ref + e) > 1;
+        if (fresh) {
+          if (j == full && len % c.page_size) copy_from(i, e);
+          row[j] = fresh_for(e);
+        }
+      }
+      n += __popc(__ballot_sync(0xffffffffu, fresh));
     }
-    if (lane == 0) req_s[i] = req;
+    __syncwarp();
+    if (lane == 0) req_s[i] = n;
   }
   __syncthreads();
+  if (tid < p.n) req = req_s[tid];
   // the free pages: every thread owns a run of words
   const int per = (W + kPlanThreads - 1) / kPlanThreads;
   int mine = 0, avail = 0, total = 0;
   for (int w = tid * per; w < min(W, tid * per + per); ++w) mine += __popc(bits[w]);
   int at = block_prefix(mine, scratch, &avail);
-  const int req = tid < p.n ? req_s[tid] : 0;
-  const int off = block_prefix(req, scratch, &total);
+  const int off = block_prefix(tid < p.n ? req : 0, scratch, &total);
   bool ok = false;
   if (tid < p.n) {
-    const Pair pr = p.pairs[tid];
     ok = pr.dst >= 0 && pr.need >= 0 && (req == 0 || off + req <= avail);
     if (pr.dst >= 0 && !ok) report_error(c.err, MGQA_ERR_INVALID_ARG);
     p.pairs[tid].off = off;
@@ -354,7 +418,9 @@ fork_apply_kernel(const __grid_constant__ ForkParams p) {
   const int i = blockIdx.x, layer = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
   grid_dependency_wait();
   allow_dependents();
-  const Pair pr = p.pairs[i];
+  const int4 *q = reinterpret_cast<const int4 *>(p.pairs + i);
+  const int4 qa = q[0], qb = q[1];
+  const Pair pr{qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
   if (pr.dst < 0) return;
   if (layer == 0 && blockIdx.z == 0) {
     int32_t *row = c.table + (int64_t)pr.dst * c.table_stride;
@@ -379,11 +445,11 @@ fork_apply_kernel(const __grid_constant__ ForkParams p) {
         for (int j0 = pr.full; j0 < pr.need; j0 += 32) {
           const int j = j0 + lane;
           const int e = j < pr.need ? from[j] : -1;
-          const bool fresh = j < pr.need && e <= kFresh;
+          const bool fresh = j < pr.need && (!keep || e <= kFresh);
           const uint32_t m = __ballot_sync(0xffffffffu, fresh);
           if (fresh) {
             row[j] = p.fresh[at + __popc(m & ((1u << lane) - 1u))];
-            if (e < kFresh) atomicSub(c.ref + (-3 - e), 1);
+            if (keep && e < kFresh) atomicSub(c.ref + (-3 - e), 1);
           } else if (j < pr.need) {
             row[j] = e;
           }
@@ -395,7 +461,7 @@ fork_apply_kernel(const __grid_constant__ ForkParams p) {
   if (!pr.ok || pr.copy < 0) return;
   const int to = p.fresh[pr.off];  // the copied entry is the pair's first fresh one
   copy_slots(blockIdx.z ? c.v : c.k, blockIdx.z ? c.vs : c.ks, layer, pr.copy, to, c.Hkv, pr.len % c.page_size,
-             c.page_size, c.pieces, tid, kForkThreads);
+             c.page_size, c.pieces, tid / 32, kForkThreads / 32);
 }
 
 // ---- compact ---------------------------------------------------------------------------
@@ -464,7 +530,7 @@ compact_apply_kernel(const __grid_constant__ CompactParams p) {
   for (int64_t s = (int64_t)blockIdx.x * (kCompactThreads / group) + tid / group; s < segs; s += step) {
     const int mv = (int)(s / (c.layers * 2)), r = (int)(s % (c.layers * 2));
     copy_slots((r & 1) ? c.v : c.k, (r & 1) ? c.vs : c.ks, r >> 1, p.from[mv], p.to[mv], c.Hkv, c.page_size,
-               c.page_size, c.pieces, tid % group, group);
+               c.page_size, c.pieces, tid % group / 32, group / 32);
   }
   // the renamed table and the counts; a count is read and written by one thread only
   const int64_t t0 = (int64_t)blockIdx.x * kCompactThreads + tid, ts = (int64_t)gridDim.x * kCompactThreads;
@@ -528,8 +594,10 @@ mgqa_status launch_cache_append(const mgqa_cache &c, const void *k_new, const vo
     p.vns[t] = vs[t] * es;
   }
   p.T = T; p.index = index; p.count = count; p.kv_len_out = kv_len_out;
-  const int64_t pieces = (int64_t)T * c.Hkv * p.c.pieces;
-  const int64_t bx = (pieces + kAppendThreads * kAppendU - 1) / (kAppendThreads * kAppendU);
+  const int64_t per = (int64_t)c.Hkv * p.c.pieces;
+  if (per > (1 << 20)) return fail(MGQA_ERR_UNSUPPORTED, "cache append: rows of more than 16 MB");
+  p.block_rows = (int32_t)std::max<int64_t>(1, kAppendThreads / per);
+  const int64_t bx = (T + p.block_rows - 1) / p.block_rows;
   if (c.rows > 65535 || c.layers > 65535 || bx > 0x7fffffff)
     return fail(MGQA_ERR_UNSUPPORTED, "more than 65535 requests or layers");
   return launched(launch_pdl(append_kernel, dim3((unsigned)bx, c.rows, c.layers), dim3(kAppendThreads), 0, s, p),
@@ -552,8 +620,13 @@ mgqa_status launch_cache_fork(const mgqa_cache &c, int n, const int32_t *src, co
   static std::atomic<uint64_t> attr{0};
   mgqa_status st = ensure_smem_attr(fork_plan_kernel, kMaxPages / 8, attr, "fork planning kernel");
   if (st != MGQA_OK) return st;
-  st = launched(launch_pdl(fork_gather_kernel, dim3(n), dim3(kForkThreads), 0, s, p), "cache fork");
-  if (st != MGQA_OK) return st;
+  // few table entries: the planning block stages them itself, a launch less (one
+  // block is slow at more: 2304 entries 17 us, against 4.5 + 7.3 us apart)
+  p.gather = (int64_t)n * c.max_pages <= 1024;
+  if (!p.gather) {
+    st = launched(launch_pdl(fork_gather_kernel, dim3(n), dim3(kForkThreads), 0, s, p), "cache fork");
+    if (st != MGQA_OK) return st;
+  }
   st = launched(launch_pdl(fork_plan_kernel, dim3(1), dim3(kPlanThreads), smem, s, p), "cache fork");
   if (st != MGQA_OK) return st;
   return launched(launch_pdl(fork_apply_kernel, dim3(n, c.layers, 2), dim3(kForkThreads), 0, s, p), "cache fork");
@@ -577,7 +650,7 @@ mgqa_status launch_cache_compact(const mgqa_cache &c, int32_t *table_out, int64_
   w += aligned16(words * 4);
   p.rank = reinterpret_cast<int32_t *>(w);
   const int64_t seg = (int64_t)c.Hkv * c.page_size * p.c.pieces;  // 16-byte pieces of a segment
-  p.warp_segments = seg <= 32 * kCopyU;
+  p.warp_segments = seg <= 256;
   static std::atomic<uint64_t> attr{0};
   mgqa_status st = ensure_smem_attr(compact_plan_kernel, kMaxPages / 8, attr, "compact planning kernel");
   if (st != MGQA_OK) return st;
