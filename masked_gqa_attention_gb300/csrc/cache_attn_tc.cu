@@ -48,12 +48,13 @@ struct TcCacheParams {
 
 template <int D, int NT>
 struct Lay {
-  static constexpr int STAGES = D == 128 ? 2 : 4;
+  static constexpr int STAGES = D == 128 ? 2 : 4;                // K tiles
+  static constexpr int VSTAGES = D == 128 && NT == 1 ? 3 : STAGES;  // V tiles: held until P V, and there is room
   static constexpr int KB = D / 64;
   static constexpr int q_off = 0;
   static constexpr int k_off = q_off + NT * KB * BOX;
   static constexpr int v_off = k_off + STAGES * KB * BOX;
-  static constexpr int misc_off = v_off + STAGES * KB * BOX;
+  static constexpr int misc_off = v_off + VSTAGES * KB * BOX;
   static constexpr int threads = 128 * (1 + NT);
   static constexpr int ROWS = BM * NT;
   static constexpr int SB = NT == 1 ? 2 : 1;  // score buffers of a row block
@@ -65,8 +66,8 @@ struct Lay {
     Piece pieces[kPieceRing];      // rp.nt < 0: no more
     uint64_t pready[kPieceRing], qfree;
     uint4 ok[kOkRing];  // which keys of a tile count
-    uint64_t kfull[STAGES], vfull[STAGES], kempty[STAGES], vempty[STAGES];
-    uint64_t sfull[NT * SB], pfull[NT], odone[NT], ofree[NT], qfull[NT], drain;
+    uint64_t kfull[STAGES], vfull[VSTAGES], kempty[STAGES], vempty[VSTAGES];
+    uint64_t sfull[NT * SB], pfull[NT * SB], odone[NT], ofree[NT], qfull[NT], drain;
     uint32_t tmem;
     int maxdepth;
   };
@@ -177,7 +178,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                      const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_vn,
                      const __grid_constant__ TcCacheParams tp) {
   using L = Lay<D, NT>;
-  constexpr int KB = L::KB, STAGES = L::STAGES, ROWS = L::ROWS;
+  constexpr int KB = L::KB, STAGES = L::STAGES, VS = L::VSTAGES, ROWS = L::ROWS;
   const CacheAttnParams &p = tp.a;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -187,13 +188,17 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(sm.kfull + s, 1);
-      mbar_init(sm.vfull + s, 1);
       mbar_init(sm.kempty + s, 1);
+    }
+    for (int s = 0; s < VS; ++s) {
+      mbar_init(sm.vfull + s, 1);
       mbar_init(sm.vempty + s, 1);
     }
-    for (int t = 0; t < NT * L::SB; ++t) mbar_init(sm.sfull + t, 1);
-    for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < NT * L::SB; ++t) {
+      mbar_init(sm.sfull + t, 1);
       mbar_init(sm.pfull + t, 128);
+    }
+    for (int t = 0; t < NT; ++t) {
       mbar_init(sm.odone + t, 1);
       mbar_init(sm.ofree + t, 128);
       mbar_init(sm.qfull + t, 1);
@@ -284,16 +289,17 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           for (int c = 0; c < KB; ++c)
             tc::tma_load_4d(smem + L::k_off + (st * KB + c) * BOX + row_off, kind ? &tm_kn : &tm_k, c * 64, slot, pc.g,
                             z, sm.kfull + st);
+        const int sv = it % VS, use_v = it / VS;
         ++it;
-        if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(sm.vempty + st, (use - 1) & 1, p.err));
+        if (use_v > 0) ok = __all_sync(0xffffffffu, mbar_wait(sm.vempty + sv, (use_v - 1) & 1, p.err));
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(sm.vfull + st, bytes);
+        if (lane == 0) mbar_arrive_expect_tx(sm.vfull + sv, bytes);
         __syncwarp();
         if (take)
 #pragma unroll
           for (int c = 0; c < KB; ++c)
-            tc::tma_load_4d(smem + L::v_off + (st * KB + c) * BOX + row_off, kind ? &tm_vn : &tm_v, c * 64, slot, pc.g,
-                            z, sm.vfull + st);
+            tc::tma_load_4d(smem + L::v_off + (sv * KB + c) * BOX + row_off, kind ? &tm_vn : &tm_v, c * 64, slot, pc.g,
+                            z, sm.vfull + sv);
         ++v_issued;
         page = next;
       }
@@ -301,7 +307,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     // no copy may be in flight when the CTA exits (only this warp arms the full
     // barriers: the last armed phase of each is the newest it can reach)
     for (int i = max(0, it - STAGES); i < it; ++i) mbar_wait(sm.kfull + i % STAGES, (i / STAGES) & 1, p.err);
-    for (int i = max(0, v_issued - STAGES); i < v_issued; ++i) mbar_wait(sm.vfull + i % STAGES, (i / STAGES) & 1, p.err);
+    for (int i = max(0, v_issued - VS); i < v_issued; ++i) mbar_wait(sm.vfull + i % VS, (i / VS) & 1, p.err);
     __syncwarp();
     role_end();
   } else if (warp == 1) {
@@ -360,26 +366,33 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         tc::fence_after_sync();
         issue_s(t, it % L::SB, it % STAGES, 0, D / 16, nk == 1);
       }
-      if (!ok || !wait(sm.vfull + it % STAGES, (it / STAGES) & 1)) break;
+      if (!ok || !wait(sm.vfull + it % VS, (it / VS) & 1)) break;
       bool p0_seen = false;
       for (int n = 0; n < nk && ok; ++n) {
-        const int at = it + n, st = at % STAGES, st1 = (at + 1) % STAGES;
+        const int at = it + n, st1 = (at + 1) % STAGES;
         const uint32_t par1 = (uint32_t)((at + 1) / STAGES) & 1u;
+        const int sv = at % VS, sv1 = (at + 1) % VS;
+        const uint32_t vpar1 = (uint32_t)((at + 1) / VS) & 1u;
         const bool has_next = n + 1 < nk;
-        {  // values of keys that do not count: cleared (their rows may hold anything)
+        {  // values of keys that do not count: cleared (their rows may hold anything,
+           // but for those behind the drafts, which the copy fills with zeros)
           const uint4 okw = sm.ok[at % kOkRing];
           if (all_of(okw) != 0xffffffffu) {
-            const uint32_t w4[4] = {okw.x, okw.y, okw.z, okw.w};
+            int kind;
+            const int k0 = first_key(pc.rp, pc.t0 + n, kShift, kind);
+            const int rows = kind && pc.rp.live > k0 ? p.T - k0 : BN;
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
-              if (w4[w] != 0xffffffffu)  // 16-byte pieces (the swizzle permutes them within a row)
-#pragma unroll 8
-                for (int u = lane; u < 32 * (D / 8); u += 32) {
-                  const int r = u / (D / 8), c = u % (D / 8);
-                  if (!((w4[w] >> r) & 1u))
-                    *reinterpret_cast<uint4 *>(smem + L::v_off + (st * KB + (c >> 3)) * BOX + (32 * w + r) * 128 +
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t clear = ~word_of(okw, w) & low_mask(rows - 32 * w);
+              if (clear)  // 16-byte pieces (the swizzle permutes them within a row)
+#pragma unroll
+                for (int u = 0; u < D / 8; ++u) {
+                  const int r = (u * 32 + lane) / (D / 8), c = (u * 32 + lane) % (D / 8);
+                  if ((clear >> r) & 1u)
+                    *reinterpret_cast<uint4 *>(smem + L::v_off + (sv * KB + (c >> 3)) * BOX + (32 * w + r) * 128 +
                                                (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
+            }
             fence_proxy_async_smem();
             __syncwarp();
           }
@@ -391,32 +404,34 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             tc::fence_after_sync();
             issue_s(0, (at + 1) & 1, st1, 0, D / 16, n + 2 == nk);
           }
-          if (!wait(sm.pfull, at & 1)) break;
+          // (a barrier per score buffer: P(n+1), which no longer waits for P V of tile n,
+          // would otherwise be able to complete a second phase ahead of this wait)
+          if (!wait(sm.pfull + (at & 1), (at >> 1) & 1)) break;
           if (n == 0 && piece > 0 && !wait(sm.ofree, (piece - 1) & 1)) break;
           tc::fence_after_sync();
-          issue_pv(0, at & 1, st, 0, BN / 16, n == 0);
+          issue_pv(0, at & 1, sv, 0, BN / 16, n == 0);
           if (leader) {
-            tc::mma_commit(sm.vempty + st);
+            tc::mma_commit(sm.vempty + sv);
             if (!has_next) tc::mma_commit(sm.odone);
           }
           __syncwarp();
-          if (has_next && !wait(sm.vfull + st1, par1)) break;
+          if (has_next && !wait(sm.vfull + sv1, vpar1)) break;
         } else {
           bool p1_seen = false;
           for (int t = 0; t < NT && ok; ++t) {
             if (!(t == 0 ? p0_seen : p1_seen) && !wait(sm.pfull + t, at & 1)) break;
             if (n == 0 && piece > 0 && !wait(sm.ofree + t, (piece - 1) & 1)) break;
             tc::fence_after_sync();
-            issue_pv(t, 0, st, 0, kHalfPV, n == 0);
+            issue_pv(t, 0, sv, 0, kHalfPV, n == 0);
             if (has_next) {  // K of the next tile before its first S, V before the next P.V
               if (t == 0 && !wait(sm.kfull + st1, par1)) break;
-              if (t == NT - 1 && !wait(sm.vfull + st1, par1)) break;
+              if (t == NT - 1 && !wait(sm.vfull + sv1, vpar1)) break;
               tc::fence_after_sync();
             }
-            issue_pv(t, 0, st, kHalfPV, BN / 16, n == 0);
+            issue_pv(t, 0, sv, kHalfPV, BN / 16, n == 0);
             if (leader) {
               if (!has_next) tc::mma_commit(sm.odone + t);
-              if (t == NT - 1) tc::mma_commit(sm.vempty + st);
+              if (t == NT - 1) tc::mma_commit(sm.vempty + sv);
             }
             __syncwarp();
             if (has_next) {
@@ -433,7 +448,8 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     // the last release of every stage has landed before the CTA exits; after a
     // wait that gave up, every MMA issued completes before tensor memory is freed
     for (int i = max(0, it - STAGES); i < it && ok; ++i)
-      wait(sm.kempty + i % STAGES, (i / STAGES) & 1) && wait(sm.vempty + i % STAGES, (i / STAGES) & 1);
+      wait(sm.kempty + i % STAGES, (i / STAGES) & 1);
+    for (int i = max(0, it - VS); i < it && ok; ++i) wait(sm.vempty + i % VS, (i / VS) & 1);
     if (!ok) {
       if (leader) tc::mma_commit(&sm.drain);
       __syncwarp();
@@ -530,8 +546,8 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           const bool full = !kind && all_of(okw) == 0xffffffffu && (k0 >= lo_all || k0 + BN <= min(p.sinks, rp.s_end));
           tc::fence_after_sync();
           // (a rescale follows an earlier tile of the piece; its P V releases that tile's V stage)
-          uint64_t *pv_done = L::SB > 1 ? sm.vempty + (it - 1 + STAGES) % STAGES : nullptr;
-          const uint32_t pv_parity = (uint32_t)((it - 1) / STAGES) & 1u;
+          uint64_t *pv_done = L::SB > 1 ? sm.vempty + (it - 1 + VS) % VS : nullptr;
+          const uint32_t pv_parity = (uint32_t)((it - 1) / VS) & 1u;
           uint32_t mw[4] = {0u, 0u, 0u, 0u};
           if (full) {
             softmax_row<T, D, false>(t_s, t_o, mw, sl2, m_used, l, pv_done, pv_parity, p.err);
@@ -556,7 +572,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           }
           tc::fence_before_sync();
         }
-        mbar_arrive(sm.pfull + t);
+        mbar_arrive(sm.pfull + t + sb);
       }
       // ---- the piece's rows: O out of tensor memory, finished or as a partial result
       if (ok) ok = mbar_wait(sm.odone + t, piece & 1, p.err);
@@ -608,7 +624,7 @@ mgqa_status launch_t(const CUtensorMap (&maps)[4], TcCacheParams tp, mgqa_dtype 
   const int box[5] = {64, p.n_rep, tp.q_drafts, 1, 1};
   if (!make_tma_map(&mq, dt, p.q, 5, dims, strides, box, true))
     return fail(MGQA_ERR_CUDA, "cuTensorMapEncodeTiled failed for q");
-  p.lead = 3;
+  p.lead = NT == 1 ? 4 : 8;  // (3 and 6 are within 2 % on NT = 1; 3 costs 9 % with two blocks and one request)
   p.min_run = 4;
   const int64_t tiles = (int64_t)p.B * p.Hkv * p.RB * (most_tiles(p) + p.lead);
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(how.sms, kCacheAttnMaxCtas / 2), tiles));
