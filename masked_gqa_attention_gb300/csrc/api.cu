@@ -328,7 +328,7 @@ mgqa_status masked_gqa_attn_prefill_window(const mgqa_args *args, int32_t window
   const mgqa::WindowRule win{window < mgqa::kWidestWindow ? window : mgqa::kWidestWindow,
                              sinks < args->Lk ? sinks : args->Lk};
   if (args->dtype != MGQA_FP32) return mgqa::launch_prefill_tc(*args, stream, mgqa::FusedRope(), win);
-  return mgqa::launch_prefill_simt(*args, stream, win);
+  return mgqa::launch_prefill_window_f32(*args, win, stream);
 }
 
 size_t masked_gqa_attn_cache_workspace_size(void) { return mgqa::cache_attn_workspace_bytes(); }

@@ -643,6 +643,8 @@ mgqa_status launch_merge(const CacheAttnParams &p, int grid, cudaStream_t s) {
 template <typename T, int D>
 mgqa_status launch_merge(const CacheAttnParams &p, int block_rows, int grid, cudaStream_t s) {
   switch (block_rows) {
+    case 4: return launch_merge<T, D, 4>(p, grid, s);
+    case 8: return launch_merge<T, D, 8>(p, grid, s);
     case 16: return launch_merge<T, D, 16>(p, grid, s);
     case 32: return launch_merge<T, D, 32>(p, grid, s);
     case 64: return launch_merge<T, D, 64>(p, grid, s);
@@ -705,7 +707,9 @@ mgqa_status launch_cache_merge(const CacheAttnParams &p, mgqa_dtype dt, int D, i
   if (dt == MGQA_BF16)
     return D == 64 ? launch_merge<__nv_bfloat16, 64>(p, block_rows, grid, s)
                    : launch_merge<__nv_bfloat16, 128>(p, block_rows, grid, s);
-  return D == 64 ? launch_merge<__half, 64>(p, block_rows, grid, s) : launch_merge<__half, 128>(p, block_rows, grid, s);
+  if (dt == MGQA_FP16)
+    return D == 64 ? launch_merge<__half, 64>(p, block_rows, grid, s) : launch_merge<__half, 128>(p, block_rows, grid, s);
+  return D == 64 ? launch_merge<float, 64>(p, block_rows, grid, s) : launch_merge<float, 128>(p, block_rows, grid, s);
 }
 
 mgqa_status launch_cache_attn(const mgqa_args &a, const mgqa_pages *pages, const mgqa_tree *tree, int32_t window,
@@ -748,6 +752,7 @@ mgqa_status launch_cache_attn(const mgqa_args &a, const mgqa_pages *pages, const
   p.lse = a.lse; p.err = a.dev_error;
   const CacheAttnLaunch how{ws, device_sm_count()};
   if (how.sms < 1) return fail(MGQA_ERR_CUDA, "cannot read the SM count of the current device");
+  if (cache_attn_f32_takes(p, a.dtype)) return launch_cache_attn_f32(p, a.D, how, s);
   if (cache_attn_tma_takes(p, a.dtype, a.D)) return launch_cache_attn_tma(p, a.dtype, a.D, how, s);
   if (cache_attn_tc_takes(p, a.dtype)) return launch_cache_attn_tc(p, a.dtype, a.D, how, s);
   if (a.dtype == MGQA_BF16)

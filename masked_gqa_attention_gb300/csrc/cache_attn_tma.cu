@@ -22,8 +22,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "cache_sched.cuh"
-#include "tc_ptx.cuh"
+#include "cache_producer.cuh"
 
 namespace mgqa {
 namespace {
@@ -31,12 +30,6 @@ namespace {
 constexpr int kConsumers = 128;
 constexpr int kThreads = kConsumers + 32;
 constexpr int kMaxT = 64;  // R <= 64
-
-struct TmaParams {
-  CacheAttnParams a;
-  int32_t box_rows;  // slots of a box of cached keys
-  int32_t cluster;   // CTAs of a unit's cluster; 0: equal runs
-};
 
 template <int D, int WM>
 struct Cfg {
@@ -66,8 +59,6 @@ struct Cfg {
     return (uint32_t)((c >> 3) * BOXB + r * 128 + (((c & 7) ^ (r & 7)) << 4));
   }
 };
-
-MGQA_DEV uint64_t low64(int n) { return n >= 64 ? ~0ull : (n <= 0 ? 0ull : ((1ull << n) - 1ull)); }
 
 template <typename T, int D, int WM>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -99,94 +90,12 @@ cache_attn_tma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
   grid_dependency_wait();
   allow_dependents();  // lengths and tables are final from here on
 
-  // ---- this CTA's pieces
-  Walker walk;
-  Piece only;
-  const int S = tp.cluster;
-  const int rank = S ? (int)blockIdx.x % S : 0;
-  if (S) {
-    const int unit = (int)blockIdx.x / S, units = p.Hkv * p.RB;
-    only.b = unit / units;
-    only.g = unit % units / p.RB;
-    only.rb = unit % p.RB;
-    only.rp = plan_row(p, only.b, rank == 0 && unit % units == 0 && tid == 0);
-    only.t0 = (int)((int64_t)only.rp.nt * rank / S);
-    only.t1 = (int)((int64_t)only.rp.nt * (rank + 1) / S);
-    __syncthreads();  // the barriers are initialised
-  } else {
-    walk.start(p, locate<kThreads>(p, sm.scratch, gridDim.x, blockIdx.x, -1, blockIdx.x == 0), blockIdx.x);
-  }
-  bool first = true;
-  auto next_piece = [&](Piece &pc) {
-    if (!S) return walk.next(p, pc);
-    const bool r = first && only.t0 < only.t1;
-    first = false;
-    pc = only;
-    return r;
-  };
+  Pieces pieces{};
+  pieces.start<kThreads>(tp, sm.scratch);  // (its barrier: the mbarriers are initialised)
+  const int S = pieces.S;
 
   if (warp == 4) {
-    // ---------------- producer ----------------
-    const int br = tp.box_rows, nbox = kTile / br;
-    bool ok = true;
-    int it = 0;  // tiles issued
-    Piece pc;
-    while (ok && next_piece(pc)) {
-      const RowPlan &rp = pc.rp;
-      // lane i: box i of the tile; the page of the next tile's box is looked up a tile ahead
-      auto look_up = [&](int t) {
-        int kind;
-        const int j0 = first_key(rp, t, 6, kind) + lane * br;
-        const bool some = !kind && lane < nbox && j0 < rp.n && ((rp.lo < rp.n && j0 + br > rp.lo) || j0 < rp.s_end);
-        return some ? page_of(p, pc.b, j0) : -2;  // -1: a page that is not there
-      };
-      int page = look_up(pc.t0);
-      for (int t = pc.t0; t < pc.t1 && ok; ++t, ++it) {
-        const int next = t + 1 < pc.t1 ? look_up(t + 1) : -2;
-        int kind;
-        const int k0 = first_key(rp, t, 6, kind);
-        uint64_t bits = 0ull;
-        if (kind) {
-          bits = lane == 0 ? low64(rp.live - k0) : 0ull;
-        } else if (page >= 0) {
-          const int j0 = k0 + lane * br;
-          bits = (low64(rp.n - j0) & (~low64(rp.lo - j0) | low64(rp.s_end - j0)) & low64(br)) << (lane * br);
-        } else if (page == -1) {
-          report_error(p.err, MGQA_ERR_INVALID_ARG);
-        }
-        const uint32_t lo = __reduce_or_sync(0xffffffffu, (uint32_t)bits);
-        const uint32_t hi = __reduce_or_sync(0xffffffffu, (uint32_t)(bits >> 32));
-        const bool take = bits != 0ull;
-        const int boxes = __popc(__ballot_sync(0xffffffffu, take));
-        const int st = it % STAGES, use = it / STAGES;
-        if (use > 0) {
-          const bool r = mbar_wait(sm.empty + st, (use - 1) & 1, p.err);
-          ok = __all_sync(0xffffffffu, r);
-          if (!ok) break;
-        }
-        const int rows = kind ? kTile : br;
-        if (lane == 0) {
-          sm.ok[st] = make_uint2(lo, hi);
-          mbar_arrive_expect_tx(sm.full + st, (uint32_t)(boxes * rows * 128 * C::KB * 2));
-        }
-        __syncwarp();
-        if (take) {
-          unsigned char *kd = ring + st * 2 * C::TILEB + (kind ? 0 : lane * br * 128), *vd = kd + C::TILEB;
-          const CUtensorMap *mk = kind ? &tm_kn : &tm_k, *mv = kind ? &tm_vn : &tm_v;
-          const int slot = kind ? k0 : slot_in_page(p, k0 + lane * br), z = kind ? pc.b : page;
-#pragma unroll
-          for (int c = 0; c < C::KB; ++c) {
-            tc::tma_load_4d(kd + c * C::BOXB, mk, c * 64, slot, pc.g, z, sm.full + st);
-            tc::tma_load_4d(vd + c * C::BOXB, mv, c * 64, slot, pc.g, z, sm.full + st);
-          }
-        }
-        page = next;
-      }
-    }
-    // the consumers see every tile land; after a wait that gave up, let the
-    // copies in flight land (bounded) before the CTA exits
-    if (!ok)
-      for (int i = max(0, it - STAGES); i < it; ++i) mbar_wait(sm.full + i % STAGES, (i / STAGES) & 1, p.err);
+    produce_tiles<C::KB, 64, STAGES>(tp, pieces, &tm_k, &tm_v, &tm_kn, &tm_vn, ring, sm.ok, sm.full, sm.empty);
   } else {
     // ---------------- consumers ----------------
     const int wm = warp / WK, wk = warp % WK;
@@ -194,8 +103,8 @@ cache_attn_tma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     bool ok = true;
     int it = 0, staged = -1;
     Piece pc;
-    if (S && only.t0 >= only.t1 && tid < ROWS) sm.ml[tid] = make_float2(-INFINITY, 0.f);  // no share of the unit
-    while (next_piece(pc)) {
+    if (pieces.idle() && tid < ROWS) sm.ml[tid] = make_float2(-INFINITY, 0.f);  // no share of the unit
+    while (pieces.next(p, pc)) {
       const RowPlan &rp = pc.rp;
       const PieceOut po = out_of(p, pc, blockIdx.x);
       uint32_t qa[D / 16][4];
@@ -436,52 +345,7 @@ cache_attn_tma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     }
   }
 
-  if (S) {
-    // ---- the cluster joins its shares: CTA `rank` a part of the rows' pieces
-    __syncwarp();
-    cluster_sync();
-    if (warp < 4) {
-      const PieceOut po{true, 0, only.b, only.g, only.rb * ROWS, min(ROWS, p.R - only.rb * ROWS)};
-      const uint32_t ml0 = smem_u32(sm.ml), res0 = smem_u32(ring);
-      for (int u = rank * kConsumers + tid; u < po.rows * (D / 4); u += S * kConsumers) {
-        const int r = u / (D / 4), d = (u % (D / 4)) * 4;
-        float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-        float2 ml[16];
-        float4 v[16];
-#pragma unroll
-        for (int x = 0; x < 16; ++x) {  // every load in flight at once
-          ml[x] = make_float2(-INFINITY, 0.f);
-          v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (x < S) {
-            ml[x] = ld_cluster_f32x2(cluster_map_u32(ml0 + r * 8, x));
-            v[x] = ld_cluster_f32x4(cluster_map_u32(res0 + (r * C::OP + d) * 4, x));
-          }
-        }
-#pragma unroll
-        for (int x = 0; x < 16; ++x) m = fmaxf(m, ml[x].x);
-#pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          if (ml[x].x == -INFINITY) continue;
-          const float w = fast_exp2(ml[x].x - m);
-          l = fmaf(ml[x].y, w, l);
-          acc[0] = fmaf(v[x].x, w, acc[0]);
-          acc[1] = fmaf(v[x].y, w, acc[1]);
-          acc[2] = fmaf(v[x].z, w, acc[2]);
-          acc[3] = fmaf(v[x].w, w, acc[3]);
-        }
-        RowOut<T, D, ROWS>(p, po, r, m, l, d == 0).put(d, acc);
-      }
-    }
-    __syncwarp();
-    cluster_sync();  // no CTA exits while its shared memory is read
-  }
-}
-
-// Whether the reads take at most ~10 us at 6.8 TB/s, whatever the lengths are.
-bool short_call(const CacheAttnParams &p, int D) {
-  CacheAttnParams q = p;
-  q.tile_shift = 6;
-  return (int64_t)p.B * p.Hkv * most_tiles(q) * (2 * kTile * D * 2) <= (int64_t)64 << 20;
+  if (S) join_cluster<T, D, ROWS, C::OP, kConsumers>(p, pieces, sm.ml, reinterpret_cast<const float *>(ring));
 }
 
 template <typename T, int D, int WM>
@@ -497,14 +361,7 @@ mgqa_status launch_t(const CUtensorMap (&maps)[4], TmaParams tp, const CacheAttn
   p.tile_shift = 6;
   const int64_t units = (int64_t)p.B * p.Hkv * p.RB;
   const int64_t tiles = most_tiles(p);  // of one unit, at most
-  // A cluster per unit while the call cannot be long (it saves the merge
-  // kernel's launch; equal runs balance long and ragged calls), and no more CTAs
-  // than SMs: a second one on an SM keeps whole clusters waiting.
-  tp.cluster = 0;
-  if (short_call(p, D)) {
-    tp.cluster = 1;
-    while (tp.cluster < 16 && tp.cluster < tiles && units * tp.cluster * 2 <= how.sms) tp.cluster *= 2;
-  }
+  tp.cluster = cluster_size(p, D * 2, how.sms);
   if (tp.cluster) {
     const cudaError_t e = launch_pdl_cluster(kern, dim3((unsigned)(units * tp.cluster)), dim3(kThreads), C::smem, s,
                                              tp.cluster, maps[0], maps[1], maps[2], maps[3], tp);
@@ -531,17 +388,18 @@ mgqa_status launch_d(const CUtensorMap (&maps)[4], const TmaParams &tp, const Ca
 }  // namespace
 
 bool cache_attn_maps(const CacheAttnParams &p, mgqa_dtype dt, int D, int tile, CUtensorMap (&maps)[4], int &box_rows) {
+  const int cols = dt == MGQA_FP32 ? 32 : 64;  // 128 bytes
   box_rows = tile;
   if (p.table)
     for (; p.page_size % box_rows; box_rows /= 2) {}
   const int pages = p.table ? p.num_pages : p.B, slots = p.table ? p.page_size : p.cap;
-  if (!make_tma_map_4d(&maps[0], dt, p.k, pages, p.Hkv, slots, D, p.ks, 64, box_rows, true) ||
-      !make_tma_map_4d(&maps[1], dt, p.v, pages, p.Hkv, slots, D, p.vs, 64, box_rows, true))
+  if (!make_tma_map_4d(&maps[0], dt, p.k, pages, p.Hkv, slots, D, p.ks, cols, box_rows, true) ||
+      !make_tma_map_4d(&maps[1], dt, p.v, pages, p.Hkv, slots, D, p.vs, cols, box_rows, true))
     return false;
   maps[2] = maps[0];
   maps[3] = maps[1];
-  return !p.tree || (make_tma_map_4d(&maps[2], dt, p.kn, p.B, p.Hkv, p.T, D, p.kns, 64, tile, true) &&
-                     make_tma_map_4d(&maps[3], dt, p.vn, p.B, p.Hkv, p.T, D, p.vns, 64, tile, true));
+  return !p.tree || (make_tma_map_4d(&maps[2], dt, p.kn, p.B, p.Hkv, p.T, D, p.kns, cols, tile, true) &&
+                     make_tma_map_4d(&maps[3], dt, p.vn, p.B, p.Hkv, p.T, D, p.vns, cols, tile, true));
 }
 
 // Up to 64 rows; past 32 only short calls, where a cluster saves a launch: on
@@ -549,7 +407,7 @@ bool cache_attn_maps(const CacheAttnParams &p, mgqa_dtype dt, int D, int tile, C
 // 131072: 305 us here, 234 us there; one request of up to 4096: 13 and 19 us).
 bool cache_attn_tma_takes(const CacheAttnParams &p, mgqa_dtype dt, int D) {
   if (dt == MGQA_FP32 || p.R > 64 || (p.table && p.page_size % 8)) return false;
-  return p.R <= 32 || short_call(p, D) || !cache_attn_tc_takes(p, dt);
+  return p.R <= 32 || short_call(p, D * 2) || !cache_attn_tc_takes(p, dt);
 }
 
 mgqa_status launch_cache_attn_tma(const CacheAttnParams &p, mgqa_dtype dt, int D, const CacheAttnLaunch &how,

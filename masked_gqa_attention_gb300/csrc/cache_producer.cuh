@@ -1,0 +1,187 @@
+// The producer warp of the cache attention kernels that fetch 64-key tiles by
+// TMA: it follows the page table and issues every tile as boxes that never cross
+// a page into a ring of stages.
+#pragma once
+
+#include "cache_sched.cuh"
+#include "tc_ptx.cuh"
+
+namespace mgqa {
+
+struct TmaParams {
+  CacheAttnParams a;
+  int32_t box_rows;  // slots of a box of cached keys
+  int32_t cluster;   // CTAs of a unit's cluster; 0: equal runs
+};
+
+MGQA_DEV uint64_t low64(int n) { return n >= 64 ? ~0ull : (n <= 0 ? 0ull : ((1ull << n) - 1ull)); }
+
+// The pieces of a CTA: its run of the flat tile list, or, in a cluster, its share
+// of one unit's tiles.
+struct Pieces {
+  Walker walk;
+  Piece only;
+  int S, rank;
+  bool first;
+
+  // Every thread of the block (it ends with a barrier).
+  template <int THREADS>
+  MGQA_DEV void start(const TmaParams &tp, LocateScratch<THREADS> &scratch) {
+    const CacheAttnParams &p = tp.a;
+    S = tp.cluster;
+    rank = S ? (int)blockIdx.x % S : 0;
+    first = true;
+    if (S) {
+      const int unit = (int)blockIdx.x / S, units = p.Hkv * p.RB;
+      only.b = unit / units;
+      only.g = unit % units / p.RB;
+      only.rb = unit % p.RB;
+      only.rp = plan_row(p, only.b, rank == 0 && unit % units == 0 && threadIdx.x == 0);
+      only.t0 = (int)((int64_t)only.rp.nt * rank / S);
+      only.t1 = (int)((int64_t)only.rp.nt * (rank + 1) / S);
+      __syncthreads();
+    } else {
+      walk.start(p, locate<THREADS>(p, scratch, gridDim.x, blockIdx.x, -1, blockIdx.x == 0), blockIdx.x);
+    }
+  }
+  MGQA_DEV bool next(const CacheAttnParams &p, Piece &pc) {
+    if (!S) return walk.next(p, pc);
+    const bool r = first && only.t0 < only.t1;
+    first = false;
+    pc = only;
+    return r;
+  }
+  MGQA_DEV bool idle() const { return S && only.t0 >= only.t1; }  // a cluster's CTA without a share
+};
+
+// A whole warp. A tile of K (or V) in the ring is KB boxes of 64 rows x 128
+// bytes (COLS elements), 128-byte swizzled; ok[stage] receives which keys count.
+template <int KB, int COLS, int STAGES>
+MGQA_DEV void produce_tiles(const TmaParams &tp, Pieces pieces, const CUtensorMap *tm_k, const CUtensorMap *tm_v,
+                            const CUtensorMap *tm_kn, const CUtensorMap *tm_vn, unsigned char *ring, uint2 *ok_words,
+                            uint64_t *full, uint64_t *empty) {
+  constexpr int BOXB = kTile * 128, TILEB = KB * BOXB;
+  const CacheAttnParams &p = tp.a;
+  const int lane = threadIdx.x & 31;
+  const int br = tp.box_rows, nbox = kTile / br;
+  bool ok = true;
+  int it = 0;  // tiles issued
+  Piece pc;
+  while (ok && pieces.next(p, pc)) {
+    const RowPlan &rp = pc.rp;
+    // lane i: box i of the tile; the page of the next tile's box is looked up a tile ahead
+    auto look_up = [&](int t) {
+      int kind;
+      const int j0 = first_key(rp, t, 6, kind) + lane * br;
+      const bool some = !kind && lane < nbox && j0 < rp.n && ((rp.lo < rp.n && j0 + br > rp.lo) || j0 < rp.s_end);
+      return some ? page_of(p, pc.b, j0) : -2;  // -1: a page that is not there
+    };
+    int page = look_up(pc.t0);
+    for (int t = pc.t0; t < pc.t1 && ok; ++t, ++it) {
+      const int next = t + 1 < pc.t1 ? look_up(t + 1) : -2;
+      int kind;
+      const int k0 = first_key(rp, t, 6, kind);
+      uint64_t bits = 0ull;
+      if (kind) {
+        bits = lane == 0 ? low64(rp.live - k0) : 0ull;
+      } else if (page >= 0) {
+        const int j0 = k0 + lane * br;
+        bits = (low64(rp.n - j0) & (~low64(rp.lo - j0) | low64(rp.s_end - j0)) & low64(br)) << (lane * br);
+      } else if (page == -1) {
+        report_error(p.err, MGQA_ERR_INVALID_ARG);
+      }
+      const uint32_t lo = __reduce_or_sync(0xffffffffu, (uint32_t)bits);
+      const uint32_t hi = __reduce_or_sync(0xffffffffu, (uint32_t)(bits >> 32));
+      const bool take = bits != 0ull;
+      const int boxes = __popc(__ballot_sync(0xffffffffu, take));
+      const int st = it % STAGES, use = it / STAGES;
+      if (use > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(empty + st, (use - 1) & 1, p.err));
+        if (!ok) break;
+      }
+      if (lane == 0) {
+        ok_words[st] = make_uint2(lo, hi);
+        mbar_arrive_expect_tx(full + st, (uint32_t)(boxes * (kind ? kTile : br) * 128 * KB * 2));
+      }
+      __syncwarp();
+      if (take) {
+        unsigned char *kd = ring + st * 2 * TILEB + (kind ? 0 : lane * br * 128), *vd = kd + TILEB;
+        const CUtensorMap *mk = kind ? tm_kn : tm_k, *mv = kind ? tm_vn : tm_v;
+        const int slot = kind ? k0 : slot_in_page(p, k0 + lane * br), z = kind ? pc.b : page;
+#pragma unroll
+        for (int c = 0; c < KB; ++c) {
+          tc::tma_load_4d(kd + c * BOXB, mk, c * COLS, slot, pc.g, z, full + st);
+          tc::tma_load_4d(vd + c * BOXB, mv, c * COLS, slot, pc.g, z, full + st);
+        }
+      }
+      page = next;
+    }
+  }
+  // no copy may be in flight when the CTA exits, even if the consumers gave up
+  // (only this warp arms the full barriers: these are the newest phases)
+  __syncwarp();
+  for (int i = max(0, it - STAGES); i < it; ++i) mbar_wait(full + i % STAGES, (i / STAGES) & 1, p.err);
+}
+
+// The cluster's CTAs join their shares of a unit, each a part of its rows: every
+// CTA has its (m, l) in `ml` and its unnormalised rows in `res` (row pitch OP
+// floats, 16-byte aligned) of shared memory. The whole block takes part; threads
+// [0, WORKERS) do the work.
+template <typename T, int D, int ROWS, int OP, int WORKERS>
+MGQA_DEV void join_cluster(const CacheAttnParams &p, const Pieces &pieces, const float2 *ml_s, const float *res) {
+  __syncwarp();
+  cluster_sync();
+  const Piece &pc = pieces.only;
+  if (threadIdx.x < WORKERS) {
+    const PieceOut po{true, 0, pc.b, pc.g, pc.rb * ROWS, min(ROWS, p.R - pc.rb * ROWS)};
+    const uint32_t ml0 = smem_u32(ml_s), res0 = smem_u32(res);
+    for (int u = pieces.rank * WORKERS + threadIdx.x; u < po.rows * (D / 4); u += pieces.S * WORKERS) {
+      const int r = u / (D / 4), d = (u % (D / 4)) * 4;
+      float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+      float2 ml[16];
+      float4 v[16];
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {  // every load in flight at once
+        ml[x] = make_float2(-INFINITY, 0.f);
+        v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (x < pieces.S) {
+          ml[x] = ld_cluster_f32x2(cluster_map_u32(ml0 + r * 8, x));
+          v[x] = ld_cluster_f32x4(cluster_map_u32(res0 + (r * OP + d) * 4, x));
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 16; ++x) m = fmaxf(m, ml[x].x);
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        if (ml[x].x == -INFINITY) continue;
+        const float w = exp2f(ml[x].x - m);
+        l = fmaf(ml[x].y, w, l);
+        acc[0] = fmaf(v[x].x, w, acc[0]);
+        acc[1] = fmaf(v[x].y, w, acc[1]);
+        acc[2] = fmaf(v[x].z, w, acc[2]);
+        acc[3] = fmaf(v[x].w, w, acc[3]);
+      }
+      RowOut<T, D, ROWS>(p, po, r, m, l, d == 0).put(d, acc);
+    }
+  }
+  __syncwarp();
+  cluster_sync();  // no CTA exits while its shared memory is read
+}
+
+// Clusters for short calls: whether the reads take at most ~10 us at 6.8 TB/s,
+// whatever the lengths are, and how many CTAs a unit gets then: no more CTAs
+// than SMs in all (a second one on an SM keeps whole clusters waiting).
+inline bool short_call(const CacheAttnParams &p, int row_bytes) {
+  CacheAttnParams q = p;
+  q.tile_shift = 6;
+  return (int64_t)p.B * p.Hkv * most_tiles(q) * (2 * kTile * row_bytes) <= (int64_t)64 << 20;
+}
+inline int cluster_size(const CacheAttnParams &p, int row_bytes, int sms) {
+  if (!short_call(p, row_bytes)) return 0;
+  const int64_t units = (int64_t)p.B * p.Hkv * p.RB, tiles = most_tiles(p);
+  int s = 1;
+  while (s < 16 && s < tiles && units * s * 2 <= sms) s *= 2;
+  return s;
+}
+
+}  // namespace mgqa

@@ -74,6 +74,9 @@ mgqa_status launch_cache_merge(const CacheAttnParams &p, mgqa_dtype dt, int D, i
 bool cache_attn_tma_takes(const CacheAttnParams &p, mgqa_dtype dt, int D);
 mgqa_status launch_cache_attn_tma(const CacheAttnParams &p, mgqa_dtype dt, int D, const CacheAttnLaunch &how,
                                   cudaStream_t s);
+// fp32 on the CUDA cores (the same caches).
+bool cache_attn_f32_takes(const CacheAttnParams &p, mgqa_dtype dt);
+mgqa_status launch_cache_attn_f32(const CacheAttnParams &p, int D, const CacheAttnLaunch &how, cudaStream_t s);
 // Tensor-memory kernel (the same caches, more rows).
 bool cache_attn_tc_takes(const CacheAttnParams &p, mgqa_dtype dt);
 mgqa_status launch_cache_attn_tc(const CacheAttnParams &p, mgqa_dtype dt, int D, const CacheAttnLaunch &how,

@@ -170,8 +170,9 @@ bool make_tma_map(CUtensorMap *m, mgqa_dtype dt, const void *base, int rank, con
                   const int64_t *strides, const int *box, bool swizzle128);
 
 // Prefill on the CUDA cores (fp32 I/O).
-mgqa_status launch_prefill_simt(const mgqa_args &a, cudaStream_t s,
-                                const WindowRule &win = WindowRule());
+mgqa_status launch_prefill_simt(const mgqa_args &a, cudaStream_t s);
+// The same under a sliding window.
+mgqa_status launch_prefill_window_f32(const mgqa_args &a, const WindowRule &win, cudaStream_t s);
 
 // Prefill on the tensor cores (bf16 / fp16 I/O): TMA + tcgen05 + TMEM.
 mgqa_status launch_prefill_tc(const mgqa_args &a, cudaStream_t s,

@@ -105,28 +105,15 @@ prefill_simt_kernel(const __grid_constant__ SimtParams p) {
       mw[w] = row_ok ? mask_word(p.mask, b, ic, j0 + 32 * w, p.Lk, p.Lq, kvl, segq) : 0u;
   };
 
-  // tiles that a window leaves to these rows: the sinks' [0, w_sink) and
-  // [w_lo, w_hi); without a window all of them
-  const int ntile = (p.Lk + kKeys - 1) / kKeys;
-  int w_sink = 0, w_lo = 0, w_hi = ntile;
-  if (p.mask.window) {
-    const int first = qt * kRows + p.mask.coff, last = first + min(kRows, p.Lq - qt * kRows) - 1;
-    w_sink = min(ntile, (p.mask.sinks + kKeys - 1) / kKeys);
-    w_lo = max(w_sink, max(0, first - p.mask.window + 1) / kKeys);
-    w_hi = min(ntile, (max(0, p.mask.causal ? last + 1 : last + p.mask.window) + kKeys - 1) / kKeys);
-  }
-  const int n_cand = w_sink + max(0, w_hi - w_lo);
-  auto tile_key = [&](int c) { return (c < w_sink ? c : w_lo + c - w_sink) * kKeys; };
-
   uint32_t mw[kKeys / 32] = {0u, 0u};
-  if (n_cand > 0) {
-    fetch(tile_key(0), 0);
-    mask_words(tile_key(0), mw);
+  if (p.Lk > 0) {
+    fetch(0, 0);
+    mask_words(0, mw);
   }
-  for (int c = 0, bf = 0; c < n_cand; ++c, bf ^= 1) {
+  for (int j0 = 0, bf = 0; j0 < p.Lk; j0 += kKeys, bf ^= 1) {
+    const int jn = j0 + kKeys;
     uint32_t mwn[kKeys / 32] = {0u, 0u};
-    if (c + 1 < n_cand) {
-      const int jn = tile_key(c + 1);
+    if (jn < p.Lk) {
       fetch(jn, bf ^ 1);  // that buffer's last reader passed the barrier ending the previous tile
       mask_words(jn, mwn);
       cp_async_wait<1>();
@@ -213,7 +200,7 @@ mgqa_status launch_t(const SimtParams &p, cudaStream_t s) {
 
 }  // namespace
 
-mgqa_status launch_prefill_simt(const mgqa_args &a, cudaStream_t s, const WindowRule &win) {
+mgqa_status launch_prefill_simt(const mgqa_args &a, cudaStream_t s) {
   SimtParams p{};
   p.q = a.q; p.k = a.k; p.v = a.v; p.out = a.out;
   for (int t = 0; t < 3; ++t) {
@@ -221,7 +208,7 @@ mgqa_status launch_prefill_simt(const mgqa_args &a, cudaStream_t s, const Window
     p.vs[t] = a.v_stride[t]; p.os[t] = a.o_stride[t];
   }
   p.mask = MaskView{a.mask_bits, a.mask_stride_b, a.mask_stride_q, a.kv_len, a.seg_q, a.seg_k,
-                    a.causal != 0, a.Lk - a.Lq, win.window, win.sinks};
+                    a.causal != 0, a.Lk - a.Lq};
   p.scale_log2 = a.scale * kLog2e;
   p.lse = a.lse; p.err = a.dev_error;
   p.B = a.B; p.Hq = a.Hq; p.Hkv = a.Hkv; p.Lq = a.Lq; p.Lk = a.Lk; p.n_rep = a.Hq / a.Hkv;
