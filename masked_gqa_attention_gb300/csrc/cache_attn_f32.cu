@@ -1,7 +1,7 @@
 // The fp32 cache attention over slots, or pages of a multiple of 8 slots: the
 // formulas of cache_attn.cu on the CUDA cores (single-precision accuracy rules
 // the tensor cores out), with the tiles, the two ways to cut the work and the
-// producer warp of cache_attn_tma.cu.
+// producer warps of cache_attn_tma.cu.
 //
 // A key is 8 D bytes and 4 R D operations: up to R = 8 or so the reads bound it,
 // beyond that the fp32 rate. Two forms:
@@ -20,7 +20,7 @@ namespace mgqa {
 namespace {
 
 constexpr int kConsumers = 256;
-constexpr int kThreads = kConsumers + 32;
+constexpr int kThreads = kConsumers + 64;
 
 template <int D>
 struct Ring {
@@ -140,7 +140,7 @@ cache_attn_f32_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(sm.full + s, 1);
+      mbar_init(sm.full + s, 2);
       mbar_init(sm.empty + s, kConsumers / 32);
     }
     fence_mbarrier_init();
@@ -150,8 +150,10 @@ cache_attn_f32_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid
   allow_dependents();
   Pieces pieces{};
   pieces.start<kThreads>(tp, sm.scratch);
-  if (warp == kConsumers / 32) {
-    produce_tiles<Ring<D>::KB, 32, STAGES>(tp, pieces, &tm_k, &tm_v, &tm_kn, &tm_vn, ring, sm.ok, sm.full, sm.empty);
+  if (warp >= kConsumers / 32) {
+    const int of_v = warp - kConsumers / 32;
+    produce_tiles<Ring<D>::KB, 32, STAGES>(tp, pieces, of_v, of_v ? &tm_v : &tm_k, of_v ? &tm_vn : &tm_kn, ring,
+                                           sm.ok, sm.full, sm.empty);
   } else {
     if (pieces.idle() && tid < ROWS) sm.ml[tid] = make_float2(-INFINITY, 0.f);
     bool ok = true;
@@ -319,7 +321,7 @@ cache_attn_f32_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __gri
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(sm.full + s, 1);
+      mbar_init(sm.full + s, 2);
       mbar_init(sm.empty + s, kConsumers / 32);
     }
     fence_mbarrier_init();
@@ -329,8 +331,10 @@ cache_attn_f32_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __gri
   allow_dependents();
   Pieces pieces{};
   pieces.start<kThreads>(tp, sm.scratch);
-  if (warp == kConsumers / 32) {
-    produce_tiles<Ring<D>::KB, 32, STAGES>(tp, pieces, &tm_k, &tm_v, &tm_kn, &tm_vn, ring, sm.ok, sm.full, sm.empty);
+  if (warp >= kConsumers / 32) {
+    const int of_v = warp - kConsumers / 32;
+    produce_tiles<Ring<D>::KB, 32, STAGES>(tp, pieces, of_v, of_v ? &tm_v : &tm_k, of_v ? &tm_vn : &tm_kn, ring,
+                                           sm.ok, sm.full, sm.empty);
   } else {
     if (pieces.idle() && tid < ROWS) sm.ml[tid] = make_float2(-INFINITY, 0.f);
     const int tx = tid & 15, ty = tid >> 4;

@@ -8,9 +8,9 @@
 // memory. A CTA holds NT blocks of up to 128 query rows (row = draft * group +
 // head, so a tile of keys serves every head of the group) and walks
 // its run of the flat tile list (cache_sched.cuh), one CTA an SM:
-//   warp 0      : follows the page table, K and V boxes of 128-key tiles by TMA
+//   warps 0, 3  : follow the page table, K and V boxes of 128-key tiles by TMA
 //   warp 1      : tensor memory, the MMA loop (one elected lane issues)
-//   warps 2, 3  : the query rows of the next piece, as soon as the last S of
+//   warp 2      : the query rows of the next piece, as soon as the last S of
 //                 the current one is done, and its description for the others
 //   warps 4..   : one softmax warpgroup per 128 rows (thread = row)
 // Per tile n and row block t: S_t = Q_t K_n^T; softmax (running maximum, lazy
@@ -231,11 +231,17 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     named_sync(1, L::threads);
   };
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
     if constexpr (NT == 2) tc::regs_dec<104>();
-    // ---------------- producer ----------------
-    const int br = tp.box_rows, nbox = BN / br;
-    int it = 0, v_issued = 0;  // tiles whose K (V) has been issued
+    // ---------------- producers: K (warp 0) and V (warp 3) ----------------
+    // (a box is issued by one lane at a time, ~80 cycles each: with pages of 8
+    // slots the boxes of a whole tile took one warp longer than the reads)
+    const bool of_v = warp == 3;
+    const int br = tp.box_rows, nbox = BN / br, stages = of_v ? VS : STAGES;
+    uint64_t *full = of_v ? sm.vfull : sm.kfull, *empty = of_v ? sm.vempty : sm.kempty;
+    unsigned char *buf = smem + (of_v ? L::v_off : L::k_off);
+    const CUtensorMap *tm = of_v ? &tm_v : &tm_k, *tm_new = of_v ? &tm_vn : &tm_kn;
+    int it = 0;  // tiles issued
     while (ok && walk.next(p, pc)) {
       const RowPlan &rp = pc.rp;
       auto look_up = [&](int t) {
@@ -245,7 +251,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         return some ? page_of(p, pc.b, j0) : -2;  // -1: a page that is not there
       };
       int page = look_up(pc.t0);
-      for (int t = pc.t0; t < pc.t1; ++t) {
+      for (int t = pc.t0; t < pc.t1; ++t, ++it) {
         const int next = t + 1 < pc.t1 ? look_up(t + 1) : -2;
         int kind;
         const int k0 = first_key(rp, t, kShift, kind);
@@ -269,45 +275,34 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           report_error(p.err, MGQA_ERR_INVALID_ARG);
         }
         uint4 words;
-        words.x = __reduce_or_sync(0xffffffffu, mine[0]);
-        words.y = __reduce_or_sync(0xffffffffu, mine[1]);
-        words.z = __reduce_or_sync(0xffffffffu, mine[2]);
-        words.w = __reduce_or_sync(0xffffffffu, mine[3]);
+        if (!of_v) {
+          words.x = __reduce_or_sync(0xffffffffu, mine[0]);
+          words.y = __reduce_or_sync(0xffffffffu, mine[1]);
+          words.z = __reduce_or_sync(0xffffffffu, mine[2]);
+          words.w = __reduce_or_sync(0xffffffffu, mine[3]);
+        }
         const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, take)) * (kind ? BN : br) * 128 * KB);
-        const int st = it % STAGES, use = it / STAGES;
+        const int st = it % stages, use = it / stages;
         const int slot = kind ? k0 : slot_in_page(p, j0), z = kind ? pc.b : page;
-        const int row_off = kind ? 0 : lane * br * 128;
-        if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(sm.kempty + st, (use - 1) & 1, p.err));
+        unsigned char *dst = buf + st * KB * BOX + (kind ? 0 : lane * br * 128);
+        if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(empty + st, (use - 1) & 1, p.err));
         if (!ok) break;
         if (lane == 0) {
-          sm.ok[it % kOkRing] = words;
-          mbar_arrive_expect_tx(sm.kfull + st, bytes);
+          if (!of_v) sm.ok[it % kOkRing] = words;
+          mbar_arrive_expect_tx(full + st, bytes);
         }
         __syncwarp();
         if (take)
 #pragma unroll
           for (int c = 0; c < KB; ++c)
-            tc::tma_load_4d(smem + L::k_off + (st * KB + c) * BOX + row_off, kind ? &tm_kn : &tm_k, c * 64, slot, pc.g,
-                            z, sm.kfull + st);
-        const int sv = it % VS, use_v = it / VS;
-        ++it;
-        if (use_v > 0) ok = __all_sync(0xffffffffu, mbar_wait(sm.vempty + sv, (use_v - 1) & 1, p.err));
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(sm.vfull + sv, bytes);
-        __syncwarp();
-        if (take)
-#pragma unroll
-          for (int c = 0; c < KB; ++c)
-            tc::tma_load_4d(smem + L::v_off + (sv * KB + c) * BOX + row_off, kind ? &tm_vn : &tm_v, c * 64, slot, pc.g,
-                            z, sm.vfull + sv);
-        ++v_issued;
+            tc::tma_load_4d(dst + c * BOX, kind ? tm_new : tm, c * 64, slot, pc.g, z, full + st);
         page = next;
       }
     }
-    // no copy may be in flight when the CTA exits (only this warp arms the full
+    // no copy may be in flight when the CTA exits (only this warp arms these full
     // barriers: the last armed phase of each is the newest it can reach)
-    for (int i = max(0, it - STAGES); i < it; ++i) mbar_wait(sm.kfull + i % STAGES, (i / STAGES) & 1, p.err);
-    for (int i = max(0, v_issued - VS); i < v_issued; ++i) mbar_wait(sm.vfull + i % VS, (i / VS) & 1, p.err);
+    __syncwarp();
+    for (int i = max(0, it - stages); i < it; ++i) mbar_wait(full + i % stages, (i / stages) & 1, p.err);
     __syncwarp();
     role_end();
   } else if (warp == 1) {
@@ -459,10 +454,10 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     role_end();
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, L::tmem_cols);
-  } else if (warp < 4) {
+  } else if (warp == 2) {
     if constexpr (NT == 2) tc::regs_dec<104>();
-    // ---------------- query rows and piece descriptions (warp 2) ----------------
-    bool more = warp == 2;
+    // ---------------- query rows and piece descriptions ----------------
+    bool more = true;
     for (int piece = 0; more; ++piece) {
       more = walk.next(p, pc);
       // (the slot is free: its piece's query rows were overwritten long ago)

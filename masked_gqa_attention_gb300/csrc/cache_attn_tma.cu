@@ -2,7 +2,7 @@
 // up to 64 query rows per KV head (one token's heads, or a small tree): the
 // formulas of cache_attn.cu with the keys and values fetched as TMA boxes.
 //
-// Reads bound it. A producer warp follows the page table and issues each
+// Reads bound it. Two producer warps follow the page table and issue each
 // 64-key tile as boxes that never cross a page (gcd(page_size, 64) rows, 64
 // columns, 128-byte swizzle) into a ring of 96 KB; two CTAs an SM keep up to
 // 192 KB in flight. Four consumer warps run the products on mma.sync with no
@@ -28,7 +28,7 @@ namespace mgqa {
 namespace {
 
 constexpr int kConsumers = 128;
-constexpr int kThreads = kConsumers + 32;
+constexpr int kThreads = kConsumers + 64;
 constexpr int kMaxT = 64;  // R <= 64
 
 template <int D, int WM>
@@ -75,7 +75,7 @@ cache_attn_tma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
 
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(sm.full + s, 1);
+      mbar_init(sm.full + s, 2);
       mbar_init(sm.empty + s, 4);
     }
     fence_mbarrier_init();
@@ -94,8 +94,10 @@ cache_attn_tma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
   pieces.start<kThreads>(tp, sm.scratch);  // (its barrier: the mbarriers are initialised)
   const int S = pieces.S;
 
-  if (warp == 4) {
-    produce_tiles<C::KB, 64, STAGES>(tp, pieces, &tm_k, &tm_v, &tm_kn, &tm_vn, ring, sm.ok, sm.full, sm.empty);
+  if (warp >= 4) {
+    const int of_v = warp - 4;
+    produce_tiles<C::KB, 64, STAGES>(tp, pieces, of_v, of_v ? &tm_v : &tm_k, of_v ? &tm_vn : &tm_kn, ring, sm.ok,
+                                     sm.full, sm.empty);
   } else {
     // ---------------- consumers ----------------
     const int wm = warp / WK, wk = warp % WK;

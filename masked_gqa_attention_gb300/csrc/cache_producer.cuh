@@ -1,6 +1,8 @@
-// The producer warp of the cache attention kernels that fetch 64-key tiles by
-// TMA: it follows the page table and issues every tile as boxes that never cross
-// a page into a ring of stages.
+// The producer warps (one for K, one for V) of the cache attention kernels that
+// fetch 64-key tiles by TMA: they follow the page table and issue every tile as
+// boxes that never cross a page into a ring of stages. (A box is issued by one
+// lane at a time, ~80 cycles each: with pages of 8 slots one warp for both was
+// slower than the reads.)
 #pragma once
 
 #include "cache_sched.cuh"
@@ -54,12 +56,13 @@ struct Pieces {
   MGQA_DEV bool idle() const { return S && only.t0 >= only.t1; }  // a cluster's CTA without a share
 };
 
-// A whole warp. A tile of K (or V) in the ring is KB boxes of 64 rows x 128
-// bytes (COLS elements), 128-byte swizzled; ok[stage] receives which keys count.
+// A whole warp, for K (of_v 0) or V. A tile of either in the ring is KB boxes of
+// 64 rows x 128 bytes (COLS elements), 128-byte swizzled. Both warps arrive on
+// full[stage] (count 2); K's also writes which keys count to ok_words[stage].
 template <int KB, int COLS, int STAGES>
-MGQA_DEV void produce_tiles(const TmaParams &tp, Pieces pieces, const CUtensorMap *tm_k, const CUtensorMap *tm_v,
-                            const CUtensorMap *tm_kn, const CUtensorMap *tm_vn, unsigned char *ring, uint2 *ok_words,
-                            uint64_t *full, uint64_t *empty) {
+MGQA_DEV void produce_tiles(const TmaParams &tp, Pieces pieces, int of_v, const CUtensorMap *tm,
+                            const CUtensorMap *tm_new, unsigned char *ring, uint2 *ok_words, uint64_t *full,
+                            uint64_t *empty) {
   constexpr int BOXB = kTile * 128, TILEB = KB * BOXB;
   const CacheAttnParams &p = tp.a;
   const int lane = threadIdx.x & 31;
@@ -90,8 +93,11 @@ MGQA_DEV void produce_tiles(const TmaParams &tp, Pieces pieces, const CUtensorMa
       } else if (page == -1) {
         report_error(p.err, MGQA_ERR_INVALID_ARG);
       }
-      const uint32_t lo = __reduce_or_sync(0xffffffffu, (uint32_t)bits);
-      const uint32_t hi = __reduce_or_sync(0xffffffffu, (uint32_t)(bits >> 32));
+      uint32_t lo = 0u, hi = 0u;
+      if (!of_v) {
+        lo = __reduce_or_sync(0xffffffffu, (uint32_t)bits);
+        hi = __reduce_or_sync(0xffffffffu, (uint32_t)(bits >> 32));
+      }
       const bool take = bits != 0ull;
       const int boxes = __popc(__ballot_sync(0xffffffffu, take));
       const int st = it % STAGES, use = it / STAGES;
@@ -100,25 +106,22 @@ MGQA_DEV void produce_tiles(const TmaParams &tp, Pieces pieces, const CUtensorMa
         if (!ok) break;
       }
       if (lane == 0) {
-        ok_words[st] = make_uint2(lo, hi);
-        mbar_arrive_expect_tx(full + st, (uint32_t)(boxes * (kind ? kTile : br) * 128 * KB * 2));
+        if (!of_v) ok_words[st] = make_uint2(lo, hi);
+        mbar_arrive_expect_tx(full + st, (uint32_t)(boxes * (kind ? kTile : br) * 128 * KB));
       }
       __syncwarp();
       if (take) {
-        unsigned char *kd = ring + st * 2 * TILEB + (kind ? 0 : lane * br * 128), *vd = kd + TILEB;
-        const CUtensorMap *mk = kind ? tm_kn : tm_k, *mv = kind ? tm_vn : tm_v;
+        unsigned char *dst = ring + (st * 2 + of_v) * TILEB + (kind ? 0 : lane * br * 128);
         const int slot = kind ? k0 : slot_in_page(p, k0 + lane * br), z = kind ? pc.b : page;
 #pragma unroll
-        for (int c = 0; c < KB; ++c) {
-          tc::tma_load_4d(kd + c * BOXB, mk, c * COLS, slot, pc.g, z, full + st);
-          tc::tma_load_4d(vd + c * BOXB, mv, c * COLS, slot, pc.g, z, full + st);
-        }
+        for (int c = 0; c < KB; ++c)
+          tc::tma_load_4d(dst + c * BOXB, kind ? tm_new : tm, c * COLS, slot, pc.g, z, full + st);
       }
       page = next;
     }
   }
   // no copy may be in flight when the CTA exits, even if the consumers gave up
-  // (only this warp arms the full barriers: these are the newest phases)
+  // (the two producers alone arm the full barriers: these are the newest phases)
   __syncwarp();
   for (int i = max(0, it - STAGES); i < it; ++i) mbar_wait(full + i % STAGES, (i / STAGES) & 1, p.err);
 }

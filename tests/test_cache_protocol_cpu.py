@@ -61,17 +61,13 @@ class Model:
         while not self.b[name].passes(phase):
             yield
 
-    def producer(self):
-        it = 0
-        for _, nk in enumerate(self.pieces):
-            for _ in range(nk):
-                for full, empty, n in (("kfull", "kempty", self.KS), ("vfull", "vempty", self.VS)):
-                    st, use = it % n, it // n
-                    if use:
-                        yield from self.wait((empty, st), use - 1)
-                    self.copies.append(((full, st), full[0], st, it))
-                    yield
-                it += 1
+    def producer(self, full, empty, n):
+        for it in range(sum(self.pieces)):
+            st, use = it % n, it // n
+            if use:
+                yield from self.wait((empty, st), use - 1)
+            self.copies.append(((full, st), full[0], st, it))
+            yield
 
     def loader(self):
         for k in range(len(self.pieces) + 1):
@@ -195,7 +191,8 @@ class Model:
 
     def run(self):
         self.state["q"] = {}
-        roles = {"load": self.producer(), "mma": self.mma(), "q": self.loader()}
+        roles = {"k": self.producer("kfull", "kempty", self.KS), "v": self.producer("vfull", "vempty", self.VS),
+                 "mma": self.mma(), "q": self.loader()}
         roles.update({f"soft{t}": self.softmax(t) for t in range(self.NT)})
         speed = {r: self.rng.choice([0.05, 0.3, 1.0]) for r in [*roles, "async"]}
         idle = 0
