@@ -35,8 +35,8 @@
 namespace mgqa {
 namespace {
 
-constexpr int BM = 128, BN = 128, kShift = 7;
-constexpr int BOX = BN * 128;  // bytes of 128 rows x 64 columns, 128-byte swizzled
+constexpr int BM = 128;
+constexpr int QBOX = BM * 128;  // bytes of 128 query rows x 64 columns, 128-byte swizzled
 constexpr int kPieceRing = 4;  // a piece's slot is taken again after the S of the third piece behind it
 constexpr int kOkRing = 8;     // tiles whose key masks are kept: the producer is at most 4 ahead of a softmax
 
@@ -48,55 +48,62 @@ struct TcCacheParams {
 
 template <int D, int NT>
 struct Lay {
-  static constexpr int STAGES = D == 128 ? 2 : 4;                // K tiles
-  static constexpr int VSTAGES = D == 128 && NT == 1 ? 3 : STAGES;  // V tiles: held until P V, and there is room
+  static constexpr int SHIFT = NT == 1 ? 6 : 7, BN = 1 << SHIFT;  // keys of a tile
+  static constexpr int CTAS = NT == 1 ? 2 : 1;                    // of an SM
+  static constexpr int MAXT = NT == 1 ? BM : kMaxDrafts;          // drafts (one block: at most its rows)
+  // registers: what the first warpgroup gives away goes to the softmax ones
+  // (80 + 176 = 2 x 128, 104 + 2 x 200 = 3 x 168 a scheduler at launch)
+  static constexpr int kDec = NT == 1 ? 80 : 104, kInc = NT == 1 ? 176 : 200;
+  static constexpr int STAGES = D == 128 ? 2 : 4;
   static constexpr int KB = D / 64;
+  static constexpr int BOX = BN * 128;  // bytes of a tile's 64 columns
   static constexpr int q_off = 0;
-  static constexpr int k_off = q_off + NT * KB * BOX;
+  static constexpr int k_off = q_off + NT * KB * QBOX;
   static constexpr int v_off = k_off + STAGES * KB * BOX;
-  static constexpr int misc_off = v_off + VSTAGES * KB * BOX;
+  static constexpr int misc_off = v_off + STAGES * KB * BOX;
   static constexpr int threads = 128 * (1 + NT);
   static constexpr int ROWS = BM * NT;
   static constexpr int SB = NT == 1 ? 2 : 1;  // score buffers of a row block
   static constexpr uint32_t tmem_used = NT * (SB * BN + D);
   static constexpr uint32_t tmem_cols = tmem_used <= 256 ? 256 : 512;
   struct Misc {
-    Drafts<kMaxDrafts> drafts;
+    Drafts<MAXT> drafts;
     LocateScratch<threads> scratch;
     Piece pieces[kPieceRing];      // rp.nt < 0: no more
     uint64_t pready[kPieceRing], qfree;
     uint4 ok[kOkRing];  // which keys of a tile count
-    uint64_t kfull[STAGES], vfull[VSTAGES], kempty[STAGES], vempty[VSTAGES];
+    uint64_t kfull[STAGES], vfull[STAGES], kempty[STAGES], vempty[STAGES];
     uint64_t sfull[NT * SB], pfull[NT * SB], odone[NT], ofree[NT], qfull[NT], drain;
     uint32_t tmem;
     int maxdepth;
   };
   static constexpr int smem = misc_off + (int)sizeof(Misc) + 1024;
-  static_assert(smem <= 227 * 1024, "shared memory");
+  static_assert(CTAS * (smem + 1024) <= 228 * 1024 && CTAS * tmem_cols <= 512, "an SM holds the CTAs");
 };
 
 MGQA_DEV uint32_t all_of(const uint4 &w) { return w.x & w.y & w.z & w.w; }
 MGQA_DEV uint32_t word_of(const uint4 &w, int i) { return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w; }
 
-// One 128-key tile of one softmax row (thread = row) in tensor memory: see the
+// One tile of one softmax row (thread = row) in tensor memory: see the
 // prefill kernel's softmax_tile; the scale is not negative here.
 // `pv_done`: phase `pv_parity` of that barrier tells that O holds every tile
 // before this one (null: S of this tile was issued behind them).
-template <typename T, int D, bool PARTIAL>
+template <typename T, int D, int BN, bool PARTIAL>
 MGQA_DEV void softmax_row(uint32_t t_s, uint32_t t_o, const uint32_t (&mw)[4], float sl2, float &m_used, float &l,
                           uint64_t *pv_done, uint32_t pv_parity, int32_t *err) {
   uint32_t sr[BN];
   float mr;
   if constexpr (!PARTIAL) {
-    float red[4];
+    float red[BN / 32];
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int c = 0; c < BN / 32; ++c)
       tc::tmem_ld32_red<true>(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]), red[c]);
     tc::tmem_wait_ld();
-    mr = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    mr = fmaxf(red[0], red[1]);
+    if constexpr (BN == 128) mr = fmaxf(mr, fmaxf(red[2], red[3]));
   } else {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) tc::tmem_ld32(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+    for (int c = 0; c < BN / 32; ++c) tc::tmem_ld32(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
     tc::tmem_wait_ld();
     float mx[8];
 #pragma unroll
@@ -145,7 +152,7 @@ MGQA_DEV void softmax_row(uint32_t t_s, uint32_t t_o, const uint32_t (&mw)[4], f
 #pragma unroll
   for (int k = 0; k < 4; ++k) acc[k] = tc::pk2(0.f, 0.f);
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < BN / 32; ++c) {
     uint32_t pk[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
@@ -173,12 +180,12 @@ MGQA_DEV void softmax_row(uint32_t t_s, uint32_t t_o, const uint32_t (&mw)[4], f
 }
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(128 * (1 + NT), 1)
+__global__ void __launch_bounds__(128 * (1 + NT), NT == 1 ? 2 : 1)
 cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_vn,
                      const __grid_constant__ TcCacheParams tp) {
   using L = Lay<D, NT>;
-  constexpr int KB = L::KB, STAGES = L::STAGES, VS = L::VSTAGES, ROWS = L::ROWS;
+  constexpr int KB = L::KB, STAGES = L::STAGES, ROWS = L::ROWS, BN = L::BN, BOX = L::BOX, kShift = L::SHIFT;
   const CacheAttnParams &p = tp.a;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -188,10 +195,8 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(sm.kfull + s, 1);
-      mbar_init(sm.kempty + s, 1);
-    }
-    for (int s = 0; s < VS; ++s) {
       mbar_init(sm.vfull + s, 1);
+      mbar_init(sm.kempty + s, 1);
       mbar_init(sm.vempty + s, 1);
     }
     for (int t = 0; t < NT * L::SB; ++t) {
@@ -232,12 +237,12 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   };
 
   if (warp == 0 || warp == 3) {
-    if constexpr (NT == 2) tc::regs_dec<104>();
+    tc::regs_dec<L::kDec>();
     // ---------------- producers: K (warp 0) and V (warp 3) ----------------
     // (a box is issued by one lane at a time, ~80 cycles each: with pages of 8
     // slots the boxes of a whole tile took one warp longer than the reads)
     const bool of_v = warp == 3;
-    const int br = tp.box_rows, nbox = BN / br, stages = of_v ? VS : STAGES;
+    const int br = tp.box_rows, nbox = BN / br;
     uint64_t *full = of_v ? sm.vfull : sm.kfull, *empty = of_v ? sm.vempty : sm.kempty;
     unsigned char *buf = smem + (of_v ? L::v_off : L::k_off);
     const CUtensorMap *tm = of_v ? &tm_v : &tm_k, *tm_new = of_v ? &tm_vn : &tm_kn;
@@ -256,17 +261,17 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         int kind;
         const int k0 = first_key(rp, t, kShift, kind);
         const int j0 = k0 + lane * br;
-        uint32_t mine[4] = {0u, 0u, 0u, 0u};
+        uint32_t mine[4] = {0u, 0u, 0u, 0u};  // (a tile of 64 keys has two words)
         bool take = false;
         if (kind) {
           take = lane == 0 && rp.live > k0;
           if (lane == 0)
 #pragma unroll
-            for (int w = 0; w < 4; ++w) mine[w] = low_mask(rp.live - k0 - 32 * w);
+            for (int w = 0; w < BN / 32; ++w) mine[w] = low_mask(rp.live - k0 - 32 * w);
         } else if (page >= 0) {
           take = true;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
+          for (int w = 0; w < BN / 32; ++w) {
             const int j = k0 + 32 * w;
             mine[w] = low_mask(rp.n - j) & (~low_mask(rp.lo - j) | low_mask(rp.s_end - j)) & low_mask(j0 + br - j) &
                       ~low_mask(j0 - j);
@@ -278,11 +283,11 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (!of_v) {
           words.x = __reduce_or_sync(0xffffffffu, mine[0]);
           words.y = __reduce_or_sync(0xffffffffu, mine[1]);
-          words.z = __reduce_or_sync(0xffffffffu, mine[2]);
-          words.w = __reduce_or_sync(0xffffffffu, mine[3]);
+          words.z = BN == 64 ? 0xffffffffu : __reduce_or_sync(0xffffffffu, mine[2]);
+          words.w = BN == 64 ? 0xffffffffu : __reduce_or_sync(0xffffffffu, mine[3]);
         }
         const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, take)) * (kind ? BN : br) * 128 * KB);
-        const int st = it % stages, use = it / stages;
+        const int st = it % STAGES, use = it / STAGES;
         const int slot = kind ? k0 : slot_in_page(p, j0), z = kind ? pc.b : page;
         unsigned char *dst = buf + st * KB * BOX + (kind ? 0 : lane * br * 128);
         if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(empty + st, (use - 1) & 1, p.err));
@@ -302,11 +307,11 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     // no copy may be in flight when the CTA exits (only this warp arms these full
     // barriers: the last armed phase of each is the newest it can reach)
     __syncwarp();
-    for (int i = max(0, it - stages); i < it; ++i) mbar_wait(full + i % stages, (i / stages) & 1, p.err);
+    for (int i = max(0, it - STAGES); i < it; ++i) mbar_wait(full + i % STAGES, (i / STAGES) & 1, p.err);
     __syncwarp();
     role_end();
   } else if (warp == 1) {
-    if constexpr (NT == 2) tc::regs_dec<104>();
+    tc::regs_dec<L::kDec>();
     // ---------------- MMA issuer ----------------
     const bool leader = tc::elect_one();
     constexpr bool kBf16 = !__is_same(T, __half);
@@ -316,20 +321,21 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     const uint64_t qd0 = tc::sw128_desc(sb + L::q_off, 16, 1024);
     const uint64_t kd0 = tc::sw128_desc(sb + L::k_off, 16, 1024);
     const uint64_t vd0 = tc::sw128_desc(sb + L::v_off, BOX, 1024);
-    constexpr uint64_t kTileStep = (uint64_t)(KB * BOX) >> 4;
+    constexpr uint64_t kTileStep = (uint64_t)(KB * BOX) >> 4, kQStep = (uint64_t)(KB * QBOX) >> 4;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
       ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity, p.err));
       return ok;
     };
     // S of row block t, into score buffer sb
     auto issue_s = [&](int t, int sb, int st, int k0, int k1, bool last) {
-      const uint64_t qd = qd0 + (uint64_t)t * kTileStep, kd = kd0 + (uint64_t)st * kTileStep;
+      const uint64_t qd = qd0 + (uint64_t)t * kQStep, kd = kd0 + (uint64_t)st * kTileStep;
       if (leader) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           if (kk < k0 || kk >= k1) continue;
-          const uint64_t off = (uint64_t)((kk / 4) * BOX + (kk % 4) * 32) >> 4;
-          tc::mma_ss(tmem + (t + sb) * BN, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
+          const uint64_t qo = (uint64_t)((kk / 4) * QBOX + (kk % 4) * 32) >> 4;
+          const uint64_t ko = (uint64_t)((kk / 4) * BOX + (kk % 4) * 32) >> 4;
+          tc::mma_ss(tmem + (t + sb) * BN, qd + qo, kd + ko, id_s, kk > 0 ? 1u : 0u);
         }
         if (k1 == D / 16) {
           tc::mma_commit(sm.sfull + t + sb);
@@ -361,13 +367,12 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         tc::fence_after_sync();
         issue_s(t, it % L::SB, it % STAGES, 0, D / 16, nk == 1);
       }
-      if (!ok || !wait(sm.vfull + it % VS, (it / VS) & 1)) break;
+      if (!ok || !wait(sm.vfull + it % STAGES, (it / STAGES) & 1)) break;
       bool p0_seen = false;
       for (int n = 0; n < nk && ok; ++n) {
         const int at = it + n, st1 = (at + 1) % STAGES;
         const uint32_t par1 = (uint32_t)((at + 1) / STAGES) & 1u;
-        const int sv = at % VS, sv1 = (at + 1) % VS;
-        const uint32_t vpar1 = (uint32_t)((at + 1) / VS) & 1u;
+        const int sv = at % STAGES;
         const bool has_next = n + 1 < nk;
         {  // values of keys that do not count: cleared (their rows may hold anything,
            // but for those behind the drafts, which the copy fills with zeros)
@@ -377,7 +382,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             const int k0 = first_key(pc.rp, pc.t0 + n, kShift, kind);
             const int rows = kind && pc.rp.live > k0 ? p.T - k0 : BN;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
+            for (int w = 0; w < BN / 32; ++w) {
               const uint32_t clear = ~word_of(okw, w) & low_mask(rows - 32 * w);
               if (clear)  // 16-byte pieces (the swizzle permutes them within a row)
 #pragma unroll
@@ -410,7 +415,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             if (!has_next) tc::mma_commit(sm.odone);
           }
           __syncwarp();
-          if (has_next && !wait(sm.vfull + sv1, vpar1)) break;
+          if (has_next && !wait(sm.vfull + st1, par1)) break;
         } else {
           bool p1_seen = false;
           for (int t = 0; t < NT && ok; ++t) {
@@ -420,7 +425,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             issue_pv(t, 0, sv, 0, kHalfPV, n == 0);
             if (has_next) {  // K of the next tile before its first S, V before the next P.V
               if (t == 0 && !wait(sm.kfull + st1, par1)) break;
-              if (t == NT - 1 && !wait(sm.vfull + sv1, vpar1)) break;
+              if (t == NT - 1 && !wait(sm.vfull + st1, par1)) break;
               tc::fence_after_sync();
             }
             issue_pv(t, 0, sv, kHalfPV, BN / 16, n == 0);
@@ -443,8 +448,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     // the last release of every stage has landed before the CTA exits; after a
     // wait that gave up, every MMA issued completes before tensor memory is freed
     for (int i = max(0, it - STAGES); i < it && ok; ++i)
-      wait(sm.kempty + i % STAGES, (i / STAGES) & 1);
-    for (int i = max(0, it - VS); i < it && ok; ++i) wait(sm.vempty + i % VS, (i / VS) & 1);
+      wait(sm.kempty + i % STAGES, (i / STAGES) & 1) && wait(sm.vempty + i % STAGES, (i / STAGES) & 1);
     if (!ok) {
       if (leader) tc::mma_commit(&sm.drain);
       __syncwarp();
@@ -455,7 +459,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, L::tmem_cols);
   } else if (warp == 2) {
-    if constexpr (NT == 2) tc::regs_dec<104>();
+    tc::regs_dec<L::kDec>();
     // ---------------- query rows and piece descriptions ----------------
     bool more = true;
     for (int piece = 0; more; ++piece) {
@@ -475,7 +479,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             mbar_arrive_expect_tx(sm.qfull + t, (uint32_t)(KB * drafts * p.n_rep * 128));
 #pragma unroll
             for (int c = 0; c < KB; ++c)
-              tc::tma_load_5d(smem + L::q_off + (t * KB + c) * BOX, &tm_q, c * 64, 0, first + t * drafts, pc.g, pc.b,
+              tc::tma_load_5d(smem + L::q_off + (t * KB + c) * QBOX, &tm_q, c * 64, 0, first + t * drafts, pc.g, pc.b,
                               sm.qfull + t);
           }
           q_pieces = piece + 1;
@@ -489,7 +493,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     __syncwarp();
     role_end();
   } else {
-    if constexpr (NT == 2) tc::regs_inc<200>();
+    tc::regs_inc<L::kInc>();
     // ---------------- softmax warpgroup t ----------------
     const int t = (warp - 4) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;  // row of the tile
@@ -541,14 +545,14 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           const bool full = !kind && all_of(okw) == 0xffffffffu && (k0 >= lo_all || k0 + BN <= min(p.sinks, rp.s_end));
           tc::fence_after_sync();
           // (a rescale follows an earlier tile of the piece; its P V releases that tile's V stage)
-          uint64_t *pv_done = L::SB > 1 ? sm.vempty + (it - 1 + VS) % VS : nullptr;
-          const uint32_t pv_parity = (uint32_t)((it - 1) / VS) & 1u;
+          uint64_t *pv_done = L::SB > 1 ? sm.vempty + (it - 1 + STAGES) % STAGES : nullptr;
+          const uint32_t pv_parity = (uint32_t)((it - 1) / STAGES) & 1u;
           uint32_t mw[4] = {0u, 0u, 0u, 0u};
           if (full) {
-            softmax_row<T, D, false>(t_s, t_o, mw, sl2, m_used, l, pv_done, pv_parity, p.err);
+            softmax_row<T, D, BN, false>(t_s, t_o, mw, sl2, m_used, l, pv_done, pv_parity, p.err);
           } else {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
+            for (int w = 0; w < BN / 32; ++w) {
               const int j = k0 + 32 * w;
               uint32_t x = rs.ok ? word_of(okw, w) : 0u;
               if (!kind) {
@@ -563,7 +567,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
               }
               mw[w] = x;
             }
-            softmax_row<T, D, true>(t_s, t_o, mw, sl2, m_used, l, pv_done, pv_parity, p.err);
+            softmax_row<T, D, BN, true>(t_s, t_o, mw, sl2, m_used, l, pv_done, pv_parity, p.err);
           }
           tc::fence_before_sync();
         }
@@ -600,9 +604,11 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 }
 
 template <typename T, int D, int NT>
-mgqa_status launch_t(const CUtensorMap (&maps)[4], TcCacheParams tp, mgqa_dtype dt, const CacheAttnLaunch &how,
-                     cudaStream_t s) {
+mgqa_status launch_t(TcCacheParams tp, mgqa_dtype dt, const CacheAttnLaunch &how, cudaStream_t s) {
   using L = Lay<D, NT>;
+  CUtensorMap maps[4];
+  if (!cache_attn_maps(tp.a, dt, D, L::BN, maps, tp.box_rows))
+    return fail(MGQA_ERR_CUDA, "cuTensorMapEncodeTiled failed for the cache");
   auto kern = cache_attn_tc_kernel<T, D, NT>;
   static std::atomic<uint64_t> attr{0};
   const mgqa_status st = ensure_smem_attr(kern, L::smem, attr, "cache attention kernel");
@@ -611,7 +617,7 @@ mgqa_status launch_t(const CUtensorMap (&maps)[4], TcCacheParams tp, mgqa_dtype 
   tp.q_drafts = BM / p.n_rep;
   p.block_rows = NT * tp.q_drafts * p.n_rep;
   p.RB = (p.R + p.block_rows - 1) / p.block_rows;
-  p.tile_shift = kShift;
+  p.tile_shift = L::SHIFT;
   // q [B][Hkv][T][group][D]: a box is a block's drafts with the heads of one group
   CUtensorMap mq;
   const int64_t dims[5] = {D, p.n_rep, p.T, p.Hkv, p.B};
@@ -622,7 +628,7 @@ mgqa_status launch_t(const CUtensorMap (&maps)[4], TcCacheParams tp, mgqa_dtype 
   p.lead = NT == 1 ? 4 : 8;  // (3 and 6 are within 2 % on NT = 1; 3 costs 9 % with two blocks and one request)
   p.min_run = 4;
   const int64_t tiles = (int64_t)p.B * p.Hkv * p.RB * (most_tiles(p) + p.lead);
-  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(how.sms, kCacheAttnMaxCtas / 2), tiles));
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(how.sms, kCacheAttnMaxCtas / 2) * L::CTAS, tiles));
   set_partials(p, how.workspace, grid, L::ROWS, D);
   const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(L::threads), L::smem, s, mq, maps[0], maps[1], maps[2],
                                    maps[3], tp);
@@ -631,9 +637,8 @@ mgqa_status launch_t(const CUtensorMap (&maps)[4], TcCacheParams tp, mgqa_dtype 
 }
 
 template <typename T, int D>
-mgqa_status launch_d(const CUtensorMap (&maps)[4], const TcCacheParams &tp, mgqa_dtype dt, const CacheAttnLaunch &how,
-                     cudaStream_t s) {
-  return tp.a.T <= BM / tp.a.n_rep ? launch_t<T, D, 1>(maps, tp, dt, how, s) : launch_t<T, D, 2>(maps, tp, dt, how, s);
+mgqa_status launch_d(const TcCacheParams &tp, mgqa_dtype dt, const CacheAttnLaunch &how, cudaStream_t s) {
+  return tp.a.T <= BM / tp.a.n_rep ? launch_t<T, D, 1>(tp, dt, how, s) : launch_t<T, D, 2>(tp, dt, how, s);
 }
 
 }  // namespace
@@ -646,12 +651,9 @@ mgqa_status launch_cache_attn_tc(const CacheAttnParams &p, mgqa_dtype dt, int D,
                                  cudaStream_t s) {
   TcCacheParams tp{};
   tp.a = p;
-  CUtensorMap maps[4];
-  if (!cache_attn_maps(p, dt, D, BN, maps, tp.box_rows))
-    return fail(MGQA_ERR_CUDA, "cuTensorMapEncodeTiled failed for the cache");
   if (dt == MGQA_BF16)
-    return D == 64 ? launch_d<__nv_bfloat16, 64>(maps, tp, dt, how, s) : launch_d<__nv_bfloat16, 128>(maps, tp, dt, how, s);
-  return D == 64 ? launch_d<__half, 64>(maps, tp, dt, how, s) : launch_d<__half, 128>(maps, tp, dt, how, s);
+    return D == 64 ? launch_d<__nv_bfloat16, 64>(tp, dt, how, s) : launch_d<__nv_bfloat16, 128>(tp, dt, how, s);
+  return D == 64 ? launch_d<__half, 64>(tp, dt, how, s) : launch_d<__half, 128>(tp, dt, how, s);
 }
 
 }  // namespace mgqa
