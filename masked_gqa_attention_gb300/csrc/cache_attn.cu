@@ -131,13 +131,15 @@ cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
 
   grid_dependency_wait();
   allow_dependents();  // the merge kernel; lengths and tables are final from here on
-  const Located loc = locate<kThreads>(p, sm.scratch, gridDim.x, blockIdx.x, -1, blockIdx.x == 0);
+  const Located loc = locate<kThreads>(p, sm.scratch, gridDim.x, blockIdx.x, blockIdx.x == 0);
   Walker walk;
   walk.start(p, loc, blockIdx.x);
   Piece pc;
+  if (tid == 0) tell_cut(p, blockIdx.x, nullptr);
   int staged = -1;  // request whose drafts are staged
 
   while (walk.next(p, pc)) {
+    if (tid == 0) tell_cut(p, blockIdx.x, &pc);
     const RowPlan &rp = pc.rp;
     const int b = pc.b, g = pc.g, t0 = pc.t0, t1 = pc.t1;
     const PieceOut po = out_of(p, pc, blockIdx.x);
@@ -381,13 +383,15 @@ cache_attn_fp32_kernel(const __grid_constant__ CacheAttnParams p) {
 
   grid_dependency_wait();
   allow_dependents();
-  const Located loc = locate<kSimtThreads>(p, sm.scratch, gridDim.x, blockIdx.x, -1, blockIdx.x == 0);
+  const Located loc = locate<kSimtThreads>(p, sm.scratch, gridDim.x, blockIdx.x, blockIdx.x == 0);
   Walker walk;
   walk.start(p, loc, blockIdx.x);
   Piece pc;
+  if (tid == 0) tell_cut(p, blockIdx.x, nullptr);
   int staged = -1;
 
   while (walk.next(p, pc)) {
+    if (tid == 0) tell_cut(p, blockIdx.x, &pc);
     const RowPlan &rp = pc.rp;
     const int b = pc.b, g = pc.g, t0 = pc.t0, t1 = pc.t1;
     const PieceOut po = out_of(p, pc, blockIdx.x);
@@ -553,47 +557,27 @@ cache_attn_fp32_kernel(const __grid_constant__ CacheAttnParams p) {
 
 constexpr int kMergeThreads = 128;
 
-// A thread has four features of a row; a block 16 rows by 32 features, so that
-// the partial results are read in runs of 16 rows x 16 bytes.
-// by_unit: block (unit, rows). Otherwise block (run, rows) serves the unit that
-// the run's start cuts, if it is the first cut of that unit: with more units
-// than runs most units are whole, and so need no block.
+// Block (unit or run, 16 rows, 32 features): joins the pieces of the unit, if it
+// was cut, in the order of the runs. A thread has four features of a
+// row; partial results are read in runs of 16 rows x 16 bytes.
 template <typename T, int D, int BR>
 __global__ void __launch_bounds__(kMergeThreads)
-cache_merge_kernel(const __grid_constant__ CacheAttnParams p, int grid, int by_unit) {
-  __shared__ LocateScratch<kMergeThreads> scratch;
-  const int units = p.Hkv * p.RB;
-  // the lengths are final: this grid starts when every CTA of the attention
-  // kernel is past its own wait
-  const int x0 = blockIdx.x;
-  const Located loc = locate<kMergeThreads>(p, scratch, grid, by_unit ? 0 : x0, by_unit ? x0 / units : -1, false);
-  const int run = (int)min(loc.cut.run, (int64_t)0x7fffffff);  // (a longer run has no second CTA)
-  const int64_t at = (int64_t)x0 * run;
-  bool mine = by_unit || at < loc.cut.total;
-  int b = 0, unit = 0;
-  int64_t first = 0, last = 0;
-  if (mine) {
-    b = by_unit ? x0 / units : loc.b;
-    const int len = loc.rp.nt + p.lead;
-    unit = by_unit ? x0 % units : div_small(at - loc.start, len);
-    const int64_t s = loc.start + (int64_t)unit * len;
-    first = div_up(s + p.lead + 1, run) - 1;  // the run that holds the unit's first tile
-    last = div_up(s + len, run) - 1;
-    mine = by_unit ? first != last : x0 == first + 1 && x0 <= last;
-  }
+cache_merge_kernel(const __grid_constant__ CacheAttnParams p) {
+  const int r = blockIdx.y * 16 + threadIdx.x % 16, d = (blockIdx.z * 8 + threadIdx.x / 16) * 4;
   grid_dependency_wait();
   allow_dependents();
-  if (!mine) return;
+  const int4 cut = __ldcg(p.cuts + blockIdx.x);
+  if (cut.z < 0) return;
+  const int b = cut.x, unit = cut.y, last = cut.z, first = cut.w;
   const int row0 = (unit % p.RB) * p.block_rows, rows = min(p.block_rows, p.R - row0);
-  const PieceOut po{true, 0, b, unit / p.RB, row0, rows};
-  const int r = blockIdx.y * 16 + threadIdx.x % 16, d = (blockIdx.z * 8 + threadIdx.x / 16) * 4;
   if (r >= rows) return;
+  const PieceOut po{true, 0, b, unit / p.RB, row0, rows};
   const float2 *ml = p.part_ml + r;
   const float *po_ = p.part_o + (d / 4) * (BR * 4) + r * 4;
   float m = -INFINITY, l = 0.f;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   constexpr int U = 8;  // partial results in flight
-  for (int64_t x = first; x <= last; x += U) {
+  for (int x = first; x <= last; x += U) {
     float2 a[U];
     float4 v[U];
 #pragma unroll
@@ -633,10 +617,9 @@ cache_merge_kernel(const __grid_constant__ CacheAttnParams p, int grid, int by_u
 
 template <typename T, int D, int BR>
 mgqa_status launch_merge(const CacheAttnParams &p, int grid, cudaStream_t s) {
-  const int64_t units = (int64_t)p.B * p.Hkv * p.RB;
-  const int by_unit = units <= grid;
-  const dim3 g((unsigned)(by_unit ? units : grid), (std::min(p.block_rows, p.R) + 15) / 16, D / 32);
-  const cudaError_t e = launch_pdl(cache_merge_kernel<T, D, BR>, g, dim3(kMergeThreads), 0, s, p, grid, by_unit);
+  const int blocks = p.by_unit ? p.B * p.Hkv * p.RB : grid;
+  const dim3 g((unsigned)blocks, (std::min(p.block_rows, p.R) + 15) / 16, D / 32);
+  const cudaError_t e = launch_pdl(cache_merge_kernel<T, D, BR>, g, dim3(kMergeThreads), 0, s, p);
   if (e != cudaSuccess) return fail(MGQA_ERR_CUDA, "cache attention merge launch: %s", cudaGetErrorString(e));
   return MGQA_OK;
 }
@@ -697,9 +680,9 @@ mgqa_status launch_simt(const CacheAttnParams &p, const CacheAttnLaunch &how, cu
 }  // namespace
 
 size_t cache_attn_workspace_bytes() {
-  // two partial results per CTA, rows of D + 2 floats: up to 64 rows with two
-  // CTAs an SM, up to 256 with one
-  return (size_t)kCacheAttnMaxCtas / 2 * 2 * 256 * (128 + 2) * sizeof(float);
+  // two partial results per CTA, rows of D + 2 floats: up to 128 rows with two
+  // CTAs an SM, up to 256 with one; and a word about every run's end
+  return kCacheAttnMaxCtas * sizeof(int4) + (size_t)kCacheAttnMaxCtas / 2 * 2 * 256 * (128 + 2) * sizeof(float);
 }
 
 mgqa_status launch_cache_merge(const CacheAttnParams &p, mgqa_dtype dt, int D, int block_rows, int grid,

@@ -223,7 +223,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   grid_dependency_wait();
   allow_dependents();  // lengths and tables are final from here on
   Walker walk;
-  walk.start(p, locate<L::threads>(p, sm.scratch, gridDim.x, blockIdx.x, -1, blockIdx.x == 0), blockIdx.x);
+  walk.start(p, locate<L::threads>(p, sm.scratch, gridDim.x, blockIdx.x, blockIdx.x == 0), blockIdx.x);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -462,8 +462,10 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     tc::regs_dec<L::kDec>();
     // ---------------- query rows and piece descriptions ----------------
     bool more = true;
+    if (lane == 0) tell_cut(p, blockIdx.x, nullptr);
     for (int piece = 0; more; ++piece) {
       more = walk.next(p, pc);
+      if (more && lane == 0) tell_cut(p, blockIdx.x, &pc);
       // (the slot is free: its piece's query rows were overwritten long ago)
       if (ok && piece > 0) ok = __all_sync(0xffffffffu, mbar_wait(&sm.qfree, (piece - 1) & 1, p.err));
       if (!ok) more = false;

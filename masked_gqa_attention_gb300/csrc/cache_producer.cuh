@@ -41,9 +41,10 @@ struct Pieces {
       only.rp = plan_row(p, only.b, rank == 0 && unit % units == 0 && threadIdx.x == 0);
       only.t0 = (int)((int64_t)only.rp.nt * rank / S);
       only.t1 = (int)((int64_t)only.rp.nt * (rank + 1) / S);
+      only.more = 0;
       __syncthreads();
     } else {
-      walk.start(p, locate<THREADS>(p, scratch, gridDim.x, blockIdx.x, -1, blockIdx.x == 0), blockIdx.x);
+      walk.start(p, locate<THREADS>(p, scratch, gridDim.x, blockIdx.x, blockIdx.x == 0), blockIdx.x);
     }
   }
   MGQA_DEV bool next(const CacheAttnParams &p, Piece &pc) {
@@ -70,7 +71,10 @@ MGQA_DEV void produce_tiles(const TmaParams &tp, Pieces pieces, int of_v, const 
   bool ok = true;
   int it = 0;  // tiles issued
   Piece pc;
+  const bool teller = !of_v && lane == 0 && !pieces.S;
+  if (teller) tell_cut(p, blockIdx.x, nullptr);
   while (ok && pieces.next(p, pc)) {
+    if (teller) tell_cut(p, blockIdx.x, &pc);
     const RowPlan &rp = pc.rp;
     // lane i: box i of the tile; the page of the next tile's box is looked up a tile ahead
     auto look_up = [&](int t) {

@@ -46,6 +46,11 @@ struct CacheAttnParams {
   int32_t *err;
   float *part_o;    // [2 * grid][D / 4][block rows][4] unnormalised partial outputs
   float2 *part_ml;  // [2 * grid][block rows] their (max, sum)
+  // What the merge kernel has to join: (request, unit, last run (-1: nothing),
+  // first run). By unit when there are no more units than runs, else by the run
+  // that ends with a unit's first piece.
+  int4 *cuts;
+  int32_t by_unit;
 };
 
 // What every launcher of the cache attention needs besides the parameters.
@@ -64,7 +69,9 @@ inline int64_t most_tiles(const CacheAttnParams &p) {
 
 // The workspace as the partial results of `grid` CTAs (two each).
 inline void set_partials(CacheAttnParams &p, void *ws, int grid, int block_rows, int D) {
-  p.part_o = static_cast<float *>(ws);
+  p.by_unit = (int64_t)p.B * p.Hkv * p.RB <= grid;
+  p.cuts = static_cast<int4 *>(ws);
+  p.part_o = reinterpret_cast<float *>(p.cuts + kCacheAttnMaxCtas);
   p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)2 * grid * block_rows * D);
 }
 
@@ -141,13 +148,12 @@ MGQA_DEV int64_t div_up(int64_t a, int b) {
   a += b - 1;
   return a <= 0x7fffffff ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
-MGQA_DEV int div_small(int64_t a, int b) {  // the quotient fits in 32 bits
-  return a <= 0x7fffffff ? (int)((uint32_t)a / (uint32_t)b) : (int)(a / b);
+MGQA_DEV int div_small(int64_t a, int64_t b) {  // the quotient fits in 32 bits
+  return a <= 0x7fffffff && b <= 0x7fffffff ? (int)((uint32_t)a / (uint32_t)b) : (int)(a / b);
 }
 
 // Scans the requests (every thread of the block takes part), finds the cut and
-// the request that holds the first tile of run `cta`, or, with want_b >= 0,
-// where request want_b starts.
+// the request that holds the first tile of run `cta`.
 struct Located {
   Cut cut;
   int b;          // the request
@@ -163,8 +169,7 @@ struct LocateScratch {
 };
 
 template <int THREADS>
-MGQA_DEV Located locate(const CacheAttnParams &p, LocateScratch<THREADS> &sc, int grid, int cta, int want_b,
-                        bool report) {
+MGQA_DEV Located locate(const CacheAttnParams &p, LocateScratch<THREADS> &sc, int grid, int cta, bool report) {
   constexpr int NW = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + THREADS - 1) / THREADS;
@@ -203,7 +208,7 @@ MGQA_DEV Located locate(const CacheAttnParams &p, LocateScratch<THREADS> &sc, in
     if (b >= p.B) break;
     if (per > 1) one = plan_row(p, b, false);
     const int len = one.nt + p.lead;
-    if (want_b >= 0 ? b == want_b : (want >= before * units && want < (before + len) * units)) {
+    if (want >= before * units && want < (before + len) * units) {
       sc.b = b;
       sc.start = before * units;
       sc.rp = one;
@@ -286,15 +291,18 @@ MGQA_DEV bool wanted(const RowPlan &rp, int kind, int j) {
 struct Piece {
   RowPlan rp;
   int b, g, rb, t0, t1;
+  int more;  // further runs that the unit reaches into
 };
 struct Walker {
   int64_t left;  // tiles of the run that are left
+  int64_t run;
   int b, unit, v0, units, RB, lead;
   RowPlan rp;
 
   MGQA_DEV void start(const CacheAttnParams &p, const Located &loc, int cta) {
     const int64_t f = (int64_t)cta * loc.cut.run;
     left = min(loc.cut.run, loc.cut.total - f);
+    run = loc.cut.run;
     RB = p.RB;
     lead = p.lead;
     units = p.Hkv * p.RB;
@@ -322,11 +330,23 @@ struct Walker {
       pc.rp = rp;
       pc.t0 = max(0, from - lead);
       pc.t1 = v1 - lead;
+      pc.more = pc.t1 < rp.nt ? div_small((int64_t)(rp.nt - pc.t1) + run - 1, run) : 0;
       return true;
     }
     return false;
   }
 };
+
+// Tells the merge kernel what run `cta` knows (one thread, which walks it too):
+// once with `pc` null, then with every piece.
+MGQA_DEV void tell_cut(const CacheAttnParams &p, int cta, const Piece *pc) {
+  if (!pc) {
+    if (!p.by_unit) p.cuts[cta] = make_int4(0, 0, -1, 0);
+  } else if (pc->t0 == 0 && (p.by_unit || pc->more)) {
+    const int unit = pc->g * p.RB + pc->rb;
+    p.cuts[p.by_unit ? pc->b * (p.Hkv * p.RB) + unit : cta] = make_int4(pc->b, unit, pc->more ? cta + pc->more : -1, cta);
+  }
+}
 
 // Where the finished or partial rows of a piece go. `whole`: the piece is the
 // whole unit.
