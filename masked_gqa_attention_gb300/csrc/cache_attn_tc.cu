@@ -50,7 +50,6 @@ template <int D, int NT>
 struct Lay {
   static constexpr int SHIFT = NT == 1 ? 6 : 7, BN = 1 << SHIFT;  // keys of a tile
   static constexpr int CTAS = NT == 1 ? 2 : 1;                    // of an SM
-  static constexpr int MAXT = NT == 1 ? BM : kMaxDrafts;          // drafts (one block: at most its rows)
   // registers: what the first warpgroup gives away goes to the softmax ones
   // (80 + 176 = 2 x 128, 104 + 2 x 200 = 3 x 168 a scheduler at launch)
   static constexpr int kDec = NT == 1 ? 80 : 104, kInc = NT == 1 ? 176 : 200;
@@ -67,7 +66,7 @@ struct Lay {
   static constexpr uint32_t tmem_used = NT * (SB * BN + D);
   static constexpr uint32_t tmem_cols = tmem_used <= 256 ? 256 : 512;
   struct Misc {
-    Drafts<MAXT> drafts;
+    Drafts<kMaxDrafts> drafts;
     LocateScratch<threads> scratch;
     Piece pieces[kPieceRing];      // rp.nt < 0: no more
     uint64_t pready[kPieceRing], qfree;
@@ -640,7 +639,17 @@ mgqa_status launch_t(TcCacheParams tp, mgqa_dtype dt, const CacheAttnLaunch &how
 
 template <typename T, int D>
 mgqa_status launch_d(const TcCacheParams &tp, mgqa_dtype dt, const CacheAttnLaunch &how, cudaStream_t s) {
-  return tp.a.T <= BM / tp.a.n_rep ? launch_t<T, D, 1>(tp, dt, how, s) : launch_t<T, D, 2>(tp, dt, how, s);
+  // More than 128 rows: two blocks a CTA share every key tile, one CTA an SM; or
+  // one block a CTA, two CTAs an SM, each reading the keys (mostly from the L2)
+  // but covering for one another between units. The second is ahead while the
+  // call is not long (64 drafts, 32 heads over 8: one request of up to 4096 tokens
+  // 22.0 and 14.9 us; 16 of up to 2048 57 and 48; 16 of up to 8192 99 and 108; 4 of
+  // up to 131072 266 and 396; D = 64, 16 of about 8100 117 and 113).
+  CacheAttnParams q = tp.a;
+  q.tile_shift = 6;
+  const int64_t reads = (int64_t)q.B * q.Hkv * most_tiles(q) * (kTile * D * 4);
+  const bool one = q.T <= BM / q.n_rep || reads <= ((int64_t)(D == 64 ? 384 : 192) << 20);
+  return one ? launch_t<T, D, 1>(tp, dt, how, s) : launch_t<T, D, 2>(tp, dt, how, s);
 }
 
 }  // namespace
