@@ -568,7 +568,11 @@ cache_merge_kernel(const __grid_constant__ CacheAttnParams p) {
   allow_dependents();
   const int4 cut = __ldcg(p.cuts + blockIdx.x);
   if (cut.z < 0) return;
-  const int b = cut.x, unit = cut.y, last = cut.z, first = cut.w;
+  const int b = cut.x, unit = cut.y, last = cut.z, first = cut.w, units = p.Hkv * p.RB;
+  // (an attention kernel whose waits gave up may have left no word: nothing is joined then)
+  if ((unsigned)b >= (unsigned)p.B || (unsigned)unit >= (unsigned)units || (unsigned)first >= (unsigned)p.grid ||
+      last >= p.grid || (p.by_unit ? b * units + unit : first) != (int)blockIdx.x)
+    return;
   const int row0 = (unit % p.RB) * p.block_rows, rows = min(p.block_rows, p.R - row0);
   if (r >= rows) return;
   const PieceOut po{true, 0, b, unit / p.RB, row0, rows};

@@ -50,7 +50,7 @@ struct CacheAttnParams {
   // first run). By unit when there are no more units than runs, else by the run
   // that ends with a unit's first piece.
   int4 *cuts;
-  int32_t by_unit;
+  int32_t by_unit, grid;
 };
 
 // What every launcher of the cache attention needs besides the parameters.
@@ -69,6 +69,7 @@ inline int64_t most_tiles(const CacheAttnParams &p) {
 
 // The workspace as the partial results of `grid` CTAs (two each).
 inline void set_partials(CacheAttnParams &p, void *ws, int grid, int block_rows, int D) {
+  p.grid = grid;
   p.by_unit = (int64_t)p.B * p.Hkv * p.RB <= grid;
   p.cuts = static_cast<int4 *>(ws);
   p.part_o = reinterpret_cast<float *>(p.cuts + kCacheAttnMaxCtas);
@@ -88,6 +89,9 @@ mgqa_status launch_cache_attn_f32(const CacheAttnParams &p, int D, const CacheAt
 bool cache_attn_tc_takes(const CacheAttnParams &p, mgqa_dtype dt);
 mgqa_status launch_cache_attn_tc(const CacheAttnParams &p, mgqa_dtype dt, int D, const CacheAttnLaunch &how,
                                  cudaStream_t s);
+// Whether TMA can describe the call's tensors: a stride of 0 (a broadcast) over
+// more than one element it cannot.
+bool cache_attn_plain_strides(const CacheAttnParams &p);
 // Tensor maps of the cache (boxes of `box_rows` slots: the largest power of two
 // up to `tile` that divides the page) and of the drafts.
 bool cache_attn_maps(const CacheAttnParams &p, mgqa_dtype dt, int D, int tile, CUtensorMap (&maps)[4], int &box_rows);
