@@ -471,7 +471,7 @@ mgqa_status launch_d(const CUtensorMap (&maps)[4], const TmaParams &tp, const Ca
 }  // namespace
 
 bool cache_attn_f32_takes(const CacheAttnParams &p, mgqa_dtype dt) {
-  return dt == MGQA_FP32 && (!p.table || p.page_size % 8 == 0);
+  return dt == MGQA_FP32 && (!p.table || p.page_size % 8 == 0) && cache_attn_plain_strides(p);
 }
 
 mgqa_status launch_cache_attn_f32(const CacheAttnParams &p, int D, const CacheAttnLaunch &how, cudaStream_t s) {

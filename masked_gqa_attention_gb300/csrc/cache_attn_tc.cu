@@ -655,7 +655,8 @@ mgqa_status launch_d(const TcCacheParams &tp, mgqa_dtype dt, const CacheAttnLaun
 }  // namespace
 
 bool cache_attn_tc_takes(const CacheAttnParams &p, mgqa_dtype dt) {
-  return dt != MGQA_FP32 && (!p.table || p.page_size % 8 == 0) && p.n_rep <= BM && p.scale_log2 >= 0.f;
+  return dt != MGQA_FP32 && (!p.table || p.page_size % 8 == 0) && p.n_rep <= BM && p.scale_log2 >= 0.f &&
+         cache_attn_plain_strides(p);
 }
 
 mgqa_status launch_cache_attn_tc(const CacheAttnParams &p, mgqa_dtype dt, int D, const CacheAttnLaunch &how,

@@ -389,6 +389,15 @@ mgqa_status launch_d(const CUtensorMap (&maps)[4], const TmaParams &tp, const Ca
 
 }  // namespace
 
+bool cache_attn_plain_strides(const CacheAttnParams &p) {
+  auto plain = [](const int64_t *st, int64_t n0, int64_t n1, int64_t n2) {
+    return (st[0] || n0 == 1) && (st[1] || n1 == 1) && (st[2] || n2 == 1);
+  };
+  const int pages = p.table ? p.num_pages : p.B, slots = p.table ? p.page_size : p.cap;
+  return plain(p.ks, pages, p.Hkv, slots) && plain(p.vs, pages, p.Hkv, slots) && plain(p.qs, p.B, p.Hq, p.T) &&
+         (!p.tree || (plain(p.kns, p.B, p.Hkv, p.T) && plain(p.vns, p.B, p.Hkv, p.T)));
+}
+
 bool cache_attn_maps(const CacheAttnParams &p, mgqa_dtype dt, int D, int tile, CUtensorMap (&maps)[4], int &box_rows) {
   const int cols = dt == MGQA_FP32 ? 32 : 64;  // 128 bytes
   box_rows = tile;
@@ -408,7 +417,7 @@ bool cache_attn_maps(const CacheAttnParams &p, mgqa_dtype dt, int D, int tile, C
 // longer ones the tensor-memory kernel is ahead (64 rows, 4 requests of up to
 // 131072: 305 us here, 234 us there; one request of up to 4096: 13 and 19 us).
 bool cache_attn_tma_takes(const CacheAttnParams &p, mgqa_dtype dt, int D) {
-  if (dt == MGQA_FP32 || p.R > 64 || (p.table && p.page_size % 8)) return false;
+  if (dt == MGQA_FP32 || p.R > 64 || (p.table && p.page_size % 8) || !cache_attn_plain_strides(p)) return false;
   return p.R <= 32 || short_call(p, D * 2) || !cache_attn_tc_takes(p, dt);
 }
 

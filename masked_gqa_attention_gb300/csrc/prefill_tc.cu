@@ -1078,7 +1078,7 @@ bool make_tma_map(CUtensorMap *m, mgqa_dtype dt, const void *base, int rank, con
     d[i] = (cuuint64_t)dims[i];
     b[i] = (cuuint32_t)box[i];
     estr[i] = 1;
-    if (i) st[i - 1] = (cuuint64_t)strides[i - 1] * es;
+    if (i) st[i - 1] = dims[i] > 1 ? (cuuint64_t)strides[i - 1] * es : 16;  // (one element: any stride)
   }
   return fn(m, t, (cuuint32_t)rank, const_cast<void *>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,

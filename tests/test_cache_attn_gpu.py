@@ -209,6 +209,96 @@ def test_scales(M, dtype):
         Case([130, 5], 6, 4, 2, 64, dtype, page=16, scale=scale).run(M)
 
 
+@pytest.mark.parametrize("dtype", [BF, HF, FP])
+def test_many_rows(M, dtype):
+    # past one block of 128 rows, two of 128, and a group that no block holds
+    Case([700, 0, 129], 64, 8, 2, 128, dtype, page=16).run(M)
+    Case([300, 65], 40, 28, 4, 64, dtype, page=64, window=100, sinks=3).run(M)
+    Case([130], 3, 200, 1, 64, dtype, page=16).run(M)
+    Case([9000, 20], 70, 24, 8, 128, dtype, page=0).run(M)
+
+
+def test_large_trees_over_long_rows(M):
+    # reads past the size where two row blocks share the key tiles
+    Case([40000, 39000, 33, 40001], 64, 64, 16, 128, BF, page=64, cap=40100).run(M)
+    Case([70000, 12], 61, 24, 8, 64, HF, page=0, cap=100000, window=30000, sinks=4, live=[61, 3]).run(M)
+    Case([33000, 31000, 100], 44, 48, 16, 128, BF, page=16, cap=33100).run(M)  # groups of three heads
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_scales_of_many_rows(M, dtype):
+    for scale in (0.0, -0.4, 3.0):
+        Case([300, 5], 50, 8, 2, 64, dtype, page=16, scale=scale).run(M)
+
+
+def test_rising_scores_rescale(M):
+    # keys whose scores climb by more than 2^8 from tile to tile: the running
+    # maximum moves at every one and the outputs so far are rescaled
+    for T, Hq, window in ((1, 4, 0), (24, 8, 0), (64, 8, 0), (24, 8, 900)):
+        c = Case([1500, 700], T, Hq, 2, 128, BF, page=64, window=window)
+        g = torch.linspace(1, 40, c.k.shape[0], device="cuda").to(BF)  # by page: any order of tiles
+        q = c.q[:, :, :, :1].sign() * torch.ones_like(c.q)
+        kk = torch.full_like(c.k, 0.05) * g[:, None, None, None]
+        c.k = torch.where(torch.isnan(c.k), c.k, kk)
+        c.q = q
+        want = []
+        for b, n in enumerate((1500, 700)):
+            rows = c.table[b].long()
+            rows = torch.where((rows >= 0) & (rows < c.k.shape[0]), rows, 0)
+            k = c.k[rows].transpose(0, 1).reshape(2, -1, 128)[:, :n]
+            v = c.v[rows].transpose(0, 1).reshape(2, -1, 128)[:, :n]
+            seen = c.seen[b].cuda()
+            pos = n + seen.sum(1) - 1
+            see = torch.ones(T, n, dtype=torch.bool, device="cuda")
+            if window:
+                see = pos[:, None] - torch.arange(n, device="cuda") < window
+                seen = seen & (pos[:, None] - pos < window)
+            want.append((attention(q[b], torch.cat([k, c.kn[b]], 1), torch.cat([v, c.vn[b]], 1),
+                                   torch.cat([see, seen], 1), c.scale), n + T))
+        c.want = want
+        c.run(M)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_other_layouts(M, dtype):
+    for T in (1, 6, 40):
+        c = Case([100, 300], T, 8, 2, 64, dtype, page=16)
+        want = c.run(M).clone()
+        # pools stored slot by slot, [pages, page, Hkv, D], and a table inside a wider one
+        k, v, table = c.k, c.v, c.table
+        c.k, c.v = (x.transpose(1, 2).contiguous().transpose(1, 2) for x in (k, v))
+        wide = torch.full((2, table.shape[1] + 7), -5, dtype=torch.int32, device="cuda")
+        wide[:, 3:3 + table.shape[1]] = table
+        c.table = wide[:, 3:3 + table.shape[1]]
+        assert torch.equal(c.run(M), want)
+        # K and V in one tensor, q as a projection leaves it
+        c.k, c.v = torch.stack([k, v], 2).unbind(2)
+        c.q = c.q.transpose(1, 2).contiguous().transpose(1, 2)
+        assert torch.equal(c.run(M), want)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_broadcast_tensors(M, dtype):
+    # one row of drafts for the whole batch, one mask for every request
+    for T in (5, 40):
+        c = Case([100, 300], T, 4, 2, 64, dtype, page=16)
+        d = Case([100, 300], T, 4, 2, 64, dtype, page=16)
+        for name in ("kn", "vn", "q"):
+            x = getattr(c, name)[:1]
+            setattr(c, name, x.expand(2, -1, -1, -1))
+            setattr(d, name, x.expand(2, -1, -1, -1).contiguous())
+        c.bits, d.bits = c.bits[:1], c.bits[:1].expand(2, -1, -1).contiguous()
+        a, b = c.call(M), d.call(M)
+        assert int(c.err) == 0 and (a.float() - b.float()).abs().max() <= 2e-2 and torch.isfinite(a).all()
+
+
+def test_sizes_past_32_bits_in_counts(M):
+    c = Case([100], 4, 4, 2, 64, BF, page=16)
+    want = c.run(M).clone()
+    c.window, c.sinks = 2 ** 40, 2 ** 33 + 1  # wider than anything: no window
+    assert torch.equal(c.call(M), want)
+
+
 def test_largest_slots(M):
     # past 2^31 elements of one cache: 64-bit offsets (bf16, 2 x 4.4 GB)
     n, Hkv, D = 2_200_000, 8, 128
