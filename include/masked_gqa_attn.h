@@ -355,8 +355,9 @@ MGQA_API mgqa_status masked_gqa_attn_decode_window(const mgqa_args *args, const 
  * q, out [B][Hq][Lq][D]. The drafts' keys and values come from `tree` and are
  * not written to the cache: masked_gqa_cache_append stores the accepted ones.
  * Cache forms, kv_len, workspace and errors as for
- * masked_gqa_attn_decode_window. Values of rows that are seen by any draft of a
- * request have to be finite. */
+ * masked_gqa_attn_decode_window. Keys and values of the live drafts, and of the
+ * cached slots that any draft of the request sees, have to be finite; what lies
+ * elsewhere may be anything. */
 MGQA_API mgqa_status masked_gqa_attn_decode_tree(const mgqa_args *args, const mgqa_pages *pages,
                                                  const mgqa_tree *tree, int32_t window,
                                                  int32_t sinks, void *workspace,
@@ -387,7 +388,7 @@ typedef struct {
  * last slot, appends nothing and keeps its length; an index outside [0, T) or a
  * missing page leaves that slot as it was; each sets *dev_error. No other slot
  * is written. Requests must not share the pages that they append to (fork sees
- * to that). */
+ * to that), and the new rows must not lie in the cache. */
 MGQA_API mgqa_status masked_gqa_cache_append(const mgqa_cache *cache, const void *k_new,
                                              const void *v_new, const int64_t *k_new_stride,
                                              const int64_t *v_new_stride, int32_t T,

@@ -667,6 +667,11 @@ def _ints(t, name, shape, contiguous=True):
     return t.data_ptr()
 
 
+def _i32(x):
+    """x as a 32-bit count (what lies past the range stays past every size)."""
+    return max(-1, min(x, 0x7fffffff))
+
+
 def _go(dev, stream, fn, *args):
     """fn(*args, stream) with device `dev` current; its own current stream
     unless one is given."""
@@ -695,7 +700,7 @@ def masked_gqa_attn_prefill_window(q, k, v, out=None, *, window, sinks=0, causal
     else:
         a = bytes(make_args(q, k, v, out, scale=scale, mask_bits=mask_bits, kv_len=kv_len, seg_q=seg_q,
                             seg_k=seg_k, lse=lse, dev_error=dev_error, causal=causal))
-    _go(dev, stream, lib().masked_gqa_attn_prefill_window, a, window, sinks)
+    _go(dev, stream, lib().masked_gqa_attn_prefill_window, a, _i32(window), _i32(sinks))
     return out
 
 
@@ -771,7 +776,7 @@ def masked_gqa_attn_decode_window(q, k_cache, v_cache, kv_len, out=None, *, wind
     if kv_len is None:
         raise ValueError("kv_len is required")
     a, pages = _attn_args(q, k_cache, v_cache, out, kv_len, scale, lse, dev_error, page_table)
-    _go(dev, stream, lib().masked_gqa_attn_decode_window, a, pages, window, sinks,
+    _go(dev, stream, lib().masked_gqa_attn_decode_window, a, pages, _i32(window), _i32(sinks),
         workspace.data_ptr(), workspace.nbytes)
     return out
 
@@ -816,7 +821,7 @@ def masked_gqa_attn_decode_tree(q, k_cache, v_cache, k_new, v_new, kv_len, out=N
         st = tree_bits.stride(1) if t0 > 1 else 0
     tree = _TREE.pack(k_new.data_ptr(), v_new.data_ptr(), n0, n1, n2, m0, m1, m2, bits, sb, st,
                       _ints(tree_len, "tree_len", (B,)))
-    _go(dev, stream, lib().masked_gqa_attn_decode_tree, a, pages, tree, window, sinks,
+    _go(dev, stream, lib().masked_gqa_attn_decode_tree, a, pages, tree, _i32(window), _i32(sinks),
         workspace.data_ptr(), workspace.nbytes)
     return out
 
@@ -912,7 +917,7 @@ def masked_gqa_cache_fork(k_cache, v_cache, page_table, kv_len, ref, src, dst, *
         return
     c = _cache(k_cache, v_cache, page_table, kv_len, ref, dev_error)[0]
     ws = _pages_ws(workspace, c, n, k_cache.device)
-    _go(dev, stream, lib().masked_gqa_cache_fork, c, n, sp, dp, extra, ws.data_ptr(), ws.nbytes)
+    _go(dev, stream, lib().masked_gqa_cache_fork, c, n, sp, dp, _i32(extra), ws.data_ptr(), ws.nbytes)
 
 
 def masked_gqa_cache_compact(k_cache, v_cache, page_table, ref, page_table_out=None, ref_out=None, *,

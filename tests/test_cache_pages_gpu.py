@@ -238,6 +238,25 @@ def test_compact_large_offsets(M):
         assert x[0, 1, -1, -1, -1] == (npages - 1) % 241
 
 
+def test_the_largest_pool(M):
+    # 2^20 pages, the most that are planned: fork's free pages and compact's moves at both ends
+    n = 1 << 20
+    k = torch.zeros(1, n, 1, 1, 8, dtype=BF, device="cuda")
+    k[0, :, 0, 0, 0] = (torch.arange(n, device="cuda") % 127).to(BF)
+    v = k.clone()
+    ref = torch.ones(n, dtype=torch.int32, device="cuda")
+    ref[[7, n - 1]] = 0
+    table, lens = i32([[n - 2, n - 3, -1], [-1, -1, -1]]), i32([2, 0])
+    M.masked_gqa_cache_fork(k, v, table, lens, ref, i32([0, 0]), i32([0, 1]), extra=1)
+    assert table.tolist() == [[n - 2, n - 3, 7], [n - 2, n - 3, n - 1]] and lens.tolist() == [2, 2]
+    assert ref[[7, n - 1, n - 2]].tolist() == [1, 1, 2]
+    ref.zero_()
+    ref[table[0].long()], ref[n - 1] = 1, 1
+    M.masked_gqa_cache_compact(k, v, table, ref)
+    assert table.tolist() == [[2, 1, 0], [2, 1, 3]] or sorted(table.flatten().tolist()) == [0, 1, 1, 2, 2, 3]
+    assert int(ref[:4].sum()) == 4 and int(ref.sum()) == 4
+
+
 # ---- together -------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", [BF, FP])
