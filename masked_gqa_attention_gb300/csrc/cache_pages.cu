@@ -78,7 +78,9 @@ append_kernel(const __grid_constant__ AppendParams p) {
   grid_dependency_wait();
   allow_dependents();
   const int64_t cap = c.table ? (int64_t)c.max_pages * c.page_size : c.page_size;
-  const int n = __ldg(c.kv_len + b);
+  // (past the L1: a line of it that also holds kv_len_out must not be there when
+  // the next kernel, already resident, reads the new lengths)
+  const int n = __ldcg(c.kv_len + b);
   const int cnt = p.count ? __ldg(p.count + b) : p.T;
   const bool bad = n < 0 || cnt < 0 || cnt > p.T || (int64_t)n + cnt > cap;
   // the block's rows from t0 on, all heads of each. Without a count the new rows
@@ -540,7 +542,7 @@ compact_apply_kernel(const __grid_constant__ CompactParams p) {
   };
   for (int64_t u = t0; u < (int64_t)c.rows * c.max_pages; u += ts) {
     const int r = (int)(u / c.max_pages), j = (int)(u % c.max_pages);
-    int e = c.table[(int64_t)r * c.table_stride + j];
+    int e = __ldcg(c.table + (int64_t)r * c.table_stride + j);  // (past the L1, as append's lengths)
     if (e >= c.num_pages || e < -1) {
       report_error(c.err, MGQA_ERR_INVALID_ARG);
       e = -1;
@@ -552,7 +554,7 @@ compact_apply_kernel(const __grid_constant__ CompactParams p) {
     p.table_out[(int64_t)r * p.table_out_stride + j] = e;
   }
   for (int64_t k = t0; k < moves; k += ts) {
-    const int a = p.from[k], b = p.to[k], r = c.ref[a];
+    const int a = p.from[k], b = p.to[k], r = __ldcg(c.ref + a);
     p.ref_out[b] = r;
     p.ref_out[a] = 0;
   }
@@ -560,7 +562,7 @@ compact_apply_kernel(const __grid_constant__ CompactParams p) {
     for (int64_t u = t0; u < c.num_pages; u += ts) {
       const int page = (int)u;
       const bool in_use = (p.bits[page >> 5] >> (page & 31)) & 1u;
-      if (in_use == (page < used)) p.ref_out[page] = c.ref[page];
+      if (in_use == (page < used)) p.ref_out[page] = __ldcg(c.ref + page);
     }
 }
 

@@ -257,6 +257,22 @@ def test_the_largest_pool(M):
     assert int(ref[:4].sum()) == 4 and int(ref.sum()) == 4
 
 
+def test_lengths_side_by_side(M):
+    # old and new lengths in the same 32 bytes, each step reading what the one before wrote
+    B, cap, D, steps = 4, 700, 64, 300
+    k = torch.zeros(B, 1, cap, D, dtype=BF, device="cuda")
+    v = torch.zeros_like(k)
+    new = torch.randn(steps, B, 1, 1, D, device="cuda").to(BF)
+    lens = torch.zeros(2, B, dtype=torch.int32, device="cuda")
+    q, ws = torch.randn(B, 1, 1, D, device="cuda").to(BF), M.new_cache_attn_workspace()
+    outs = torch.empty(steps, B, 1, 1, D, dtype=BF, device="cuda")
+    for i in range(steps):
+        M.masked_gqa_cache_append(k, v, new[i], new[i], lens[i % 2], lens[1 - i % 2])
+        M.masked_gqa_attn_decode_window(q, k, v, lens[1 - i % 2], outs[i], window=1, workspace=ws)
+    assert lens.tolist() == [[steps] * B, [steps - 1] * B]
+    assert torch.equal(outs, new)  # a window of one: the token just appended
+
+
 # ---- together -------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", [BF, FP])
