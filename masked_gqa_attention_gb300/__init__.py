@@ -672,6 +672,18 @@ def _i32(x):
     return max(-1, min(x, 0x7fffffff))
 
 
+def _kept(ws, stream):
+    """A workspace allocated for a call on `stream`: not given out again before
+    the call is done there."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            handle = _stream_handle(stream)
+            stream = torch.cuda.ExternalStream(handle, device=ws.device) if handle \
+                else torch.cuda.default_stream(ws.device)
+        ws.record_stream(stream)
+    return ws
+
+
 def _go(dev, stream, fn, *args):
     """fn(*args, stream) with device `dev` current; its own current stream
     unless one is given."""
@@ -770,7 +782,7 @@ def masked_gqa_attn_decode_window(q, k_cache, v_cache, kv_len, out=None, *, wind
     if out is None:
         out = torch.empty_like(q)
     if workspace is None:
-        workspace = new_cache_attn_workspace(q.device)
+        workspace = _kept(new_cache_attn_workspace(q.device), stream)
     dev = _together(q, (k_cache, v_cache, kv_len, out, page_table, workspace, lse, dev_error),
                     "k_cache v_cache kv_len out page_table workspace lse dev_error")
     if kv_len is None:
@@ -794,7 +806,7 @@ def masked_gqa_attn_decode_tree(q, k_cache, v_cache, k_new, v_new, kv_len, out=N
     if out is None:
         out = torch.empty_like(q)
     if workspace is None:
-        workspace = new_cache_attn_workspace(q.device)
+        workspace = _kept(new_cache_attn_workspace(q.device), stream)
     dev = _together(q, (k_cache, v_cache, k_new, v_new, kv_len, out, tree_bits, tree_len, page_table,
                         workspace, lse, dev_error),
                     "k_cache v_cache k_new v_new kv_len out tree_bits tree_len page_table workspace "
@@ -889,13 +901,13 @@ def masked_gqa_cache_workspace_size(k_cache, v_cache, page_table, ref, n=0) -> i
     return size
 
 
-def _pages_ws(workspace, c, n, device):
+def _pages_ws(workspace, c, n, device, stream):
     if workspace is not None:
         return workspace
     size = int(lib().masked_gqa_cache_workspace_size(c, n))
     if size == 0:
         _check(MGQA_ERR_INVALID_ARG)
-    return torch.empty(size, dtype=torch.uint8, device=device)
+    return _kept(torch.empty(size, dtype=torch.uint8, device=device), stream)
 
 
 def masked_gqa_cache_fork(k_cache, v_cache, page_table, kv_len, ref, src, dst, *, extra=0,
@@ -916,7 +928,7 @@ def masked_gqa_cache_fork(k_cache, v_cache, page_table, kv_len, ref, src, dst, *
     if n == 0:
         return
     c = _cache(k_cache, v_cache, page_table, kv_len, ref, dev_error)[0]
-    ws = _pages_ws(workspace, c, n, k_cache.device)
+    ws = _pages_ws(workspace, c, n, k_cache.device, stream)
     _go(dev, stream, lib().masked_gqa_cache_fork, c, n, sp, dp, _i32(extra), ws.data_ptr(), ws.nbytes)
 
 
@@ -936,7 +948,7 @@ def masked_gqa_cache_compact(k_cache, v_cache, page_table, ref, page_table_out=N
     tp = _ints(page_table_out, "page_table_out", page_table.shape, contiguous=False)
     if page_table_out.stride(1) != 1:
         raise ValueError("page_table_out must have unit-stride rows")
-    ws = _pages_ws(workspace, c, 0, k_cache.device)
+    ws = _pages_ws(workspace, c, 0, k_cache.device, stream)
     _go(dev, stream, lib().masked_gqa_cache_compact, c, tp, page_table_out.stride(0),
         _ints(ref_out, "ref_out", ref.shape), _ints(used_out, "used_out", (1,)), ws.data_ptr(), ws.nbytes)
     return page_table_out, ref_out

@@ -359,6 +359,21 @@ def test_captured_replayed_and_other_stream(M):
     assert torch.equal(oa, want)
 
 
+@pytest.mark.parametrize("plain", [True, False])
+def test_own_workspace_on_another_stream(M, plain):
+    # a workspace that the call allocates is not given out again before the call is done
+    c = Case([3000, 1500], 8, 8, 2, 64, BF, page=5)  # (the general form: partial results in the workspace)
+    want = c.run(M).clone()
+    s, out = torch.cuda.Stream(), torch.empty_like(want)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    c.call(M, out=out, stream=s if plain else s.cuda_stream, workspace=None)
+    junk = [torch.full((M.masked_gqa_attn_cache_workspace_size(),), 255, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and len(junk) == 3
+
+
 @pytest.mark.parametrize("dtype", [BF, FP])
 def test_bad_lengths_and_pages_are_reported(M, dtype):
     c = Case([100, 50], 4, 4, 2, 64, dtype, page=16, cap=128)
