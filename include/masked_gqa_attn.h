@@ -301,7 +301,8 @@ MGQA_API mgqa_status masked_gqa_attn_decode_append_rope(
  * window >= 1 counts the query's own position; sinks >= 0. Only the key tiles
  * that the window and the sinks reach are read. Same types, head dims, strides
  * and errors as masked_gqa_attn_prefill; with kv_len or segment ids the forms
- * are combined with AND, so a padded row keeps positions 0 .. Lk - 1. */
+ * are combined with AND, so a padded row keeps positions 0 .. Lk - 1. Keys and
+ * values behind kv_len may hold anything; all others have to be finite. */
 MGQA_API mgqa_status masked_gqa_attn_prefill_window(const mgqa_args *args, int32_t window,
                                                     int32_t sinks, cudaStream_t stream);
 

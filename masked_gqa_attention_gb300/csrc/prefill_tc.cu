@@ -870,9 +870,22 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       // likewise probed before the last MMA of head 0's S group.
       constexpr int kHalfPV = BN / 32, kLateS = D / 16 - 1;
       bool p0_seen = false;  // P_0(n) already observed complete
+      // Under a window the value rows behind kv_len may hold anything: the tile
+      // that kv_len ends in (the last one, if it has a key to give) is cleared there.
+      const int tail = !ROPE && p.mask.window && kvl > 0 && kvl < p.Lk ? kvl % BN : 0;
+      const bool cut = tail && ((ne_bits[(kvl / BN) >> 5] >> ((kvl / BN) & 31)) & 1u);
       for (int n = 0; n < nk && ok; ++n) {
         const int st = n % STAGES;
         const bool has_next = n + 1 < nk;
+        if (cut && !has_next) {
+          for (int u = lane; u < (BN - tail) * (D / 8); u += 32) {
+            const int c = u % (D / 8);  // 16-byte pieces (the swizzle permutes them within a row)
+            *reinterpret_cast<uint4 *>(smem + Lay::v_off + (st * KB + (c >> 3)) * BOX + (tail + u / (D / 8)) * 128 +
+                                       (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
         const int st1 = (n + 1) % STAGES, use1 = (n + 1) / STAGES;
         bool p1_seen = false;  // P_1(n) already observed complete
         for (int t = 0; t < NT && ok; ++t) {

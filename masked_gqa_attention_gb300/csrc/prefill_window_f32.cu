@@ -162,7 +162,8 @@ prefill_window_f32_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid
         }
       }
       __syncwarp();  // a row's weights come from the 16 lanes that read them
-      simt::values<D, kRPT, C::WP>(o, &sm.w[0][0], vt, ty, tx, 0xffffffffu, 0xffffffffu);
+      // (values behind kv_len may hold anything)
+      simt::values<D, kRPT, C::WP>(o, &sm.w[0][0], vt, ty, tx, low_mask(kvl - k0), low_mask(kvl - k0 - 32));
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(sm.empty + st);

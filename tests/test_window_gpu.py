@@ -105,6 +105,26 @@ def test_hidden_keys_may_hold_anything_outside_the_read_tiles(M, dtype):
     check(out[0], None, attention(q[0, :, 768:], k[0], v[0], vis, 64 ** -0.5), 1024)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype,D", [(BF, 128), (HF, 64), (FP, 64), (FP, 128)])
+def test_rows_behind_their_length_may_hold_anything(M, dtype, D, causal):
+    lens, L, bad = [400, 130, 1, 0, 256, 399, 17], 400, float("nan")
+    B, H = len(lens), 2
+    q, k, v = (rand((B, H, L, D), dtype, s) for s in (1, 2, 3))
+    for b, n in enumerate(lens):
+        k[b, :, n:], v[b, :, n:] = bad, bad
+        bad = -bad if b % 2 else float("inf")
+    lse = torch.empty(B, H, L, device="cuda")
+    for window, sinks in ((70, 3), (400, 0)):
+        out = M.masked_gqa_attn_prefill_window(q, k, v, window=window, sinks=sinks, causal=causal, lse=lse,
+                                               kv_len=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+        vis = visible(L, L, window, sinks, causal)
+        for b, n in enumerate(lens):
+            kb, vb = k[b].clone(), v[b].clone()
+            kb[:, n:], vb[:, n:] = 0, 0
+            check(out[b], lse[b], attention(q[b], kb, vb, vis & (torch.arange(L, device="cuda") < n), D ** -0.5), L, f"row {b}")
+
+
 def test_negative_scale_and_strides(M):
     run(M, 1, 4, 2, 260, 260, 128, BF, 99, 4, True, scale=-0.3)
     # a [B, L, H, D] projection's views
