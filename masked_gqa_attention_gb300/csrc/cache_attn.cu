@@ -39,51 +39,63 @@ MGQA_DEV void cp_async16_or_zero(uint32_t dst, const void *src, bool take) {
                : "memory");
 }
 
-// The rows of one tile, fetched by a whole CTA: pass u of thread tid brings
-// 16-byte piece tid % CH of row tid / CH + u * RPP. `pg` holds the pages of
-// those rows of the tile that is fetched next.
+// The rows of one tile, fetched by a whole CTA. One thread a row finds where it
+// lies (the page two tiles ahead of its use, so the table is never waited for)
+// and leaves the two offsets in shared memory; then pass u of thread tid brings
+// 16-byte piece tid % CH of row tid / CH + u * RPP. (Every thread finding its own
+// rows' addresses took three times the instructions of the copies themselves.)
+constexpr int64_t kHidden = -1, kMissing = -2;  // offsets of rows that nobody sees, of a page that is not there
+struct RowOffsets {
+  longlong2 at[2][kTile];  // of alternating tiles: bytes of the row in K and in V
+};
+
 template <typename T, int D, int THREADS>
 struct TileLoader {
   static constexpr int CH = D * (int)sizeof(T) / 16;
   static constexpr int RPP = THREADS / CH;
   static constexpr int NP = kTile / RPP;
-  static_assert(THREADS % CH == 0 && kTile % RPP == 0, "whole rows per pass");
-  int pg[NP];
+  static_assert(THREADS % CH == 0 && kTile % RPP == 0 && THREADS >= kTile, "whole rows per pass");
+  int page;  // of this thread's row of the tile that is placed next (-2: hidden, -1: missing)
 
   MGQA_DEV void look_up(const CacheAttnParams &p, const RowPlan &rp, int b, int i, int tid) {
+    if (tid >= kTile) return;
     int kind;
-    const int k0 = first_key(rp, i, 6, kind);
-#pragma unroll
-    for (int u = 0; u < NP; ++u) {
-      const int j = k0 + tid / CH + u * RPP;
-      pg[u] = -1;
-      if (wanted(rp, kind, j)) pg[u] = kind ? b : page_of(p, b, j);
-    }
+    const int j = first_key(rp, i, 6, kind) + tid;
+    page = wanted(rp, kind, j) ? (kind ? b : page_of(p, b, j)) : -2;
+  }
+  // Row offsets of tile i, whose page was looked up, to `off`.
+  MGQA_DEV void place(const CacheAttnParams &p, const RowPlan &rp, int g, int i, int tid, longlong2 *off) const {
+    if (tid >= kTile) return;
+    int kind;
+    const int j = first_key(rp, i, 6, kind) + tid;
+    const int64_t *ks = kind ? p.kns : p.ks, *vs = kind ? p.vns : p.vs;
+    const int s = kind ? j : slot_in_page(p, j);
+    longlong2 at = make_longlong2(page == -2 ? kHidden : kMissing, 0);
+    if (page >= 0)
+      at = make_longlong2(((int64_t)page * ks[0] + (int64_t)g * ks[1] + (int64_t)s * ks[2]) * (int64_t)sizeof(T),
+                          ((int64_t)page * vs[0] + (int64_t)g * vs[1] + (int64_t)s * vs[2]) * (int64_t)sizeof(T));
+    off[tid] = at;
   }
   // Issues tile i into kdst / vdst (shared addresses; row_addr(r, piece)); ok[r]
   // tells whether row r counts, *bad is raised when a page is missing.
   template <typename RowAddr>
-  MGQA_DEV void issue(const CacheAttnParams &p, const RowPlan &rp, int g, int i, int tid,
+  MGQA_DEV void issue(const CacheAttnParams &p, const RowPlan &rp, int i, int tid, const longlong2 *off,
                       uint32_t kdst, uint32_t vdst, uint8_t *ok, int *bad, RowAddr row_addr) const {
-    int kind;
-    const int k0 = first_key(rp, i, 6, kind);
-    const char *kb = static_cast<const char *>(kind ? p.kn : p.k);
-    const char *vb = static_cast<const char *>(kind ? p.vn : p.v);
-    const int64_t *ks = kind ? p.kns : p.ks, *vs = kind ? p.vns : p.vs;
+    const bool kind = i >= rp.np;
     const int piece = tid % CH;
+    const char *kb = static_cast<const char *>(kind ? p.kn : p.k) + piece * 16;
+    const char *vb = static_cast<const char *>(kind ? p.vn : p.v) + piece * 16;
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
-      const int r = tid / CH + u * RPP, j = k0 + r;
-      const bool want = wanted(rp, kind, j), take = want && pg[u] >= 0;
-      const int s = kind ? j : slot_in_page(p, j);
-      const int64_t ko = take ? ((int64_t)pg[u] * ks[0] + (int64_t)g * ks[1] + (int64_t)s * ks[2]) * (int64_t)sizeof(T) + piece * 16 : 0;
-      const int64_t vo = take ? ((int64_t)pg[u] * vs[0] + (int64_t)g * vs[1] + (int64_t)s * vs[2]) * (int64_t)sizeof(T) + piece * 16 : 0;
+      const int r = tid / CH + u * RPP;
+      const longlong2 at = off[r];
+      const bool take = at.x >= 0;
       // a row that does not count gives zeros and is not read (any valid address)
-      cp_async16_or_zero(kdst + row_addr(r, piece), take ? kb + ko : static_cast<const char *>(p.k), take);
-      cp_async16_or_zero(vdst + row_addr(r, piece), take ? vb + vo : static_cast<const char *>(p.v), take);
+      cp_async16_or_zero(kdst + row_addr(r, piece), take ? kb + at.x : static_cast<const char *>(p.k), take);
+      cp_async16_or_zero(vdst + row_addr(r, piece), take ? vb + at.y : static_cast<const char *>(p.v), take);
       if (piece == 0) {
         ok[r] = take;
-        if (want && !take) {
+        if (at.x == kMissing) {
           *bad = 1;
           report_error(p.err, MGQA_ERR_INVALID_ARG);
         }
@@ -108,6 +120,7 @@ struct MmaCfg {
     Drafts<kMaxDrafts> drafts;
     LocateScratch<kThreads> scratch;
     float wm[WK][ROWS], wl[WK][ROWS];
+    RowOffsets off;
     uint8_t ok[STAGES][kTile];
     int bad, maxdepth;
   };
@@ -156,15 +169,27 @@ cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
     auto issue = [&](int i) {
       if (i < nt) {
         const int st = i % STAGES;
-        ld.issue(p, rp, g, t0 + i, tid, ring_a + st * 2 * Cfg::TILEB,
+        ld.issue(p, rp, t0 + i, tid, sm.off.at[i & 1], ring_a + st * 2 * Cfg::TILEB,
                  ring_a + st * 2 * Cfg::TILEB + Cfg::TILEB, sm.ok[st], &sm.bad, Cfg::at);
-        if (i + 1 < nt) ld.look_up(p, rp, b, t0 + i + 1, tid);
       }
       cp_async_commit();
     };
-    ld.look_up(p, rp, b, t0, tid);
+    auto look_up = [&](int i) {
+      if (i < nt) ld.look_up(p, rp, b, t0 + i, tid);
+    };
+    auto place = [&](int i) {  // (a barrier before tile i is issued, and one since tile i - 2 was)
+      if (i < nt) ld.place(p, rp, g, t0 + i, tid, sm.off.at[i & 1]);
+    };
+    look_up(0);
 #pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) issue(i);
+    for (int i = 0; i < STAGES - 1; ++i) {
+      place(i);
+      look_up(i + 1);
+      __syncthreads();
+      issue(i);
+    }
+    place(STAGES - 1);
+    look_up(STAGES);
 
     uint32_t qa[D / 16][4];
 #pragma unroll
@@ -209,6 +234,8 @@ cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
       cp_async_wait<STAGES - 2>();
       __syncthreads();  // tile i landed for everyone, and tile i - 1 has been read
       issue(i + STAGES - 1);
+      place(i + STAGES);
+      look_up(i + STAGES + 1);
       const int st = i % STAGES;
       const unsigned char *kt = ring + st * 2 * Cfg::TILEB, *vt = kt + Cfg::TILEB;
       const int key0 = wk * KW;  // this warp's keys of the tile
@@ -362,6 +389,7 @@ struct SimtCfg {
   struct Misc {
     Drafts<kMaxDrafts> drafts;
     LocateScratch<kSimtThreads> scratch;
+    RowOffsets off;
     uint8_t ok[STAGES][kTile];
     int bad, maxdepth;
   };
@@ -406,14 +434,25 @@ cache_attn_fp32_kernel(const __grid_constant__ CacheAttnParams p) {
     auto issue = [&](int i) {
       if (i < nt) {
         const int st = i % STAGES;
-        ld.issue(p, rp, g, t0 + i, tid, ring_a + st * 2 * Cfg::TILEF * 4,
+        ld.issue(p, rp, t0 + i, tid, sm.off.at[i & 1], ring_a + st * 2 * Cfg::TILEF * 4,
                  ring_a + (st * 2 + 1) * Cfg::TILEF * 4, sm.ok[st], &sm.bad, Cfg::at);
-        if (i + 1 < nt) ld.look_up(p, rp, b, t0 + i + 1, tid);
       }
       cp_async_commit();
     };
-    ld.look_up(p, rp, b, t0, tid);
+    auto look_up = [&](int i) {
+      if (i < nt) ld.look_up(p, rp, b, t0 + i, tid);
+    };
+    auto place = [&](int i) {  // (a barrier before tile i is issued, and one since tile i - 2 was)
+      if (i < nt) ld.place(p, rp, g, t0 + i, tid, sm.off.at[i & 1]);
+    };
+    look_up(0);
+    place(0);
+    look_up(1);
+    __syncthreads();
     issue(0);
+    place(1);
+    look_up(2);
+    __syncthreads();
     for (int u = tid; u < ROWS * (D / 4); u += kSimtThreads) {  // q, in log2 units
       const int r = u / (D / 4), d = (u % (D / 4)) * 4, row = row0 + r;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -455,6 +494,8 @@ cache_attn_fp32_kernel(const __grid_constant__ CacheAttnParams p) {
     }
     for (int i = 0; i < nt; ++i) {
       issue(i + 1);  // its buffer's readers passed the barrier that ends a tile
+      place(i + 2);
+      look_up(i + 3);
       cp_async_wait<1>();
       __syncthreads();
       const int st = i % STAGES;
