@@ -140,7 +140,7 @@ cache_attn_f32_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(sm.full + s, 2);
+      mbar_init(sm.full + s, full_count(tp));
       mbar_init(sm.empty + s, kConsumers / 32);
     }
     fence_mbarrier_init();
@@ -321,7 +321,7 @@ cache_attn_f32_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __gri
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(sm.full + s, 2);
+      mbar_init(sm.full + s, full_count(tp));
       mbar_init(sm.empty + s, kConsumers / 32);
     }
     fence_mbarrier_init();
@@ -469,10 +469,6 @@ mgqa_status launch_d(const CUtensorMap (&maps)[4], const TmaParams &tp, const Ca
 }
 
 }  // namespace
-
-bool cache_attn_f32_takes(const CacheAttnParams &p, mgqa_dtype dt) {
-  return dt == MGQA_FP32 && (!p.table || p.page_size % 8 == 0) && cache_attn_plain_strides(p);
-}
 
 mgqa_status launch_cache_attn_f32(const CacheAttnParams &p, int D, const CacheAttnLaunch &how, cudaStream_t s) {
   TmaParams tp{};

@@ -29,7 +29,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "cache_sched.cuh"
+#include "cache_producer.cuh"
 #include "tc_ptx.cuh"
 
 namespace mgqa {
@@ -212,10 +212,12 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     mbar_init(&sm.drain, 1);
     fence_mbarrier_init();
     tc::prefetch_tensormap(&tm_q);
-    tc::prefetch_tensormap(&tm_k);
-    tc::prefetch_tensormap(&tm_v);
-    tc::prefetch_tensormap(&tm_kn);
-    tc::prefetch_tensormap(&tm_vn);
+    if (tp.box_rows) {
+      tc::prefetch_tensormap(&tm_k);
+      tc::prefetch_tensormap(&tm_v);
+      tc::prefetch_tensormap(&tm_kn);
+      tc::prefetch_tensormap(&tm_vn);
+    }
   }
   if (warp == 1) tc::tmem_alloc(&sm.tmem, L::tmem_cols);
   if (warp == 2) touch_params(tp, lane);
@@ -241,12 +243,53 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     // (a box is issued by one lane at a time, ~80 cycles each: with pages of 8
     // slots the boxes of a whole tile took one warp longer than the reads)
     const bool of_v = warp == 3;
-    const int br = tp.box_rows, nbox = BN / br;
+    const int br = tp.box_rows, nbox = br ? BN / br : 0;
     uint64_t *full = of_v ? sm.vfull : sm.kfull, *empty = of_v ? sm.vempty : sm.kempty;
     unsigned char *buf = smem + (of_v ? L::v_off : L::k_off);
     const CUtensorMap *tm = of_v ? &tm_v : &tm_k, *tm_new = of_v ? &tm_vn : &tm_kn;
-    int it = 0;  // tiles issued
-    while (ok && walk.next(p, pc)) {
+    int it = 0;  // tiles issued as boxes
+    if (!br) {   // row by row
+      // (the tensor cores read what the copies wrote only behind a proxy fence of the
+      // copying threads, so a tile is told by its warp, when the next one has been
+      // started, or ahead of a wait)
+      RowFeed<KB, 2, kShift> feed;
+      int told = 0;
+      auto tell = [&](int upto) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        for (; told < upto; ++told)
+          if (lane == 0) mbar_arrive(full + told % STAGES);
+      };
+      while (ok && walk.next(p, pc)) {
+        feed.look_up(p, pc.rp, pc.b, pc.t0);
+        for (int t = pc.t0; t < pc.t1; ++t) {
+          const int st = it % STAGES, use = it / STAGES;
+          if (use > 0) {
+            const uint32_t parity = (uint32_t)(use - 1) & 1u;
+            if (!__all_sync(0xffffffffu, mbar_test_wait(empty + st, parity))) {
+              cp_async_wait<0>();
+              tell(it);
+              ok = __all_sync(0xffffffffu, mbar_wait(empty + st, parity, p.err));
+              if (!ok) break;
+            }
+          }
+          const auto now = feed;
+          if (t + 1 < pc.t1) feed.look_up(p, pc.rp, pc.b, t + 1);
+          uint32_t words[BN / 32];
+          now.issue(p, pc.rp, pc.g, t, of_v, buf + st * KB * BOX, words);
+          if (!of_v && lane == 0)
+            sm.ok[it % kOkRing] = make_uint4(words[0], words[1], BN == 64 ? 0xffffffffu : words[BN / 32 - 2],
+                                             BN == 64 ? 0xffffffffu : words[BN / 32 - 1]);
+          cp_async_commit();
+          cp_async_wait<1>();
+          tell(it++);
+        }
+      }
+      cp_async_wait<0>();  // (also: no copy is in flight when the CTA exits)
+      tell(it);
+      it = 0;
+    }
+    while (br && ok && walk.next(p, pc)) {
       const RowPlan &rp = pc.rp;
       auto look_up = [&](int t) {
         int kind;
@@ -374,12 +417,12 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         const int sv = at % STAGES;
         const bool has_next = n + 1 < nk;
         {  // values of keys that do not count: cleared (their rows may hold anything,
-           // but for those behind the drafts, which the copy fills with zeros)
+           // but for those behind the drafts, which a box fills with zeros)
           const uint4 okw = sm.ok[at % kOkRing];
           if (all_of(okw) != 0xffffffffu) {
             int kind;
             const int k0 = first_key(pc.rp, pc.t0 + n, kShift, kind);
-            const int rows = kind && pc.rp.live > k0 ? p.T - k0 : BN;
+            const int rows = tp.box_rows && kind && pc.rp.live > k0 ? p.T - k0 : BN;
 #pragma unroll
             for (int w = 0; w < BN / 32; ++w) {
               const uint32_t clear = ~word_of(okw, w) & low_mask(rows - 32 * w);
@@ -654,9 +697,8 @@ mgqa_status launch_d(const TcCacheParams &tp, mgqa_dtype dt, const CacheAttnLaun
 
 }  // namespace
 
-bool cache_attn_tc_takes(const CacheAttnParams &p, mgqa_dtype dt) {
-  return dt != MGQA_FP32 && (!p.table || p.page_size % 8 == 0) && p.n_rep <= BM && p.scale_log2 >= 0.f &&
-         cache_attn_plain_strides(p);
+bool cache_attn_tc_takes(const CacheAttnParams &p) {
+  return p.n_rep <= BM && p.scale_log2 >= 0.f && plain_strides(p.qs, p.B, p.Hq, p.T);
 }
 
 mgqa_status launch_cache_attn_tc(const CacheAttnParams &p, mgqa_dtype dt, int D, const CacheAttnLaunch &how,

@@ -21,6 +21,7 @@
 //   cluster barrier all of them join and write a part of the rows.
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 
 #include "cache_producer.cuh"
 
@@ -29,7 +30,6 @@ namespace {
 
 constexpr int kConsumers = 128;
 constexpr int kThreads = kConsumers + 64;
-constexpr int kMaxT = 64;  // R <= 64
 
 template <int D, int WM>
 struct Cfg {
@@ -47,7 +47,7 @@ struct Cfg {
     float join[WK > 1 ? (WK - 1) * WM : 1][16][WK > 1 ? 66 : 1];  // half a result of the warps that join
     float wm[WK][ROWS], wl[WK][ROWS];
     float2 ml[ROWS];  // the CTA's (m, l), read by its cluster
-    Drafts<kMaxT> drafts;
+    Drafts<WM == 4 ? kMaxDrafts : 32> drafts;  // (up to 32 rows: no more drafts)
     LocateScratch<kThreads> scratch;
     uint2 ok[STAGES];  // which keys of a stage's tile count
     uint64_t full[STAGES], empty[STAGES];
@@ -75,13 +75,15 @@ cache_attn_tma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
 
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(sm.full + s, 2);
+      mbar_init(sm.full + s, full_count(tp));
       mbar_init(sm.empty + s, 4);
     }
     fence_mbarrier_init();
-    tc::prefetch_tensormap(&tm_k);
-    tc::prefetch_tensormap(&tm_v);
-    if (p.tree) {
+    if (tp.box_rows) {
+      tc::prefetch_tensormap(&tm_k);
+      tc::prefetch_tensormap(&tm_v);
+    }
+    if (tp.box_rows && p.tree) {
       tc::prefetch_tensormap(&tm_kn);
       tc::prefetch_tensormap(&tm_vn);
     }
@@ -128,7 +130,9 @@ cache_attn_tma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         if (tid == 0) sm.maxdepth = 0;
         stage_drafts(p, sm.drafts, pc.b, rp.live, tid, kConsumers);
         named_sync(1, kConsumers);
-        if (tid < rp.live && sm.drafts.depth[tid]) atomicMax(&sm.maxdepth, sm.drafts.depth[tid]);
+        int md = 0;
+        for (int x = tid; x < rp.live; x += kConsumers) md = max(md, sm.drafts.depth[x]);
+        if (md) atomicMax(&sm.maxdepth, md);
         named_sync(1, kConsumers);
         staged = pc.b;
       }
@@ -389,17 +393,19 @@ mgqa_status launch_d(const CUtensorMap (&maps)[4], const TmaParams &tp, const Ca
 
 }  // namespace
 
-bool cache_attn_plain_strides(const CacheAttnParams &p) {
-  auto plain = [](const int64_t *st, int64_t n0, int64_t n1, int64_t n2) {
-    return (st[0] || n0 == 1) && (st[1] || n1 == 1) && (st[2] || n2 == 1);
-  };
-  const int pages = p.table ? p.num_pages : p.B, slots = p.table ? p.page_size : p.cap;
-  return plain(p.ks, pages, p.Hkv, slots) && plain(p.vs, pages, p.Hkv, slots) && plain(p.qs, p.B, p.Hq, p.T) &&
-         (!p.tree || (plain(p.kns, p.B, p.Hkv, p.T) && plain(p.vns, p.B, p.Hkv, p.T)));
+bool plain_strides(const int64_t *st, int64_t n0, int64_t n1, int64_t n2) {
+  return (st[0] || n0 == 1) && (st[1] || n1 == 1) && (st[2] || n2 == 1);
 }
 
 bool cache_attn_maps(const CacheAttnParams &p, mgqa_dtype dt, int D, int tile, CUtensorMap (&maps)[4], int &box_rows) {
   const int cols = dt == MGQA_FP32 ? 32 : 64;  // 128 bytes
+  const int n0 = p.table ? p.num_pages : p.B, n2 = p.table ? p.page_size : p.cap;
+  if ((p.table && p.page_size % 8) || !plain_strides(p.ks, n0, p.Hkv, n2) || !plain_strides(p.vs, n0, p.Hkv, n2) ||
+      (p.tree && (!plain_strides(p.kns, p.B, p.Hkv, p.T) || !plain_strides(p.vns, p.B, p.Hkv, p.T)))) {
+    box_rows = 0;
+    std::memset(maps, 0, sizeof(maps));
+    return true;
+  }
   box_rows = tile;
   if (p.table)
     for (; p.page_size % box_rows; box_rows /= 2) {}
@@ -413,12 +419,12 @@ bool cache_attn_maps(const CacheAttnParams &p, mgqa_dtype dt, int D, int tile, C
                      make_tma_map_4d(&maps[3], dt, p.vn, p.B, p.Hkv, p.T, D, p.vns, cols, tile, true));
 }
 
-// Up to 64 rows; past 32 only short calls, where a cluster saves a launch: on
+// Up to 32 rows; up to 64 for short calls, where a cluster saves a launch: on
 // longer ones the tensor-memory kernel is ahead (64 rows, 4 requests of up to
 // 131072: 305 us here, 234 us there; one request of up to 4096: 13 and 19 us).
+// And what that kernel does not take.
 bool cache_attn_tma_takes(const CacheAttnParams &p, mgqa_dtype dt, int D) {
-  if (dt == MGQA_FP32 || p.R > 64 || (p.table && p.page_size % 8) || !cache_attn_plain_strides(p)) return false;
-  return p.R <= 32 || short_call(p, D * 2) || !cache_attn_tc_takes(p, dt);
+  return p.R <= 32 || (p.R <= 64 && short_call(p, D * 2)) || !cache_attn_tc_takes(p);
 }
 
 mgqa_status launch_cache_attn_tma(const CacheAttnParams &p, mgqa_dtype dt, int D, const CacheAttnLaunch &how,

@@ -1,8 +1,12 @@
-// The producer warps (one for K, one for V) of the cache attention kernels that
-// fetch 64-key tiles by TMA: they follow the page table and issue every tile as
-// boxes that never cross a page into a ring of stages. (A box is issued by one
-// lane at a time, ~80 cycles each: with pages of 8 slots one warp for both was
-// slower than the reads.)
+// The producer warps (one for K, one for V) of the cache attention kernels: they
+// follow the page table and bring every tile into a ring of stages. Two ways:
+//   boxes (TMA) that never cross a page, where pages are a multiple of 8 slots. (A
+//     box is issued by one lane at a time, ~80 cycles each: with pages of 8 slots
+//     one warp for both was slower than the reads.)
+//   rows by 16-byte asynchronous copies, for any other page size and for tensors
+//     expanded over a dimension (TMA knows no stride of 0): a lane finds where its
+//     rows lie, the warp copies them into the boxes' own layout, so the consumers
+//     are the same. A copy costs ~8 instructions.
 #pragma once
 
 #include "cache_sched.cuh"
@@ -12,7 +16,7 @@ namespace mgqa {
 
 struct TmaParams {
   CacheAttnParams a;
-  int32_t box_rows;  // slots of a box of cached keys
+  int32_t box_rows;  // slots of a box of cached keys; 0: row by row
   int32_t cluster;   // CTAs of a unit's cluster; 0: equal runs
 };
 
@@ -57,6 +61,95 @@ struct Pieces {
   MGQA_DEV bool idle() const { return S && only.t0 >= only.t1; }  // a cluster's CTA without a share
 };
 
+// The rows of one tile of 2^SHIFT keys, for a whole warp. KB boxes of 64, 32 ...
+// columns (128 bytes) a row, elements of ES bytes.
+template <int KB, int ES, int SHIFT>
+struct RowFeed {
+  static constexpr int ROWS = 1 << SHIFT, RL = ROWS / 32;  // rows of a tile, of a lane
+  int page[RL];  // of this lane's rows of the tile that is issued next (-2: hidden, -1: not there)
+
+  // The pages of tile t, ahead of its issue.
+  MGQA_DEV void look_up(const CacheAttnParams &p, const RowPlan &rp, int b, int t) {
+    int kind;
+    const int k0 = first_key(rp, t, SHIFT, kind) + (int)(threadIdx.x & 31);
+#pragma unroll
+    for (int s = 0; s < RL; ++s) {
+      const int j = k0 + 32 * s;
+      page[s] = wanted(rp, kind, j) ? (kind ? b : page_of(p, b, j)) : -2;
+    }
+  }
+  // Starts the copies of the looked-up tile t to dst (boxes of ROWS x 128 bytes,
+  // 128-byte swizzled); words: which rows count. The others' rows are left as
+  // they are.
+  MGQA_DEV void issue(const CacheAttnParams &p, const RowPlan &rp, int g, int t, int of_v, unsigned char *dst,
+                      uint32_t (&words)[RL]) const {
+    const int lane = threadIdx.x & 31;
+    int kind;
+    const int k0 = first_key(rp, t, SHIFT, kind);
+    const int64_t *st = kind ? (of_v ? p.vns : p.kns) : (of_v ? p.vs : p.ks);
+    const char *base = static_cast<const char *>(kind ? (of_v ? p.vn : p.kn) : (of_v ? p.v : p.k));
+    const int c = lane & 7;  // 16-byte piece of 128 bytes
+#pragma unroll
+    for (int s = 0; s < RL; ++s) {
+      if (page[s] == -1) report_error(p.err, MGQA_ERR_INVALID_ARG);
+      const int j = k0 + 32 * s + lane;
+      const int64_t at = (int64_t)page[s] * st[0] + (int64_t)g * st[1] + (int64_t)(kind ? j : slot_in_page(p, j)) * st[2];
+      const unsigned long long row = reinterpret_cast<unsigned long long>(base) + (unsigned long long)(at * ES);
+      const uint32_t word = words[s] = __ballot_sync(0xffffffffu, page[s] >= 0);
+      if (word == 0u) continue;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {  // four rows a pass, eight lanes (a line of 128 bytes) each
+        const int r = 4 * u + lane / 8;
+        const char *src = reinterpret_cast<const char *>(__shfl_sync(0xffffffffu, row, r)) + c * 16;
+        if ((word >> r) & 1u)
+#pragma unroll
+          for (int k = 0; k < KB; ++k)
+            cp_async16(dst + k * (ROWS * 128) + (32 * s + r) * 128 + ((c ^ (r & 7)) << 4), src + k * 128);
+      }
+    }
+  }
+};
+
+// Arrivals on a stage's full barrier: K's and V's warp, box by box; every lane of
+// both when its copies have landed, and K's first lane, row by row.
+MGQA_DEV int full_count(const TmaParams &tp) { return tp.box_rows ? 2 : 65; }
+
+// As produce_tiles, row by row.
+template <int KB, int COLS, int STAGES>
+MGQA_DEV void produce_rows(const TmaParams &tp, Pieces pieces, int of_v, unsigned char *ring, uint2 *ok_words,
+                           uint64_t *full, uint64_t *empty) {
+  constexpr int TILEB = KB * kTile * 128;
+  const CacheAttnParams &p = tp.a;
+  const int lane = threadIdx.x & 31;
+  RowFeed<KB, 128 / COLS, 6> feed;
+  bool ok = true;
+  int it = 0;  // tiles started
+  Piece pc;
+  const bool teller = !of_v && lane == 0 && !pieces.S;
+  if (teller) tell_cut(p, blockIdx.x, nullptr);
+  while (ok && pieces.next(p, pc)) {
+    if (teller) tell_cut(p, blockIdx.x, &pc);
+    feed.look_up(p, pc.rp, pc.b, pc.t0);
+    for (int t = pc.t0; t < pc.t1; ++t, ++it) {
+      const int st = it % STAGES, use = it / STAGES;
+      if (use > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(empty + st, (use - 1) & 1, p.err));
+        if (!ok) break;
+      }
+      const auto now = feed;
+      if (t + 1 < pc.t1) feed.look_up(p, pc.rp, pc.b, t + 1);
+      uint32_t words[2];
+      now.issue(p, pc.rp, pc.g, t, of_v, ring + (st * 2 + of_v) * TILEB, words);
+      cp_async_arrive(full + st);
+      if (!of_v && lane == 0) {
+        ok_words[st] = make_uint2(words[0], words[1]);
+        mbar_arrive(full + st);
+      }
+    }
+  }
+  cp_async_wait_all();  // no copy may be in flight when the CTA exits
+}
+
 // A whole warp, for K (of_v 0) or V. A tile of either in the ring is KB boxes of
 // 64 rows x 128 bytes (COLS elements), 128-byte swizzled. Both warps arrive on
 // full[stage] (count 2); K's also writes which keys count to ok_words[stage].
@@ -64,6 +157,10 @@ template <int KB, int COLS, int STAGES>
 MGQA_DEV void produce_tiles(const TmaParams &tp, Pieces pieces, int of_v, const CUtensorMap *tm,
                             const CUtensorMap *tm_new, unsigned char *ring, uint2 *ok_words, uint64_t *full,
                             uint64_t *empty) {
+  if (!tp.box_rows) {
+    produce_rows<KB, COLS, STAGES>(tp, pieces, of_v, ring, ok_words, full, empty);
+    return;
+  }
   constexpr int BOXB = kTile * 128, TILEB = KB * BOXB;
   const CacheAttnParams &p = tp.a;
   const int lane = threadIdx.x & 31;

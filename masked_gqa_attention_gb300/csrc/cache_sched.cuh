@@ -78,22 +78,22 @@ inline void set_partials(CacheAttnParams &p, void *ws, int grid, int block_rows,
 
 mgqa_status launch_cache_merge(const CacheAttnParams &p, mgqa_dtype dt, int D, int block_rows, int grid,
                                cudaStream_t s);
-// TMA-fed kernels (16-bit; slots, or pages of a multiple of 8 slots; few rows).
+// 16 bits on mma.sync: few rows, or any (in blocks of 64).
 bool cache_attn_tma_takes(const CacheAttnParams &p, mgqa_dtype dt, int D);
 mgqa_status launch_cache_attn_tma(const CacheAttnParams &p, mgqa_dtype dt, int D, const CacheAttnLaunch &how,
                                   cudaStream_t s);
-// fp32 on the CUDA cores (the same caches).
-bool cache_attn_f32_takes(const CacheAttnParams &p, mgqa_dtype dt);
+// fp32 on the CUDA cores.
 mgqa_status launch_cache_attn_f32(const CacheAttnParams &p, int D, const CacheAttnLaunch &how, cudaStream_t s);
-// Tensor-memory kernel (the same caches, more rows).
-bool cache_attn_tc_takes(const CacheAttnParams &p, mgqa_dtype dt);
+// 16 bits in tensor memory, for more rows.
+bool cache_attn_tc_takes(const CacheAttnParams &p);
 mgqa_status launch_cache_attn_tc(const CacheAttnParams &p, mgqa_dtype dt, int D, const CacheAttnLaunch &how,
                                  cudaStream_t s);
-// Whether TMA can describe the call's tensors: a stride of 0 (a broadcast) over
-// more than one element it cannot.
-bool cache_attn_plain_strides(const CacheAttnParams &p);
+// Whether TMA can describe a tensor of [n0][n1][n2] rows: a stride of 0 (a
+// broadcast) over more than one element it cannot.
+bool plain_strides(const int64_t *st, int64_t n0, int64_t n1, int64_t n2);
 // Tensor maps of the cache (boxes of `box_rows` slots: the largest power of two
-// up to `tile` that divides the page) and of the drafts.
+// up to `tile` that divides the page) and of the drafts; box_rows 0: the call is
+// fetched row by row, without maps.
 bool cache_attn_maps(const CacheAttnParams &p, mgqa_dtype dt, int D, int tile, CUtensorMap (&maps)[4], int &box_rows);
 
 // What one request's queries may see.

@@ -438,6 +438,11 @@ MGQA_DEV void cp_async_wait_all() {
   asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
 }
 // Close the group of this thread's copies issued since the last commit.
+// An arrival of this thread on an mbarrier (one of its count) once every copy that
+// it has started has landed.
+MGQA_DEV void cp_async_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 MGQA_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Wait until at most N of this thread's committed groups are still in flight.
 template <int N> MGQA_DEV void cp_async_wait() {

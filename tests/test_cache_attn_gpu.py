@@ -218,6 +218,22 @@ def test_many_rows(M, dtype):
     Case([9000, 20], 70, 24, 8, 128, dtype, page=0).run(M)
 
 
+@pytest.mark.parametrize("dtype,D", [(BF, 128), (HF, 64), (FP, 64), (FP, 128)])
+@pytest.mark.parametrize("page", [1, 3, 20])
+def test_odd_pages(M, page, dtype, D):
+    # rows fetched one by one: few and many rows, short calls and long ones, windows, live drafts, scales
+    Case([5, 0, 333, 64], 3, 8, 2, D, dtype, page=page).run(M)
+    Case([700, 129], 40, 8, 2, D, dtype, page=page, live=[40, 9]).run(M)
+    Case([200, 1], 130, 4, 2, D, dtype, page=page, window=70, sinks=3).run(M)
+    Case([900, 333], 20, 8, 2, D, dtype, page=page, scale=-0.2).run(M)
+    Case([30000, 700], 8, 16, 2, D, dtype, page=page, cap=60000 // page * page).run(M)
+
+
+def test_odd_pages_long(M):
+    Case([40000, 39000, 33, 40001], 64, 32, 8, 128, BF, page=5, cap=200000).run(M)
+    Case([300, 100], 100, 8, 2, 64, FP, page=1, cap=300000, window=50).run(M)
+
+
 def test_large_trees_over_long_rows(M):
     # reads past the size where two row blocks share the key tiles
     Case([40000, 39000, 33, 40001], 64, 64, 16, 128, BF, page=64, cap=40100).run(M)
@@ -280,10 +296,10 @@ def test_other_layouts(M, dtype):
 @pytest.mark.parametrize("dtype", [BF, FP])
 def test_broadcast_tensors(M, dtype):
     # one row of drafts for the whole batch, one mask for every request
-    for T in (5, 40):
+    for T, names in ((5, ("kn", "vn", "q")), (40, ("kn", "vn", "q")), (70, ("kn", "vn"))):
         c = Case([100, 300], T, 4, 2, 64, dtype, page=16)
         d = Case([100, 300], T, 4, 2, 64, dtype, page=16)
-        for name in ("kn", "vn", "q"):
+        for name in names:
             x = getattr(c, name)[:1]
             setattr(c, name, x.expand(2, -1, -1, -1))
             setattr(d, name, x.expand(2, -1, -1, -1).contiguous())
