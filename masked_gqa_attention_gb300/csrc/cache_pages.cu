@@ -69,6 +69,10 @@ struct AppendParams {
   int32_t block_rows;  // new rows of a block
   const int32_t *index, *count;
   int32_t *kv_len_out;
+  // kv_len and kv_len_out share no 128-byte line. Otherwise kv_len is read past the
+  // L1: the next kernel is resident before this one ends, and a line left there
+  // could give it an old kv_len_out. (Read so always, 32768 rows take 46 us, not 42.)
+  int32_t lens_apart;
 };
 
 __global__ void __launch_bounds__(kAppendThreads)
@@ -78,9 +82,7 @@ append_kernel(const __grid_constant__ AppendParams p) {
   grid_dependency_wait();
   allow_dependents();
   const int64_t cap = c.table ? (int64_t)c.max_pages * c.page_size : c.page_size;
-  // (past the L1: a line of it that also holds kv_len_out must not be there when
-  // the next kernel, already resident, reads the new lengths)
-  const int n = __ldcg(c.kv_len + b);
+  const int n = p.lens_apart ? __ldg(c.kv_len + b) : __ldcg(c.kv_len + b);
   const int cnt = p.count ? __ldg(p.count + b) : p.T;
   const bool bad = n < 0 || cnt < 0 || cnt > p.T || (int64_t)n + cnt > cap;
   // the block's rows from t0 on, all heads of each. Without a count the new rows
@@ -542,7 +544,7 @@ compact_apply_kernel(const __grid_constant__ CompactParams p) {
   };
   for (int64_t u = t0; u < (int64_t)c.rows * c.max_pages; u += ts) {
     const int r = (int)(u / c.max_pages), j = (int)(u % c.max_pages);
-    int e = __ldcg(c.table + (int64_t)r * c.table_stride + j);  // (past the L1, as append's lengths)
+    int e = __ldcg(c.table + (int64_t)r * c.table_stride + j);  // (past the L1, as append's lengths when they share a line)
     if (e >= c.num_pages || e < -1) {
       report_error(c.err, MGQA_ERR_INVALID_ARG);
       e = -1;
@@ -596,6 +598,8 @@ mgqa_status launch_cache_append(const mgqa_cache &c, const void *k_new, const vo
     p.vns[t] = vs[t] * es;
   }
   p.T = T; p.index = index; p.count = count; p.kv_len_out = kv_len_out;
+  const uintptr_t line = 128, in = reinterpret_cast<uintptr_t>(c.kv_len), to = reinterpret_cast<uintptr_t>(kv_len_out);
+  p.lens_apart = (in + 4 * (uintptr_t)c.rows - 1) / line < to / line || (to + 4 * (uintptr_t)c.rows - 1) / line < in / line;
   const int64_t per = (int64_t)c.Hkv * p.c.pieces;
   if (per > (1 << 20)) return fail(MGQA_ERR_UNSUPPORTED, "cache append: rows of more than 16 MB");
   p.block_rows = (int32_t)std::max<int64_t>(1, kAppendThreads / per);
