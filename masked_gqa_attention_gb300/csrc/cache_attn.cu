@@ -13,14 +13,11 @@
 //
 // What bounds it: every visible key and value row is read once per KV head,
 // 4 R D operations per key for its R = T * Hq / Hkv query rows, so up to about
-// R = 64 the reads are the floor. K and V rows arrive by 16-byte asynchronous
-// copies, one page lookup per row and no rule on the page size, into a ring of
-// tiles; rows are stored with their 16-byte pieces exchanged (piece ^ row % 8),
-// which makes every matrix load conflict-free.
-//   16-bit: the products on mma.sync (m16n8k16). A CTA holds 16, 32 or 64 rows;
-//     with 16 or 32 rows its four warps split each tile's keys, so a single
-//     token's few rows still use the whole CTA, and join once at the end.
-//   fp32: the CUDA cores, register tiles of 1 x 4 or 4 x 4 scores per thread.
+// R = 64 the reads are the floor, and beyond a few hundred the products. Three
+// kernels, by the type and R (launch_cache_attn): cache_attn_tma.cu (mma.sync),
+// cache_attn_tc.cu (tensor memory), cache_attn_f32.cu (CUDA cores); all over
+// slots or pages of any size. This file picks one and has the kernel that joins
+// the partial results.
 #include <algorithm>
 #include <cmath>
 
@@ -34,8 +31,8 @@ namespace {
 constexpr int kMergeThreads = 128;
 
 // Block (unit or run, 16 rows, 32 features): joins the pieces of the unit, if it
-// was cut, in the order of the runs. A thread has four features of a
-// row; partial results are read in runs of 16 rows x 16 bytes.
+// was cut, in the order of the runs. A thread has four features of a row; partial
+// results are read in runs of 16 rows x 16 bytes.
 template <typename T, int D, int BR>
 __global__ void __launch_bounds__(kMergeThreads)
 cache_merge_kernel(const __grid_constant__ CacheAttnParams p) {

@@ -1,15 +1,15 @@
-// The fp32 cache attention over slots, or pages of a multiple of 8 slots: the
-// formulas of cache_attn.cu on the CUDA cores (single-precision accuracy rules
-// the tensor cores out), with the tiles, the two ways to cut the work and the
-// producer warps of cache_attn_tma.cu.
+// The fp32 cache attention: the formulas of cache_attn.cu on the CUDA cores
+// (single-precision accuracy rules the tensor cores out), with the tiles, the two
+// ways to cut the work and the producer warps of cache_attn_tma.cu.
 //
-// A key is 8 D bytes and 4 R D operations: up to R = 8 or so the reads bound it,
-// beyond that the fp32 rate. Two forms:
+// A key is 8 D bytes and 4 R D operations: up to R = 4 the reads bound it (64 rows
+// of up to 32768 slots, window 4096, R = 4: 329 us, 90 % of the copy rate; R = 8:
+// 640), beyond that the CUDA cores. Two forms:
 //   16 rows or fewer: a thread has 4 rows and one key of the scores (a quarter,
 //     half or all of the head dim), then 4 rows and 4 features of the values
 //     (every 8th, 4th or 2nd key), so each K and V element is read from shared
 //     memory once per 4 rows; two block barriers a tile.
-//   32 or 64 rows: the register tiles of simt_fp32.cuh, no block barrier.
+//   32 or 64 rows: the register tiles of simt_fp32.cuh.
 #include <algorithm>
 #include <cmath>
 
@@ -58,24 +58,28 @@ struct FewCfg {
     uint64_t full[STAGES], empty[STAGES];
     int maxdepth;
   };
+  static constexpr int threads = kThreads;
   static constexpr int smem = ring + (int)sizeof(Misc) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory");
 };
 
 // ---- 32 or 64 rows ---------------------------------------------------------------------
 
-template <int D, int RPT>
+template <int D, int RPG>
 struct ManyCfg {
-  static constexpr int ROWS = 16 * RPT;
+  static constexpr int ROWS = 8 * RPG;
   static constexpr int STAGES = 131072 / (2 * Ring<D>::TILEB);
   static constexpr int ring = STAGES * 2 * Ring<D>::TILEB;
-  static constexpr int QP = D + 4, WP = 2 * kTile + 4, OP = D + 4;
+  static constexpr int QP = D + 4, OP = D + 4;
+  // a third warpgroup with the producers gives its registers to the two others
+  // (104 + 2 x 200 = 3 x 168, the launch's)
+  static constexpr int threads = kConsumers + 128;
   struct Misc {
     float q[ROWS][QP];
-    float w[ROWS][WP];
+    simt::Shared<ROWS, D> sh;
     float2 ml[ROWS];
     Drafts<kMaxDrafts> drafts;
-    LocateScratch<kThreads> scratch;
+    LocateScratch<threads> scratch;
     uint2 ok[STAGES];
     uint64_t full[STAGES], empty[STAGES];
     int maxdepth;
@@ -307,12 +311,12 @@ cache_attn_f32_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid
   if (pieces.S) join_cluster<float, D, ROWS, C::OP, kConsumers>(p, pieces, sm.ml, reinterpret_cast<const float *>(ring));
 }
 
-template <int D, int RPT>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int RPG>
+__global__ void __launch_bounds__(kConsumers + 128, 1)
 cache_attn_f32_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                            const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_vn,
                            const __grid_constant__ TmaParams tp) {
-  using C = ManyCfg<D, RPT>;
+  using C = ManyCfg<D, RPG>;
   constexpr int ROWS = C::ROWS, STAGES = C::STAGES, TILEB = Ring<D>::TILEB;
   const CacheAttnParams &p = tp.a;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -330,14 +334,17 @@ cache_attn_f32_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __gri
   grid_dependency_wait();
   allow_dependents();
   Pieces pieces{};
-  pieces.start<kThreads>(tp, sm.scratch);
+  pieces.start<C::threads>(tp, sm.scratch);
   if (warp >= kConsumers / 32) {
+    tc::regs_dec<104>();
     const int of_v = warp - kConsumers / 32;
-    produce_tiles<Ring<D>::KB, 32, STAGES>(tp, pieces, of_v, of_v ? &tm_v : &tm_k, of_v ? &tm_vn : &tm_kn, ring,
-                                           sm.ok, sm.full, sm.empty);
+    if (of_v < 2)
+      produce_tiles<Ring<D>::KB, 32, STAGES>(tp, pieces, of_v, of_v ? &tm_v : &tm_k, of_v ? &tm_vn : &tm_kn, ring,
+                                             sm.ok, sm.full, sm.empty);
   } else {
+    tc::regs_inc<200>();
     if (pieces.idle() && tid < ROWS) sm.ml[tid] = make_float2(-INFINITY, 0.f);
-    const int tx = tid & 15, ty = tid >> 4;
+    const simt::Place at(tid);
     bool ok = true;
     int it = 0, staged = -1;
     Piece pc;
@@ -345,75 +352,58 @@ cache_attn_f32_many_kernel(const __grid_constant__ CUtensorMap tm_k, const __gri
       const RowPlan &rp = pc.rp;
       const PieceOut po = out_of(p, pc, blockIdx.x);
       const bool need = begin_piece<D, ROWS, C::QP>(p, pc, po.row0, &sm.q[0][0], sm.drafts, sm.maxdepth, staged);
-      RowSight sight[RPT];
-      float m[RPT], l[RPT];
-      uint64_t o[RPT][D / 64][2];
+      RowSight sight[RPG / 2];
+      float m[RPG / 2], l[RPG / 2];
+      uint64_t o[RPG][D / 64][2];
 #pragma unroll
-      for (int a = 0; a < RPT; ++a) {
-        sight[a] = sight_of(p, pc, po.row0 + ty + 16 * a, need, sm.drafts);
+      for (int a = 0; a < RPG / 2; ++a) {
+        sight[a] = sight_of(p, pc, po.row0 + at.own<RPG>(a), need, sm.drafts);
         m[a] = -INFINITY;
         l[a] = 0.f;
+      }
+#pragma unroll
+      for (int a = 0; a < RPG; ++a)
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) o[a][c][0] = o[a][c][1] = 0ull;
-      }
       const int lo_all = rp.n + (p.tree ? (need ? sm.maxdepth : 0) : -1) - p.window + 1;
       for (int t = pc.t0; t < pc.t1; ++t, ++it) {
         const int st = it % STAGES;
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(sm.full + st, (it / STAGES) & 1, p.err));
-        if (ok) {
-          const unsigned char *kt = ring + st * 2 * TILEB, *vt = kt + TILEB;
-          const uint2 okw = sm.ok[st];
-          float s[RPT][4];
-          simt::scores<D, RPT, C::QP>(s, &sm.q[0][0], kt, ty, tx);
-          int kind;
-          const int k0 = first_key(rp, t, 6, kind);
-          const bool full = !kind && (okw.x & okw.y) == 0xffffffffu &&
-                            (k0 >= lo_all || k0 + kTile <= min(p.sinks, rp.s_end));
-#pragma unroll
-          for (int a = 0; a < RPT; ++a) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int col = tx + 16 * c;
-              const bool see = full || (((col < 32 ? okw.x : okw.y) >> (col & 31) & 1u) &&
-                                        (kind ? sees_draft(p, sm.drafts, sight[a], rp.n, k0 + col)
-                                              : sees_cached(p, sight[a], k0 + col)));
-              s[a][c] = see ? s[a][c] * p.scale_log2 : -INFINITY;
-            }
-            const float f = simt::softmax_row(s[a], m[a], l[a], sm.w[ty + 16 * a], tx);
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-              o[a][c][0] = simt::mul2(o[a][c][0], f);
-              o[a][c][1] = simt::mul2(o[a][c][1], f);
-            }
-          }
-          __syncwarp();  // a row's weights come from the 16 lanes that read them
-          simt::values<D, RPT, C::WP>(o, &sm.w[0][0], vt, ty, tx, okw.x, okw.y);
-        }
+        const unsigned char *kt = ring + st * 2 * TILEB;
+        const uint2 okw = sm.ok[st];
+        int kind;
+        const int k0 = first_key(rp, t, 6, kind);
+        const bool full = !kind && (okw.x & okw.y) == 0xffffffffu &&
+                          (k0 >= lo_all || k0 + kTile <= min(p.sinks, rp.s_end));
+        simt::tile<D, RPG, C::QP>(ok, it & 1, &sm.q[0][0], kt, kt + TILEB, sm.sh, o, m, l, at, okw.x, okw.y,
+                                  [&](int a, int col, float s) {
+                                    const bool see =
+                                        full || (((col < 32 ? okw.x : okw.y) >> (col & 31) & 1u) &&
+                                                 (kind ? sees_draft(p, sm.drafts, sight[a], rp.n, k0 + col)
+                                                       : sees_cached(p, sight[a], k0 + col)));
+                                    return see ? s * p.scale_log2 : -INFINITY;
+                                  });
         __syncwarp();
         if (lane == 0) mbar_arrive(sm.empty + st);
       }
-      if (pieces.S) named_sync(1, kConsumers);  // every tile has been read: the ring takes the result
+      float x[RPG / 2][D / 64][4];
+      simt::finish<D, RPG>(sm.sh, o, l, x, at);  // (its barriers: every tile has been read, the ring takes the result)
 #pragma unroll
-      for (int a = 0; a < RPT; ++a) {
-        float ls = l[a];
-#pragma unroll
-        for (int off = 1; off < 16; off <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, off);
-        const int r = ty + 16 * a;
+      for (int a = 0; a < RPG / 2; ++a) {
+        const int r = at.own<RPG>(a);
         const bool none = !ok || !sight[a].ok || m[a] == -INFINITY;
-        const float2 ml = none ? make_float2(-INFINITY, 0.f) : make_float2(m[a], ls);
-        const RowOut<float, D, ROWS> dst(p, po, r < po.rows ? r : 0, ml.x, ml.y, !pieces.S && tx == 0 && r < po.rows);
-        if (pieces.S && tx == 0) sm.ml[r] = ml;
+        const float2 ml = none ? make_float2(-INFINITY, 0.f) : make_float2(m[a], l[a]);
+        const RowOut<float, D, ROWS> dst(p, po, r < po.rows ? r : 0, ml.x, ml.y,
+                                         !pieces.S && at.tx == 0 && r < po.rows);
+        if (pieces.S && at.tx == 0) sm.ml[r] = ml;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-          float x[4];
-          tc::upk2(o[a][c][0], x[0], x[1]);
-          tc::upk2(o[a][c][1], x[2], x[3]);
-          if (none) x[0] = x[1] = x[2] = x[3] = 0.f;
+          if (none) x[a][c][0] = x[a][c][1] = x[a][c][2] = x[a][c][3] = 0.f;
           if (pieces.S)
-            *reinterpret_cast<float4 *>(reinterpret_cast<float *>(ring) + r * C::OP + tx * 4 + 64 * c) =
-                make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4 *>(reinterpret_cast<float *>(ring) + r * C::OP + at.tx * 4 + 64 * c) =
+                make_float4(x[a][c][0], x[a][c][1], x[a][c][2], x[a][c][3]);
           else if (r < po.rows)
-            dst.put(tx * 4 + 64 * c, x);
+            dst.put(at.tx * 4 + 64 * c, x[a][c]);
         }
       }
     }
@@ -433,7 +423,7 @@ mgqa_status launch_t(Kern kern, std::atomic<uint64_t> &attr, const CUtensorMap (
   const int64_t units = (int64_t)p.B * p.Hkv * p.RB, tiles = most_tiles(p);
   tp.cluster = cluster_size(p, D * 4, how.sms);
   if (tp.cluster) {
-    const cudaError_t e = launch_pdl_cluster(kern, dim3((unsigned)(units * tp.cluster)), dim3(kThreads), C::smem, s,
+    const cudaError_t e = launch_pdl_cluster(kern, dim3((unsigned)(units * tp.cluster)), dim3(C::threads), C::smem, s,
                                              tp.cluster, maps[0], maps[1], maps[2], maps[3], tp);
     if (e != cudaSuccess) return fail(MGQA_ERR_CUDA, "fp32 cache attention launch: %s", cudaGetErrorString(e));
     return MGQA_OK;
@@ -442,7 +432,7 @@ mgqa_status launch_t(Kern kern, std::atomic<uint64_t> &attr, const CUtensorMap (
   p.min_run = 4;
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(how.sms, kCacheAttnMaxCtas), units * (tiles + lead)));
   set_partials(p, how.workspace, grid, C::ROWS, D);
-  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kThreads), C::smem, s, maps[0], maps[1], maps[2], maps[3], tp);
+  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(C::threads), C::smem, s, maps[0], maps[1], maps[2], maps[3], tp);
   if (e != cudaSuccess) return fail(MGQA_ERR_CUDA, "fp32 cache attention launch: %s", cudaGetErrorString(e));
   return launch_cache_merge(p, MGQA_FP32, D, C::ROWS, grid, s);
 }
@@ -452,10 +442,10 @@ mgqa_status launch_few(const CUtensorMap (&maps)[4], const TmaParams &tp, const 
   static std::atomic<uint64_t> attr{0};
   return launch_t<D, FewCfg<D, RG>>(cache_attn_f32_few_kernel<D, RG>, attr, maps, tp, 3, how, s);
 }
-template <int D, int RPT>
+template <int D, int RPG>
 mgqa_status launch_many(const CUtensorMap (&maps)[4], const TmaParams &tp, const CacheAttnLaunch &how, cudaStream_t s) {
   static std::atomic<uint64_t> attr{0};
-  return launch_t<D, ManyCfg<D, RPT>>(cache_attn_f32_many_kernel<D, RPT>, attr, maps, tp, 1, how, s);
+  return launch_t<D, ManyCfg<D, RPG>>(cache_attn_f32_many_kernel<D, RPG>, attr, maps, tp, 1, how, s);
 }
 
 template <int D>
@@ -464,8 +454,8 @@ mgqa_status launch_d(const CUtensorMap (&maps)[4], const TmaParams &tp, const Ca
   if (R <= 4) return launch_few<D, 1>(maps, tp, how, s);
   if (R <= 8) return launch_few<D, 2>(maps, tp, how, s);
   if (R <= 16) return launch_few<D, 4>(maps, tp, how, s);
-  if (R <= 32) return launch_many<D, 2>(maps, tp, how, s);
-  return launch_many<D, 4>(maps, tp, how, s);
+  if (R <= 32) return launch_many<D, 4>(maps, tp, how, s);
+  return launch_many<D, 8>(maps, tp, how, s);
 }
 
 }  // namespace

@@ -1,14 +1,17 @@
-// The 16-bit cache attention for more than 64 query rows per KV head (trees of
-// drafted tokens over grouped heads): the formulas of cache_attn.cu on the
-// 5th-generation tensor cores, over slots or pages of a multiple of 8 slots.
+// The 16-bit cache attention for more than 32 query rows per KV head (trees of
+// drafted tokens over grouped heads; short calls of up to 64 rows excepted): the
+// formulas of cache_attn.cu on the 5th-generation tensor cores.
 //
 // With R rows per KV head a key costs 4 R D operations for its 4 D bytes: at
 // R = 256 the products take about as long as the reads, and mma.sync reaches a
 // fraction of the tensor rate, so here the scores and outputs live in tensor
 // memory. A CTA holds NT blocks of up to 128 query rows (row = draft * group +
-// head, so a tile of keys serves every head of the group) and walks
-// its run of the flat tile list (cache_sched.cuh), one CTA an SM:
-//   warps 0, 3  : follow the page table, K and V boxes of 128-key tiles by TMA
+// head, so a tile of keys serves every head of the group) and walks its run of
+// the flat tile list (cache_sched.cuh). Two forms, by a rule at launch_d:
+//   NT = 1: tiles of 64 keys, two score buffers, two CTAs an SM;
+//   NT = 2: tiles of 128 keys, one CTA an SM.
+// Warps:
+//   warps 0, 3  : K and V, as boxes by TMA or row by row (cache_producer.cuh)
 //   warp 1      : tensor memory, the MMA loop (one elected lane issues)
 //   warp 2      : the query rows of the next piece, as soon as the last S of
 //                 the current one is done, and its description for the others
@@ -17,14 +20,16 @@
 // rescale of O_t past 2^8) hands P_t over in tensor memory; O_t += P_t V_n.
 // With two row blocks S_t(n+1) follows O_t += P_t V_n at once and the blocks
 // take turns on the tensor cores and the softmax warps, as the heads in the
-// prefill kernel. With one row block S has two buffers instead, and S(n+1) runs
-// under the softmax of tile n (S behind P V, the chain of softmax, P V and S took
-// 3000 cycles a tile, more than the reads'). Between two pieces the softmax
-// warpgroups read O_t out while the next query rows, K and V are on their way.
-// (The softmax warps loading the rows themselves, between the pieces, cost ~4000
-// cycles a piece, and their walk over the pieces the registers of the score row.) Values of keys that do not
+// prefill kernel. With one row block S(n+1) runs under the softmax of tile n (S
+// behind P V, the chain of softmax, P V and S took longer than the reads).
+// Between two pieces the softmax warpgroups read O_t out while the next query
+// rows, K and V are on their way. (The softmax warps loading the rows themselves,
+// between the pieces, cost ~4000 cycles a piece.) Values of keys that do not
 // count (the end of a request, a missing page) are cleared in shared memory by
 // the MMA warp before the product, on the tiles that have any.
+// The reads bound long calls (61 drafts, 4 requests of up to 131072 slots, 32
+// heads over 8, NT = 2: 269 us, 88 % of the copy rate); ragged batches lose the
+// start and the join (24 drafts, 16 requests of up to 8192, NT = 1: 62 us, 65 %).
 // Every wait is bounded and reports MGQA_ERR_TIMEOUT.
 #include <algorithm>
 #include <cmath>
@@ -38,7 +43,7 @@ namespace {
 constexpr int BM = 128;
 constexpr int QBOX = BM * 128;  // bytes of 128 query rows x 64 columns, 128-byte swizzled
 constexpr int kPieceRing = 4;  // a piece's slot is taken again after the S of the third piece behind it
-constexpr int kOkRing = 8;     // tiles whose key masks are kept: the producer is at most 4 ahead of a softmax
+constexpr int kOkRing = 8;     // tiles whose key masks are kept: K's producer is at most STAGES + 1 ahead of a softmax
 
 struct TcCacheParams {
   CacheAttnParams a;

@@ -10,8 +10,9 @@
 // the CTAs cut into equal runs. Rows of very different lengths so cost every
 // CTA the same, whatever the batch. A unit inside one run is finished by its
 // CTA; a unit that crosses a run's end leaves one partial result per run in the
-// workspace, and the merge kernel joins them in ascending order. The cut depends on the lengths, the
-// call's shapes and the device alone, so results repeat bit for bit.
+// workspace, and the merge kernel joins them in ascending order. The cut depends
+// on the lengths, the call's shapes and the device alone, so results repeat bit
+// for bit.
 #pragma once
 
 #include "common.cuh"
@@ -19,7 +20,7 @@
 
 namespace mgqa {
 
-constexpr int kTile = 64;        // keys of a tile of the mma.sync and CUDA-core kernels
+constexpr int kTile = 64;  // keys of a tile (but for the tensor-memory kernel's larger form)
 constexpr int kMaxDrafts = kMaxDraftsHost;
 constexpr int kNoWindow = 1 << 30;
 

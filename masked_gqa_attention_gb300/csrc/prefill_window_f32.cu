@@ -4,10 +4,11 @@
 // of keys shared by 64 queries, so the fp32 rate bounds it. CTA = 64 query rows
 // of one head; a producer warp fetches the 64-key tiles that the window and the
 // sinks reach (TMA boxes, two stages at D = 128), 256 threads run the register
-// tiles of simt_fp32.cuh, whose rows need no block barrier; partial tiles take
-// their mask words from shared memory. (The unwindowed fp32 prefill keeps its
-// kernel of four threads per row: 4096 queries x 16 heads, window 4096, took
-// 5.2 ms with it.)
+// tiles of simt_fp32.cuh; partial tiles take their mask words from shared memory.
+// The last rows, which have the most keys under a causal limit, start first
+// (4096 queries x 16 heads, window 4096: 1854 us, in rising order 2153). (The
+// unwindowed fp32 prefill keeps its kernel of four threads per row, which took
+// 5.2 ms of that.)
 #include <algorithm>
 #include <cmath>
 
@@ -18,8 +19,8 @@ namespace mgqa {
 namespace {
 
 constexpr int kConsumers = 256;
-constexpr int kThreads = kConsumers + 32;
-constexpr int kRPT = 4, kRows = 16 * kRPT;
+constexpr int kThreads = kConsumers + 128;  // (a warpgroup for the producer, whose registers the others get)
+constexpr int kRPG = 8, kRows = 8 * kRPG;
 
 struct WinParams {
   const float *q;
@@ -38,10 +39,10 @@ struct WinCfg {
   static constexpr int TILEB = KB * simt::kBox;
   static constexpr int STAGES = 131072 / (2 * TILEB);
   static constexpr int ring = STAGES * 2 * TILEB;
-  static constexpr int QP = D + 4, WP = 2 * kTile + 4;
+  static constexpr int QP = D + 4;
   struct Misc {
     float q[kRows][QP];
-    float w[kRows][WP];
+    simt::Shared<kRows, D> sh;
     uint32_t mask[2][kRows][2];  // of alternating partial tiles
     uint64_t full[STAGES], empty[STAGES];
   };
@@ -59,7 +60,9 @@ prefill_window_f32_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid
   unsigned char *ring = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   auto &sm = *reinterpret_cast<typename C::Misc *>(ring + C::ring);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row0 = (int)blockIdx.x * kRows, h = blockIdx.y, b = blockIdx.z, g = h / p.n_rep;
+  // the last rows first: with a causal limit they have the most keys
+  const int qt = (int)gridDim.x / p.Hq - 1 - (int)blockIdx.x / p.Hq, h = (int)blockIdx.x % p.Hq, b = blockIdx.y;
+  const int row0 = qt * kRows, g = h / p.n_rep;
   const int rows = min(kRows, p.Lq - row0);
   // the tiles that the window leaves to these rows: the sinks' and the window's
   const int first = row0 + p.mask.coff, last = first + rows - 1, ntile = (p.Lk + kTile - 1) / kTile;
@@ -81,8 +84,9 @@ prefill_window_f32_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid
   __syncthreads();
   grid_dependency_wait();
   allow_dependents();
-  if (warp == kConsumers / 32) {
-    if (lane == 0) {
+  if (warp >= kConsumers / 32) {
+    tc::regs_dec<104>();
+    if (warp == kConsumers / 32 && lane == 0) {
       bool ok = true;
       int it = 0;
       for (; it < nt && ok; ++it) {
@@ -100,8 +104,9 @@ prefill_window_f32_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid
     }
     return;
   }
-  const int tx = tid & 15, ty = tid >> 4;
-  const int kvl = load_kv_len(p.mask.kv_len, b, p.Lk, p.err, blockIdx.x == 0 && h == 0 && tid == 0);
+  tc::regs_inc<200>();
+  const simt::Place at(tid);
+  const int kvl = load_kv_len(p.mask.kv_len, b, p.Lk, p.err, qt == 0 && h == 0 && tid == 0);
   const float *qb = p.q + (int64_t)b * p.qs[0] + (int64_t)h * p.qs[1];
 #pragma unroll
   for (int u = tid; u < kRows * (D / 4); u += kConsumers) {
@@ -115,15 +120,17 @@ prefill_window_f32_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid
       p.mask.seg_q && tid < 2 * kRows && mrow < p.Lq ? __ldg(p.mask.seg_q + (int64_t)b * p.Lq + mrow) : -1;
   named_sync(1, kConsumers);
 
-  float m[kRPT], l[kRPT];
-  uint64_t o[kRPT][D / 64][2];
+  float m[kRPG / 2], l[kRPG / 2];
+  uint64_t o[kRPG][D / 64][2];
 #pragma unroll
-  for (int a = 0; a < kRPT; ++a) {
+  for (int a = 0; a < kRPG / 2; ++a) {
     m[a] = -INFINITY;
     l[a] = 0.f;
+  }
+#pragma unroll
+  for (int a = 0; a < kRPG; ++a)
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) o[a][c][0] = o[a][c][1] = 0ull;
-  }
   bool ok = true;
   int parts = 0;  // partial tiles so far
   for (int t = 0; t < nt; ++t) {
@@ -142,50 +149,31 @@ prefill_window_f32_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid
       ++parts;
     }
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(sm.full + st, (t / STAGES) & 1, p.err));
-    if (ok) {
-      const unsigned char *kt = ring + st * 2 * TILEB, *vt = kt + TILEB;
-      float s[kRPT][4];
-      simt::scores<D, kRPT, C::QP>(s, &sm.q[0][0], kt, ty, tx);
-#pragma unroll
-      for (int a = 0; a < kRPT; ++a) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int col = tx + 16 * c;
-          const bool see = full || ((sm.mask[mb][ty + 16 * a][c >> 1] >> (col & 31)) & 1u);
-          s[a][c] = see ? s[a][c] * p.scale_log2 : -INFINITY;
-        }
-        const float f = simt::softmax_row(s[a], m[a], l[a], sm.w[ty + 16 * a], tx);
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          o[a][c][0] = simt::mul2(o[a][c][0], f);
-          o[a][c][1] = simt::mul2(o[a][c][1], f);
-        }
-      }
-      __syncwarp();  // a row's weights come from the 16 lanes that read them
-      // (values behind kv_len may hold anything)
-      simt::values<D, kRPT, C::WP>(o, &sm.w[0][0], vt, ty, tx, low_mask(kvl - k0), low_mask(kvl - k0 - 32));
-    }
+    const unsigned char *kt = ring + st * 2 * TILEB;
+    // (values behind kv_len may hold anything)
+    simt::tile<D, kRPG, C::QP>(ok, t & 1, &sm.q[0][0], kt, kt + TILEB, sm.sh, o, m, l, at, low_mask(kvl - k0),
+                               low_mask(kvl - k0 - 32), [&](int a, int col, float s) {
+                                 const bool see =
+                                     full || ((sm.mask[mb][at.own<kRPG>(a)][col >> 5] >> (col & 31)) & 1u);
+                                 return see ? s * p.scale_log2 : -INFINITY;
+                               });
     __syncwarp();
     if (lane == 0) mbar_arrive(sm.empty + st);
   }
+  float x[kRPG / 2][D / 64][4];
+  simt::finish<D, kRPG>(sm.sh, o, l, x, at);
 #pragma unroll
-  for (int a = 0; a < kRPT; ++a) {
-    float ls = l[a];
-#pragma unroll
-    for (int off = 1; off < 16; off <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, off);
-    const int i = row0 + ty + 16 * a;
+  for (int a = 0; a < kRPG / 2; ++a) {
+    const int i = row0 + at.own<kRPG>(a);
     if (i >= p.Lq) continue;
-    const float inv = ok && ls > 0.f ? 1.f / ls : 0.f;
+    const float inv = ok && l[a] > 0.f ? 1.f / l[a] : 0.f;
     float *orow = p.out + (int64_t)b * p.os[0] + (int64_t)h * p.os[1] + (int64_t)i * p.os[2];
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c) {
-      float x[4];
-      tc::upk2(o[a][c][0], x[0], x[1]);
-      tc::upk2(o[a][c][1], x[2], x[3]);
-      *reinterpret_cast<float4 *>(orow + tx * 4 + 64 * c) = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-    }
-    if (p.lse && tx == 0)
-      p.lse[((int64_t)b * p.Hq + h) * p.Lq + i] = inv > 0.f ? (m[a] + log2f(ls)) * kLn2 : -INFINITY;
+    for (int c = 0; c < D / 64; ++c)
+      *reinterpret_cast<float4 *>(orow + at.tx * 4 + 64 * c) =
+          make_float4(x[a][c][0] * inv, x[a][c][1] * inv, x[a][c][2] * inv, x[a][c][3] * inv);
+    if (p.lse && at.tx == 0)
+      p.lse[((int64_t)b * p.Hq + h) * p.Lq + i] = inv > 0.f ? (m[a] + log2f(l[a])) * kLn2 : -INFINITY;
   }
 }
 
@@ -200,7 +188,7 @@ mgqa_status launch_t(const mgqa_args &a, const WinParams &p, cudaStream_t s) {
   static std::atomic<uint64_t> attr{0};
   const mgqa_status st = ensure_smem_attr(kern, C::smem, attr, "fp32 windowed prefill");
   if (st != MGQA_OK) return st;
-  const cudaError_t e = launch_pdl(kern, dim3((a.Lq + kRows - 1) / kRows, a.Hq, a.B), dim3(kThreads), C::smem, s, mk, mv, p);
+  const cudaError_t e = launch_pdl(kern, dim3((unsigned)((a.Lq + kRows - 1) / kRows * a.Hq), a.B), dim3(kThreads), C::smem, s, mk, mv, p);
   if (e != cudaSuccess) return fail(MGQA_ERR_CUDA, "windowed prefill launch: %s", cudaGetErrorString(e));
   return MGQA_OK;
 }
