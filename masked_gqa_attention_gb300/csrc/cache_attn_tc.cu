@@ -183,7 +183,9 @@ MGQA_DEV void softmax_row(uint32_t t_s, uint32_t t_o, const uint32_t (&mw)[4], f
   tc::tmem_wait_st();
 }
 
-template <typename T, int D, int NT>
+// BOXES: K and V come as TMA boxes (else row by row: an instance of its own, the
+// code of both in one cost 2 %).
+template <typename T, int D, int NT, bool BOXES>
 __global__ void __launch_bounds__(128 * (1 + NT), NT == 1 ? 2 : 1)
 cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_vn,
@@ -217,7 +219,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     mbar_init(&sm.drain, 1);
     fence_mbarrier_init();
     tc::prefetch_tensormap(&tm_q);
-    if (tp.box_rows) {
+    if (BOXES) {
       tc::prefetch_tensormap(&tm_k);
       tc::prefetch_tensormap(&tm_v);
       tc::prefetch_tensormap(&tm_kn);
@@ -248,12 +250,12 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     // (a box is issued by one lane at a time, ~80 cycles each: with pages of 8
     // slots the boxes of a whole tile took one warp longer than the reads)
     const bool of_v = warp == 3;
-    const int br = tp.box_rows, nbox = br ? BN / br : 0;
+    const int br = tp.box_rows;
     uint64_t *full = of_v ? sm.vfull : sm.kfull, *empty = of_v ? sm.vempty : sm.kempty;
     unsigned char *buf = smem + (of_v ? L::v_off : L::k_off);
     const CUtensorMap *tm = of_v ? &tm_v : &tm_k, *tm_new = of_v ? &tm_vn : &tm_kn;
-    int it = 0;  // tiles issued as boxes
-    if (!br) {   // row by row
+    int it = 0;  // tiles issued
+    if constexpr (!BOXES) {
       // (the tensor cores read what the copies wrote only behind a proxy fence of the
       // copying threads, so a tile is told by its warp, when the next one has been
       // started, or ahead of a wait)
@@ -292,70 +294,64 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
       }
       cp_async_wait<0>();  // (also: no copy is in flight when the CTA exits)
       tell(it);
-      it = 0;
-    }
-    while (br && ok && walk.next(p, pc)) {
-      const RowPlan &rp = pc.rp;
-      auto look_up = [&](int t) {
-        int kind;
-        const int j0 = first_key(rp, t, kShift, kind) + lane * br;
-        const bool some = !kind && lane < nbox && j0 < rp.n && ((rp.lo < rp.n && j0 + br > rp.lo) || j0 < rp.s_end);
-        return some ? page_of(p, pc.b, j0) : -2;  // -1: a page that is not there
-      };
-      int page = look_up(pc.t0);
-      for (int t = pc.t0; t < pc.t1; ++t, ++it) {
-        const int next = t + 1 < pc.t1 ? look_up(t + 1) : -2;
-        int kind;
-        const int k0 = first_key(rp, t, kShift, kind);
-        const int j0 = k0 + lane * br;
-        uint32_t mine[4] = {0u, 0u, 0u, 0u};  // (a tile of 64 keys has two words)
-        bool take = false;
-        if (kind) {
-          take = lane == 0 && rp.live > k0;
-          if (lane == 0)
+    } else {
+      BoxPages pages;
+      while (ok && walk.next(p, pc)) {
+        const RowPlan &rp = pc.rp;
+        pages.start(p, pc, kShift, br);
+        for (int t = pc.t0; t < pc.t1; ++t, ++it) {
+          const int page = pages.page(p, pc, kShift, br, t);  // (lane i: box i of the tile)
+          int kind;
+          const int k0 = first_key(rp, t, kShift, kind);
+          const int j0 = k0 + lane * br;
+          uint32_t mine[4] = {0u, 0u, 0u, 0u};  // (a tile of 64 keys has two words)
+          bool take = false;
+          if (kind) {
+            take = lane == 0 && rp.live > k0;
+            if (lane == 0)
 #pragma unroll
-            for (int w = 0; w < BN / 32; ++w) mine[w] = low_mask(rp.live - k0 - 32 * w);
-        } else if (page >= 0) {
-          take = true;
+              for (int w = 0; w < BN / 32; ++w) mine[w] = low_mask(rp.live - k0 - 32 * w);
+          } else if (page >= 0) {
+            take = true;
 #pragma unroll
-          for (int w = 0; w < BN / 32; ++w) {
-            const int j = k0 + 32 * w;
-            mine[w] = low_mask(rp.n - j) & (~low_mask(rp.lo - j) | low_mask(rp.s_end - j)) & low_mask(j0 + br - j) &
-                      ~low_mask(j0 - j);
+            for (int w = 0; w < BN / 32; ++w) {
+              const int j = k0 + 32 * w;
+              mine[w] = low_mask(rp.n - j) & (~low_mask(rp.lo - j) | low_mask(rp.s_end - j)) & low_mask(j0 + br - j) &
+                        ~low_mask(j0 - j);
+            }
+          } else if (page == -1) {
+            report_error(p.err, MGQA_ERR_INVALID_ARG);
           }
-        } else if (page == -1) {
-          report_error(p.err, MGQA_ERR_INVALID_ARG);
-        }
-        uint4 words;
-        if (!of_v) {
-          words.x = __reduce_or_sync(0xffffffffu, mine[0]);
-          words.y = __reduce_or_sync(0xffffffffu, mine[1]);
-          words.z = BN == 64 ? 0xffffffffu : __reduce_or_sync(0xffffffffu, mine[2]);
-          words.w = BN == 64 ? 0xffffffffu : __reduce_or_sync(0xffffffffu, mine[3]);
-        }
-        const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, take)) * (kind ? BN : br) * 128 * KB);
-        const int st = it % STAGES, use = it / STAGES;
-        const int slot = kind ? k0 : slot_in_page(p, j0), z = kind ? pc.b : page;
-        unsigned char *dst = buf + st * KB * BOX + (kind ? 0 : lane * br * 128);
-        if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(empty + st, (use - 1) & 1, p.err));
-        if (!ok) break;
-        if (lane == 0) {
-          if (!of_v) sm.ok[it % kOkRing] = words;
-          mbar_arrive_expect_tx(full + st, bytes);
-        }
-        __syncwarp();
-        if (take)
+          uint4 words;
+          if (!of_v) {
+            words.x = __reduce_or_sync(0xffffffffu, mine[0]);
+            words.y = __reduce_or_sync(0xffffffffu, mine[1]);
+            words.z = BN == 64 ? 0xffffffffu : __reduce_or_sync(0xffffffffu, mine[2]);
+            words.w = BN == 64 ? 0xffffffffu : __reduce_or_sync(0xffffffffu, mine[3]);
+          }
+          const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, take)) * (kind ? BN : br) * 128 * KB);
+          const int st = it % STAGES, use = it / STAGES;
+          const int slot = kind ? k0 : slot_in_page(p, j0), z = kind ? pc.b : page;
+          unsigned char *dst = buf + st * KB * BOX + (kind ? 0 : lane * br * 128);
+          if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(empty + st, (use - 1) & 1, p.err));
+          if (!ok) break;
+          if (lane == 0) {
+            if (!of_v) sm.ok[it % kOkRing] = words;
+            mbar_arrive_expect_tx(full + st, bytes);
+          }
+          __syncwarp();
+          if (take)
 #pragma unroll
-          for (int c = 0; c < KB; ++c)
-            tc::tma_load_4d(dst + c * BOX, kind ? tm_new : tm, c * 64, slot, pc.g, z, full + st);
-        page = next;
+            for (int c = 0; c < KB; ++c)
+              tc::tma_load_4d(dst + c * BOX, kind ? tm_new : tm, c * 64, slot, pc.g, z, full + st);
+        }
       }
+      // no copy may be in flight when the CTA exits (only this warp arms these full
+      // barriers: the last armed phase of each is the newest it can reach)
+      __syncwarp();
+      for (int i = max(0, it - STAGES); i < it; ++i) mbar_wait(full + i % STAGES, (i / STAGES) & 1, p.err);
+      __syncwarp();
     }
-    // no copy may be in flight when the CTA exits (only this warp arms these full
-    // barriers: the last armed phase of each is the newest it can reach)
-    __syncwarp();
-    for (int i = max(0, it - STAGES); i < it; ++i) mbar_wait(full + i % STAGES, (i / STAGES) & 1, p.err);
-    __syncwarp();
     role_end();
   } else if (warp == 1) {
     tc::regs_dec<L::kDec>();
@@ -427,7 +423,7 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
           if (all_of(okw) != 0xffffffffu) {
             int kind;
             const int k0 = first_key(pc.rp, pc.t0 + n, kShift, kind);
-            const int rows = tp.box_rows && kind && pc.rp.live > k0 ? p.T - k0 : BN;
+            const int rows = BOXES && kind && pc.rp.live > k0 ? p.T - k0 : BN;
 #pragma unroll
             for (int w = 0; w < BN / 32; ++w) {
               const uint32_t clear = ~word_of(okw, w) & low_mask(rows - 32 * w);
@@ -652,13 +648,11 @@ cache_attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   }
 }
 
-template <typename T, int D, int NT>
-mgqa_status launch_t(TcCacheParams tp, mgqa_dtype dt, const CacheAttnLaunch &how, cudaStream_t s) {
+template <typename T, int D, int NT, bool BOXES>
+mgqa_status launch_b(TcCacheParams tp, mgqa_dtype dt, const CUtensorMap (&maps)[4], const CacheAttnLaunch &how,
+                     cudaStream_t s) {
   using L = Lay<D, NT>;
-  CUtensorMap maps[4];
-  if (!cache_attn_maps(tp.a, dt, D, L::BN, maps, tp.box_rows))
-    return fail(MGQA_ERR_CUDA, "cuTensorMapEncodeTiled failed for the cache");
-  auto kern = cache_attn_tc_kernel<T, D, NT>;
+  auto kern = cache_attn_tc_kernel<T, D, NT, BOXES>;
   static std::atomic<uint64_t> attr{0};
   const mgqa_status st = ensure_smem_attr(kern, L::smem, attr, "cache attention kernel");
   if (st != MGQA_OK) return st;
@@ -683,6 +677,14 @@ mgqa_status launch_t(TcCacheParams tp, mgqa_dtype dt, const CacheAttnLaunch &how
                                    maps[3], tp);
   if (e != cudaSuccess) return fail(MGQA_ERR_CUDA, "cache attention launch: %s", cudaGetErrorString(e));
   return launch_cache_merge(p, dt, D, L::ROWS, grid, s);
+}
+
+template <typename T, int D, int NT>
+mgqa_status launch_t(TcCacheParams tp, mgqa_dtype dt, const CacheAttnLaunch &how, cudaStream_t s) {
+  CUtensorMap maps[4];
+  if (!cache_attn_maps(tp.a, dt, D, Lay<D, NT>::BN, maps, tp.box_rows))
+    return fail(MGQA_ERR_CUDA, "cuTensorMapEncodeTiled failed for the cache");
+  return tp.box_rows ? launch_b<T, D, NT, true>(tp, dt, maps, how, s) : launch_b<T, D, NT, false>(tp, dt, maps, how, s);
 }
 
 template <typename T, int D>

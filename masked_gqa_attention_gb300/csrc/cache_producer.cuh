@@ -61,6 +61,43 @@ struct Pieces {
   MGQA_DEV bool idle() const { return S && only.t0 >= only.t1; }  // a cluster's CTA without a share
 };
 
+// The pages of the boxes of the tiles to come, one a lane of a warp: 32 / NBOX tiles
+// with every load, which is started that many tiles ahead (one tile ahead, the
+// latency of the page table bounded tiles of 16 KB: 64 rows, D = 64, window 4096,
+// 104 us, 99 so).
+struct BoxPages {
+  int nbox, tiles, base;  // boxes of a tile; tiles of a load; first tile of `now`
+  int now, next;          // -2: nothing to fetch, -1: a page that is not there
+
+  MGQA_DEV int look_up(const CacheAttnParams &p, const Piece &pc, int shift, int br, int first) const {
+    const int lane = threadIdx.x & 31, t = first + lane / nbox;
+    if (t >= pc.t1) return -2;
+    const RowPlan &rp = pc.rp;
+    int kind;
+    const int j0 = first_key(rp, t, shift, kind) + lane % nbox * br;
+    const bool some = !kind && j0 < rp.n && ((rp.lo < rp.n && j0 + br > rp.lo) || j0 < rp.s_end);
+    return some ? page_of(p, pc.b, j0) : -2;
+  }
+  MGQA_DEV void start(const CacheAttnParams &p, const Piece &pc, int shift, int br) {
+    nbox = (1 << shift) / br;
+    tiles = 32 / nbox;
+    base = pc.t0;
+    now = look_up(p, pc, shift, br, base);
+    next = look_up(p, pc, shift, br, base + tiles);
+  }
+  // The page of box `lane` of tile t (tiles in ascending order).
+  MGQA_DEV int page(const CacheAttnParams &p, const Piece &pc, int shift, int br, int t) {
+    if (t - base == tiles) {
+      base = t;
+      now = next;
+      next = look_up(p, pc, shift, br, base + tiles);
+    }
+    const int lane = threadIdx.x & 31;
+    const int x = __shfl_sync(0xffffffffu, now, (t - base) * nbox + lane % nbox);
+    return lane < nbox ? x : -2;
+  }
+};
+
 // The rows of one tile of 2^SHIFT keys, for a whole warp. KB boxes of 64, 32 ...
 // columns (128 bytes) a row, elements of ES bytes.
 template <int KB, int ES, int SHIFT>
@@ -164,7 +201,8 @@ MGQA_DEV void produce_tiles(const TmaParams &tp, Pieces pieces, int of_v, const 
   constexpr int BOXB = kTile * 128, TILEB = KB * BOXB;
   const CacheAttnParams &p = tp.a;
   const int lane = threadIdx.x & 31;
-  const int br = tp.box_rows, nbox = kTile / br;
+  const int br = tp.box_rows;
+  BoxPages pages;
   bool ok = true;
   int it = 0;  // tiles issued
   Piece pc;
@@ -173,16 +211,9 @@ MGQA_DEV void produce_tiles(const TmaParams &tp, Pieces pieces, int of_v, const 
   while (ok && pieces.next(p, pc)) {
     if (teller) tell_cut(p, blockIdx.x, &pc);
     const RowPlan &rp = pc.rp;
-    // lane i: box i of the tile; the page of the next tile's box is looked up a tile ahead
-    auto look_up = [&](int t) {
-      int kind;
-      const int j0 = first_key(rp, t, 6, kind) + lane * br;
-      const bool some = !kind && lane < nbox && j0 < rp.n && ((rp.lo < rp.n && j0 + br > rp.lo) || j0 < rp.s_end);
-      return some ? page_of(p, pc.b, j0) : -2;  // -1: a page that is not there
-    };
-    int page = look_up(pc.t0);
+    pages.start(p, pc, 6, br);
     for (int t = pc.t0; t < pc.t1 && ok; ++t, ++it) {
-      const int next = t + 1 < pc.t1 ? look_up(t + 1) : -2;
+      const int page = pages.page(p, pc, 6, br, t);  // (lane i: box i of the tile)
       int kind;
       const int k0 = first_key(rp, t, 6, kind);
       uint64_t bits = 0ull;
@@ -218,7 +249,6 @@ MGQA_DEV void produce_tiles(const TmaParams &tp, Pieces pieces, int of_v, const 
         for (int c = 0; c < KB; ++c)
           tc::tma_load_4d(dst + c * BOXB, kind ? tm_new : tm, c * COLS, slot, pc.g, z, full + st);
       }
-      page = next;
     }
   }
   // no copy may be in flight when the CTA exits, even if the consumers gave up

@@ -48,6 +48,7 @@
 // Every wait is bounded (about 2 s) and reports MGQA_ERR_TIMEOUT.
 #include <climits>
 #include <cmath>
+#include <type_traits>
 #include <cuda.h>
 
 #include "common.cuh"
@@ -178,6 +179,7 @@ MGQA_DEV int next_tile(const uint32_t *ne, int prev, int nkt) {
 // Segment ids: each lane loads 4 of the tile's key ids (coalesced) and the
 // warp builds each row's words with ballots, one round per distinct query
 // segment among its 32 rows (usually one or two).
+template <bool WIN>
 MGQA_DEV void tile_mask_words(const TcParams &p, int b, int i, bool row_ok, int k0, int kvl,
                               int segq, int lane, uint32_t (&mw)[BN / 32]) {
 #pragma unroll
@@ -186,7 +188,7 @@ MGQA_DEV void tile_mask_words(const TcParams &p, int b, int i, bool row_ok, int 
     int lim = min(p.Lk, kvl) - jw;
     if (p.mask.causal) lim = min(lim, i + p.mask.coff + 1 - jw);
     mw[w] = lim >= 32 ? 0xffffffffu : (lim <= 0 ? 0u : ((1u << lim) - 1u));
-    if (p.mask.window) mw[w] &= window_word(p.mask, i + p.mask.coff, jw);
+    if (WIN) mw[w] &= window_word(p.mask, i + p.mask.coff, jw);
   }
   if (p.mask.bits) {
     const uint32_t *mrow = p.mask.bits + (int64_t)b * p.mask.sb + (int64_t)i * p.mask.sq;
@@ -393,8 +395,9 @@ MGQA_DEV void softmax_tile(uint32_t t_s, uint32_t t_o, const uint32_t (&mw)[BN /
 }
 
 // ROPE: the query tile is normalised / rotated in shared memory first (a
-// separate instantiation, so the plain kernel carries none of that code).
-template <typename T, int D, int NT, int STAGES, bool ROPE>
+// separate instantiation, so the plain kernel carries none of that code). WIN: a
+// sliding window (likewise; its code in every instance cost the plain calls 1 %).
+template <typename T, int D, int NT, int STAGES, bool ROPE, bool WIN>
 __global__ void __launch_bounds__(128 * (1 + NT), 1)
 prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -434,7 +437,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   // [0, w_sink) and [w_lo, w_hi); without a window [0, nkt). The tile loaded
   // ahead of the classification is the first of them.
   int w_sink = 0, w_lo = 0, w_hi = p.nkt;
-  if (p.mask.window) {
+  if (WIN) {
     const int first = row0 + p.mask.coff, last = first + rows - 1;  // positions
     w_sink = min(p.nkt, (p.mask.sinks + BN - 1) / BN);
     w_lo = max(w_sink, max(0, first - p.mask.window + 1) / BN);
@@ -659,7 +662,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       ne = ne && k0 <= row0 + rows - 1 + p.mask.coff;
       full = full && k0 + BN - 1 <= row0 + p.mask.coff;
     }
-    if (p.mask.window) {  // (the candidates hold a key that some row's window or sinks reach)
+    if (WIN) {  // (the candidates hold a key that some row's window or sinks reach)
       const int first = row0 + p.mask.coff, last = first + rows - 1;
       full = full && (k0 + BN <= p.mask.sinks ||
                       (k0 > last - p.mask.window && (p.mask.causal || k0 + BN <= first + p.mask.window)));
@@ -872,12 +875,12 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       bool p0_seen = false;  // P_0(n) already observed complete
       // Under a window the value rows behind kv_len may hold anything: the tile
       // that kv_len ends in (the last one, if it has a key to give) is cleared there.
-      const int tail = !ROPE && p.mask.window && kvl > 0 && kvl < p.Lk ? kvl % BN : 0;
-      const bool cut = tail && ((ne_bits[(kvl / BN) >> 5] >> ((kvl / BN) & 31)) & 1u);
+      const int tail = WIN && kvl > 0 && kvl < p.Lk ? kvl % BN : 0;
+      const int n_cut = tail && ((ne_bits[(kvl / BN) >> 5] >> ((kvl / BN) & 31)) & 1u) ? nk - 1 : -1;
       for (int n = 0; n < nk && ok; ++n) {
         const int st = n % STAGES;
         const bool has_next = n + 1 < nk;
-        if (cut && !has_next) {
+        if (WIN && n == n_cut) {
           for (int u = lane; u < (BN - tail) * (D / 8); u += 32) {
             const int c = u % (D / 8);  // 16-byte pieces (the swizzle permutes them within a row)
             *reinterpret_cast<uint4 *>(smem + Lay::v_off + (st * KB + (c >> 3)) * BOX + (tail + u / (D / 8)) * 128 +
@@ -978,7 +981,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       kt = next_tile(ne_bits, kt, p.nkt);
       const bool partial = !((full_bits[kt >> 5] >> (kt & 31)) & 1u);
       uint32_t mw[BN / 32] = {0u, 0u, 0u, 0u};
-      if (partial) tile_mask_words(p, b, ic, row_ok, kt * BN, kvl, segq, lane, mw);
+      if (partial) tile_mask_words<WIN>(p, b, ic, row_ok, kt * BN, kvl, segq, lane, mw);
       // warp-uniform outcome: the tile pass below is made of warp-wide
       // tensor-memory loads and stores
       if (ok) ok = mbar_wait(bar_sfull + t, n & 1, p.err, lim);
@@ -1107,11 +1110,11 @@ bool make_tma_map_4d(CUtensorMap *m, mgqa_dtype dt, const void *base, int B, int
 
 namespace {
 
-template <typename T, int D, int NT, int STAGES, bool ROPE>
+template <typename T, int D, int NT, int STAGES, bool ROPE, bool WIN>
 mgqa_status launch_t(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                      const CUtensorMap &mo, const TcParams &p, cudaStream_t s) {
   using Lay = Layout<D, NT, STAGES>;
-  auto kern = prefill_tc_kernel<T, D, NT, STAGES, ROPE>;
+  auto kern = prefill_tc_kernel<T, D, NT, STAGES, ROPE, WIN>;
   static std::atomic<uint64_t> attr_done{0};
   const mgqa_status st = ensure_smem_attr(kern, Lay::smem_bytes, attr_done, "tensor-core prefill");
   if (st != MGQA_OK) return st;
@@ -1122,16 +1125,16 @@ mgqa_status launch_t(const CUtensorMap &mq, const CUtensorMap &mk, const CUtenso
   return MGQA_OK;
 }
 
-template <typename T, bool ROPE>
+template <typename T, bool ROPE, bool WIN>
 mgqa_status dispatch_d(int D, bool pair, const CUtensorMap &mq, const CUtensorMap &mk,
                        const CUtensorMap &mv, const CUtensorMap &mo, const TcParams &p,
                        cudaStream_t s) {
   if (D == 128)
-    return pair ? launch_t<T, 128, 2, 2, ROPE>(mq, mk, mv, mo, p, s)
-                : launch_t<T, 128, 1, 2, ROPE>(mq, mk, mv, mo, p, s);
+    return pair ? launch_t<T, 128, 2, 2, ROPE, WIN>(mq, mk, mv, mo, p, s)
+                : launch_t<T, 128, 1, 2, ROPE, WIN>(mq, mk, mv, mo, p, s);
   if (D == 64)
-    return pair ? launch_t<T, 64, 2, 3, ROPE>(mq, mk, mv, mo, p, s)
-                : launch_t<T, 64, 1, 3, ROPE>(mq, mk, mv, mo, p, s);
+    return pair ? launch_t<T, 64, 2, 3, ROPE, WIN>(mq, mk, mv, mo, p, s)
+                : launch_t<T, 64, 1, 3, ROPE, WIN>(mq, mk, mv, mo, p, s);
   return fail(MGQA_ERR_UNSUPPORTED, "head dim %d", D);
 }
 
@@ -1173,11 +1176,14 @@ mgqa_status launch_prefill_tc(const mgqa_args &a, cudaStream_t s, const FusedRop
   p.rope = rope;
   const bool pair = (p.n_rep % 2) == 0;
   const bool rope_on = rope.inv_freq != nullptr;
-  if (a.dtype == MGQA_BF16)
-    return rope_on ? dispatch_d<__nv_bfloat16, true>(a.D, pair, mq, mk, mv, mo, p, s)
-                   : dispatch_d<__nv_bfloat16, false>(a.D, pair, mq, mk, mv, mo, p, s);
-  return rope_on ? dispatch_d<__half, true>(a.D, pair, mq, mk, mv, mo, p, s)
-                 : dispatch_d<__half, false>(a.D, pair, mq, mk, mv, mo, p, s);
+  const auto go = [&](auto rope_c, auto win_c) {
+    constexpr bool R = decltype(rope_c)::value, W = decltype(win_c)::value;
+    return a.dtype == MGQA_BF16 ? dispatch_d<__nv_bfloat16, R, W>(a.D, pair, mq, mk, mv, mo, p, s)
+                                : dispatch_d<__half, R, W>(a.D, pair, mq, mk, mv, mo, p, s);
+  };
+  // (no entry has both)
+  if (rope_on) return go(std::true_type(), std::false_type());
+  return win.window ? go(std::false_type(), std::true_type()) : go(std::false_type(), std::false_type());
 }
 
 }  // namespace mgqa
