@@ -21,9 +21,9 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
-import struct
 from typing import Optional
 
 import torch
@@ -216,7 +216,7 @@ def _bind(L: ctypes.CDLL) -> ctypes.CDLL:
     L.masked_gqa_attn_decode_append_rope.argtypes = [ctypes.POINTER(MgqaArgs), P, P, I64P, I64P, P,
                                                      ctypes.POINTER(MgqaQkRope), P, ctypes.c_size_t, P]
     L.masked_gqa_attn_decode_append_rope.restype = ctypes.c_int
-    # (structs of the cache calls go as plain addresses: cheaper per call than typed pointers)
+    # (structs of the cache calls go as plain addresses)
     SZ, I64 = ctypes.c_size_t, ctypes.c_int64
     for name, args, res in (
             ("masked_gqa_attn_prefill_window", [P, I32, I32, P], ctypes.c_int),
@@ -630,41 +630,24 @@ def masked_gqa_attn_decode_append_rope(q, k_cache, v_cache, k_new, v_new, kv_len
 
 
 # ---- sliding windows, drafted tokens, and a cache in slots or pages ---------------
-# These calls are made once per layer and token, so their marshalling is kept
-# short: each C struct is packed by one struct.pack in its native layout (the
-# layout of the ctypes mirrors above).
+# These calls are made once per layer and token, so their tensors are checked and
+# passed on natively (csrc/bind.cpp).
 
-_ARGS = struct.Struct("@7i4P12qP2q3PfPPi0P")
-_PAGES = struct.Struct("@Pq3i0P")
-_TREE = struct.Struct("@2P6qP2qP")
-_CACHE = struct.Struct("@6i2P8q2iPq3P")
-_QUAD = struct.Struct("@4q")
-_CODES = {torch.bfloat16: MGQA_BF16, torch.float16: MGQA_FP16, torch.float32: MGQA_FP32}
-_I32, _F32 = torch.int32, torch.float32
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_native = None
 
 
-def _together(first, others, names):
-    """The device index of `first`, which every other tensor must share."""
-    dev = first.get_device()
-    if dev < 0:
-        raise ValueError("tensors must be CUDA tensors")
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            name = names.split()[[x is t for x in others].index(True)]
-            raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
-    return dev
-
-
-def _ints(t, name, shape, contiguous=True):
-    """Address of an int32 tensor of the given shape (0: absent)."""
-    if t is None:
-        return 0
-    if t.dtype != _I32 or t.shape != shape or (contiguous and not t.is_contiguous()):
-        raise ValueError(f"{name} must be {'contiguous ' if contiguous else ''}int32 {list(shape)}")
-    return t.data_ptr()
+def _calls():
+    """The native calls (raises if they have not been built)."""
+    global _native
+    if _native is None:
+        from .build import BIND
+        if not os.path.exists(BIND):
+            raise RuntimeError(f"{os.path.basename(BIND)} is not built ({BIND}); run build_library()")
+        lib()
+        spec = importlib.util.spec_from_file_location("_mgqa_bind", BIND)
+        _native = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_native)
+    return _native
 
 
 def _i32(x):
@@ -684,18 +667,6 @@ def _kept(ws, stream):
     return ws
 
 
-def _go(dev, stream, fn, *args):
-    """fn(*args, stream) with device `dev` current; its own current stream
-    unless one is given."""
-    if dev != _current_device():
-        with torch.cuda.device(dev):
-            status = fn(*args, _raw_stream(dev) if stream is None else _stream_handle(stream))
-    else:
-        status = fn(*args, _raw_stream(dev) if stream is None else _stream_handle(stream))
-    if status != MGQA_OK:
-        _check(status)
-
-
 def masked_gqa_attn_prefill_window(q, k, v, out=None, *, window, sinks=0, causal=True, scale=None,
                                    mask_bits=None, kv_len=None, seg_q=None, seg_k=None, lse=None,
                                    dev_error=None, stream=None):
@@ -705,14 +676,20 @@ def masked_gqa_attn_prefill_window(q, k, v, out=None, *, window, sinks=0, causal
     whatever the other mask forms allow. Returns out."""
     if out is None:
         out = torch.empty_like(q)
-    dev = _together(q, (k, v, out, mask_bits, kv_len, seg_q, seg_k, lse, dev_error),
-                    "k v out mask_bits kv_len seg_q seg_k lse dev_error")
     if mask_bits is None and seg_q is None and seg_k is None:
-        a = _attn_args(q, k, v, out, kv_len, scale, lse, dev_error, None, causal)[0]
+        status = (_native or _calls()).prefill_window(q, k, v, out, kv_len, scale, lse, dev_error, causal, window, sinks,
+                                                      stream)
     else:
-        a = bytes(make_args(q, k, v, out, scale=scale, mask_bits=mask_bits, kv_len=kv_len, seg_q=seg_q,
-                            seg_k=seg_k, lse=lse, dev_error=dev_error, causal=causal))
-    _go(dev, stream, lib().masked_gqa_attn_prefill_window, a, _i32(window), _i32(sinks))
+        for t in (k, v, out, mask_bits, kv_len, seg_q, seg_k, lse, dev_error):
+            if t is not None and t.device != q.device:
+                raise ValueError(f"tensors on {t.device} and {q.device}")
+        a = make_args(q, k, v, out, scale=scale, mask_bits=mask_bits, kv_len=kv_len, seg_q=seg_q,
+                      seg_k=seg_k, lse=lse, dev_error=dev_error, causal=causal)
+        with torch.cuda.device(q.device):
+            status = lib().masked_gqa_attn_prefill_window(ctypes.byref(a), _i32(window), _i32(sinks),
+                                                          _stream_handle(stream))
+    if status:
+        _check(status)
     return out
 
 
@@ -733,44 +710,6 @@ def new_cache_attn_workspace(device="cuda") -> torch.Tensor:
     return torch.empty(masked_gqa_attn_cache_workspace_size(), dtype=torch.uint8, device=device)
 
 
-def _attn_args(q, k, v, out, kv_len, scale, lse, dev_error, page_table, causal=False):
-    """(mgqa_args, mgqa_pages or None) packed, for k / v [B, Hkv, slots, D] or,
-    with a page table, [pages, Hkv, page_size, D]."""
-    shape, ks = q.shape, k.shape
-    if len(shape) != 4 or len(ks) != 4 or v.shape != ks or out.shape != shape:
-        raise ValueError("q, out must be [B, Hq, L, D] and k, v [B or pages, Hkv, slots, D]")
-    dtype = q.dtype
-    dt = _CODES.get(dtype)
-    if dt is None or k.dtype != dtype or v.dtype != dtype or out.dtype != dtype:
-        raise ValueError("q, out, k and v must share one dtype of bfloat16, float16, float32")
-    B, Hq, L, D = shape
-    P0, Hkv, S, Dk = ks
-    q0, q1, q2, q3 = q.stride()
-    k0, k1, k2, k3 = k.stride()
-    v0, v1, v2, v3 = v.stride()
-    o0, o1, o2, o3 = out.stride()
-    if Dk != D or not q3 == k3 == v3 == o3 == 1:
-        raise ValueError("the head dims must agree and have unit stride")
-    pages, cap = None, S
-    if page_table is not None:
-        if page_table.dtype != _I32 or page_table.dim() != 2 or page_table.shape[0] != B \
-                or page_table.stride(1) != 1:
-            raise ValueError("page_table must be int32 [B, max_pages] with unit-stride rows")
-        mp = page_table.shape[1]
-        pages = _PAGES.pack(page_table.data_ptr(), page_table.stride(0), P0, S, mp)
-        cap = mp * S
-    elif P0 != B:
-        raise ValueError("k and v without a page table must be [B, Hkv, slots, D]")
-    if lse is not None and (lse.dtype != _F32 or lse.shape != shape[:3] or not lse.is_contiguous()):
-        raise ValueError("lse must be contiguous fp32 [B, Hq, L]")
-    a = _ARGS.pack(dt, B, Hq, Hkv, L, cap, D, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                   q0, q1, q2, k0, k1, k2, v0, v1, v2, o0, o1, o2, 0, 0, 0,
-                   _ints(kv_len, "kv_len", (B,)), 0, 0, D ** -0.5 if scale is None else scale,
-                   0 if lse is None else lse.data_ptr(), _ints(dev_error, "dev_error", (1,)),
-                   1 if causal else 0)
-    return a, pages
-
-
 def masked_gqa_attn_decode_window(q, k_cache, v_cache, kv_len, out=None, *, window, sinks=0,
                                   page_table=None, workspace=None, scale=None, lse=None,
                                   dev_error=None, stream=None):
@@ -783,13 +722,10 @@ def masked_gqa_attn_decode_window(q, k_cache, v_cache, kv_len, out=None, *, wind
         out = torch.empty_like(q)
     if workspace is None:
         workspace = _kept(new_cache_attn_workspace(q.device), stream)
-    dev = _together(q, (k_cache, v_cache, kv_len, out, page_table, workspace, lse, dev_error),
-                    "k_cache v_cache kv_len out page_table workspace lse dev_error")
-    if kv_len is None:
-        raise ValueError("kv_len is required")
-    a, pages = _attn_args(q, k_cache, v_cache, out, kv_len, scale, lse, dev_error, page_table)
-    _go(dev, stream, lib().masked_gqa_attn_decode_window, a, pages, _i32(window), _i32(sinks),
-        workspace.data_ptr(), workspace.nbytes)
+    status = (_native or _calls()).decode_window(q, k_cache, v_cache, kv_len, out, window, sinks, page_table,
+                                                 workspace, scale, lse, dev_error, stream)
+    if status:
+        _check(status)
     return out
 
 
@@ -807,60 +743,11 @@ def masked_gqa_attn_decode_tree(q, k_cache, v_cache, k_new, v_new, kv_len, out=N
         out = torch.empty_like(q)
     if workspace is None:
         workspace = _kept(new_cache_attn_workspace(q.device), stream)
-    dev = _together(q, (k_cache, v_cache, k_new, v_new, kv_len, out, tree_bits, tree_len, page_table,
-                        workspace, lse, dev_error),
-                    "k_cache v_cache k_new v_new kv_len out tree_bits tree_len page_table workspace "
-                    "lse dev_error")
-    if kv_len is None:
-        raise ValueError("kv_len is required")
-    a, pages = _attn_args(q, k_cache, v_cache, out, kv_len, scale, lse, dev_error, page_table)
-    B, _, T, D = q.shape
-    shape = (B, k_cache.shape[1], T, D)
-    n0, n1, n2, n3 = k_new.stride()
-    m0, m1, m2, m3 = v_new.stride()
-    if k_new.shape != shape or v_new.shape != shape or k_new.dtype != q.dtype or v_new.dtype != q.dtype \
-            or n3 != 1 or m3 != 1:
-        raise ValueError(f"k_new and v_new must be {q.dtype} {list(shape)} with a unit-stride head dim")
-    bits = sb = st = 0
-    if tree_bits is not None:
-        if tree_bits.dtype not in (_I32, torch.uint32) or tree_bits.dim() != 3 or tree_bits.stride(2) != 1:
-            raise ValueError("tree_bits must be 3-D int32/uint32 words, contiguous along drafts")
-        b0, t0, w0 = tree_bits.shape
-        if b0 not in (1, B) or t0 not in (1, T) or w0 < (T + 31) // 32:
-            raise ValueError(f"tree_bits must be [B or 1, T or 1, >= {(T + 31) // 32}] words")
-        bits = tree_bits.data_ptr()
-        sb = tree_bits.stride(0) if b0 > 1 else 0
-        st = tree_bits.stride(1) if t0 > 1 else 0
-    tree = _TREE.pack(k_new.data_ptr(), v_new.data_ptr(), n0, n1, n2, m0, m1, m2, bits, sb, st,
-                      _ints(tree_len, "tree_len", (B,)))
-    _go(dev, stream, lib().masked_gqa_attn_decode_tree, a, pages, tree, _i32(window), _i32(sinks),
-        workspace.data_ptr(), workspace.nbytes)
+    status = (_native or _calls()).decode_tree(q, k_cache, v_cache, k_new, v_new, kv_len, out, tree_bits, tree_len,
+                                               window, sinks, page_table, workspace, scale, lse, dev_error, stream)
+    if status:
+        _check(status)
     return out
-
-
-def _cache(k_cache, v_cache, page_table, kv_len, ref, dev_error):
-    """(mgqa_cache packed, (layers, rows, Hkv, D)) of tensors
-    [layers, pages, Hkv, page_size, D] (or without the layer dimension)."""
-    sh, ks, vs = k_cache.shape, k_cache.stride(), v_cache.stride()
-    if len(sh) not in (4, 5) or v_cache.shape != sh or ks[-1] != 1 or vs[-1] != 1:
-        raise ValueError("the caches must be [layers, pages, Hkv, page_size, D] (or 4-D, one layer) "
-                         "with a unit-stride head dim")
-    dt = _CODES.get(k_cache.dtype)
-    if dt is None or v_cache.dtype != k_cache.dtype:
-        raise ValueError("the caches must share one dtype of bfloat16, float16, float32")
-    if len(sh) == 4:
-        sh, ks, vs = (1, *sh), (0, *ks), (0, *vs)
-    L, pages, Hkv, page, D = sh
-    rows, mp, tp, ts = pages, 0, 0, 0
-    if page_table is not None:
-        if page_table.dtype != _I32 or page_table.dim() != 2 or page_table.stride(1) != 1:
-            raise ValueError("page_table must be int32 [rows, max_pages] with unit-stride rows")
-        rows, mp = page_table.shape
-        tp, ts = page_table.data_ptr(), page_table.stride(0)
-    c = _CACHE.pack(dt, L, pages, Hkv, page, D, k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2],
-                    ks[3], vs[0], vs[1], vs[2], vs[3], rows, mp, tp, ts, _ints(kv_len, "kv_len", (rows,)),
-                    _ints(ref, "ref", (pages,)), _ints(dev_error, "dev_error", (1,)))
-    return c, (L, rows, Hkv, D)
 
 
 def masked_gqa_cache_append(k_cache, v_cache, k_new, v_new, kv_len, kv_len_out, *, index=None,
@@ -871,43 +758,25 @@ def masked_gqa_cache_append(k_cache, v_cache, k_new, v_new, kv_len, kv_len_out, 
     kv_len_out (int32 [B], not kv_len) receives kv_len + count. The cache is
     [layers, B, Hkv, slots, D], or in pages with page_table int32
     [B, max_pages]. Returns kv_len_out."""
-    dev = _together(k_cache, (v_cache, k_new, v_new, kv_len, kv_len_out, index, count, page_table, dev_error),
-                    "v_cache k_new v_new kv_len kv_len_out index count page_table dev_error")
-    if kv_len is None or kv_len_out is None:
-        raise ValueError("kv_len and kv_len_out are required")
-    c, (L, rows, Hkv, D) = _cache(k_cache, v_cache, page_table, kv_len, None, dev_error)
-    dims = k_cache.dim()
-    T = k_new.shape[-2]
-    want = (L, rows, Hkv, T, D)[5 - dims:]
-    ks, vs = k_new.stride(), v_new.stride()
-    if k_new.shape != want or v_new.shape != want or k_new.dtype != k_cache.dtype \
-            or v_new.dtype != k_cache.dtype or ks[-1] != 1 or vs[-1] != 1:
-        raise ValueError(f"k_new and v_new must be {k_cache.dtype} {list(want)} with a unit-stride head dim")
-    if dims == 4:
-        ks, vs = (0, *ks), (0, *vs)
-    _go(dev, stream, lib().masked_gqa_cache_append, c, k_new.data_ptr(), v_new.data_ptr(),
-        _QUAD.pack(*ks[:4]), _QUAD.pack(*vs[:4]), T, _ints(index, "index", (rows, T)),
-        _ints(count, "count", (rows,)), _ints(kv_len_out, "kv_len_out", (rows,)))
+    status = (_native or _calls()).cache_append(k_cache, v_cache, k_new, v_new, kv_len, kv_len_out, index, count,
+                                                page_table, dev_error, stream)
+    if status:
+        _check(status)
     return kv_len_out
 
 
 def masked_gqa_cache_workspace_size(k_cache, v_cache, page_table, ref, n=0) -> int:
     """Bytes of the workspace of masked_gqa_cache_fork with n pairs, or (n = 0)
     of masked_gqa_cache_compact."""
-    c = _cache(k_cache, v_cache, page_table, None, ref, None)[0]
-    size = int(lib().masked_gqa_cache_workspace_size(c, n))
+    size = _calls().cache_workspace_size(k_cache, v_cache, page_table, ref, n)
     if size == 0:
         _check(MGQA_ERR_INVALID_ARG)
     return size
 
 
-def _pages_ws(workspace, c, n, device, stream):
-    if workspace is not None:
-        return workspace
-    size = int(lib().masked_gqa_cache_workspace_size(c, n))
-    if size == 0:
-        _check(MGQA_ERR_INVALID_ARG)
-    return _kept(torch.empty(size, dtype=torch.uint8, device=device), stream)
+def _pages_ws(k_cache, v_cache, page_table, ref, n, stream):
+    size = masked_gqa_cache_workspace_size(k_cache, v_cache, page_table, ref, n)
+    return _kept(torch.empty(size, dtype=torch.uint8, device=k_cache.device), stream)
 
 
 def masked_gqa_cache_fork(k_cache, v_cache, page_table, kv_len, ref, src, dst, *, extra=0,
@@ -919,17 +788,12 @@ def masked_gqa_cache_fork(k_cache, v_cache, page_table, kv_len, ref, src, dst, *
     [rows, max_pages], kv_len int32 [rows] and ref int32 [pages] (table entries
     that hold a page) are updated in place; new pages are the free ones of
     lowest index. The caches are [layers, pages, Hkv, page_size, D] or 4-D."""
-    dev = _together(k_cache, (v_cache, page_table, kv_len, ref, src, dst, workspace, dev_error),
-                    "v_cache page_table kv_len ref src dst workspace dev_error")
-    if page_table is None or kv_len is None or ref is None:
-        raise ValueError("page_table, kv_len and ref are required")
-    n = src.numel()
-    sp, dp = _ints(src, "src", (n,)), _ints(dst, "dst", (n,))
-    if n == 0:
-        return
-    c = _cache(k_cache, v_cache, page_table, kv_len, ref, dev_error)[0]
-    ws = _pages_ws(workspace, c, n, k_cache.device, stream)
-    _go(dev, stream, lib().masked_gqa_cache_fork, c, n, sp, dp, _i32(extra), ws.data_ptr(), ws.nbytes)
+    if workspace is None:
+        workspace = _pages_ws(k_cache, v_cache, page_table, ref, max(1, src.numel()), stream)
+    status = (_native or _calls()).cache_fork(k_cache, v_cache, page_table, kv_len, ref, src, dst, extra, workspace,
+                                              dev_error, stream)
+    if status:
+        _check(status)
 
 
 def masked_gqa_cache_compact(k_cache, v_cache, page_table, ref, page_table_out=None, ref_out=None, *,
@@ -938,17 +802,12 @@ def masked_gqa_cache_compact(k_cache, v_cache, page_table, ref, page_table_out=N
     values move, page_table_out and ref_out (default: page_table and ref, in
     place) get the renamed tables and used_out (int32 [1], optional) the number
     of pages in use. Returns (page_table_out, ref_out)."""
-    dev = _together(k_cache, (v_cache, page_table, ref, page_table_out, ref_out, used_out, workspace, dev_error),
-                    "v_cache page_table ref page_table_out ref_out used_out workspace dev_error")
-    if page_table is None or ref is None:
-        raise ValueError("page_table and ref are required")
     page_table_out = page_table if page_table_out is None else page_table_out
     ref_out = ref if ref_out is None else ref_out
-    c = _cache(k_cache, v_cache, page_table, None, ref, dev_error)[0]
-    tp = _ints(page_table_out, "page_table_out", page_table.shape, contiguous=False)
-    if page_table_out.stride(1) != 1:
-        raise ValueError("page_table_out must have unit-stride rows")
-    ws = _pages_ws(workspace, c, 0, k_cache.device, stream)
-    _go(dev, stream, lib().masked_gqa_cache_compact, c, tp, page_table_out.stride(0),
-        _ints(ref_out, "ref_out", ref.shape), _ints(used_out, "used_out", (1,)), ws.data_ptr(), ws.nbytes)
+    if workspace is None:
+        workspace = _pages_ws(k_cache, v_cache, page_table, ref, 0, stream)
+    status = (_native or _calls()).cache_compact(k_cache, v_cache, page_table, ref, page_table_out, ref_out, used_out,
+                                                 workspace, dev_error, stream)
+    if status:
+        _check(status)
     return page_table_out, ref_out

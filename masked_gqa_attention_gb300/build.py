@@ -6,6 +6,9 @@ the objects link into two libraries under masked_gqa_attention_gb300/_lib:
   * libmgqa_debug.so  -- the same sources with MGQA_DEBUG: device-side bounds
                          checks, event counters and an injectable pipeline
                          stall (include/masked_gqa_attn_debug.h); test equipment.
+csrc/bind.cpp, the Python side of the calls made once per layer and token, goes
+into _lib/_mgqa_bind.so beside them (g++ with PyTorch's headers), linked to
+libmgqa.so.
 The CUDA runtime is linked statically; the driver entry point used for TMA
 tensor maps is fetched at run time, so the libraries load on machines
 without a GPU.
@@ -23,6 +26,7 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libmgqa.so")
 LIB_DEBUG = os.path.join(OUT_DIR, "libmgqa_debug.so")
+BIND = os.path.join(OUT_DIR, "_mgqa_bind.so")
 OBJ_DIR = os.path.join(PKG, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -47,7 +51,7 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
+    return _sources() + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
         glob.glob(os.path.join(os.path.dirname(PKG), "include", "*.h"))
 
 
@@ -58,12 +62,34 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def _bind_flags():
+    """(compile, link) flags of bind.cpp."""
+    import sysconfig
+
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tlib = os.path.join(t, "lib")
+    return (["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w", *(f"-I{d}" for d in inc)],
+            [f"-L{OUT_DIR}", "-l:libmgqa.so", f"-L{tlib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+             "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{tlib}"])
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(),
           variants=("release", "debug")) -> str:
     """Compile and link the requested variants (both by default); returns the
     product library's path."""
     todo = [v for v in variants if force or not up_to_date(VARIANTS[v][0])]
-    if not todo:
+    bind = force or not up_to_date(BIND)
+    if not todo and not bind:
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     cc = nvcc()
@@ -85,9 +111,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(),
     for v in todo:
         os.makedirs(VARIANTS[v][1], exist_ok=True)
     jobs = [(v, src) for v in todo for src in srcs]
-    workers = max(1, min(len(jobs), os.cpu_count() or 8))
+    workers = max(1, min(len(jobs) + 1, os.cpu_count() or 8))
+    bind_obj = os.path.join(OBJ_DIR, "bind.o")
     with cf.ThreadPoolExecutor(max_workers=workers) as ex:
+        if bind:
+            os.makedirs(OBJ_DIR, exist_ok=True)
+            flags, link = _bind_flags()
+            bound = ex.submit(_run, ["g++", *flags, "-c", os.path.join(CSRC, "bind.cpp"), "-o", bind_obj], "bind.cpp")
         objs = list(ex.map(compile_one, jobs))
+        if bind:
+            bound.result()
     for v in todo:
         lib = VARIANTS[v][0]
         vobjs = [o for (vv, _), o in zip(jobs, objs) if vv == v]
@@ -97,6 +130,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(),
         if r.returncode != 0:
             raise RuntimeError(f"link failed ({v}):\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, lib)
+    if bind:
+        tmp = BIND + f".tmp{os.getpid()}"
+        _run(["g++", "-shared", "-o", tmp, bind_obj, *link], "link of _mgqa_bind.so")
+        os.replace(tmp, BIND)
     return LIB
 
 

@@ -37,19 +37,6 @@ def test_struct_layout_matches_header(tmp_path, cname, py):
     assert int(got["size"]) == ctypes.sizeof(py)
 
 
-@pytest.mark.parametrize("packer,py", [(M._ARGS, M.MgqaArgs), (M._PAGES, M.MgqaPages), (M._TREE, M.MgqaTree),
-                                       (M._CACHE, M.MgqaCache)])
-def test_packed_structs_have_the_mirrors_layout(packer, py):
-    # every value lands in its own field: pack 1, 2, 3, ... and read them through the mirror
-    n = len(packer.unpack(bytes(packer.size)))
-    got = py.from_buffer_copy(packer.pack(*range(1, n + 1)))
-    flat = []
-    for f, _ in py._fields_:
-        x = getattr(got, f)
-        flat += list(x) if hasattr(x, "__len__") else [x]
-    assert packer.size == ctypes.sizeof(py) and [int(x) for x in flat] == list(range(1, n + 1))
-
-
 def args(Lq=1, cap=1024, B=2):
     a = M.MgqaArgs()
     a.dtype = M.MGQA_BF16
@@ -234,6 +221,21 @@ def test_cache_steps_refuse(L):
     c = cache()
     c.kv_len = None
     assert fork(L, c) == INVALID and append(L, c) == INVALID
+
+
+def test_binding_takes_all_arguments_or_none():
+    calls = M._calls()
+    for f in (calls.prefill_window, calls.decode_window, calls.decode_tree, calls.cache_append, calls.cache_fork,
+              calls.cache_compact, calls.cache_workspace_size):
+        with pytest.raises(TypeError, match="wanted"):
+            f(1, 2, 3)
+    with pytest.raises(ValueError, match="tensor"):
+        calls.cache_workspace_size(1, 2, None, None, 0)
+    k = torch.zeros(3, 2, 4, 64, dtype=torch.bfloat16)
+    assert M.masked_gqa_cache_workspace_size(k, k, torch.zeros(5, 7, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)) > 0
+    for bad in (torch.zeros(4, dtype=torch.int32), torch.zeros(3)):
+        with pytest.raises(ValueError, match="ref"):
+            M.masked_gqa_cache_workspace_size(k, k, torch.zeros(5, 7, dtype=torch.int32), bad)
 
 
 def test_binding_refuses_tensors_off_the_gpu():
