@@ -213,6 +213,17 @@ struct Cache {
   }
 };
 
+// The status of a C call, made without the interpreter's lock: a launch may wait.
+// (Nothing in it may throw: what PyTorch is asked for is asked before.)
+template <typename F>
+PyObject *status_of(F call) {
+  mgqa_status st;
+  Py_BEGIN_ALLOW_THREADS
+  st = call();
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+
 // f(args) as a Python function of `want` positional arguments.
 template <typename F>
 PyObject *guarded(PyObject *const *, Py_ssize_t n, Py_ssize_t want, F f) {
@@ -245,7 +256,9 @@ PyObject *prefill_window(PyObject *, PyObject *const *o, Py_ssize_t n) {
     at.a.causal = causal;
     const int32_t window = count(o[9]), sinks = count(o[10]);
     const Launch l(dev, o[11]);
-    return PyLong_FromLong(masked_gqa_attn_prefill_window(&at.a, window, sinks, l.stream));
+    return status_of([&] {
+      return masked_gqa_attn_prefill_window(&at.a, window, sinks, l.stream);
+    });
   });
 }
 
@@ -261,9 +274,12 @@ PyObject *decode_window(PyObject *, PyObject *const *o, Py_ssize_t n) {
                    {&ws, "workspace"}, {lse, "lse"}, {err, "dev_error"}});
     const Attention at(q, k, v, out, &len, o[9], lse, err, table);
     const int32_t window = count(o[5]), sinks = count(o[6]);
+    void *wp = ws.data_ptr();
+    const size_t wn = ws.nbytes();
     const Launch l(dev, o[12]);
-    return PyLong_FromLong(
-        masked_gqa_attn_decode_window(&at.a, at.paged, window, sinks, ws.data_ptr(), ws.nbytes(), l.stream));
+    return status_of([&] {
+      return masked_gqa_attn_decode_window(&at.a, at.paged, window, sinks, wp, wn, l.stream);
+    });
   });
 }
 
@@ -306,9 +322,12 @@ PyObject *decode_tree(PyObject *, PyObject *const *o, Py_ssize_t n) {
     }
     tree.len = ints(live, "tree_len", {B});
     const int32_t window = count(o[9]), sinks = count(o[10]);
+    void *wp = ws.data_ptr();
+    const size_t wn = ws.nbytes();
     const Launch l(dev, o[16]);
-    return PyLong_FromLong(
-        masked_gqa_attn_decode_tree(&at.a, at.paged, &tree, window, sinks, ws.data_ptr(), ws.nbytes(), l.stream));
+    return status_of([&] {
+      return masked_gqa_attn_decode_tree(&at.a, at.paged, &tree, window, sinks, wp, wn, l.stream);
+    });
   });
 }
 
@@ -339,9 +358,12 @@ PyObject *cache_append(PyObject *, PyObject *const *o, Py_ssize_t n) {
     }
     const int32_t *ip = ints(index, "index", {cache.rows, T}), *cp = ints(cnt, "count", {cache.rows});
     int32_t *lp = ints(&len_out, "kv_len_out", {cache.rows});
+    const void *kp = kn.data_ptr(), *vp = vn.data_ptr();
+    const int32_t rows = small(T, "T");
     const Launch l(dev, o[10]);
-    return PyLong_FromLong(masked_gqa_cache_append(&cache.c, kn.data_ptr(), vn.data_ptr(), ks, vs, small(T, "T"), ip, cp,
-                                                   lp, l.stream));
+    return status_of([&] {
+      return masked_gqa_cache_append(&cache.c, kp, vp, ks, vs, rows, ip, cp, lp, l.stream);
+    });
   });
 }
 
@@ -368,9 +390,13 @@ PyObject *cache_fork(PyObject *, PyObject *const *o, Py_ssize_t n) {
     const int32_t *sp = ints(&src, "src", {pairs}), *dp = ints(&dst, "dst", {pairs});
     const Cache cache(k, v, &table, &len, &ref, err);
     const int32_t extra = count(o[7]);
+    void *wp = ws.data_ptr();
+    const size_t wn = ws.nbytes();
+    const int32_t np = small(pairs, "pairs");
     const Launch l(dev, o[10]);
-    return PyLong_FromLong(masked_gqa_cache_fork(&cache.c, small(pairs, "pairs"), sp, dp, extra, ws.data_ptr(),
-                                                 ws.nbytes(), l.stream));
+    return status_of([&] {
+      return masked_gqa_cache_fork(&cache.c, np, sp, dp, extra, wp, wn, l.stream);
+    });
   });
 }
 
@@ -388,15 +414,21 @@ PyObject *cache_compact(PyObject *, PyObject *const *o, Py_ssize_t n) {
     if (to.scalar_type() != at::kInt || to.sizes() != table.sizes() || to.stride(1) != 1)
       bad("page_table_out must be int32 of page_table's shape with unit-stride rows");
     int32_t *rp = ints(&ref_out, "ref_out", {ref.numel()}), *up = ints(used, "used_out", {1});
+    int32_t *tp = static_cast<int32_t *>(to.data_ptr());
+    const int64_t stride = to.stride(0);
+    void *wp = ws.data_ptr();
+    const size_t wn = ws.nbytes();
     const Launch l(dev, o[9]);
-    return PyLong_FromLong(masked_gqa_cache_compact(&cache.c, static_cast<int32_t *>(to.data_ptr()), to.stride(0), rp,
-                                                    up, ws.data_ptr(), ws.nbytes(), l.stream));
+    return status_of([&] {
+      return masked_gqa_cache_compact(&cache.c, tp, stride, rp, up, wp, wn, l.stream);
+    });
   });
 }
 
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FAST(prefill_window), FAST(decode_window),        FAST(decode_tree), FAST(cache_append),
-                         FAST(cache_fork),     FAST(cache_workspace_size), FAST(cache_compact), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {FAST(prefill_window), FAST(decode_window), FAST(decode_tree), FAST(cache_append),
+                         FAST(cache_workspace_size), FAST(cache_fork), FAST(cache_compact),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mgqa_bind", nullptr, -1, methods};
 
 }  // namespace

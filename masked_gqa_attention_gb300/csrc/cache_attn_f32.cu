@@ -3,7 +3,7 @@
 // ways to cut the work and the producer warps of cache_attn_tma.cu.
 //
 // A key is 8 D bytes and 4 R D operations: up to R = 4 the reads bound it (64 rows
-// of up to 32768 slots, window 4096, R = 4: 329 us, 90 % of the copy rate; R = 8:
+// of up to 32768 slots, window 4096, R = 4: 329 us, 89 % of the copy rate; R = 8:
 // 640), beyond that the CUDA cores. Two forms:
 //   16 rows or fewer: a thread has 4 rows and one key of the scores (a quarter,
 //     half or all of the head dim), then 4 rows and 4 features of the values
@@ -450,11 +450,17 @@ mgqa_status launch_many(const CUtensorMap (&maps)[4], const TmaParams &tp, const
 
 template <int D>
 mgqa_status launch_d(const CUtensorMap (&maps)[4], const TmaParams &tp, const CacheAttnLaunch &how, cudaStream_t s) {
-  const int R = tp.a.R;  // the smallest block that holds the rows
-  if (R <= 4) return launch_few<D, 1>(maps, tp, how, s);
-  if (R <= 8) return launch_few<D, 2>(maps, tp, how, s);
-  if (R <= 16) return launch_few<D, 4>(maps, tp, how, s);
-  if (R <= 32) return launch_many<D, 4>(maps, tp, how, s);
+  // the smallest block that holds the rows, or a smaller one of its kind on short
+  // calls (one row of 16 heads over 2, window 1024, D = 64: 7.6 us in blocks of 4
+  // rows, 9.0 in one of 8; 8 drafts over 4096 slots 11.5 in blocks of 32, 15.7 in
+  // one of 64, 20 in blocks of 8)
+  const CacheAttnParams &p = tp.a;
+  int rows = p.R <= 4 ? 4 : p.R <= 8 ? 8 : p.R <= 16 ? 16 : p.R <= 32 ? 32 : 64;
+  if (p.T <= 32) rows = short_block(p, D * 4, how.sms, rows, rows > 16 ? 32 : 4);
+  if (rows == 4) return launch_few<D, 1>(maps, tp, how, s);
+  if (rows == 8) return launch_few<D, 2>(maps, tp, how, s);
+  if (rows == 16) return launch_few<D, 4>(maps, tp, how, s);
+  if (rows == 32) return launch_many<D, 4>(maps, tp, how, s);
   return launch_many<D, 8>(maps, tp, how, s);
 }
 

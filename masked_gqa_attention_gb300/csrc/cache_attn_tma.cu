@@ -2,7 +2,7 @@
 // heads, or a small tree), and for more in blocks of 64 where tensor memory is
 // not used: the formulas of cache_attn.cu.
 //
-// Reads bound it (64 rows of up to 32768 keys, window 4096: 160 us, 92 % of the
+// Reads bound it (64 rows of up to 32768 keys, window 4096: 158 us, 92 % of the
 // copy rate; in pages of one slot, row by row, 221). Two producer warps
 // (cache_producer.cuh) bring each 64-key tile into a ring of 96 KB, as TMA boxes
 // of gcd(page_size, 64) rows x 64 columns, 128-byte swizzled; two CTAs an SM keep
@@ -48,7 +48,7 @@ struct Cfg {
     float join[WK > 1 ? (WK - 1) * WM : 1][16][WK > 1 ? 66 : 1];  // half a result of the warps that join
     float wm[WK][ROWS], wl[WK][ROWS];
     float2 ml[ROWS];  // the CTA's (m, l), read by its cluster
-    Drafts<WM == 4 ? kMaxDrafts : 32> drafts;  // (up to 32 rows: no more drafts)
+    Drafts<WM == 4 ? kMaxDrafts : 32> drafts;  // (smaller blocks: up to 32)
     LocateScratch<kThreads> scratch;
     uint2 ok[STAGES];  // which keys of a stage's tile count
     uint64_t full[STAGES], empty[STAGES];
@@ -387,8 +387,14 @@ mgqa_status launch_t(const CUtensorMap (&maps)[4], TmaParams tp, const CacheAttn
 
 template <typename T, int D>
 mgqa_status launch_d(const CUtensorMap (&maps)[4], const TmaParams &tp, const CacheAttnLaunch &how, cudaStream_t s) {
-  if (tp.a.R <= 16) return launch_t<T, D, 1>(maps, tp, how, s);
-  if (tp.a.R <= 32) return launch_t<T, D, 2>(maps, tp, how, s);
+  // the smallest block that holds the rows, or a smaller one on short calls (8 drafts
+  // of 16 heads over 2, 4096 slots, D = 128: 10.5 us in blocks of 16 rows, 12.5 in
+  // one of 64; D = 64: 8.6 and 8.4)
+  const CacheAttnParams &p = tp.a;
+  int rows = p.R <= 16 ? 16 : p.R <= 32 ? 32 : 64;
+  if (p.T <= 32) rows = short_block(p, D * 2, how.sms, rows, 16);
+  if (rows == 16) return launch_t<T, D, 1>(maps, tp, how, s);
+  if (rows == 32) return launch_t<T, D, 2>(maps, tp, how, s);
   return launch_t<T, D, 4>(maps, tp, how, s);
 }
 

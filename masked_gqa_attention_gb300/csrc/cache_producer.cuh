@@ -9,6 +9,8 @@
 //     are the same. A copy costs ~8 instructions.
 #pragma once
 
+#include <algorithm>
+
 #include "cache_sched.cuh"
 #include "tc_ptx.cuh"
 
@@ -316,6 +318,19 @@ inline int cluster_size(const CacheAttnParams &p, int row_bytes, int sms) {
   int s = 1;
   while (s < 16 && s < tiles && units * s * 2 <= sms) s *= 2;
   return s;
+}
+
+// Short calls leave SMs idle, so a unit's rows go in smaller blocks (half of
+// `rows`, and again, down to `least`) while the clusters of all units stay as
+// large and fit on the SMs: a block's CTAs read the same keys, from the L2, but
+// each has less to compute.
+inline int short_block(const CacheAttnParams &p, int row_bytes, int sms, int rows, int least) {
+  if (!short_call(p, row_bytes)) return rows;
+  CacheAttnParams q = p;
+  q.tile_shift = 6;
+  auto ctas = [&](int r) { return (int64_t)p.B * p.Hkv * ((p.R + r - 1) / r) * std::min<int64_t>(16, most_tiles(q)); };
+  while (rows > least && ctas(rows / 2) <= sms) rows /= 2;
+  return rows;
 }
 
 }  // namespace mgqa
