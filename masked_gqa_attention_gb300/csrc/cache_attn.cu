@@ -102,16 +102,18 @@ mgqa_status launch_merge(const CacheAttnParams &p, int grid, cudaStream_t s) {
 }
 template <typename T, int D>
 mgqa_status launch_merge(const CacheAttnParams &p, int block_rows, int grid, cudaStream_t s) {
-  switch (block_rows) {
-    case 4: return launch_merge<T, D, 4>(p, grid, s);
-    case 8: return launch_merge<T, D, 8>(p, grid, s);
-    case 16: return launch_merge<T, D, 16>(p, grid, s);
-    case 32: return launch_merge<T, D, 32>(p, grid, s);
-    case 64: return launch_merge<T, D, 64>(p, grid, s);
-    case 128: return launch_merge<T, D, 128>(p, grid, s);
-    case 256: return launch_merge<T, D, 256>(p, grid, s);
-    default: return fail(MGQA_ERR_UNSUPPORTED, "merge: blocks of %d rows", block_rows);
+  if (block_rows == 16) return launch_merge<T, D, 16>(p, grid, s);
+  if (block_rows == 32) return launch_merge<T, D, 32>(p, grid, s);
+  if (block_rows == 64) return launch_merge<T, D, 64>(p, grid, s);
+  if constexpr (sizeof(T) == 4) {
+    if (block_rows == 4) return launch_merge<T, D, 4>(p, grid, s);
+    if (block_rows == 8) return launch_merge<T, D, 8>(p, grid, s);
+    if (block_rows == 48) return launch_merge<T, D, 48>(p, grid, s);
+  } else {
+    if (block_rows == 128) return launch_merge<T, D, 128>(p, grid, s);
+    if (block_rows == 256) return launch_merge<T, D, 256>(p, grid, s);
   }
+  return fail(MGQA_ERR_UNSUPPORTED, "merge: blocks of %d rows", block_rows);
 }
 
 }  // namespace

@@ -9,7 +9,7 @@
 //     half or all of the head dim), then 4 rows and 4 features of the values
 //     (every 8th, 4th or 2nd key), so each K and V element is read from shared
 //     memory once per 4 rows; two block barriers a tile.
-//   32 or 64 rows: the register tiles of simt_fp32.cuh.
+//   32, 48 or 64 rows: the register tiles of simt_fp32.cuh.
 #include <algorithm>
 #include <cmath>
 
@@ -63,7 +63,7 @@ struct FewCfg {
   static_assert(smem <= 227 * 1024, "shared memory");
 };
 
-// ---- 32 or 64 rows ---------------------------------------------------------------------
+// ---- 32, 48 or 64 rows ---------------------------------------------------------------------
 
 template <int D, int RPG>
 struct ManyCfg {
@@ -455,12 +455,21 @@ mgqa_status launch_d(const CUtensorMap (&maps)[4], const TmaParams &tp, const Ca
   // rows, 9.0 in one of 8; 8 drafts over 4096 slots 11.5 in blocks of 32, 15.7 in
   // one of 64, 20 in blocks of 8)
   const CacheAttnParams &p = tp.a;
-  int rows = p.R <= 4 ? 4 : p.R <= 8 ? 8 : p.R <= 16 ? 16 : p.R <= 32 ? 32 : 64;
-  if (p.T <= 32) rows = short_block(p, D * 4, how.sms, rows, rows > 16 ? 32 : 4);
+  int rows = p.R <= 4 ? 4 : p.R <= 8 ? 8 : 16;
+  if (p.R > 16) {
+    // more rows: the blocks that cost least together; a tile of one costs as its rows
+    // and 6 more (32 rows 343, 64 rows 635 us for the same tiles; 16 trees of 24
+    // drafts and 4 heads, 96 rows: 1270 us in two blocks of 64, 946 in two of 48)
+    auto cost = [&](int r) { return (int64_t)((p.R + r - 1) / r) * (r + 6); };
+    rows = cost(48) < cost(64) ? 48 : 64;
+    if (cost(32) < cost(rows)) rows = 32;
+  }
+  if (p.T <= 32 && rows != 48) rows = short_block(p, D * 4, how.sms, rows, rows > 16 ? 32 : 4);
   if (rows == 4) return launch_few<D, 1>(maps, tp, how, s);
   if (rows == 8) return launch_few<D, 2>(maps, tp, how, s);
   if (rows == 16) return launch_few<D, 4>(maps, tp, how, s);
   if (rows == 32) return launch_many<D, 4>(maps, tp, how, s);
+  if (rows == 48) return launch_many<D, 6>(maps, tp, how, s);
   return launch_many<D, 8>(maps, tp, how, s);
 }
 

@@ -1,6 +1,6 @@
 // Register-tiled fp32 products of the CUDA-core attention kernels: 64 keys per
 // tile, K and V in shared memory as TMA leaves them (boxes of 64 rows x 32
-// floats, 128-byte swizzled), 256 threads over ROWS = 32 or 64 query rows.
+// floats, 128-byte swizzled), 256 threads over ROWS = 32, 48 or 64 query rows.
 //
 // A multiply-add reads its operands from registers, so the shared-memory reads
 // per product fall with a thread's tile, which is as large as the registers
@@ -15,7 +15,8 @@
 // rate on 4096 queries x 16 heads, window 4096: 1854 us), since eight warps, all
 // an SM's registers, do not cover one another's latencies. One group with tiles
 // of 4 x 4 and no block barrier: 16 trees of 24 drafts over 8192 slots 1387 us
-// against 1270, of 6 drafts 435 against 343, that prefill 1820.
+// against 1270 (in blocks of 64 rows), of 6 drafts 435 against 343, that prefill
+// 1820.
 #pragma once
 
 #include "common.cuh"

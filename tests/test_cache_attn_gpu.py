@@ -216,6 +216,9 @@ def test_many_rows(M, dtype):
     Case([300, 65], 40, 28, 4, 64, dtype, page=64, window=100, sinks=3).run(M)
     Case([130], 3, 200, 1, 64, dtype, page=16).run(M)
     Case([9000, 20], 70, 24, 8, 128, dtype, page=0).run(M)
+    for T in (10, 12, 24, 26):  # 40, 48, 96 and 104 rows, short calls and long ones
+        Case([333, 64, 0], T, 8, 2, 64, dtype, page=16).run(M)
+        Case([20000, 17], T, 32, 8, 128, dtype, page=32, cap=40000, live=[T, 3]).run(M)
 
 
 @pytest.mark.parametrize("dtype,D", [(BF, 128), (HF, 64), (FP, 64), (FP, 128)])
