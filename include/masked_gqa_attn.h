@@ -302,7 +302,8 @@ MGQA_API mgqa_status masked_gqa_attn_decode_append_rope(
  * that the window and the sinks reach are read. Same types, head dims, strides
  * and errors as masked_gqa_attn_prefill; with kv_len or segment ids the forms
  * are combined with AND, so a padded row keeps positions 0 .. Lk - 1. Keys and
- * values behind kv_len may hold anything; all others have to be finite. */
+ * values behind kv_len may hold anything; all others have to be finite. A stride
+ * of 0 over more than one element (k, v; q in 16 bits) is MGQA_ERR_UNSUPPORTED. */
 MGQA_API mgqa_status masked_gqa_attn_prefill_window(const mgqa_args *args, int32_t window,
                                                     int32_t sinks, cudaStream_t stream);
 

@@ -325,6 +325,11 @@ mgqa_status masked_gqa_attn_prefill_window(const mgqa_args *args, int32_t window
   mgqa_status st = mgqa::validate(args, false);
   if (st != MGQA_OK) return st;
   if ((st = mgqa::check_window(window, sinks, 1)) != MGQA_OK) return st;
+  // the tiles come by TMA, which knows no stride of 0 (fp32 reads q without it)
+  if (!mgqa::plain_strides(args->k_stride, args->B, args->Hkv, args->Lk) ||
+      !mgqa::plain_strides(args->v_stride, args->B, args->Hkv, args->Lk) ||
+      (args->dtype != MGQA_FP32 && !mgqa::plain_strides(args->q_stride, args->B, args->Hq, args->Lq)))
+    return mgqa::fail(MGQA_ERR_UNSUPPORTED, "windowed prefill: a tensor expanded over a dimension");
   const mgqa::WindowRule win{window < mgqa::kWidestWindow ? window : mgqa::kWidestWindow,
                              sinks < args->Lk ? sinks : args->Lk};
   if (args->dtype != MGQA_FP32) return mgqa::launch_prefill_tc(*args, stream, mgqa::FusedRope(), win);

@@ -400,10 +400,6 @@ mgqa_status launch_d(const CUtensorMap (&maps)[4], const TmaParams &tp, const Ca
 
 }  // namespace
 
-bool plain_strides(const int64_t *st, int64_t n0, int64_t n1, int64_t n2) {
-  return (st[0] || n0 == 1) && (st[1] || n1 == 1) && (st[2] || n2 == 1);
-}
-
 bool cache_attn_maps(const CacheAttnParams &p, mgqa_dtype dt, int D, int tile, CUtensorMap (&maps)[4], int &box_rows) {
   const int cols = dt == MGQA_FP32 ? 32 : 64;  // 128 bytes
   const int n0 = p.table ? p.num_pages : p.B, n2 = p.table ? p.page_size : p.cap;

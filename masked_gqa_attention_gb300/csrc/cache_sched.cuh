@@ -89,9 +89,6 @@ mgqa_status launch_cache_attn_f32(const CacheAttnParams &p, int D, const CacheAt
 bool cache_attn_tc_takes(const CacheAttnParams &p);
 mgqa_status launch_cache_attn_tc(const CacheAttnParams &p, mgqa_dtype dt, int D, const CacheAttnLaunch &how,
                                  cudaStream_t s);
-// Whether TMA can describe a tensor of [n0][n1][n2] rows: a stride of 0 (a
-// broadcast) over more than one element it cannot.
-bool plain_strides(const int64_t *st, int64_t n0, int64_t n1, int64_t n2);
 // Tensor maps of the cache (boxes of `box_rows` slots: the largest power of two
 // up to `tile` that divides the page) and of the drafts; box_rows 0: the call is
 // fetched row by row, without maps.

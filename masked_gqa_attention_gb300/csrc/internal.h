@@ -164,6 +164,12 @@ mgqa_status pack_pair(bool unpack, mgqa_dtype dt, int B, int H, int D, const voi
 bool make_tma_map_4d(CUtensorMap *m, mgqa_dtype dt, const void *base, int B, int H, int L, int D,
                      const int64_t *st, int box_x, int box_y, bool swizzle128);
 
+// Whether TMA can describe a tensor of [n0][n1][n2] rows: a stride of 0 (a
+// broadcast) over more than one element it cannot.
+inline bool plain_strides(const int64_t *st, int64_t n0, int64_t n1, int64_t n2) {
+  return (st[0] || n0 == 1) && (st[1] || n1 == 1) && (st[2] || n2 == 1);
+}
+
 // The general form: `rank` dimensions, innermost first (its stride is 1; the
 // others' in elements).
 bool make_tma_map(CUtensorMap *m, mgqa_dtype dt, const void *base, int rank, const int64_t *dims,

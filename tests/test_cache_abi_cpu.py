@@ -223,6 +223,21 @@ def test_cache_steps_refuse(L):
     assert fork(L, c) == INVALID and append(L, c) == INVALID
 
 
+def test_windowed_prefill_refuses_expanded_tensors(L):
+    for field, dtypes in (("k_stride", (M.MGQA_BF16, M.MGQA_FP32)), ("v_stride", (M.MGQA_FP16, M.MGQA_FP32)),
+                          ("q_stride", (M.MGQA_BF16, M.MGQA_FP16))):
+        for dt in dtypes:
+            for i in range(3):
+                a = args(9)
+                a.dtype = dt
+                getattr(a, field)[i] = 0
+                assert L.masked_gqa_attn_prefill_window(ctypes.byref(a), 4, 0, None) == UNSUPPORTED
+    a = args(1, B=1)  # one element: the stride says nothing
+    a.q_stride[0] = a.k_stride[0] = a.q_stride[2] = 0
+    if not torch.cuda.is_available():
+        assert L.masked_gqa_attn_prefill_window(ctypes.byref(a), 4, 0, None) == CUDA
+
+
 def test_binding_takes_all_arguments_or_none():
     calls = M._calls()
     for f in (calls.prefill_window, calls.decode_window, calls.decode_tree, calls.cache_append, calls.cache_fork,
