@@ -310,7 +310,8 @@ MGQA_API mgqa_status masked_gqa_attn_prefill_window(const mgqa_args *args, int32
 /* A cache in pages: slot j of request b lies in page table[b*table_stride +
  * j/page_size] at slot j % page_size. With pages, args->k and args->v are the
  * pools [num_pages][Hkv][page_size][D] (k_stride, v_stride = page, head, slot)
- * and args->Lk is max_pages * page_size. Any page_size >= 1. Entries of slots
+ * and args->Lk is max_pages * page_size. Any page_size >= 1 (multiples of 8 are
+ * fetched faster). Entries of slots
  * that no query sees (behind kv_len, or between the sinks and the window) are
  * not looked at. An entry outside [0, num_pages) that is needed is a device
  * error; its slots count as masked. */

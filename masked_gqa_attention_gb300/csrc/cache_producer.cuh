@@ -5,8 +5,10 @@
 //     one warp for both was slower than the reads.)
 //   rows by 16-byte asynchronous copies, for any other page size and for tensors
 //     expanded over a dimension (TMA knows no stride of 0): a lane finds where its
-//     rows lie, the warp copies them into the boxes' own layout, so the consumers
-//     are the same. A copy costs ~8 instructions.
+//     rows lie, then eight lanes copy a line of 128 bytes of a row, into the boxes'
+//     own layout, so the consumers are the same. (Whole rows a pass, with the row's
+//     address exchanged for every 16 bytes: 16 trees of 24 drafts 111 us, 105 so; one
+//     fp32 row, 64 requests, window 4096, 609 and 418.)
 #pragma once
 
 #include <algorithm>
