@@ -36,7 +36,7 @@ class Bar:
 
 
 class Model:
-    def __init__(self, NT, KS, VS, pieces, rng, shared_p=False):
+    def __init__(self, NT, KS, VS, pieces, rng, shared_p=False, rows=False):
         self.NT, self.KS, self.VS, self.pieces, self.rng = NT, KS, VS, pieces, rng
         self.SB = 2 if NT == 1 else 1
         self.PB = 1 if shared_p else self.SB
@@ -55,6 +55,7 @@ class Model:
         for i in range(4):
             b["pready", i] = Bar(1)
         self.pipe, self.copies = [], []  # tensor pipe (in order), copies (any order)
+        self.rows, self.landed = rows, set()
         self.state = {"k": {}, "v": {}, "q": None, "s": {}, "o": {}}
 
     def wait(self, name, phase):
@@ -68,6 +69,28 @@ class Model:
                 yield from self.wait((empty, st), use - 1)
             self.copies.append(((full, st), full[0], st, it))
             yield
+
+    def producer_rows(self, full, empty, n):
+        """Row by row: a tile is told by its warp, when the next one has been started or ahead of a wait."""
+        told = 0
+
+        def tell(upto):
+            nonlocal told
+            while any((full[0], i) not in self.landed for i in range(told, upto)):
+                yield
+            for i in range(told, upto):
+                self.b[full, i % n].arrive()
+            told = max(told, upto)
+
+        for it in range(sum(self.pieces)):
+            st, use = it % n, it // n
+            if use and not self.b[empty, st].passes(use - 1):
+                yield from tell(it)
+                yield from self.wait((empty, st), use - 1)
+            self.copies.append((None, full[0], st, it))
+            yield
+            yield from tell(it)
+        yield from tell(sum(self.pieces))
 
     def loader(self):
         for k in range(len(self.pieces) + 1):
@@ -171,7 +194,10 @@ class Model:
             self.state[what][st] = tag if what != "q" else None
             if what == "q":
                 self.state["q"] = dict(self.state["q"] or {}, **{str(st): tag})
-            self.b[name].arrive()
+            if name is None:
+                self.landed.add((what, tag))
+            else:
+                self.b[name].arrive()
             return True
         op = self.pipe.pop(0)
         if op[0] == "commit":
@@ -191,7 +217,8 @@ class Model:
 
     def run(self):
         self.state["q"] = {}
-        roles = {"k": self.producer("kfull", "kempty", self.KS), "v": self.producer("vfull", "vempty", self.VS),
+        feed = self.producer_rows if self.rows else self.producer
+        roles = {"k": feed("kfull", "kempty", self.KS), "v": feed("vfull", "vempty", self.VS),
                  "mma": self.mma(), "q": self.loader()}
         roles.update({f"soft{t}": self.softmax(t) for t in range(self.NT)})
         speed = {r: self.rng.choice([0.05, 0.3, 1.0]) for r in [*roles, "async"]}
@@ -219,11 +246,12 @@ def pieces_of(rng):
     return [rng.choice([1, 1, 2, 3, 7]) for _ in range(rng.randint(1, 7))]
 
 
+@pytest.mark.parametrize("rows", [False, True])
 @pytest.mark.parametrize("NT,KS,VS", [(1, 2, 3), (1, 4, 4), (2, 2, 2), (2, 4, 4)])
-def test_every_schedule_is_sound(NT, KS, VS):
+def test_every_schedule_is_sound(NT, KS, VS, rows):
     for seed in range(150):
         rng = random.Random(seed * 31 + NT * 7 + KS)
-        Model(NT, KS, VS, pieces_of(rng), rng).run()
+        Model(NT, KS, VS, pieces_of(rng), rng, rows=rows).run()
 
 
 def test_one_barrier_for_two_score_buffers_is_found():
