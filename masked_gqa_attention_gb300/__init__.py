@@ -20,6 +20,7 @@ Entry points (same names as the C ABI):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.util
 import math
@@ -655,16 +656,17 @@ def _i32(x):
     return max(-1, min(x, 0x7fffffff))
 
 
-def _kept(ws, stream):
-    """A workspace allocated for a call on `stream`: not given out again before
-    the call is done there."""
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            handle = _stream_handle(stream)
-            stream = torch.cuda.ExternalStream(handle, device=ws.device) if handle \
-                else torch.cuda.default_stream(ws.device)
-        ws.record_stream(stream)
-    return ws
+def _allocating_on(stream, device):
+    """Context in which PyTorch allocates for a call on `stream` (None: the current
+    one). The allocator hands a block out again as soon as the stream it belongs to
+    has work queued behind its last use: a block of the current stream, used on
+    another, may still be read or written by work queued here."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream_handle(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def masked_gqa_attn_prefill_window(q, k, v, out=None, *, window, sinks=0, causal=True, scale=None,
@@ -721,7 +723,8 @@ def masked_gqa_attn_decode_window(q, k_cache, v_cache, kv_len, out=None, *, wind
     if out is None:
         out = torch.empty_like(q)
     if workspace is None:
-        workspace = _kept(new_cache_attn_workspace(q.device), stream)
+        with _allocating_on(stream, q.device):
+            workspace = new_cache_attn_workspace(q.device)
     status = (_native or _calls()).decode_window(q, k_cache, v_cache, kv_len, out, window, sinks, page_table,
                                                  workspace, scale, lse, dev_error, stream)
     if status:
@@ -742,7 +745,8 @@ def masked_gqa_attn_decode_tree(q, k_cache, v_cache, k_new, v_new, kv_len, out=N
     if out is None:
         out = torch.empty_like(q)
     if workspace is None:
-        workspace = _kept(new_cache_attn_workspace(q.device), stream)
+        with _allocating_on(stream, q.device):
+            workspace = new_cache_attn_workspace(q.device)
     status = (_native or _calls()).decode_tree(q, k_cache, v_cache, k_new, v_new, kv_len, out, tree_bits, tree_len,
                                                window, sinks, page_table, workspace, scale, lse, dev_error, stream)
     if status:
@@ -776,7 +780,8 @@ def masked_gqa_cache_workspace_size(k_cache, v_cache, page_table, ref, n=0) -> i
 
 def _pages_ws(k_cache, v_cache, page_table, ref, n, stream):
     size = masked_gqa_cache_workspace_size(k_cache, v_cache, page_table, ref, n)
-    return _kept(torch.empty(size, dtype=torch.uint8, device=k_cache.device), stream)
+    with _allocating_on(stream, k_cache.device):
+        return torch.empty(size, dtype=torch.uint8, device=k_cache.device)
 
 
 def masked_gqa_cache_fork(k_cache, v_cache, page_table, kv_len, ref, src, dst, *, extra=0,
