@@ -363,12 +363,46 @@ def _stream_handle(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _allocating_on(stream, device):
+    """Context in which PyTorch allocates for a call on `stream` (None: the current
+    one). The allocator hands a block out again as soon as the stream it belongs to
+    has work queued behind its last use: a block of the current stream, used on
+    another, may still be read or written by work queued here."""
+    if stream is None or device.type != "cuda":
+        return contextlib.nullcontext()
+    handle = _stream_handle(stream)
+    if handle == torch.cuda.current_stream(device).cuda_stream:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def _output(new, device, stream):
+    """An output new() of a call on `stream`."""
+    if stream is None:
+        return new()
+    with _allocating_on(stream, device):
+        out = new()
+    if out.is_cuda:
+        out.record_stream(torch.cuda.current_stream(device))  # where the caller goes on with it
+    return out
+
+
+def _new_out(q, stream):
+    return _output(lambda: torch.empty_like(q), q.device, stream)
+
+
+def _new_tensor(shape, dtype, device, stream):
+    return _output(lambda: torch.empty(shape, dtype=dtype, device=device), device, stream)
+
+
 def masked_gqa_attn_prefill(q, k, v, out=None, *, scale=None, mask_bits=None, kv_len=None,
                             seg_q=None, seg_k=None, lse=None, dev_error=None, causal=False,
                             stream=None):
     """Masked GQA attention over full sequences (bidirectional unless causal); returns out."""
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_out(q, stream)
     a = make_args(q, k, v, out, scale=scale, mask_bits=mask_bits, kv_len=kv_len, seg_q=seg_q,
                   seg_k=seg_k, lse=lse, dev_error=dev_error, causal=causal)
     _check(lib().masked_gqa_attn_prefill(ctypes.byref(a), _stream_handle(stream)))
@@ -404,7 +438,7 @@ def masked_gqa_attn_decode(q, k, v, out=None, *, workspace: Optional[torch.Tenso
                            dev_error=None, stream=None):
     """One query per row (q [B, Hq, 1, D]) over a static cache k/v [B, Hkv, Lk, D]."""
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_out(q, stream)
     a = make_args(q, k, v, out, scale=scale, mask_bits=mask_bits, kv_len=kv_len, seg_q=seg_q,
                   seg_k=seg_k, lse=lse, dev_error=dev_error)
     wp, wn = _workspace(workspace)
@@ -418,7 +452,7 @@ def masked_gqa_attn_decode_static(q, k, v, out=None, *, scale=None, mask_bits=No
     may not allocate device memory: the kernel's scratch is its own on-chip
     shared memory, so nothing is allocated and calls do not share state."""
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_out(q, stream)
     a = make_args(q, k, v, out, scale=scale, mask_bits=mask_bits, kv_len=kv_len, seg_q=seg_q,
                   seg_k=seg_k, lse=lse, dev_error=dev_error)
     _check(lib().masked_gqa_attn_decode_static(ctypes.byref(a), _stream_handle(stream)))
@@ -434,7 +468,7 @@ def masked_gqa_attn_decode_append(q, k_cache, v_cache, k_new, v_new, kv_len, out
     then q [B, Hq, 1, D] attends over slots 0..kv_len[b]; kv_len_out (int32 [B],
     optional, not kv_len itself) receives kv_len + 1."""
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_out(q, stream)
     a = make_args(q, k_cache, v_cache, out, scale=scale, kv_len=kv_len, lse=lse,
                   dev_error=dev_error)
     for name, t in (("k_new", k_new), ("v_new", v_new)):
@@ -466,8 +500,8 @@ def masked_gqa_pack_pair(a, b, *, stream=None):
         _dev(t, name, a.dtype)
     B, H, La, D = a.shape
     Lb = b.shape[2]
-    packed = torch.empty((B, H, La + Lb, D), dtype=a.dtype, device=a.device)
-    seg = torch.empty((B, La + Lb), dtype=torch.int32, device=a.device)
+    packed = _new_tensor((B, H, La + Lb, D), a.dtype, a.device, stream)
+    seg = _new_tensor((B, La + Lb), torch.int32, a.device, stream)
     _check(lib().masked_gqa_pack_pair(_dtype_code(a), B, H, D, a.data_ptr(), _st3(a), La,
                                       b.data_ptr(), _st3(b), Lb, packed.data_ptr(),
                                       _st3(packed), seg.data_ptr(), _stream_handle(stream)))
@@ -478,8 +512,8 @@ def masked_gqa_unpack_pair(packed, La, *, stream=None):
     """Split a packed [B, H, La + Lb, D] output into ([B, H, La, D], [B, H, Lb, D])."""
     _dev(packed, "packed")
     B, H, L, D = packed.shape
-    a = torch.empty((B, H, La, D), dtype=packed.dtype, device=packed.device)
-    b = torch.empty((B, H, L - La, D), dtype=packed.dtype, device=packed.device)
+    a = _new_tensor((B, H, La, D), packed.dtype, packed.device, stream)
+    b = _new_tensor((B, H, L - La, D), packed.dtype, packed.device, stream)
     _check(lib().masked_gqa_unpack_pair(_dtype_code(packed), B, H, D, packed.data_ptr(),
                                         _st3(packed), a.data_ptr(), _st3(a), La, b.data_ptr(),
                                         _st3(b), L - La, _stream_handle(stream)))
@@ -582,7 +616,7 @@ def masked_gqa_attn_prefill_rope(q, k, v, out=None, *, inv_freq, positions=None,
     """masked_gqa_attn_prefill with the rotary embedding (and optional RMS
     norm) applied to q inside the kernel; k must already be rotated. Returns out."""
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_out(q, stream)
     a = make_args(q, k, v, out, scale=scale, mask_bits=mask_bits, kv_len=kv_len, seg_q=seg_q,
                   seg_k=seg_k, lse=lse, dev_error=dev_error, causal=causal)
     if positions is not None and tuple(positions.shape) != (q.shape[0], q.shape[2]):
@@ -607,7 +641,7 @@ def masked_gqa_attn_decode_append_rope(q, k_cache, v_cache, k_new, v_new, kv_len
     new token's position (positions int32 [B], default kv_len); the cache
     receives the rotated key row. Returns out."""
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_out(q, stream)
     a = make_args(q, k_cache, v_cache, out, scale=scale, kv_len=kv_len, lse=lse,
                   dev_error=dev_error)
     for name, t in (("k_new", k_new), ("v_new", v_new)):
@@ -656,19 +690,6 @@ def _i32(x):
     return max(-1, min(x, 0x7fffffff))
 
 
-def _allocating_on(stream, device):
-    """Context in which PyTorch allocates for a call on `stream` (None: the current
-    one). The allocator hands a block out again as soon as the stream it belongs to
-    has work queued behind its last use: a block of the current stream, used on
-    another, may still be read or written by work queued here."""
-    if stream is None:
-        return contextlib.nullcontext()
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = _stream_handle(stream)
-        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
-    return torch.cuda.stream(stream)
-
-
 def masked_gqa_attn_prefill_window(q, k, v, out=None, *, window, sinks=0, causal=True, scale=None,
                                    mask_bits=None, kv_len=None, seg_q=None, seg_k=None, lse=None,
                                    dev_error=None, stream=None):
@@ -677,7 +698,7 @@ def masked_gqa_attn_prefill_window(q, k, v, out=None, *, window, sinks=0, causal
     counts; without causal also ahead of it) and the first `sinks` keys, AND
     whatever the other mask forms allow. Returns out."""
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_out(q, stream)
     if mask_bits is None and seg_q is None and seg_k is None:
         status = (_native or _calls()).prefill_window(q, k, v, out, kv_len, scale, lse, dev_error, causal, window, sinks,
                                                       stream)
@@ -721,7 +742,7 @@ def masked_gqa_attn_decode_window(q, k_cache, v_cache, kv_len, out=None, *, wind
     [pages, Hkv, page_size, D] with page_table int32 [B, max_pages].
     workspace: new_cache_attn_workspace() (None: allocated here). Returns out."""
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_out(q, stream)
     if workspace is None:
         with _allocating_on(stream, q.device):
             workspace = new_cache_attn_workspace(q.device)
@@ -743,7 +764,7 @@ def masked_gqa_attn_decode_tree(q, k_cache, v_cache, k_new, v_new, kv_len, out=N
     drafts; the rows behind them give 0 and -inf. The drafts are not written to
     the cache (masked_gqa_cache_append). Returns out."""
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_out(q, stream)
     if workspace is None:
         with _allocating_on(stream, q.device):
             workspace = new_cache_attn_workspace(q.device)

@@ -105,3 +105,79 @@ def test_own_workspaces_of_two_streams_are_apart(M):
         b(out=ob, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(oa, wa) and torch.equal(ob, wb)
+
+
+def outputs():
+    """Calls that allocate their output, by name: a function of the module that gives (a call of a stream, the shape
+    of its output)."""
+    def attn(Lq, Lk=256):
+        return randn(2, 4, Lq, 64), randn(2, 2, Lk, 64), randn(2, 2, Lk, 64)
+
+    def plain(name, Lq, **kw):
+        def make(M):
+            q, k, v = attn(Lq)
+            more = {x: y() for x, y in kw.items()}
+            return lambda s: getattr(M, name)(q, k, v, stream=s, **more)
+        return make
+
+    def append(M):
+        q, k, v = attn(1)
+        new, lens = randn(2, 2, 1, 64), i32([100, 7])
+        return lambda s: M.masked_gqa_attn_decode_append(q, k, v, new, new, lens, stream=s)
+
+    def append_rope(M):
+        q, k, v = attn(1)
+        new, lens, f = randn(2, 2, 1, 64), i32([100, 7]), torch.rand(32, device="cuda")
+        return lambda s: M.masked_gqa_attn_decode_append_rope(q, k, v, new, new, lens, inv_freq=f, stream=s)
+
+    def window(M):
+        q, k, v = attn(1)
+        lens, ws = i32([200, 7]), M.new_cache_attn_workspace()
+        return lambda s: M.masked_gqa_attn_decode_window(q, k, v, lens, window=64, workspace=ws, stream=s)
+
+    def tree(M):
+        q, k, v = attn(3)
+        new, lens, ws = randn(2, 2, 3, 64), i32([200, 7]), M.new_cache_attn_workspace()
+        return lambda s: M.masked_gqa_attn_decode_tree(q, k, v, new, new, lens, workspace=ws, stream=s)
+
+    def pack(M):
+        a = randn(2, 4, 100, 64)
+        return lambda s: M.masked_gqa_pack_pair(a, a, stream=s)[0]
+
+    def unpack(M):
+        a = randn(2, 4, 200, 64)
+        return lambda s: M.masked_gqa_unpack_pair(a, 90, stream=s)[0]
+
+    rope = dict(inv_freq=lambda: torch.rand(32, device="cuda"))
+    return dict(prefill=plain("masked_gqa_attn_prefill", 256), prefill_rope=plain("masked_gqa_attn_prefill_rope", 256, **rope),
+                prefill_window=plain("masked_gqa_attn_prefill_window", 256, window=lambda: 32),
+                decode=plain("masked_gqa_attn_decode", 1), decode_static=plain("masked_gqa_attn_decode_static", 1),
+                append=append, append_rope=append_rope, decode_window=window, decode_tree=tree, pack=pack, unpack=unpack)
+
+
+@pytest.mark.parametrize("name", list(outputs()))
+def test_own_output_spares_memory_in_use(M, name):
+    call = outputs()[name](M)
+    want = call(None).clone()
+    s = torch.cuda.Stream()
+    for on in (s, s.cuda_stream):
+        total = sum_in_flight(want.numel() * want.element_size())
+        out = call(on)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        assert int(total) == 7 * want.numel() * want.element_size()
+
+
+def test_output_lives_while_the_current_stream_reads_it(M):
+    call = outputs()["prefill"](M)
+    want = call(None).float().sum()
+    s = torch.cuda.Stream()
+    out = call(s)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda._sleep(DELAY)
+    total, shape = out.float().sum(), out.shape
+    del out
+    with torch.cuda.stream(s):  # s may not get the block again before that sum is done
+        junk = [torch.full(shape, 1e4, dtype=BF, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert float(total) == float(want) and len(junk) == 4
