@@ -390,7 +390,11 @@ fork_plan_kernel(const __grid_constant__ ForkParams p) {
     if (lane == 0) req_s[i] = n;
   }
   __syncthreads();
-  if (tid < p.n) req = req_s[tid];
+  // A pair that wants more pages than there are is not served, whatever it wants: its
+  // request counts as one more than that, so that all of them add up within 32 bits
+  // (uncut, 128 rows of 2^24 entries would not).
+  static_assert((int64_t)kMaxForks * (kMaxPages + 1) < 0x7fffffff, "the requests' sum");
+  if (tid < p.n) req = min(req_s[tid], c.num_pages + 1);
   // the free pages: every thread owns a run of words
   const int per = (W + kPlanThreads - 1) / kPlanThreads;
   int mine = 0, avail = 0, total = 0;
