@@ -386,12 +386,13 @@ typedef struct {
 /* Appends T new rows, or the chosen ones of them, to every request and layer:
  * for i < count[b] (count NULL: T) slot kv_len[b] + i gets row index[b*T + i]
  * (index NULL: i) of k_new and v_new ([layers][rows][Hkv][T][D], strides layer,
- * batch, head, row). kv_len_out[b] = kv_len[b] + count[b]; it must not alias
- * kv_len. A request whose count is outside [0, T], or whose rows would pass its
- * last slot, appends nothing and keeps its length; an index outside [0, T) or a
- * missing page leaves that slot as it was; each sets *dev_error. No other slot
- * is written. Requests must not share the pages that they append to (fork sees
- * to that), and the new rows must not lie in the cache. */
+ * batch, head, row). kv_len_out[b] = kv_len[b] + count[b]; it must not overlap
+ * kv_len, count, index or the page table. A request whose count is outside
+ * [0, T], or whose rows would pass its last slot, appends nothing and keeps its
+ * length; an index outside [0, T) or a missing page leaves that slot as it was;
+ * each sets *dev_error. No other slot is written. Requests must not share the
+ * pages that they append to (fork sees to that), and the new rows must not lie in
+ * the cache. */
 MGQA_API mgqa_status masked_gqa_cache_append(const mgqa_cache *cache, const void *k_new,
                                              const void *v_new, const int64_t *k_new_stride,
                                              const int64_t *v_new_stride, int32_t T,

@@ -780,7 +780,8 @@ def masked_gqa_cache_append(k_cache, v_cache, k_new, v_new, kv_len, kv_len_out, 
     """Append rows of k_new / v_new [layers, B, Hkv, T, D] (4-D with a 4-D
     cache) to every request: slot kv_len[b] + i of the cache gets row
     index[b, i] (int32 [B, T]; None: i) for i < count[b] (int32 [B]; None: T).
-    kv_len_out (int32 [B], not kv_len) receives kv_len + count. The cache is
+    kv_len_out (int32 [B], apart from kv_len, index, count and page_table)
+    receives kv_len + count. The cache is
     [layers, B, Hkv, slots, D], or in pages with page_table int32
     [B, max_pages]. Returns kv_len_out."""
     status = (_native or _calls()).cache_append(k_cache, v_cache, k_new, v_new, kv_len, kv_len_out, index, count,

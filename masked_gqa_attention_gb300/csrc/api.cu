@@ -202,6 +202,12 @@ mgqa_status validate_tree(const mgqa_args *a, const mgqa_tree *tree) {
   return MGQA_OK;
 }
 
+// Do n ints at a and m ints at b share any? (a null b shares none)
+bool ints_overlap(const int32_t *a, int64_t n, const int32_t *b, int64_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return b && x < y + 4 * (uintptr_t)m && y < x + 4 * (uintptr_t)n;
+}
+
 mgqa_status check_workspace(const void *ws, size_t have, size_t need) {
   if (!ws || !aligned(ws, 16)) return fail(MGQA_ERR_INVALID_ARG, "workspace missing or not 16-byte aligned");
   if (have < need) return fail(MGQA_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", have, need);
@@ -369,10 +375,15 @@ mgqa_status masked_gqa_cache_append(const mgqa_cache *cache, const void *k_new, 
   mgqa_status st = mgqa::validate_cache(cache, false);
   if (st != MGQA_OK) return st;
   if (!cache->kv_len || !kv_len_out) return mgqa::fail(MGQA_ERR_INVALID_ARG, "kv_len and kv_len_out are required");
-  if (kv_len_out == cache->kv_len) return mgqa::fail(MGQA_ERR_INVALID_ARG, "kv_len_out must not alias kv_len");
   if (!mgqa::aligned(kv_len_out, 4) || !mgqa::aligned(index, 4) || !mgqa::aligned(count, 4))
     return mgqa::fail(MGQA_ERR_INVALID_ARG, "kv_len_out, index or count misaligned");
   if (T < 1 || T > (1 << 24)) return mgqa::fail(MGQA_ERR_INVALID_ARG, "T must be in [1, 2^24]");
+  // one block writes a request's new length while others still read the inputs
+  const int64_t rows = cache->rows, entries = (rows - 1) * cache->table_stride + cache->max_pages;
+  if (mgqa::ints_overlap(kv_len_out, rows, cache->kv_len, rows) ||
+      mgqa::ints_overlap(kv_len_out, rows, count, rows) || mgqa::ints_overlap(kv_len_out, rows, index, rows * T) ||
+      mgqa::ints_overlap(kv_len_out, rows, cache->page_table, entries))
+    return mgqa::fail(MGQA_ERR_INVALID_ARG, "kv_len_out must not overlap kv_len, count, index or the page table");
   if ((st = mgqa::check_new_rows(k_new, v_new, k_new_stride, v_new_stride, 4, cache->dtype == MGQA_FP32 ? 4 : 2)) !=
       MGQA_OK)
     return st;
