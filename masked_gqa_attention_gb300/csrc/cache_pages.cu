@@ -69,10 +69,11 @@ struct AppendParams {
   int32_t block_rows;  // new rows of a block
   const int32_t *index, *count;
   int32_t *kv_len_out;
-  // kv_len and kv_len_out share no 128-byte line. Otherwise kv_len is read past the
-  // L1: the next kernel is resident before this one ends, and a line left there
-  // could give it an old kv_len_out. (Read so always, 32768 rows take 46 us, not 42.)
-  int32_t lens_apart;
+  // kv_len_out shares no 128-byte line with kv_len, count, index or the page table.
+  // Otherwise those are read past the L1: the next kernel is resident before this one
+  // ends, and a line left there could give it an old kv_len_out. (kv_len alone read
+  // so always: 32768 rows take 46 us, not 42.)
+  int32_t ints_apart;
 };
 
 __global__ void __launch_bounds__(kAppendThreads)
@@ -82,8 +83,9 @@ append_kernel(const __grid_constant__ AppendParams p) {
   grid_dependency_wait();
   allow_dependents();
   const int64_t cap = c.table ? (int64_t)c.max_pages * c.page_size : c.page_size;
-  const int n = p.lens_apart ? __ldg(c.kv_len + b) : __ldcg(c.kv_len + b);
-  const int cnt = p.count ? __ldg(p.count + b) : p.T;
+  const auto load = [&](const int32_t *x) { return p.ints_apart ? __ldg(x) : __ldcg(x); };
+  const int n = load(c.kv_len + b);
+  const int cnt = p.count ? load(p.count + b) : p.T;
   const bool bad = n < 0 || cnt < 0 || cnt > p.T || (int64_t)n + cnt > cap;
   // the block's rows from t0 on, all heads of each. Without a count the new rows
   // are read ahead of what tells where they go (the length, then the page).
@@ -93,7 +95,7 @@ append_kernel(const __grid_constant__ AppendParams p) {
     const int tl = i / per, rem = i - tl * per, t = t0 + tl;
     const int h = rem / c.pieces, piece = rem - h * c.pieces;
     if (p.count && (bad || t >= cnt)) break;
-    const int from = p.index ? __ldg(p.index + (int64_t)b * p.T + t) : t;
+    const int from = p.index ? load(p.index + (int64_t)b * p.T + t) : t;
     const bool has = (unsigned)from < (unsigned)p.T;
     uint4 kx, vx;
     if (has) {
@@ -107,7 +109,7 @@ append_kernel(const __grid_constant__ AppendParams p) {
     int page = b, slot = j;
     if (c.table) {
       const int pi = j / c.page_size;
-      page = valid_page(c, __ldg(c.table + (int64_t)b * c.table_stride + pi));
+      page = valid_page(c, load(c.table + (int64_t)b * c.table_stride + pi));
       slot = j - pi * c.page_size;
     }
     if (has && page >= 0) {
@@ -602,8 +604,12 @@ mgqa_status launch_cache_append(const mgqa_cache &c, const void *k_new, const vo
     p.vns[t] = vs[t] * es;
   }
   p.T = T; p.index = index; p.count = count; p.kv_len_out = kv_len_out;
-  const uintptr_t line = 128, in = reinterpret_cast<uintptr_t>(c.kv_len), to = reinterpret_cast<uintptr_t>(kv_len_out);
-  p.lens_apart = (in + 4 * (uintptr_t)c.rows - 1) / line < to / line || (to + 4 * (uintptr_t)c.rows - 1) / line < in / line;
+  const auto apart = [&](const int32_t *x, int64_t n) {  // no line of x[0, n) holds a new length
+    const uintptr_t line = 128, in = reinterpret_cast<uintptr_t>(x), to = reinterpret_cast<uintptr_t>(kv_len_out);
+    return !x || (in + 4 * (uintptr_t)n - 1) / line < to / line || (to + 4 * (uintptr_t)c.rows - 1) / line < in / line;
+  };
+  p.ints_apart = apart(c.kv_len, c.rows) && apart(count, c.rows) && apart(index, (int64_t)c.rows * T) &&
+                 apart(c.page_table, (int64_t)(c.rows - 1) * c.table_stride + c.max_pages);
   const int64_t per = (int64_t)c.Hkv * p.c.pieces;
   if (per > (1 << 20)) return fail(MGQA_ERR_UNSUPPORTED, "cache append: rows of more than 16 MB");
   p.block_rows = (int32_t)std::max<int64_t>(1, kAppendThreads / per);

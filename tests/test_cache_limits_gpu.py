@@ -34,3 +34,26 @@ def test_fork_requests_that_add_up_past_32_bits(M):
     assert ref.nonzero().flatten().tolist() == [5] and int(ref[5]) == 1
     assert int(table[0, 0]) == 5 and int((table != -1).sum()) == 1
     assert torch.equal(k, k1) and torch.equal(v, v1)
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_counts_and_tables_beside_the_lengths(M, paged):
+    # the step's small integers in one buffer, so in one line of 128 bytes: each step reads what the one before wrote
+    B, cap, D, steps = 4, 700, 64, 300
+    k = torch.zeros(B, 1, cap, D, dtype=BF, device="cuda")
+    v = torch.zeros_like(k)
+    new = torch.randn(steps, B, 1, 1, D, device="cuda").to(BF)
+    ints = torch.zeros(32, dtype=torch.int32, device="cuda")
+    lens, count, index, table = ints[:8].view(2, B), ints[8:12], ints[12:16].view(B, 1), None
+    count.fill_(1)
+    if paged:
+        table = ints[16:20].view(B, 1)
+        table.copy_(torch.tensor([[2], [0], [3], [1]], dtype=torch.int32))
+    q, ws = torch.randn(B, 1, 1, D, device="cuda").to(BF), M.new_cache_attn_workspace()
+    outs = torch.empty(steps, B, 1, 1, D, dtype=BF, device="cuda")
+    for i in range(steps):
+        old, now = lens[i % 2], lens[1 - i % 2]
+        M.masked_gqa_cache_append(k, v, new[i], new[i], old, now, index=index, count=count, page_table=table)
+        M.masked_gqa_attn_decode_window(q, k, v, now, outs[i], window=1, page_table=table, workspace=ws)
+    assert lens.tolist() == [[steps] * B, [steps - 1] * B]
+    assert torch.equal(outs, new)  # a window of one: the token just appended
