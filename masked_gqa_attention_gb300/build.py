@@ -83,12 +83,21 @@ def _run(cmd, what):
         raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
 
 
+def _compile_bind(obj):
+    """bind.cpp to obj; returns the flags of its link."""
+    os.makedirs(os.path.dirname(obj), exist_ok=True)
+    flags, link = _bind_flags()
+    _run(["g++", *flags, "-c", os.path.join(CSRC, "bind.cpp"), "-o", obj], "bind.cpp")
+    return link
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(),
           variants=("release", "debug")) -> str:
-    """Compile and link the requested variants (both by default); returns the
-    product library's path."""
+    """Compile and link the requested variants (both by default), and the Python
+    side of the product library with it; returns the product library's path. The
+    libraries are in place before a failure of the Python side is raised."""
     todo = [v for v in variants if force or not up_to_date(VARIANTS[v][0])]
-    bind = force or not up_to_date(BIND)
+    bind = "release" in variants and (force or not up_to_date(BIND))
     if not todo and not bind:
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
@@ -114,13 +123,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(),
     workers = max(1, min(len(jobs) + 1, os.cpu_count() or 8))
     bind_obj = os.path.join(OBJ_DIR, "bind.o")
     with cf.ThreadPoolExecutor(max_workers=workers) as ex:
-        if bind:
-            os.makedirs(OBJ_DIR, exist_ok=True)
-            flags, link = _bind_flags()
-            bound = ex.submit(_run, ["g++", *flags, "-c", os.path.join(CSRC, "bind.cpp"), "-o", bind_obj], "bind.cpp")
+        bound = ex.submit(_compile_bind, bind_obj) if bind else None
         objs = list(ex.map(compile_one, jobs))
-        if bind:
-            bound.result()
     for v in todo:
         lib = VARIANTS[v][0]
         vobjs = [o for (vv, _), o in zip(jobs, objs) if vv == v]
@@ -130,7 +134,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(),
         if r.returncode != 0:
             raise RuntimeError(f"link failed ({v}):\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, lib)
-    if bind:
+    if bound:
+        link = bound.result()
         tmp = BIND + f".tmp{os.getpid()}"
         _run(["g++", "-shared", "-o", tmp, bind_obj, *link], "link of _mgqa_bind.so")
         os.replace(tmp, BIND)
