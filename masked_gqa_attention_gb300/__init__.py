@@ -708,6 +708,9 @@ def masked_gqa_attn_prefill_window(q, k, v, out=None, *, window, sinks=0, causal
                 raise ValueError(f"tensors on {t.device} and {q.device}")
         a = make_args(q, k, v, out, scale=scale, mask_bits=mask_bits, kv_len=kv_len, seg_q=seg_q,
                       seg_k=seg_k, lse=lse, dev_error=dev_error, causal=causal)
+        for name, t, n in (("kv_len", kv_len, q.shape[0]), ("dev_error", dev_error, 1)):
+            if t is not None and (tuple(t.shape) != (n,) or not t.is_contiguous()):
+                raise ValueError(f"{name} must be contiguous int32 [{n}]")
         with torch.cuda.device(q.device):
             status = lib().masked_gqa_attn_prefill_window(ctypes.byref(a), _i32(window), _i32(sinks),
                                                           _stream_handle(stream))
