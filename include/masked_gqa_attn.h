@@ -420,7 +420,7 @@ MGQA_API size_t masked_gqa_cache_workspace_size(const mgqa_cache *cache, int32_t
  * for is not carried out: dst is left empty (src != dst) or unchanged; a pair
  * with src or dst out of range, or with the dst of an earlier pair, is skipped;
  * each sets *dev_error. Table entries outside [0, num_pages) count as -1.
- * num_pages <= 2^20. */
+ * num_pages <= 2^20, and page_size rows of a head at most 2^34 bytes. */
 MGQA_API mgqa_status masked_gqa_cache_fork(const mgqa_cache *cache, int32_t n, const int32_t *src,
                                            const int32_t *dst, int32_t extra, void *workspace,
                                            size_t workspace_bytes, cudaStream_t stream);
@@ -429,7 +429,8 @@ MGQA_API mgqa_status masked_gqa_cache_fork(const mgqa_cache *cache, int32_t n, c
  * >= U moves, in ascending order, to the i-th free page of index < U; every
  * layer's keys and values are copied, page_table_out and ref_out get the
  * renamed tables (they may be page_table and ref themselves) and *used_out,
- * when given, U. Pages moved away from keep their contents and become free. */
+ * when given, U. Pages moved away from keep their contents and become free.
+ * Limits as for masked_gqa_cache_fork. */
 MGQA_API mgqa_status masked_gqa_cache_compact(const mgqa_cache *cache, int32_t *page_table_out,
                                               int64_t table_out_stride, int32_t *ref_out,
                                               int32_t *used_out, void *workspace,

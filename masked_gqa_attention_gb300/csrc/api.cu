@@ -247,6 +247,8 @@ mgqa_status validate_cache(const mgqa_cache *c, bool counted) {
   if (counted) {
     if (!c->ref || !aligned(c->ref, 4)) return fail(MGQA_ERR_INVALID_ARG, "ref missing or misaligned");
     if (c->num_pages > kMaxPages) return fail(MGQA_ERR_UNSUPPORTED, "more than %d pages", kMaxPages);
+    if ((int64_t)c->page_size * (int64_t)(c->D * es / 16) > kMaxPagePieces)
+      return fail(MGQA_ERR_UNSUPPORTED, "a page of more than 2^34 bytes of a head");
   }
   return MGQA_OK;
 }

@@ -139,7 +139,7 @@ MGQA_DEV void copy_slots(char *base, const int64_t *st, int64_t layer, int a, in
   char *dst = base + layer * st[0] + (int64_t)b * st[1];
   const bool rows_run = st[3] == pieces * 16;
   int per = slots * pieces;  // pieces of a run
-  if (rows_run && slots == page_size && st[2] == (int64_t)page_size * st[3] && (int64_t)per * heads < 0x7fffffff) {
+  if (rows_run && slots == page_size && st[2] == (int64_t)page_size * st[3] && (int64_t)per * heads <= kMaxPagePieces) {
     per *= heads;
     heads = 1;
   }
@@ -534,11 +534,12 @@ compact_apply_kernel(const __grid_constant__ CompactParams p) {
   allow_dependents();
   const int used = p.state[0], moves = p.state[1];
   // the copies: a segment is one (move, layer, K or V)
-  const int64_t segs = (int64_t)moves * c.layers * 2;
+  const int64_t both = (int64_t)c.layers * 2, segs = moves * both;
   const int group = p.warp_segments ? 32 : kCompactThreads;
   const int64_t step = (int64_t)gridDim.x * (kCompactThreads / group);
   for (int64_t s = (int64_t)blockIdx.x * (kCompactThreads / group) + tid / group; s < segs; s += step) {
-    const int mv = (int)(s / (c.layers * 2)), r = (int)(s % (c.layers * 2));
+    const int64_t r = s % both;
+    const int mv = (int)(s / both);
     copy_slots((r & 1) ? c.v : c.k, (r & 1) ? c.vs : c.ks, r >> 1, p.from[mv], p.to[mv], c.Hkv, c.page_size,
                c.page_size, c.pieces, tid % group / 32, group / 32);
   }

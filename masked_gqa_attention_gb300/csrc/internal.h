@@ -133,6 +133,7 @@ constexpr int kMaxDraftsHost = 256;  // drafted tokens of a request
 
 // The cache's own steps (cache_pages.cu).
 constexpr int kMaxPages = 1 << 20;  // bounds the planning kernels' bitmaps
+constexpr int kMaxPagePieces = 1 << 30;  // 16-byte pieces of a head's page that is copied: counted in 32 bits
 constexpr int kMaxForks = 1024;     // pairs of a fork call: one thread each
 size_t cache_pages_workspace_bytes(const mgqa_cache &c, int n);
 mgqa_status launch_cache_append(const mgqa_cache &c, const void *k_new, const void *v_new,

@@ -3,7 +3,7 @@
 import pytest
 
 import masked_gqa_attention_gb300 as M
-from test_cache_abi_cpu import BASE, CUDA, INVALID, append, cache, no_gpu
+from test_cache_abi_cpu import BASE, CUDA, INVALID, UNSUPPORTED, append, cache, compact, fork, no_gpu, ref
 
 
 @pytest.fixture(scope="module")
@@ -46,3 +46,21 @@ def test_new_lengths_of_the_static_cache(L):
     c.page_table, c.max_pages, c.table_stride, c.num_pages = None, 0, 0, c.rows
     assert append(L, c, out=c.kv_len + 4 * c.rows) == CUDA
     assert append(L, c, out=c.kv_len + 4 * c.rows - 4) == INVALID
+
+
+@pytest.mark.parametrize("page,D,dtype", [(1 << 24, 2048, M.MGQA_BF16), (1 << 24, 513 * 8, M.MGQA_FP16),
+                                          (1 << 24, 260, M.MGQA_FP32), ((1 << 23) + 1, 1024, M.MGQA_BF16)])
+def test_copied_pages_past_32_bits_are_refused(L, page, D, dtype):
+    c = cache()
+    c.page_size, c.max_pages, c.D, c.dtype = page, 1, D, dtype
+    assert fork(L, c) == UNSUPPORTED and compact(L, c) == UNSUPPORTED
+    assert L.masked_gqa_cache_workspace_size(ref(c), 3) == 0
+
+
+@no_gpu
+def test_the_largest_copied_pages_are_taken(L):
+    c = cache()
+    c.page_size, c.max_pages, c.D = 1 << 24, 1, 512
+    assert fork(L, c) == CUDA and compact(L, c) == CUDA
+    c.D = 2048  # (no page is copied)
+    assert append(L, c) == CUDA
