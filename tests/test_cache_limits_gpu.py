@@ -57,3 +57,45 @@ def test_counts_and_tables_beside_the_lengths(M, paged):
         M.masked_gqa_attn_decode_window(q, k, v, now, outs[i], window=1, page_table=table, workspace=ws)
     assert lens.tolist() == [[steps] * B, [steps - 1] * B]
     assert torch.equal(outs, new)  # a window of one: the token just appended
+
+
+def test_the_largest_pool_is_packed_in_order(M):
+    # 2^20 pages: which page moves where is fixed, for the tables, the counts and the contents
+    n = 1 << 20
+    mark = (torch.arange(n, device="cuda") % 127).to(BF)
+    k = torch.zeros(1, n, 1, 1, 8, dtype=BF, device="cuda")
+    k[0, :, 0, 0, 0] = mark
+    v = k * 2
+    used = [5, n - 1 - 1000, n - 3, n - 2, n - 1]  # five pages: 5 stays behind the holes 0 .. 4 and moves, as the others do
+    ref = torch.zeros(n, dtype=torch.int32, device="cuda")
+    ref[torch.tensor(used, device="cuda")] = i32([3, 1, 4, 1, 5])
+    table, n_used, err = i32([[n - 1, 5, n - 3, -1], [n - 2, n - 1001, 5, n - 1]]), i32([-1]), i32([0])
+    M.masked_gqa_cache_compact(k, v, table, ref, used_out=n_used, dev_error=err)
+    assert table.tolist() == [[4, 0, 2, -1], [3, 1, 0, 4]] and int(n_used) == 5 and int(err) == 0
+    assert ref[:5].tolist() == [3, 1, 4, 1, 5] and int(ref.sum()) == 14
+    want = mark.clone()
+    want[:5] = mark[torch.tensor(used, device="cuda")]
+    assert torch.equal(k[0, :, 0, 0, 0], want) and torch.equal(v[0, :, 0, 0, 0], 2 * want)
+    assert not k[..., 1:].any() and not v[..., 1:].any()
+
+
+def test_the_largest_pool_is_forked_in_order(M):
+    # the fresh pages are the lowest free ones in the order of the pairs, over the whole pool
+    n = 1 << 20
+    k = torch.zeros(1, n, 1, 2, 8, dtype=BF, device="cuda")
+    k[0, :, 0, :, 0] = (torch.arange(n, device="cuda") % 127).to(BF)[:, None]
+    v = k * 2
+    ref = torch.ones(n, dtype=torch.int32, device="cuda")
+    free = [7, 32767, 500000, n - 1]
+    ref[torch.tensor(free, device="cuda")] = 0
+    table = i32([[n - 2, n - 5, -1], [-1] * 3, [-1] * 3, [n - 3, -1, -1]])
+    lens, err = i32([3, 0, 0, 2]), i32([0])
+    M.masked_gqa_cache_fork(k, v, table, lens, ref, i32([0, 3, 0]), i32([1, 2, 3]), extra=1, dev_error=err)
+    # request 1: a shared page and a copy of the half one; request 2: a shared page and a new one; request 3 as 1
+    assert table.tolist() == [[n - 2, n - 5, -1], [n - 2, 7, -1], [n - 3, 32767, -1], [n - 2, 500000, -1]]
+    assert lens.tolist() == [3, 3, 2, 3] and int(err) == 0
+    assert ref[torch.tensor([n - 2, n - 5, n - 3, *free], device="cuda")].tolist() == [3, 1, 1, 1, 1, 1, 0]
+    for x, f in ((k, 1), (v, 2)):
+        for page, src in ((7, n - 5), (500000, n - 5)):
+            assert x[0, page, 0, 0, 0] == f * (src % 127) and x[0, page, 0, 1, 0] == f * (page % 127)
+        assert x[0, 32767, 0, :, 0].tolist() == [f * (32767 % 127)] * 2
