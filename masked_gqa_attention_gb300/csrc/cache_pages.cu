@@ -12,10 +12,12 @@
 //   own, joined by programmatic dependent launches:
 //     fork    -- gather (stages the sources' table rows, gives back and takes
 //                shares by integer atomics, whose order cannot matter; a block
-//                per pair, or, when the rows are few, the planning block itself:
-//                one launch less), plan (one block: free pages as a bitmap in
-//                shared memory, requests and free pages matched by prefix
-//                sums), apply (table rows, lengths, and the copies);
+//                per pair), plan (one block: free pages as a bitmap in shared
+//                memory, requests and free pages matched by prefix sums), apply
+//                (table rows, lengths, and the copies). (The planning block
+//                gathering by itself, a launch less: no call was faster. 4 pairs
+//                of 33 entries 9.5 us against 8.8, of 252 14.5 against 8.9;
+//                32 pairs of 64 12.9 against 11.2.)
 //     compact -- plan (one block: the used pages as a bitmap, moves by prefix
 //                sums over its words) and apply (copies, table, counts).
 //   One block is enough for the plan: a pool of 2^16 pages is 256 KB of counts.
@@ -255,34 +257,38 @@ struct ForkParams {
   int32_t *stage;  // [n][max_pages]
   Pair *pairs;     // [n]
   int32_t *fresh;  // [num_pages]
-  int32_t gather;  // the planning block gathers itself
 };
 
 constexpr int kForkThreads = 256;
 
-// Pair i: its numbers, its source's row staged, pages given back and shares
-// taken, by `threads` threads of which this is `t`; taken: an earlier pair has
-// this dst.
-MGQA_DEV void gather_pair(const ForkParams &p, int i, int s, int d, bool taken, int t, int threads) {
+// Pair i: its numbers, its source's row staged, pages given back and shares taken.
+__global__ void __launch_bounds__(kForkThreads)
+fork_gather_kernel(const __grid_constant__ ForkParams p) {
   const Pool &c = p.c;
-  const bool skip = taken || d < 0 || d >= c.rows || s < -1 || s >= c.rows;
+  const int i = blockIdx.x, tid = threadIdx.x;
+  grid_dependency_wait();
+  allow_dependents();
+  const int s = __ldg(p.src + i), d = __ldg(p.dst + i);
+  bool taken = false;  // an earlier pair has this dst
+  for (int k = tid; k < i; k += kForkThreads) taken = taken || __ldg(p.dst + k) == d;
+  const bool skip = __syncthreads_or(taken) || d < 0 || d >= c.rows || s < -1 || s >= c.rows;
   int len = 0;
   const int64_t cap = (int64_t)c.max_pages * c.page_size;
   if (!skip && s >= 0) {
     len = __ldg(c.kv_len + s);
     if (len < 0 || len > cap) {
-      if (t == 0) report_error(c.err, MGQA_ERR_INVALID_ARG);
+      if (tid == 0) report_error(c.err, MGQA_ERR_INVALID_ARG);
       len = len < 0 ? 0 : (int)cap;
     }
   }
   const int full = len / c.page_size;
-  if (t == 0) {
+  if (tid == 0) {
     if (skip) report_error(c.err, MGQA_ERR_INVALID_ARG);
     const int64_t need = s < 0 ? 0 : ((int64_t)len + p.extra + c.page_size - 1) / c.page_size;
     p.pairs[i] = Pair{s, skip ? -1 : d, len, full, need > c.max_pages ? -1 : (int32_t)need, 0, 0, -1};
   }
   if (skip) return;
-  for (int j = t; j < c.max_pages; j += threads) {
+  for (int j = tid; j < c.max_pages; j += kForkThreads) {
     const int e = s >= 0 ? valid_page(c, __ldg(c.table + (int64_t)s * c.table_stride + j)) : -1;
     p.stage[(int64_t)i * c.max_pages + j] = e;
     if (s != d) {
@@ -293,39 +299,16 @@ MGQA_DEV void gather_pair(const ForkParams &p, int i, int s, int d, bool taken, 
   }
 }
 
-__global__ void __launch_bounds__(kForkThreads)
-fork_gather_kernel(const __grid_constant__ ForkParams p) {
-  const int i = blockIdx.x, tid = threadIdx.x;
-  grid_dependency_wait();
-  allow_dependents();
-  const int s = __ldg(p.src + i), d = __ldg(p.dst + i);
-  bool taken = false;
-  for (int k = tid; k < i; k += kForkThreads) taken = taken || __ldg(p.dst + k) == d;
-  gather_pair(p, i, s, d, __syncthreads_or(taken), tid, kForkThreads);
-}
-
 // dynamic shared memory: the bitmap of free pages
 __global__ void __launch_bounds__(kPlanThreads)
 fork_plan_kernel(const __grid_constant__ ForkParams p) {
   extern __shared__ uint32_t bits[];
-  __shared__ int scratch[33], req_s[kMaxForks], dst_s[kMaxForks];
+  __shared__ int scratch[33], req_s[kMaxForks];
   const Pool &c = p.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int W = (c.num_pages + 31) / 32;
   grid_dependency_wait();
   allow_dependents();
-  if (p.gather) {
-    if (tid < p.n) dst_s[tid] = __ldg(p.dst + tid);
-    __syncthreads();
-    for (int i = warp; i < p.n; i += kPlanThreads / 32) {
-      const int d = dst_s[i];
-      bool taken = false;
-      for (int k = lane; k < i; k += 32) taken = taken || dst_s[k] == d;
-      gather_pair(p, i, __ldg(p.src + i), d, __any_sync(0xffffffffu, taken), lane, 32);
-    }
-    __threadfence();  // the counts were changed by atomics, the rows by other threads
-    __syncthreads();
-  }
   used_bitmap(c, bits);
   __syncthreads();
   for (int w = tid; w < W; w += kPlanThreads)
@@ -637,13 +620,8 @@ mgqa_status launch_cache_fork(const mgqa_cache &c, int n, const int32_t *src, co
   static std::atomic<uint64_t> attr{0};
   mgqa_status st = ensure_smem_attr(fork_plan_kernel, kMaxPages / 8, attr, "fork planning kernel");
   if (st != MGQA_OK) return st;
-  // few table entries: the planning block stages them itself, a launch less (one
-  // block is slow at more: 2304 entries 17 us, against 4.5 + 7.3 us apart)
-  p.gather = (int64_t)n * c.max_pages <= 1024;
-  if (!p.gather) {
-    st = launched(launch_pdl(fork_gather_kernel, dim3(n), dim3(kForkThreads), 0, s, p), "cache fork");
-    if (st != MGQA_OK) return st;
-  }
+  st = launched(launch_pdl(fork_gather_kernel, dim3(n), dim3(kForkThreads), 0, s, p), "cache fork");
+  if (st != MGQA_OK) return st;
   st = launched(launch_pdl(fork_plan_kernel, dim3(1), dim3(kPlanThreads), smem, s, p), "cache fork");
   if (st != MGQA_OK) return st;
   return launched(launch_pdl(fork_apply_kernel, dim3(n, c.layers, 2), dim3(kForkThreads), 0, s, p), "cache fork");
