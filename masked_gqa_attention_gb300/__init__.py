@@ -17,6 +17,7 @@ Entry points (same names as the C ABI):
   * :func:`masked_gqa_attn_decode_tree` -- drafted tokens over such a cache;
   * :func:`masked_gqa_cache_append`, :func:`masked_gqa_cache_fork`,
     :func:`masked_gqa_cache_compact` -- the cache's own steps.
+Outputs and workspaces that are not given are allocated for the call's `stream`.
 """
 from __future__ import annotations
 

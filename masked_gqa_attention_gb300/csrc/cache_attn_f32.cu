@@ -3,7 +3,7 @@
 // ways to cut the work and the producer warps of cache_attn_tma.cu.
 //
 // A key is 8 D bytes and 4 R D operations: up to R = 4 the reads bound it (64 rows
-// of up to 32768 slots, window 4096, R = 4: 329 us, 89 % of the copy rate; R = 8:
+// of up to 32768 slots, window 4096, R = 4: 323 us, 90 % of the copy rate; R = 8:
 // 640), beyond that the CUDA cores. Two forms:
 //   16 rows or fewer: a thread has 4 rows and one key of the scores (a quarter,
 //     half or all of the head dim), then 4 rows and 4 features of the values

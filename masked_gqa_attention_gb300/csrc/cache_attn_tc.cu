@@ -27,11 +27,12 @@
 // between the pieces, cost ~4000 cycles a piece.) Values of keys that do not
 // count (the end of a request, a missing page) are cleared in shared memory by
 // the MMA warp before the product, on the tiles that have any.
-// 61 drafts, 4 requests of 82020 slots on average, 32 heads over 8 (NT = 2): 267 us,
-// 74 % of the copy rate and 0.66 of the bf16 rate with both needed at once; a tile
+// 61 drafts, 4 requests of 82020 slots on average, 32 heads over 8 (NT = 2): 270 us,
+// 73 % of the copy rate and 0.64 of the bf16 rate with both needed at once (72 to 76 %
+// from 75078 to 131004 slots; 6 % longer in runs of seconds); a tile
 // takes ~4000 cycles against 3000 of reads and 2048 of products, the chain of P V,
 // S and softmax of the prefill kernel. 24 drafts, 16 requests of 4739 slots on
-// average (NT = 1): 66 us, 70 %; the rest is the start and the join.
+// average (NT = 1): 67 us, 70 %; the rest is the start and the join.
 // Every wait is bounded and reports MGQA_ERR_TIMEOUT.
 #include <algorithm>
 #include <cmath>
@@ -696,7 +697,9 @@ mgqa_status launch_d(const TcCacheParams &tp, mgqa_dtype dt, const CacheAttnLaun
   // but covering for one another between units. The second is ahead while the
   // call is not long (64 drafts, 32 heads over 8: one request of up to 4096 tokens
   // 22.0 and 14.9 us; 16 of up to 2048 57 and 48; 16 of up to 8192 99 and 108; 4 of
-  // up to 131072 266 and 396; D = 64, 16 of about 8100 117 and 113).
+  // up to 131072 266 and 396; D = 64, 16 of about 8100 117 and 113). The lengths are
+  // on the device, so the capacity decides: one request of 4000 tokens takes 18.4 us
+  // in a table for 4096 slots and 24.3 in one for 131072.
   CacheAttnParams q = tp.a;
   q.tile_shift = 6;
   const int64_t reads = (int64_t)q.B * q.Hkv * most_tiles(q) * (kTile * D * 4);

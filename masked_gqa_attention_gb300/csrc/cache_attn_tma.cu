@@ -3,7 +3,7 @@
 // not used: the formulas of cache_attn.cu.
 //
 // Reads bound it (64 rows of up to 32768 keys, window 4096: 158 us, 92 % of the
-// copy rate; in pages of one slot, row by row, 221). Two producer warps
+// copy rate; in pages of one slot, row by row, 222). Two producer warps
 // (cache_producer.cuh) bring each 64-key tile into a ring of 96 KB, as TMA boxes
 // of gcd(page_size, 64) rows x 64 columns, 128-byte swizzled; two CTAs an SM keep
 // up to 192 KB in flight. Four consumer warps run the products on mma.sync with no
@@ -229,7 +229,8 @@ cache_attn_tma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             l[1] += s[nn][2] + s[nn][3];
           }
           // O += P V; P is rounded to the 16-bit type (l keeps the fp32 weights), as
-          // the tensor cores' operand: half a step per weight, unbiased over keys.
+          // the tensor cores' operand: half a step per weight, unbiased over keys
+          // (fp16 below 2^-14 of the row's largest weight: 2^-25 of that one).
           // Values of keys that do not count are cleared (their rows may hold anything).
 #pragma unroll
           for (int kp = 0; kp < KW / 16; ++kp) {
@@ -424,8 +425,11 @@ bool cache_attn_maps(const CacheAttnParams &p, mgqa_dtype dt, int D, int tile, C
 
 // Up to 32 rows; up to 64 for short calls, where a cluster saves a launch: on
 // longer ones the tensor-memory kernel is ahead (64 rows, 4 requests of up to
-// 131072: 305 us here, 234 us there; one request of up to 4096: 13 and 19 us).
-// And what that kernel does not take.
+// 131072: 305 us here, 234 us there). One request, full: 2 KV heads, D = 64, 4096
+// slots 11.2 us here, 12.9 there; 8 KV heads, D = 128, 256 slots 11.2 and 13.1, but
+// 1024 slots 18.0 and 12.8 and 4096 23.7 and 17.0 (eight units leave no SMs for
+// smaller blocks), which a rule on the reads alone misses. And what that kernel
+// does not take.
 bool cache_attn_tma_takes(const CacheAttnParams &p, mgqa_dtype dt, int D) {
   return p.R <= 32 || (p.R <= 64 && short_call(p, D * 2)) || !cache_attn_tc_takes(p);
 }

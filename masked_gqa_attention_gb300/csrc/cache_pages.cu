@@ -5,7 +5,7 @@
 // append: one pass, a block per (layer, request, run of rows); a thread has
 //   one 16-byte piece of K and of V in flight, read in the order in which a
 //   projection leaves them ([T][Hkv][D]) and written as whole D-rows. (32768 rows
-//   of 8 x 128 bf16: eight pieces a thread 64.6 us, four 51.7, two 45.5, one 42.2:
+//   of 8 x 128 bf16: eight pieces a thread 64.6 us, four 51.7, two 45.5, one 43:
 //   smaller blocks overlap their look-ups with other blocks' copies.)
 // fork and compact: the page bookkeeping is integer work on a few arrays whose
 //   result every block needs, so it runs ahead of the copies in kernels of its

@@ -307,8 +307,10 @@ MGQA_DEV void join_cluster(const CacheAttnParams &p, const Pieces &pieces, const
 }
 
 // Clusters for short calls: whether the reads take at most ~10 us at 6.8 TB/s,
-// whatever the lengths are, and how many CTAs a unit gets then: no more CTAs
-// than SMs in all (a second one on an SM keeps whole clusters waiting).
+// whatever the lengths are (8 drafts of one request of 4000 tokens over 8 KV heads:
+// 15.8 us in a table for 4096 slots, 18.7 as a long call in one for 131072), and how
+// many CTAs a unit gets then: no more CTAs than SMs in all (a second one on an SM
+// keeps whole clusters waiting).
 inline bool short_call(const CacheAttnParams &p, int row_bytes) {
   CacheAttnParams q = p;
   q.tile_shift = 6;

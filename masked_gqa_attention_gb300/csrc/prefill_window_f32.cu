@@ -5,6 +5,7 @@
 // of one head; a producer warp fetches the 64-key tiles that the window and the
 // sinks reach (TMA boxes, two stages at D = 128), 256 threads run the register
 // tiles of simt_fp32.cuh; partial tiles take their mask words from shared memory.
+// Tiles behind a request's kv_len are fetched and masked like any other.
 // The last rows, which have the most keys under a causal limit, start first
 // (4096 queries x 16 heads, window 4096: 1854 us, in rising order 2153). (The
 // unwindowed fp32 prefill keeps its kernel of four threads per row, which took
