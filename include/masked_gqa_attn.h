@@ -436,6 +436,88 @@ MGQA_API mgqa_status masked_gqa_cache_compact(const mgqa_cache *cache, int32_t *
                                               int32_t *used_out, void *workspace,
                                               size_t workspace_bytes, cudaStream_t stream);
 
+/* ---- a cache that takes less memory: rows in 4 bits, and eviction ------------------
+ *
+ * A row of D features (64 or 128) in 4 bits is a record of D/2 + 16 bytes: four
+ * groups of D/4 features, each with a code u in 0 .. 15 per feature, a scale and a
+ * least value, which stand for scale * u + least. First the codes, two a byte, the
+ * even feature in the low half: for D = 128 byte i has features 2i and 2i + 1; for
+ * D = 64 the bytes of groups 0 and 1 come by turns in bytes 0 .. 15 (byte 2i: features
+ * 2i and 2i + 1, byte 2i + 1: 16 + 2i and 17 + 2i), those of groups 2 and 3 in bytes
+ * 16 .. 31. Then four scales and four least values in fp16. A cache of records is
+ * static or in pages as any other, its strides are BYTES (multiples of 16), and fork
+ * and compact take it as rows of D/4 + 8 fp16 values (with the strides to match). */
+
+/* masked_gqa_cache_append to a cache of records: cache->dtype is the type of k_new and
+ * v_new, cache->D their head dim, cache->k and v the records and their strides bytes.
+ * Each row is quantised by groups, every step one fp32 operation (so the records
+ * are the same bit for bit wherever they are computed):
+ *   least = fp16(min x), clamped to +-65504, never a negative zero
+ *   scale = fp16(clamp((max x - least) * fl32(1/15), 0, 65504))
+ *   u     = clamp(round((x - least) / scale), 0, 15), half to even; 0 where scale is 0
+ * The rows have to be finite. All else as for masked_gqa_cache_append. */
+MGQA_API mgqa_status masked_gqa_cache_append_q4(const mgqa_cache *cache, const void *k_new,
+                                                const void *v_new, const int64_t *k_new_stride,
+                                                const int64_t *v_new_stride, int32_t T,
+                                                const int32_t *index, const int32_t *count,
+                                                int32_t *kv_len_out, cudaStream_t stream);
+
+/* Attention of the last Lq (1 .. 256) cached tokens of every request over a cache of
+ * records (args->k, v; k_stride, v_stride in bytes): with n = kv_len[b] query t stands
+ * at position n - Lq + t (below 0 it sees nothing) and sees slot j when j is at most
+ * its position and, with window > 0, less than `window` behind it (its own position
+ * counts) or below `sinks`. args->dtype is the type of q and out; the products are
+ * with the values that the records stand for, not rounded. Cache forms, kv_len,
+ * workspace and errors as for masked_gqa_attn_decode_window. Slots that no query sees
+ * may hold anything; the scales and least values of the others have to be finite. */
+MGQA_API mgqa_status masked_gqa_attn_decode_q4(const mgqa_args *args, const mgqa_pages *pages, int32_t window,
+                                               int32_t sinks, void *workspace, size_t workspace_bytes,
+                                               cudaStream_t stream);
+
+/* The weights that the last Lq (1 .. 256) cached tokens give to the cache's slots,
+ * by the rule of masked_gqa_attn_decode_q4, added up:
+ *   weight[b][g][j] += sum over t and over the query heads h of KV head g of
+ *                      exp(scale <q[b,h,t], k[b,g,j]> - args->lse[b][h][t])
+ * for the slots j that some query sees; the others are left as they are. args->lse is
+ * an INPUT, the log-sums of the attention call (a row of -inf gives nothing); args->v,
+ * out and their strides are not looked at. q4 nonzero: a cache of records (k_stride in
+ * bytes), else one of args->dtype. weight is device fp32 [B][Hkv][weight_slots] with
+ * element strides weight_stride = {request, head}, 4-byte aligned; kv_len past
+ * weight_slots is a device error, too (clamped). One thread adds to a slot's
+ * weight, once per call (in fp32), so results repeat bit for bit; two calls that may
+ * run at the same time need weights of their own. */
+MGQA_API mgqa_status masked_gqa_attn_cache_weights(const mgqa_args *args, const mgqa_pages *pages, int32_t window,
+                                                   int32_t sinks, int32_t q4, float *weight,
+                                                   const int64_t *weight_stride, int32_t weight_slots,
+                                                   cudaStream_t stream);
+
+/* Bytes of the workspace of masked_gqa_cache_evict; 0 when the arguments are invalid.
+ * It needs no initial contents. */
+MGQA_API size_t masked_gqa_cache_evict_workspace_size(const mgqa_cache *cache, int32_t budget);
+
+/* Cuts every request with more than `budget` (>= 1) slots back to the budget: its first
+ * `sinks` and its last `recent` slots stay (sinks + recent <= budget) and, in each layer
+ * and KV head, of the others the budget - sinks - recent with the largest
+ * weight[layer][b][g][j] (of equal ones the first; NaN is less than any number). The
+ * rows that stay move, in their order, to slots 0 .. budget - 1; weight_out gets their
+ * weights there and 0 in slots budget .. kv_len[b] - 1, and the weights as they are of
+ * requests within the budget. kv_len_out[b] = min(kv_len[b], budget); it may be kv_len
+ * itself and weight_out may be weight itself (with the same strides: layer, request,
+ * head), but they may not overlap otherwise. weight and weight_out are device fp32
+ * [layers][rows][Hkv][weight_slots], slots contiguous.
+ * With a page table, pages that are written to must not be shared (fork sees to
+ * that), and with `ref` given (optional here) the table entries behind the budget of a
+ * request that is cut become -1 and their pages are given back (ref - 1). A request
+ * with kv_len out of range (or past weight_slots), a missing page or (with ref) a shared page among those that
+ * would be written is left as it is and sets *dev_error.
+ * Rows of any type: a cache of records goes as for fork. */
+MGQA_API mgqa_status masked_gqa_cache_evict(const mgqa_cache *cache, const float *weight,
+                                            const int64_t *weight_stride, float *weight_out,
+                                            const int64_t *weight_out_stride, int32_t weight_slots,
+                                            int32_t budget, int32_t sinks, int32_t recent,
+                                            int32_t *kv_len_out, void *workspace, size_t workspace_bytes,
+                                            cudaStream_t stream);
+
 /* Static description of a status code. */
 MGQA_API const char *mgqa_status_string(mgqa_status status);
 

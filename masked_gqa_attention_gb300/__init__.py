@@ -16,7 +16,11 @@ Entry points (same names as the C ABI):
     one token over a cache in slots or pages;
   * :func:`masked_gqa_attn_decode_tree` -- drafted tokens over such a cache;
   * :func:`masked_gqa_cache_append`, :func:`masked_gqa_cache_fork`,
-    :func:`masked_gqa_cache_compact` -- the cache's own steps.
+    :func:`masked_gqa_cache_compact` -- the cache's own steps;
+  * :func:`masked_gqa_cache_append_q4`, :func:`masked_gqa_attn_decode_q4` -- a
+    cache whose rows are held in 4 bits;
+  * :func:`masked_gqa_attn_cache_weights`, :func:`masked_gqa_cache_evict` -- what
+    attention looks at, summed up, and the eviction of the slots with the least.
 Outputs and workspaces that are not given are allocated for the call's `stream`.
 """
 from __future__ import annotations
@@ -49,6 +53,8 @@ __all__ = [
     "masked_gqa_attn_decode_tree", "masked_gqa_attn_cache_workspace_size", "new_cache_attn_workspace",
     "masked_gqa_cache_append", "masked_gqa_cache_fork", "masked_gqa_cache_compact",
     "masked_gqa_cache_workspace_size",
+    "masked_gqa_cache_append_q4", "masked_gqa_attn_decode_q4", "masked_gqa_attn_cache_weights",
+    "masked_gqa_cache_evict", "masked_gqa_cache_evict_workspace_size",
 ]
 
 (MGQA_OK, MGQA_ERR_INVALID_ARG, MGQA_ERR_UNSUPPORTED, MGQA_ERR_CUDA, MGQA_ERR_TIMEOUT,
@@ -78,6 +84,11 @@ EXPORTED_SYMBOLS = (
     "masked_gqa_cache_workspace_size",
     "masked_gqa_cache_fork",
     "masked_gqa_cache_compact",
+    "masked_gqa_cache_append_q4",
+    "masked_gqa_attn_decode_q4",
+    "masked_gqa_attn_cache_weights",
+    "masked_gqa_cache_evict_workspace_size",
+    "masked_gqa_cache_evict",
 )
 # exported by the debug library only (include/masked_gqa_attn_debug.h)
 DEBUG_SYMBOLS = (
@@ -228,7 +239,12 @@ def _bind(L: ctypes.CDLL) -> ctypes.CDLL:
             ("masked_gqa_cache_append", [P, P, P, P, P, I32, P, P, P, P], ctypes.c_int),
             ("masked_gqa_cache_workspace_size", [P, I32], SZ),
             ("masked_gqa_cache_fork", [P, I32, P, P, I32, P, SZ, P], ctypes.c_int),
-            ("masked_gqa_cache_compact", [P, P, I64, P, P, P, SZ, P], ctypes.c_int)):
+            ("masked_gqa_cache_compact", [P, P, I64, P, P, P, SZ, P], ctypes.c_int),
+            ("masked_gqa_cache_append_q4", [P, P, P, P, P, I32, P, P, P, P], ctypes.c_int),
+            ("masked_gqa_attn_decode_q4", [P, P, I32, I32, P, SZ, P], ctypes.c_int),
+            ("masked_gqa_attn_cache_weights", [P, P, I32, I32, I32, P, P, I32, P], ctypes.c_int),
+            ("masked_gqa_cache_evict_workspace_size", [P, I32], SZ),
+            ("masked_gqa_cache_evict", [P, P, P, P, P, I32, I32, I32, I32, P, P, SZ, P], ctypes.c_int)):
         f = getattr(L, name)
         f.argtypes, f.restype = args, res
     return L
@@ -724,7 +740,7 @@ _cache_ws_bytes = 0
 
 
 def masked_gqa_attn_cache_workspace_size() -> int:
-    """Bytes of the workspace of the two calls below; the same for every shape."""
+    """Bytes of the workspace of masked_gqa_attn_decode_window, _tree and _q4; the same for every shape."""
     global _cache_ws_bytes
     if not _cache_ws_bytes:
         _cache_ws_bytes = int(lib().masked_gqa_attn_cache_workspace_size())
@@ -732,7 +748,7 @@ def masked_gqa_attn_cache_workspace_size() -> int:
 
 
 def new_cache_attn_workspace(device="cuda") -> torch.Tensor:
-    """A workspace (uint8) for masked_gqa_attn_decode_window / _tree. Nothing in
+    """A workspace (uint8) for masked_gqa_attn_decode_window / _tree / _q4. Nothing in
     it outlives a call; calls that may overlap need one each."""
     return torch.empty(masked_gqa_attn_cache_workspace_size(), dtype=torch.uint8, device=device)
 
@@ -842,3 +858,90 @@ def masked_gqa_cache_compact(k_cache, v_cache, page_table, ref, page_table_out=N
     if status:
         _check(status)
     return page_table_out, ref_out
+
+
+# ---- a cache that takes less memory: rows in 4 bits, and eviction ------------------
+
+def masked_gqa_cache_append_q4(k_cache, v_cache, k_new, v_new, kv_len, kv_len_out, *, index=None,
+                               count=None, page_table=None, dev_error=None, stream=None):
+    """masked_gqa_cache_append to a cache whose rows are held in 4 bits: k_cache /
+    v_cache uint8 [layers, B, Hkv, slots, D/2 + 16] (or pages, or 4-D), k_new / v_new
+    of any of the dtypes. A row's four groups of D/4 features each get a least value
+    and a scale (fp16) and a code in 0 .. 15 per feature; the record is described
+    in include/masked_gqa_attn.h. masked_gqa_cache_fork, _compact and _evict take
+    such caches too. Returns kv_len_out."""
+    status = (_native or _calls()).cache_append_q4(k_cache, v_cache, k_new, v_new, kv_len, kv_len_out, index, count,
+                                                   page_table, dev_error, stream)
+    if status:
+        _check(status)
+    return kv_len_out
+
+
+def masked_gqa_attn_decode_q4(q, k_cache, v_cache, kv_len, out=None, *, window=0, sinks=0,
+                              page_table=None, workspace=None, scale=None, lse=None, dev_error=None,
+                              stream=None):
+    """Attention of the last T cached tokens of every request (q [B, Hq, T, D],
+    T <= 256) over a cache of 4-bit records (uint8 [B, Hkv, slots, D/2 + 16], or
+    [pages, Hkv, page_size, D/2 + 16] with page_table int32 [B, max_pages]): query t
+    stands at position kv_len[b] - T + t (below 0 it sees nothing) and sees the
+    slots up to it, with a window those less than `window` behind it and the first
+    `sinks`. workspace: new_cache_attn_workspace() (None: allocated here).
+    Returns out."""
+    if out is None:
+        out = _new_out(q, stream)
+    if workspace is None:
+        with _allocating_on(stream, q.device):
+            workspace = new_cache_attn_workspace(q.device)
+    status = (_native or _calls()).decode_q4(q, k_cache, v_cache, kv_len, out, window, sinks, page_table, workspace,
+                                             scale, lse, dev_error, stream)
+    if status:
+        _check(status)
+    return out
+
+
+def masked_gqa_attn_cache_weights(q, k_cache, kv_len, lse, weight, *, window=0, sinks=0,
+                                  page_table=None, scale=None, dev_error=None, stream=None):
+    """The attention weights that the last T cached tokens (q [B, Hq, T, D], T <= 256,
+    positions and window as for masked_gqa_attn_decode_q4) give to every slot, summed
+    over the tokens and over the query heads of each KV head and added to weight
+    (fp32 [B, Hkv, slots], with slots for every kv_len). lse fp32 [B, Hq, T]: the log-sums that the attention
+    call left. k_cache: of q's dtype, or 4-bit records (uint8), in slots or pages.
+    Returns weight."""
+    status = (_native or _calls()).cache_weights(q, k_cache, kv_len, lse, weight, window, sinks, page_table, scale,
+                                                 dev_error, stream)
+    if status:
+        _check(status)
+    return weight
+
+
+def masked_gqa_cache_evict_workspace_size(k_cache, v_cache, budget, *, page_table=None, ref=None) -> int:
+    """Bytes of the workspace of masked_gqa_cache_evict."""
+    size = _calls().cache_evict_workspace_size(k_cache, v_cache, page_table, ref, budget)
+    if size == 0:
+        _check(MGQA_ERR_INVALID_ARG)
+    return size
+
+
+def masked_gqa_cache_evict(k_cache, v_cache, weight, kv_len, *, budget, sinks=0, recent=0, page_table=None,
+                           ref=None, weight_out=None, kv_len_out=None, workspace=None, dev_error=None,
+                           stream=None):
+    """Cut every request with more than `budget` slots back to it: the first `sinks`
+    and the last `recent` slots stay and, per layer and KV head, of the others those
+    with the largest weight (fp32 [layers, B, Hkv, slots], without the layers for
+    4-D caches, with slots for every kv_len; of equal ones the first). The rows that stay move, in their order,
+    to slots 0 .. budget - 1, and their weights with them; the slots behind get
+    weight 0. weight_out and kv_len_out (default: weight and kv_len, in place). With
+    ref (int32 [pages]) the pages behind the budget are given back. The caches are
+    [layers, B, Hkv, slots, D], or in pages, of any dtype or 4-bit records.
+    Returns kv_len_out."""
+    weight_out = weight if weight_out is None else weight_out
+    kv_len_out = kv_len if kv_len_out is None else kv_len_out
+    if workspace is None:
+        size = masked_gqa_cache_evict_workspace_size(k_cache, v_cache, budget, page_table=page_table, ref=ref)
+        with _allocating_on(stream, k_cache.device):
+            workspace = torch.empty(size, dtype=torch.uint8, device=k_cache.device)
+    status = (_native or _calls()).cache_evict(k_cache, v_cache, weight, kv_len, budget, sinks, recent, page_table, ref,
+                                               weight_out, kv_len_out, workspace, dev_error, stream)
+    if status:
+        _check(status)
+    return kv_len_out

@@ -253,6 +253,76 @@ mgqa_status validate_cache(const mgqa_cache *c, bool counted) {
   return MGQA_OK;
 }
 
+// A cache of records in 4 bits: dtype and D are those of the rows that are appended,
+// the strides bytes.
+mgqa_status validate_cache_q4(const mgqa_cache *c) {
+  g_detail[0] = '\0';
+  if (!c) return fail(MGQA_ERR_INVALID_ARG, "cache is null");
+  if (c->D != 64 && c->D != 128) return fail(MGQA_ERR_UNSUPPORTED, "head dim %d (64 or 128)", c->D);
+  for (int t = 0; t < 4; ++t)
+    if (c->k_stride[t] % 16 || c->v_stride[t] % 16)
+      return fail(MGQA_ERR_INVALID_ARG, "cache strides must be non-negative multiples of 16 bytes");
+  return validate_cache(c, false);
+}
+
+// The last Lq cached tokens over a cache (of records, or of the call's type).
+mgqa_status validate_last(const mgqa_args *args, const mgqa_pages *pages, int32_t window, int32_t sinks, bool q4,
+                          bool values) {
+  g_detail[0] = '\0';
+  if (!args) return fail(MGQA_ERR_INVALID_ARG, "args is null");
+  mgqa_args a = *args;
+  if (!values) {  // the call has no values and no output
+    a.v = a.k;
+    a.out = const_cast<void *>(a.q);
+    for (int t = 0; t < 3; ++t) {
+      a.v_stride[t] = a.k_stride[t];
+      a.o_stride[t] = a.q_stride[t];
+    }
+  }
+  if (q4)
+    for (int t = 0; t < 3; ++t)
+      if (a.k_stride[t] % 16 || a.v_stride[t] % 16)
+        return fail(MGQA_ERR_INVALID_ARG, "strides of records must be non-negative multiples of 16 bytes");
+  mgqa_status st = validate_cached(&a, pages);
+  if (st != MGQA_OK) return st;
+  if (a.Lq > kMaxDraftsHost) return fail(MGQA_ERR_UNSUPPORTED, "%d queries a request (at most %d)", a.Lq, kMaxDraftsHost);
+  return check_window(window, sinks, 0);
+}
+
+// fp32 [n0][n1][n2][slots] with strides st.
+mgqa_status check_weight(const char *name, const float *w, const int64_t *st, const int64_t *n, int64_t slots) {
+  if (!w || !st || !aligned(w, 4)) return fail(MGQA_ERR_INVALID_ARG, "%s or its strides missing or misaligned", name);
+  if (slots < 1) return fail(MGQA_ERR_INVALID_ARG, "weight_slots must be >= 1");
+  // the heads' rows may not overlap: in some order of the dimensions, each stride is
+  // at least what the smaller ones span
+  int64_t span = slots;
+  bool done[3] = {n[0] == 1, n[1] == 1, n[2] == 1};
+  for (int k = 0; k < 3; ++k) {
+    int next = -1;
+    for (int t = 0; t < 3; ++t)
+      if (!done[t] && (next < 0 || st[t] < st[next])) next = t;
+    if (next < 0) break;
+    if (st[next] < span || st[next] > ((int64_t)1 << 60) / n[next])
+      return fail(MGQA_ERR_INVALID_ARG, "%s: the slots of two heads overlap", name);
+    span += (n[next] - 1) * st[next];
+    done[next] = true;
+  }
+  return MGQA_OK;
+}
+
+mgqa_status validate_evict(const mgqa_cache *c, int32_t budget, int32_t sinks, int32_t recent) {
+  mgqa_status st = validate_cache(c, false);
+  if (st != MGQA_OK) return st;
+  if (c->ref && !aligned(c->ref, 4)) return fail(MGQA_ERR_INVALID_ARG, "ref misaligned");
+  if (c->ref && !c->page_table) return fail(MGQA_ERR_INVALID_ARG, "ref without a page table");
+  if (budget < 1 || budget > (1 << 24)) return fail(MGQA_ERR_INVALID_ARG, "budget must be in [1, 2^24]");
+  if (sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget)
+    return fail(MGQA_ERR_INVALID_ARG, "sinks and recent must be >= 0 and sum to at most the budget");
+  if ((int64_t)c->layers * c->rows * c->Hkv > (1 << 26))
+    return fail(MGQA_ERR_UNSUPPORTED, "layers x requests x KV heads past 2^26");
+  return MGQA_OK;
+}
+
 }  // namespace
 }  // namespace mgqa
 
@@ -370,11 +440,12 @@ mgqa_status masked_gqa_attn_decode_tree(const mgqa_args *args, const mgqa_pages 
   return mgqa::launch_cache_attn(*args, pages, tree, window, sinks, workspace, stream);
 }
 
-mgqa_status masked_gqa_cache_append(const mgqa_cache *cache, const void *k_new, const void *v_new,
-                                    const int64_t *k_new_stride, const int64_t *v_new_stride, int32_t T,
-                                    const int32_t *index, const int32_t *count, int32_t *kv_len_out,
-                                    cudaStream_t stream) {
-  mgqa_status st = mgqa::validate_cache(cache, false);
+namespace {
+
+mgqa_status append_rows(const mgqa_cache *cache, const void *k_new, const void *v_new, const int64_t *k_new_stride,
+                        const int64_t *v_new_stride, int32_t T, const int32_t *index, const int32_t *count,
+                        int32_t *kv_len_out, bool q4, cudaStream_t stream) {
+  mgqa_status st = q4 ? mgqa::validate_cache_q4(cache) : mgqa::validate_cache(cache, false);
   if (st != MGQA_OK) return st;
   if (!cache->kv_len || !kv_len_out) return mgqa::fail(MGQA_ERR_INVALID_ARG, "kv_len and kv_len_out are required");
   if (!mgqa::aligned(kv_len_out, 4) || !mgqa::aligned(index, 4) || !mgqa::aligned(count, 4))
@@ -389,8 +460,81 @@ mgqa_status masked_gqa_cache_append(const mgqa_cache *cache, const void *k_new, 
   if ((st = mgqa::check_new_rows(k_new, v_new, k_new_stride, v_new_stride, 4, cache->dtype == MGQA_FP32 ? 4 : 2)) !=
       MGQA_OK)
     return st;
-  return mgqa::launch_cache_append(*cache, k_new, v_new, k_new_stride, v_new_stride, T, index, count, kv_len_out,
+  return mgqa::launch_cache_append(*cache, k_new, v_new, k_new_stride, v_new_stride, T, index, count, kv_len_out, q4,
                                    stream);
+}
+
+}  // namespace
+
+mgqa_status masked_gqa_cache_append(const mgqa_cache *cache, const void *k_new, const void *v_new,
+                                    const int64_t *k_new_stride, const int64_t *v_new_stride, int32_t T,
+                                    const int32_t *index, const int32_t *count, int32_t *kv_len_out,
+                                    cudaStream_t stream) {
+  return append_rows(cache, k_new, v_new, k_new_stride, v_new_stride, T, index, count, kv_len_out, false, stream);
+}
+
+mgqa_status masked_gqa_cache_append_q4(const mgqa_cache *cache, const void *k_new, const void *v_new,
+                                       const int64_t *k_new_stride, const int64_t *v_new_stride, int32_t T,
+                                       const int32_t *index, const int32_t *count, int32_t *kv_len_out,
+                                       cudaStream_t stream) {
+  return append_rows(cache, k_new, v_new, k_new_stride, v_new_stride, T, index, count, kv_len_out, true, stream);
+}
+
+mgqa_status masked_gqa_attn_decode_q4(const mgqa_args *args, const mgqa_pages *pages, int32_t window, int32_t sinks,
+                                      void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+  mgqa_status st = mgqa::validate_last(args, pages, window, sinks, true, true);
+  if (st != MGQA_OK) return st;
+  if ((st = mgqa::check_workspace(workspace, workspace_bytes, mgqa::cache_attn_workspace_bytes())) != MGQA_OK)
+    return st;
+  return mgqa::launch_attn_q4(*args, pages, window, sinks, workspace, stream);
+}
+
+mgqa_status masked_gqa_attn_cache_weights(const mgqa_args *args, const mgqa_pages *pages, int32_t window,
+                                          int32_t sinks, int32_t q4, float *weight, const int64_t *weight_stride,
+                                          int32_t weight_slots, cudaStream_t stream) {
+  mgqa_status st = mgqa::validate_last(args, pages, window, sinks, q4 != 0, false);
+  if (st != MGQA_OK) return st;
+  if (!args->lse) return mgqa::fail(MGQA_ERR_INVALID_ARG, "lse is required");
+  const int64_t heads[3] = {1, args->B, args->Hkv}, strides[3] = {0, weight_stride ? weight_stride[0] : 0,
+                                                                  weight_stride ? weight_stride[1] : 0};
+  if ((st = mgqa::check_weight("weight", weight, weight_stride ? strides : nullptr, heads, weight_slots)) != MGQA_OK)
+    return st;
+  return mgqa::launch_cache_weights(*args, pages, window, sinks, q4 != 0, weight, weight_stride, weight_slots, stream);
+}
+
+size_t masked_gqa_cache_evict_workspace_size(const mgqa_cache *cache, int32_t budget) {
+  if (mgqa::validate_evict(cache, budget, 0, 0) != MGQA_OK) return 0;
+  return mgqa::cache_evict_workspace_bytes(*cache, budget);
+}
+
+mgqa_status masked_gqa_cache_evict(const mgqa_cache *cache, const float *weight, const int64_t *weight_stride,
+                                   float *weight_out, const int64_t *weight_out_stride, int32_t weight_slots,
+                                   int32_t budget, int32_t sinks, int32_t recent, int32_t *kv_len_out, void *workspace,
+                                   size_t workspace_bytes, cudaStream_t stream) {
+  mgqa_status st = mgqa::validate_evict(cache, budget, sinks, recent);
+  if (st != MGQA_OK) return st;
+  if (!cache->kv_len || !kv_len_out || !mgqa::aligned(kv_len_out, 4))
+    return mgqa::fail(MGQA_ERR_INVALID_ARG, "kv_len or kv_len_out missing or misaligned");
+  const int64_t rows = cache->rows, n[3] = {cache->layers, rows, cache->Hkv};
+  const int64_t slots = weight_slots;
+  if ((st = mgqa::check_weight("weight", weight, weight_stride, n, slots)) != MGQA_OK) return st;
+  if ((st = mgqa::check_weight("weight_out", weight_out, weight_out_stride, n, slots)) != MGQA_OK) return st;
+  const auto span = [&](const int64_t *t) { return (n[0] - 1) * t[0] + (n[1] - 1) * t[1] + (n[2] - 1) * t[2] + slots; };
+  const auto as_ints = [](const void *p) { return static_cast<const int32_t *>(p); };
+  bool same = weight == weight_out;
+  for (int t = 0; t < 3; ++t) same = same && (n[t] == 1 || weight_stride[t] == weight_out_stride[t]);
+  if (!same && mgqa::ints_overlap(as_ints(weight), span(weight_stride), as_ints(weight_out), span(weight_out_stride)))
+    return mgqa::fail(MGQA_ERR_INVALID_ARG, "weight_out must be weight itself or not overlap it");
+  if (cache->kv_len != kv_len_out && mgqa::ints_overlap(cache->kv_len, rows, kv_len_out, rows))
+    return mgqa::fail(MGQA_ERR_INVALID_ARG, "kv_len_out must be kv_len itself or not overlap it");
+  if (mgqa::ints_overlap(kv_len_out, rows, as_ints(weight_out), span(weight_out_stride)) ||
+      mgqa::ints_overlap(kv_len_out, rows, cache->page_table, (rows - 1) * cache->table_stride + cache->max_pages))
+    return mgqa::fail(MGQA_ERR_INVALID_ARG, "kv_len_out must not overlap the weights or the page table");
+  if ((st = mgqa::check_workspace(workspace, workspace_bytes, mgqa::cache_evict_workspace_bytes(*cache, budget))) !=
+      MGQA_OK)
+    return st;
+  return mgqa::launch_cache_evict(*cache, weight, weight_stride, weight_out, weight_out_stride, weight_slots, budget,
+                                  sinks, recent, kv_len_out, workspace, stream);
 }
 
 size_t masked_gqa_cache_workspace_size(const mgqa_cache *cache, int32_t n) {

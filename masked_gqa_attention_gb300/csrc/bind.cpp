@@ -109,21 +109,28 @@ struct Launch {
 };
 
 // The attention arguments for k / v [B, Hkv, slots, D] or, with a page table,
-// [pages, Hkv, page_size, D].
+// [pages, Hkv, page_size, D]; or for caches of records ([.., D/2 + 16] bytes, their
+// strides in bytes), where `records` allows them. v and out may be null.
 struct Attention {
   mgqa_args a{};
   mgqa_pages pages{};
   const mgqa_pages *paged = nullptr;
+  bool q4 = false;
 
-  Attention(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor &out, const Tensor *kv_len, PyObject *scale,
-            const Tensor *lse, const Tensor *err, const Tensor *table) {
-    if (q.dim() != 4 || k.dim() != 4 || v.sizes() != k.sizes() || out.sizes() != q.sizes())
+  Attention(const Tensor &q, const Tensor &k, const Tensor *v, const Tensor *out, const Tensor *kv_len, PyObject *scale,
+            const Tensor *lse, const Tensor *err, const Tensor *table, bool records = false) {
+    if (q.dim() != 4 || k.dim() != 4 || (v && v->sizes() != k.sizes()) || (out && out->sizes() != q.sizes()))
       bad("q, out must be [B, Hq, L, D] and k, v [B or pages, Hkv, slots, D]");
     a.dtype = dtype_of(q);
-    if (k.scalar_type() != q.scalar_type() || v.scalar_type() != q.scalar_type() || out.scalar_type() != q.scalar_type())
+    q4 = records && k.scalar_type() == at::kByte;
+    const auto other = [](const Tensor *t, at::ScalarType type) { return t && t->scalar_type() != type; };
+    if (other(out, q.scalar_type()) || other(v, k.scalar_type()) || (!q4 && other(&k, q.scalar_type())))
       bad("q, out, k and v must share one dtype of bfloat16, float16, float32");
-    if (k.size(3) != q.size(3) || q.stride(3) != 1 || k.stride(3) != 1 || v.stride(3) != 1 || out.stride(3) != 1)
-      bad("the head dims must agree and have unit stride");
+    const int64_t row = q4 ? q.size(3) / 2 + 16 : q.size(3);
+    if (k.size(3) != row || q.stride(3) != 1 || k.stride(3) != 1 || (v && v->stride(3) != 1) ||
+        (out && out->stride(3) != 1))
+      bad(q4 ? "the caches must have records of D/2 + 16 bytes; records and head dims must have unit stride"
+             : "the head dims must agree and have unit stride");
     a.B = small(q.size(0), "B");
     a.Hq = small(q.size(1), "Hq");
     a.Hkv = small(k.size(1), "Hkv");
@@ -146,13 +153,13 @@ struct Attention {
     a.Lk = small(cap, "slots of a request");
     a.q = q.data_ptr();
     a.k = k.data_ptr();
-    a.v = v.data_ptr();
-    a.out = out.data_ptr();
+    a.v = v ? v->data_ptr() : nullptr;
+    a.out = out ? out->data_ptr() : nullptr;
     for (int t = 0; t < 3; ++t) {
       a.q_stride[t] = q.stride(t);
       a.k_stride[t] = k.stride(t);
-      a.v_stride[t] = v.stride(t);
-      a.o_stride[t] = out.stride(t);
+      a.v_stride[t] = v ? v->stride(t) : 0;
+      a.o_stride[t] = out ? out->stride(t) : 0;
     }
     a.kv_len = ints(kv_len, "kv_len", {q.size(0)});
     if (scale == Py_None) {
@@ -176,13 +183,17 @@ struct Cache {
   mgqa_cache c{};
   int64_t layers, rows, Hkv, D;
 
+  // Records (bytes) that only move go as fp16 values; where rows are quantised into
+  // them, `rows_of` has the rows' type and head dim and the strides are bytes.
   Cache(const Tensor &k, const Tensor &v, const Tensor *table, const Tensor *kv_len, const Tensor *ref,
-        const Tensor *err) {
+        const Tensor *err, const Tensor *rows_of = nullptr) {
     const int n = (int)k.dim(), x = n - 4;  // x: the page dimension
     if ((n != 4 && n != 5) || v.sizes() != k.sizes() || k.stride(n - 1) != 1 || v.stride(n - 1) != 1)
       bad("the caches must be [layers, pages, Hkv, page_size, D] (or 4-D, one layer) with a unit-stride head dim");
     if (v.scalar_type() != k.scalar_type()) bad("the caches must share one dtype of bfloat16, float16, float32");
-    c.dtype = dtype_of(k);
+    const bool records = k.scalar_type() == at::kByte;
+    if (rows_of && !records) bad("the caches must be uint8 records");
+    c.dtype = !records ? dtype_of(k) : rows_of ? dtype_of(*rows_of) : MGQA_FP16;
     layers = x ? k.size(0) : 1;
     rows = k.size(x);
     Hkv = k.size(x + 1);
@@ -191,12 +202,23 @@ struct Cache {
     c.num_pages = small(rows, "pages");
     c.Hkv = small(Hkv, "Hkv");
     c.page_size = small(k.size(x + 2), "page_size");
+    if (records && rows_of) {
+      if (rows_of->dim() != n) bad("the new rows must have as many dimensions as the caches");
+      D = rows_of->size(n - 1);
+      if (k.size(x + 3) != D / 2 + 16) bad("the caches must have records of D/2 + 16 bytes");
+    } else if (records) {
+      if (D % 16) bad("records must be a multiple of 16 bytes");
+      D /= 2;
+    }
     c.D = small(D, "D");
     c.k = k.data_ptr();
     c.v = v.data_ptr();
+    const int64_t unit = records && !rows_of ? 2 : 1;
     for (int t = 0; t < 4; ++t) {
-      c.k_stride[t] = t || x ? k.stride(x - 1 + t) : 0;
-      c.v_stride[t] = t || x ? v.stride(x - 1 + t) : 0;
+      c.k_stride[t] = t || x ? k.stride(x - 1 + t) / unit : 0;
+      c.v_stride[t] = t || x ? v.stride(x - 1 + t) / unit : 0;
+      if ((t || x) && unit > 1 && (k.stride(x - 1 + t) % 16 || v.stride(x - 1 + t) % 16))
+        bad("strides of records must be multiples of 16 bytes");
     }
     if (table) {
       if (table->scalar_type() != at::kInt || table->dim() != 2 || table->stride(1) != 1)
@@ -250,7 +272,7 @@ PyObject *prefill_window(PyObject *, PyObject *const *o, Py_ssize_t n) {
                  *err = optional_tensor(o[7], "dev_error");
     const int dev = device_of(q);
     together(dev, {{&k, "k"}, {&v, "v"}, {&out, "out"}, {len, "kv_len"}, {lse, "lse"}, {err, "dev_error"}});
-    Attention at(q, k, v, out, len, o[5], lse, err, nullptr);
+    Attention at(q, k, &v, &out, len, o[5], lse, err, nullptr);
     const int causal = PyObject_IsTrue(o[8]);
     if (causal < 0) throw PythonError();
     at.a.causal = causal;
@@ -272,7 +294,7 @@ PyObject *decode_window(PyObject *, PyObject *const *o, Py_ssize_t n) {
     const int dev = device_of(q);
     together(dev, {{&k, "k_cache"}, {&v, "v_cache"}, {&len, "kv_len"}, {&out, "out"}, {table, "page_table"},
                    {&ws, "workspace"}, {lse, "lse"}, {err, "dev_error"}});
-    const Attention at(q, k, v, out, &len, o[9], lse, err, table);
+    const Attention at(q, k, &v, &out, &len, o[9], lse, err, table);
     const int32_t window = count(o[5]), sinks = count(o[6]);
     void *wp = ws.data_ptr();
     const size_t wn = ws.nbytes();
@@ -297,7 +319,7 @@ PyObject *decode_tree(PyObject *, PyObject *const *o, Py_ssize_t n) {
     together(dev, {{&k, "k_cache"}, {&v, "v_cache"}, {&kn, "k_new"}, {&vn, "v_new"}, {&len, "kv_len"}, {&out, "out"},
                    {bits, "tree_bits"}, {live, "tree_len"}, {table, "page_table"}, {&ws, "workspace"}, {lse, "lse"},
                    {err, "dev_error"}});
-    const Attention at(q, k, v, out, &len, o[13], lse, err, table);
+    const Attention at(q, k, &v, &out, &len, o[13], lse, err, table);
     const int64_t B = q.size(0), T = q.size(2), W = (T + 31) / 32, shape[4] = {B, k.size(1), T, q.size(3)};
     if (kn.sizes() != at::IntArrayRef(shape, 4) || vn.sizes() != kn.sizes() || kn.scalar_type() != q.scalar_type() ||
         vn.scalar_type() != q.scalar_type() || kn.stride(3) != 1 || vn.stride(3) != 1)
@@ -332,7 +354,7 @@ PyObject *decode_tree(PyObject *, PyObject *const *o, Py_ssize_t n) {
 }
 
 // k_cache v_cache k_new v_new kv_len kv_len_out index count page_table dev_error stream
-PyObject *cache_append(PyObject *, PyObject *const *o, Py_ssize_t n) {
+PyObject *append_rows(PyObject *const *o, Py_ssize_t n, bool q4) {
   return guarded(o, n, 11, [&] {
     const Tensor &k = tensor(o[0], "k_cache"), &v = tensor(o[1], "v_cache"), &kn = tensor(o[2], "k_new"),
                  &vn = tensor(o[3], "v_new"), &len = tensor(o[4], "kv_len"), &len_out = tensor(o[5], "kv_len_out");
@@ -341,15 +363,15 @@ PyObject *cache_append(PyObject *, PyObject *const *o, Py_ssize_t n) {
     const int dev = device_of(k);
     together(dev, {{&v, "v_cache"}, {&kn, "k_new"}, {&vn, "v_new"}, {&len, "kv_len"}, {&len_out, "kv_len_out"},
                    {index, "index"}, {cnt, "count"}, {table, "page_table"}, {err, "dev_error"}});
-    const Cache cache(k, v, table, &len, nullptr, err);
+    const Cache cache(k, v, table, &len, nullptr, err, q4 ? &kn : nullptr);
     const int x = (int)k.dim() - 4;
-    bool fits = kn.dim() == k.dim() && vn.sizes() == kn.sizes() && kn.scalar_type() == k.scalar_type() &&
-                vn.scalar_type() == k.scalar_type() && kn.stride(x + 3) == 1 && vn.stride(x + 3) == 1;
+    bool fits = kn.dim() == k.dim() && vn.sizes() == kn.sizes() && (q4 || kn.scalar_type() == k.scalar_type()) &&
+                vn.scalar_type() == kn.scalar_type() && kn.stride(x + 3) == 1 && vn.stride(x + 3) == 1;
     fits = fits && (!x || kn.size(0) == cache.layers) && kn.size(x) == cache.rows && kn.size(x + 1) == cache.Hkv &&
            kn.size(x + 3) == cache.D;
     if (!fits)
-      bad("k_new and v_new must have the caches' dtype, [layers, B, Hkv, T, D] (4-D with 4-D caches) and a "
-          "unit-stride head dim");
+      bad(std::string("k_new and v_new must have ") + (q4 ? "one" : "the caches'") +
+          " dtype, [layers, B, Hkv, T, D] (4-D with 4-D caches) and a unit-stride head dim");
     const int64_t T = kn.size(x + 2);
     int64_t ks[4] = {0}, vs[4] = {0};
     for (int t = x ? 0 : 1; t < 4; ++t) {
@@ -362,7 +384,115 @@ PyObject *cache_append(PyObject *, PyObject *const *o, Py_ssize_t n) {
     const int32_t rows = small(T, "T");
     const Launch l(dev, o[10]);
     return status_of([&] {
-      return masked_gqa_cache_append(&cache.c, kp, vp, ks, vs, rows, ip, cp, lp, l.stream);
+      return (q4 ? masked_gqa_cache_append_q4 : masked_gqa_cache_append)(&cache.c, kp, vp, ks, vs, rows, ip, cp, lp,
+                                                                         l.stream);
+    });
+  });
+}
+PyObject *cache_append(PyObject *, PyObject *const *o, Py_ssize_t n) { return append_rows(o, n, false); }
+PyObject *cache_append_q4(PyObject *, PyObject *const *o, Py_ssize_t n) { return append_rows(o, n, true); }
+
+// q k_cache v_cache kv_len out window sinks page_table workspace scale lse dev_error stream
+PyObject *decode_q4(PyObject *, PyObject *const *o, Py_ssize_t n) {
+  return guarded(o, n, 13, [&] {
+    const Tensor &q = tensor(o[0], "q"), &k = tensor(o[1], "k_cache"), &v = tensor(o[2], "v_cache"),
+                 &len = tensor(o[3], "kv_len"), &out = tensor(o[4], "out"), &ws = tensor(o[8], "workspace");
+    const Tensor *table = optional_tensor(o[7], "page_table"), *lse = optional_tensor(o[10], "lse"),
+                 *err = optional_tensor(o[11], "dev_error");
+    const int dev = device_of(q);
+    together(dev, {{&k, "k_cache"}, {&v, "v_cache"}, {&len, "kv_len"}, {&out, "out"}, {table, "page_table"},
+                   {&ws, "workspace"}, {lse, "lse"}, {err, "dev_error"}});
+    const Attention at(q, k, &v, &out, &len, o[9], lse, err, table, true);
+    if (!at.q4) bad("k_cache and v_cache must be uint8 records");
+    const int32_t window = count(o[5]), sinks = count(o[6]);
+    void *wp = ws.data_ptr();
+    const size_t wn = ws.nbytes();
+    const Launch l(dev, o[12]);
+    return status_of([&] {
+      return masked_gqa_attn_decode_q4(&at.a, at.paged, window, sinks, wp, wn, l.stream);
+    });
+  });
+}
+
+// fp32 weights of the given leading sizes, slots last: their address; their strides to
+// st; `slots` becomes the least number of slots of the weights of a call.
+float *weights(const Tensor &w, const char *name, std::initializer_list<int64_t> lead, int64_t *st, int32_t &slots) {
+  const int n = (int)lead.size();
+  bool fits = w.scalar_type() == at::kFloat && w.dim() == n + 1 && w.stride(n) == 1;
+  int t = 0;
+  for (int64_t x : lead) {
+    fits = fits && w.size(t) == x;
+    if (fits) st[t] = w.stride(t);
+    ++t;
+  }
+  if (!fits) {
+    std::string s;
+    for (int64_t x : lead) s += std::to_string(x) + ", ";
+    bad(std::string(name) + " must be fp32 [" + s + "slots] with unit-stride slots");
+  }
+  if (w.size(n) < slots) slots = (int32_t)w.size(n);
+  return static_cast<float *>(w.data_ptr());
+}
+
+// q k_cache kv_len lse weight window sinks page_table scale dev_error stream
+PyObject *cache_weights(PyObject *, PyObject *const *o, Py_ssize_t n) {
+  return guarded(o, n, 11, [&] {
+    const Tensor &q = tensor(o[0], "q"), &k = tensor(o[1], "k_cache"), &len = tensor(o[2], "kv_len"),
+                 &lse = tensor(o[3], "lse"), &w = tensor(o[4], "weight");
+    const Tensor *table = optional_tensor(o[7], "page_table"), *err = optional_tensor(o[9], "dev_error");
+    const int dev = device_of(q);
+    together(dev, {{&k, "k_cache"}, {&len, "kv_len"}, {&lse, "lse"}, {&w, "weight"}, {table, "page_table"},
+                   {err, "dev_error"}});
+    const Attention at(q, k, nullptr, nullptr, &len, o[8], &lse, err, table, true);
+    int64_t st[2];
+    int32_t slots = 0x7fffffff;
+    float *wp = weights(w, "weight", {q.size(0), k.size(1)}, st, slots);
+    const int32_t window = count(o[5]), sinks = count(o[6]);
+    const Launch l(dev, o[10]);
+    return status_of([&] {
+      return masked_gqa_attn_cache_weights(&at.a, at.paged, window, sinks, at.q4, wp, st, slots, l.stream);
+    });
+  });
+}
+
+// k_cache v_cache page_table ref budget
+PyObject *cache_evict_workspace_size(PyObject *, PyObject *const *o, Py_ssize_t n) {
+  return guarded(o, n, 5, [&] {
+    const Tensor &k = tensor(o[0], "k_cache");
+    const Cache cache(k, tensor(o[1], "v_cache"), optional_tensor(o[2], "page_table"), nullptr,
+                      optional_tensor(o[3], "ref"), nullptr);
+    return PyLong_FromSize_t(masked_gqa_cache_evict_workspace_size(&cache.c, count(o[4])));
+  });
+}
+
+// k_cache v_cache weight kv_len budget sinks recent page_table ref weight_out kv_len_out workspace dev_error stream
+PyObject *cache_evict(PyObject *, PyObject *const *o, Py_ssize_t n) {
+  return guarded(o, n, 14, [&] {
+    const Tensor &k = tensor(o[0], "k_cache"), &v = tensor(o[1], "v_cache"), &w = tensor(o[2], "weight"),
+                 &len = tensor(o[3], "kv_len"), &wo = tensor(o[9], "weight_out"), &len_out = tensor(o[10], "kv_len_out"),
+                 &ws = tensor(o[11], "workspace");
+    const Tensor *table = optional_tensor(o[7], "page_table"), *ref = optional_tensor(o[8], "ref"),
+                 *err = optional_tensor(o[12], "dev_error");
+    const int dev = device_of(k);
+    together(dev, {{&v, "v_cache"}, {&w, "weight"}, {&len, "kv_len"}, {&wo, "weight_out"}, {&len_out, "kv_len_out"},
+                   {&ws, "workspace"}, {table, "page_table"}, {ref, "ref"}, {err, "dev_error"}});
+    const Cache cache(k, v, table, &len, ref, err);
+    int32_t slots = 0x7fffffff;
+    int64_t in[3] = {0}, out[3] = {0};
+    const bool layered = k.dim() == 5;
+    const auto take = [&](const Tensor &x, const char *name, int64_t *st) {
+      return layered ? weights(x, name, {cache.layers, cache.rows, cache.Hkv}, st, slots)
+                     : weights(x, name, {cache.rows, cache.Hkv}, st + 1, slots);
+    };
+    const float *wp = take(w, "weight", in);
+    float *wop = take(wo, "weight_out", out);
+    int32_t *lp = ints(&len_out, "kv_len_out", {cache.rows});
+    const int32_t budget = count(o[4]), sinks = count(o[5]), recent = count(o[6]);
+    void *p = ws.data_ptr();
+    const size_t wn = ws.nbytes();
+    const Launch l(dev, o[13]);
+    return status_of([&] {
+      return masked_gqa_cache_evict(&cache.c, wp, in, wop, out, slots, budget, sinks, recent, lp, p, wn, l.stream);
     });
   });
 }
@@ -427,7 +557,8 @@ PyObject *cache_compact(PyObject *, PyObject *const *o, Py_ssize_t n) {
 
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(prefill_window), FAST(decode_window), FAST(decode_tree), FAST(cache_append),
-                         FAST(cache_workspace_size), FAST(cache_fork), FAST(cache_compact),
+                         FAST(cache_workspace_size), FAST(cache_fork), FAST(cache_compact), FAST(cache_append_q4),
+                         FAST(decode_q4), FAST(cache_weights), FAST(cache_evict_workspace_size), FAST(cache_evict),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mgqa_bind", nullptr, -1, methods};
 

@@ -105,9 +105,9 @@ mgqa_status launch_merge(const CacheAttnParams &p, int block_rows, int grid, cud
   if (block_rows == 16) return launch_merge<T, D, 16>(p, grid, s);
   if (block_rows == 32) return launch_merge<T, D, 32>(p, grid, s);
   if (block_rows == 64) return launch_merge<T, D, 64>(p, grid, s);
+  if (block_rows == 8) return launch_merge<T, D, 8>(p, grid, s);
   if constexpr (sizeof(T) == 4) {
     if (block_rows == 4) return launch_merge<T, D, 4>(p, grid, s);
-    if (block_rows == 8) return launch_merge<T, D, 8>(p, grid, s);
     if (block_rows == 48) return launch_merge<T, D, 48>(p, grid, s);
   } else {
     if (block_rows == 128) return launch_merge<T, D, 128>(p, grid, s);
@@ -134,9 +134,9 @@ mgqa_status launch_cache_merge(const CacheAttnParams &p, mgqa_dtype dt, int D, i
   return D == 64 ? launch_merge<float, 64>(p, block_rows, grid, s) : launch_merge<float, 128>(p, block_rows, grid, s);
 }
 
-mgqa_status launch_cache_attn(const mgqa_args &a, const mgqa_pages *pages, const mgqa_tree *tree, int32_t window,
-                              int32_t sinks, void *ws, cudaStream_t s) {
-  CacheAttnParams p{};
+void cache_attn_params(const mgqa_args &a, const mgqa_pages *pages, const mgqa_tree *tree, int32_t window,
+                              int32_t sinks, CacheAttnParams &p) {
+  p = CacheAttnParams{};
   p.q = a.q; p.k = a.k; p.v = a.v; p.out = a.out;
   for (int t = 0; t < 3; ++t) {
     p.qs[t] = a.q_stride[t]; p.ks[t] = a.k_stride[t];
@@ -172,6 +172,12 @@ mgqa_status launch_cache_attn(const mgqa_args &a, const mgqa_pages *pages, const
   p.R = p.T * p.n_rep;
   p.scale_log2 = a.scale * kLog2e;
   p.lse = a.lse; p.err = a.dev_error;
+}
+
+mgqa_status launch_cache_attn(const mgqa_args &a, const mgqa_pages *pages, const mgqa_tree *tree, int32_t window,
+                              int32_t sinks, void *ws, cudaStream_t s) {
+  CacheAttnParams p;
+  cache_attn_params(a, pages, tree, window, sinks, p);
   const CacheAttnLaunch how{ws, device_sm_count()};
   if (how.sms < 1) return fail(MGQA_ERR_CUDA, "cannot read the SM count of the current device");
   if (a.dtype == MGQA_FP32) return launch_cache_attn_f32(p, a.D, how, s);

@@ -129,6 +129,135 @@ append_kernel(const __grid_constant__ AppendParams p) {
   }
 }
 
+// ---- append to a cache in 4 bits -----------------------------------------------------
+
+// As append, the rows quantised on the way (cache_q4.cuh has the record). A thread
+// has eight features of a row of K and of V; a group's extremes are found between
+// its 4 (D = 64: 2) threads. Every step is one fp32 operation, so the codes are the
+// same wherever they are computed:
+//   least = fp16(min), scale = fp16((max - least) fl(1/15)), both within +-65504 and
+//   without a negative zero; u = clamp(rint((x - least) / scale), 0, 15), 0 where
+//   scale is 0.
+struct Q4Piece {
+  uint32_t codes;  // of the thread's eight features, in the record's order
+  uint32_t par;    // scale and least value of its group
+};
+
+template <typename T>
+MGQA_DEV void load_eight(const char *p, float (&x)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  } else {
+    unpack16_t<T>(__ldcs(reinterpret_cast<const uint4 *>(p)), x);
+  }
+}
+
+// mask: the lanes of the row, all of which take part.
+template <int D>
+MGQA_DEV Q4Piece quantise(const float (&x)[8], uint32_t mask) {
+  float lo = x[0], hi = x[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    lo = fminf(lo, x[i]);
+    hi = fmaxf(hi, x[i]);
+  }
+#pragma unroll
+  for (int o = 1; o < D / 32; o <<= 1) {
+    lo = fminf(lo, __shfl_xor_sync(mask, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(mask, hi, o));
+  }
+  uint32_t least = __half_as_ushort(__float2half_rn(fminf(fmaxf(lo, -65504.f), 65504.f)));
+  if (least == 0x8000u) least = 0u;
+  const float base = __half2float(__ushort_as_half((unsigned short)least));
+  const float range = __fmul_rn(__fsub_rn(hi, base), 1.f / 15.f);
+  const __half scale = __float2half_rn(fminf(fmaxf(range, 0.f), 65504.f));
+  const float step = __half2float(scale);
+  Q4Piece r;
+  r.par = (uint32_t)__half_as_ushort(scale) | least << 16;
+  r.codes = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float u = step > 0.f ? rintf(__fdiv_rn(__fsub_rn(x[i], base), step)) : 0.f;
+    r.codes |= (uint32_t)(int)fminf(fmaxf(u, 0.f), 15.f) << (4 * i);
+  }
+  if constexpr (D == 64) {
+    // the bytes of groups 0 and 1 (2 and 3) by turns: the first group's thread keeps
+    // the first two bytes of each, the other one the last two
+    const uint32_t other = __shfl_xor_sync(mask, r.codes, 2);
+    r.codes = (threadIdx.x & 2) ? __byte_perm(other, r.codes, 0x7362) : __byte_perm(r.codes, other, 0x5140);
+  }
+  return r;
+}
+
+// The thread's part of a record: its codes, and from the row's first thread the parameters.
+template <int D>
+MGQA_DEV void store_record(char *rec, const Q4Piece &r, int piece, uint32_t mask) {
+  constexpr int GL = D / 32;  // threads of a group
+  uint32_t g[4];
+  const int first = (int)(threadIdx.x & 31) - piece;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) g[i] = __shfl_sync(mask, r.par, first + i * GL);
+  if (!rec) return;
+  // (D = 64: threads 0..3 of a chunk have its words 0, 2, 1, 3)
+  const int word = D == 64 ? (piece & ~3) | (piece & 1) << 1 | (piece >> 1 & 1) : piece;
+  __stcs(reinterpret_cast<uint32_t *>(rec) + word, r.codes);
+  if (piece == 0)
+    __stcs(reinterpret_cast<uint4 *>(rec + D / 2),
+           make_uint4(__byte_perm(g[0], g[1], 0x5410), __byte_perm(g[2], g[3], 0x5410), __byte_perm(g[0], g[1], 0x7632),
+                      __byte_perm(g[2], g[3], 0x7632)));
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kAppendThreads)
+append_q4_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int LR = D / 8;  // threads of a row
+  const Pool &c = p.c;
+  const int b = blockIdx.y, layer = blockIdx.z;
+  grid_dependency_wait();
+  allow_dependents();
+  const int64_t cap = c.table ? (int64_t)c.max_pages * c.page_size : c.page_size;
+  const auto load = [&](const int32_t *x) { return p.ints_apart ? __ldg(x) : __ldcg(x); };
+  const int n = load(c.kv_len + b);
+  const int cnt = p.count ? load(p.count + b) : p.T;
+  const bool bad = n < 0 || cnt < 0 || cnt > p.T || (int64_t)n + cnt > cap;
+  const int per = c.Hkv * LR;
+  const int t0 = (int)blockIdx.x * p.block_rows, rows = min(p.block_rows, p.T - t0);
+  const uint32_t mask = low_mask(LR) << (threadIdx.x & 31 & ~(LR - 1));  // (a row's threads go together)
+  for (int i = threadIdx.x; i < rows * per; i += kAppendThreads) {
+    const int tl = i / per, rem = i - tl * per, t = t0 + tl;
+    const int h = rem / LR, piece = rem % LR;
+    if (p.count && (bad || t >= cnt)) break;
+    const int from = p.index ? load(p.index + (int64_t)b * p.T + t) : t;
+    const bool has = (unsigned)from < (unsigned)p.T;
+    float kx[8] = {}, vx[8] = {};
+    if (has) {
+      const int64_t at = (int64_t)from;
+      load_eight<T>(p.kn + layer * p.kns[0] + b * p.kns[1] + h * p.kns[2] + at * p.kns[3] + piece * (8 * (int)sizeof(T)), kx);
+      load_eight<T>(p.vn + layer * p.vns[0] + b * p.vns[1] + h * p.vns[2] + at * p.vns[3] + piece * (8 * (int)sizeof(T)), vx);
+    }
+    if (bad) break;
+    const int j = n + t;
+    int page = b, slot = j;
+    if (c.table) {
+      const int pi = j / c.page_size;
+      page = valid_page(c, load(c.table + (int64_t)b * c.table_stride + pi));
+      slot = j - pi * c.page_size;
+    }
+    const bool to = has && page >= 0;
+    if (!to && layer == 0 && rem == 0) report_error(c.err, MGQA_ERR_INVALID_ARG);
+    store_record<D>(to ? c.k + layer * c.ks[0] + (int64_t)page * c.ks[1] + h * c.ks[2] + (int64_t)slot * c.ks[3] : nullptr,
+                    quantise<D>(kx, mask), piece, mask);
+    store_record<D>(to ? c.v + layer * c.vs[0] + (int64_t)page * c.vs[1] + h * c.vs[2] + (int64_t)slot * c.vs[3] : nullptr,
+                    quantise<D>(vx, mask), piece, mask);
+  }
+  if (blockIdx.x == 0 && layer == 0 && threadIdx.x == 0) {
+    if (bad) report_error(c.err, MGQA_ERR_INVALID_ARG);
+    p.kv_len_out[b] = bad ? n : n + cnt;
+  }
+}
+
 // ---- copies of (parts of) pages --------------------------------------------------
 
 // Slots [0, slots) of page a of one layer's K or V to page b, by `warps` warps
@@ -577,9 +706,16 @@ size_t cache_pages_workspace_bytes(const mgqa_cache &c, int n) {
 
 mgqa_status launch_cache_append(const mgqa_cache &c, const void *k_new, const void *v_new, const int64_t *ks,
                                 const int64_t *vs, int32_t T, const int32_t *index, const int32_t *count,
-                                int32_t *kv_len_out, cudaStream_t s) {
+                                int32_t *kv_len_out, bool q4, cudaStream_t s) {
   AppendParams p{};
   p.c = pool_of(c);
+  if (q4) {
+    p.c.pieces = c.D / 8;  // threads of a row
+    for (int t = 0; t < 4; ++t) {
+      p.c.ks[t] = c.k_stride[t];
+      p.c.vs[t] = c.v_stride[t];
+    }
+  }
   p.kn = static_cast<const char *>(k_new);
   p.vn = static_cast<const char *>(v_new);
   const int64_t es = c.dtype == MGQA_FP32 ? 4 : 2;
@@ -600,7 +736,13 @@ mgqa_status launch_cache_append(const mgqa_cache &c, const void *k_new, const vo
   const int64_t bx = (T + p.block_rows - 1) / p.block_rows;
   if (c.rows > 65535 || c.layers > 65535 || bx > 0x7fffffff)
     return fail(MGQA_ERR_UNSUPPORTED, "more than 65535 requests or layers");
-  return launched(launch_pdl(append_kernel, dim3((unsigned)bx, c.rows, c.layers), dim3(kAppendThreads), 0, s, p),
+  auto kern = append_kernel;
+  if (q4) {
+    kern = c.dtype == MGQA_BF16   ? (c.D == 64 ? append_q4_kernel<__nv_bfloat16, 64> : append_q4_kernel<__nv_bfloat16, 128>)
+           : c.dtype == MGQA_FP16 ? (c.D == 64 ? append_q4_kernel<__half, 64> : append_q4_kernel<__half, 128>)
+                                  : (c.D == 64 ? append_q4_kernel<float, 64> : append_q4_kernel<float, 128>);
+  }
+  return launched(launch_pdl(kern, dim3((unsigned)bx, c.rows, c.layers), dim3(kAppendThreads), 0, s, p),
                   "cache append");
 }
 

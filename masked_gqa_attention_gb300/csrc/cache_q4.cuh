@@ -1,0 +1,225 @@
+// Rows of a cache in 4 bits, and products with them on the tensor cores.
+//
+// A row of D features is a record of D/2 + 16 bytes: four groups of D/4 features,
+// each with codes u in 0..15, a scale and a least value (fp16), x = scale u + least.
+// The codes come first, two a byte (the even feature in the low half; D = 128: a
+// group is 16 bytes; D = 64: 8 bytes, with those of groups 0 and 1, and of 2 and 3,
+// by turns), then the four scales and the four least values.
+//
+// The raw bits of a code in the low bits of an fp16 are the number u 2^-24 (a
+// subnormal), and one place higher u 2^-20, so four masks and a shift make eight
+// codes exact tensor-core operands, with nothing subtracted and nothing rounded;
+// the scales and least values come in beside the products:
+//   s_j   = sum_g scale_jg <q_g, u_jg> + sum_g least_jg sum(q_g)
+//   out_d = sum_j (p_j scale_jg(d)) u_jd + sum_j p_j least_jg(d)
+// The least values' sums are products with the eight parameters of a record, taken
+// as a row (or column) of 8. (As 16-bit rows, scaled and rounded, a value took 1.3
+// instructions to unpack instead of 0.63, and lost 2^-9 of it.)
+// A pitch of 80 (48) bytes spreads eight rows over all banks, so records are copied
+// as they lie.
+#pragma once
+
+#include "common.cuh"
+
+namespace mgqa {
+
+template <int D>
+struct Q4 {
+  static constexpr int CODES = D / 2;        // bytes of codes
+  static constexpr int REC = CODES + 16;     // bytes of a record
+  static constexpr int CHUNKS = CODES / 16;  // 16-byte pieces of codes
+  static constexpr int KS = D / 64;          // products of 16 features per group
+  static constexpr int GW = D / 4;           // features of a group
+  // Feature of value i of a query's fragment in group g: a lane (quad place tq) has
+  // GW / 4 features of every group, one run of them.
+  static MGQA_DEV int first(int g, int tq) { return g * GW + tq * (GW / 4); }
+  // First feature of what a lane (gq) has of the outputs of chunk c, and how many
+  // features follow it: half h adds the codes 2h and 2h + 1 of a 16-bit unit.
+  static MGQA_DEV int out_feature(int c, int h, int gq) {
+    return D == 128 ? 32 * c + 4 * gq + 2 * h : 16 * (2 * c + h) + 2 * gq;
+  }
+  static constexpr int group_of(int c, int h) { return D == 128 ? c : 2 * c + h; }
+};
+
+// Eight codes as four operand registers: the low and the next code of each 16-bit
+// unit (worth 2^-24 and 2^-20), then those of its upper byte.
+MGQA_DEV void q4_unpack(uint32_t w, uint32_t (&a)[4]) {
+  a[0] = w & 0x000f000fu;
+  a[1] = w & 0x00f000f0u;
+  w >>= 8;
+  a[2] = w & 0x000f000fu;
+  a[3] = w & 0x00f000f0u;
+}
+
+// 2^k, k in [-126, 127].
+MGQA_DEV float pow2i(int k) { return __int_as_float((k + 127) << 23); }
+
+// One query row's operands in a lane (quad place tq): fp16 of q 2^k, the row's
+// largest in [2^9, 2^10), so bf16 and fp16 queries keep every bit that counts (what
+// is below 2^-24 of the row's largest loses some). fp32 ones are two terms (22
+// bits). The second code of a unit is worth 16 times the first: its features are
+// divided by that. `sums`: the groups' sums in two terms, for the least values (the
+// lanes tq 2 and 3 have them; the scales' columns are 0).
+template <int D, bool SPLIT>
+struct Q4Row {
+  uint32_t a[4][Q4<D>::KS][2], b[SPLIT ? 4 : 1][Q4<D>::KS][2];  // b: second terms
+  uint32_t sums[2];
+  float down;  // 2^-k
+
+  template <typename T>
+  MGQA_DEV void load(const T *row, int tq) {  // null: zeros. (The four lanes of a quad together.)
+    constexpr int N = Q4<D>::GW / 4;  // features of a group
+    float x[4][N];
+    float top = 0.f;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      if (row) {
+        const T *src = row + Q4<D>::first(g, tq);
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+          for (int i = 0; i < N; i += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(src + i);
+            x[g][i] = v.x; x[g][i + 1] = v.y; x[g][i + 2] = v.z; x[g][i + 3] = v.w;
+          }
+        } else if constexpr (N == 8) {
+          unpack16_t<T>(*reinterpret_cast<const uint4 *>(src), x[g]);
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2 *>(src);
+          float f[8];
+          unpack16_t<T>(make_uint4(u.x, u.y, 0u, 0u), f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[g][i] = f[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[g][i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) top = fmaxf(top, fabsf(x[g][i]));
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int e = (int)(__float_as_uint(top) >> 23) - 127;  // (0: -127)
+    const int k = min(9 - e, 120);
+    const float up = pow2i(k);
+    down = pow2i(-k);
+    float sum[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      sum[g] = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        x[g][i] *= up;
+        sum[g] += x[g][i];
+      }
+      sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+      sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+#pragma unroll
+      for (int s = 0; s < Q4<D>::KS; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // D = 128: features {2s, 2s + 4}, {2s + 1, 2s + 5}; D = 64: {0, 2}, {1, 3}
+          const float m = h ? 0.0625f : 1.f;
+          const float u = x[g][2 * s + h] * m, v = x[g][2 * s + h + (N == 8 ? 4 : 2)] * m;
+          a[g][s][h] = pack2<__half>(u, v);
+          if constexpr (SPLIT) {
+            const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&a[g][s][h]));
+            b[g][s][h] = pack2<__half>(u - hi.x, v - hi.y);
+          }
+        }
+    }
+    sums[0] = sums[1] = 0u;
+    if (tq >= 2) {
+      const float u = tq == 2 ? sum[0] : sum[2], v = tq == 2 ? sum[1] : sum[3];
+      sums[0] = pack2<__half>(u, v);
+      const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&sums[0]));
+      sums[1] = pack2<__half>(u - hi.x, v - hi.y);
+    }
+  }
+};
+
+// Four halves at p (8-byte aligned, shared memory) as floats.
+MGQA_DEV void q4_four(const unsigned char *p, float (&f)[4]) {
+  const uint2 w = *reinterpret_cast<const uint2 *>(p);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
+  f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+}
+
+// Scores of 8 RT query rows (RT = 1: rows gq of a warp; else gq and gq + 8, ...)
+// with 32 keys, whose records lie at `tile` in shared memory: s[r][n][e], row group
+// r, key 8 n + 2 tq + e, unscaled (q 2^k's: times `down`).
+template <int D, int RT, bool SPLIT>
+MGQA_DEV void q4_scores(const Q4Row<D, SPLIT> (&q)[RT], const unsigned char *tile, float (&s)[RT][4][2]) {
+  using F = Q4<D>;
+  const int lane = threadIdx.x & 31, tq = lane & 3;
+  const unsigned char *mine = tile + lane * F::REC;  // ldmatrix: lane = key
+  uint32_t par[4];
+  ldmatrix_x4(par[0], par[1], par[2], par[3], mine + F::CODES);
+  float sc[4][2][4];  // scales of the lane's keys
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      q4_four(tile + (8 * n + 2 * tq + e) * F::REC + F::CODES, sc[n][e]);
+    }
+  constexpr int MT = (RT + 1) / 2;
+  float least[MT][4][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      float(&c)[4] = least[m][n];
+      c[0] = c[1] = c[2] = c[3] = 0.f;
+      constexpr bool two = RT > 1;
+      const int r1 = two ? 2 * m + 1 : 0;
+      mma_16816<__half>(c, q[2 * m].sums[0], two ? q[r1].sums[0] : 0u, q[2 * m].sums[1], two ? q[r1].sums[1] : 0u,
+                        par[n], par[n]);
+    }
+  float acc[RT][4][2];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int n = 0; n < 4; ++n) acc[r][n][0] = acc[r][n][1] = 0.f;
+#pragma unroll
+  for (int c = 0; c < F::CHUNKS; ++c) {
+    uint32_t w[4];
+    ldmatrix_x4(w[0], w[1], w[2], w[3], mine + c * 16);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      uint32_t u[4];
+      q4_unpack(w[n], u);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        constexpr bool two = RT > 1;
+        const int r0 = 2 * m, r1 = two ? 2 * m + 1 : 0;
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int g = F::group_of(c, h), st = D == 128 ? h : 0;
+          mma_16816<__half>(part, q[r0].a[g][st][0], two ? q[r1].a[g][st][0] : 0u, q[r0].a[g][st][1],
+                            two ? q[r1].a[g][st][1] : 0u, u[2 * h], u[2 * h + 1]);
+          if constexpr (SPLIT)
+            mma_16816<__half>(part, q[r0].b[g][st][0], two ? q[r1].b[g][st][0] : 0u, q[r0].b[g][st][1],
+                              two ? q[r1].b[g][st][1] : 0u, u[2 * h], u[2 * h + 1]);
+          if (D == 64 || h == 1) {  // the group is complete
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              acc[r0][n][e] = fmaf(part[e], sc[n][e][g], acc[r0][n][e]);
+              if (two) acc[r1][n][e] = fmaf(part[2 + e], sc[n][e][g], acc[r1][n][e]);
+            }
+            part[0] = part[1] = part[2] = part[3] = 0.f;
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) s[r][n][e] = fmaf(acc[r][n][e], 16777216.f, least[r / 2][n][(r & 1) * 2 + e]);
+}
+
+}  // namespace mgqa

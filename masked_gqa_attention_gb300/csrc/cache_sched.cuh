@@ -36,7 +36,7 @@ struct CacheAttnParams {
   const uint32_t *bits;  // null: each draft sees those before it
   int64_t bits_b, bits_t;
   int32_t window, sinks;  // window: kNoWindow when there is none
-  int32_t tree;           // 1: drafts follow the cache; 0: the one query is the last cached token
+  int32_t tree;           // 1: drafts follow the cache; 0: the queries are the last T cached tokens
   int32_t B, Hq, Hkv, T, n_rep, R, RB;  // R = T * n_rep rows per KV head, in RB blocks
   int32_t block_rows;                   // query rows of a block (a unit's)
   int32_t tile_shift;                   // log2 of a tile's keys
@@ -77,6 +77,9 @@ inline void set_partials(CacheAttnParams &p, void *ws, int grid, int block_rows,
   p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)2 * grid * block_rows * D);
 }
 
+// The parameters of a call, but for those of the kernel's form.
+void cache_attn_params(const mgqa_args &a, const mgqa_pages *pages, const mgqa_tree *tree, int32_t window,
+                       int32_t sinks, CacheAttnParams &p);
 mgqa_status launch_cache_merge(const CacheAttnParams &p, mgqa_dtype dt, int D, int block_rows, int grid,
                                cudaStream_t s);
 // 16 bits on mma.sync: few rows, or any (in blocks of 64).
@@ -118,7 +121,7 @@ MGQA_DEV RowPlan plan_row(const CacheAttnParams &p, int b, bool report) {
   n = min(max(n, 0), p.cap);
   r.n = n;
   r.live = live;
-  const int p0 = p.tree ? n : n - 1;  // the first query's position
+  const int p0 = p.tree ? n : n - p.T;  // the first query's position
   r.lo = min(max(p0 - p.window + 1, 0), n);
   r.s_end = min(p.sinks, r.lo);
   const int ts = p.tile_shift, up = (1 << ts) - 1;

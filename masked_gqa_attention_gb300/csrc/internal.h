@@ -129,6 +129,12 @@ constexpr int kCacheAttnMaxCtas = 320;  // partial results in the workspace: two
 size_t cache_attn_workspace_bytes();
 mgqa_status launch_cache_attn(const mgqa_args &a, const mgqa_pages *pages, const mgqa_tree *tree,
                               int32_t window, int32_t sinks, void *ws, cudaStream_t s);
+// The last Lq cached tokens over a cache in 4 bits (strides of k and v in bytes).
+mgqa_status launch_attn_q4(const mgqa_args &a, const mgqa_pages *pages, int32_t window, int32_t sinks, void *ws,
+                           cudaStream_t s);
+// The weights that those tokens give to every slot, added to `weight`.
+mgqa_status launch_cache_weights(const mgqa_args &a, const mgqa_pages *pages, int32_t window, int32_t sinks, bool q4,
+                                 float *weight, const int64_t *weight_stride, int32_t weight_slots, cudaStream_t s);
 constexpr int kMaxDraftsHost = 256;  // drafted tokens of a request
 
 // The cache's own steps (cache_pages.cu).
@@ -139,7 +145,11 @@ size_t cache_pages_workspace_bytes(const mgqa_cache &c, int n);
 mgqa_status launch_cache_append(const mgqa_cache &c, const void *k_new, const void *v_new,
                                 const int64_t *ks, const int64_t *vs, int32_t T,
                                 const int32_t *index, const int32_t *count, int32_t *kv_len_out,
-                                cudaStream_t s);
+                                bool q4, cudaStream_t s);  // q4: rows in 4 bits, the cache's strides in bytes
+size_t cache_evict_workspace_bytes(const mgqa_cache &c, int32_t budget);
+mgqa_status launch_cache_evict(const mgqa_cache &c, const float *weight, const int64_t *ws_in, float *weight_out,
+                               const int64_t *ws_out, int32_t weight_slots, int32_t budget, int32_t sinks,
+                               int32_t recent, int32_t *kv_len_out, void *ws, cudaStream_t s);
 mgqa_status launch_cache_fork(const mgqa_cache &c, int n, const int32_t *src, const int32_t *dst,
                               int32_t extra, void *ws, cudaStream_t s);
 mgqa_status launch_cache_compact(const mgqa_cache &c, int32_t *table_out, int64_t table_out_stride,
