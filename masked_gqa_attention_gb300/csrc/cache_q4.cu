@@ -8,16 +8,17 @@
 // Every visible record is read once per KV head and block of query rows; a warp
 // spends some 900 instructions on 64 keys of 128 features, which the reads take
 // 435 cycles for, so the kernel has to keep both going. Each warp streams tiles of
-// 32 keys of its own through a ring in shared memory: one bulk copy per page and
-// tensor, counted on the warp's own barrier, and no barrier between warps inside a
-// unit. Rows of queries are the first operand of the scores and the second one of
-// the outputs (transposed), so the scores' accumulators are the weights' operand as
-// they are.
+// 32 keys of its own through a ring in shared memory, by 16-byte asynchronous copies
+// that only it waits for: no barrier between warps inside a unit. (One bulk copy per
+// page and tensor took more instructions than the products: 918 a tile, not 560.) The records are the first operand of both products (16 keys, or 16
+// features, by 8 rows of queries), so a code is unpacked once for all rows and no part
+// of a product is empty with 8 rows; the weights turn from one layout to the other by
+// four transposes of 8 x 8 a tile.
 //
-// Weights: p is 2^14 at most (the maximum is subtracted 14 short), and p times a
-// scale is divided by the largest scale's power of two so far, so the fp16 operand
-// keeps 2^-11 of it down to 2^-28 of the largest (2^-22 in two terms for fp32
-// calls). Sums of weights and outputs are fp32, a tile's from the tensor cores and
+// Weights: p is 2^14 at most (the maximum is subtracted 14 short) and becomes fp16,
+// 2^-11 of it down to 2^-28 of the largest; p times a scale is rounded once more.
+// Scales of 2 and more are divided by a power of two first, which the outputs are in
+// units of. fp32 calls hold both in two terms (2^-22). Sums of weights and outputs are fp32, a tile's from the tensor cores and
 // those of the tiles in rounded additions: codes and least values are sums of one
 // sign that nearly cancel, and the tensor cores' accumulators truncate (32 rows of
 // 98000 keys: 0.0066 of the outputs' size from 64 bits with running accumulators).
@@ -41,18 +42,128 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kShift = 5, kKeys = 32;  // keys of a tile
+constexpr float kNothing = -3.4028235e38f;  // the maximum of a row that has seen nothing (no score is below it)
 constexpr int kMostCtas = 512;         // partial results: two per CTA
 
 struct Q4Params {
   TmaParams t;  // (its strides of k and v are bytes)
-  int32_t run_slots;  // slots of a page that lie one after the other: page_size (or cap), or 1
+  uint32_t kstep[2], vstep[2];  // from page to page and from slot to slot, in 16-byte pieces
+  int32_t alike;                // they agree
+  int32_t halves;               // the slots of half a tile lie one after the other
+};
+
+// The tiles of a warp, in order, ahead of their use: every kWarps-th of each piece.
+// What stays the same in a piece is in shared memory, one per warp (in registers it
+// took as many as the outputs).
+struct alignas(16) Feed {
+  int ns, past, np, n;      // first slot of tile t < np: (t < ns ? t : t + past) * kKeys
+  int lo, s_end;            // slots between s_end and lo are hidden
+  const int32_t *table;     // of the request; null: static
+  const char *k, *v;        // of the KV head (and, static, of the request)
+  Pieces pieces;
+};
+struct Ahead {
+  Feed &f;
+  int t, end;              // next tile, end of its piece
+  int k0, page, slot;      // its first slot; where the lane's row is
+  bool want, live;         // the row is wanted; there is a tile
+
+  MGQA_DEV void settle(const Q4Params &p, int warp, int lane) {  // to the next tile that there is
+    const CacheAttnParams &c = p.t.a;
+    while (live && t >= end) {
+      Pieces all = f.pieces;
+      Piece pc;
+      live = all.next(c, pc);
+      __syncwarp();
+      if (lane == 0) {
+        f.pieces = all;
+        f.ns = pc.rp.ns;
+        f.past = pc.rp.mt0 - pc.rp.ns;
+        f.np = pc.rp.np;
+        f.n = pc.rp.n;
+        f.lo = pc.rp.lo;
+        f.s_end = pc.rp.s_end;
+        f.table = c.table ? c.table + (int64_t)pc.b * c.table_stride : nullptr;
+        f.k = static_cast<const char *>(c.k) + pc.g * c.ks[1] + (c.table ? 0 : pc.b * c.ks[0]);
+        f.v = static_cast<const char *>(c.v) + pc.g * c.vs[1] + (c.table ? 0 : pc.b * c.vs[0]);
+      }
+      __syncwarp();
+      t = pc.t0 + warp;
+      end = pc.t1;
+    }
+    if (live) {
+      const int4 x = *reinterpret_cast<const int4 *>(&f.ns);
+      const int2 y = *reinterpret_cast<const int2 *>(&f.lo);
+      k0 = (t < x.x ? t : t + x.y) * kKeys;
+      const int j = k0 + lane;
+      page = slot = 0;
+      want = t < x.z && j < x.w && (j >= y.x || j < y.y);
+      if (want) {
+        slot = j;
+        if (f.table) {
+          const int i = c.page_shift >= 0 ? j >> c.page_shift : j / c.page_size;
+          slot = j - i * c.page_size;
+          page = __ldg(f.table + i);  // (looked at by the next issue: here its latency would show)
+        }
+      }
+    }
+  }
+  MGQA_DEV void start(const Q4Params &p, const Pieces &all, int warp, int lane) {
+    if (lane == 0) f.pieces = all;
+    __syncwarp();
+    live = true;
+    t = end = 0;
+    settle(p, warp, lane);
+  }
+  // Starts the copies of the tile that was looked up (zeros for the rows that do not
+  // count), and looks the next one up. Consecutive lanes copy consecutive 16-byte
+  // pieces; a lane knows where its row is.
+  template <int D>
+  MGQA_DEV void issue(const Q4Params &p, int warp, int lane, unsigned char *dst, int2 *what) {
+    constexpr int P = Q4<D>::REC / 16;  // pieces of a record, and copies of a lane
+    const bool there = !p.t.a.table || (unsigned)page < (unsigned)p.t.a.num_pages;
+    if (want && !there) report_error(p.t.a.err, MGQA_ERR_INVALID_ARG);
+    const uint32_t ok = __ballot_sync(0xffffffffu, want && there);
+    if (lane == 0) *what = make_int2(k0, (int)ok);
+    const uint32_t pg = there ? (uint32_t)page : 0u, sl = (uint32_t)slot;
+    const uint64_t at = (uint64_t)pg * p.kstep[0] + (uint64_t)sl * p.kstep[1];  // in pieces
+    const uint64_t av = p.alike ? at : (uint64_t)pg * p.vstep[0] + (uint64_t)sl * p.vstep[1];
+    const char *k = f.k, *v = f.v;
+    if (p.halves && ok == 0xffffffffu) {  // two runs of 16 rows
+      constexpr int kRun = 16 * Q4<D>::REC;  // (a lane's piece of the one or the other)
+      const uint64_t a = __shfl_sync(0xffffffffu, at, 0), b = __shfl_sync(0xffffffffu, at, 16);
+      const char *ka = k + a * 16 + lane * 16, *kb = k + b * 16 + lane * 16 - kRun;
+      const char *va = v + a * 16 + lane * 16, *vb = v + b * 16 + lane * 16 - kRun;
+      dst += lane * 16;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const bool second = 512 * i >= kRun || (512 * i + 512 > kRun && 512 * i + lane * 16 >= kRun);
+        cp_async16(dst + 512 * i, (second ? kb : ka) + 512 * i);
+        cp_async16(dst + kKeys * Q4<D>::REC + 512 * i, (second ? vb : va) + 512 * i);
+      }
+      t += kWarps;
+      settle(p, warp, lane);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int row = (lane + 32 * i) / P, piece = (lane + 32 * i) % P;
+      const uint64_t to = __shfl_sync(0xffffffffu, at, row) + piece;
+      const uint64_t tv = p.alike ? to : __shfl_sync(0xffffffffu, av, row) + piece;
+      const bool take = ok >> row & 1u;
+      cp_async16_or_zero(dst + (lane + 32 * i) * 16, k + to * 16, take);
+      cp_async16_or_zero(dst + kKeys * Q4<D>::REC + (lane + 32 * i) * 16, v + tv * 16, take);
+    }
+    t += kWarps;
+    settle(p, warp, lane);
+  }
 };
 
 template <int D, int RT>
 struct Cfg {
   static constexpr int ROWS = 8 * RT;
-  static constexpr int STAGES = RT == 4 ? 4 : 3;
-  static constexpr int CTAS = 2;  // of an SM
+  static constexpr int STAGES = 2;
+  static constexpr int CTAS = RT == 1 ? 3 : 2;  // of an SM
   static constexpr int TILEB = kKeys * Q4<D>::REC;
   static constexpr int ring = kWarps * STAGES * 2 * TILEB;
   static constexpr int OP = D + 4;  // row pitch of a CTA's result (floats)
@@ -61,93 +172,10 @@ struct Cfg {
     float wm[kWarps][ROWS], wl[kWarps][ROWS];
     float2 ml[ROWS];
     LocateScratch<kThreads> scratch;
-    uint64_t full[kWarps][STAGES];
-    uint32_t ok[kWarps][STAGES];      // which keys of a stage's tile count
+    int2 what[kWarps][STAGES];        // a stage's first slot, and which keys count
+    Feed feed[kWarps];
   };
   static constexpr int smem = ring + (int)sizeof(Misc);
-};
-
-// The tiles of a warp, in order, ahead of their use: every kWarps-th of each piece.
-struct Feed {
-  Pieces pieces;
-  Piece pc;
-  int t, page;
-  bool live;
-
-  MGQA_DEV void settle(const Q4Params &p, int warp) {  // to the next tile that there is
-    while (live && t >= pc.t1) {
-      live = pieces.next(p.t.a, pc);
-      t = pc.t0 + warp;
-    }
-    if (live) look_up(p);
-  }
-  MGQA_DEV void start(const Q4Params &p, const Pieces &all, int warp) {
-    pieces = all;
-    live = true;
-    t = 0;
-    pc.t1 = 0;
-    settle(p, warp);
-  }
-  // Slots [a, e) of this lane's part of tile t: a page's, or one.
-  MGQA_DEV void part(const Q4Params &p, int &k0, int &a, int &e) const {
-    const CacheAttnParams &c = p.t.a;
-    const int lane = threadIdx.x & 31;
-    int kind;
-    k0 = first_key(pc.rp, t, kShift, kind);
-    const int end = kind ? k0 : min(k0 + kKeys, pc.rp.n);
-    if (p.run_slots == 1) {
-      a = k0 + lane;
-      e = a + 1;
-    } else if (c.table) {
-      const int i = (c.page_shift >= 0 ? k0 >> c.page_shift : k0 / c.page_size) + lane;
-      const int64_t s = (int64_t)i * c.page_size;
-      a = (int)min((int64_t)end, max((int64_t)k0, s));
-      e = (int)min((int64_t)end, s + c.page_size);
-    } else {
-      a = lane == 0 ? k0 : end;
-      e = end;
-    }
-    e = min(e, end);
-    if (e <= pc.rp.lo && a >= pc.rp.s_end) e = a;  // between the sinks and the window
-  }
-  MGQA_DEV void look_up(const Q4Params &p) {
-    int k0, a, e;
-    part(p, k0, a, e);
-    page = a < e ? page_of(p.t.a, pc.b, a) : -2;
-  }
-  // Starts the copies of the tile that was looked up, and looks the next one up.
-  template <int D>
-  MGQA_DEV void issue(const Q4Params &p, int warp, unsigned char *dst, uint64_t *full, uint32_t *ok) {
-    constexpr int REC = Q4<D>::REC;
-    const CacheAttnParams &c = p.t.a;
-    const int lane = threadIdx.x & 31;
-    int k0, a, e;
-    part(p, k0, a, e);
-    const bool take = page >= 0;
-    if (page == -1) report_error(c.err, MGQA_ERR_INVALID_ARG);
-    uint32_t bits = 0u;
-    int bytes = 0;
-    if (take) {
-      bytes = (e - a) * REC;
-      bits = low_mask(e - k0) & ~low_mask(a - k0) & (~low_mask(pc.rp.lo - k0) | low_mask(pc.rp.s_end - k0));
-    }
-    bits = __reduce_or_sync(0xffffffffu, bits);
-    const int total = __reduce_add_sync(0xffffffffu, bytes);
-    if (lane == 0) {
-      *ok = bits;
-      mbar_arrive_expect_tx(full, (uint32_t)(2 * total));
-    }
-    __syncwarp();
-    if (take) {
-      const int64_t slot = slot_in_page(c, a);
-      const char *k = static_cast<const char *>(c.k) + page * c.ks[0] + pc.g * c.ks[1] + slot * c.ks[2];
-      const char *v = static_cast<const char *>(c.v) + page * c.vs[0] + pc.g * c.vs[1] + slot * c.vs[2];
-      bulk_g2s(dst + (a - k0) * REC, k, (uint32_t)bytes, full);
-      bulk_g2s(dst + (kKeys + a - k0) * REC, v, (uint32_t)bytes, full);
-    }
-    t += kWarps;
-    settle(p, warp);
-  }
 };
 
 template <typename T, int D, int RT>
@@ -161,32 +189,28 @@ cache_q4_kernel(const __grid_constant__ Q4Params qp) {
   const CacheAttnParams &p = qp.t.a;
   extern __shared__ __align__(1024) unsigned char smem[];
   auto &sm = *reinterpret_cast<typename C::Misc *>(smem + C::ring);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, tq = lane & 3;
+  const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5, gq = lane >> 2, tq = lane & 3;
   unsigned char *ring = smem + warp * (STAGES * 2 * C::TILEB);
-  uint64_t *full = sm.full[warp];
-
-  if (lane == 0) {
-    for (int s = 0; s < STAGES; ++s) mbar_init(full + s, 1);
-    fence_mbarrier_init();
-  }
   if (warp == 1) touch_params(qp, lane);
   grid_dependency_wait();
   allow_dependents();
   Pieces pieces{};
-  pieces.start<kThreads>(qp.t, sm.scratch);  // (its barrier: the mbarriers are initialised)
+  pieces.start<kThreads>(qp.t, sm.scratch);
   const int S = pieces.S;
   const bool teller = tid == 0 && !S;
   if (teller) tell_cut(p, blockIdx.x, nullptr);
 
-  Feed feed;
-  feed.start(qp, pieces, warp);
-  int put = 0, it = 0, used = 0;  // tiles started, passed, and used
-  bool ok = true;
+  Ahead ahead{sm.feed[warp], 0, 0, 0, 0, 0, false, false};
+  ahead.start(qp, pieces, warp, lane);
+  int put = 0, st = 0;  // stages: filled next, used next
   const auto start_one = [&] {
-    feed.template issue<D>(qp, warp, ring + put % STAGES * 2 * C::TILEB, full + put % STAGES, sm.ok[warp] + put % STAGES);
-    ++put;
+    if (ahead.live) {
+      ahead.template issue<D>(qp, warp, lane, ring + put * 2 * C::TILEB, sm.what[warp] + put);
+      put = put + 1 == STAGES ? 0 : put + 1;
+    }
+    cp_async_commit();
   };
-  for (int s = 0; s < STAGES - 1 && feed.live; ++s) start_one();
+  for (int s = 0; s < STAGES - 1; ++s) start_one();
 
   if (pieces.idle())
     for (int r = tid; r < ROWS; r += kThreads) sm.ml[r] = make_float2(-INFINITY, 0.f);  // no share of the unit
@@ -196,61 +220,92 @@ cache_q4_kernel(const __grid_constant__ Q4Params qp) {
     const RowPlan &rp = pc.rp;
     const PieceOut po = out_of(p, pc, blockIdx.x);
     Q4Row<D, SPLIT> q[RT];
-    int pos[RT], lo[RT];
+    // of the rows 2 tq and 2 tq + 1 of each group, whose scores and outputs the lane has
+    float scale[RT][2];
+    int pos[RT][2];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       const int row = po.row0 + 8 * r + gq;
       const bool in = row < p.R;
       const int t = in ? row / p.n_rep : 0, h = pc.g * p.n_rep + (in ? row - t * p.n_rep : 0);
       q[r].load(in ? static_cast<const T *>(p.q) + (int64_t)pc.b * p.qs[0] + (int64_t)h * p.qs[1] + (int64_t)t * p.qs[2]
-                   : static_cast<const T *>(nullptr), tq);
-      pos[r] = in ? rp.n - p.T + t : -1;
-      lo[r] = pos[r] - p.window + 1;
+                   : static_cast<const T *>(nullptr), tq, p.scale_log2 < 0.f);
+      const int at = in ? rp.n - p.T + t : -1;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        // (above 0, so that a hidden key's -inf stays one)
+        scale[r][e] = fmaxf(__shfl_sync(0xffffffffu, q[r].down, 8 * tq + 4 * e) * fabsf(p.scale_log2), 1.2e-38f);
+        pos[r][e] = __shfl_sync(0xffffffffu, at, 8 * tq + 4 * e);
+      }
     }
     // every row of the block sees the keys from `far` (and the sinks) to `near`
     const int near = rp.n - p.T + po.row0 / p.n_rep;
     const int far = rp.n - p.T + (po.row0 + po.rows - 1) / p.n_rep - p.window + 1;
 
-    float o[RT][2 * NC][4], vmin[RT][2], m[RT], l[RT];
-    int top = -30;  // 2^top: above every scale of V so far
+    float o[RT][2 * NC][4], vmin[RT][2], m[RT][2], l[RT][2];
+    int top = SPLIT ? -30 : 0;  // outputs are in units of 2^top (see below)
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      m[r] = -INFINITY;
-      l[r] = 0.f;
-      vmin[r][0] = vmin[r][1] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[r][e] = kNothing;
+        l[r][e] = vmin[r][e] = 0.f;
+      }
 #pragma unroll
       for (int c = 0; c < 2 * NC; ++c) o[r][c][0] = o[r][c][1] = o[r][c][2] = o[r][c][3] = 0.f;
     }
-    for (int t = pc.t0 + warp; t < pc.t1; t += kWarps, ++it) {
-      if (ok && feed.live) start_one();
-      const int st = it % STAGES;
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(full + st, (it / STAGES) & 1, p.err));
-      if (!ok) continue;
-      used = it + 1;
+    for (int t = pc.t0 + warp; t < pc.t1; t += kWarps) {
+      start_one();
+      cp_async_wait<STAGES - 1>();
+      __syncwarp();
       const unsigned char *kt = ring + st * 2 * C::TILEB;
       unsigned char *vt = ring + (st * 2 + 1) * C::TILEB;
-      const uint32_t okw = sm.ok[warp][st];
-      float s[RT][4][2];
-      q4_scores<D, RT, SPLIT>(q, kt, s);
-      int kind;
-      const int k0 = first_key(rp, t, kShift, kind);
-      const bool clean = okw == 0xffffffffu;
-      const bool all = clean && k0 + kKeys - 1 <= near && (k0 >= far || k0 + kKeys <= p.sinks);
-      const uint4 vpar = *reinterpret_cast<const uint4 *>(vt + lane * F::REC + F::CODES);
-      uint32_t big = 0u;
-      if (clean || (okw >> lane & 1u)) {
-        big = __vmaxu2(vpar.x, vpar.y);
-        big = max(big & 0xffffu, big >> 16);
-      } else {  // what lies there may be anything: it counts as 0
-        *reinterpret_cast<uint4 *>(vt + lane * F::REC + F::CODES) = make_uint4(0u, 0u, 0u, 0u);
+      const int k0 = sm.what[warp][st].x;
+      const uint32_t okw = (uint32_t)sm.what[warp][st].y;
+      const unsigned char *krow = kt + lane * F::REC;
+      unsigned char *vrow = vt + lane * F::REC;
+
+      // ---- scores: keys 16 i + gq and 16 i + 8 + gq
+      Q4Scores<D, SPLIT> x[RT][2];
+      {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // (the two halves of the first operand's columns are the same parameters)
+          uint32_t par[4];
+          ldmatrix_x4(par[0], par[1], par[2], par[3], kt + (16 * i + (lane & 15)) * F::REC + F::CODES);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) x[r][i].least(par, q[r].sums);
+        }
+        float sc[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q4_four(kt + (8 * i + gq) * F::REC + F::CODES, sc[i]);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          uint32_t w[4];
+          ldmatrix_x4(w[0], w[1], w[2], w[3], krow + c * 16);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t u[2][4];
+            q4_unpack(w[2 * i], u[0]);
+            q4_unpack(w[2 * i + 1], u[1]);
+            const float(&two)[2][4] = reinterpret_cast<const float(&)[2][4]>(sc[2 * i]);
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+              x[r][i].chunk(c, u, two, [&](int g, int s) { return make_uint2(q[r].a[g][s][0], q[r].a[g][s][1]); },
+                            [&](int g, int s) { return make_uint2(q[r].b[SPLIT ? g : 0][s][0], q[r].b[SPLIT ? g : 0][s][1]); });
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) x[r][i].finish();
       }
-      if (!clean) {
-        fence_proxy_async_smem();  // (the next copy to this place comes after these stores)
-        __syncwarp();
-      }
-      // a scale's bits, so its exponent + 1 (fp16; subnormal ones are below 2^-14)
+
+      // ---- the largest scale of V: its bits give an exponent, every scale is below 2^high
+      const uint2 vsc = *reinterpret_cast<const uint2 *>(vrow + F::CODES);
+      uint32_t big = __vmaxu2(vsc.x, vsc.y);
+      big = max(big & 0xffffu, big >> 16);
       const int high = (int)(__reduce_max_sync(0xffffffffu, big) >> 10) - 14;
-      if (high > top) {
+      if (high > (SPLIT ? top : max(top, 1))) {
         const float f = pow2i(top - high);
         top = high;
 #pragma unroll
@@ -260,175 +315,211 @@ cache_q4_kernel(const __grid_constant__ Q4Params qp) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[r][c][e] *= f;
       }
-      const float vscale = pow2i(-top);
-      float f0[RT], f1[RT];  // what the rows 2 tq and 2 tq + 1 of the outputs are scaled by
+
+      // ---- weights, and their transpose: pw[r][n] has row gq, keys 8 n + 2 tq and + 1
+      const bool all = okw == 0xffffffffu && k0 + kKeys - 1 <= near && (k0 >= far || k0 + kKeys <= p.sinks);
+      if (!all) {
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const float f = q[r].down * p.scale_log2;
-        float mx = m[r];
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+          for (int n = 0; n < 4; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = s[r][n][e] * f;
-            if (!all) {
-              const int c = 8 * n + 2 * tq + e, j = k0 + c;
-              const bool see = (okw >> c & 1u) && j <= pos[r] && (j >= lo[r] || j < p.sinks);
-              x = see ? x : -INFINITY;
+            for (int e = 0; e < 2; ++e) {
+              const int c = 8 * n + gq, j = k0 + c;
+              const bool see = (okw >> c & 1u) && j <= pos[r][e] && (j > pos[r][e] - p.window || j < p.sinks);
+              float &s = x[r][n / 2].s[n % 2 * 2 + e];
+              s = see ? s : -INFINITY;
             }
-            s[r][n][e] = x;
-            mx = fmaxf(mx, x);
-          }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float ref = mx == -INFINITY ? 0.f : mx - 14.f;
-        const float down = mx == -INFINITY ? 0.f : fast_exp2(m[r] - mx);
-        m[r] = mx;
-        f0[r] = __shfl_sync(0xffffffffu, down, 8 * tq);
-        f1[r] = __shfl_sync(0xffffffffu, down, 8 * tq + 4);
-        l[r] *= down;
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            s[r][n][e] = fast_exp2(s[r][n][e] - ref);
-            l[r] += s[r][n][e];
-          }
       }
-      const unsigned char *vrow = vt + lane * F::REC;
-      uint32_t par[4];
-      ldmatrix_x4_trans(par[0], par[1], par[2], par[3], vrow + F::CODES);
+      uint32_t pw[RT][4], pw2[SPLIT ? RT : 1][4];
+      float down[RT][2];
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        float add[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          const uint32_t b0 = pack2<__half>(s[r][2 * kb][0], s[r][2 * kb][1]);
-          const uint32_t b1 = pack2<__half>(s[r][2 * kb + 1][0], s[r][2 * kb + 1][1]);
-          mma_16816<__half>(add, par[2 * kb], 0u, par[2 * kb + 1], 0u, b0, b1);
-          if constexpr (SPLIT) {
-            const float2 h0 = __half22float2(*reinterpret_cast<const __half2 *>(&b0));
-            const float2 h1 = __half22float2(*reinterpret_cast<const __half2 *>(&b1));
-            mma_16816<__half>(add, par[2 * kb], 0u, par[2 * kb + 1], 0u,
-                              pack2<__half>(s[r][2 * kb][0] - h0.x, s[r][2 * kb][1] - h0.y),
-                              pack2<__half>(s[r][2 * kb + 1][0] - h1.x, s[r][2 * kb + 1][1] - h1.y));
-          }
-        }
-        if constexpr (MIDDLE) {  // (the lanes of the least values take those of the scales)
-          const float x = __shfl_xor_sync(0xffffffffu, add[0], 16), y = __shfl_xor_sync(0xffffffffu, add[1], 16);
-          add[0] = fmaf(8.f, x, add[0]);
-          add[1] = fmaf(8.f, y, add[1]);
-        }
-        vmin[r][0] = fmaf(vmin[r][0], f0[r], add[0]);
-        vmin[r][1] = fmaf(vmin[r][1], f1[r], add[1]);
-      }
-      float sc[4][2][4];  // scales of the lane's keys
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
+        float ref[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          q4_four(vt + (8 * n + 2 * tq + e) * F::REC + F::CODES, sc[n][e]);
-#pragma unroll
-          for (int g = 0; g < 4; ++g) sc[n][e][g] *= vscale;
+          float mx = fmaxf(fmaxf(x[r][0].s[e], x[r][0].s[2 + e]), fmaxf(x[r][1].s[e], x[r][1].s[2 + e]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          mx = fmaxf(m[r][e], __fmul_rn(mx, scale[r][e]));
+          ref[e] = mx - 14.f;
+          down[r][e] = fast_exp2(m[r][e] - mx);
+          m[r][e] = mx;
+          l[r][e] *= down[r][e];
         }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          float *s = x[r][n / 2].s + n % 2 * 2;
+          // (rounded as the maximum was: of huge scores only equal ones cancel)
+          s[0] = fast_exp2(__fsub_rn(__fmul_rn(s[0], scale[r][0]), ref[0]));
+          s[1] = fast_exp2(__fsub_rn(__fmul_rn(s[1], scale[r][1]), ref[1]));
+          l[r][0] += s[0];
+          l[r][1] += s[1];
+          const uint32_t w = pack2<__half>(s[0], s[1]);
+          pw[r][n] = movmatrix_trans(w);
+          if constexpr (SPLIT) {
+            const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+            pw2[r][n] = movmatrix_trans(pack2<__half>(s[0] - hi.x, s[1] - hi.y));
+          }
+        }
+      }
+
+      // ---- outputs. The parameters of V: lane (g, tq) has the scales of group g of two
+      // keys, lane (4 + g, tq) their least values: keys 2 tq and + 1 behind 0, 16, 8 and
+      // 24. So both halves of the keys are in one operand, above and below (of each
+      // product one half of the rows is of no use).
+      uint32_t vpar[4];
+      ldmatrix_x4_trans(vpar[0], vpar[1], vpar[2], vpar[3],
+                        vt + ((lane & 7) | (lane & 8) << 1 | (lane & 16) >> 1) * F::REC + F::CODES);
+      {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          float add[4], behind[4];
+          mma_16816_first<__half>(add, vpar[0], vpar[1], vpar[2], vpar[3], pw[r][0], pw[r][1]);
+          mma_16816_first<__half>(behind, vpar[0], vpar[1], vpar[2], vpar[3], pw[r][2], pw[r][3]);
+          if constexpr (SPLIT) {
+            mma_16816<__half>(add, vpar[0], vpar[1], vpar[2], vpar[3], pw2[r][0], pw2[r][1]);
+            mma_16816<__half>(behind, vpar[0], vpar[1], vpar[2], vpar[3], pw2[r][2], pw2[r][3]);
+          }
+          add[0] += behind[2];
+          add[1] += behind[3];
+          if constexpr (MIDDLE) {  // (the lanes of the least values take those of the scales)
+            const float a = __shfl_xor_sync(0xffffffffu, add[0], 16), b = __shfl_xor_sync(0xffffffffu, add[1], 16);
+            add[0] = fmaf(8.f, a, add[0]);
+            add[1] = fmaf(8.f, b, add[1]);
+          }
+          vmin[r][0] = fmaf(vmin[r][0], down[r][0], add[0]);
+          vmin[r][1] = fmaf(vmin[r][1], down[r][1], add[1]);
+        }
+      }
+      uint32_t sc[4][4];  // scales of keys 8 n + 2 tq and + 1, by groups
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) sc[g][n] = __shfl_sync(0xffffffffu, vpar[(n & 1) << 1 | n >> 1], 4 * g + tq);
+      if (!SPLIT && top != 0) {
+        const __half2 f = __float2half2_rn(pow2i(-top));
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&sc[g][n]), f);
+            sc[g][n] = *reinterpret_cast<const uint32_t *>(&y);
+          }
+      }
+      const float unit = pow2i(-top);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         uint32_t w[4], u[4][4];
         ldmatrix_x4_trans(w[0], w[1], w[2], w[3], vrow + c * 16);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q4_unpack(w[i], u[i]);
+        for (int n = 0; n < 4; ++n) q4_unpack(w[n], u[n]);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          uint32_t b[4], b2[4];  // p times scale, of the chunk's group (of each half's: D = 64)
-          float from[4] = {0.f, 0.f, 0.f, 0.f};  // - 8 times their sums
+          uint32_t b[4], b2[4];  // weight times scale, of the chunk's group (of each half's: D = 64)
+          float from[4];         // - 8 times their sums
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int g = F::group_of(c, h);
             if (D == 64 || h == 0) {
 #pragma unroll
               for (int n = 0; n < 4; ++n) {
-                const float x = s[r][n][0] * sc[n][0][g], y = s[r][n][1] * sc[n][1][g];
-                b[n] = pack2<__half>(x, y);
+                const __half2 s2 = *reinterpret_cast<const __half2 *>(&sc[g][n]), p2 = *reinterpret_cast<const __half2 *>(&pw[r][n]);
                 if constexpr (SPLIT) {
-                  const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&b[n]));
-                  b2[n] = pack2<__half>(x - hi.x, y - hi.y);
+                  const float2 hi = __half22float2(p2), lo = __half22float2(*reinterpret_cast<const __half2 *>(&pw2[r][n]));
+                  const float2 sf = __half22float2(s2);
+                  const float y = (hi.x + lo.x) * (sf.x * unit), z = (hi.y + lo.y) * (sf.y * unit);
+                  b[n] = pack2<__half>(y, z);
+                  const float2 got = __half22float2(*reinterpret_cast<const __half2 *>(&b[n]));
+                  b2[n] = pack2<__half>(y - got.x, z - got.y);
+                } else {
+                  const __half2 y = __hmul2(p2, s2);
+                  b[n] = *reinterpret_cast<const uint32_t *>(&y);
                 }
               }
               if constexpr (MIDDLE) {
-                constexpr uint32_t low = 0x80088008u, high = 0x80808080u;  // -8 2^-24, -8 2^-20
-                from[0] = from[1] = from[2] = from[3] = 0.f;
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                  mma_16816<__half>(from, low, high, low, high, b[2 * kb], b[2 * kb + 1]);
-                  if constexpr (SPLIT) mma_16816<__half>(from, low, high, low, high, b2[2 * kb], b2[2 * kb + 1]);
+                constexpr uint32_t low = 0x80088008u, top8 = 0x80808080u;  // -8 2^-24, -8 2^-20
+                mma_16816_first<__half>(from, low, top8, low, top8, b[0], b[1]);
+                mma_16816<__half>(from, low, top8, low, top8, b[2], b[3]);
+                if constexpr (SPLIT) {
+                  mma_16816<__half>(from, low, top8, low, top8, b2[0], b2[1]);
+                  mma_16816<__half>(from, low, top8, low, top8, b2[2], b2[3]);
                 }
               }
             }
-            float add[4] = {from[0], from[1], from[2], from[3]};
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-              mma_16816<__half>(add, u[2 * kb][2 * h], u[2 * kb][2 * h + 1], u[2 * kb + 1][2 * h],
-                                u[2 * kb + 1][2 * h + 1], b[2 * kb], b[2 * kb + 1]);
-              if constexpr (SPLIT)
-                mma_16816<__half>(add, u[2 * kb][2 * h], u[2 * kb][2 * h + 1], u[2 * kb + 1][2 * h],
-                                  u[2 * kb + 1][2 * h + 1], b2[2 * kb], b2[2 * kb + 1]);
+            float add[4];
+            if constexpr (MIDDLE) {
+              add[0] = from[0]; add[1] = from[1]; add[2] = from[2]; add[3] = from[3];
+              mma_16816<__half>(add, u[0][2 * h], u[0][2 * h + 1], u[1][2 * h], u[1][2 * h + 1], b[0], b[1]);
+            } else {
+              mma_16816_first<__half>(add, u[0][2 * h], u[0][2 * h + 1], u[1][2 * h], u[1][2 * h + 1], b[0], b[1]);
             }
-            o[r][2 * c + h][0] = fmaf(o[r][2 * c + h][0], f0[r], add[0]);
-            o[r][2 * c + h][1] = fmaf(o[r][2 * c + h][1], f1[r], add[1]);
-            o[r][2 * c + h][2] = fmaf(o[r][2 * c + h][2], f0[r], add[2]);
-            o[r][2 * c + h][3] = fmaf(o[r][2 * c + h][3], f1[r], add[3]);
+            mma_16816<__half>(add, u[2][2 * h], u[2][2 * h + 1], u[3][2 * h], u[3][2 * h + 1], b[2], b[3]);
+            if constexpr (SPLIT) {
+              mma_16816<__half>(add, u[0][2 * h], u[0][2 * h + 1], u[1][2 * h], u[1][2 * h + 1], b2[0], b2[1]);
+              mma_16816<__half>(add, u[2][2 * h], u[2][2 * h + 1], u[3][2 * h], u[3][2 * h + 1], b2[2], b2[3]);
+            }
+            float(&to)[4] = o[r][2 * c + h];
+            to[0] = fmaf(to[0], down[r][0], add[0]);
+            to[1] = fmaf(to[1], down[r][1], add[1]);
+            to[2] = fmaf(to[2], down[r][0], add[2]);
+            to[3] = fmaf(to[3], down[r][1], add[3]);
           }
         }
       }
       __syncwarp();  // the stage has been read
+      st = st + 1 == STAGES ? 0 : st + 1;
     }
 
     // ---- join the warps: each adds its part to the CTA's result in turn
-    float f[RT];
+    float f[RT][2];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if (!ok) {
-        m[r] = -INFINITY;
-        l[r] = 0.f;
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], 4);
+        l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], 8);
+        l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], 16);
+        if (m[r][e] == kNothing) m[r][e] = -INFINITY;
+        if (gq == 0) {
+          sm.wm[warp][8 * r + 2 * tq + e] = m[r][e];
+          sm.wl[warp][8 * r + 2 * tq + e] = l[r][e];
+        }
       }
-      if (tq == 0) {
-        sm.wm[warp][8 * r + gq] = m[r];
-        sm.wl[warp][8 * r + gq] = l[r];
-      }
-    }
     __syncthreads();  // (and the result of an earlier piece has been read)
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      float mr = -INFINITY, lr = 0.f;
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) mr = fmaxf(mr, sm.wm[w][8 * r + gq]);
+      for (int e = 0; e < 2; ++e) {
+        const int row = 8 * r + 2 * tq + e;
+        float mr = -INFINITY, lr = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-        if (sm.wm[w][8 * r + gq] != -INFINITY) lr = fmaf(sm.wl[w][8 * r + gq], fast_exp2(sm.wm[w][8 * r + gq] - mr), lr);
-      f[r] = m[r] == -INFINITY ? 0.f : fast_exp2(m[r] - mr);
-      if (warp == 0 && tq == 0) sm.ml[8 * r + gq] = make_float2(mr - 14.f, lr);  // (-inf: nothing seen)
-    }
+        for (int w = 0; w < kWarps; ++w) mr = fmaxf(mr, sm.wm[w][row]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+          if (sm.wm[w][row] != -INFINITY) lr = fmaf(sm.wl[w][row], fast_exp2(sm.wm[w][row] - mr), lr);
+        f[r][e] = m[r][e] == -INFINITY ? 0.f : fast_exp2(m[r][e] - mr);
+        if (warp == 0 && gq == 0) sm.ml[row] = make_float2(mr - 14.f, lr);  // (-inf: nothing seen)
+      }
     for (int w = 0; w < kWarps; ++w) {
       if (warp == w && pc.t0 + w < pc.t1) {
+        const float up = pow2i(24) * pow2i(top);
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float fr = __shfl_sync(0xffffffffu, f[r], 8 * tq + 4 * e);
-            const float up = pow2i(24) * pow2i(top);
             float *res = sm.res + (8 * r + 2 * tq + e) * C::OP;
 #pragma unroll
             for (int c = 0; c < NC; ++c)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const float low = __shfl_sync(0xffffffffu, vmin[r][e], 16 + 4 * F::group_of(c, h) + tq);
-                const float x = fmaf(o[r][2 * c + h][e], up, low), y = fmaf(o[r][2 * c + h][2 + e], up * 0.0625f, low);
+                const float y = fmaf(o[r][2 * c + h][e], up, low), z = fmaf(o[r][2 * c + h][2 + e], up * 0.0625f, low);
                 float2 *at = reinterpret_cast<float2 *>(res + F::out_feature(c, h, gq));
                 float2 v = w ? *at : make_float2(0.f, 0.f);
-                v.x += fr == 0.f ? 0.f : x * fr;
-                v.y += fr == 0.f ? 0.f : y * fr;
+                v.x += f[r][e] == 0.f ? 0.f : y * f[r][e];
+                v.y += f[r][e] == 0.f ? 0.f : z * f[r][e];
                 *at = v;
               }
           }
@@ -445,8 +536,6 @@ cache_q4_kernel(const __grid_constant__ Q4Params qp) {
       }
     }
   }
-  // no copy may be in flight when the CTA exits, even if a wait gave up
-  for (; used < put; ++used) mbar_wait(full + used % STAGES, (used / STAGES) & 1, p.err);
   if (S) join_cluster<T, D, ROWS, C::OP, kThreads>(p, pieces, sm.ml, sm.res);
 }
 
@@ -504,8 +593,15 @@ mgqa_status launch_attn_q4(const mgqa_args &a, const mgqa_pages *pages, int32_t 
   cache_attn_params(a, pages, nullptr, window, sinks, p);
   const CacheAttnLaunch how{ws, device_sm_count()};
   if (how.sms < 1) return fail(MGQA_ERR_CUDA, "cannot read the SM count of the current device");
-  const int64_t rec = a.D / 2 + 16;
-  qp.run_slots = p.ks[2] == rec && p.vs[2] == rec ? (p.table ? p.page_size : p.cap) : 1;
+  for (int t = 0; t < 2; ++t) {
+    const int64_t ks = p.ks[2 * t] / 16, vs = p.vs[2 * t] / 16;
+    if (ks > 0xffffffffll || vs > 0xffffffffll) return fail(MGQA_ERR_UNSUPPORTED, "strides of records past 2^36 bytes");
+    qp.kstep[t] = (uint32_t)ks;
+    qp.vstep[t] = (uint32_t)vs;
+  }
+  const uint32_t rec = (uint32_t)(a.D / 2 + 16) / 16;
+  qp.halves = qp.kstep[1] == rec && qp.vstep[1] == rec && qp.kstep[0] == qp.vstep[0] && (!pages || pages->page_size % 16 == 0);
+  qp.alike = qp.kstep[0] == qp.vstep[0] && qp.kstep[1] == qp.vstep[1];
   if (a.dtype == MGQA_BF16)
     return a.D == 64 ? launch_d<__nv_bfloat16, 64>(qp, a.dtype, how, s) : launch_d<__nv_bfloat16, 128>(qp, a.dtype, how, s);
   if (a.dtype == MGQA_FP16)

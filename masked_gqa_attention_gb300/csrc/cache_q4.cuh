@@ -67,7 +67,7 @@ struct Q4Row {
   float down;  // 2^-k
 
   template <typename T>
-  MGQA_DEV void load(const T *row, int tq) {  // null: zeros. (The four lanes of a quad together.)
+  MGQA_DEV void load(const T *row, int tq, bool negate = false) {  // null: zeros. (The four lanes of a quad together.)
     constexpr int N = Q4<D>::GW / 4;  // features of a group
     float x[4][N];
     float top = 0.f;
@@ -101,7 +101,7 @@ struct Q4Row {
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const int e = (int)(__float_as_uint(top) >> 23) - 127;  // (0: -127)
     const int k = min(9 - e, 120);
-    const float up = pow2i(k);
+    const float up = negate ? -pow2i(k) : pow2i(k);
     down = pow2i(-k);
     float sum[4];
 #pragma unroll
@@ -146,80 +146,41 @@ MGQA_DEV void q4_four(const unsigned char *p, float (&f)[4]) {
   f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
 }
 
-// Scores of 8 RT query rows (RT = 1: rows gq of a warp; else gq and gq + 8, ...)
-// with 32 keys, whose records lie at `tile` in shared memory: s[r][n][e], row group
-// r, key 8 n + 2 tq + e, unscaled (q 2^k's: times `down`).
-template <int D, int RT, bool SPLIT>
-MGQA_DEV void q4_scores(const Q4Row<D, SPLIT> (&q)[RT], const unsigned char *tile, float (&s)[RT][4][2]) {
-  using F = Q4<D>;
-  const int lane = threadIdx.x & 31, tq = lane & 3;
-  const unsigned char *mine = tile + lane * F::REC;  // ldmatrix: lane = key
-  uint32_t par[4];
-  ldmatrix_x4(par[0], par[1], par[2], par[3], mine + F::CODES);
-  float sc[4][2][4];  // scales of the lane's keys
+// Scores of 16 keys with 8 query rows, unscaled (times the row's `down`): s[0], s[1]
+// are key gq with rows 2 tq and 2 tq + 1, s[2], s[3] key gq + 8. least: the keys'
+// parameters (word tq of each); u: their codes of chunk c, unpacked; sc: their scales.
+// A piece at a time, so that unpacked codes serve several groups of rows.
+template <int D, bool SPLIT>
+struct Q4Scores {
+  float s[4], acc[4];
+
+  MGQA_DEV void least(const uint32_t (&p)[4], const uint32_t (&sums)[2]) {  // p: keys gq, gq + 8, and both again
+    mma_16816_first<__half>(s, p[0], p[1], p[2], p[3], sums[0], sums[1]);
+  }
+  // q(g, i): both operand registers of product i of group g; q2: their second terms
+  template <typename Q, typename Q2>
+  MGQA_DEV void chunk(int c, const uint32_t (&u)[2][4], const float (&sc)[2][4], Q q, Q2 q2) {
+    float part[4];
 #pragma unroll
-  for (int n = 0; n < 4; ++n)
+    for (int h = 0; h < 2; ++h) {
+      const int g = Q4<D>::group_of(c, h), i = D == 128 ? h : 0;
+      const uint2 b = q(g, i);
+      if (D == 64 || h == 0) mma_16816_first<__half>(part, u[0][2 * h], u[1][2 * h], u[0][2 * h + 1], u[1][2 * h + 1], b.x, b.y);
+      else mma_16816<__half>(part, u[0][2 * h], u[1][2 * h], u[0][2 * h + 1], u[1][2 * h + 1], b.x, b.y);
+      if constexpr (SPLIT) {
+        const uint2 b2 = q2(g, i);
+        mma_16816<__half>(part, u[0][2 * h], u[1][2 * h], u[0][2 * h + 1], u[1][2 * h + 1], b2.x, b2.y);
+      }
+      if (D == 64 || h == 1) {  // the group is complete
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      q4_four(tile + (8 * n + 2 * tq + e) * F::REC + F::CODES, sc[n][e]);
-    }
-  constexpr int MT = (RT + 1) / 2;
-  float least[MT][4][4];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      float(&c)[4] = least[m][n];
-      c[0] = c[1] = c[2] = c[3] = 0.f;
-      constexpr bool two = RT > 1;
-      const int r1 = two ? 2 * m + 1 : 0;
-      mma_16816<__half>(c, q[2 * m].sums[0], two ? q[r1].sums[0] : 0u, q[2 * m].sums[1], two ? q[r1].sums[1] : 0u,
-                        par[n], par[n]);
-    }
-  float acc[RT][4][2];
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int n = 0; n < 4; ++n) acc[r][n][0] = acc[r][n][1] = 0.f;
-#pragma unroll
-  for (int c = 0; c < F::CHUNKS; ++c) {
-    uint32_t w[4];
-    ldmatrix_x4(w[0], w[1], w[2], w[3], mine + c * 16);
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      uint32_t u[4];
-      q4_unpack(w[n], u);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        constexpr bool two = RT > 1;
-        const int r0 = 2 * m, r1 = two ? 2 * m + 1 : 0;
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int g = F::group_of(c, h), st = D == 128 ? h : 0;
-          mma_16816<__half>(part, q[r0].a[g][st][0], two ? q[r1].a[g][st][0] : 0u, q[r0].a[g][st][1],
-                            two ? q[r1].a[g][st][1] : 0u, u[2 * h], u[2 * h + 1]);
-          if constexpr (SPLIT)
-            mma_16816<__half>(part, q[r0].b[g][st][0], two ? q[r1].b[g][st][0] : 0u, q[r0].b[g][st][1],
-                              two ? q[r1].b[g][st][1] : 0u, u[2 * h], u[2 * h + 1]);
-          if (D == 64 || h == 1) {  // the group is complete
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              acc[r0][n][e] = fmaf(part[e], sc[n][e][g], acc[r0][n][e]);
-              if (two) acc[r1][n][e] = fmaf(part[2 + e], sc[n][e][g], acc[r1][n][e]);
-            }
-            part[0] = part[1] = part[2] = part[3] = 0.f;
-          }
-        }
+        for (int e = 0; e < 4; ++e) acc[e] = g == 0 ? part[e] * sc[e / 2][g] : fmaf(part[e], sc[e / 2][g], acc[e]);
       }
     }
   }
+  MGQA_DEV void finish() {
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) s[r][n][e] = fmaf(acc[r][n][e], 16777216.f, least[r / 2][n][(r & 1) * 2 + e]);
-}
+    for (int e = 0; e < 4; ++e) s[e] = fmaf(acc[e], 16777216.f, s[e]);
+  }
+};
 
 }  // namespace mgqa

@@ -64,11 +64,11 @@ struct Keys {
   }
   // s: key gq, rows 2 tq and 2 tq + 1; key gq + 8
   MGQA_DEV void scores(const unsigned char *staged, int lane, float (&s)[4]) const {
-    s[0] = s[1] = s[2] = s[3] = 0.f;
 #pragma unroll
     for (int c = 0; c < N; ++c) {
       const uint4 q = reinterpret_cast<const uint4 *>(staged)[c * 32 + lane];
-      mma_16816<T>(s, k[0][c].x, k[1][c].x, k[0][c].y, k[1][c].y, q.x, q.y);
+      if (c == 0) mma_16816_first<T>(s, k[0][c].x, k[1][c].x, k[0][c].y, k[1][c].y, q.x, q.y);
+      else mma_16816<T>(s, k[0][c].x, k[1][c].x, k[0][c].y, k[1][c].y, q.x, q.y);
       mma_16816<T>(s, k[0][c].z, k[1][c].z, k[0][c].w, k[1][c].w, q.z, q.w);
     }
   }
@@ -171,40 +171,29 @@ struct Q4Keys {
   static MGQA_DEV uint32_t word(const uint4 &p, int tq) { return tq < 2 ? (tq ? p.y : p.x) : (tq == 2 ? p.z : p.w); }
   MGQA_DEV void scores(const unsigned char *staged, int lane, float (&s)[4]) const {
     const uint32_t *w = reinterpret_cast<const uint32_t *>(staged);
-    const uint2 sums = *reinterpret_cast<const uint2 *>(w + (STAGED / 4 - 64) + 2 * lane);
-    const uint32_t p0 = word(par[0], lane & 3), p1 = word(par[1], lane & 3);
-    s[0] = s[1] = s[2] = s[3] = 0.f;
-    mma_16816<__half>(s, p0, p1, p0, p1, sums.x, sums.y);
+    const uint2 q = *reinterpret_cast<const uint2 *>(w + (STAGED / 4 - 64) + 2 * lane);
+    const uint32_t sums[2] = {q.x, q.y};
     float sc[2][4];
     scales(par[0], sc[0]);
     scales(par[1], sc[1]);
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    Q4Scores<D, SPLIT> x;
+    const uint32_t p0 = word(par[0], lane & 3), p1 = word(par[1], lane & 3), both[4] = {p0, p1, p0, p1};
+    x.least(both, sums);
+    const auto term = [&](int t) {
+      return [=](int g, int i) {
+        return *reinterpret_cast<const uint2 *>(w + t * WORDS * 32 + (g * F::KS + i) * 64 + 2 * lane);
+      };
+    };
 #pragma unroll
     for (int c = 0; c < N; ++c) {
       uint32_t u[2][4];
       q4_unpack(k[0][c], u[0]);
       q4_unpack(k[1][c], u[1]);
-      float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int g = F::group_of(c, h), at = (g * F::KS + (D == 128 ? h : 0)) * 64 + 2 * lane;
-        const uint2 q = *reinterpret_cast<const uint2 *>(w + at);
-        mma_16816<__half>(part, u[0][2 * h], u[1][2 * h], u[0][2 * h + 1], u[1][2 * h + 1], q.x, q.y);
-        if constexpr (SPLIT) {
-          const uint2 r = *reinterpret_cast<const uint2 *>(w + WORDS * 32 + at);
-          mma_16816<__half>(part, u[0][2 * h], u[1][2 * h], u[0][2 * h + 1], u[1][2 * h + 1], r.x, r.y);
-        }
-        if (D == 64 || h == 1) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            acc[e] = fmaf(part[e], sc[e / 2][g], acc[e]);
-            part[e] = 0.f;
-          }
-        }
-      }
+      x.chunk(c, u, sc, term(0), term(1));
     }
+    x.finish();
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] = fmaf(acc[e], 16777216.f, s[e]);
+    for (int e = 0; e < 4; ++e) s[e] = x.s[e];
   }
 };
 
