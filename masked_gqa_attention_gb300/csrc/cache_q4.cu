@@ -33,8 +33,8 @@
 #include <algorithm>
 #include <cmath>
 
-#include "cache_producer.cuh"
 #include "cache_q4.cuh"
+#include "cache_stream.cuh"
 
 namespace mgqa {
 namespace {
@@ -43,121 +43,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kShift = 5, kKeys = 32;  // keys of a tile
 constexpr float kNothing = -3.4028235e38f;  // the maximum of a row that has seen nothing (no score is below it)
-constexpr int kMostCtas = 512;         // partial results: two per CTA
-
-struct Q4Params {
-  TmaParams t;  // (its strides of k and v are bytes)
-  uint32_t kstep[2], vstep[2];  // from page to page and from slot to slot, in 16-byte pieces
-  int32_t alike;                // they agree
-  int32_t halves;               // the slots of half a tile lie one after the other
-};
-
-// The tiles of a warp, in order, ahead of their use: every kWarps-th of each piece.
-// What stays the same in a piece is in shared memory, one per warp (in registers it
-// took as many as the outputs).
-struct alignas(16) Feed {
-  int ns, past, np, n;      // first slot of tile t < np: (t < ns ? t : t + past) * kKeys
-  int lo, s_end;            // slots between s_end and lo are hidden
-  const int32_t *table;     // of the request; null: static
-  const char *k, *v;        // of the KV head (and, static, of the request)
-  Pieces pieces;
-};
-struct Ahead {
-  Feed &f;
-  int t, end;              // next tile, end of its piece
-  int k0, page, slot;      // its first slot; where the lane's row is
-  bool want, live;         // the row is wanted; there is a tile
-
-  MGQA_DEV void settle(const Q4Params &p, int warp, int lane) {  // to the next tile that there is
-    const CacheAttnParams &c = p.t.a;
-    while (live && t >= end) {
-      Pieces all = f.pieces;
-      Piece pc;
-      live = all.next(c, pc);
-      __syncwarp();
-      if (lane == 0) {
-        f.pieces = all;
-        f.ns = pc.rp.ns;
-        f.past = pc.rp.mt0 - pc.rp.ns;
-        f.np = pc.rp.np;
-        f.n = pc.rp.n;
-        f.lo = pc.rp.lo;
-        f.s_end = pc.rp.s_end;
-        f.table = c.table ? c.table + (int64_t)pc.b * c.table_stride : nullptr;
-        f.k = static_cast<const char *>(c.k) + pc.g * c.ks[1] + (c.table ? 0 : pc.b * c.ks[0]);
-        f.v = static_cast<const char *>(c.v) + pc.g * c.vs[1] + (c.table ? 0 : pc.b * c.vs[0]);
-      }
-      __syncwarp();
-      t = pc.t0 + warp;
-      end = pc.t1;
-    }
-    if (live) {
-      const int4 x = *reinterpret_cast<const int4 *>(&f.ns);
-      const int2 y = *reinterpret_cast<const int2 *>(&f.lo);
-      k0 = (t < x.x ? t : t + x.y) * kKeys;
-      const int j = k0 + lane;
-      page = slot = 0;
-      want = t < x.z && j < x.w && (j >= y.x || j < y.y);
-      if (want) {
-        slot = j;
-        if (f.table) {
-          const int i = c.page_shift >= 0 ? j >> c.page_shift : j / c.page_size;
-          slot = j - i * c.page_size;
-          page = __ldg(f.table + i);  // (looked at by the next issue: here its latency would show)
-        }
-      }
-    }
-  }
-  MGQA_DEV void start(const Q4Params &p, const Pieces &all, int warp, int lane) {
-    if (lane == 0) f.pieces = all;
-    __syncwarp();
-    live = true;
-    t = end = 0;
-    settle(p, warp, lane);
-  }
-  // Starts the copies of the tile that was looked up (zeros for the rows that do not
-  // count), and looks the next one up. Consecutive lanes copy consecutive 16-byte
-  // pieces; a lane knows where its row is.
-  template <int D>
-  MGQA_DEV void issue(const Q4Params &p, int warp, int lane, unsigned char *dst, int2 *what) {
-    constexpr int P = Q4<D>::REC / 16;  // pieces of a record, and copies of a lane
-    const bool there = !p.t.a.table || (unsigned)page < (unsigned)p.t.a.num_pages;
-    if (want && !there) report_error(p.t.a.err, MGQA_ERR_INVALID_ARG);
-    const uint32_t ok = __ballot_sync(0xffffffffu, want && there);
-    if (lane == 0) *what = make_int2(k0, (int)ok);
-    const uint32_t pg = there ? (uint32_t)page : 0u, sl = (uint32_t)slot;
-    const uint64_t at = (uint64_t)pg * p.kstep[0] + (uint64_t)sl * p.kstep[1];  // in pieces
-    const uint64_t av = p.alike ? at : (uint64_t)pg * p.vstep[0] + (uint64_t)sl * p.vstep[1];
-    const char *k = f.k, *v = f.v;
-    if (p.halves && ok == 0xffffffffu) {  // two runs of 16 rows
-      constexpr int kRun = 16 * Q4<D>::REC;  // (a lane's piece of the one or the other)
-      const uint64_t a = __shfl_sync(0xffffffffu, at, 0), b = __shfl_sync(0xffffffffu, at, 16);
-      const char *ka = k + a * 16 + lane * 16, *kb = k + b * 16 + lane * 16 - kRun;
-      const char *va = v + a * 16 + lane * 16, *vb = v + b * 16 + lane * 16 - kRun;
-      dst += lane * 16;
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const bool second = 512 * i >= kRun || (512 * i + 512 > kRun && 512 * i + lane * 16 >= kRun);
-        cp_async16(dst + 512 * i, (second ? kb : ka) + 512 * i);
-        cp_async16(dst + kKeys * Q4<D>::REC + 512 * i, (second ? vb : va) + 512 * i);
-      }
-      t += kWarps;
-      settle(p, warp, lane);
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int row = (lane + 32 * i) / P, piece = (lane + 32 * i) % P;
-      const uint64_t to = __shfl_sync(0xffffffffu, at, row) + piece;
-      const uint64_t tv = p.alike ? to : __shfl_sync(0xffffffffu, av, row) + piece;
-      const bool take = ok >> row & 1u;
-      cp_async16_or_zero(dst + (lane + 32 * i) * 16, k + to * 16, take);
-      cp_async16_or_zero(dst + kKeys * Q4<D>::REC + (lane + 32 * i) * 16, v + tv * 16, take);
-    }
-    t += kWarps;
-    settle(p, warp, lane);
-  }
-};
+constexpr int kMostCtas = 512;  // partial results: two per CTA
 
 template <int D, int RT>
 struct Cfg {
@@ -180,7 +66,7 @@ struct Cfg {
 
 template <typename T, int D, int RT>
 __global__ void __launch_bounds__(kThreads, (Cfg<D, RT>::CTAS))
-cache_q4_kernel(const __grid_constant__ Q4Params qp) {
+cache_q4_kernel(const __grid_constant__ StreamParams qp) {
   using C = Cfg<D, RT>;
   using F = Q4<D>;
   constexpr bool SPLIT = sizeof(T) == 4;
@@ -200,12 +86,12 @@ cache_q4_kernel(const __grid_constant__ Q4Params qp) {
   const bool teller = tid == 0 && !S;
   if (teller) tell_cut(p, blockIdx.x, nullptr);
 
-  Ahead ahead{sm.feed[warp], 0, 0, 0, 0, 0, false, false};
+  Stream<kKeys, F::REC / 16, false, true, kWarps> ahead(sm.feed[warp], 1);
   ahead.start(qp, pieces, warp, lane);
   int put = 0, st = 0;  // stages: filled next, used next
   const auto start_one = [&] {
     if (ahead.live) {
-      ahead.template issue<D>(qp, warp, lane, ring + put * 2 * C::TILEB, sm.what[warp] + put);
+      ahead.issue(qp, warp, lane, ring + put * 2 * C::TILEB, sm.what[warp] + put);
       put = put + 1 == STAGES ? 0 : put + 1;
     }
     cp_async_commit();
@@ -540,7 +426,7 @@ cache_q4_kernel(const __grid_constant__ Q4Params qp) {
 }
 
 template <typename T, int D, int RT>
-mgqa_status launch_t(Q4Params qp, mgqa_dtype dt, const CacheAttnLaunch &how, cudaStream_t s) {
+mgqa_status launch_t(StreamParams qp, mgqa_dtype dt, const CacheAttnLaunch &how, cudaStream_t s) {
   using C = Cfg<D, RT>;
   auto kern = cache_q4_kernel<T, D, RT>;
   static std::atomic<uint64_t> attr{0};
@@ -574,7 +460,7 @@ mgqa_status launch_t(Q4Params qp, mgqa_dtype dt, const CacheAttnLaunch &how, cud
 }
 
 template <typename T, int D>
-mgqa_status launch_d(const Q4Params &qp, mgqa_dtype dt, const CacheAttnLaunch &how, cudaStream_t s) {
+mgqa_status launch_d(const StreamParams &qp, mgqa_dtype dt, const CacheAttnLaunch &how, cudaStream_t s) {
   if (qp.t.a.R <= 8) return launch_t<T, D, 1>(qp, dt, how, s);
   return launch_t<T, D, 2>(qp, dt, how, s);
 }
@@ -588,20 +474,13 @@ static_assert(kMostCtas * 16 + (size_t)2 * kMostCtas * 32 * (128 + 2) * 4 <=
 
 mgqa_status launch_attn_q4(const mgqa_args &a, const mgqa_pages *pages, int32_t window, int32_t sinks, void *ws,
                            cudaStream_t s) {
-  Q4Params qp{};
+  StreamParams qp{};
   CacheAttnParams &p = qp.t.a;
   cache_attn_params(a, pages, nullptr, window, sinks, p);
   const CacheAttnLaunch how{ws, device_sm_count()};
   if (how.sms < 1) return fail(MGQA_ERR_CUDA, "cannot read the SM count of the current device");
-  for (int t = 0; t < 2; ++t) {
-    const int64_t ks = p.ks[2 * t] / 16, vs = p.vs[2 * t] / 16;
-    if (ks > 0xffffffffll || vs > 0xffffffffll) return fail(MGQA_ERR_UNSUPPORTED, "strides of records past 2^36 bytes");
-    qp.kstep[t] = (uint32_t)ks;
-    qp.vstep[t] = (uint32_t)vs;
-  }
-  const uint32_t rec = (uint32_t)(a.D / 2 + 16) / 16;
-  qp.halves = qp.kstep[1] == rec && qp.vstep[1] == rec && qp.kstep[0] == qp.vstep[0] && (!pages || pages->page_size % 16 == 0);
-  qp.alike = qp.kstep[0] == qp.vstep[0] && qp.kstep[1] == qp.vstep[1];
+  if (!set_steps(qp, p.ks, p.vs, a.D / 2 + 16, pages ? pages->page_size : 0))
+    return fail(MGQA_ERR_UNSUPPORTED, "strides of records past 2^36 bytes");
   if (a.dtype == MGQA_BF16)
     return a.D == 64 ? launch_d<__nv_bfloat16, 64>(qp, a.dtype, how, s) : launch_d<__nv_bfloat16, 128>(qp, a.dtype, how, s);
   if (a.dtype == MGQA_FP16)
