@@ -4,10 +4,12 @@
 // (of equal ones the first; a NaN is less than any number), in their order, in slots
 // 0 .. budget - 1; the weights move along, and those of the slots given up become 0.
 //
-//   select -- a block per (layer, request, KV head): the smallest weight that stays,
-//             by three passes over the weights as ordered integers (11, 11 and 10
-//             bits, counted in shared memory), then one pass that writes the kept
-//             slots, in order, to the workspace and the weights to their new places.
+//   select -- a cluster of 1 to 8 blocks per (layer, request, KV head), each with a
+//             part of its weights in shared memory: the smallest weight that stays, by
+//             up to three passes over the weights as ordered integers (11, 11 and 10
+//             bits, counted per block and summed over the cluster), done when every
+//             weight left stays; then the kept slots, in order, to the workspace and
+//             the weights to their new places.
 //   move   -- the rows, in place. Every row moves towards the front, so rounds of
 //             consecutive rows, each read as a whole before any of it is written,
 //             overwrite nothing that a later round reads. A cluster of up to 16
@@ -25,13 +27,15 @@
 namespace mgqa {
 namespace {
 
-constexpr int kSelectThreads = 1024;
+constexpr int kSelectThreads = 512;
+constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kPart = 40960;  // weights that a block holds
 
 struct EvictParams {
   char *k, *v;
   int64_t ks[4], vs[4];  // layer, page, head, slot strides in bytes
-  int32_t layers, num_pages, Hkv, page_size, pieces, rows, max_pages;
+  int32_t layers, num_pages, Hkv, page_size, page_shift, pieces, rows, max_pages;
   int32_t *table;
   int64_t table_stride;
   const int32_t *kv_len;
@@ -43,7 +47,9 @@ struct EvictParams {
   int32_t budget, sinks, recent;
   int32_t *plan;   // [rows]: 1: the request is cut to the budget
   int32_t *kept;   // [layers][rows][Hkv][budget] slots that stay
-  int32_t cluster;
+  int32_t parts;   // blocks of a selection
+  int32_t cluster; // blocks of a move
+  int32_t round_rows, piece_shift;  // rows of a block's round; of a power of two of pieces, else -1
 };
 
 // A weight as an integer of the same order (NaN lowest, one zero).
@@ -54,8 +60,17 @@ MGQA_DEV uint32_t ordered(float x) {
   return u >> 31 ? ~u : u | 0x80000000u;
 }
 
-// Exclusive prefix sum over the block; *total receives the sum. scratch: 33 ints.
-MGQA_DEV int block_scan(int x, int *scratch, int *total) {
+struct alignas(16) Select {
+  int bins[kBins];
+  int scan[kSelectWarps + 1];
+  int2 count[kSelectWarps];  // slots that stay for sure, and those equal to the cut, of a warp's part
+  int2 all;                  // of the block, read by its cluster
+  uint32_t digit;
+  int left, within;
+};
+
+// Exclusive prefix sum over the block's threads.
+MGQA_DEV int block_scan(int x, int *scan) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int inc = x;
 #pragma unroll
@@ -63,136 +78,214 @@ MGQA_DEV int block_scan(int x, int *scratch, int *total) {
     const int up = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += up;
   }
-  if (lane == 31) scratch[warp] = inc;
+  if (lane == 31) scan[warp] = inc;
   __syncthreads();
-  if (warp == 0) {
-    const int w = scratch[lane];
-    int wi = w;
+  int before = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, wi, o);
-      if (lane >= o) wi += up;
-    }
-    scratch[lane] = wi - w;
-    if (lane == 31) scratch[32] = wi;
-  }
-  __syncthreads();
-  const int r = scratch[warp] + inc - x;
-  *total = scratch[32];
-  __syncthreads();
-  return r;
+  for (int w = 0; w < kSelectWarps; ++w) before += w < warp ? scan[w] : 0;
+  return before + inc - x;
 }
 
 __global__ void __launch_bounds__(kSelectThreads)
 evict_select_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ int bins[kBins];
-  __shared__ int scratch[33];
-  __shared__ uint32_t s_digit;
-  __shared__ int s_left;
-  const int tid = threadIdx.x;
-  const int g = blockIdx.x % p.Hkv, b = blockIdx.x / p.Hkv % p.rows, layer = blockIdx.x / p.Hkv / p.rows;
+  extern __shared__ __align__(16) float held[];  // the block's weights
+  __shared__ Select sm;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, C = p.parts;
+  const int unit = blockIdx.x / C, rank = blockIdx.x % C;
+  const int g = unit % p.Hkv, b = unit / p.Hkv % p.rows, layer = unit / p.Hkv / p.rows;
+  for (int i = tid; i < kBins; i += kSelectThreads) sm.bins[i] = 0;
   grid_dependency_wait();
   allow_dependents();
   const int n = __ldcg(p.kv_len + b);
-  const bool first = layer == 0 && g == 0;
-  bool bad = n < 0 || n > p.slots;
-  if (!bad && n > p.budget && p.table) {  // every page that is read is there, and none that is written is shared
+  const bool first = layer == 0 && g == 0 && rank == 0;
+  const bool wrong_n = n < 0 || n > p.slots;
+  int wrong = 0;
+  if (!wrong_n && n > p.budget && p.table) {  // every page that is read is there, and none that is written is shared
     const int np = (n + p.page_size - 1) / p.page_size, wp = (p.budget + p.page_size - 1) / p.page_size;
-    int wrong = 0;
+#pragma unroll 4
     for (int i = tid; i < np; i += kSelectThreads) {
       const int e = __ldcg(p.table + (int64_t)b * p.table_stride + i);
       if ((unsigned)e >= (unsigned)p.num_pages || (p.ref && i < wp && __ldcg(p.ref + e) > 1)) wrong = 1;
     }
-    bad = __syncthreads_or(wrong) != 0;
   }
-  const bool over = !bad && n > p.budget;
+  const float *w = p.w + layer * p.wi[0] + b * p.wi[1] + g * p.wi[2];
+  float *out = p.w_out + layer * p.wo[0] + b * p.wo[1] + g * p.wo[2];
+  // a block's part of the slots: whole steps of its warps (beyond what the blocks hold
+  // together, the weights are read again for every use, by one block)
+  const bool holds = n <= C * kPart;
+  if (!holds && rank > 0 && !wrong_n) return;  // (the whole cluster but one, which then uses no cluster barrier)
+  const int parts = holds ? C : 1;
+  const int part = holds ? (n + C * 32 - 1) / (C * 32) * 32 : n, j0 = rank * part, len = min(part, n - j0);
+  const bool want = !wrong_n && n > p.budget;
+  if (want && holds) {
+    int i = tid;
+    for (; i + 7 * kSelectThreads < len; i += 8 * kSelectThreads) {
+      float x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x[u] = __ldcg(w + j0 + i + u * kSelectThreads);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) held[i + u * kSelectThreads] = x[u];
+    }
+#pragma unroll 4
+    for (; i < len; i += kSelectThreads) held[i] = __ldcg(w + j0 + i);
+  }
+  const bool bad = __syncthreads_or(wrong) != 0 || wrong_n;
+  const bool over = !bad && want;
   if (first && tid == 0) {
     p.plan[b] = over;
     if (bad) report_error(p.err, MGQA_ERR_INVALID_ARG);
   }
-  const float *w = p.w + layer * p.wi[0] + b * p.wi[1] + g * p.wi[2];
-  float *out = p.w_out + layer * p.wo[0] + b * p.wo[1] + g * p.wo[2];
   if (!over) {
     if (out != w && !bad)
-      for (int j = tid; j < n; j += kSelectThreads) out[j] = __ldcg(w + j);
+      for (int j = rank * kSelectThreads + tid; j < n; j += parts * kSelectThreads) out[j] = __ldcg(w + j);
     return;
   }
+  const auto weight = [&](int i) { return holds ? held[i] : __ldcg(w + i); };  // of slot j0 + i
+
   // ---- the weight of rank `left` among slots [from, to)
   const int from = p.sinks, to = n - p.recent;
   int left = p.budget - p.sinks - p.recent;  // how many of them stay
-  uint32_t cut = 0xffffffffu;                // everything above it stays, and `left` of those equal to it
+  uint32_t cut = 0xffffffffu;                // everything above it stays, and `left` of those equal to it,
+  int same = 0;                              // compared from this bit on
   if (left > 0) {
     cut = 0u;
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
       const int high = shift + width;
-      for (int i = tid; i < kBins; i += kSelectThreads) bins[i] = 0;
-      __syncthreads();
-      for (int j = from + tid; j < to; j += kSelectThreads) {
-        const uint32_t u = ordered(__ldcg(w + j));
-        if (pass == 0 || u >> high == cut >> high) atomicAdd(&bins[u >> shift & ((1u << width) - 1u)], 1);
+      const int a = max(0, from - j0), z = min(len, to - j0);
+#pragma unroll 4
+      for (int i = a + tid; i < z; i += kSelectThreads) {
+        const uint32_t u = ordered(weight(i));
+        if (pass == 0 || u >> high == cut >> high) atomicAdd(&sm.bins[u >> shift & ((1u << width) - 1u)], 1);
       }
-      __syncthreads();
-      // bins from the top: thread t has bins 2047 - 2 t and 2046 - 2 t
-      const int hi = bins[kBins - 1 - 2 * tid], lo = bins[kBins - 2 - 2 * tid];
-      int total;
-      const int above = block_scan(hi + lo, scratch, &total);
-      if (above < left && above + hi + lo >= left) {
-        const bool top = above + hi >= left;
-        s_digit = (uint32_t)(kBins - (top ? 1 : 2) - 2 * tid);
-        s_left = left - above - (top ? 0 : hi);
-      }
-      __syncthreads();
-      cut |= s_digit << shift;
-      left = s_left;
-      __syncthreads();
-    }
-  }
-  // ---- the kept slots in order, and their weights
-  int32_t *kept = p.kept + (int64_t)blockIdx.x * p.budget;
-  int sure = 0, equal = 0;  // kept for sure, and equal to the cut, ahead of this round
-  for (int j0 = 0; j0 < n; j0 += 4 * kSelectThreads) {
-    float x[4];
-    int mine = 0;
-    uint32_t what = 0u;  // 2 bits a slot: 1 kept, 2 equal
+      if (parts > 1) cluster_sync();
+      else __syncthreads();
+      // bins from the top: thread t has bins 2047 - 4 t and the three below
+      const int top = kBins - 4 - 4 * tid;
+      int4 c = *reinterpret_cast<const int4 *>(sm.bins + top);
+      if (parts > 1) {
+        float4 f[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int j = j0 + 4 * tid + i;
-      if (j < n) {
-        x[i] = __ldcg(w + j);
-        const uint32_t u = ordered(x[i]);
-        const bool keep = j < from || j >= to || (left > 0 && u > cut);
-        const bool same = !keep && left > 0 && u == cut;
-        mine += keep ? 1 : same ? 1 << 16 : 0;
-        what |= (keep ? 1u : same ? 2u : 0u) << (2 * i);
-      }
-    }
-    int total;
-    const int ahead = block_scan(mine, scratch, &total);  // (its barriers: the round's weights have been read)
-    int a = sure + (ahead & 0xffff), e = equal + (ahead >> 16);
+        for (int r = 0; r < 8; ++r) {  // every load in flight at once
+          f[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (r < parts) f[r] = ld_cluster_f32x4(cluster_map_u32(smem_u32(sm.bins + top), r));
+        }
+        c = make_int4(0, 0, 0, 0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t k = what >> (2 * i) & 3u;
-      if (k == 1u || (k == 2u && e < left)) {
-        const int d = a + min(e, left);
-        kept[d] = j0 + 4 * tid + i;
-        out[d] = x[i];
+        for (int r = 0; r < 8; ++r) {
+          c.x += __float_as_int(f[r].x);
+          c.y += __float_as_int(f[r].y);
+          c.z += __float_as_int(f[r].z);
+          c.w += __float_as_int(f[r].w);
+        }
       }
-      a += k == 1u;
-      e += k == 2u;
+      const int sum = c.x + c.y + c.z + c.w;
+      int above = block_scan(sum, sm.scan);
+      if (above < left && above + sum >= left) {
+        int at = 3, have = c.w;
+        if (above + have < left) { above += have; at = 2; have = c.z; }
+        if (above + have < left) { above += have; at = 1; have = c.y; }
+        if (above + have < left) { above += have; at = 0; have = c.x; }
+        sm.digit = (uint32_t)(top + at);
+        sm.left = left - above;
+        sm.within = have;
+      }
+      if (parts > 1) cluster_sync();  // (every block has read the counts)
+      else __syncthreads();
+      cut |= sm.digit << shift;
+      left = sm.left;
+      same = shift;
+      if (sm.within == left) break;  // all of them stay
+      if (pass < 2) {
+        for (int i = tid; i < kBins; i += kSelectThreads) sm.bins[i] = 0;
+        __syncthreads();
+      }
     }
-    sure += total & 0xffff;
-    equal += total >> 16;
+  } else if (parts > 1) {
+    cluster_sync();  // every block has its weights: they may be overwritten
   }
+  // ---- the kept slots in order, and their weights: a run of the part per warp
+  const auto kind = [&](int i, float x) {  // 1: stays, 2: equal to the cut
+    const int j = j0 + i;
+    const uint32_t u = ordered(x) >> same;
+    return j < from || j >= to || (left > 0 && u > cut >> same) ? 1 : left > 0 && u == cut >> same ? 2 : 0;
+  };
+  const int run = (len + kSelectThreads - 1) / kSelectThreads * 32, i0 = warp * run, i1 = min(len, i0 + run);
+  int sure = 0, equal = 0;
+  for (int i = i0 + lane; i - lane < i1; i += 32) {
+    const int k = i < i1 ? kind(i, weight(i)) : 0;
+    sure += __popc(__ballot_sync(0xffffffffu, k == 1));
+    equal += __popc(__ballot_sync(0xffffffffu, k == 2));
+  }
+  if (lane == 0) sm.count[warp] = make_int2(sure, equal);
   __syncthreads();
-  for (int j = p.budget + tid; j < n; j += kSelectThreads) out[j] = 0.f;
+  sure = equal = 0;
+  int2 all = make_int2(0, 0);
+  for (int x = 0; x < kSelectWarps; ++x) {
+    const int2 c = sm.count[x];
+    if (x < warp) {
+      sure += c.x;
+      equal += c.y;
+    }
+    all.x += c.x;
+    all.y += c.y;
+  }
+  if (parts > 1) {
+    if (tid == 0) sm.all = all;
+    cluster_sync();
+    float2 f[7];
+#pragma unroll
+    for (int r = 0; r < 7; ++r) {
+      f[r] = make_float2(0.f, 0.f);
+      if (r < rank) f[r] = ld_cluster_f32x2(cluster_map_u32(smem_u32(&sm.all), r));
+    }
+#pragma unroll
+    for (int r = 0; r < 7; ++r) {
+      sure += __float_as_int(f[r].x);
+      equal += __float_as_int(f[r].y);
+    }
+  }
+  int32_t *kept = p.kept + (int64_t)unit * p.budget;
+  for (int i = i0 + lane; i - lane < i1; i += 32) {
+    const float x = i < i1 ? weight(i) : 0.f;
+    const int k = i < i1 ? kind(i, x) : 0;
+    const uint32_t ones = __ballot_sync(0xffffffffu, k == 1), twos = __ballot_sync(0xffffffffu, k == 2);
+    const uint32_t ahead = low_mask(lane);
+    const int e = equal + __popc(twos & ahead), d = sure + __popc(ones & ahead) + min(e, left);
+    if (k == 1 || (k == 2 && e < left)) {
+      kept[d] = j0 + i;
+      if (holds) out[d] = x;
+    }
+    sure += __popc(ones);
+    equal += __popc(twos);
+  }
+  if (!holds) {  // weights to their places in rounds of the block, each read before it is written
+    __syncthreads();
+    for (int d0 = 0; d0 < p.budget; d0 += kSelectThreads) {
+      const int d = d0 + tid;
+      const float x = d < p.budget ? __ldcg(w + kept[d]) : 0.f;
+      __syncthreads();
+      if (d < p.budget) out[d] = x;
+    }
+    __syncthreads();
+  }
+  for (int j = max(p.budget, j0) + tid; j < j0 + len; j += kSelectThreads) out[j] = 0.f;
+  if (parts > 1) cluster_sync();  // no block exits while its counts are read
 }
 
-constexpr int kMoveThreads = 512;
-constexpr int kMoveU = 4;  // 16-byte pieces of K, and of V, that a thread holds
+constexpr int kMoveThreads = 256;
+constexpr int kMoveRows = 512;  // rows of a round, at most
 
-__global__ void __launch_bounds__(kMoveThreads, 2)
+struct Move {
+  // of a round's rows (and of the next one's): the slot that comes there, its page,
+  // the page it goes to
+  int4 row[2][kMoveRows];
+};
+
+__global__ void __launch_bounds__(kMoveThreads)
 evict_move_kernel(const __grid_constant__ EvictParams p) {
+  extern __shared__ __align__(16) unsigned char round[];  // a round's rows: K's, then V's
+  __shared__ Move sm;
   const int tid = threadIdx.x, C = p.cluster;
   const int unit = blockIdx.x / C, rank = blockIdx.x % C;
   const int g = unit % p.Hkv, b = unit / p.Hkv % p.rows, layer = unit / p.Hkv / p.rows;
@@ -202,49 +295,60 @@ evict_move_kernel(const __grid_constant__ EvictParams p) {
   if (unit % p.Hkv == 0 && layer == 0 && rank == 0 && tid == 0)
     p.kv_len_out[b] = over ? p.budget : __ldcg(p.kv_len + b);
   if (!over) return;  // (the whole cluster)
-  const int32_t *kept = p.kept + (int64_t)unit * p.budget;
+  const int32_t *kept = p.kept + (int64_t)unit * p.budget, *table = p.table + (int64_t)b * p.table_stride;
   char *k = p.k + layer * p.ks[0] + (int64_t)g * p.ks[2], *v = p.v + layer * p.vs[0] + (int64_t)g * p.vs[2];
-  const auto place = [&](int j, int64_t &ok, int64_t &ov) {  // of slot j
-    int page = b, slot = j;
-    if (p.table) {
-      const int i = j / p.page_size;
-      page = __ldcg(p.table + (int64_t)b * p.table_stride + i);
-      slot = j - i * p.page_size;
-    }
-    ok = (int64_t)page * p.ks[1] + (int64_t)slot * p.ks[3];
-    ov = (int64_t)page * p.vs[1] + (int64_t)slot * p.vs[3];
-  };
-  const int64_t all = (int64_t)p.budget * p.pieces, step = (int64_t)kMoveThreads * kMoveU * C;
-  for (int64_t i0 = 0; i0 < all; i0 += step) {
-    uint4 x[kMoveU], y[kMoveU];
-    int64_t tk[kMoveU], tv[kMoveU];  // where to; -1: nowhere
-#pragma unroll
-    for (int u = 0; u < kMoveU; ++u) {
-      const int64_t i = i0 + ((int64_t)u * C + rank) * kMoveThreads + tid;
-      tk[u] = -1;
-      tv[u] = 0;
-      if (i < all) {
-        const int d = (int)(i / p.pieces), piece = (int)(i - (int64_t)d * p.pieces) * 16;
-        const int j = __ldcg(kept + d);
-        if (j != d) {
-          int64_t fk, fv;
-          place(j, fk, fv);
-          place(d, tk[u], tv[u]);
-          tk[u] += piece;
-          tv[u] += piece;
-          x[u] = __ldcg(reinterpret_cast<const uint4 *>(k + fk + piece));
-          y[u] = __ldcg(reinterpret_cast<const uint4 *>(v + fv + piece));
+  if (!p.table) {
+    k += b * p.ks[1];
+    v += b * p.vs[1];
+  }
+  const auto index = [&](int j) { return p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size; };
+  const int R = p.round_rows, step = R * C;
+  const auto look = [&](int first, int4 *row) {  // rows [first, first + R)
+    for (int r = tid; r < R; r += kMoveThreads) {
+      const int d = first + r;
+      int4 x = make_int4(d, 0, 0, 0);
+      if (d < p.budget) {
+        x.x = __ldcg(kept + d);
+        if (p.table) {
+          x.z = __ldcg(table + index(d));
+          x.y = __ldcg(table + index(x.x));
         }
       }
+      row[r] = x;
     }
+  };
+  // of piece i of a round's K or V
+  const auto row_of = [&](int i) { return p.piece_shift >= 0 ? i >> p.piece_shift : i / p.pieces; };
+  look(rank * R, sm.row[0]);
+  __syncthreads();
+  int now = 0;
+  for (int d0 = rank * R; d0 < p.budget + rank * R; d0 += step, now ^= 1) {  // (as many rounds for every block)
+    const int4 *rows = sm.row[now];
+    const int n = max(0, min(R, p.budget - d0)) * p.pieces;
+    for (int i = tid; i < n; i += kMoveThreads) {
+      const int r = row_of(i), piece = (i - r * p.pieces) * 16;
+      const int4 x = rows[r];
+      if (x.x == d0 + r) continue;  // it stays where it is
+      const int64_t slot = p.table ? x.x - index(x.x) * p.page_size : x.x;
+      cp_async16(round + i * 16, k + ((int64_t)x.y * p.ks[1] + slot * p.ks[3] + piece));
+      cp_async16(round + (R * p.pieces + i) * 16, v + ((int64_t)x.y * p.vs[1] + slot * p.vs[3] + piece));
+    }
+    if (d0 + step < p.budget) look(d0 + step, sm.row[now ^ 1]);
+    cp_async_wait_all();
     if (C > 1) cluster_sync();
     else __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kMoveU; ++u)
-      if (tk[u] >= 0) {
-        __stcg(reinterpret_cast<uint4 *>(k + tk[u]), x[u]);
-        __stcg(reinterpret_cast<uint4 *>(v + tv[u]), y[u]);
-      }
+    for (int i = tid; i < n; i += kMoveThreads) {
+      const int r = row_of(i), piece = (i - r * p.pieces) * 16;
+      const int4 x = rows[r];
+      const int d = d0 + r;
+      if (x.x == d) continue;
+      const int64_t slot = p.table ? d - index(d) * p.page_size : d;
+      __stcg(reinterpret_cast<uint4 *>(k + ((int64_t)x.z * p.ks[1] + slot * p.ks[3] + piece)),
+             *reinterpret_cast<const uint4 *>(round + i * 16));
+      __stcg(reinterpret_cast<uint4 *>(v + ((int64_t)x.z * p.vs[1] + slot * p.vs[3] + piece)),
+             *reinterpret_cast<const uint4 *>(round + (R * p.pieces + i) * 16));
+    }
+    __syncthreads();  // the round's rows have been written from shared memory
   }
 }
 
@@ -260,6 +364,10 @@ __global__ void __launch_bounds__(256) evict_free_kernel(const __grid_constant__
     *at = -1;
   }
 }
+
+
+constexpr int kMoveMost = 204800, kMoveBytes = 49152;  // bytes of a block's round: alone on its SM, or not
+constexpr int kMoveFill = 4;                         // blocks of an SM that the clusters are made for
 
 int64_t aligned16(int64_t n) { return (n + 15) / 16 * 16; }
 
@@ -297,15 +405,33 @@ mgqa_status launch_cache_evict(const mgqa_cache &c, const float *weight, const i
   const int sms = device_sm_count();
   if (sms < 1) return fail(MGQA_ERR_CUDA, "cannot read the SM count of the current device");
   const int64_t units = (int64_t)c.layers * c.rows * c.Hkv;
-  const int64_t rounds = ((int64_t)budget * p.pieces + kMoveThreads * kMoveU - 1) / (kMoveThreads * kMoveU);
-  p.cluster = 1;
-  while (p.cluster < 16 && p.cluster < rounds && units * p.cluster * 2 <= 2 * sms) p.cluster *= 2;
-  static std::atomic<uint64_t> attr{0};
-  mgqa_status st = ensure_cluster_attr(evict_move_kernel, 0, attr, "cache eviction kernel");
+  p.page_shift = -1;
+  if ((c.page_size & (c.page_size - 1)) == 0)
+    for (p.page_shift = 0; (1 << p.page_shift) < c.page_size;) ++p.page_shift;
+  // more blocks while the SMs have room for them (a block of either kernel is a
+  // quarter of an SM) and each has enough to do
+  const int row_bytes = p.pieces * 32;  // of K and V
+  p.piece_shift = -1;
+  if ((p.pieces & (p.pieces - 1)) == 0)
+    for (p.piece_shift = 0; (1 << p.piece_shift) < p.pieces;) ++p.piece_shift;
+  p.cluster = p.parts = 1;
+  const auto fits = [&](int bytes) { return std::max(1, std::min(kMoveRows, bytes / row_bytes)); };
+  while (p.cluster < 16 && (int64_t)p.cluster * 64 < budget && units * p.cluster < kMoveFill * sms) p.cluster *= 2;
+  p.round_rows = std::min((budget + p.cluster - 1) / p.cluster, fits(units * p.cluster <= sms ? kMoveMost : kMoveBytes));
+  if (row_bytes > kMoveMost) return fail(MGQA_ERR_UNSUPPORTED, "cache eviction: rows of more than %d bytes", kMoveMost / 2);
+  while (p.parts < 8 && p.slots > p.parts * 8 * kSelectThreads &&
+         (units * p.parts < sms || p.slots > p.parts * kPart))
+    p.parts *= 2;
+  const int held = std::min<int>(kPart, (p.slots + p.parts * 32 - 1) / (p.parts * 32) * 32) * 4;
+  static std::atomic<uint64_t> select_attr{0}, move_attr{0};
+  mgqa_status st = ensure_cluster_attr(evict_select_kernel, kPart * 4, select_attr, "cache eviction kernel");
+  if (st == MGQA_OK) st = ensure_cluster_attr(evict_move_kernel, kMoveMost, move_attr, "cache eviction kernel");
   if (st != MGQA_OK) return st;
-  cudaError_t e = launch_pdl(evict_select_kernel, dim3((unsigned)units), dim3(kSelectThreads), 0, s, p);
+  cudaError_t e = launch_pdl_cluster(evict_select_kernel, dim3((unsigned)(units * p.parts)), dim3(kSelectThreads), held, s,
+                                     p.parts, p);
   if (e == cudaSuccess)
-    e = launch_pdl_cluster(evict_move_kernel, dim3((unsigned)(units * p.cluster)), dim3(kMoveThreads), 0, s, p.cluster, p);
+    e = launch_pdl_cluster(evict_move_kernel, dim3((unsigned)(units * p.cluster)), dim3(kMoveThreads),
+                           p.round_rows * row_bytes, s, p.cluster, p);
   if (e == cudaSuccess && p.ref && p.table)
     e = launch_pdl(evict_free_kernel, dim3(c.rows), dim3(256), 0, s, p);
   if (e != cudaSuccess) return fail(MGQA_ERR_CUDA, "cache eviction launch: %s", cudaGetErrorString(e));

@@ -133,72 +133,149 @@ append_kernel(const __grid_constant__ AppendParams p) {
 
 // As append, the rows quantised on the way (cache_q4.cuh has the record). A thread
 // has eight features of a row of K and of V; a group's extremes are found between
-// its 4 (D = 64: 2) threads. Every step is one fp32 operation, so the codes are the
-// same wherever they are computed:
+// its 4 (D = 64: 2) threads, in the rows' own type, least and (negated) greatest in
+// one word. Every step is one fp32 operation, so the codes are the same wherever they
+// are computed:
 //   least = fp16(min), scale = fp16((max - least) fl(1/15)), both within +-65504 and
 //   without a negative zero; u = clamp(rint((x - least) / scale), 0, 15), 0 where
 //   scale is 0.
+// Moving rows is all a cache needs, but a row's 16 quotients a thread are the time:
+// they come from a reciprocal. 32768 rows of 8 x 128 bf16 take 56 us (150 with
+// divisions; the reads and writes are 26): 410 instructions a warp of 32 x 16 values,
+// 85 % of the issue slots.
+struct Q4Params {
+  AppendParams a;
+  uint32_t kstep[4], vstep[4];    // cache: layer, page, head, slot in 16-byte pieces
+  uint32_t knstep[4], vnstep[4];  // new rows: layer, batch, head, row
+  int32_t alike;                  // k's and v's steps agree
+  int32_t page_shift;             // of a power of two, else -1
+  uint32_t by_heads;              // x / Hkv = x * by_heads >> 32 for x < 2^16
+};
 struct Q4Piece {
   uint32_t codes;  // of the thread's eight features, in the record's order
   uint32_t par;    // scale and least value of its group
 };
 
+// Eight values as they lie in memory.
 template <typename T>
-MGQA_DEV void load_eight(const char *p, float (&x)[8]) {
+struct Eight {
+  uint4 w[sizeof(T) / 2];
+  MGQA_DEV void load(const char *p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+  }
+  MGQA_DEV void values(float (&x)[8]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x[4 * i] = __uint_as_float(w[i].x); x[4 * i + 1] = __uint_as_float(w[i].y);
+        x[4 * i + 2] = __uint_as_float(w[i].z); x[4 * i + 3] = __uint_as_float(w[i].w);
+      }
+    } else {
+      unpack16_t<T>(w[0], x);
+    }
+  }
+};
+
+MGQA_DEV uint32_t min_pair(uint32_t a, uint32_t b, __nv_bfloat16) {
+  const __nv_bfloat162 r = __hmin2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+MGQA_DEV uint32_t min_pair(uint32_t a, uint32_t b, __half) {
+  const __half2 r = __hmin2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// The least and the greatest value of a group. (Whole warps.)
+template <typename T, int D>
+MGQA_DEV void extremes(const Eight<T> &e, const float (&x)[8], float &lo, float &hi) {
   if constexpr (sizeof(T) == 4) {
-    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    lo = hi = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      lo = fminf(lo, x[i]);
+      hi = fmaxf(hi, x[i]);
+    }
+#pragma unroll
+    for (int o = 1; o < D / 32; o <<= 1) {
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
   } else {
-    unpack16_t<T>(__ldcs(reinterpret_cast<const uint4 *>(p)), x);
+    constexpr uint32_t kSigns = 0x80008000u;
+    const uint4 &w = e.w[0];
+    const uint32_t a = min_pair(min_pair(w.x, w.y, T()), min_pair(w.z, w.w, T()), T());
+    const uint32_t b = min_pair(min_pair(w.x ^ kSigns, w.y ^ kSigns, T()), min_pair(w.z ^ kSigns, w.w ^ kSigns, T()), T());
+    // least values of the even and the odd features, then the negated greatest ones
+    uint32_t m = min_pair(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632), T());
+#pragma unroll
+    for (int o = 1; o < D / 32; o <<= 1) m = min_pair(m, __shfl_xor_sync(0xffffffffu, m, o), T());
+    float f[8];
+    unpack16_t<T>(make_uint4(m, 0u, 0u, 0u), f);
+    lo = f[0];
+    hi = -f[1];
   }
 }
 
-// mask: the lanes of the row, all of which take part.
-template <int D>
-MGQA_DEV Q4Piece quantise(const float (&x)[8], uint32_t mask) {
-  float lo = x[0], hi = x[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-  }
-#pragma unroll
-  for (int o = 1; o < D / 32; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(mask, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(mask, hi, o));
-  }
+template <typename T, int D>
+MGQA_DEV Q4Piece quantise(const Eight<T> &e) {
+  float x[8], lo, hi;
+  e.values(x);
+  extremes<T, D>(e, x, lo, hi);
   uint32_t least = __half_as_ushort(__float2half_rn(fminf(fmaxf(lo, -65504.f), 65504.f)));
   if (least == 0x8000u) least = 0u;
   const float base = __half2float(__ushort_as_half((unsigned short)least));
   const float range = __fmul_rn(__fsub_rn(hi, base), 1.f / 15.f);
   const __half scale = __float2half_rn(fminf(fmaxf(range, 0.f), 65504.f));
   const float step = __half2float(scale);
+  const float inv = step > 0.f ? __frcp_rn(step) : 0.f;
   Q4Piece r;
   r.par = (uint32_t)__half_as_ushort(scale) | least << 16;
-  r.codes = 0u;
+  // The quotients by the reciprocal and one correction, rounded as a division's (P.
+  // Markstein, IBM J. Res. Develop. 34, 1990: the reciprocal is a rounded one, the
+  // remainder exact); adding 1.5 2^23 rounds them to whole numbers, half to even, in
+  // the low bits. Where least's rounding leaves values far outside the codes, and they
+  // have to be clamped, the division does.
+  uint32_t codes = 0u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float u = step > 0.f ? rintf(__fdiv_rn(__fsub_rn(x[i], base), step)) : 0.f;
-    r.codes |= (uint32_t)(int)fminf(fmaxf(u, 0.f), 15.f) << (4 * i);
+    const float d = __fsub_rn(x[i], base), q = __fmul_rn(d, inv);
+    const float t = __fadd_rn(__fmaf_rn(__fmaf_rn(-q, step, d), inv, q), 12582912.f);
+    codes += __float_as_uint(t) << (4 * i);
+  }
+  codes -= 0x4b400000u * 0x11111111u;
+  if (!(__fmul_rn(__fsub_rn(lo, base), inv) > -0.499f && __fmul_rn(__fsub_rn(hi, base), inv) < 15.499f)) {
+    codes = 0u;
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      float u = x[0];
+#pragma unroll
+      for (int k = 1; k < 8; ++k) u = i == k ? x[k] : u;
+      u = step > 0.f ? rintf(__fdiv_rn(__fsub_rn(u, base), step)) : 0.f;
+      codes |= (uint32_t)(int)fminf(fmaxf(u, 0.f), 15.f) << (4 * i);
+    }
   }
   if constexpr (D == 64) {
     // the bytes of groups 0 and 1 (2 and 3) by turns: the first group's thread keeps
     // the first two bytes of each, the other one the last two
-    const uint32_t other = __shfl_xor_sync(mask, r.codes, 2);
-    r.codes = (threadIdx.x & 2) ? __byte_perm(other, r.codes, 0x7362) : __byte_perm(r.codes, other, 0x5140);
+    __syncwarp();
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, codes, 2);
+    codes = (threadIdx.x & 2) ? __byte_perm(other, codes, 0x7362) : __byte_perm(codes, other, 0x5140);
   }
+  r.codes = codes;
   return r;
 }
 
-// The thread's part of a record: its codes, and from the row's first thread the parameters.
+// The thread's part of a record (null: none): its codes, and from the row's first
+// thread the parameters. (Whole warps.)
 template <int D>
-MGQA_DEV void store_record(char *rec, const Q4Piece &r, int piece, uint32_t mask) {
+MGQA_DEV void store_record(char *rec, const Q4Piece &r, int piece) {
   constexpr int GL = D / 32;  // threads of a group
   uint32_t g[4];
   const int first = (int)(threadIdx.x & 31) - piece;
+  __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) g[i] = __shfl_sync(mask, r.par, first + i * GL);
+  for (int i = 0; i < 4; ++i) g[i] = __shfl_sync(0xffffffffu, r.par, first + i * GL);
   if (!rec) return;
   // (D = 64: threads 0..3 of a chunk have its words 0, 2, 1, 3)
   const int word = D == 64 ? (piece & ~3) | (piece & 1) << 1 | (piece >> 1 & 1) : piece;
@@ -211,8 +288,9 @@ MGQA_DEV void store_record(char *rec, const Q4Piece &r, int piece, uint32_t mask
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads)
-append_q4_kernel(const __grid_constant__ AppendParams p) {
+append_q4_kernel(const __grid_constant__ Q4Params qp) {
   constexpr int LR = D / 8;  // threads of a row
+  const AppendParams &p = qp.a;
   const Pool &c = p.c;
   const int b = blockIdx.y, layer = blockIdx.z;
   grid_dependency_wait();
@@ -222,35 +300,42 @@ append_q4_kernel(const __grid_constant__ AppendParams p) {
   const int n = load(c.kv_len + b);
   const int cnt = p.count ? load(p.count + b) : p.T;
   const bool bad = n < 0 || cnt < 0 || cnt > p.T || (int64_t)n + cnt > cap;
-  const int per = c.Hkv * LR;
-  const int t0 = (int)blockIdx.x * p.block_rows, rows = min(p.block_rows, p.T - t0);
-  const uint32_t mask = low_mask(LR) << (threadIdx.x & 31 & ~(LR - 1));  // (a row's threads go together)
-  for (int i = threadIdx.x; i < rows * per; i += kAppendThreads) {
-    const int tl = i / per, rem = i - tl * per, t = t0 + tl;
-    const int h = rem / LR, piece = rem % LR;
-    if (p.count && (bad || t >= cnt)) break;
-    const int from = p.index ? load(p.index + (int64_t)b * p.T + t) : t;
-    const bool has = (unsigned)from < (unsigned)p.T;
-    float kx[8] = {}, vx[8] = {};
+  const int t0 = (int)blockIdx.x * p.block_rows, rows = min(p.block_rows, p.T - t0) * c.Hkv;
+  const int live = bad ? 0 : p.count ? min(cnt, p.T) : p.T;
+  const int piece = threadIdx.x % LR;
+  const auto pieces = [&](const uint32_t (&st)[4], int x, int y, int z) {  // of layer `layer`
+    return (uint64_t)(uint32_t)layer * st[0] + (uint64_t)(uint32_t)x * st[1] + (uint64_t)(uint32_t)y * st[2] +
+           (uint64_t)(uint32_t)z * st[3];
+  };
+  for (int r0 = 0; r0 < rows; r0 += kAppendThreads / LR) {  // (whole warps)
+    const int r = r0 + (int)threadIdx.x / LR;
+    const int tl = (int)__umulhi((uint32_t)r, qp.by_heads), h = r - tl * c.Hkv, t = t0 + tl;
+    const bool mine = r < rows && t < live;
+    int from = t;
+    if (p.index && mine) from = load(p.index + (int64_t)b * p.T + t);
+    const bool has = mine && (unsigned)from < (unsigned)p.T;
+    Eight<T> kx{}, vx{};
     if (has) {
-      const int64_t at = (int64_t)from;
-      load_eight<T>(p.kn + layer * p.kns[0] + b * p.kns[1] + h * p.kns[2] + at * p.kns[3] + piece * (8 * (int)sizeof(T)), kx);
-      load_eight<T>(p.vn + layer * p.vns[0] + b * p.vns[1] + h * p.vns[2] + at * p.vns[3] + piece * (8 * (int)sizeof(T)), vx);
+      const uint64_t at = pieces(qp.knstep, b, h, from), av = qp.alike ? at : pieces(qp.vnstep, b, h, from);
+      kx.load(p.kn + (at * 16 + piece * (8 * (int)sizeof(T))));
+      vx.load(p.vn + (av * 16 + piece * (8 * (int)sizeof(T))));
     }
-    if (bad) break;
-    const int j = n + t;
-    int page = b, slot = j;
-    if (c.table) {
-      const int pi = j / c.page_size;
+    int page = b, slot = n + t;
+    if (c.table && mine) {
+      const int pi = qp.page_shift >= 0 ? slot >> qp.page_shift : slot / c.page_size;
       page = valid_page(c, load(c.table + (int64_t)b * c.table_stride + pi));
-      slot = j - pi * c.page_size;
+      slot -= pi * c.page_size;
     }
     const bool to = has && page >= 0;
-    if (!to && layer == 0 && rem == 0) report_error(c.err, MGQA_ERR_INVALID_ARG);
-    store_record<D>(to ? c.k + layer * c.ks[0] + (int64_t)page * c.ks[1] + h * c.ks[2] + (int64_t)slot * c.ks[3] : nullptr,
-                    quantise<D>(kx, mask), piece, mask);
-    store_record<D>(to ? c.v + layer * c.vs[0] + (int64_t)page * c.vs[1] + h * c.vs[2] + (int64_t)slot * c.vs[3] : nullptr,
-                    quantise<D>(vx, mask), piece, mask);
+    if (mine && !to && layer == 0 && piece == 0 && h == 0) report_error(c.err, MGQA_ERR_INVALID_ARG);
+    char *k = nullptr, *v = nullptr;
+    if (to) {
+      const uint64_t at = pieces(qp.kstep, page, h, slot), av = qp.alike ? at : pieces(qp.vstep, page, h, slot);
+      k = c.k + at * 16;
+      v = c.v + av * 16;
+    }
+    store_record<D>(k, quantise<T, D>(kx), piece);
+    store_record<D>(v, quantise<T, D>(vx), piece);
   }
   if (blockIdx.x == 0 && layer == 0 && threadIdx.x == 0) {
     if (bad) report_error(c.err, MGQA_ERR_INVALID_ARG);
@@ -733,17 +818,34 @@ mgqa_status launch_cache_append(const mgqa_cache &c, const void *k_new, const vo
   const int64_t per = (int64_t)c.Hkv * p.c.pieces;
   if (per > (1 << 20)) return fail(MGQA_ERR_UNSUPPORTED, "cache append: rows of more than 16 MB");
   p.block_rows = (int32_t)std::max<int64_t>(1, kAppendThreads / per);
+  // (four rounds a block: 32768 rows of 8 x 128 55.7 us, one 59.6, eight 58.0)
+  if (q4 && per <= kAppendThreads) p.block_rows = std::min(T, p.block_rows * 4);
   const int64_t bx = (T + p.block_rows - 1) / p.block_rows;
   if (c.rows > 65535 || c.layers > 65535 || bx > 0x7fffffff)
     return fail(MGQA_ERR_UNSUPPORTED, "more than 65535 requests or layers");
-  auto kern = append_kernel;
-  if (q4) {
-    kern = c.dtype == MGQA_BF16   ? (c.D == 64 ? append_q4_kernel<__nv_bfloat16, 64> : append_q4_kernel<__nv_bfloat16, 128>)
-           : c.dtype == MGQA_FP16 ? (c.D == 64 ? append_q4_kernel<__half, 64> : append_q4_kernel<__half, 128>)
-                                  : (c.D == 64 ? append_q4_kernel<float, 64> : append_q4_kernel<float, 128>);
+  const dim3 grid((unsigned)bx, c.rows, c.layers);
+  if (!q4) return launched(launch_pdl(append_kernel, grid, dim3(kAppendThreads), 0, s, p), "cache append");
+  Q4Params qp{};
+  bool fits = c.Hkv <= 1 << 15;
+  for (int t = 0; t < 4; ++t) {
+    const int64_t st[4] = {p.c.ks[t] / 16, p.c.vs[t] / 16, p.kns[t] / 16, p.vns[t] / 16};
+    for (const int64_t x : st) fits = fits && x <= 0xffffffffll;
+    qp.kstep[t] = (uint32_t)st[0];
+    qp.vstep[t] = (uint32_t)st[1];
+    qp.knstep[t] = (uint32_t)st[2];
+    qp.vnstep[t] = (uint32_t)st[3];
   }
-  return launched(launch_pdl(kern, dim3((unsigned)bx, c.rows, c.layers), dim3(kAppendThreads), 0, s, p),
-                  "cache append");
+  if (!fits) return fail(MGQA_ERR_UNSUPPORTED, "4-bit append: strides past 2^36 bytes, or more than 2^15 KV heads");
+  qp.alike = std::equal(qp.kstep, qp.kstep + 4, qp.vstep) && std::equal(qp.knstep, qp.knstep + 4, qp.vnstep);
+  qp.page_shift = -1;
+  if ((c.page_size & (c.page_size - 1)) == 0)
+    for (qp.page_shift = 0; (1 << qp.page_shift) < c.page_size;) ++qp.page_shift;
+  qp.by_heads = (uint32_t)((((uint64_t)1 << 32) + c.Hkv - 1) / c.Hkv);
+  qp.a = p;
+  const auto kern = c.dtype == MGQA_BF16   ? (c.D == 64 ? append_q4_kernel<__nv_bfloat16, 64> : append_q4_kernel<__nv_bfloat16, 128>)
+                    : c.dtype == MGQA_FP16 ? (c.D == 64 ? append_q4_kernel<__half, 64> : append_q4_kernel<__half, 128>)
+                                           : (c.D == 64 ? append_q4_kernel<float, 64> : append_q4_kernel<float, 128>);
+  return launched(launch_pdl(kern, grid, dim3(kAppendThreads), 0, s, qp), "cache append");
 }
 
 mgqa_status launch_cache_fork(const mgqa_cache &c, int n, const int32_t *src, const int32_t *dst, int32_t extra,

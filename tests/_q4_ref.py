@@ -136,9 +136,13 @@ def check_weights(got, before, q, k, kmag, vis, lse, scale, what=""):
 
 
 def kept_slots(w, n, budget, sinks, recent):
-    """Slots that stay of n with weights w (a list), in order."""
+    """Slots that stay of n with weights w [>= n] (on the CPU), in order."""
     if n <= budget:
         return list(range(n))
-    order = lambda x: (-1, 0.0) if math.isnan(x) else (0, x)  # noqa: E731
-    middle = sorted(range(sinks, n - recent), key=lambda j: (tuple(-y for y in order(w[j])), j))
-    return sorted(list(range(sinks)) + middle[:budget - sinks - recent] + list(range(n - recent, n)))
+    mid = w[sinks:n - recent].double()
+    mid = torch.where(mid.isnan(), -math.inf, mid)
+    # (a NaN behind -inf: by whether it is one, then by weight; stable, so the first of equal ones)
+    order = torch.sort(mid, descending=True, stable=True).indices
+    order = order[torch.sort(w[sinks:n - recent][order].isnan().int(), stable=True).indices]
+    middle = (order[:budget - sinks - recent] + sinks).tolist()
+    return sorted(list(range(sinks)) + middle + list(range(n - recent, n)))

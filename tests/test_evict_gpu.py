@@ -181,10 +181,10 @@ class Evict:
             odd = torch.tensor([0.0, -0.0, -1.0, 1.0, math.inf, -math.inf, math.nan, 1e-42, -1e-42, 3e38, 1e-3],
                                device="cuda")
             w = odd[torch.randint(0, len(odd), w.shape, generator=g, device="cuda")]
-        self.w, self.kv_len, self.err = w, i32(lens), i32([0])
+        self.w, self.host, self.kv_len, self.err = w, w.cpu(), i32(lens), i32([0])
 
     def want(self, layer, b, g):
-        return kept_slots(self.w[layer, b, g].tolist(), self.lens[b], self.budget, self.sinks, self.recent)
+        return kept_slots(self.host[layer, b, g], self.lens[b], self.budget, self.sinks, self.recent)
 
     def place(self, table, b, j):
         j = torch.as_tensor(j, device="cuda", dtype=torch.long)
@@ -249,7 +249,7 @@ def test_rows_of_any_kind(M, dtype, D, page):
 @pytest.mark.parametrize("lens,budget,layers,Hkv,weights", [
     ([33000], 4096, 1, 2, "some"), ([70001], 30000, 1, 1, "some"), ([20000, 100, 5000], 4999, 1, 3, "ties"),
     ([9000] * 20, 2048, 1, 8, "some"), ([4096], 4095, 2, 8, "equal"), ([12289], 1, 1, 1, "some"),
-    ([1030] * 5, 1024, 9, 4, "some")])
+    ([1030] * 5, 1024, 9, 4, "some"), ([330000], 5000, 1, 1, "some"), ([50000, 41000], 300, 1, 2, "ties")])
 @pytest.mark.parametrize("page", [0, 64])
 def test_long_requests(M, lens, budget, layers, Hkv, weights, page):
     Evict(lens, budget, min(4, budget - 1), min(256, budget // 2), layers=layers, Hkv=Hkv, D=128, page=page,
@@ -390,7 +390,7 @@ def test_a_serving_loop(M, q4):
         def cut(kk, vv, w):
             if kk.shape[1] <= budget:
                 return kk, vv, w
-            keep = torch.tensor([kept_slots(w[g].tolist(), kk.shape[1], budget, 2, 8) for g in range(Hkv)], device="cuda")
+            keep = torch.tensor([kept_slots(w[g].cpu(), kk.shape[1], budget, 2, 8) for g in range(Hkv)], device="cuda")
             pick = lambda x: torch.gather(x, 1, keep[..., None].expand(-1, -1, D))  # noqa: E731
             return pick(kk), pick(vv), torch.gather(w, 1, keep)
 
