@@ -86,7 +86,7 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
   const bool teller = tid == 0 && !S;
   if (teller) tell_cut(p, blockIdx.x, nullptr);
 
-  Stream<kKeys, F::REC / 16, false, true, kWarps> ahead(sm.feed[warp], 1);
+  Stream<kKeys, F::REC / 16, kAsIs, true, kWarps> ahead(sm.feed[warp], 1);
   ahead.start(qp, pieces, warp, lane);
   int put = 0, st = 0;  // stages: filled next, used next
   const auto start_one = [&] {

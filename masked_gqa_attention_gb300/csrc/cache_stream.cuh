@@ -41,10 +41,15 @@ struct alignas(16) Feed {
   Pieces pieces;
 };
 
-// KEYS rows of P 16-byte pieces a tile, of V too (behind K's) or not. SWAP: the halves
-// of every 128 bytes of odd rows change places, so that eight lanes that read four
-// pieces each of two rows meet all banks.
-template <int KEYS, int P, bool SWAP, bool V, int WARPS>
+// Where the 16-byte pieces of a row lie within 128 bytes, so that reads meet all banks.
+enum Order {
+  kAsIs,        // (rows of 80 or 48 bytes: whole rows of eight do so anyway)
+  kOddSwapped,  // the halves of odd rows change places: eight lanes read four pieces of two rows
+  kXor          // piece ^ row % 8: eight lanes read one piece of eight rows
+};
+
+// KEYS rows of P 16-byte pieces a tile, of V too (behind K's) or not.
+template <int KEYS, int P, Order ORDER, bool V, int WARPS>
 struct Stream {
   static constexpr int TILEB = KEYS * P * 16;  // bytes of a tile of one tensor
   Feed &f;
@@ -127,7 +132,7 @@ struct Stream {
     const char *k = f.k, *v = V ? f.v : nullptr;
     const auto place = [&](int i) {
       const int x = lane + 32 * i;
-      return (SWAP ? x ^ (x / P & 1) << 2 : x) * 16;
+      return (ORDER == kOddSwapped ? x ^ (x / P & 1) << 2 : ORDER == kXor ? x ^ (x / P & 7) : x) * 16;
     };
     if (p.halves && ok == low_mask(KEYS)) {  // runs of 16 rows
       constexpr int kRun = 16 * P * 16;      // (a lane's piece of the first or the second)

@@ -9,10 +9,9 @@
 // up to some 64 rows the reads bound it, then the products. Keys are independent of
 // one another, so every warp streams tiles of its own (cache_stream.cuh) and takes the
 // keys as the first operand of m16n8k16 products with 8 rows of queries each, which
-// the CTA has staged in shared memory: a quad of lanes has a key, and each of its
-// lanes the 16-byte pieces 4 i + its place, an order of the features that the queries
-// are staged in too. fp32 keys take the same places and the CUDA cores; keys in 4 bits
-// the products of cache_q4.cuh.
+// the CTA has staged in shared memory in the order of their operand registers. fp32
+// keys take the CUDA cores, a quad of lanes a key; keys in 4 bits the products of
+// cache_q4.cuh.
 //
 // The tiles of all requests and KV heads are cut into equal runs (cache_sched.cuh);
 // no sum crosses a warp but a quad's, so results repeat bit for bit.
@@ -32,50 +31,55 @@ struct WeightParams {
   StreamParams s;
   float *weight;
   int64_t ws[2];  // request, KV head
-  int32_t chunk;  // rows staged at a time: a multiple of 8
+  int32_t chunk;  // rows staged at a time: 8, or a multiple of 16
 };
 
-// The keys of a tile, as a lane holds them: block i has keys 8 i + gq. 16-bit ...
+// The keys of a tile, as a lane holds them: block i has keys 8 i + gq. 16-bit (as the
+// products take them: taken in 16-byte pieces, half of all instructions moved them) ...
 template <typename T, int D>
 struct Keys {
   using Query = T;
-  static constexpr int KEYS = 32, N = D / 32;
+  static constexpr int KEYS = 32, N = D / 16;  // N: products
   static constexpr int ROWB = D * 2;
-  static constexpr bool SWAP = true;
-  static constexpr int STAGED = N * 512;                 // bytes of 8 staged rows
-  static constexpr int CTAS = 2;
-  uint4 k[4][N];
+  static constexpr Order ORDER = kXor;
+  static constexpr int STAGED = N * 256;  // bytes of 8 staged rows
+  static constexpr int CTAS = 2, STAGES = 2;
+  uint32_t k[2][N][4];
 
   MGQA_DEV void take(const unsigned char *tile, int lane) {
+    const int row = lane & 15;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int c = 0; c < N; ++c)
-        k[i][c] = *reinterpret_cast<const uint4 *>(tile + (8 * i + lane / 4) * ROWB + ((4 * c + lane % 4) ^ (lane & 4)) * 16);
+      for (int s = 0; s < N; ++s)
+        ldmatrix_x4(k[m][s][0], k[m][s][1], k[m][s][2], k[m][s][3],
+                    tile + (16 * m + row) * ROWB + ((2 * s + (lane >> 4)) ^ (row & 7)) * 16);
   }
   // Query row (null: zeros) of this lane's quad to its place of 8 staged rows; the
   // factor that its scores still need.
   static MGQA_DEV float stage(const T *row, unsigned char *to, int lane) {
+    const uint32_t *src = reinterpret_cast<const uint32_t *>(row) + (lane & 3);
 #pragma unroll
-    for (int c = 0; c < N; ++c)
-      reinterpret_cast<uint4 *>(to)[c * 32 + lane] =
-          row ? *(reinterpret_cast<const uint4 *>(row) + 4 * c + (lane & 3)) : make_uint4(0u, 0u, 0u, 0u);
+    for (int s = 0; s < N; s += 2)
+      reinterpret_cast<uint4 *>(to)[s / 2 * 32 + lane] =
+          row ? make_uint4(src[8 * s], src[8 * s + 4], src[8 * s + 8], src[8 * s + 12]) : make_uint4(0u, 0u, 0u, 0u);
     return 1.f;
   }
   // s[i][e]: block i with row 2 tq + e
   MGQA_DEV void scores(const unsigned char *staged, int lane, float (&s)[4][2]) const {
     float x[2][4];
 #pragma unroll
-    for (int c = 0; c < N; ++c) {
-      const uint4 q = reinterpret_cast<const uint4 *>(staged)[c * 32 + lane];
+    for (int c = 0; c < N; c += 2) {
+      const uint4 q = reinterpret_cast<const uint4 *>(staged)[c / 2 * 32 + lane];
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        const uint4 &a = k[2 * m][c], &b = k[2 * m + 1][c];
-        if (c == 0) mma_16816_first<T>(x[m], a.x, b.x, a.y, b.y, q.x, q.y);
-        else mma_16816<T>(x[m], a.x, b.x, a.y, b.y, q.x, q.y);
+        const uint32_t(&a)[4] = k[m][c];
+        if (c == 0) mma_16816_first<T>(x[m], a[0], a[1], a[2], a[3], q.x, q.y);
+        else mma_16816<T>(x[m], a[0], a[1], a[2], a[3], q.x, q.y);
       }
 #pragma unroll
-      for (int m = 0; m < 2; ++m) mma_16816<T>(x[m], k[2 * m][c].z, k[2 * m + 1][c].z, k[2 * m][c].w, k[2 * m + 1][c].w, q.z, q.w);
+      for (int m = 0; m < 2; ++m)
+        mma_16816<T>(x[m], k[m][c + 1][0], k[m][c + 1][1], k[m][c + 1][2], k[m][c + 1][3], q.z, q.w);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -91,9 +95,9 @@ struct Keys<float, D> {
   using Query = float;
   static constexpr int KEYS = 16, N = D / 16;
   static constexpr int ROWB = D * 4;
-  static constexpr bool SWAP = true;
+  static constexpr Order ORDER = kOddSwapped;
   static constexpr int STAGED = 8 * D * 4;
-  static constexpr int CTAS = D == 128 ? 2 : 3;
+  static constexpr int CTAS = D == 128 ? 2 : 3, STAGES = 2;
   float4 k[2][N];
 
   MGQA_DEV void take(const unsigned char *tile, int lane) {
@@ -144,10 +148,10 @@ struct Q4Keys {
   static constexpr bool SPLIT = sizeof(T) == 4;
   static constexpr int KEYS = 32, N = F::CHUNKS;
   static constexpr int ROWB = F::REC;
-  static constexpr bool SWAP = false;
+  static constexpr Order ORDER = kAsIs;
   static constexpr int WORDS = 8 * F::KS;  // operand registers of a row, one term
   static constexpr int STAGED = (WORDS * (SPLIT ? 2 : 1) + 2) * 128;
-  static constexpr int CTAS = 3;
+  static constexpr int CTAS = 3, STAGES = 4;
   uint32_t w[N][4], par[2][4];
   float sc[4][4];
 
@@ -215,7 +219,7 @@ struct RowRule {
 
 template <typename K, int D>
 struct Cfg {
-  static constexpr int STAGES = 2;
+  static constexpr int STAGES = K::STAGES;
   static constexpr int TILEB = K::KEYS * K::ROWB;
   static constexpr int ring = kWarps * STAGES * TILEB;
   struct Misc {
@@ -246,7 +250,7 @@ cache_weights_kernel(const __grid_constant__ WeightParams wp) {
   pieces.start<kThreads>(wp.s.t, sm.scratch);
 
   const int passes = (p.R + wp.chunk - 1) / wp.chunk;
-  Stream<K::KEYS, K::ROWB / 16, K::SWAP, false, kWarps> ahead(sm.feed[warp], passes);
+  Stream<K::KEYS, K::ROWB / 16, K::ORDER, false, kWarps> ahead(sm.feed[warp], passes);
   ahead.start(wp.s, pieces, warp, lane);
   int put = 0, st = 0;
   const auto start_one = [&] {
@@ -262,7 +266,8 @@ cache_weights_kernel(const __grid_constant__ WeightParams wp) {
   while (pieces.next(p, pc)) {
     const RowPlan &rp = pc.rp;
     for (int r0 = 0; r0 < p.R; r0 += wp.chunk) {
-      const int rows = min(wp.chunk, p.R - r0), groups = (rows + 7) / 8;
+      // (eight rows, or pairs of them, with rows that give nothing behind the last one)
+      const int rows = min(wp.chunk, p.R - r0), groups = wp.chunk == 8 ? 1 : (rows + 15) / 16 * 2;
       __syncthreads();  // the rows of an earlier chunk are no longer read
       for (int g8 = warp; g8 < groups; g8 += kWarps) {
         const int row = r0 + 8 * g8 + gq;
@@ -294,9 +299,7 @@ cache_weights_kernel(const __grid_constant__ WeightParams wp) {
         keys.take(ring + st * C::TILEB, lane);
         const bool all = k0 + K::KEYS - 1 <= near && (k0 >= far || k0 + K::KEYS <= p.sinks);
         float w[NB] = {};
-        for (int g8 = 0; g8 < groups; ++g8) {
-          float s[NB][2];
-          keys.scores(staged + g8 * K::STAGED, lane, s);
+        const auto add = [&](int g8, float (&s)[NB][2]) {  // the weights of 8 rows
           const int4 ra = *reinterpret_cast<const int4 *>(&sm.rule[8 * g8 + 2 * tq]);
           const int4 rb = *reinterpret_cast<const int4 *>(&sm.rule[8 * g8 + 2 * tq + 1]);
           const float lse[2] = {__int_as_float(ra.x), __int_as_float(rb.x)}, f[2] = {__int_as_float(ra.y), __int_as_float(rb.y)};
@@ -317,6 +320,19 @@ cache_weights_kernel(const __grid_constant__ WeightParams wp) {
           }
 #pragma unroll
           for (int i = 0; i < NB; ++i) w[i] += s[i][0] + s[i][1];
+        };
+        if (groups == 1) {
+          float s[NB][2];
+          keys.scores(staged, lane, s);
+          add(0, s);
+        } else {
+          for (int g8 = 0; g8 < groups; g8 += 2) {  // (two at a time: one's products are a chain)
+            float s[NB][2], z[NB][2];
+            keys.scores(staged + g8 * K::STAGED, lane, s);
+            keys.scores(staged + (g8 + 1) * K::STAGED, lane, z);
+            add(g8, s);
+            add(g8 + 1, z);
+          }
         }
         float sum = 0.f;
 #pragma unroll
@@ -348,7 +364,7 @@ mgqa_status launch_k(WeightParams wp, int page_size, int sms, cudaStream_t s) {
   p.tile_shift = K::KEYS == 32 ? 5 : 4;
   p.lead = 4;
   p.min_run = kWarps;
-  wp.chunk = std::min(kChunkRows, (p.R + 7) / 8 * 8);
+  wp.chunk = p.R <= 8 ? 8 : std::min(kChunkRows, (p.R + 15) / 16 * 16);
   const int64_t units = (int64_t)p.B * p.Hkv;
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(K::CTAS * sms, units * (most_tiles(p) + p.lead)));
   const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kThreads), (size_t)C::fixed + (wp.chunk / 8) * K::STAGED, s, wp);
