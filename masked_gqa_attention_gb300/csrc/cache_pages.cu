@@ -149,7 +149,7 @@ struct Q4Params {
   uint32_t knstep[4], vnstep[4];  // new rows: layer, batch, head, row
   int32_t alike;                  // k's and v's steps agree
   int32_t page_shift;             // of a power of two, else -1
-  uint32_t by_heads;              // x / Hkv = x * by_heads >> 32 for x < 2^16
+  uint32_t by_heads;              // x / Hkv = x * by_heads >> 32 for x < 2^16 (and Hkv > 1)
 };
 struct Q4Piece {
   uint32_t codes;  // of the thread's eight features, in the record's order
@@ -309,7 +309,7 @@ append_q4_kernel(const __grid_constant__ Q4Params qp) {
   };
   for (int r0 = 0; r0 < rows; r0 += kAppendThreads / LR) {  // (whole warps)
     const int r = r0 + (int)threadIdx.x / LR;
-    const int tl = (int)__umulhi((uint32_t)r, qp.by_heads), h = r - tl * c.Hkv, t = t0 + tl;
+    const int tl = c.Hkv == 1 ? r : (int)__umulhi((uint32_t)r, qp.by_heads), h = r - tl * c.Hkv, t = t0 + tl;
     const bool mine = r < rows && t < live;
     int from = t;
     if (p.index && mine) from = load(p.index + (int64_t)b * p.T + t);

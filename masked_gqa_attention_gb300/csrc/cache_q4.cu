@@ -24,9 +24,10 @@
 // 98000 keys: 0.0066 of the outputs' size from 64 bits with running accumulators).
 // For the same reason fp16 and fp32 calls take the codes from their middle,
 //   out_d = sum_j (p_j scale_jg) (u_jd - 8) + sum_j p_j (least_jg + 8 scale_jg),
-// so that roundings of the weights are not multiplied by terms that cancel (the -8
-// by products with a constant; fp16: 0.0005 of the outputs' size without, where the
-// outputs' own rounding makes 0.0002). In bf16 the outputs' rounding hides it.
+// so that roundings are not multiplied by terms that cancel: fp16 the -8 by products
+// with a constant (0.0005 of the outputs' size without, where the outputs' own rounding
+// makes 0.0002), fp32 in the operand (with the constant, and in the scores without,
+// 4.5e-6). In bf16 the outputs' rounding hides it.
 //
 // The work is cut as for the other cache attention (cache_sched.cuh): equal runs of
 // tiles and the merge kernel for long calls, a cluster per unit for short ones.
@@ -171,8 +172,8 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             uint32_t u[2][4];
-            q4_unpack(w[2 * i], u[0]);
-            q4_unpack(w[2 * i + 1], u[1]);
+            q4_codes<SPLIT>(w[2 * i], u[0]);
+            q4_codes<SPLIT>(w[2 * i + 1], u[1]);
             const float(&two)[2][4] = reinterpret_cast<const float(&)[2][4]>(sc[2 * i]);
 #pragma unroll
             for (int r = 0; r < RT; ++r)
@@ -259,18 +260,34 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
       ldmatrix_x4_trans(vpar[0], vpar[1], vpar[2], vpar[3],
                         vt + ((lane & 7) | (lane & 8) << 1 | (lane & 16) >> 1) * F::REC + F::CODES);
       {
+        uint32_t vmin1[4], vmin2[4];  // (fp32: least + 8 scale, in two terms, in the lanes of the least values)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          vmin1[n] = vpar[n];
+          if constexpr (SPLIT) {
+            const uint32_t across = __shfl_xor_sync(0xffffffffu, vpar[n], 16);
+            const float2 least = __half22float2(*reinterpret_cast<const __half2 *>(&vpar[n]));
+            const float2 scale2 = __half22float2(*reinterpret_cast<const __half2 *>(&across));
+            const float y = fmaf(8.f, scale2.x, least.x), z = fmaf(8.f, scale2.y, least.y);
+            vmin1[n] = pack2<__half>(y, z);
+            const float2 got = __half22float2(*reinterpret_cast<const __half2 *>(&vmin1[n]));
+            vmin2[n] = pack2<__half>(y - got.x, z - got.y);
+          }
+        }
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           float add[4], behind[4];
-          mma_16816_first<__half>(add, vpar[0], vpar[1], vpar[2], vpar[3], pw[r][0], pw[r][1]);
-          mma_16816_first<__half>(behind, vpar[0], vpar[1], vpar[2], vpar[3], pw[r][2], pw[r][3]);
+          mma_16816_first<__half>(add, vmin1[0], vmin1[1], vmin1[2], vmin1[3], pw[r][0], pw[r][1]);
+          mma_16816_first<__half>(behind, vmin1[0], vmin1[1], vmin1[2], vmin1[3], pw[r][2], pw[r][3]);
           if constexpr (SPLIT) {
-            mma_16816<__half>(add, vpar[0], vpar[1], vpar[2], vpar[3], pw2[r][0], pw2[r][1]);
-            mma_16816<__half>(behind, vpar[0], vpar[1], vpar[2], vpar[3], pw2[r][2], pw2[r][3]);
+            mma_16816<__half>(add, vmin1[0], vmin1[1], vmin1[2], vmin1[3], pw2[r][0], pw2[r][1]);
+            mma_16816<__half>(behind, vmin1[0], vmin1[1], vmin1[2], vmin1[3], pw2[r][2], pw2[r][3]);
+            mma_16816<__half>(add, vmin2[0], vmin2[1], vmin2[2], vmin2[3], pw[r][0], pw[r][1]);
+            mma_16816<__half>(behind, vmin2[0], vmin2[1], vmin2[2], vmin2[3], pw[r][2], pw[r][3]);
           }
           add[0] += behind[2];
           add[1] += behind[3];
-          if constexpr (MIDDLE) {  // (the lanes of the least values take those of the scales)
+          if constexpr (MIDDLE && !SPLIT) {  // (the lanes of the least values take those of the scales)
             const float a = __shfl_xor_sync(0xffffffffu, add[0], 16), b = __shfl_xor_sync(0xffffffffu, add[1], 16);
             add[0] = fmaf(8.f, a, add[0]);
             add[1] = fmaf(8.f, b, add[1]);
@@ -300,7 +317,7 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
         uint32_t w[4], u[4][4];
         ldmatrix_x4_trans(w[0], w[1], w[2], w[3], vrow + c * 16);
 #pragma unroll
-        for (int n = 0; n < 4; ++n) q4_unpack(w[n], u[n]);
+        for (int n = 0; n < 4; ++n) q4_codes<SPLIT>(w[n], u[n]);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           uint32_t b[4], b2[4];  // weight times scale, of the chunk's group (of each half's: D = 64)
@@ -324,18 +341,14 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
                   b[n] = *reinterpret_cast<const uint32_t *>(&y);
                 }
               }
-              if constexpr (MIDDLE) {
+              if constexpr (MIDDLE && !SPLIT) {
                 constexpr uint32_t low = 0x80088008u, top8 = 0x80808080u;  // -8 2^-24, -8 2^-20
                 mma_16816_first<__half>(from, low, top8, low, top8, b[0], b[1]);
                 mma_16816<__half>(from, low, top8, low, top8, b[2], b[3]);
-                if constexpr (SPLIT) {
-                  mma_16816<__half>(from, low, top8, low, top8, b2[0], b2[1]);
-                  mma_16816<__half>(from, low, top8, low, top8, b2[2], b2[3]);
-                }
               }
             }
             float add[4];
-            if constexpr (MIDDLE) {
+            if constexpr (MIDDLE && !SPLIT) {
               add[0] = from[0]; add[1] = from[1]; add[2] = from[2]; add[3] = from[3];
               mma_16816<__half>(add, u[0][2 * h], u[0][2 * h + 1], u[1][2 * h], u[1][2 * h + 1], b[0], b[1]);
             } else {
@@ -390,7 +403,7 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
       }
     for (int w = 0; w < kWarps; ++w) {
       if (warp == w && pc.t0 + w < pc.t1) {
-        const float up = pow2i(24) * pow2i(top);
+        const float up = pow2i(SPLIT ? 9 : 24) * pow2i(top), up2 = SPLIT ? up : up * 0.0625f;
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -401,7 +414,7 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const float low = __shfl_sync(0xffffffffu, vmin[r][e], 16 + 4 * F::group_of(c, h) + tq);
-                const float y = fmaf(o[r][2 * c + h][e], up, low), z = fmaf(o[r][2 * c + h][2 + e], up * 0.0625f, low);
+                const float y = fmaf(o[r][2 * c + h][e], up, low), z = fmaf(o[r][2 * c + h][2 + e], up2, low);
                 float2 *at = reinterpret_cast<float2 *>(res + F::out_feature(c, h, gq));
                 float2 v = w ? *at : make_float2(0.f, 0.f);
                 v.x += f[r][e] == 0.f ? 0.f : y * f[r][e];

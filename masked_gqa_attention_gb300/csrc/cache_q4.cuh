@@ -51,15 +51,36 @@ MGQA_DEV void q4_unpack(uint32_t w, uint32_t (&a)[4]) {
   a[3] = w & 0x00f000f0u;
 }
 
+// The same as (u - 8) 2^-9, normal numbers: the tensor cores align a subnormal operand's
+// products by the least exponent, which costs their sums some 8 bits (fp32 calls: an
+// error of 5.5e-6 of the outputs' size without).
+MGQA_DEV void q4_unpack_middle(uint32_t w, uint32_t (&a)[4]) {
+  q4_unpack(w, a);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t up = i % 2 ? 0x68006800u : 0x78007800u, eight = 0xa400a400u;  // 2^11 or 2^15, and -8 2^-9
+    const __half2 x = __hfma2(*reinterpret_cast<const __half2 *>(&a[i]), *reinterpret_cast<const __half2 *>(&up),
+                              *reinterpret_cast<const __half2 *>(&eight));
+    a[i] = *reinterpret_cast<const uint32_t *>(&x);
+  }
+}
+template <bool MIDDLE>
+MGQA_DEV void q4_codes(uint32_t w, uint32_t (&a)[4]) {
+  if constexpr (MIDDLE) q4_unpack_middle(w, a);
+  else q4_unpack(w, a);
+}
+
 // 2^k, k in [-126, 127].
 MGQA_DEV float pow2i(int k) { return __int_as_float((k + 127) << 23); }
 
 // One query row's operands in a lane (quad place tq): fp16 of q 2^k, the row's
-// largest in [2^9, 2^10), so bf16 and fp16 queries keep every bit that counts (what
+// largest in [2^6, 2^7), so bf16 and fp16 queries keep every bit that counts (what
 // is below 2^-24 of the row's largest loses some). fp32 ones are two terms (22
-// bits). The second code of a unit is worth 16 times the first: its features are
-// divided by that. `sums`: the groups' sums in two terms, for the least values (the
-// lanes tq 2 and 3 have them; the scales' columns are 0).
+// bits), and meet codes from their middle, u - 8: the terms that cancel are small then
+// (the tensor cores' sums truncate). The second code of a unit is worth 16 times the
+// first there: its features are divided by that. `sums`: the groups' sums in two terms, for
+// the least values (lanes tq 2 and 3), and 8 times that for the scales (0 where codes
+// count from 0).
 template <int D, bool SPLIT>
 struct Q4Row {
   uint32_t a[4][Q4<D>::KS][2], b[SPLIT ? 4 : 1][Q4<D>::KS][2];  // b: second terms
@@ -100,7 +121,7 @@ struct Q4Row {
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const int e = (int)(__float_as_uint(top) >> 23) - 127;  // (0: -127)
-    const int k = min(9 - e, 120);
+    const int k = min(6 - e, 120);
     const float up = negate ? -pow2i(k) : pow2i(k);
     down = pow2i(-k);
     float sum[4];
@@ -119,7 +140,7 @@ struct Q4Row {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           // D = 128: features {2s, 2s + 4}, {2s + 1, 2s + 5}; D = 64: {0, 2}, {1, 3}
-          const float m = h ? 0.0625f : 1.f;
+          const float m = h && !SPLIT ? 0.0625f : 1.f;
           const float u = x[g][2 * s + h] * m, v = x[g][2 * s + h + (N == 8 ? 4 : 2)] * m;
           a[g][s][h] = pack2<__half>(u, v);
           if constexpr (SPLIT) {
@@ -129,8 +150,8 @@ struct Q4Row {
         }
     }
     sums[0] = sums[1] = 0u;
-    if (tq >= 2) {
-      const float u = tq == 2 ? sum[0] : sum[2], v = tq == 2 ? sum[1] : sum[3];
+    if (SPLIT || tq >= 2) {
+      const float by = tq < 2 ? 8.f : 1.f, u = by * (tq % 2 ? sum[2] : sum[0]), v = by * (tq % 2 ? sum[3] : sum[1]);
       sums[0] = pack2<__half>(u, v);
       const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&sums[0]));
       sums[1] = pack2<__half>(u - hi.x, v - hi.y);
@@ -179,7 +200,7 @@ struct Q4Scores {
   }
   MGQA_DEV void finish() {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] = fmaf(acc[e], 16777216.f, s[e]);
+    for (int e = 0; e < 4; ++e) s[e] = fmaf(acc[e], SPLIT ? 512.f : 16777216.f, s[e]);
   }
 };
 

@@ -197,8 +197,8 @@ struct Q4Keys {
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         uint32_t u[2][4];
-        q4_unpack(w[c][2 * m], u[0]);
-        q4_unpack(w[c][2 * m + 1], u[1]);
+        q4_codes<SPLIT>(w[c][2 * m], u[0]);
+        q4_codes<SPLIT>(w[c][2 * m + 1], u[1]);
         x[m].chunk(c, u, reinterpret_cast<const float(&)[2][4]>(sc[2 * m]), term(0), term(1));
       }
 #pragma unroll

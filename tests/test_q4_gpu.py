@@ -140,10 +140,11 @@ def test_records_of_awkward_rows(M, D, dtype):
 @pytest.mark.parametrize("dtype", [BF, HF, FP])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("page", [0, 1, 5, 16, 64])
-@pytest.mark.parametrize("layers,T,chosen", [(1, 1, False), (3, 1, False), (2, 7, True), (1, 150, False)])
-def test_append_writes_what_it_should(M, dtype, D, page, layers, T, chosen):
+@pytest.mark.parametrize("layers,T,Hkv,chosen", [(1, 1, 3, False), (3, 1, 8, False), (2, 7, 3, True), (1, 150, 3, False),
+                                                 (1, 40, 1, False), (2, 33, 40, False)])
+def test_append_writes_what_it_should(M, dtype, D, page, layers, T, Hkv, chosen):
     rng = random.Random(page + T)
-    B, Hkv, cap = 4, 3, 200
+    B, cap = 4, 200
     lens = [0, 13, cap - T, 31]
     R = D // 2 + 16
     if page:
@@ -172,6 +173,25 @@ def test_append_writes_what_it_should(M, dtype, D, page, layers, T, chosen):
     M.masked_gqa_cache_append_q4(k, v, kn, vn, i32(lens), out, index=index, count=count, page_table=table, dev_error=err)
     assert out.tolist() == [n + c for n, c in zip(lens, counts)] and int(err) == 0
     assert torch.equal(k, wk) and torch.equal(v, wv)
+
+
+@pytest.mark.parametrize("page", [0, 16])
+def test_append_takes_rows_and_caches_of_any_strides(M, page):
+    """K and V, old rows and new ones, each with strides of its own; new rows expanded over the requests."""
+    B, Hkv, D, T, R = 3, 2, 128, 5, 80
+    table = torch.randperm(12).int().view(3, 4).cuda() if page else None
+    n = 12 if page else B
+    k = torch.zeros(n, 16 if page else 64, Hkv, R, dtype=torch.uint8, device="cuda").transpose(1, 2)
+    v = torch.zeros(n, Hkv + 1, 16 if page else 64, R + 16, dtype=torch.uint8, device="cuda")[:, :Hkv, :, :R]
+    kn = rand((1, T, Hkv, D), BF, 1).transpose(1, 2).expand(B, -1, -1, -1)
+    vn = rand((B, Hkv, T + 2, D + 8), BF, 2)[:, :, :T, :D]
+    lens, new = i32([3, 0, 14]), i32([0] * 3)
+    M.masked_gqa_cache_append_q4(k, v, kn, vn, lens, new, page_table=table)
+    assert new.tolist() == [8, 5, 19]
+    for b in range(B):
+        j = int(lens[b]) + torch.arange(T, device="cuda")
+        pg, sl = (table[b].long()[j // 16], j % 16) if page else (torch.full_like(j, b), j)
+        assert torch.equal(k[pg, :, sl].transpose(0, 1), records(kn[b])) and torch.equal(v[pg, :, sl].transpose(0, 1), records(vn[b]))
 
 
 def test_append_reports_what_it_cannot_store(M):
