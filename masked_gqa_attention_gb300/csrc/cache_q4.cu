@@ -61,6 +61,10 @@ struct Cfg {
     LocateScratch<kThreads> scratch;
     int2 what[kWarps][STAGES];        // a stage's first slot, and which keys count
     Feed feed[kWarps];
+    // with four groups of rows: their operands (the products', then the sums), and of
+    // each row the scores' factor and the position
+    uint2 q[RT == kWarps ? RT : 1][RT == kWarps ? 4 * Q4<D>::KS + 1 : 1][32];
+    float2 rule[ROWS];
   };
   static constexpr int smem = ring + (int)sizeof(Misc);
 };
@@ -73,6 +77,8 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
   constexpr bool SPLIT = sizeof(T) == 4;
   constexpr bool MIDDLE = !__is_same(T, __nv_bfloat16);  // codes count from 8
   constexpr int ROWS = C::ROWS, STAGES = C::STAGES, NC = F::CHUNKS;
+  constexpr bool SHARE = RT == kWarps;
+  static_assert(!SHARE || !SPLIT, "one term of the queries is staged");
   const CacheAttnParams &p = qp.t.a;
   extern __shared__ __align__(1024) unsigned char smem[];
   auto &sm = *reinterpret_cast<typename C::Misc *>(smem + C::ring);
@@ -106,23 +112,42 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
     if (teller) tell_cut(p, blockIdx.x, &pc);
     const RowPlan &rp = pc.rp;
     const PieceOut po = out_of(p, pc, blockIdx.x);
-    Q4Row<D, SPLIT> q[RT];
     // of the rows 2 tq and 2 tq + 1 of each group, whose scores and outputs the lane has
     float scale[RT][2];
     int pos[RT][2];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
+    Q4Row<D, SPLIT> q[SHARE ? 1 : RT];  // (four groups: staged in shared memory, one by each warp)
+    const auto load_row = [&](int r, Q4Row<D, SPLIT> &to) {  // its position
       const int row = po.row0 + 8 * r + gq;
       const bool in = row < p.R;
       const int t = in ? row / p.n_rep : 0, h = pc.g * p.n_rep + (in ? row - t * p.n_rep : 0);
-      q[r].load(in ? static_cast<const T *>(p.q) + (int64_t)pc.b * p.qs[0] + (int64_t)h * p.qs[1] + (int64_t)t * p.qs[2]
-                   : static_cast<const T *>(nullptr), tq, p.scale_log2 < 0.f);
-      const int at = in ? rp.n - p.T + t : -1;
+      to.load(in ? static_cast<const T *>(p.q) + (int64_t)pc.b * p.qs[0] + (int64_t)h * p.qs[1] + (int64_t)t * p.qs[2]
+                 : static_cast<const T *>(nullptr), tq, p.scale_log2 < 0.f);
+      return in ? rp.n - p.T + t : -1;
+    };
+    // (above 0, so that a hidden key's -inf stays one)
+    const auto factor = [&](float down) { return fmaxf(down * fabsf(p.scale_log2), 1.2e-38f); };
+    if constexpr (SHARE) {
+      const int at = load_row(warp, q[0]);
+      if (tq == 0) sm.rule[8 * warp + gq] = make_float2(factor(q[0].down), __int_as_float(at));
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        // (above 0, so that a hidden key's -inf stays one)
-        scale[r][e] = fmaxf(__shfl_sync(0xffffffffu, q[r].down, 8 * tq + 4 * e) * fabsf(p.scale_log2), 1.2e-38f);
-        pos[r][e] = __shfl_sync(0xffffffffu, at, 8 * tq + 4 * e);
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int i = 0; i < F::KS; ++i) sm.q[warp][g * F::KS + i][lane] = make_uint2(q[0].a[g][i][0], q[0].a[g][i][1]);
+      sm.q[warp][4 * F::KS][lane] = make_uint2(q[0].sums[0], q[0].sums[1]);
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) scale[r][e] = sm.rule[8 * r + 2 * tq + e].x;
+    } else {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const int at = load_row(r, q[r]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          scale[r][e] = factor(__shfl_sync(0xffffffffu, q[r].down, 8 * tq + 4 * e));
+          pos[r][e] = __shfl_sync(0xffffffffu, at, 8 * tq + 4 * e);
+        }
       }
     }
     // every row of the block sees the keys from `far` (and the sinks) to `near`
@@ -160,7 +185,15 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
           uint32_t par[4];
           ldmatrix_x4(par[0], par[1], par[2], par[3], kt + (16 * i + (lane & 15)) * F::REC + F::CODES);
 #pragma unroll
-          for (int r = 0; r < RT; ++r) x[r][i].least(par, q[r].sums);
+          for (int r = 0; r < RT; ++r) {
+            if constexpr (SHARE) {
+              const uint2 both = sm.q[r][4 * F::KS][lane];
+              const uint32_t sums[2] = {both.x, both.y};
+              x[r][i].least(par, sums);
+            } else {
+              x[r][i].least(par, q[r].sums);
+            }
+          }
         }
         float sc[4][4];
 #pragma unroll
@@ -177,8 +210,15 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
             const float(&two)[2][4] = reinterpret_cast<const float(&)[2][4]>(sc[2 * i]);
 #pragma unroll
             for (int r = 0; r < RT; ++r)
-              x[r][i].chunk(c, u, two, [&](int g, int s) { return make_uint2(q[r].a[g][s][0], q[r].a[g][s][1]); },
-                            [&](int g, int s) { return make_uint2(q[r].b[SPLIT ? g : 0][s][0], q[r].b[SPLIT ? g : 0][s][1]); });
+              x[r][i].chunk(c, u, two,
+                            [&](int g, int s) {
+                              if constexpr (SHARE) return sm.q[r][g * F::KS + s][lane];
+                              else return make_uint2(q[r].a[g][s][0], q[r].a[g][s][1]);
+                            },
+                            [&](int g, int s) {
+                              const auto &row = q[SHARE ? 0 : r];
+                              return make_uint2(row.b[SPLIT ? g : 0][s][0], row.b[SPLIT ? g : 0][s][1]);
+                            });
           }
         }
 #pragma unroll
@@ -213,7 +253,8 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int c = 8 * n + gq, j = k0 + c;
-              const bool see = (okw >> c & 1u) && j <= pos[r][e] && (j > pos[r][e] - p.window || j < p.sinks);
+              const int at = SHARE ? __float_as_int(sm.rule[8 * r + 2 * tq + e].y) : pos[r][e];
+              const bool see = (okw >> c & 1u) && j <= at && (j > at - p.window || j < p.sinks);
               float &s = x[r][n / 2].s[n % 2 * 2 + e];
               s = see ? s : -INFINITY;
             }
@@ -475,6 +516,9 @@ mgqa_status launch_t(StreamParams qp, mgqa_dtype dt, const CacheAttnLaunch &how,
 template <typename T, int D>
 mgqa_status launch_d(const StreamParams &qp, mgqa_dtype dt, const CacheAttnLaunch &how, cudaStream_t s) {
   if (qp.t.a.R <= 8) return launch_t<T, D, 1>(qp, dt, how, s);
+  // (blocks of 32 rows cost less to unpack for, but a short call leaves SMs without one)
+  if constexpr (sizeof(T) == 2)
+    if (qp.t.a.R > 16 && !short_call(qp.t.a, Q4<D>::REC)) return launch_t<T, D, 4>(qp, dt, how, s);
   return launch_t<T, D, 2>(qp, dt, how, s);
 }
 
