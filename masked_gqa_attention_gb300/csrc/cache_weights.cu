@@ -43,7 +43,7 @@ struct Keys {
   static constexpr int ROWB = D * 2;
   static constexpr Order ORDER = kXor;
   static constexpr int STAGED = N * 256;  // bytes of 8 staged rows
-  static constexpr int CTAS = 2, STAGES = 2;
+  static constexpr int CTAS = 2, CTAS_ONE = 2, STAGES = 2;
   uint32_t k[2][N][4];
 
   MGQA_DEV void take(const unsigned char *tile, int lane) {
@@ -97,7 +97,7 @@ struct Keys<float, D> {
   static constexpr int ROWB = D * 4;
   static constexpr Order ORDER = kOddSwapped;
   static constexpr int STAGED = 8 * D * 4;
-  static constexpr int CTAS = D == 128 ? 2 : 3, STAGES = 2;
+  static constexpr int CTAS = D == 128 ? 2 : 3, CTAS_ONE = CTAS, STAGES = 2;
   float4 k[2][N];
 
   MGQA_DEV void take(const unsigned char *tile, int lane) {
@@ -151,7 +151,7 @@ struct Q4Keys {
   static constexpr Order ORDER = kAsIs;
   static constexpr int WORDS = 8 * F::KS;  // operand registers of a row, one term
   static constexpr int STAGED = (WORDS * (SPLIT ? 2 : 1) + 2) * 128;
-  static constexpr int CTAS = 3, STAGES = 4;
+  static constexpr int CTAS = 3, CTAS_ONE = 4, STAGES = 4;
   uint32_t w[N][4], par[2][4];
   float sc[4][4];
 
@@ -231,8 +231,9 @@ struct Cfg {
   static constexpr int fixed = ring + (int)sizeof(Misc);  // the staged rows follow
 };
 
-template <typename K, int D>
-__global__ void __launch_bounds__(kThreads, K::CTAS)
+// ONE: no more than 8 rows.
+template <typename K, int D, bool ONE>
+__global__ void __launch_bounds__(kThreads, ONE ? K::CTAS_ONE : K::CTAS)
 cache_weights_kernel(const __grid_constant__ WeightParams wp) {
   using T = typename K::Query;
   using C = Cfg<K, D>;
@@ -267,7 +268,7 @@ cache_weights_kernel(const __grid_constant__ WeightParams wp) {
     const RowPlan &rp = pc.rp;
     for (int r0 = 0; r0 < p.R; r0 += wp.chunk) {
       // (eight rows, or pairs of them, with rows that give nothing behind the last one)
-      const int rows = min(wp.chunk, p.R - r0), groups = wp.chunk == 8 ? 1 : (rows + 15) / 16 * 2;
+      const int rows = min(wp.chunk, p.R - r0), groups = ONE ? 1 : (rows + 15) / 16 * 2;
       __syncthreads();  // the rows of an earlier chunk are no longer read
       for (int g8 = warp; g8 < groups; g8 += kWarps) {
         const int row = r0 + 8 * g8 + gq;
@@ -321,7 +322,7 @@ cache_weights_kernel(const __grid_constant__ WeightParams wp) {
 #pragma unroll
           for (int i = 0; i < NB; ++i) w[i] += s[i][0] + s[i][1];
         };
-        if (groups == 1) {
+        if constexpr (ONE) {
           float s[NB][2];
           keys.scores(staged, lane, s);
           add(0, s);
@@ -349,10 +350,10 @@ cache_weights_kernel(const __grid_constant__ WeightParams wp) {
   }
 }
 
-template <typename K, int D>
+template <typename K, int D, bool ONE>
 mgqa_status launch_k(WeightParams wp, int page_size, int sms, cudaStream_t s) {
   using C = Cfg<K, D>;
-  auto kern = cache_weights_kernel<K, D>;
+  auto kern = cache_weights_kernel<K, D, ONE>;
   CacheAttnParams &p = wp.s.t.a;
   static std::atomic<uint64_t> attr{0};
   const mgqa_status st = ensure_smem_attr(kern, C::fixed + kChunkRows / 8 * K::STAGED, attr, "cache weights kernel");
@@ -364,12 +365,16 @@ mgqa_status launch_k(WeightParams wp, int page_size, int sms, cudaStream_t s) {
   p.tile_shift = K::KEYS == 32 ? 5 : 4;
   p.lead = 4;
   p.min_run = kWarps;
-  wp.chunk = p.R <= 8 ? 8 : std::min(kChunkRows, (p.R + 15) / 16 * 16);
+  wp.chunk = ONE ? 8 : std::min(kChunkRows, (p.R + 15) / 16 * 16);
   const int64_t units = (int64_t)p.B * p.Hkv;
-  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(K::CTAS * sms, units * (most_tiles(p) + p.lead)));
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>((ONE ? K::CTAS_ONE : K::CTAS) * sms, units * (most_tiles(p) + p.lead)));
   const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kThreads), (size_t)C::fixed + (wp.chunk / 8) * K::STAGED, s, wp);
   if (e != cudaSuccess) return fail(MGQA_ERR_CUDA, "cache weights launch: %s", cudaGetErrorString(e));
   return MGQA_OK;
+}
+template <typename K, int D>
+mgqa_status launch_k(const WeightParams &wp, int page_size, int sms, cudaStream_t s) {
+  return wp.s.t.a.R <= 8 ? launch_k<K, D, true>(wp, page_size, sms, s) : launch_k<K, D, false>(wp, page_size, sms, s);
 }
 template <typename T>
 mgqa_status launch_type(const WeightParams &wp, int D, bool q4, int page_size, int sms, cudaStream_t s) {
