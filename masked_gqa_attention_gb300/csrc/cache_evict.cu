@@ -18,7 +18,12 @@
 //             of the launch writes to.
 //   free   -- with counts of the pages: the table entries behind the budget go.
 // The kept rows are read once and written once: that is the floor, and the weights
-// twice.
+// twice. (4 layers, 16 requests of 4288 slots on average cut to 2048, 8 heads of 128:
+// 182 us, 0.66 of the copy rate: kept rows are 256 bytes here and there, and a block
+// reads or writes, not both. One prompt of 32768 cut to 4096: 36 us, 5 of them copies:
+// 20 for the selection, three cluster barriers and as many reads of the counts a pass.
+// Rows in registers instead of shared memory: 186 and 41 us; a selection in one block
+// per head that read its weights for every pass: 49 us alone.)
 #include <algorithm>
 
 #include "common.cuh"

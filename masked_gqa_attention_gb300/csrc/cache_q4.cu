@@ -5,29 +5,32 @@
 // (below 0: it sees nothing) and sees slot j when
 //   j <= pos and (no window, or pos - j < window, or j < sinks).
 //
-// Every visible record is read once per KV head and block of query rows; a warp
-// spends some 900 instructions on 64 keys of 128 features, which the reads take
-// 435 cycles for, so the kernel has to keep both going. Each warp streams tiles of
-// 32 keys of its own through a ring in shared memory, by 16-byte asynchronous copies
-// that only it waits for: no barrier between warps inside a unit. (One bulk copy per
-// page and tensor took more instructions than the products: 918 a tile, not 560.) The records are the first operand of both products (16 keys, or 16
-// features, by 8 rows of queries), so a code is unpacked once for all rows and no part
-// of a product is empty with 8 rows; the weights turn from one layout to the other by
-// four transposes of 8 x 8 a tile.
+// Every visible record is read once per KV head and block of query rows, and takes a
+// warp some 665 instructions per 32 keys of 128 features with 8 rows of queries, where
+// the reads take 217 cycles of an SM: the issue slots bound it (32 requests of 16425
+// slots on average, 8 KV heads of 4 query heads: 138 us, 0.72 of the copy rate; with 16
+// rows 203). Each warp streams tiles of 32 keys of its own through a ring in shared
+// memory (cache_stream.cuh). The records are the first operand of both products (16
+// keys, or 16 features, by 8 rows of queries), so a code is unpacked once for all rows
+// and no part of a product is empty with 8 rows (queries as the first operand: 204 us);
+// the weights turn from one layout to the other by four transposes of 8 x 8 a tile.
+// Long calls of more than 16 rows take blocks of 32 (four heads by 8 tokens: 278 us,
+// in blocks of 16 299).
 //
 // Weights: p is 2^14 at most (the maximum is subtracted 14 short) and becomes fp16,
 // 2^-11 of it down to 2^-28 of the largest; p times a scale is rounded once more.
 // Scales of 2 and more are divided by a power of two first, which the outputs are in
-// units of. fp32 calls hold both in two terms (2^-22). Sums of weights and outputs are fp32, a tile's from the tensor cores and
-// those of the tiles in rounded additions: codes and least values are sums of one
-// sign that nearly cancel, and the tensor cores' accumulators truncate (32 rows of
-// 98000 keys: 0.0066 of the outputs' size from 64 bits with running accumulators).
-// For the same reason fp16 and fp32 calls take the codes from their middle,
+// units of. fp32 calls hold both in two terms (2^-22). Sums of weights and outputs are
+// fp32, a tile's from the tensor cores and those of the tiles in rounded additions:
+// codes and least values are sums of one sign that nearly cancel, and the tensor
+// cores' sums are truncated (with running accumulators 0.0066 of the outputs' size from
+// 64 bits over 98000 keys). For the same reason fp16 and fp32 calls take the codes from
+// their middle,
 //   out_d = sum_j (p_j scale_jg) (u_jd - 8) + sum_j p_j (least_jg + 8 scale_jg),
 // so that roundings are not multiplied by terms that cancel: fp16 the -8 by products
-// with a constant (0.0005 of the outputs' size without, where the outputs' own rounding
-// makes 0.0002), fp32 in the operand (with the constant, and in the scores without,
-// 4.5e-6). In bf16 the outputs' rounding hides it.
+// with a constant (0.0005 of the outputs' size without, 0.0003 so, where the outputs'
+// own rounding makes 0.0002), fp32 in the operand (5e-7). In bf16 the outputs' rounding
+// hides it.
 //
 // The work is cut as for the other cache attention (cache_sched.cuh): equal runs of
 // tiles and the merge kernel for long calls, a cluster per unit for short ones.

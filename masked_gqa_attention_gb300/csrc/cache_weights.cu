@@ -11,7 +11,10 @@
 // keys as the first operand of m16n8k16 products with 8 rows of queries each, which
 // the CTA has staged in shared memory in the order of their operand registers. fp32
 // keys take the CUDA cores, a quad of lanes a key; keys in 4 bits the products of
-// cache_q4.cuh.
+// cache_q4.cuh. (32 requests of 16425 slots on average, 8 KV heads of 4 query heads,
+// D = 128: bf16 175 us, 0.93 of the copy rate; fp32 404, 0.80; 4 bits 86, 0.63, where
+// the issue slots bound it. 32 tokens, so 128 rows, over two prompts of 28140: 52 us,
+// four times the reads: chains of eight products, two warps a scheduler.)
 //
 // The tiles of all requests and KV heads are cut into equal runs (cache_sched.cuh);
 // no sum crosses a warp but a quad's, so results repeat bit for bit.
