@@ -363,6 +363,7 @@ PyObject *append_rows(PyObject *const *o, Py_ssize_t n, bool q4) {
     const int dev = device_of(k);
     together(dev, {{&v, "v_cache"}, {&kn, "k_new"}, {&vn, "v_new"}, {&len, "kv_len"}, {&len_out, "kv_len_out"},
                    {index, "index"}, {cnt, "count"}, {table, "page_table"}, {err, "dev_error"}});
+    if (!q4 && k.scalar_type() == at::kByte) bad("the caches must share one dtype of bfloat16, float16, float32");
     const Cache cache(k, v, table, &len, nullptr, err, q4 ? &kn : nullptr);
     const int x = (int)k.dim() - 4;
     bool fits = kn.dim() == k.dim() && vn.sizes() == kn.sizes() && (q4 || kn.scalar_type() == k.scalar_type()) &&

@@ -66,7 +66,7 @@ MGQA_DEV uint32_t ordered(float x) {
 }
 
 struct alignas(16) Select {
-  int bins[kBins];
+  int bins[3][kBins];  // one for each pass: none waits for the others to have read it
   int scan[kSelectWarps + 1];
   int2 count[kSelectWarps];  // slots that stay for sure, and those equal to the cut, of a warp's part
   int2 all;                  // of the block, read by its cluster
@@ -98,7 +98,7 @@ evict_select_kernel(const __grid_constant__ EvictParams p) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, C = p.parts;
   const int unit = blockIdx.x / C, rank = blockIdx.x % C;
   const int g = unit % p.Hkv, b = unit / p.Hkv % p.rows, layer = unit / p.Hkv / p.rows;
-  for (int i = tid; i < kBins; i += kSelectThreads) sm.bins[i] = 0;
+  for (int i = tid; i < 3 * kBins; i += kSelectThreads) sm.bins[0][i] = 0;
   grid_dependency_wait();
   allow_dependents();
   const int n = __ldcg(p.kv_len + b);
@@ -157,23 +157,24 @@ evict_select_kernel(const __grid_constant__ EvictParams p) {
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
       const int high = shift + width;
+      int *bins = sm.bins[pass];
       const int a = max(0, from - j0), z = min(len, to - j0);
 #pragma unroll 4
       for (int i = a + tid; i < z; i += kSelectThreads) {
         const uint32_t u = ordered(weight(i));
-        if (pass == 0 || u >> high == cut >> high) atomicAdd(&sm.bins[u >> shift & ((1u << width) - 1u)], 1);
+        if (pass == 0 || u >> high == cut >> high) atomicAdd(&bins[u >> shift & ((1u << width) - 1u)], 1);
       }
       if (parts > 1) cluster_sync();
       else __syncthreads();
       // bins from the top: thread t has bins 2047 - 4 t and the three below
       const int top = kBins - 4 - 4 * tid;
-      int4 c = *reinterpret_cast<const int4 *>(sm.bins + top);
+      int4 c = *reinterpret_cast<const int4 *>(bins + top);
       if (parts > 1) {
         float4 f[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) {  // every load in flight at once
           f[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (r < parts) f[r] = ld_cluster_f32x4(cluster_map_u32(smem_u32(sm.bins + top), r));
+          if (r < parts) f[r] = ld_cluster_f32x4(cluster_map_u32(smem_u32(bins + top), r));
         }
         c = make_int4(0, 0, 0, 0);
 #pragma unroll
@@ -195,16 +196,11 @@ evict_select_kernel(const __grid_constant__ EvictParams p) {
         sm.left = left - above;
         sm.within = have;
       }
-      if (parts > 1) cluster_sync();  // (every block has read the counts)
-      else __syncthreads();
+      __syncthreads();
       cut |= sm.digit << shift;
       left = sm.left;
       same = shift;
       if (sm.within == left) break;  // all of them stay
-      if (pass < 2) {
-        for (int i = tid; i < kBins; i += kSelectThreads) sm.bins[i] = 0;
-        __syncthreads();
-      }
     }
   } else if (parts > 1) {
     cluster_sync();  // every block has its weights: they may be overwritten
@@ -379,6 +375,8 @@ int64_t aligned16(int64_t n) { return (n + 15) / 16 * 16; }
 }  // namespace
 
 size_t cache_evict_workspace_bytes(const mgqa_cache &c, int32_t budget) {
+  const int64_t slots = c.page_table ? (int64_t)c.max_pages * c.page_size : c.page_size;
+  if (budget >= slots) budget = 0;  // no request is ever cut
   return (size_t)(aligned16((int64_t)c.rows * 4) + aligned16((int64_t)c.layers * c.rows * c.Hkv * budget * 4));
 }
 

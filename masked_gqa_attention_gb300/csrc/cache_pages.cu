@@ -300,8 +300,8 @@ append_q4_kernel(const __grid_constant__ Q4Params qp) {
   const int n = load(c.kv_len + b);
   const int cnt = p.count ? load(p.count + b) : p.T;
   const bool bad = n < 0 || cnt < 0 || cnt > p.T || (int64_t)n + cnt > cap;
-  const int t0 = (int)blockIdx.x * p.block_rows, rows = min(p.block_rows, p.T - t0) * c.Hkv;
-  const int live = bad ? 0 : p.count ? min(cnt, p.T) : p.T;
+  const int live = bad ? 0 : cnt;
+  const int t0 = (int)blockIdx.x * p.block_rows, rows = max(0, min(p.block_rows, live - t0)) * c.Hkv;
   const int piece = threadIdx.x % LR;
   const auto pieces = [&](const uint32_t (&st)[4], int x, int y, int z) {  // of layer `layer`
     return (uint64_t)(uint32_t)layer * st[0] + (uint64_t)(uint32_t)x * st[1] + (uint64_t)(uint32_t)y * st[2] +
@@ -310,7 +310,7 @@ append_q4_kernel(const __grid_constant__ Q4Params qp) {
   for (int r0 = 0; r0 < rows; r0 += kAppendThreads / LR) {  // (whole warps)
     const int r = r0 + (int)threadIdx.x / LR;
     const int tl = c.Hkv == 1 ? r : (int)__umulhi((uint32_t)r, qp.by_heads), h = r - tl * c.Hkv, t = t0 + tl;
-    const bool mine = r < rows && t < live;
+    const bool mine = r < rows;
     int from = t;
     if (p.index && mine) from = load(p.index + (int64_t)b * p.T + t);
     const bool has = mine && (unsigned)from < (unsigned)p.T;

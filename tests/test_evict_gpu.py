@@ -303,6 +303,40 @@ def test_a_page_shared_behind_the_budget_is_read_only(M):
     c.run(M, with_ref=True)
 
 
+def test_on_another_stream_with_its_own_memory(M):
+    c = Evict([500, 90], 128, 4, 32, layers=2, page=16)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    c.run(M)
+    torch.cuda.synchronize()
+    k, v, w, lens = (x.clone() for x in (c.k, c.v, c.w, c.kv_len))
+    torch.cuda.synchronize()
+    M.masked_gqa_cache_evict(k, v, w, lens, budget=128, sinks=4, recent=32, page_table=c.table, stream=s)
+    s.synchronize()
+    assert lens.tolist() == [128, 90]
+    for g in range(2):
+        keep = c.want(1, 0, g)
+        (pa, sa), (pb, sb) = c.place(c.table, 0, keep), c.place(c.table, 0, range(128))
+        assert torch.equal(k[1, pb, g, sb], c.k[1, pa, g, sa]) and torch.equal(w[1, 0, g, :128], c.w[1, 0, g, keep])
+
+
+def test_a_budget_past_every_length(M):
+    Evict([50, 3], 1 << 20, 4, 32, page=16).run(M)
+    Evict([50, 3], 1 << 24, 0, 1 << 24).run(M, in_place=False)
+
+
+def test_weights_shorter_than_the_table(M):
+    """Slots that have no weight: a longer request is left alone; shorter ones are cut."""
+    c = Evict([100, 100], 40, 2, 8, page=16, cap=160)
+    w = c.w[..., :100].contiguous()
+    k, v, lens, err = c.k.clone(), c.v.clone(), i32([100, 101]), i32([0])
+    M.masked_gqa_cache_evict(k, v, w, lens, budget=40, sinks=2, recent=8, page_table=c.table, dev_error=err)
+    assert lens.tolist() == [40, 101] and int(err) == INVALID and torch.equal(w[0, 1], c.w[0, 1, :, :100])
+    keep = c.want(0, 0, 1)
+    (pa, sa), (pb, sb) = c.place(c.table, 0, keep), c.place(c.table, 0, range(40))
+    assert torch.equal(k[0, pb, 1, sb], c.k[0, pa, 1, sa])
+
+
 def test_weights_and_eviction_captured(M):
     c = Evict([500, 200, 90], 128, 4, 32, layers=2, page=16, cap=512)
     k, v, w, lens = (x.clone() for x in (c.k, c.v, c.w, c.kv_len))

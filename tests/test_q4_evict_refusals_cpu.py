@@ -170,6 +170,13 @@ def test_binding_takes_all_arguments_or_none():
         M.masked_gqa_cache_evict_workspace_size(k, k, 0)
 
 
+def test_no_workspace_for_a_budget_that_nobody_exceeds(L):
+    c = cache()
+    least = L.masked_gqa_cache_evict_workspace_size(ref(c), c.max_pages * c.page_size)
+    assert 0 < least <= 64 and L.masked_gqa_cache_evict_workspace_size(ref(c), 1 << 24) == least
+    assert L.masked_gqa_cache_evict_workspace_size(ref(c), c.max_pages * c.page_size - 1) > 1000
+
+
 def test_binding_refuses_tensors_off_the_gpu():
     q, rec = torch.zeros(1, 2, 1, 64, dtype=torch.bfloat16), torch.zeros(1, 2, 4, 48, dtype=torch.uint8)
     n, lse, w = torch.zeros(1, dtype=torch.int32), torch.zeros(1, 2, 1), torch.zeros(1, 2, 4)

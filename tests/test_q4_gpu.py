@@ -208,6 +208,30 @@ def test_append_reports_what_it_cannot_store(M):
     assert (k[4:] == 0).all()
 
 
+def test_plain_append_refuses_records(M):
+    k = torch.zeros(2, 2, 8, 48, dtype=torch.uint8, device="cuda")
+    for D in (24, 48, 64):
+        for kind in (torch.uint8, HF):
+            x = torch.zeros(2, 2, 1, D, device="cuda").to(kind)
+            with pytest.raises(ValueError):
+                M.masked_gqa_cache_append(k, k, x, x, i32([0, 0]), i32([0, 0]))
+
+
+def test_append_of_a_few_of_many_rows(M):
+    """Counts far below T: the rows behind them are not looked at."""
+    B, Hkv, D, T = 3, 2, 64, 500
+    k, v = (torch.zeros(B, Hkv, 600, 48, dtype=torch.uint8, device="cuda") for _ in range(2))
+    x = rand((B, Hkv, T, D), HF, 3)
+    counts, new = [0, 5, 131], i32([0] * B)
+    for b, n in enumerate(counts):
+        x[b, :, n:] = float("nan")
+    M.masked_gqa_cache_append_q4(k, v, x, -x, i32([7, 0, 90]), new, count=i32(counts))
+    assert new.tolist() == [7, 5, 221]
+    for b, (a, n) in enumerate(zip([7, 0, 90], counts)):
+        assert torch.equal(k[b, :, a:a + n], records(x[b, :, :n])) and torch.equal(v[b, :, a:a + n], records(-x[b, :, :n]))
+        assert (k[b, :, a + n:] == 0).all()
+
+
 # ---- attention -----------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", [BF, HF, FP])
@@ -383,6 +407,16 @@ def test_calls_at_the_same_time(M):
             c.call(M, out=o, workspace=w, stream=s)
     torch.cuda.synchronize()
     for c, o in zip(cases, outs):
+        c.check(o)
+
+
+def test_on_another_stream_with_its_own_memory(M):
+    c = Case([9000, 700], 1, 16, 4, 128, BF, page=16)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = [c.call(M, stream=s) for _ in range(4)]
+    torch.cuda.synchronize()
+    for o in outs:
         c.check(o)
 
 
