@@ -270,9 +270,13 @@ def test_windows(M, window, sinks, T, page, D):
     ([9000 + 61 * i for i in range(24)], 1, 32, 8, 128, BF, 16),
     ([1 + 997 * i % 7000 for i in range(70)], 2, 12, 4, 64, BF, 32),
     ([3000] * 300, 1, 4, 4, 128, HF, 16),
+    ([50000, 3, 20011], 5, 16, 4, 128, BF, 16),   # blocks of 32 rows: one in part,
+    ([50000, 30, 20011], 7, 40, 4, 128, HF, 40),  # three with the last in part,
+    ([50000, 0, 44000], 16, 8, 4, 64, HF, 0),     # one whole
 ])
-def test_long_calls_are_cut_and_joined(M, lens, T, Hq, Hkv, D, dtype, page):
-    c = Case(lens, T, Hq, Hkv, D, dtype, page=page)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (9000, 70)])
+def test_long_calls_are_cut_and_joined(M, lens, T, Hq, Hkv, D, dtype, page, window, sinks):
+    c = Case(lens, T, Hq, Hkv, D, dtype, page=page, window=window, sinks=sinks)
     ws = M.new_cache_attn_workspace()
     ws.fill_(255)
     c.run(M, workspace=ws)
@@ -319,6 +323,17 @@ def test_features_and_values_of_very_different_size(M):
 @pytest.mark.parametrize("page", [0, 16])
 def test_slots_apart(M, page):
     Case([300, 45, 0], 2, 8, 2, 128, BF, page=page, slots_first=True).run(M)
+
+
+@pytest.mark.parametrize("page", [0, 16])
+def test_keys_and_values_with_strides_of_their_own(M, page):
+    c = Case([300, 45, 0], 2, 8, 2, 64, HF, page=page)
+    wide = torch.full((*c.v.shape[:3], 80), 255, dtype=torch.uint8, device="cuda")
+    wide[..., 16:64] = c.v
+    c.v = wide[..., 16:64]
+    c.run(M)
+    c.k = c.k.transpose(1, 2).contiguous().transpose(1, 2)
+    c.run(M)
 
 
 def test_queries_and_outputs_with_strides(M):
