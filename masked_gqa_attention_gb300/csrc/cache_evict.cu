@@ -19,11 +19,11 @@
 //   free   -- with counts of the pages: the table entries behind the budget go.
 // The kept rows are read once and written once: that is the floor, and the weights
 // twice. (4 layers, 16 requests of 4288 slots on average cut to 2048, 8 heads of 128:
-// 182 us, 0.66 of the copy rate: kept rows are 256 bytes here and there, and a block
-// reads or writes, not both. One prompt of 32768 cut to 4096: 36 us, 5 of them copies:
-// 20 for the selection, three cluster barriers and as many reads of the counts a pass.
-// Rows in registers instead of shared memory: 186 and 41 us; a selection in one block
-// per head that read its weights for every pass: 49 us alone.)
+// 172 us, 0.70 of the copy rate: kept rows are 256 bytes here and there, and a block
+// reads or writes, not both. One prompt of 32768 cut to 4096: 31 us, 5 of them copies,
+// most of the rest the selection's passes, a cluster barrier and a read of eight blocks'
+// counts each. Rows in registers instead of shared memory: 186 and 41 us; a selection
+// in one block per head that read its weights for every pass: 49 us alone.)
 #include <algorithm>
 
 #include "common.cuh"
@@ -274,13 +274,15 @@ evict_select_kernel(const __grid_constant__ EvictParams p) {
   if (parts > 1) cluster_sync();  // no block exits while its counts are read
 }
 
-constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 512;  // rows of a round, at most
+constexpr int kMoveThreads = 512;
+constexpr int kMoveRows = 256;  // rows of a round, at most
 
-struct Move {
-  // of a round's rows (and of the next one's): the slot that comes there, its page,
-  // the page it goes to
-  int4 row[2][kMoveRows];
+// A row's way, as offsets from the head's K and V; from -1: it stays where it is.
+struct Way {
+  int64_t from_k, to_k, from_v, to_v;
+};
+struct alignas(16) Move {
+  Way row[2][kMoveRows];  // of a round and of the next one
 };
 
 __global__ void __launch_bounds__(kMoveThreads)
@@ -304,18 +306,25 @@ evict_move_kernel(const __grid_constant__ EvictParams p) {
   }
   const auto index = [&](int j) { return p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size; };
   const int R = p.round_rows, step = R * C;
-  const auto look = [&](int first, int4 *row) {  // rows [first, first + R)
+  const auto look = [&](int first, Way *way) {  // rows [first, first + R)
     for (int r = tid; r < R; r += kMoveThreads) {
       const int d = first + r;
-      int4 x = make_int4(d, 0, 0, 0);
+      Way x{-1, 0, 0, 0};
       if (d < p.budget) {
-        x.x = __ldcg(kept + d);
-        if (p.table) {
-          x.z = __ldcg(table + index(d));
-          x.y = __ldcg(table + index(x.x));
+        const int j = __ldcg(kept + d);
+        if (j != d) {
+          int64_t a = 0, b = 0, from = j, to = d;
+          if (p.table) {
+            a = __ldcg(table + index(j));
+            b = __ldcg(table + index(d));
+            from = j - index(j) * p.page_size;
+            to = d - index(d) * p.page_size;
+          }
+          x = Way{a * p.ks[1] + from * p.ks[3], b * p.ks[1] + to * p.ks[3], a * p.vs[1] + from * p.vs[3],
+                  b * p.vs[1] + to * p.vs[3]};
         }
       }
-      row[r] = x;
+      way[r] = x;
     }
   };
   // of piece i of a round's K or V
@@ -324,30 +333,26 @@ evict_move_kernel(const __grid_constant__ EvictParams p) {
   __syncthreads();
   int now = 0;
   for (int d0 = rank * R; d0 < p.budget + rank * R; d0 += step, now ^= 1) {  // (as many rounds for every block)
-    const int4 *rows = sm.row[now];
+    const Way *way = sm.row[now];
     const int n = max(0, min(R, p.budget - d0)) * p.pieces;
+    unsigned char *round_v = round + R * p.pieces * 16;
+#pragma unroll 4
     for (int i = tid; i < n; i += kMoveThreads) {
       const int r = row_of(i), piece = (i - r * p.pieces) * 16;
-      const int4 x = rows[r];
-      if (x.x == d0 + r) continue;  // it stays where it is
-      const int64_t slot = p.table ? x.x - index(x.x) * p.page_size : x.x;
-      cp_async16(round + i * 16, k + ((int64_t)x.y * p.ks[1] + slot * p.ks[3] + piece));
-      cp_async16(round + (R * p.pieces + i) * 16, v + ((int64_t)x.y * p.vs[1] + slot * p.vs[3] + piece));
+      if (way[r].from_k < 0) continue;
+      cp_async16(round + i * 16, k + way[r].from_k + piece);
+      cp_async16(round_v + i * 16, v + way[r].from_v + piece);
     }
     if (d0 + step < p.budget) look(d0 + step, sm.row[now ^ 1]);
     cp_async_wait_all();
     if (C > 1) cluster_sync();
     else __syncthreads();
+#pragma unroll 4
     for (int i = tid; i < n; i += kMoveThreads) {
       const int r = row_of(i), piece = (i - r * p.pieces) * 16;
-      const int4 x = rows[r];
-      const int d = d0 + r;
-      if (x.x == d) continue;
-      const int64_t slot = p.table ? d - index(d) * p.page_size : d;
-      __stcg(reinterpret_cast<uint4 *>(k + ((int64_t)x.z * p.ks[1] + slot * p.ks[3] + piece)),
-             *reinterpret_cast<const uint4 *>(round + i * 16));
-      __stcg(reinterpret_cast<uint4 *>(v + ((int64_t)x.z * p.vs[1] + slot * p.vs[3] + piece)),
-             *reinterpret_cast<const uint4 *>(round + (R * p.pieces + i) * 16));
+      if (way[r].from_k < 0) continue;
+      __stcg(reinterpret_cast<uint4 *>(k + way[r].to_k + piece), *reinterpret_cast<const uint4 *>(round + i * 16));
+      __stcg(reinterpret_cast<uint4 *>(v + way[r].to_v + piece), *reinterpret_cast<const uint4 *>(round_v + i * 16));
     }
     __syncthreads();  // the round's rows have been written from shared memory
   }

@@ -12,7 +12,7 @@
 // the CTA has staged in shared memory in the order of their operand registers. fp32
 // keys take the CUDA cores, a quad of lanes a key; keys in 4 bits the products of
 // cache_q4.cuh. (32 requests of 16425 slots on average, 8 KV heads of 4 query heads,
-// D = 128: bf16 175 us, 0.93 of the copy rate; fp32 404, 0.80; 4 bits 86, 0.63, where
+// D = 128: bf16 175 us, 0.94 of the copy rate; fp32 335, 0.96; 4 bits 85, 0.64, where
 // the issue slots bound it. 32 tokens, so 128 rows, over two prompts of 28140: 52 us,
 // four times the reads: chains of eight products, two warps a scheduler.)
 //
@@ -46,7 +46,7 @@ struct Keys {
   static constexpr int ROWB = D * 2;
   static constexpr Order ORDER = kXor;
   static constexpr int STAGED = N * 256;  // bytes of 8 staged rows
-  static constexpr int CTAS = 2, CTAS_ONE = 2, STAGES = 2;
+  static constexpr int CTAS = 2, CTAS_ONE = D == 128 ? 2 : 3, STAGES = D == 128 ? 2 : 3;
   uint32_t k[2][N][4];
 
   MGQA_DEV void take(const unsigned char *tile, int lane) {
@@ -69,7 +69,7 @@ struct Keys {
     return 1.f;
   }
   // s[i][e]: block i with row 2 tq + e
-  MGQA_DEV void scores(const unsigned char *staged, int lane, float (&s)[4][2]) const {
+  MGQA_DEV void scores(const unsigned char *staged, int lane, float (&s)[4][2], int = 8) const {
     float x[2][4];
 #pragma unroll
     for (int c = 0; c < N; c += 2) {
@@ -117,10 +117,13 @@ struct Keys<float, D> {
           row ? *(reinterpret_cast<const float4 *>(row) + 4 * c + (lane & 3)) : make_float4(0.f, 0.f, 0.f, 0.f);
     return 1.f;
   }
-  MGQA_DEV void scores(const unsigned char *staged, int lane, float (&s)[2][2]) const {
+  // (rows: of the 8, how many there are)
+  MGQA_DEV void scores(const unsigned char *staged, int lane, float (&s)[2][2], int rows = 8) const {
     const int tq = lane & 3;
+    s[0][0] = s[0][1] = s[1][0] = s[1][1] = 0.f;
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
+      if (r >= rows) break;
       const float4 *q = reinterpret_cast<const float4 *>(staged) + r * (D / 4) + tq;
       float x = 0.f, y = 0.f;
 #pragma unroll
@@ -183,7 +186,7 @@ struct Q4Keys {
     *reinterpret_cast<uint2 *>(x + (STAGED / 4 - 64) + 2 * lane) = make_uint2(q.sums[0], q.sums[1]);
     return q.down;
   }
-  MGQA_DEV void scores(const unsigned char *staged, int lane, float (&s)[4][2]) const {
+  MGQA_DEV void scores(const unsigned char *staged, int lane, float (&s)[4][2], int = 8) const {
     const uint32_t *q = reinterpret_cast<const uint32_t *>(staged);
     const uint2 last = *reinterpret_cast<const uint2 *>(q + (STAGED / 4 - 64) + 2 * lane);
     const uint32_t sums[2] = {last.x, last.y};
@@ -327,7 +330,7 @@ cache_weights_kernel(const __grid_constant__ WeightParams wp) {
         };
         if constexpr (ONE) {
           float s[NB][2];
-          keys.scores(staged, lane, s);
+          keys.scores(staged, lane, s, rows);
           add(0, s);
         } else {
           for (int g8 = 0; g8 < groups; g8 += 2) {  // (two at a time: one's products are a chain)
