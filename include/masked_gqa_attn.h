@@ -334,7 +334,8 @@ typedef struct {
                                         them see nothing and are seen by none: out = 0, lse = -inf */
 } mgqa_tree;
 
-/* Bytes of the workspace of the two calls below; the same for every shape.
+/* Bytes of the workspace of the two calls below, and of masked_gqa_attn_decode_q4;
+ * the same for every shape.
  * The workspace (device, 16-byte aligned) needs no initial contents and
  * carries nothing from call to call. Calls that may run at the same time (two
  * streams, two graphs) need a workspace each. */

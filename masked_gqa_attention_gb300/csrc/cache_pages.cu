@@ -307,7 +307,7 @@ append_q4_kernel(const __grid_constant__ Q4Params qp) {
     return (uint64_t)(uint32_t)layer * st[0] + (uint64_t)(uint32_t)x * st[1] + (uint64_t)(uint32_t)y * st[2] +
            (uint64_t)(uint32_t)z * st[3];
   };
-  for (int r0 = 0; r0 < rows; r0 += kAppendThreads / LR) {  // (whole warps)
+  for (int r0 = 0; r0 < rows; r0 += (int)blockDim.x / LR) {  // (whole warps)
     const int r = r0 + (int)threadIdx.x / LR;
     const int tl = c.Hkv == 1 ? r : (int)__umulhi((uint32_t)r, qp.by_heads), h = r - tl * c.Hkv, t = t0 + tl;
     const bool mine = r < rows;
@@ -845,7 +845,10 @@ mgqa_status launch_cache_append(const mgqa_cache &c, const void *k_new, const vo
   const auto kern = c.dtype == MGQA_BF16   ? (c.D == 64 ? append_q4_kernel<__nv_bfloat16, 64> : append_q4_kernel<__nv_bfloat16, 128>)
                     : c.dtype == MGQA_FP16 ? (c.D == 64 ? append_q4_kernel<__half, 64> : append_q4_kernel<__half, 128>)
                                            : (c.D == 64 ? append_q4_kernel<float, 64> : append_q4_kernel<float, 128>);
-  return launched(launch_pdl(kern, grid, dim3(kAppendThreads), 0, s, qp), "cache append");
+  // (no idle threads where a request has few rows: a token of 32 requests x 32 layers, 8 heads
+  // of 128, in one wave of blocks)
+  const int threads = (int)std::min<int64_t>(kAppendThreads, (p.block_rows * per + 31) / 32 * 32);
+  return launched(launch_pdl(kern, grid, dim3(threads), 0, s, qp), "cache append");
 }
 
 mgqa_status launch_cache_fork(const mgqa_cache &c, int n, const int32_t *src, const int32_t *dst, int32_t extra,
