@@ -467,10 +467,12 @@ MGQA_API mgqa_status masked_gqa_cache_append_q4(const mgqa_cache *cache, const v
  * records (args->k, v; k_stride, v_stride in bytes): with n = kv_len[b] query t stands
  * at position n - Lq + t (below 0 it sees nothing) and sees slot j when j is at most
  * its position and, with window > 0, less than `window` behind it (its own position
- * counts) or below `sinks`. args->dtype is the type of q and out; the products are
- * with the values that the records stand for, not rounded. Cache forms, kv_len,
- * workspace and errors as for masked_gqa_attn_decode_window. Slots that no query sees
- * may hold anything; the scales and least values of the others have to be finite. */
+ * counts) or below `sinks`. args->dtype is the type of q and out. The codes, scales and
+ * least values are taken as they are; softmax weights, and their products with the
+ * scales, are fp16 (fp32 calls: two fp16 terms, 22 bits), and codes count from their
+ * group's middle, so the second rounding is relative to what the values add up to. Cache
+ * forms, kv_len, workspace and errors as for masked_gqa_attn_decode_window. Slots that no
+ * query sees may hold anything; the scales and least values of the others have to be finite. */
 MGQA_API mgqa_status masked_gqa_attn_decode_q4(const mgqa_args *args, const mgqa_pages *pages, int32_t window,
                                                int32_t sinks, void *workspace, size_t workspace_bytes,
                                                cudaStream_t stream);

@@ -24,13 +24,17 @@
 // fp32, a tile's from the tensor cores and those of the tiles in rounded additions:
 // codes and least values are sums of one sign that nearly cancel, and the tensor
 // cores' sums are truncated (with running accumulators 0.0066 of the outputs' size from
-// 64 bits over 98000 keys). For the same reason fp16 and fp32 calls take the codes from
-// their middle,
-//   out_d = sum_j (p_j scale_jg) (u_jd - 8) + sum_j p_j (least_jg + 8 scale_jg),
-// so that roundings are not multiplied by terms that cancel: fp16 the -8 by products
-// with a constant (0.0005 of the outputs' size without, 0.0003 so, where the outputs'
-// own rounding makes 0.0002), fp32 in the operand (5e-7). In bf16 the outputs' rounding
-// hides it.
+// 64 bits over 98000 keys). For the same reason the codes are taken from the middle c of
+// the tile's group, where its values are about 0,
+//   out_d = sum_j (p_j scale_jg) (u_jd - c) + sum_j p_j (least_jg + c scale_jg):
+// the second rounding is one and the same for all keys of one weight and scale, does not
+// average out, and would be multiplied by codes of one sign (100000 such keys: 0.11 of
+// the outputs' size with codes from 0 and a mean code of 7.5; from 8 instead of 7.5 still
+// 0.004, and 0.07 where the codes' mean is 2.5; so 0.0008). c is -sum least / sum scale
+// of the tile's keys in steps of 1/64, so that u - c is exact and any c is right: 22
+// instructions a tile, and one for every two codes (the batch above: 138 us without in
+// bf16; p times scale in two terms 153, their remainders summed beside them 145, but
+// with 32 rows 318 against 294).
 //
 // The work is cut as for the other cache attention (cache_sched.cuh): equal runs of
 // tiles and the merge kernel for long calls, a cluster per unit for short ones.
@@ -78,7 +82,6 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
   using C = Cfg<D, RT>;
   using F = Q4<D>;
   constexpr bool SPLIT = sizeof(T) == 4;
-  constexpr bool MIDDLE = !__is_same(T, __nv_bfloat16);  // codes count from 8
   constexpr int ROWS = C::ROWS, STAGES = C::STAGES, NC = F::CHUNKS;
   constexpr bool SHARE = RT == kWarps;
   static_assert(!SHARE || !SPLIT, "one term of the queries is staged");
@@ -246,6 +249,29 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
             for (int e = 0; e < 4; ++e) o[r][c][e] *= f;
       }
 
+      // ---- the parameters of V: lane (g, tq) has the scales of group g of two keys, lane
+      // (4 + g, tq) their least values: keys 2 tq and + 1 behind 0, 16, 8 and 24. So both
+      // halves of the keys are in one operand, above and below (of each product one half
+      // of the rows is of no use). And in the lanes of the least values the middle of the
+      // group's codes, as a number and as the pair -middle 2^-9.
+      uint32_t vpar[4], minus;
+      float middle;
+      const auto look = [&] {
+        ldmatrix_x4_trans(vpar[0], vpar[1], vpar[2], vpar[3],
+                          vt + ((lane & 7) | (lane & 8) << 1 | (lane & 16) >> 1) * F::REC + F::CODES);
+        constexpr uint32_t one = 0x3c003c00u;
+        float sums[4];
+        mma_16816_first<__half>(sums, vpar[0], vpar[1], vpar[2], vpar[3], one, one);
+        const float mine = sums[0] + sums[2], across = __shfl_xor_sync(0xffffffffu, mine, 16);
+        const float c = fminf(fmaxf(__fdividef(-mine, across), 0.f), 15.f);  // (0 / 0: 0)
+        middle = __fsub_rn(__fadd_rn(c, 196608.f), 196608.f);                 // 1.5 2^17: steps of 1/64
+        minus = pack2<__half>(middle * -0x1p-9f, middle * -0x1p-9f);
+      };
+      // (four groups of rows: ahead of the weights, which hide its latency; with fewer the
+      // registers are worth more: 64 tokens of 4 requests 456 us against 479, the batch
+      // above 147 against 146)
+      if constexpr (SHARE) look();
+
       // ---- weights, and their transpose: pw[r][n] has row gq, keys 8 n + 2 tq and + 1
       const bool all = okw == 0xffffffffu && k0 + kKeys - 1 <= near && (k0 >= far || k0 + kKeys <= p.sinks);
       if (!all) {
@@ -296,15 +322,10 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
         }
       }
 
-      // ---- outputs. The parameters of V: lane (g, tq) has the scales of group g of two
-      // keys, lane (4 + g, tq) their least values: keys 2 tq and + 1 behind 0, 16, 8 and
-      // 24. So both halves of the keys are in one operand, above and below (of each
-      // product one half of the rows is of no use).
-      uint32_t vpar[4];
-      ldmatrix_x4_trans(vpar[0], vpar[1], vpar[2], vpar[3],
-                        vt + ((lane & 7) | (lane & 8) << 1 | (lane & 16) >> 1) * F::REC + F::CODES);
+      // ---- outputs
+      if constexpr (!SHARE) look();
       {
-        uint32_t vmin1[4], vmin2[4];  // (fp32: least + 8 scale, in two terms, in the lanes of the least values)
+        uint32_t vmin1[4], vmin2[4];  // (fp32: least + middle scale, in two terms, in the lanes of the least values)
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
           vmin1[n] = vpar[n];
@@ -312,7 +333,7 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
             const uint32_t across = __shfl_xor_sync(0xffffffffu, vpar[n], 16);
             const float2 least = __half22float2(*reinterpret_cast<const __half2 *>(&vpar[n]));
             const float2 scale2 = __half22float2(*reinterpret_cast<const __half2 *>(&across));
-            const float y = fmaf(8.f, scale2.x, least.x), z = fmaf(8.f, scale2.y, least.y);
+            const float y = fmaf(middle, scale2.x, least.x), z = fmaf(middle, scale2.y, least.y);
             vmin1[n] = pack2<__half>(y, z);
             const float2 got = __half22float2(*reinterpret_cast<const __half2 *>(&vmin1[n]));
             vmin2[n] = pack2<__half>(y - got.x, z - got.y);
@@ -331,10 +352,10 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
           }
           add[0] += behind[2];
           add[1] += behind[3];
-          if constexpr (MIDDLE && !SPLIT) {  // (the lanes of the least values take those of the scales)
+          if constexpr (!SPLIT) {  // (the lanes of the least values take those of the scales)
             const float a = __shfl_xor_sync(0xffffffffu, add[0], 16), b = __shfl_xor_sync(0xffffffffu, add[1], 16);
-            add[0] = fmaf(8.f, a, add[0]);
-            add[1] = fmaf(8.f, b, add[1]);
+            add[0] = fmaf(middle, a, add[0]);
+            add[1] = fmaf(middle, b, add[1]);
           }
           vmin[r][0] = fmaf(vmin[r][0], down[r][0], add[0]);
           vmin[r][1] = fmaf(vmin[r][1], down[r][1], add[1]);
@@ -358,14 +379,16 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
       const float unit = pow2i(-top);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        uint32_t w[4], u[4][4];
+        uint32_t w[4], u[4][4], from[2];  // from: minus the middle of each half's group
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          from[h] = D == 128 && h ? from[0] : __shfl_sync(0xffffffffu, minus, 16 + 4 * F::group_of(c, h));
         ldmatrix_x4_trans(w[0], w[1], w[2], w[3], vrow + c * 16);
 #pragma unroll
-        for (int n = 0; n < 4; ++n) q4_codes<SPLIT>(w[n], u[n]);
+        for (int n = 0; n < 4; ++n) q4_unpack_from(w[n], from, u[n]);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           uint32_t b[4], b2[4];  // weight times scale, of the chunk's group (of each half's: D = 64)
-          float from[4];         // - 8 times their sums
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int g = F::group_of(c, h);
@@ -385,19 +408,9 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
                   b[n] = *reinterpret_cast<const uint32_t *>(&y);
                 }
               }
-              if constexpr (MIDDLE && !SPLIT) {
-                constexpr uint32_t low = 0x80088008u, top8 = 0x80808080u;  // -8 2^-24, -8 2^-20
-                mma_16816_first<__half>(from, low, top8, low, top8, b[0], b[1]);
-                mma_16816<__half>(from, low, top8, low, top8, b[2], b[3]);
-              }
             }
             float add[4];
-            if constexpr (MIDDLE && !SPLIT) {
-              add[0] = from[0]; add[1] = from[1]; add[2] = from[2]; add[3] = from[3];
-              mma_16816<__half>(add, u[0][2 * h], u[0][2 * h + 1], u[1][2 * h], u[1][2 * h + 1], b[0], b[1]);
-            } else {
-              mma_16816_first<__half>(add, u[0][2 * h], u[0][2 * h + 1], u[1][2 * h], u[1][2 * h + 1], b[0], b[1]);
-            }
+            mma_16816_first<__half>(add, u[0][2 * h], u[0][2 * h + 1], u[1][2 * h], u[1][2 * h + 1], b[0], b[1]);
             mma_16816<__half>(add, u[2][2 * h], u[2][2 * h + 1], u[3][2 * h], u[3][2 * h + 1], b[2], b[3]);
             if constexpr (SPLIT) {
               mma_16816<__half>(add, u[0][2 * h], u[0][2 * h + 1], u[1][2 * h], u[1][2 * h + 1], b2[0], b2[1]);
@@ -447,7 +460,7 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
       }
     for (int w = 0; w < kWarps; ++w) {
       if (warp == w && pc.t0 + w < pc.t1) {
-        const float up = pow2i(SPLIT ? 9 : 24) * pow2i(top), up2 = SPLIT ? up : up * 0.0625f;
+        const float up = pow2i(9) * pow2i(top);
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -458,7 +471,7 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const float low = __shfl_sync(0xffffffffu, vmin[r][e], 16 + 4 * F::group_of(c, h) + tq);
-                const float y = fmaf(o[r][2 * c + h][e], up, low), z = fmaf(o[r][2 * c + h][2 + e], up2, low);
+                const float y = fmaf(o[r][2 * c + h][e], up, low), z = fmaf(o[r][2 * c + h][2 + e], up, low);
                 float2 *at = reinterpret_cast<float2 *>(res + F::out_feature(c, h, gq));
                 float2 v = w ? *at : make_float2(0.f, 0.f);
                 v.x += f[r][e] == 0.f ? 0.f : y * f[r][e];

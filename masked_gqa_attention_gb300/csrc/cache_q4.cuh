@@ -51,18 +51,24 @@ MGQA_DEV void q4_unpack(uint32_t w, uint32_t (&a)[4]) {
   a[3] = w & 0x00f000f0u;
 }
 
-// The same as (u - 8) 2^-9, normal numbers: the tensor cores align a subnormal operand's
-// products by the least exponent, which costs their sums some 8 bits (fp32 calls: an
-// error of 5.5e-6 of the outputs' size without).
-MGQA_DEV void q4_unpack_middle(uint32_t w, uint32_t (&a)[4]) {
+// The same as (u - c) 2^-9, from[i]: -c 2^-9 (twice) of the codes of byte i of a unit; c a
+// multiple of 1/64, so exact.
+MGQA_DEV void q4_unpack_from(uint32_t w, const uint32_t (&from)[2], uint32_t (&a)[4]) {
   q4_unpack(w, a);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t up = i % 2 ? 0x68006800u : 0x78007800u, eight = 0xa400a400u;  // 2^11 or 2^15, and -8 2^-9
+    const uint32_t up = i % 2 ? 0x68006800u : 0x78007800u;  // 2^11 or 2^15
     const __half2 x = __hfma2(*reinterpret_cast<const __half2 *>(&a[i]), *reinterpret_cast<const __half2 *>(&up),
-                              *reinterpret_cast<const __half2 *>(&eight));
+                              *reinterpret_cast<const __half2 *>(&from[i / 2]));
     a[i] = *reinterpret_cast<const uint32_t *>(&x);
   }
+}
+// The same from the middle of all codes, (u - 8) 2^-9: normal numbers. (The tensor cores
+// align a subnormal operand's products by the least exponent, which costs their sums some 8
+// bits; fp32 calls: an error of 5.5e-6 of the outputs' size without.)
+MGQA_DEV void q4_unpack_middle(uint32_t w, uint32_t (&a)[4]) {
+  const uint32_t from[2] = {0xa400a400u, 0xa400a400u};
+  q4_unpack_from(w, from, a);
 }
 template <bool MIDDLE>
 MGQA_DEV void q4_codes(uint32_t w, uint32_t (&a)[4]) {
