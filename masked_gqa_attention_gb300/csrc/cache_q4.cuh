@@ -80,13 +80,14 @@ MGQA_DEV void q4_codes(uint32_t w, uint32_t (&a)[4]) {
 MGQA_DEV float pow2i(int k) { return __int_as_float((k + 127) << 23); }
 
 // One query row's operands in a lane (quad place tq): fp16 of q 2^k, the row's
-// largest in [2^6, 2^7), so bf16 and fp16 queries keep every bit that counts (what
-// is below 2^-24 of the row's largest loses some). fp32 ones are two terms (22
-// bits), and meet codes from their middle, u - 8: the terms that cancel are small then
-// (the tensor cores' sums truncate). The second code of a unit is worth 16 times the
-// first there: its features are divided by that. `sums`: the groups' sums in two terms, for
-// the least values (lanes tq 2 and 3), and 8 times that for the scales (0 where codes
-// count from 0).
+// largest in [2^6, 2^7). A feature is off by at most 2^-27 of the row's largest: those of
+// the second codes of a unit (see below) are divided by 16, and fp16's least step is 2^-24.
+// (fp16 queries keep every bit down to 2^-16 of the largest, bf16 ones down to 2^-19.) fp32
+// ones are two terms (22 bits, and 2^-31 of the largest), and meet codes from their
+// middle, u - 8: the terms that cancel are small then (the tensor cores' sums truncate).
+// Where codes count from 0 the second code of a unit is worth 16 times the first: its
+// features are divided by that. `sums`: the groups' sums in two terms, for the least values
+// (lanes tq 2 and 3), and 8 times that for the scales (0 where codes count from 0).
 template <int D, bool SPLIT>
 struct Q4Row {
   uint32_t a[4][Q4<D>::KS][2], b[SPLIT ? 4 : 1][Q4<D>::KS][2];  // b: second terms

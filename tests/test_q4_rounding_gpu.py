@@ -75,3 +75,40 @@ def test_keys_of_one_scale(M, codes, dtype, D, n, T, Hq, Hkv, power):
     tol = (2 * h + 2.0 ** -20) * A + hr * ref.abs() + h * scale / 64 + 2.0 ** -20 * mag.amax()
     worst = ((out - ref).abs() / (1.01 * tol)).max().item()
     assert worst <= 1.0, f"error {worst:.3g} times the bound ({(out - ref).abs().max() / ref.abs().max():.3g} of the output)"
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FP])
+@pytest.mark.parametrize("D", [64, 128])
+def test_features_of_a_query_far_apart(M, dtype, D):
+    """One feature of a query is 1, the others 2^-16 to 2^-24 of it; the large one meets zeros, so the scores are
+    the small ones'. A feature is held to 2^-27 of the largest of its row (scaled to [2^6, 2^7), where those of
+    every second code, divided by 16, have steps of 2^-24; fp32: two terms, 2^-31), and meets scale u; the sums
+    are off by (D + 8) 2^-24 of their terms, twice (see _q4_ref). fp32 calls multiply u - 8 and add 8 times the
+    queries' sums, so their terms are of |q| scale (|u - 8| + 8), which is not 0 for a code of 0: the large
+    feature's are 16 scale, and off by the queries' 2^-22 besides."""
+    g = torch.Generator("cuda").manual_seed(D)
+    n, H, scale = 300, 2, 16.0
+    u = torch.randint(0, 16, (H, n, D), generator=g, device="cuda", dtype=torch.uint8)
+    u[..., 0] = 0
+    size = 64.0 * (1 + torch.rand((H, n), generator=g, device="cuda"))
+    k = pack(u, size, 0 * size)
+    v = pack(u, size / 64, 0 * size)
+    q = torch.randn((1, H, 9, D), generator=g, device="cuda")
+    q *= 2.0 ** -torch.arange(16, 25, device="cuda")[:, None].float()
+    q[..., 0] = 1.0
+    q = q.to(dtype)
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    lse = [torch.empty(1, H, 1, device="cuda") for _ in range(9)]
+    for t in range(9):  # (a query a call, so that each sees every key)
+        M.masked_gqa_attn_decode_q4(q[:, :, t:t + 1], k[None], v[None], lens, scale=scale, lse=lse[t])
+    lse = torch.cat(lse, 2)
+    val, mag = values(k)
+    s = scale * (q[0].double() @ val.transpose(1, 2))
+    held = 2.0 ** (-31 if dtype == FP else -27)
+    terms = size[..., None] * ((u.double() - 8).abs() + 8) if dtype == FP else mag
+    delta = scale * (held * mag.sum(-1).amax(-1)[:, None]
+                     + 2 * (D + 8) * 2.0 ** -24 * (q[0].double().abs() @ terms.transpose(1, 2)).amax(-1))
+    want = torch.logsumexp(s, -1)
+    tol = delta + n * 2.0 ** -24 + 2.0 ** -20 * (1 + want.abs())
+    worst = ((lse[0].double() - want).abs() / tol).max().item()
+    assert worst <= 1.0, f"log-sums off by {worst:.3g} times the bound"
