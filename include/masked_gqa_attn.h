@@ -504,7 +504,7 @@ MGQA_API size_t masked_gqa_cache_evict_workspace_size(const mgqa_cache *cache, i
  * weight[layer][b][g][j] (of equal ones the first; NaN is less than any number). The
  * rows that stay move, in their order, to slots 0 .. budget - 1; weight_out gets their
  * weights there and 0 in slots budget .. kv_len[b] - 1, and the weights as they are of
- * requests within the budget. kv_len_out[b] = min(kv_len[b], budget); it may be kv_len
+ * requests that are not cut. kv_len_out[b] = min(kv_len[b], budget); it may be kv_len
  * itself and weight_out may be weight itself (with the same strides: layer, request,
  * head), but they may not overlap otherwise. weight and weight_out are device fp32
  * [layers][rows][Hkv][weight_slots], slots contiguous.
@@ -512,7 +512,8 @@ MGQA_API size_t masked_gqa_cache_evict_workspace_size(const mgqa_cache *cache, i
  * that), and with `ref` given (optional here) the table entries behind the budget of a
  * request that is cut become -1 and their pages are given back (ref - 1). A request
  * with kv_len out of range (or past weight_slots), a missing page or (with ref) a shared page among those that
- * would be written is left as it is and sets *dev_error.
+ * would be written is left as it is and sets *dev_error: kv_len_out[b] = kv_len[b], and
+ * weight_out gets its weights (nothing where kv_len is out of range).
  * Rows of any type: a cache of records goes as for fork. */
 MGQA_API mgqa_status masked_gqa_cache_evict(const mgqa_cache *cache, const float *weight,
                                             const int64_t *weight_stride, float *weight_out,

@@ -141,7 +141,7 @@ evict_select_kernel(const __grid_constant__ EvictParams p) {
     if (bad) report_error(p.err, MGQA_ERR_INVALID_ARG);
   }
   if (!over) {
-    if (out != w && !bad)
+    if (out != w && !wrong_n)  // (of a request that is left as it is, too: its length goes on)
       for (int j = rank * kSelectThreads + tid; j < n; j += parts * kSelectThreads) out[j] = __ldcg(w + j);
     return;
   }
