@@ -508,12 +508,18 @@ MGQA_API size_t masked_gqa_cache_evict_workspace_size(const mgqa_cache *cache, i
  * itself and weight_out may be weight itself (with the same strides: layer, request,
  * head), but they may not overlap otherwise. weight and weight_out are device fp32
  * [layers][rows][Hkv][weight_slots], slots contiguous.
- * With a page table, pages that are written to must not be shared (fork sees to
- * that), and with `ref` given (optional here) the table entries behind the budget of a
+ * With a page table, the pages from that of slot `sinks` to that of slot budget - 1 of a
+ * request that is cut must be its own: rows move there. Pages wholly within the first
+ * `sinks` slots are not written to and may be shared, as may those behind the budget. Fork
+ * does not see to that: it shares the full pages of a prompt, which stay shared until the
+ * other requests are freed, so such requests are cut with the prompt within the sinks, or
+ * not at all. With `ref` given (optional here) the call checks it; without, a shared page
+ * loses the other requests' rows. With `ref` the table entries behind the budget of a
  * request that is cut become -1 and their pages are given back (ref - 1). A request
- * with kv_len out of range (or past weight_slots), a missing page or (with ref) a shared page among those that
- * would be written is left as it is and sets *dev_error: kv_len_out[b] = kv_len[b], and
- * weight_out gets its weights (nothing where kv_len is out of range).
+ * with kv_len out of range (or past weight_slots), a missing page or (with ref) a shared
+ * page from that of slot `sinks` up to the budget is left as it is and sets *dev_error:
+ * kv_len_out[b] = kv_len[b], and weight_out gets its weights (nothing where kv_len is out
+ * of range).
  * Rows of any type: a cache of records goes as for fork. */
 MGQA_API mgqa_status masked_gqa_cache_evict(const mgqa_cache *cache, const float *weight,
                                             const int64_t *weight_stride, float *weight_out,

@@ -931,7 +931,9 @@ def masked_gqa_cache_evict(k_cache, v_cache, weight, kv_len, *, budget, sinks=0,
     4-D caches, with slots for every kv_len; of equal ones the first). The rows that stay move, in their order,
     to slots 0 .. budget - 1, and their weights with them; the slots behind get
     weight 0. weight_out and kv_len_out (default: weight and kv_len, in place). With
-    ref (int32 [pages]) the pages behind the budget are given back. The caches are
+    ref (int32 [pages]) the pages behind the budget are given back, and a request that
+    shares a page from that of slot `sinks` up to the budget is left as it is (without
+    ref nothing checks that, and its sharers lose their rows). The caches are
     [layers, B, Hkv, slots, D], or in pages, of any dtype or 4-bit records.
     Returns kv_len_out."""
     weight_out = weight if weight_out is None else weight_out

@@ -105,12 +105,16 @@ evict_select_kernel(const __grid_constant__ EvictParams p) {
   const bool first = layer == 0 && g == 0 && rank == 0;
   const bool wrong_n = n < 0 || n > p.slots;
   int wrong = 0;
-  if (!wrong_n && n > p.budget && p.table) {  // every page that is read is there, and none that is written is shared
+  // Every page that is read is there, and none that is written is shared (the sinks stay
+  // where they are: pages within them are not written).
+  if (!wrong_n && n > p.budget && p.table) {
     const int np = (n + p.page_size - 1) / p.page_size, wp = (p.budget + p.page_size - 1) / p.page_size;
+    const int w0 = p.sinks / p.page_size;
 #pragma unroll 4
     for (int i = tid; i < np; i += kSelectThreads) {
       const int e = __ldcg(p.table + (int64_t)b * p.table_stride + i);
-      if ((unsigned)e >= (unsigned)p.num_pages || (p.ref && i < wp && __ldcg(p.ref + e) > 1)) wrong = 1;
+      if ((unsigned)e >= (unsigned)p.num_pages || (p.ref && i >= w0 && i < wp && __ldcg(p.ref + e) > 1))
+        wrong = 1;
     }
   }
   const float *w = p.w + layer * p.wi[0] + b * p.wi[1] + g * p.wi[2];
