@@ -135,7 +135,7 @@ mgqa_status launch_cache_merge(const CacheAttnParams &p, mgqa_dtype dt, int D, i
 }
 
 void cache_attn_params(const mgqa_args &a, const mgqa_pages *pages, const mgqa_tree *tree, int32_t window,
-                              int32_t sinks, CacheAttnParams &p) {
+                       int32_t sinks, CacheAttnParams &p) {
   p = CacheAttnParams{};
   p.q = a.q; p.k = a.k; p.v = a.v; p.out = a.out;
   for (int t = 0; t < 3; ++t) {

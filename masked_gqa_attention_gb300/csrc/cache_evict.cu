@@ -19,11 +19,13 @@
 //   free   -- with counts of the pages: the table entries behind the budget go.
 // The kept rows are read once and written once: that is the floor, and the weights
 // twice. (4 layers, 16 requests of 4288 slots on average cut to 2048, 8 heads of 128:
-// 172 us, 0.70 of the copy rate: kept rows are 256 bytes here and there, and a block
-// reads or writes, not both. One prompt of 32768 cut to 4096: 31 us, 5 of them copies,
-// most of the rest the selection's passes, a cluster barrier and a read of eight blocks'
-// counts each. Rows in registers instead of shared memory: 186 and 41 us; a selection
-// in one block per head that read its weights for every pass: 49 us alone.)
+// 175 us, 0.69 of the copy rate: kept rows are 256 bytes here and there, and a block
+// reads or writes, not both; records in 4 bits 97. One prompt of 32768 cut to 4096: 30 us,
+// 5 of them copies, most of the rest the selection's passes, a cluster barrier and a read
+// of eight blocks' counts each; with weights within 0.4 % of one another 31, all equal 28
+// (the first slots stay where they are). Rows in registers instead of shared memory: 186
+// and 41 us; a selection in one block per head that read its weights for every pass: 49 us
+// alone.)
 #include <algorithm>
 
 #include "common.cuh"
@@ -377,7 +379,7 @@ __global__ void __launch_bounds__(256) evict_free_kernel(const __grid_constant__
 
 
 constexpr int kMoveMost = 204800, kMoveBytes = 49152;  // bytes of a block's round: alone on its SM, or not
-constexpr int kMoveFill = 4;                         // blocks of an SM that the clusters are made for
+constexpr int kMoveFill = 4;                         // clusters grow while there are fewer blocks an SM
 
 int64_t aligned16(int64_t n) { return (n + 15) / 16 * 16; }
 
@@ -420,8 +422,10 @@ mgqa_status launch_cache_evict(const mgqa_cache &c, const float *weight, const i
   p.page_shift = -1;
   if ((c.page_size & (c.page_size - 1)) == 0)
     for (p.page_shift = 0; (1 << p.page_shift) < c.page_size;) ++p.page_shift;
-  // more blocks while the SMs have room for them (a block of either kernel is a
-  // quarter of an SM) and each has enough to do
+  // more blocks while there are few for the SMs and each has enough to do. (A block is a
+  // quarter of an SM's threads. By shared memory three blocks of a move with 64 KB each
+  // fit one, and of a selection as few as one with all its weights: large calls take more
+  // than one wave.)
   const int row_bytes = p.pieces * 32;  // of K and V
   p.piece_shift = -1;
   if ((p.pieces & (p.pieces - 1)) == 0)

@@ -6,16 +6,19 @@
 //   j <= pos and (no window, or pos - j < window, or j < sinks).
 //
 // Every visible record is read once per KV head and block of query rows, and takes a
-// warp some 665 instructions per 32 keys of 128 features with 8 rows of queries, where
-// the reads take 217 cycles of an SM: the issue slots bound it (32 requests of 16425
-// slots on average, 8 KV heads of 4 query heads: 138 us, 0.72 of the copy rate; with 16
-// rows 203). Each warp streams tiles of 32 keys of its own through a ring in shared
-// memory (cache_stream.cuh). The records are the first operand of both products (16
-// keys, or 16 features, by 8 rows of queries), so a code is unpacked once for all rows
-// and no part of a product is empty with 8 rows (queries as the first operand: 204 us);
-// the weights turn from one layout to the other by four transposes of 8 x 8 a tile.
-// Long calls of more than 16 rows take blocks of 32 (four heads by 8 tokens: 278 us,
-// in blocks of 16 299).
+// warp some 747 instructions per 32 keys of 128 features with 8 rows of queries, where
+// the reads take 217 cycles of an SM. The latency of that work bounds it: three warps a
+// scheduler issue 2.5 instructions a cycle of an SM's four, no pipe is half used, and a
+// warp mostly waits for its own last instruction (32 requests of 16425 slots on average, 8
+// KV heads of 4 query heads: 145 us, 0.68 of the copy rate; with 16 rows 216). Each warp
+// streams tiles of 32 keys of its own through a ring in shared memory (cache_stream.cuh).
+// The records are the first operand of both products (16 keys, or 16 features, by 8 rows
+// of queries), so a code is unpacked once for all rows and no part of a product is empty
+// with 8 rows (queries as the first operand took half as long again); the weights turn from
+// one layout to the other by four transposes of 8 x 8 a tile. Long calls of more than 16
+// rows take blocks of 32 (four heads by 8 tokens: 298 us, in blocks of 16 9 % more), which
+// at D = 128 spill 304 bytes a thread to local memory, blocks of 16 72 (fp32 36), at two
+// CTAs an SM; 8 rows spill none.
 //
 // Weights: p is 2^14 at most (the maximum is subtracted 14 short) and becomes fp16,
 // 2^-11 of it down to 2^-28 of the largest; p times a scale is rounded once more.
@@ -31,10 +34,9 @@
 // average out, and would be multiplied by codes of one sign (100000 such keys: 0.11 of
 // the outputs' size with codes from 0 and a mean code of 7.5; from 8 instead of 7.5 still
 // 0.004, and 0.07 where the codes' mean is 2.5; so 0.0008). c is -sum least / sum scale
-// of the tile's keys in steps of 1/64, so that u - c is exact and any c is right: 22
-// instructions a tile, and one for every two codes (the batch above: 138 us without in
-// bf16; p times scale in two terms 153, their remainders summed beside them 145, but
-// with 32 rows 318 against 294).
+// of the tile's keys in steps of 1/64, so that u - c is exact and any c is right: 82 of
+// the instructions (the batch above 138 us without; p times scale in two terms 153, the
+// roundings summed and put right at the end 145, but with 32 rows 8 % more than this).
 //
 // The work is cut as for the other cache attention (cache_sched.cuh): equal runs of
 // tiles and the merge kernel for long calls, a cluster per unit for short ones.
@@ -267,9 +269,8 @@ cache_q4_kernel(const __grid_constant__ StreamParams qp) {
         middle = __fsub_rn(__fadd_rn(c, 196608.f), 196608.f);                 // 1.5 2^17: steps of 1/64
         minus = pack2<__half>(middle * -0x1p-9f, middle * -0x1p-9f);
       };
-      // (four groups of rows: ahead of the weights, which hide its latency; with fewer the
-      // registers are worth more: 64 tokens of 4 requests 456 us against 479, the batch
-      // above 147 against 146)
+      // (four groups of rows: ahead of the weights, which hide its latency: 64 tokens a
+      // request 5 % faster; with one group the registers are worth more, 1 %)
       if constexpr (SHARE) look();
 
       // ---- weights, and their transpose: pw[r][n] has row gq, keys 8 n + 2 tq and + 1

@@ -12,9 +12,13 @@
 // the CTA has staged in shared memory in the order of their operand registers. fp32
 // keys take the CUDA cores, a quad of lanes a key; keys in 4 bits the products of
 // cache_q4.cuh. (32 requests of 16425 slots on average, 8 KV heads of 4 query heads,
-// D = 128: bf16 175 us, 0.94 of the copy rate; fp32 335, 0.96; 4 bits 85, 0.64, where
-// the issue slots bound it. 32 tokens, so 128 rows, over two prompts of 28140: 52 us,
-// four times the reads: chains of eight products, two warps a scheduler.)
+// D = 128: bf16 175 us, 0.94 of the copy rate; fp32 334, 0.96; 4 bits 85, 0.64: 1.9
+// instructions a cycle of four, warps that wait for their own last one. 32 tokens, so
+// 128 rows, over two prompts of 28140: 54 us, four times the reads: chains of eight
+// products, two warps a scheduler; fp32 571, some 200 of them the multiply-adds alone; 4
+// bits 92, with fp32 queries 137. The forms for more than 8 rows that ask for three CTAs an
+// SM spill 56 to 168 bytes a thread; with 128 rows staged two of the three fit for 4 bits,
+// and of fp32 keys at D = 128 one of two, but the grid counts them all.)
 //
 // The tiles of all requests and KV heads are cut into equal runs (cache_sched.cuh);
 // no sum crosses a warp but a quad's, so results repeat bit for bit.
