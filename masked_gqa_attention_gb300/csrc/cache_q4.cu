@@ -31,9 +31,9 @@
 // the tile's group, where its values are about 0,
 //   out_d = sum_j (p_j scale_jg) (u_jd - c) + sum_j p_j (least_jg + c scale_jg):
 // the second rounding is one and the same for all keys of one weight and scale, does not
-// average out, and would be multiplied by codes of one sign (100000 such keys: 0.11 of
-// the outputs' size with codes from 0 and a mean code of 7.5; from 8 instead of 7.5 still
-// 0.004, and 0.07 where the codes' mean is 2.5; so 0.0008). c is -sum least / sum scale
+// average out, and would be multiplied by codes of one sign (100000 such keys: 0.05 of
+// the outputs' size with codes from 0 and a mean code of 7.5, up to 0.11 with other means;
+// from 8 instead of 7.5 still 0.004, and 0.07 where the mean is 2.5; so 0.0008). c is -sum least / sum scale
 // of the tile's keys in steps of 1/64, so that u - c is exact and any c is right: 82 of
 // the instructions (the batch above 138 us without; p times scale in two terms 153, the
 // roundings summed and put right at the end 145, but with 32 rows 8 % more than this).
